@@ -22,7 +22,8 @@ INCLUDE = os.path.join(REPO_ROOT, "include")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libconv3d_fp8.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
-SOURCES = ["api.cu", "pack.cu", "conv_tc.cu", "conv_tc_pair.cu", "quant.cu"]
+SOURCES = ["api.cu", "pack.cu", "conv_tc.cu", "conv_tc_pair.cu", "quant.cu", "q8_api.cu",
+           "q8_rows.cu", "q8_linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                  "-I", INCLUDE, "-I", CSRC]
@@ -38,7 +39,7 @@ def _nvcc() -> str:
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
              if f.endswith((".cu", ".cuh", ".h"))]
-    files.append(os.path.join(INCLUDE, "conv3d_fp8.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("conv3d_fp8.h", "q8.h")]
     files.append(os.path.abspath(__file__))
     return files
 

@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in ``include/conv3d_fp8.h`` (argument marshalling only).
+"""ctypes binding of the C ABI in ``include/conv3d_fp8.h`` and ``include/q8.h`` (argument
+marshalling only).
 
 Every entry point keeps its C name. Tensors are passed as raw device pointers (``data_ptr()``);
 torch is only used for device memory and streams. There is no fallback of any kind: if the CUDA
@@ -8,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -120,6 +122,20 @@ def load() -> ctypes.CDLL:
             lib.conv3d_fp8_destroy.argtypes = [vp]
             lib.conv3d_fp8_strerror.restype = ctypes.c_char_p
             lib.conv3d_fp8_strerror.argtypes = [ci]
+            cq = ctypes.c_longlong
+            for name in ("rmsnorm_q8_run", "silu_mul_q8_run"):
+                getattr(lib, name).restype = ci
+                getattr(lib, name).argtypes = [ctypes.c_char_p]
+            lib.linear_q8_plan.restype = ci
+            lib.linear_q8_plan.argtypes = [ctypes.POINTER(vp), cq, cq, cq, ci, ci]
+            lib.linear_q8_run.restype = ci
+            lib.linear_q8_run.argtypes = [vp, ctypes.c_char_p]
+            lib.linear_q8_check.restype = ci
+            lib.linear_q8_check.argtypes = [vp]
+            lib.linear_q8_workspace_size.restype = ctypes.c_size_t
+            lib.linear_q8_workspace_size.argtypes = [vp]
+            lib.linear_q8_destroy.restype = None
+            lib.linear_q8_destroy.argtypes = [vp]
             _lib = lib
     return _lib
 
@@ -421,3 +437,164 @@ def conv3d_fp8_run_quantize_x(plan, x_src, w, scale_w, y, stride, pad, scale_x_o
                               stream=None) -> None:
     _raise(conv3d_fp8_run_quantize_x_status(plan, x_src, w, scale_w, y, stride, pad, scale_x_out,
                                             stream), "conv3d_fp8_run_quantize_x")
+
+
+# --------------------------------------------------- 8-bit codes with scales (include/q8.h)
+Q8_F32, Q8_BF16, Q8_F16 = 1, 2, 3
+Q8_INT8, Q8_E4M3 = 1, 2
+
+# The argument structs of include/q8.h, packed as C lays them out on a 64-bit host: one bytes object
+# crosses the boundary, which costs less than a dozen converted arguments.
+_RMSNORM_ARGS = struct.Struct("@6P4q2qP4ifi")
+_SILU_MUL_ARGS = struct.Struct("@4P3q2qP4i")
+_LINEAR_ARGS = struct.Struct("@6P6qP4i")
+
+_value_types = {}
+_code_types = {}
+_f32 = None  # torch.float32, once torch is imported
+
+
+def _q8_types():
+    global _f32
+    import torch
+    _f32 = torch.float32
+    _value_types.update({torch.float32: Q8_F32, torch.bfloat16: Q8_BF16, torch.float16: Q8_F16})
+    _code_types.update({torch.int8: Q8_INT8, torch.uint8: Q8_E4M3, torch.float8_e4m3fn: Q8_E4M3})
+
+
+def q8_code_type(dtype) -> int:
+    """Q8_INT8 for torch.int8, Q8_E4M3 for torch.float8_e4m3fn or torch.uint8 (e4m3 bytes)."""
+    if not _code_types:
+        _q8_types()
+    t = _code_types.get(dtype)
+    if t is None:
+        raise ValueError(f"codes are int8, float8_e4m3fn or uint8 (e4m3 bytes), not {dtype}")
+    return t
+
+
+def _q8_value_type(t, name) -> int:
+    if not _value_types:
+        _q8_types()
+    v = _value_types.get(t.dtype)
+    if v is None:
+        raise ValueError(f"{name} holds fp32, bfloat16 or float16 values, not {t.dtype}")
+    return v
+
+
+def _q8_matrix(t, name, shape=None, dtype=None):
+    """Pitch of a CUDA matrix whose rows are contiguous."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name}: expected a matrix with contiguous rows")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.stride(0)
+
+
+def _q8_vector(t, name, size, dtype=None):
+    if t.dim() != 1 or t.shape[0] != size or (size > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected {size} contiguous elements")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def _q8_device(*tensors) -> int:
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise ValueError("expected tensors of one device")
+    return d
+
+
+def rmsnorm_q8_run(x, weight, q, scale, eps, residual=None, residual_out=None,
+                   stream=None) -> None:
+    """h = x + residual; residual_out = h; q, scale = the codes of h / rms(h) * weight, a scale a
+    row. Matrices [rows, cols] with contiguous rows (any pitch); the codes' type is q's."""
+    shape = x.shape
+    value_type = _q8_value_type(x, "x")
+    x_pitch = _q8_matrix(x, "x")
+    rows, cols = shape
+    code_type = q8_code_type(q.dtype)
+    q_pitch = _q8_matrix(q, "q", shape)
+    r_ptr = out_ptr = r_pitch = out_pitch = 0
+    if residual is not None:
+        r_pitch, r_ptr = _q8_matrix(residual, "residual", shape, x.dtype), residual.data_ptr()
+    if residual_out is not None:
+        out_pitch = _q8_matrix(residual_out, "residual_out", shape, x.dtype)
+        out_ptr = residual_out.data_ptr()
+    args = _RMSNORM_ARGS.pack(
+        x.data_ptr(), r_ptr, _q8_vector(weight, "weight", cols), out_ptr, q.data_ptr(),
+        _q8_vector(scale, "scale", rows, _f32), x_pitch, r_pitch, out_pitch, q_pitch,
+        rows, cols, _stream(stream), value_type, _q8_value_type(weight, "weight"), code_type,
+        _q8_device(x, weight, q, scale, residual, residual_out), eps, 0)
+    _raise(load().rmsnorm_q8_run(args), "rmsnorm_q8_run")
+
+
+def silu_mul_q8_run(gate, up, q, scale, stream=None) -> None:
+    """q, scale = the codes of silu(gate) * up, a scale a row. Matrices [rows, cols] with contiguous
+    rows (any pitch; gate and up may be two halves of one matrix); the codes' type is q's."""
+    shape = gate.shape
+    value_type = _q8_value_type(gate, "gate")
+    gate_pitch = _q8_matrix(gate, "gate")
+    up_pitch = _q8_matrix(up, "up", shape, gate.dtype)
+    code_type = q8_code_type(q.dtype)
+    q_pitch = _q8_matrix(q, "q", shape)
+    rows, cols = shape
+    args = _SILU_MUL_ARGS.pack(
+        gate.data_ptr(), up.data_ptr(), q.data_ptr(),
+        _q8_vector(scale, "scale", rows, _f32), gate_pitch, up_pitch, q_pitch, rows, cols,
+        _stream(stream), value_type, code_type, _q8_device(gate, up, q, scale), 0)
+    _raise(load().silu_mul_q8_run(args), "silu_mul_q8_run")
+
+
+def linear_q8_plan(max_rows, N, K, code_type, device=0) -> int:
+    """Create a plan for products of up to max_rows tokens by an [N, K] weight (code_type: Q8_INT8
+    or Q8_E4M3); returns its handle."""
+    h = ctypes.c_void_p()
+    _raise(load().linear_q8_plan(ctypes.byref(h), max_rows, N, K, code_type, device),
+           "linear_q8_plan")
+    return h.value
+
+
+def linear_q8_run(plan, x, scale_x, w, scale_w, y, bias=None, stream=None) -> None:
+    """y[m, n] = scale_x[m] * scale_w[n] * sum_k x[m, k] * w[n, k] + bias[n]. x [rows, K] and
+    w [N, K] are codes of one type with row pitches that are multiples of 16, y is [rows, N]."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w: expected matrices")
+    rows, K = x.shape
+    N = w.shape[0]
+    code_type = q8_code_type(x.dtype)
+    if code_type != q8_code_type(w.dtype):
+        raise ValueError(f"x and w hold codes of one type, not {x.dtype} and {w.dtype}")
+    x_pitch = _q8_matrix(x, "x")
+    w_pitch = _q8_matrix(w, "w", (N, K))
+    y_pitch = _q8_matrix(y, "y", (rows, N))
+    b_ptr = b_type = 0
+    if bias is not None:
+        b_ptr, b_type = _q8_vector(bias, "bias", N), _q8_value_type(bias, "bias")
+    _q8_device(x, scale_x, w, scale_w, y, bias)
+    args = _LINEAR_ARGS.pack(
+        x.data_ptr(), _q8_vector(scale_x, "scale_x", rows, _f32), w.data_ptr(),
+        _q8_vector(scale_w, "scale_w", N, _f32), b_ptr, y.data_ptr(), x_pitch, w_pitch,
+        y_pitch, rows, N, K, _stream(stream), _q8_value_type(y, "y"), b_type, code_type, 0)
+    _raise(load().linear_q8_run(plan, args), "linear_q8_run")
+
+
+def linear_q8_check(plan) -> int:
+    """Synchronise and return (and clear) the plan's device status: CONV3D_OK or CONV3D_EDEVICE."""
+    return load().linear_q8_check(plan)
+
+
+def linear_q8_workspace_size(plan) -> int:
+    return int(load().linear_q8_workspace_size(plan))
+
+
+def linear_q8_destroy(plan) -> None:
+    if plan:
+        load().linear_q8_destroy(plan)
