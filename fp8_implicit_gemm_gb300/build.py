@@ -23,7 +23,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libconv3d_fp8.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["api.cu", "pack.cu", "conv_tc.cu", "conv_tc_pair.cu", "quant.cu", "q8_api.cu",
-           "q8_rows.cu", "q8_linear.cu"]
+           "q8_rows.cu", "q8_linear_few.cu", "q8_linear_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                  "-I", INCLUDE, "-I", CSRC]

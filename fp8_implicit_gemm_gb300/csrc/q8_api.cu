@@ -1,4 +1,5 @@
 // q8_api.cu -- the C ABI declared in include/q8.h: validation, planning and launch.
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -10,8 +11,9 @@ struct linear_q8_plan_s {
   int device = -1;
   int code_type = 0;
   long long max_rows = 0, N = 0, K = 0;
-  void* workspace = nullptr;
-  size_t workspace_bytes = 0;
+  int pairs = 0;                   // CTA pairs the device holds at once
+  uint8_t* workspace = nullptr;    // x as f16 (int8), partial sums, arrival counters, status word
+  size_t part_off = 0, counter_off = 0, status_off = 0, workspace_bytes = 0;
 };
 
 namespace {
@@ -21,6 +23,17 @@ bool code_type_ok(int t) { return t == Q8_INT8 || t == Q8_E4M3; }
 int value_bytes(int t) { return t == Q8_F32 ? 4 : 2; }
 long long round_up(long long a, long long b) { return (a + b - 1) / b * b; }
 bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// Puts the current device back at the end of a scope.
+struct DeviceRestore {
+  int prev = -1;
+  DeviceRestore() {
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+  }
+  ~DeviceRestore() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
 
 // Whether `device` is the current device and an sm_103.
 conv3d_status check_device(int device) {
@@ -38,6 +51,13 @@ conv3d_status check_device(int device) {
   return major == 10 && minor == 3 ? CONV3D_OK : CONV3D_EUNSUPPORTED;
 }
 
+// The status of a launch; its error, if any, is not left behind for the caller's next CUDA call.
+conv3d_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return CONV3D_OK;
+  cudaGetLastError();
+  return CONV3D_ECUDA;
+}
+
 // A matrix argument: its pointer, the alignment it needs and its pitch (which a single row has no
 // use for).
 bool matrix_ok(const void* p, int align, long long rows, long long pitch, long long cols) {
@@ -50,6 +70,52 @@ conv3d_status check_rows(long long rows, long long cols, int value_type, int cod
     return CONV3D_EINVAL;
   if (cols > Q8_MAX_COLS || rows >= (1LL << 31)) return CONV3D_EUNSUPPORTED;
   return CONV3D_OK;
+}
+
+constexpr unsigned long long kLinearTimeoutNs = 2000ull * 1000ull * 1000ull;
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(ptr);
+  }();
+  return fn;
+}
+
+// A matrix of `rows` rows of `cols` elements (1 byte, or f16), loaded in boxes of 128 bytes by
+// box_rows rows with the 128-byte swizzle; what lies outside reads zero.
+bool encode_rows(CUtensorMap* map, const void* base, int elem, long long rows, long long cols,
+                 long long pitch, int box_rows) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(pitch * elem)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether every row starts on the grid of the vector accesses. A pitch counts only between rows.
+bool rows_aligned(const RowsParams& p, int vb) {
+  const bool one = p.rows <= 1;
+  auto on = [&](const void* m, long long pitch, int grid, int elem) {
+    return !m || (aligned(m, grid) && (one || pitch * elem % grid == 0));
+  };
+  return on(p.a, p.a_pitch, 16, vb) && on(p.b, p.b_pitch, 16, vb) &&
+         on(p.sum_out, p.sum_pitch, 16, vb) && on(p.q, p.q_pitch, 8, 1);
 }
 
 }  // namespace
@@ -86,11 +152,12 @@ extern "C" conv3d_status rmsnorm_q8_run(const rmsnorm_q8_args* a) {
   p.q_pitch = a->q_pitch;
   p.rows = a->rows;
   p.cols = (int)a->cols;
+  p.code_type = a->code_type;
+  p.weight_type = a->weight_type;
   p.eps = a->eps;
-  return launch_rmsnorm_q8(p, a->value_type, a->weight_type, a->code_type,
-                           static_cast<cudaStream_t>(a->stream)) == cudaSuccess
-             ? CONV3D_OK
-             : CONV3D_ECUDA;
+  const bool vec = rows_aligned(p, vb) && aligned(p.weight, 16);
+  return launched(
+      launch_rows_q8(p, a->value_type, true, vec, static_cast<cudaStream_t>(a->stream)));
 }
 
 extern "C" conv3d_status silu_mul_q8_run(const silu_mul_q8_args* a) {
@@ -115,10 +182,9 @@ extern "C" conv3d_status silu_mul_q8_run(const silu_mul_q8_args* a) {
   p.q_pitch = a->q_pitch;
   p.rows = a->rows;
   p.cols = (int)a->cols;
-  return launch_silu_mul_q8(p, a->value_type, a->code_type,
-                            static_cast<cudaStream_t>(a->stream)) == cudaSuccess
-             ? CONV3D_OK
-             : CONV3D_ECUDA;
+  p.code_type = a->code_type;
+  return launched(launch_rows_q8(p, a->value_type, false, rows_aligned(p, vb),
+                                 static_cast<cudaStream_t>(a->stream)));
 }
 
 extern "C" conv3d_status linear_q8_plan(linear_q8_plan_t* plan, long long max_rows, long long N,
@@ -136,6 +202,38 @@ extern "C" conv3d_status linear_q8_plan(linear_q8_plan_t* plan, long long max_ro
   pl->max_rows = max_rows;
   pl->N = N;
   pl->K = K;
+  if (max_rows > kFewTokens) {
+    int sms = 0;
+    if (linear_tc_setup() != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+      cudaGetLastError();
+      delete pl;
+      return CONV3D_ECUDA;
+    }
+    const int held = linear_tc_max_pairs();
+    pl->pairs = held > 0 ? std::min(held, sms / 2) : sms / 2;
+    // Split tiles are at most as many as the pairs: a tile of 256 channels by up to 256 tokens each.
+    const long long xh = code_type == Q8_INT8 ? max_rows * round_up(K, 16) * 2 : 0;
+    const long long tokens = std::min<long long>(kTcMaxTokens, round_up(max_rows, 32));
+    pl->part_off = (size_t)round_up(xh, 256);
+    pl->counter_off = pl->part_off + (size_t)(pl->pairs * tokens * kTcChannels * 4);
+    pl->status_off = pl->counter_off + (size_t)round_up(pl->pairs * 2 * 4, 256);
+    pl->workspace_bytes = pl->status_off + 256;
+    if (cudaMalloc(&pl->workspace, pl->workspace_bytes) != cudaSuccess) {
+      cudaGetLastError();
+      delete pl;
+      return CONV3D_ENOMEM;
+    }
+    // the counters and the status word are zero between runs; on every stream from here on
+    if (cudaMemset(pl->workspace + pl->counter_off, 0, pl->workspace_bytes - pl->counter_off) !=
+            cudaSuccess ||
+        cudaDeviceSynchronize() != cudaSuccess) {
+      cudaGetLastError();
+      cudaFree(pl->workspace);
+      delete pl;
+      return CONV3D_ECUDA;
+    }
+  }
   *plan = pl;
   return CONV3D_OK;
 }
@@ -177,14 +275,46 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
   p.K = (int)plan->K;
   p.y_type = a->y_type;
   p.bias_type = a->bias_type;
-  return launch_linear_q8(p, plan->code_type, static_cast<cudaStream_t>(a->stream)) == cudaSuccess
-             ? CONV3D_OK
-             : CONV3D_ECUDA;
+  cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
+  if (p.M <= kFewTokens)
+    return launched(launch_linear_few(p, plan->code_type, stream));
+  const bool int8 = plan->code_type == Q8_INT8;
+  linear_tc_decide(p, plan->code_type, plan->pairs);
+  p.xh = reinterpret_cast<uint16_t*>(plan->workspace);
+  p.xh_pitch = round_up(plan->K, 16);
+  p.partials = reinterpret_cast<float*>(plan->workspace + plan->part_off);
+  p.counters = reinterpret_cast<unsigned*>(plan->workspace + plan->counter_off);
+  p.status = reinterpret_cast<int*>(plan->workspace + plan->status_off);
+  p.timeout_ns = kLinearTimeoutNs;
+  CUtensorMap wmap{}, xmap{};
+  if (!encode_rows(&wmap, p.w, 1, p.N, p.K, p.w_pitch, kTcWBoxRows) ||
+      !(int8 ? encode_rows(&xmap, p.xh, 2, p.M, p.K, p.xh_pitch, p.block_t / 2)
+             : encode_rows(&xmap, p.x, 1, p.M, p.K, p.x_pitch, p.block_t / 2)))
+    return CONV3D_ECUDA;
+  if (int8) {
+    const conv3d_status st = launched(launch_linear_expand(p, stream));
+    if (st != CONV3D_OK) return st;
+  }
+  return launched(launch_linear_tc(p, plan->code_type, wmap, xmap, plan->pairs, stream));
 }
 
 extern "C" conv3d_status linear_q8_check(linear_q8_plan_t plan) {
   if (!plan) return CONV3D_EINVAL;
-  return cudaDeviceSynchronize() == cudaSuccess ? CONV3D_OK : CONV3D_ECUDA;
+  DeviceRestore restore;
+  if (cudaSetDevice(plan->device) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
+    return CONV3D_ECUDA;
+  if (!plan->workspace) return CONV3D_OK;
+  int word = 0;
+  if (cudaMemcpy(&word, plan->workspace + plan->status_off, sizeof(int), cudaMemcpyDeviceToHost) !=
+      cudaSuccess)
+    return CONV3D_ECUDA;
+  if (word == 0) return CONV3D_OK;
+  // a run that stopped early may have left arrivals behind: the next one starts from zero
+  if (cudaMemset(plan->workspace + plan->counter_off, 0,
+                 plan->workspace_bytes - plan->counter_off) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess)
+    return CONV3D_ECUDA;
+  return CONV3D_EDEVICE;
 }
 
 extern "C" size_t linear_q8_workspace_size(linear_q8_plan_t plan) {
@@ -192,5 +322,14 @@ extern "C" size_t linear_q8_workspace_size(linear_q8_plan_t plan) {
 }
 
 extern "C" void linear_q8_destroy(linear_q8_plan_t plan) {
+  if (!plan) return;
+  if (plan->workspace) {
+    DeviceRestore restore;
+    if (cudaSetDevice(plan->device) == cudaSuccess) {
+      cudaDeviceSynchronize();
+      cudaFree(plan->workspace);
+    }
+    cudaGetLastError();
+  }
   delete plan;
 }

@@ -2,6 +2,7 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "q8.h"
@@ -19,15 +20,17 @@ struct RowsParams {
   long long a_pitch, b_pitch, sum_pitch, q_pitch;  // elements
   long long rows;
   int cols;
+  int code_type, weight_type;
+  int row_threads;       // threads that hold one row (set by the launcher)
   float eps;
 };
 
-cudaError_t launch_rmsnorm_q8(const RowsParams& p, int value_type, int weight_type, int code_type,
-                              cudaStream_t stream);
-cudaError_t launch_silu_mul_q8(const RowsParams& p, int value_type, int code_type,
-                               cudaStream_t stream);
+// `aligned`: every base and pitch lies on the grid of 8 elements' accesses (16 bytes of values, 8 of
+// codes).
+cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, bool aligned,
+                           cudaStream_t stream);
 
-// One product y = (x * w^T) scaled.
+// One product y = scale_x * scale_w * (x * w^T) + bias.
 struct LinearParams {
   const uint8_t* x;
   const float* scale_x;
@@ -38,8 +41,36 @@ struct LinearParams {
   long long x_pitch, w_pitch, y_pitch;
   int M, N, K;           // tokens, channels, summed length
   int y_type, bias_type;
+  // the tensor-core kernel's tiling (linear_tc_decide) and workspace
+  int block_t;           // tokens of a tile (a tile has kTcChannels channels)
+  int m_tiles, n_tiles, k_blocks;
+  int splits, kb_per_split;
+  int stages, acc_bufs, acc_stride, a_slots;
+  uint16_t* xh;          // int8 only: x as f16, [M][xh_pitch]
+  long long xh_pitch;
+  float* partials;       // split tiles: [unit][rank][block_t][128]
+  unsigned* counters;    // split tiles: arrivals, [tile][rank], zero between runs
+  int* status;
+  unsigned long long timeout_ns;
 };
 
-cudaError_t launch_linear_q8(const LinearParams& p, int code_type, cudaStream_t stream);
+// Tokens that the kernel for few tokens takes at most; it needs no workspace.
+constexpr int kFewTokens = 16;
+cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t stream);
+
+// The tensor-core kernel: CTA pairs, tiles of 256 channels by block_t tokens.
+constexpr int kTcChannels = 256;
+constexpr int kTcBlockK = 128;         // codes of K a pipeline stage holds
+constexpr int kTcMaxTokens = 256;
+// Fills in the tiling of a product of M, N and K for `pairs` co-resident CTA pairs.
+void linear_tc_decide(LinearParams& p, int code_type, int pairs);
+// Boxes of the tensor maps: rows of w and of x (or xh) one CTA loads at a time.
+constexpr int kTcWBoxRows = 128;
+size_t linear_tc_smem_bytes(const LinearParams& p, int code_type);
+int linear_tc_max_pairs();             // CTA pairs the current device holds at once; 0: unknown
+cudaError_t linear_tc_setup();         // the kernels' shared-memory grant
+cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream);  // x -> xh
+cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
+                             const CUtensorMap& xmap, int pairs, cudaStream_t stream);
 
 }  // namespace c3d

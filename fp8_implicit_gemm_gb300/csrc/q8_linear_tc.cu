@@ -1,0 +1,504 @@
+// q8_linear_tc.cu -- products of 8-bit codes on the tensor cores (tcgen05, CTA pairs):
+// y[m][n] = scale_x[m] * scale_w[n] * sum_k x[m][k] * w[n][k] + bias[n].
+//
+// The channels are the rows of the MMA (M = 256 over the pair, 128 a CTA) and the tokens its columns
+// (N = block_t, 32 to 256), so that a batch of any size fills whole rows: the accumulator has a
+// channel in each TMEM lane and a token in each column, and a warp's stores of one token cover 32
+// consecutive channels of y.
+//
+// e4m3: both operands go from global memory to shared memory by TMA and into kind::f8f6f4.
+//
+// int8: sm_103a has no fast integer pipe, but an int8 code is exact in f16 (an 11-bit significand),
+// a product of two is an integer of at most 2^14, and the fp32 accumulator holds their sums exactly
+// up to 2^24. So the product runs as kind::f16, at the f16 rate, on codes turned into f16:
+//   - x, which every channel tile reads again, is expanded to f16 once by a small kernel before
+//     (3 bytes of traffic a code);
+//   - w stays 8 bits wide all the way to shared memory. Four converter warps read a row of 128 codes
+//     each thread, turn it into f16 (a byte under the exponent of 1024, minus 1152 with the sign bit
+//     flipped: a permute and a subtraction for each two codes) and write it to TMEM, from where the
+//     MMA takes its A operand. Shared memory then carries the codes once in and once out, and no f16
+//     copy of w: 96 bytes a cycle at 256 tokens in place of 192, of the 128 that it moves.
+//
+// Roles of a CTA: warps 0-3 epilogue, 4-7 converters (int8), 8 TMA, 9 MMA (the leader CTA's). Every
+// wait is bounded; one that runs out records a status bit and both CTAs wind down.
+#include <algorithm>
+
+#include "conv_common.cuh"
+#include "q8_common.cuh"
+
+namespace c3d {
+
+constexpr int kTcThreads = 320;
+constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // w's codes of one stage: 16 KB a CTA
+constexpr int kTcMaxStages = 8;
+constexpr int kTcSmemBudget = 200 * 1024;
+constexpr int kTcTmemCols = 512;
+constexpr int kTcSlotCols = kTcBlockK / 2;          // one stage of w in f16: 64 columns
+constexpr uint64_t kTcAbortSettleNs = 2ull * 1000 * 1000;  // let copies in flight land on abort
+
+// x's bytes of one stage of one CTA (half of the tile's tokens).
+__host__ __device__ inline uint32_t tc_x_bytes(int block_t, bool int8) {
+  return (uint32_t)(block_t / 2) * kTcBlockK * (int8 ? 2 : 1);
+}
+
+// One work unit: a tile and a slice [kb0, kb1) of the K blocks. Tiles are taken in groups of
+// kTcGroup channel tiles, tokens before the next group, so that the tiles of one wave share their
+// operands in L2 (8 x ~10 of them read 18 operand tiles; in plain order a wide w is read again for
+// each tile of tokens).
+constexpr int kTcGroup = 8;
+struct TcUnit {
+  int tile, m_tile, n_tile, kb0, kb1;
+};
+__device__ __forceinline__ TcUnit tc_unit(const LinearParams& p, int u) {
+  TcUnit r;
+  r.tile = u / p.splits;
+  const int split = u - r.tile * p.splits;
+  r.kb0 = split * p.kb_per_split;
+  r.kb1 = min(r.kb0 + p.kb_per_split, p.k_blocks);
+  const int per_group = kTcGroup * p.m_tiles;
+  const int group = r.tile / per_group;
+  const int rest = r.tile - group * per_group;
+  const int width = min(kTcGroup, p.n_tiles - group * kTcGroup);
+  r.m_tile = rest / width;
+  r.n_tile = group * kTcGroup + (rest - r.m_tile * width);
+  return r;
+}
+
+template <bool kInt8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+    linear_q8_tc_kernel(const __grid_constant__ CUtensorMap wmap,
+                        const __grid_constant__ CUtensorMap xmap, const LinearParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
+  const int S = p.stages;
+  const uint32_t x_bytes = tc_x_bytes(p.block_t, kInt8);
+  uint8_t* sW = smem;
+  uint8_t* sX = smem + (size_t)S * kTcWBytes;
+  float* sScale = reinterpret_cast<float*>(sX + (size_t)S * x_bytes);  // [4 warps][kTcMaxTokens]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + 4 * kTcMaxTokens);
+  // bars: full[S] (the leader's; e4m3: both operands, int8: x), empty[S], w_full[S] (int8),
+  // slot_full[4] (the leader's), slot_empty[4], acc_full[2], acc_empty[2] (the leader's), drain
+  const uint32_t bars_u32 = smem_u32(bars);
+  auto full = [&](int s) { return bars_u32 + 8u * s; };
+  auto empty = [&](int s) { return bars_u32 + 8u * (kTcMaxStages + s); };
+  auto w_full = [&](int s) { return bars_u32 + 8u * (2 * kTcMaxStages + s); };
+  auto slot_full = [&](int s) { return bars_u32 + 8u * (3 * kTcMaxStages + s); };
+  auto slot_empty = [&](int s) { return bars_u32 + 8u * (3 * kTcMaxStages + 4 + s); };
+  auto acc_full = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 8 + b); };
+  auto acc_empty = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 10 + b); };
+  const uint32_t drain_bar = bars_u32 + 8u * (3 * kTcMaxStages + 12);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kTcMaxStages + 13);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile unsigned* last_flag = reinterpret_cast<volatile unsigned*>(tmem_slot + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const uint32_t leader_bars = map_to_cta(bars_u32, 0);
+  const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  const int num_units = p.m_tiles * p.n_tiles * p.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+      mbar_init(w_full(s), 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(slot_full(s), 2 * 4);  // a converter warp's arrival each, of both CTAs
+      mbar_init(slot_empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 2 * 4);  // an epilogue warp's arrival each, of both CTAs
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTcTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tensormap(&wmap);
+    prefetch_tensormap(&xmap);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before anyone signals across the pair
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t slots_base = tmem_base + (uint32_t)(p.acc_bufs * p.acc_stride);
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const AbortState ab{abort_flag, p.status, p.timeout_ns};
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------------------ epilogue
+    float* scale = sScale + warp * kTcMaxTokens;
+    int buf = 0;
+    uint32_t phase = 0;
+    for (int u = pair_id; u < num_units; u += num_pairs) {
+      const TcUnit un = tc_unit(p, u);
+      const long long n = (long long)un.n_tile * kTcChannels + rank * 128 + threadIdx.x;
+      const bool n_ok = n < p.N;
+      const long long m0 = (long long)un.m_tile * p.block_t;
+      const int tokens = (int)min((long long)p.block_t, p.M - m0);
+      __syncwarp();
+      for (int t = lane; t < p.block_t; t += 32) scale[t] = t < tokens ? p.scale_x[m0 + t] : 0.0f;
+      ScaleBias sc{0.0f, 0.0f};
+      if (n_ok) {
+        sc.w = __ldg(p.scale_w + n);
+        if (p.bias) sc.bias = q8_load_value(p.bias, p.bias_type, n);
+      }
+      __syncwarp();
+      bool ok = wait_bounded_warp<true>(acc_full(buf), phase, ab, kStatusWaitAccFull);
+      if (p.splits > 1) ok = named_barrier_and(1, 128, ok);  // the four warps join the partials
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t trow = tmem_base + (uint32_t)(buf * p.acc_stride) + ((uint32_t)(warp * 32) << 16);
+      if (p.splits == 1) {
+        for (int c = 0; c < p.block_t; c += 32) {
+          if (c >= tokens) break;
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(trow + c, r);
+          tmem_ld_wait();
+          if (n_ok) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c + j < tokens)
+                q8_store_value(p.y, p.y_type, (m0 + c + j) * p.y_pitch + n,
+                               sc(__uint_as_float(r[j]), scale[c + j]));
+          }
+        }
+      } else {
+        float* part = p.partials + ((long long)u * 2 + rank) * p.block_t * 128 + threadIdx.x;
+        for (int c = 0; c < p.block_t; c += 32) {
+          if (c >= tokens) break;
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(trow + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c + j < tokens) __stcg(part + (c + j) * 128, __uint_as_float(r[j]));
+        }
+        // The last of a tile's slices to arrive adds them all up, in their order.
+        __threadfence();
+        named_barrier_sync(1, 128);
+        if (threadIdx.x == 0) {
+          unsigned* counter = p.counters + un.tile * 2 + rank;
+          const unsigned before = atomicAdd(counter, 1u);
+          const bool last = before + 1 == (unsigned)p.splits;
+          if (last) *counter = 0;  // for the next run
+          *last_flag = last;
+        }
+        named_barrier_sync(1, 128);
+        if (*last_flag) {
+          __threadfence();
+          const long long slice = 2LL * p.block_t * 128;
+          const float* first = p.partials +
+                               ((long long)un.tile * p.splits * 2 + rank) * p.block_t * 128 +
+                               threadIdx.x;
+          for (int c = 0; c < tokens; c += 8) {
+            float acc[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = c + j < tokens ? __ldcg(first + (c + j) * 128) : 0.0f;
+            for (int s = 1; s < p.splits; ++s)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (c + j < tokens) acc[j] += __ldcg(first + s * slice + (c + j) * 128);
+            if (n_ok) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (c + j < tokens)
+                  q8_store_value(p.y, p.y_type, (m0 + c + j) * p.y_pitch + n,
+                                 sc(acc[j], scale[c + j]));
+            }
+          }
+        }
+        named_barrier_sync(1, 128);  // last_flag is read before it is written again
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_bars + (acc_empty(buf) - bars_u32));
+      if (++buf == p.acc_bufs) {
+        buf = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------------------- converters
+    if (kInt8) {
+      const int row = (warp - 4) * 32 + lane;
+      const uint32_t lane_base = (uint32_t)((warp - 4) * 32) << 16;
+      Ring ring, slots;
+      bool aborted = false;
+      for (int u = pair_id; u < num_units && !aborted; u += num_pairs) {
+        const TcUnit un = tc_unit(p, u);
+        for (int kb = un.kb0; kb < un.kb1; ++kb) {
+          if (!wait_bounded_warp(w_full(ring.stage), ring.phase, ab, kStatusWaitFull)) {
+            aborted = true;
+            break;
+          }
+          const uint8_t* src = sW + (size_t)ring.stage * kTcWBytes + row * kTcBlockK;
+          uint4 c[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)  // 16-byte chunk i of the row, where the swizzle put it
+            c[i] = *reinterpret_cast<const uint4*>(src + ((i ^ (row & 7)) << 4));
+          if (!wait_bounded_warp<true>(slot_empty(slots.stage), slots.phase ^ 1u, ab,
+                                       kStatusWaitEmpty)) {
+            aborted = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t dst = slots_base + lane_base + (uint32_t)(slots.stage * kTcSlotCols);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t h[32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) int8_to_f16(c[4 * half + i], h + 8 * i);
+            tmem_st_32x32b_x32(dst + 32 * half, h);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader_bars + (slot_full(slots.stage) - bars_u32));
+          ring.next(S);
+          slots.next(p.a_slots);
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------------------ TMA loader
+    Ring ring;
+    bool aborted = false;
+    const int half_t = p.block_t / 2;
+    for (int u = pair_id; u < num_units && !aborted; u += num_pairs) {
+      const TcUnit un = tc_unit(p, u);
+      const int n0 = un.n_tile * kTcChannels + (int)rank * 128;
+      const int m0 = un.m_tile * p.block_t + (int)rank * half_t;
+      for (int kb = un.kb0; kb < un.kb1; ++kb) {
+        const int s = ring.stage;
+        if (!wait_bounded_warp<true>(empty(s), ring.phase ^ 1u, ab, kStatusWaitEmpty)) {
+          aborted = true;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t bar = leader_bars + (full(s) - bars_u32);
+          const uint32_t w_dst = smem_u32(sW) + (uint32_t)s * kTcWBytes;
+          const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * x_bytes;
+          const int k0 = kb * kTcBlockK;
+          if (kInt8) {
+            mbar_arrive_expect_tx(w_full(s), kTcWBytes);
+            tma_load_2d(w_dst, &wmap, w_full(s), k0, n0);
+            if (leader) mbar_arrive_expect_tx(full(s), 2 * x_bytes);
+            tma_load_2d_pair(x_dst, &xmap, bar, k0, m0);
+            tma_load_2d_pair(x_dst + x_bytes / 2, &xmap, bar, k0 + kTcBlockK / 2, m0);
+          } else {
+            if (leader) mbar_arrive_expect_tx(full(s), 2 * (kTcWBytes + x_bytes));
+            tma_load_2d_pair(w_dst, &wmap, bar, k0, n0);
+            tma_load_2d_pair(x_dst, &xmap, bar, k0, m0);
+          }
+        }
+        __syncwarp();
+        ring.next(S);
+      }
+    }
+  } else if (leader) {
+    // ------------------------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = kInt8 ? make_idesc_f16_f32(kTcChannels, (uint32_t)p.block_t)
+                                 : make_idesc_e4m3_f32(kTcChannels, (uint32_t)p.block_t);
+    const uint64_t wdesc0 = make_sw128_kmajor_desc(smem_u32(sW));
+    const uint64_t xdesc0 = make_sw128_kmajor_desc(smem_u32(sX));
+    Ring ring, slots;
+    int buf = 0;
+    uint32_t phase = 0;
+    bool aborted = false;
+    for (int u = pair_id; u < num_units && !aborted; u += num_pairs) {
+      const TcUnit un = tc_unit(p, u);
+      if (!wait_bounded_warp<true>(acc_empty(buf), phase ^ 1u, ab, kStatusWaitAccEmpty)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + (uint32_t)(buf * p.acc_stride);
+      for (int kb = un.kb0; kb < un.kb1; ++kb) {
+        const int s = ring.stage;
+        bool ok = wait_bounded_warp<true>(full(s), ring.phase, ab, kStatusWaitFull);
+        if (kInt8 && ok)
+          ok = wait_bounded_warp<true>(slot_full(slots.stage), slots.phase, ab, kStatusWaitFull);
+        if (!ok) {
+          aborted = true;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t acc0 = kb > un.kb0 ? 1u : 0u;
+          const int rem = p.K - kb * kTcBlockK;  // codes past K are zeros, and mostly left out
+          const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 4));
+          if (kInt8) {
+            const uint32_t a = slots_base + (uint32_t)(slots.stage * kTcSlotCols);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (16 * j < rem)
+                mma_f16_pair_tmem_a(d, a + 8 * j, xdesc + (j >> 2) * (x_bytes >> 5) + 2 * (j & 3),
+                                    idesc, j > 0 ? 1u : acc0);
+            mma_commit_pair(slot_empty(slots.stage), 0x3);
+          } else {
+            const uint64_t wdesc = wdesc0 + (uint64_t)((uint32_t)s * (kTcWBytes >> 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (32 * j < rem)
+                mma_f8f6f4_pair(d, wdesc + 2 * j, xdesc + 2 * j, idesc, j > 0 ? 1u : acc0);
+          }
+          mma_commit_pair(empty(s), 0x3);
+          if (kb + 1 == un.kb1) mma_commit_pair(acc_full(buf), 0x3);
+        }
+        __syncwarp();
+        ring.next(S);
+        slots.next(p.a_slots);
+      }
+      if (++buf == p.acc_bufs) {
+        buf = 0;
+        phase ^= 1u;
+      }
+    }
+    // every MMA of the pair is complete before TMEM is released
+    if (elect_one()) mma_commit_pair(drain_bar, 0x1);
+    __syncwarp();
+    wait_drain(drain_bar, 0, p.timeout_ns, p.status, kStatusWaitDrain);
+  }
+  __syncwarp();
+  if (*abort_flag) sleep_ns_bounded(kTcAbortSettleNs);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still signal or read its memory
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc_pair(tmem_base, kTcTmemCols);
+}
+
+// x's int8 codes as f16, 16 a thread and step.
+__global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int per_row = (p.K + 15) / 16;  // the codes past K, inside the pitch, are not read later
+  const long long total = (long long)p.M * per_row;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const long long m = i / per_row;
+    const int c = (int)(i - m * per_row);
+    uint32_t h[8];
+    int8_to_f16(__ldg(reinterpret_cast<const uint4*>(p.x + m * p.x_pitch) + c), h);
+    uint4* dst = reinterpret_cast<uint4*>(p.xh + m * p.xh_pitch) + 2 * c;
+    dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
+
+void linear_tc_decide(LinearParams& p, int code_type, int pairs) {
+  const bool int8 = code_type == Q8_INT8;
+  p.n_tiles = (p.N + kTcChannels - 1) / kTcChannels;
+  p.k_blocks = (p.K + kTcBlockK - 1) / kTcBlockK;
+  // Tokens of a tile: the size whose waves of tiles take the fewest tensor-core cycles. A K block of
+  // a 256 x t tile takes 4t cycles of f16 MMAs (2t of e4m3's), never less than its operands' bytes
+  // take to arrive (16 KB of w a CTA at the SM's share of the memory, about 24 bytes a cycle; the
+  // tile's x comes from L2). An epilogue that no second accumulator hides costs about 8 cycles a
+  // token.
+  double best = 1e300;
+  for (int t = 32; t <= kTcMaxTokens && t < p.M + 32; t += 32) {
+    const long long m_tiles = (p.M + t - 1) / t, tiles = m_tiles * p.n_tiles;
+    const bool two = !int8 || t <= 192;
+    const double kb = std::max(int8 ? 4.0 * t : 2.0 * t, 700.0);
+    long long splits = 1;
+    if (tiles * 2 <= pairs) splits = std::max<long long>(1, std::min<long long>(pairs / tiles, p.k_blocks / 4));
+    const long long waves = (tiles * splits + pairs - 1) / pairs;
+    const double unit = (double)((p.k_blocks + splits - 1) / splits) * kb + (two ? 0.0 : 8.0 * t);
+    const double cost = waves * unit + 8.0 * t;
+    if (cost < best) {
+      best = cost;
+      p.block_t = t;
+      p.m_tiles = (int)m_tiles;
+      p.splits = (int)splits;
+    }
+  }
+  p.kb_per_split = (p.k_blocks + p.splits - 1) / p.splits;
+  p.splits = (p.k_blocks + p.kb_per_split - 1) / p.kb_per_split;
+  if (!int8) {
+    p.acc_bufs = 2;
+    p.acc_stride = kTcMaxTokens;
+    p.a_slots = 1;
+  } else {
+    p.acc_bufs = p.block_t <= 192 ? 2 : 1;
+    p.acc_stride = p.block_t <= 128 ? 128 : (p.block_t <= 192 ? 192 : 256);
+    p.a_slots = (kTcTmemCols - p.acc_bufs * p.acc_stride) / kTcSlotCols;  // 4 or 2
+  }
+  const int stage = kTcWBytes + (int)tc_x_bytes(p.block_t, int8);
+  p.stages = std::min(kTcMaxStages, kTcSmemBudget / stage);
+}
+
+size_t linear_tc_smem_bytes(const LinearParams& p, int code_type) {
+  return 1024 + (size_t)p.stages * (kTcWBytes + tc_x_bytes(p.block_t, code_type == Q8_INT8)) +
+         4 * kTcMaxTokens * sizeof(float) + (3 * kTcMaxStages + 13) * 8 + 16;
+}
+
+cudaError_t linear_tc_setup() {
+  const int most = 1024 + kTcSmemBudget + 4 * kTcMaxTokens * 4 + (3 * kTcMaxStages + 13) * 8 + 16;
+  cudaError_t e = cudaFuncSetAttribute(linear_q8_tc_kernel<true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(linear_q8_tc_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  return e;
+}
+
+int linear_tc_max_pairs() {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kTcThreads, 1, 1);
+  cfg.dynamicSmemBytes = kTcSmemBudget;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, linear_q8_tc_kernel<true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+template <typename Kernel, typename... Args>
+static cudaError_t launch_pdl(Kernel kernel, int grid, int block, size_t smem, cudaStream_t stream,
+                              const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream) {
+  const long long total = (long long)p.M * ((p.K + 15) / 16);
+  const int grid = (int)std::min<long long>((total + 255) / 256, 152 * 8);
+  return launch_pdl(linear_expand_kernel, grid, 256, 0, stream, p);
+}
+
+cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
+                             const CUtensorMap& xmap, int pairs, cudaStream_t stream) {
+  const long long units = (long long)p.m_tiles * p.n_tiles * p.splits;
+  const int grid = 2 * (int)std::min<long long>(units, pairs);
+  const size_t smem = linear_tc_smem_bytes(p, code_type);
+  if (code_type == Q8_INT8)
+    return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads, smem, stream, wmap, xmap, p);
+  return launch_pdl(linear_q8_tc_kernel<false>, grid, kTcThreads, smem, stream, wmap, xmap, p);
+}
+
+}  // namespace c3d
