@@ -39,6 +39,12 @@ class Options(ctypes.Structure):
                 ("overlap", ctypes.c_int)]
 
 
+class LinearOptions(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int), ("block_t", ctypes.c_int), ("splits", ctypes.c_int),
+                ("max_ctas", ctypes.c_int), ("wait_timeout_ms", ctypes.c_int),
+                ("debug_flags", ctypes.c_int)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("Do", ctypes.c_int), ("Ho", ctypes.c_int), ("Wo", ctypes.c_int),
                 ("npq", ctypes.c_longlong), ("k_gemm", ctypes.c_int), ("block_m", ctypes.c_int),
@@ -128,6 +134,9 @@ def load() -> ctypes.CDLL:
                 getattr(lib, name).argtypes = [ctypes.c_char_p]
             lib.linear_q8_plan.restype = ci
             lib.linear_q8_plan.argtypes = [ctypes.POINTER(vp), cq, cq, cq, ci, ci]
+            lib.linear_q8_plan_ex.restype = ci
+            lib.linear_q8_plan_ex.argtypes = ([ctypes.POINTER(vp), cq, cq, cq, ci, ci]
+                                              + [ctypes.POINTER(LinearOptions)])
             lib.linear_q8_run.restype = ci
             lib.linear_q8_run.argtypes = [vp, ctypes.c_char_p]
             lib.linear_q8_check.restype = ci
@@ -553,12 +562,19 @@ def silu_mul_q8_run(gate, up, q, scale, stream=None) -> None:
     _raise(load().silu_mul_q8_run(args), "silu_mul_q8_run")
 
 
-def linear_q8_plan(max_rows, N, K, code_type, device=0) -> int:
+def linear_q8_plan(max_rows, N, K, code_type, device=0, **options) -> int:
     """Create a plan for products of up to max_rows tokens by an [N, K] weight (code_type: Q8_INT8
-    or Q8_E4M3); returns its handle."""
+    or Q8_E4M3); returns its handle. Keyword options (0 = the library's choice): kernel, block_t,
+    splits, max_ctas, wait_timeout_ms, debug_flags; see linear_q8_options in include/q8.h."""
+    lib = load()
     h = ctypes.c_void_p()
-    _raise(load().linear_q8_plan(ctypes.byref(h), max_rows, N, K, code_type, device),
-           "linear_q8_plan")
+    if not options:
+        st = lib.linear_q8_plan(ctypes.byref(h), max_rows, N, K, code_type, device)
+    else:
+        o = LinearOptions(**{k: int(v) for k, v in options.items()})
+        st = lib.linear_q8_plan_ex(ctypes.byref(h), max_rows, N, K, code_type, device,
+                                   ctypes.byref(o))
+    _raise(st, "linear_q8_plan")
     return h.value
 
 

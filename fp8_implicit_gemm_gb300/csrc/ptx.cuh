@@ -77,6 +77,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                : "memory");
 }
 
+// The same arrival for a thread that has only tcgen05 work to hand over, which its
+// tcgen05.fence::before_thread_sync orders: release at CTA scope. Release at cluster scope waits for
+// the thread's other memory operations first, which was measured to cost a converter warp about a
+// thousand cycles each time.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 // Shared abort state of one CTA: the first role whose wait runs out sets `flag`, records the
 // reason in the global status word and every other role stops at its next wait.
 struct AbortState {

@@ -11,9 +11,12 @@ struct linear_q8_plan_s {
   int device = -1;
   int code_type = 0;
   long long max_rows = 0, N = 0, K = 0;
-  int pairs = 0;                   // CTA pairs the device holds at once
-  uint8_t* workspace = nullptr;    // x as f16 (int8), partial sums, arrival counters, status word
-  size_t part_off = 0, counter_off = 0, status_off = 0, workspace_bytes = 0;
+  TcLimits lim{};
+  int few = kFewTokens;            // tokens up to which the kernel for few tokens runs
+  unsigned long long timeout_ns = 0;
+  int debug_flags = 0;
+  uint8_t* workspace = nullptr;    // x as f16 (int8), status word
+  size_t status_off = 0, workspace_bytes = 0;
 };
 
 namespace {
@@ -189,10 +192,23 @@ extern "C" conv3d_status silu_mul_q8_run(const silu_mul_q8_args* a) {
 
 extern "C" conv3d_status linear_q8_plan(linear_q8_plan_t* plan, long long max_rows, long long N,
                                         long long K, int code_type, int device) {
+  return linear_q8_plan_ex(plan, max_rows, N, K, code_type, device, nullptr);
+}
+
+extern "C" conv3d_status linear_q8_plan_ex(linear_q8_plan_t* plan, long long max_rows, long long N,
+                                           long long K, int code_type, int device,
+                                           const linear_q8_options* opts) {
   if (!plan) return CONV3D_EINVAL;
   *plan = nullptr;
   if (max_rows < 1 || N < 1 || K < 1 || !code_type_ok(code_type)) return CONV3D_EINVAL;
+  linear_q8_options o{};
+  if (opts) o = *opts;
+  if (o.kernel < 0 || o.kernel > 2 || o.block_t < 0 || o.block_t > kTcMaxTokens ||
+      o.block_t % 32 != 0 || (o.splits != 0 && o.splits != 1 && o.splits != 2 && o.splits != 4) ||
+      o.max_ctas < 0 || o.wait_timeout_ms < 0)
+    return CONV3D_EINVAL;
   if (max_rows >= (1LL << 30) || N >= (1LL << 30) || K >= (1LL << 30)) return CONV3D_EUNSUPPORTED;
+  if (o.kernel == 1 && max_rows > kFewTokens) return CONV3D_EUNSUPPORTED;
   const conv3d_status st = check_device(device);
   if (st != CONV3D_OK) return st;
   linear_q8_plan_s* pl = new (std::nothrow) linear_q8_plan_s();
@@ -202,31 +218,31 @@ extern "C" conv3d_status linear_q8_plan(linear_q8_plan_t* plan, long long max_ro
   pl->max_rows = max_rows;
   pl->N = N;
   pl->K = K;
-  if (max_rows > kFewTokens) {
-    int sms = 0;
-    if (linear_tc_setup() != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+  pl->few = o.kernel == 2 ? 0 : kFewTokens;
+  pl->timeout_ns = o.wait_timeout_ms > 0 ? o.wait_timeout_ms * 1000000ull : kLinearTimeoutNs;
+  pl->debug_flags = o.debug_flags;
+  if (max_rows > pl->few) {
+    if (linear_tc_setup() != cudaSuccess || linear_tc_max_clusters(pl->lim.clusters) != cudaSuccess) {
       cudaGetLastError();
       delete pl;
       return CONV3D_ECUDA;
     }
-    const int held = linear_tc_max_pairs();
-    pl->pairs = held > 0 ? std::min(held, sms / 2) : sms / 2;
-    // Split tiles are at most as many as the pairs: a tile of 256 channels by up to 256 tokens each.
+    for (int i = 0; i < 3; ++i)
+      if (o.max_ctas > 0)
+        pl->lim.clusters[i] = std::min(pl->lim.clusters[i], o.max_ctas / (2 << i));
+    // a forced tile no larger than the tokens need, forced slices no more than K has blocks
+    pl->lim.block_t = o.block_t;
+    pl->lim.splits = o.splits;
     const long long xh = code_type == Q8_INT8 ? max_rows * round_up(K, 16) * 2 : 0;
-    const long long tokens = std::min<long long>(kTcMaxTokens, round_up(max_rows, 32));
-    pl->part_off = (size_t)round_up(xh, 256);
-    pl->counter_off = pl->part_off + (size_t)(pl->pairs * tokens * kTcChannels * 4);
-    pl->status_off = pl->counter_off + (size_t)round_up(pl->pairs * 2 * 4, 256);
+    pl->status_off = (size_t)round_up(xh, 256);
     pl->workspace_bytes = pl->status_off + 256;
     if (cudaMalloc(&pl->workspace, pl->workspace_bytes) != cudaSuccess) {
       cudaGetLastError();
       delete pl;
       return CONV3D_ENOMEM;
     }
-    // the counters and the status word are zero between runs; on every stream from here on
-    if (cudaMemset(pl->workspace + pl->counter_off, 0, pl->workspace_bytes - pl->counter_off) !=
-            cudaSuccess ||
+    // the status word is zero between runs; on every stream from here on
+    if (cudaMemset(pl->workspace + pl->status_off, 0, 256) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
       cudaGetLastError();
       cudaFree(pl->workspace);
@@ -275,17 +291,19 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
   p.K = (int)plan->K;
   p.y_type = a->y_type;
   p.bias_type = a->bias_type;
+  const int yb = value_bytes(a->y_type);
+  p.y_vec = aligned(a->y, 4 * yb) && (p.M <= 1 || p.y_pitch % 4 == 0);
   cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
-  if (p.M <= kFewTokens)
+  if (p.M <= plan->few)
     return launched(launch_linear_few(p, plan->code_type, stream));
   const bool int8 = plan->code_type == Q8_INT8;
-  linear_tc_decide(p, plan->code_type, plan->pairs);
+  linear_tc_decide(p, plan->code_type, plan->lim);
+  if (!p.block_t) return CONV3D_EUNSUPPORTED;  // the options leave no tiling for this many tokens
   p.xh = reinterpret_cast<uint16_t*>(plan->workspace);
   p.xh_pitch = round_up(plan->K, 16);
-  p.partials = reinterpret_cast<float*>(plan->workspace + plan->part_off);
-  p.counters = reinterpret_cast<unsigned*>(plan->workspace + plan->counter_off);
   p.status = reinterpret_cast<int*>(plan->workspace + plan->status_off);
-  p.timeout_ns = kLinearTimeoutNs;
+  p.timeout_ns = plan->timeout_ns;
+  p.debug_flags = plan->debug_flags;
   CUtensorMap wmap{}, xmap{};
   if (!encode_rows(&wmap, p.w, 1, p.N, p.K, p.w_pitch, kTcWBoxRows) ||
       !(int8 ? encode_rows(&xmap, p.xh, 2, p.M, p.K, p.xh_pitch, p.block_t / 2)
@@ -295,7 +313,7 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
     const conv3d_status st = launched(launch_linear_expand(p, stream));
     if (st != CONV3D_OK) return st;
   }
-  return launched(launch_linear_tc(p, plan->code_type, wmap, xmap, plan->pairs, stream));
+  return launched(launch_linear_tc(p, plan->code_type, wmap, xmap, plan->lim, stream));
 }
 
 extern "C" conv3d_status linear_q8_check(linear_q8_plan_t plan) {
@@ -309,10 +327,7 @@ extern "C" conv3d_status linear_q8_check(linear_q8_plan_t plan) {
       cudaSuccess)
     return CONV3D_ECUDA;
   if (word == 0) return CONV3D_OK;
-  // a run that stopped early may have left arrivals behind: the next one starts from zero
-  if (cudaMemset(plan->workspace + plan->counter_off, 0,
-                 plan->workspace_bytes - plan->counter_off) != cudaSuccess ||
-      cudaDeviceSynchronize() != cudaSuccess)
+  if (cudaMemset(plan->workspace + plan->status_off, 0, sizeof(int)) != cudaSuccess)
     return CONV3D_ECUDA;
   return CONV3D_EDEVICE;
 }

@@ -41,17 +41,17 @@ struct LinearParams {
   long long x_pitch, w_pitch, y_pitch;
   int M, N, K;           // tokens, channels, summed length
   int y_type, bias_type;
+  int y_vec;             // four channels of y may be stored at once
   // the tensor-core kernel's tiling (linear_tc_decide) and workspace
   int block_t;           // tokens of a tile (a tile has kTcChannels channels)
   int m_tiles, n_tiles, k_blocks;
-  int splits, kb_per_split;
+  int splits;            // slices of K, one for each pair of a cluster: 1, 2 or 4
   int stages, acc_bufs, acc_stride, a_slots;
   uint16_t* xh;          // int8 only: x as f16, [M][xh_pitch]
   long long xh_pitch;
-  float* partials;       // split tiles: [unit][rank][block_t][128]
-  unsigned* counters;    // split tiles: arrivals, [tile][rank], zero between runs
   int* status;
   unsigned long long timeout_ns;
+  int debug_flags;
 };
 
 // Tokens that the kernel for few tokens takes at most; it needs no workspace.
@@ -62,15 +62,20 @@ cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t
 constexpr int kTcChannels = 256;
 constexpr int kTcBlockK = 128;         // codes of K a pipeline stage holds
 constexpr int kTcMaxTokens = 256;
-// Fills in the tiling of a product of M, N and K for `pairs` co-resident CTA pairs.
-void linear_tc_decide(LinearParams& p, int code_type, int pairs);
+// What a plan's device and options allow.
+struct TcLimits {
+  int clusters[3];       // clusters of 2, 4 and 8 CTAs held at once
+  int block_t, splits;   // 0: the choice of linear_tc_decide
+};
+// Fills in the tiling of a product of M, N and K.
+void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim);
 // Boxes of the tensor maps: rows of w and of x (or xh) one CTA loads at a time.
 constexpr int kTcWBoxRows = 128;
 size_t linear_tc_smem_bytes(const LinearParams& p, int code_type);
-int linear_tc_max_pairs();             // CTA pairs the current device holds at once; 0: unknown
 cudaError_t linear_tc_setup();         // the kernels' shared-memory grant
+cudaError_t linear_tc_max_clusters(int (&clusters)[3]);
 cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream);  // x -> xh
 cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
-                             const CUtensorMap& xmap, int pairs, cudaStream_t stream);
+                             const CUtensorMap& xmap, const TcLimits& lim, cudaStream_t stream);
 
 }  // namespace c3d

@@ -13,14 +13,20 @@
 // up to 2^24. So the product runs as kind::f16, at the f16 rate, on codes turned into f16:
 //   - x, which every channel tile reads again, is expanded to f16 once by a small kernel before
 //     (3 bytes of traffic a code);
-//   - w stays 8 bits wide all the way to shared memory. Four converter warps read a row of 128 codes
-//     each thread, turn it into f16 (a byte under the exponent of 1024, minus 1152 with the sign bit
-//     flipped: a permute and a subtraction for each two codes) and write it to TMEM, from where the
-//     MMA takes its A operand. Shared memory then carries the codes once in and once out, and no f16
-//     copy of w: 96 bytes a cycle at 256 tokens in place of 192, of the 128 that it moves.
+//   - w stays 8 bits wide all the way to shared memory. Eight converter warps (four for each half of
+//     a stage's 128 codes) read 64 codes of a row each thread, turn them into f16 (a byte under the
+//     exponent of 1024, minus 1152 with the sign bit flipped: a permute and a subtraction for each
+//     two codes) and write them to TMEM, from where the MMA takes its A operand. Shared memory then
+//     carries the codes once in and once out, and no f16 copy of w: 96 bytes a cycle at 256 tokens
+//     in place of 192, of the 128 that it moves.
 //
-// Roles of a CTA: warps 0-3 epilogue, 4-7 converters (int8), 8 TMA, 9 MMA (the leader CTA's). Every
-// wait is bounded; one that runs out records a status bit and both CTAs wind down.
+// Few tiles: a tile is split along K over the pairs of one cluster (4 or 8 CTAs). Each CTA leaves its
+// partial sums in its own shared memory and adds up its share of the tokens from all of them over
+// distributed shared memory, in the order of the slices: nothing passes through global memory, and
+// a result does not depend on which slice is ready first.
+//
+// Roles of a CTA: warps 0-3 epilogue, 4-11 converters (int8), then TMA and MMA (the leader CTA's).
+// Every wait is bounded; one that runs out records a status bit and both CTAs wind down.
 #include <algorithm>
 
 #include "conv_common.cuh"
@@ -28,13 +34,18 @@
 
 namespace c3d {
 
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 448;
+constexpr int kTcTmaWarp = 12, kTcMmaWarp = 13;
 constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // w's codes of one stage: 16 KB a CTA
 constexpr int kTcMaxStages = 8;
 constexpr int kTcSmemBudget = 200 * 1024;
 constexpr int kTcTmemCols = 512;
-constexpr int kTcSlotCols = kTcBlockK / 2;          // one stage of w in f16: 64 columns
+constexpr int kTcSlotK = 64;                        // codes of w a TMEM slot holds as f16
+constexpr int kTcSlotCols = kTcSlotK / 2;           // in 32 columns
+constexpr int kTcMaxSlots = 8;
 constexpr uint64_t kTcAbortSettleNs = 2ull * 1000 * 1000;  // let copies in flight land on abort
+
+constexpr int kTcBars = 3 * kTcMaxStages + 2 * kTcMaxSlots + 5;
 
 // x's bytes of one stage of one CTA (half of the tile's tokens).
 __host__ __device__ inline uint32_t tc_x_bytes(int block_t, bool int8) {
@@ -46,26 +57,91 @@ __host__ __device__ inline uint32_t tc_x_bytes(int block_t, bool int8) {
 // operands in L2 (8 x ~10 of them read 18 operand tiles; in plain order a wide w is read again for
 // each tile of tokens).
 constexpr int kTcGroup = 8;
-struct TcUnit {
-  int tile, m_tile, n_tile, kb0, kb1;
+struct TcTile {
+  int m_tile, n_tile;
 };
-__device__ __forceinline__ TcUnit tc_unit(const LinearParams& p, int u) {
-  TcUnit r;
-  r.tile = u / p.splits;
-  const int split = u - r.tile * p.splits;
-  r.kb0 = split * p.kb_per_split;
-  r.kb1 = min(r.kb0 + p.kb_per_split, p.k_blocks);
+__device__ __forceinline__ TcTile tc_tile(const LinearParams& p, int tile) {
+  TcTile r;
   const int per_group = kTcGroup * p.m_tiles;
-  const int group = r.tile / per_group;
-  const int rest = r.tile - group * per_group;
+  const int group = tile / per_group;
+  const int rest = tile - group * per_group;
   const int width = min(kTcGroup, p.n_tiles - group * kTcGroup);
   r.m_tile = rest / width;
   r.n_tile = group * kTcGroup + (rest - r.m_tile * width);
   return r;
 }
 
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Four consecutive channels of y (element i is a multiple of 4 elements into an aligned row).
+__device__ __forceinline__ void store_y4(const LinearParams& p, long long i, const float (&v)[4]) {
+  if (p.y_type == Q8_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.y) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if (p.y_type == Q8_BF16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(static_cast<__half*>(p.y) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// Adds up the partial sums that the cluster's CTAs of this rank hold, [token][128 channels] at the
+// same offset of their shared memory, for this CTA's share of the tile's tokens. All threads.
+__device__ __forceinline__ void tc_join(const LinearParams& p, const TcTile& t, uint32_t part,
+                                        int split, uint32_t rank) {
+  const int lane = threadIdx.x & 31;
+  const long long n = (long long)t.n_tile * kTcChannels + rank * 128 + 4 * lane;
+  const long long m0 = (long long)t.m_tile * p.block_t;
+  const int tokens = (int)min((long long)p.block_t, p.M - m0);
+  const int share = p.block_t / p.splits;
+  if (n >= p.N) return;
+  const int have = (int)min(4LL, p.N - n);
+  ScaleBias sc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long c = min(n + i, (long long)p.N - 1);
+    sc[i] = ScaleBias{__ldg(p.scale_w + c), p.bias ? q8_load_value(p.bias, p.bias_type, c) : 0.0f};
+  }
+  const int end = min(tokens, (split + 1) * share);
+  for (int c = split * share + (threadIdx.x >> 5); c < end; c += kTcThreads / 32) {
+    const uint32_t at = part + (uint32_t)(c * 128 + 4 * lane) * 4u;
+    float4 a[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (s < p.splits) a[s] = ld_cluster_f4(map_to_cta(at, 2u * s + rank));
+#pragma unroll
+    for (int s = 1; s < 4; ++s)
+      if (s < p.splits) {
+        a[0].x += a[s].x;
+        a[0].y += a[s].y;
+        a[0].z += a[s].z;
+        a[0].w += a[s].w;
+      }
+    const float sx = __ldg(p.scale_x + m0 + c);
+    const float v[4] = {sc[0](a[0].x, sx), sc[1](a[0].y, sx), sc[2](a[0].z, sx), sc[3](a[0].w, sx)};
+    const long long i = (m0 + c) * p.y_pitch + n;
+    if (p.y_vec && have == 4) {
+      store_y4(p, i, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < have) q8_store_value(p.y, p.y_type, i + e, v[e]);
+    }
+  }
+}
+
 template <bool kInt8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
     linear_q8_tc_kernel(const __grid_constant__ CUtensorMap wmap,
                         const __grid_constant__ CUtensorMap xmap, const LinearParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -78,26 +154,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   float* sScale = reinterpret_cast<float*>(sX + (size_t)S * x_bytes);  // [4 warps][kTcMaxTokens]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + 4 * kTcMaxTokens);
   // bars: full[S] (the leader's; e4m3: both operands, int8: x), empty[S], w_full[S] (int8),
-  // slot_full[4] (the leader's), slot_empty[4], acc_full[2], acc_empty[2] (the leader's), drain
+  // slot_full[8] (the leader's), slot_empty[8], acc_full[2], acc_empty[2] (the leader's), drain
   const uint32_t bars_u32 = smem_u32(bars);
   auto full = [&](int s) { return bars_u32 + 8u * s; };
   auto empty = [&](int s) { return bars_u32 + 8u * (kTcMaxStages + s); };
   auto w_full = [&](int s) { return bars_u32 + 8u * (2 * kTcMaxStages + s); };
   auto slot_full = [&](int s) { return bars_u32 + 8u * (3 * kTcMaxStages + s); };
-  auto slot_empty = [&](int s) { return bars_u32 + 8u * (3 * kTcMaxStages + 4 + s); };
-  auto acc_full = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 8 + b); };
-  auto acc_empty = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 10 + b); };
-  const uint32_t drain_bar = bars_u32 + 8u * (3 * kTcMaxStages + 12);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * kTcMaxStages + 13);
+  auto slot_empty = [&](int s) { return bars_u32 + 8u * (3 * kTcMaxStages + kTcMaxSlots + s); };
+  auto acc_full = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 2 * kTcMaxSlots + b); };
+  auto acc_empty = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 2 * kTcMaxSlots + 2 + b); };
+  const uint32_t drain_bar = bars_u32 + 8u * (kTcBars - 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kTcBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile unsigned* last_flag = reinterpret_cast<volatile unsigned*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  // a cluster is 2 * splits CTAs: pair `split` of it takes that slice of a tile's K blocks
+  const uint32_t cluster_rank = cluster_ctarank();
+  const uint32_t rank = cluster_rank & 1u;  // within the pair
+  const int split = (int)(cluster_rank >> 1);
   const bool leader = rank == 0;
-  const uint32_t leader_bars = map_to_cta(bars_u32, 0);
-  const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
-  const int num_units = p.m_tiles * p.n_tiles * p.splits;
+  const uint32_t leader_bars = map_to_cta(bars_u32, cluster_rank & ~1u);
+  const uint16_t pair_mask = (uint16_t)(0x3u << (cluster_rank & ~1u));
+  const int first_tile = blockIdx.x / (2 * p.splits), tile_step = gridDim.x / (2 * p.splits);
+  const int num_tiles = p.m_tiles * p.n_tiles;
+  const int kb0 = (int)((long long)split * p.k_blocks / p.splits);
+  const int kb1 = (int)((long long)(split + 1) * p.k_blocks / p.splits);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -105,7 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       mbar_init(empty(s), 1);
       mbar_init(w_full(s), 1);
     }
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < kTcMaxSlots; ++s) {
       mbar_init(slot_full(s), 2 * 4);  // a converter warp's arrival each, of both CTAs
       mbar_init(slot_empty(s), 1);
     }
@@ -117,11 +198,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == kTcMmaWarp) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTcTmemCols);
     tmem_relinquish_pair();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kTcTmaWarp && lane == 0) {
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&xmap);
   }
@@ -140,8 +221,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     float* scale = sScale + warp * kTcMaxTokens;
     int buf = 0;
     uint32_t phase = 0;
-    for (int u = pair_id; u < num_units; u += num_pairs) {
-      const TcUnit un = tc_unit(p, u);
+    for (int u = first_tile; u < num_tiles; u += tile_step) {
+      const TcTile un = tc_tile(p, u);
       const long long n = (long long)un.n_tile * kTcChannels + rank * 128 + threadIdx.x;
       const bool n_ok = n < p.N;
       const long long m0 = (long long)un.m_tile * p.block_t;
@@ -154,9 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (p.bias) sc.bias = q8_load_value(p.bias, p.bias_type, n);
       }
       __syncwarp();
-      bool ok = wait_bounded_warp<true>(acc_full(buf), phase, ab, kStatusWaitAccFull);
-      if (p.splits > 1) ok = named_barrier_and(1, 128, ok);  // the four warps join the partials
-      if (!ok) break;
+      if (!wait_bounded_warp(acc_full(buf), phase, ab, kStatusWaitAccFull)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t)(buf * p.acc_stride) + ((uint32_t)(warp * 32) << 16);
       if (p.splits == 1) {
@@ -174,118 +253,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           }
         }
       } else {
-        float* part = p.partials + ((long long)u * 2 + rank) * p.block_t * 128 + threadIdx.x;
+        // the pipeline's stages are free: every copy of this pair has been consumed
+        float* part = reinterpret_cast<float*>(sW) + threadIdx.x;
         for (int c = 0; c < p.block_t; c += 32) {
-          if (c >= tokens) break;
           uint32_t r[32];
           tmem_ld_32x32b_x32(trow + c, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < tokens) __stcg(part + (c + j) * 128, __uint_as_float(r[j]));
+          for (int j = 0; j < 32; ++j) part[(c + j) * 128] = __uint_as_float(r[j]);
         }
-        // The last of a tile's slices to arrive adds them all up, in their order.
-        __threadfence();
-        named_barrier_sync(1, 128);
-        if (threadIdx.x == 0) {
-          unsigned* counter = p.counters + un.tile * 2 + rank;
-          const unsigned before = atomicAdd(counter, 1u);
-          const bool last = before + 1 == (unsigned)p.splits;
-          if (last) *counter = 0;  // for the next run
-          *last_flag = last;
-        }
-        named_barrier_sync(1, 128);
-        if (*last_flag) {
-          __threadfence();
-          const long long slice = 2LL * p.block_t * 128;
-          const float* first = p.partials +
-                               ((long long)un.tile * p.splits * 2 + rank) * p.block_t * 128 +
-                               threadIdx.x;
-          for (int c = 0; c < tokens; c += 8) {
-            float acc[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = c + j < tokens ? __ldcg(first + (c + j) * 128) : 0.0f;
-            for (int s = 1; s < p.splits; ++s)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (c + j < tokens) acc[j] += __ldcg(first + s * slice + (c + j) * 128);
-            if (n_ok) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (c + j < tokens)
-                  q8_store_value(p.y, p.y_type, (m0 + c + j) * p.y_pitch + n,
-                                 sc(acc[j], scale[c + j]));
-            }
-          }
-        }
-        named_barrier_sync(1, 128);  // last_flag is read before it is written again
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(leader_bars + (acc_empty(buf) - bars_u32));
+      if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (acc_empty(buf) - bars_u32));
       if (++buf == p.acc_bufs) {
         buf = 0;
         phase ^= 1u;
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < kTcTmaWarp) {
     // ---------------------------------------------------------------------------- converters
     if (kInt8) {
-      const int row = (warp - 4) * 32 + lane;
-      const uint32_t lane_base = (uint32_t)((warp - 4) * 32) << 16;
-      Ring ring, slots;
+      const int quad = warp & 3, half = (warp - 4) >> 2;
+      const int row = quad * 32 + lane;
+      const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+      Ring ring;
+      Ring slots;
+      slots.stage = half;  // this half's slots are half, half + 2, ...
+      int pending = -1;    // the slot whose store is under way
+      auto publish = [&]() {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (slot_full(pending) - bars_u32));
+      };
       bool aborted = false;
-      for (int u = pair_id; u < num_units && !aborted; u += num_pairs) {
-        const TcUnit un = tc_unit(p, u);
-        for (int kb = un.kb0; kb < un.kb1; ++kb) {
+      for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
+        const TcTile un = tc_tile(p, u);
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded_warp(w_full(ring.stage), ring.phase, ab, kStatusWaitFull)) {
             aborted = true;
             break;
           }
           const uint8_t* src = sW + (size_t)ring.stage * kTcWBytes + row * kTcBlockK;
-          uint4 c[8];
+          uint4 c[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)  // 16-byte chunk i of the row, where the swizzle put it
-            c[i] = *reinterpret_cast<const uint4*>(src + ((i ^ (row & 7)) << 4));
-          if (!wait_bounded_warp<true>(slot_empty(slots.stage), slots.phase ^ 1u, ab,
+          for (int i = 0; i < 4; ++i)  // 16-byte chunk i of this half, where the swizzle put it
+            c[i] = *reinterpret_cast<const uint4*>(src + (((4 * half + i) ^ (row & 7)) << 4));
+          if (pending >= 0) publish();  // the store before has had the loads' time to finish
+          uint32_t h[32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) int8_to_f16(c[i], h + 8 * i);
+          if (!wait_bounded_warp(slot_empty(slots.stage), slots.phase ^ 1u, ab,
                                        kStatusWaitEmpty)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          const uint32_t dst = slots_base + lane_base + (uint32_t)(slots.stage * kTcSlotCols);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t h[32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) int8_to_f16(c[4 * half + i], h + 8 * i);
-            tmem_st_32x32b_x32(dst + 32 * half, h);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(leader_bars + (slot_full(slots.stage) - bars_u32));
+          tmem_st_32x32b_x32(slots_base + lane_base + (uint32_t)(slots.stage * kTcSlotCols), h);
+          pending = slots.stage;
           ring.next(S);
-          slots.next(p.a_slots);
+          slots.stage += 2;
+          if (slots.stage >= p.a_slots) {
+            slots.stage = half;
+            slots.phase ^= 1u;
+          }
         }
       }
+      if (pending >= 0) publish();
     }
-  } else if (warp == 8) {
+  } else if (warp == kTcTmaWarp) {
     // ------------------------------------------------------------------------------ TMA loader
     Ring ring;
     bool aborted = false;
     const int half_t = p.block_t / 2;
-    for (int u = pair_id; u < num_units && !aborted; u += num_pairs) {
-      const TcUnit un = tc_unit(p, u);
+    bool skip = (p.debug_flags & 1) != 0;
+    for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
+      const TcTile un = tc_tile(p, u);
       const int n0 = un.n_tile * kTcChannels + (int)rank * 128;
       const int m0 = un.m_tile * p.block_t + (int)rank * half_t;
-      for (int kb = un.kb0; kb < un.kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         const int s = ring.stage;
-        if (!wait_bounded_warp<true>(empty(s), ring.phase ^ 1u, ab, kStatusWaitEmpty)) {
+        if (!wait_bounded_warp(empty(s), ring.phase ^ 1u, ab, kStatusWaitEmpty)) {
           aborted = true;
           break;
         }
-        if (elect_one()) {
+        if (!skip && elect_one()) {
           const uint32_t bar = leader_bars + (full(s) - bars_u32);
           const uint32_t w_dst = smem_u32(sW) + (uint32_t)s * kTcWBytes;
           const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * x_bytes;
@@ -302,6 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             tma_load_2d_pair(x_dst, &xmap, bar, k0, m0);
           }
         }
+        skip = false;
         __syncwarp();
         ring.next(S);
       }
@@ -316,46 +370,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     int buf = 0;
     uint32_t phase = 0;
     bool aborted = false;
-    for (int u = pair_id; u < num_units && !aborted; u += num_pairs) {
-      const TcUnit un = tc_unit(p, u);
-      if (!wait_bounded_warp<true>(acc_empty(buf), phase ^ 1u, ab, kStatusWaitAccEmpty)) break;
+    for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
+      const TcTile un = tc_tile(p, u);
+      if (!wait_bounded_warp(acc_empty(buf), phase ^ 1u, ab, kStatusWaitAccEmpty)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(buf * p.acc_stride);
-      for (int kb = un.kb0; kb < un.kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         const int s = ring.stage;
-        bool ok = wait_bounded_warp<true>(full(s), ring.phase, ab, kStatusWaitFull);
-        if (kInt8 && ok)
-          ok = wait_bounded_warp<true>(slot_full(slots.stage), slots.phase, ab, kStatusWaitFull);
-        if (!ok) {
+        if (!wait_bounded_warp(full(s), ring.phase, ab, kStatusWaitFull)) {
           aborted = true;
           break;
         }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t acc0 = kb > un.kb0 ? 1u : 0u;
-          const int rem = p.K - kb * kTcBlockK;  // codes past K are zeros, and mostly left out
-          const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 4));
-          if (kInt8) {
-            const uint32_t a = slots_base + (uint32_t)(slots.stage * kTcSlotCols);
+        const uint32_t acc0 = kb > kb0 ? 1u : 0u;
+        const int rem = p.K - kb * kTcBlockK;  // codes past K are zeros, and mostly left out
+        const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 4));
+        if (kInt8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (16 * j < rem)
-                mma_f16_pair_tmem_a(d, a + 8 * j, xdesc + (j >> 2) * (x_bytes >> 5) + 2 * (j & 3),
-                                    idesc, j > 0 ? 1u : acc0);
-            mma_commit_pair(slot_empty(slots.stage), 0x3);
-          } else {
+          for (int half = 0; half < 2; ++half) {
+            if (!wait_bounded_warp(slot_full(slots.stage), slots.phase, ab,
+                                         kStatusWaitFull)) {
+              aborted = true;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t a = slots_base + (uint32_t)(slots.stage * kTcSlotCols);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (kTcSlotK * half + 16 * j < rem)
+                  mma_f16_pair_tmem_a(d, a + 8 * j, xdesc + half * (x_bytes >> 5) + 2 * j, idesc,
+                                      half + j > 0 ? 1u : acc0);
+              mma_commit_pair(slot_empty(slots.stage), pair_mask);
+              if (half == 1) {
+                mma_commit_pair(empty(s), pair_mask);
+                if (kb + 1 == kb1) mma_commit_pair(acc_full(buf), pair_mask);
+              }
+            }
+            __syncwarp();
+            slots.next(p.a_slots);
+          }
+          if (aborted) break;
+        } else {
+          tc_fence_after();
+          if (elect_one()) {
             const uint64_t wdesc = wdesc0 + (uint64_t)((uint32_t)s * (kTcWBytes >> 4));
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (32 * j < rem)
                 mma_f8f6f4_pair(d, wdesc + 2 * j, xdesc + 2 * j, idesc, j > 0 ? 1u : acc0);
+            mma_commit_pair(empty(s), pair_mask);
+            if (kb + 1 == kb1) mma_commit_pair(acc_full(buf), pair_mask);
           }
-          mma_commit_pair(empty(s), 0x3);
-          if (kb + 1 == un.kb1) mma_commit_pair(acc_full(buf), 0x3);
+          __syncwarp();
         }
-        __syncwarp();
         ring.next(S);
-        slots.next(p.a_slots);
       }
       if (++buf == p.acc_bufs) {
         buf = 0;
@@ -363,17 +431,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       }
     }
     // every MMA of the pair is complete before TMEM is released
-    if (elect_one()) mma_commit_pair(drain_bar, 0x1);
+    if (elect_one()) mma_commit_pair(drain_bar, (uint16_t)(1u << cluster_rank));
     __syncwarp();
     wait_drain(drain_bar, 0, p.timeout_ns, p.status, kStatusWaitDrain);
   }
   __syncwarp();
   if (*abort_flag) sleep_ns_bounded(kTcAbortSettleNs);
   tc_fence_before();
+  if (p.splits > 1) {
+    __syncthreads();
+    cluster_sync();  // every slice's partial sums are in place
+    if (first_tile < num_tiles) tc_join(p, tc_tile(p, first_tile), smem_u32(sW), split, rank);
+  }
   __syncthreads();
-  cluster_sync();  // neither CTA leaves while the other may still signal or read its memory
+  cluster_sync();  // no CTA leaves while another may still signal or read its memory
   tc_fence_after();
-  if (warp == 9) tmem_dealloc_pair(tmem_base, kTcTmemCols);
+  if (warp == kTcMmaWarp) tmem_dealloc_pair(tmem_base, kTcTmemCols);
 }
 
 // x's int8 codes as f16, 16 a thread and step.
@@ -393,34 +466,41 @@ __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p
   }
 }
 
-void linear_tc_decide(LinearParams& p, int code_type, int pairs) {
+void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
   const bool int8 = code_type == Q8_INT8;
   p.n_tiles = (p.N + kTcChannels - 1) / kTcChannels;
   p.k_blocks = (p.K + kTcBlockK - 1) / kTcBlockK;
-  // Tokens of a tile: the size whose waves of tiles take the fewest tensor-core cycles. A K block of
-  // a 256 x t tile takes 4t cycles of f16 MMAs (2t of e4m3's), never less than its operands' bytes
-  // take to arrive (16 KB of w a CTA at the SM's share of the memory, about 24 bytes a cycle; the
-  // tile's x comes from L2). An epilogue that no second accumulator hides costs about 8 cycles a
-  // token.
+  // Tokens of a tile and slices of K: the choice whose waves of tiles are estimated to take the
+  // fewest cycles. A K block of a 256 x t tile takes 4t cycles of f16 MMAs (2t of e4m3's), and never
+  // less than w's 16 KB a CTA take to arrive: the memory's 6.8 TB/s (3570 bytes a cycle) shared by
+  // the CTAs at work, up to 40 bytes a cycle each. An epilogue that no second accumulator hides
+  // costs about 8 cycles a token, so does a kernel's last one; joining slices about 20 a token and
+  // 2500 for the cluster's barriers.
   double best = 1e300;
   for (int t = 32; t <= kTcMaxTokens && t < p.M + 32; t += 32) {
+    if (lim.block_t && t != lim.block_t) continue;
     const long long m_tiles = (p.M + t - 1) / t, tiles = m_tiles * p.n_tiles;
-    const bool two = !int8 || t <= 192;
-    const double kb = std::max(int8 ? 4.0 * t : 2.0 * t, 700.0);
-    long long splits = 1;
-    if (tiles * 2 <= pairs) splits = std::max<long long>(1, std::min<long long>(pairs / tiles, p.k_blocks / 4));
-    const long long waves = (tiles * splits + pairs - 1) / pairs;
-    const double unit = (double)((p.k_blocks + splits - 1) / splits) * kb + (two ? 0.0 : 8.0 * t);
-    const double cost = waves * unit + 8.0 * t;
-    if (cost < best) {
-      best = cost;
-      p.block_t = t;
-      p.m_tiles = (int)m_tiles;
-      p.splits = (int)splits;
+    for (int i = 0; i < 3; ++i) {
+      const int splits = 1 << i;
+      if (lim.splits ? splits != lim.splits : splits > 1 && p.k_blocks < 2 * splits) continue;
+      if (splits > p.k_blocks || (splits > 1 && tiles > lim.clusters[i])) continue;
+      const long long held = std::max(1, lim.clusters[i]);
+      const long long waves = (tiles + held - 1) / held;
+      const double ctas = 2.0 * splits * (double)std::min(tiles, held);
+      const double arrive = kTcWBytes / std::min(40.0, 3570.0 / ctas);
+      const double kb = std::max((int8 ? 4.0 : 2.0) * t, arrive);
+      const bool two = !int8 || t <= 192;
+      const double unit =
+          (double)((p.k_blocks + splits - 1) / splits) * kb + (two ? 0.0 : 8.0 * t);
+      const double cost = (double)waves * unit + (splits > 1 ? 20.0 * t + 2500.0 : 8.0 * t);
+      if (cost < best) {
+        best = cost;
+        p.block_t = t;
+        p.m_tiles = (int)m_tiles;
+        p.splits = splits;
+      }
     }
   }
-  p.kb_per_split = (p.k_blocks + p.splits - 1) / p.splits;
-  p.splits = (p.k_blocks + p.kb_per_split - 1) / p.kb_per_split;
   if (!int8) {
     p.acc_bufs = 2;
     p.acc_stride = kTcMaxTokens;
@@ -428,7 +508,7 @@ void linear_tc_decide(LinearParams& p, int code_type, int pairs) {
   } else {
     p.acc_bufs = p.block_t <= 192 ? 2 : 1;
     p.acc_stride = p.block_t <= 128 ? 128 : (p.block_t <= 192 ? 192 : 256);
-    p.a_slots = (kTcTmemCols - p.acc_bufs * p.acc_stride) / kTcSlotCols;  // 4 or 2
+    p.a_slots = (kTcTmemCols - p.acc_bufs * p.acc_stride) / kTcSlotCols;  // 8 or 4
   }
   const int stage = kTcWBytes + (int)tc_x_bytes(p.block_t, int8);
   p.stages = std::min(kTcMaxStages, kTcSmemBudget / stage);
@@ -436,11 +516,11 @@ void linear_tc_decide(LinearParams& p, int code_type, int pairs) {
 
 size_t linear_tc_smem_bytes(const LinearParams& p, int code_type) {
   return 1024 + (size_t)p.stages * (kTcWBytes + tc_x_bytes(p.block_t, code_type == Q8_INT8)) +
-         4 * kTcMaxTokens * sizeof(float) + (3 * kTcMaxStages + 13) * 8 + 16;
+         4 * kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
 }
 
 cudaError_t linear_tc_setup() {
-  const int most = 1024 + kTcSmemBudget + 4 * kTcMaxTokens * 4 + (3 * kTcMaxStages + 13) * 8 + 16;
+  const int most = 1024 + kTcSmemBudget + 4 * kTcMaxTokens * 4 + kTcBars * 8 + 16;
   cudaError_t e = cudaFuncSetAttribute(linear_q8_tc_kernel<true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e == cudaSuccess)
@@ -449,56 +529,64 @@ cudaError_t linear_tc_setup() {
   return e;
 }
 
-int linear_tc_max_pairs() {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(kTcThreads, 1, 1);
-  cfg.dynamicSmemBytes = kTcSmemBudget;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_q8_tc_kernel<true>, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
+// Clusters of 2, 4 and 8 CTAs that the current device holds at once.
+cudaError_t linear_tc_max_clusters(int (&clusters)[3]) {
+  for (int i = 0; i < 3; ++i) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2u << i;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2u << i, 1, 1);
+    cfg.blockDim = dim3(kTcThreads, 1, 1);
+    cfg.dynamicSmemBytes = kTcSmemBudget;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaOccupancyMaxActiveClusters(&clusters[i], linear_q8_tc_kernel<true>, &cfg);
+    if (e != cudaSuccess) return e;
   }
-  return n;
+  return cudaSuccess;
 }
 
 template <typename Kernel, typename... Args>
-static cudaError_t launch_pdl(Kernel kernel, int grid, int block, size_t smem, cudaStream_t stream,
-                              const Args&... args) {
+static cudaError_t launch_pdl(Kernel kernel, int grid, int block, int cluster, size_t smem,
+                              cudaStream_t stream, const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream) {
   const long long total = (long long)p.M * ((p.K + 15) / 16);
   const int grid = (int)std::min<long long>((total + 255) / 256, 152 * 8);
-  return launch_pdl(linear_expand_kernel, grid, 256, 0, stream, p);
+  return launch_pdl(linear_expand_kernel, grid, 256, 1, 0, stream, p);
 }
 
 cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
-                             const CUtensorMap& xmap, int pairs, cudaStream_t stream) {
-  const long long units = (long long)p.m_tiles * p.n_tiles * p.splits;
-  const int grid = 2 * (int)std::min<long long>(units, pairs);
+                             const CUtensorMap& xmap, const TcLimits& lim, cudaStream_t stream) {
+  const long long tiles = (long long)p.m_tiles * p.n_tiles;
+  const int cluster = 2 * p.splits;
+  const int grid = cluster * (int)std::min<long long>(tiles, std::max(1, lim.clusters[p.splits / 2]));
   const size_t smem = linear_tc_smem_bytes(p, code_type);
   if (code_type == Q8_INT8)
-    return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads, smem, stream, wmap, xmap, p);
-  return launch_pdl(linear_q8_tc_kernel<false>, grid, kTcThreads, smem, stream, wmap, xmap, p);
+    return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads, cluster, smem, stream, wmap, xmap,
+                      p);
+  return launch_pdl(linear_q8_tc_kernel<false>, grid, kTcThreads, cluster, smem, stream, wmap, xmap,
+                    p);
 }
 
 }  // namespace c3d

@@ -7,6 +7,8 @@
 // therefore taken in the same pass, reduced together, and the row's values stay in registers: every
 // input is read once, every output written once, which is the operator's floor (both are bound by
 // the memory's bandwidth, and by one row's latency when there are few rows).
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "q8_common.cuh"
 
@@ -28,44 +30,77 @@ __device__ __forceinline__ RowStat warp_reduce(RowStat s) {
   return s;
 }
 
-// Over the threads of one row: a warp, or the whole block.
-__device__ __forceinline__ RowStat row_reduce(RowStat s, int threads) {
+// Over the threads of one row: a warp, or the whole block. Consecutive rows of a block alternate
+// between two buffers, so that one barrier a row is enough.
+__device__ __forceinline__ RowStat row_reduce(RowStat s, int threads, int buffer) {
   s = warp_reduce(s);
   if (threads == 32) return s;
-  __shared__ RowStat warp_stat[32];
+  __shared__ RowStat warp_stat[2][32];
   const int lane = threadIdx.x & 31;
-  if (lane == 0) warp_stat[threadIdx.x >> 5] = s;
+  if (lane == 0) warp_stat[buffer][threadIdx.x >> 5] = s;
   __syncthreads();
-  s = lane < threads / 32 ? warp_stat[lane] : RowStat{0.0f, 0u};
+  s = lane < threads / 32 ? warp_stat[buffer][lane] : RowStat{0.0f, 0u};
   return warp_reduce(s);
 }
 
-// Eight consecutive values at p (16-byte aligned) as fp32.
-__device__ __forceinline__ void load8(const float* p, float (&v)[kChunk]) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[kChunk]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Eight values of a row on their way to registers, as they lie in memory: the loads of the next row
+// are in flight while this one is worked on, so they are held unconverted.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float v[kChunk];
+  __device__ __forceinline__ void load8(const float* p) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
-}
-__device__ __forceinline__ void load8(const __half* p, float (&v)[kChunk]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  __device__ __forceinline__ void load1(int e, const float* p) { v[e] = *p; }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+    for (int e = 0; e < kChunk; ++e) v[e] = 0.0f;
   }
-}
+  __device__ __forceinline__ void values(float (&f)[kChunk]) const {
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e) f[e] = v[e];
+  }
+};
+template <typename T>
+struct Raw16 {
+  uint32_t w[4];  // two values each, the first in the low half
+  __device__ __forceinline__ void load8(const T* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+  }
+  __device__ __forceinline__ void load1(int e, const T* p) {
+    const uint32_t h = *reinterpret_cast<const uint16_t*>(p);
+    w[e / 2] = e % 2 ? (w[e / 2] & 0xFFFFu) | (h << 16) : h;
+  }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0; }
+};
+template <>
+struct Raw<__nv_bfloat16> : Raw16<__nv_bfloat16> {
+  __device__ __forceinline__ void values(float (&f)[kChunk]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Raw<__half> : Raw16<__half> {
+  __device__ __forceinline__ void values(float (&f)[kChunk]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  }
+};
+
 __device__ __forceinline__ void store8(float* p, const float (&v)[kChunk]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -89,47 +124,48 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[kChunk]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Where a thread's kChunk values of step i lie. Aligned rows: consecutive columns, moved by 16-byte
-// accesses (the row's last, incomplete chunk by single elements). Other rows (a base, a pitch or a
-// weight off the 16-byte grid): columns one row-team apart, moved one by one, so that a warp still
-// touches consecutive addresses.
-template <bool kAligned>
+// Where a thread's kChunk values of step i lie in rows on the 16-byte grid: consecutive columns,
+// moved by 16-byte accesses (the row's last, incomplete chunk by single elements).
 struct Place {
   int tid, threads, cols;
-  __device__ __forceinline__ int col(int i, int e) const {
-    return kAligned ? (i * threads + tid) * kChunk + e : (i * kChunk + e) * threads + tid;
-  }
-  __device__ __forceinline__ bool whole(int i) const {
-    return kAligned && col(i, 0) + kChunk <= cols;
-  }
+  __device__ __forceinline__ int col(int i) const { return (i * threads + tid) * kChunk; }
+  __device__ __forceinline__ bool whole(int i) const { return col(i) + kChunk <= cols; }
   // Columns past the row's end read 0, which changes neither a sum of squares nor an amax.
   template <typename T>
-  __device__ __forceinline__ void load(const T* row, int i, float (&v)[kChunk]) const {
+  __device__ __forceinline__ void load(const T* row, int i, Raw<T>& r) const {
     if (whole(i)) {
-      load8(row + col(i, 0), v);
+      r.load8(row + col(i));
     } else {
+      r.clear();
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e)
-        v[e] = col(i, e) < cols ? q8_to_float(row[col(i, e)]) : 0.0f;
+      for (int e = 0; e < kChunk - 1; ++e)
+        if (col(i) + e < cols) r.load1(e, row + col(i) + e);
     }
+  }
+  template <typename T>
+  __device__ __forceinline__ void values(const void* row, int i, float (&v)[kChunk]) const {
+    Raw<T> r;
+    load(static_cast<const T*>(row), i, r);
+    r.values(v);
   }
   template <typename T>
   __device__ __forceinline__ void store(T* row, int i, const float (&v)[kChunk]) const {
     if (whole(i)) {
-      store8(row + col(i, 0), v);
+      store8(row + col(i), v);
     } else {
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e)
-        if (col(i, e) < cols) row[col(i, e)] = q8_from_float<T>(v[e]);
+      for (int e = 0; e < kChunk - 1; ++e)
+        if (col(i) + e < cols) row[col(i) + e] = q8_from_float<T>(v[e]);
     }
   }
   __device__ __forceinline__ void store_codes(uint8_t* row, int i, uint2 c) const {
     if (whole(i)) {
-      *reinterpret_cast<uint2*>(row + col(i, 0)) = c;
+      *reinterpret_cast<uint2*>(row + col(i)) = c;
     } else {
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e)
-        if (col(i, e) < cols) row[col(i, e)] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+      for (int e = 0; e < kChunk - 1; ++e)
+        if (col(i) + e < cols)
+          row[col(i) + e] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
     }
   }
 };
@@ -150,128 +186,203 @@ __device__ __forceinline__ uint32_t e4m3_codes(const float* v, float inv) {
   return (lo & 0xFFFFu) | (hi << 16);
 }
 
-// Codes and scale of one row whose values the threads hold; `gain` is what the scale is multiplied
-// by (the norm's r). A row that is not finite gets the scale NaN and codes 0.
-template <int NV, bool kAligned>
-__device__ __forceinline__ void row_write(float (&v)[NV][kChunk], const RowStat& st, float gain,
-                                          const RowsParams& p, long long row,
-                                          const Place<kAligned>& at) {
+// How a row's values turn into its codes: code = round(v * lift * inv).
+struct RowCode {
+  float lift, inv;
+};
+
+// The row's scale, written by one thread, and its codes' factors; `gain` is what the scale is
+// multiplied by (the norm's r). A row that is not finite gets the scale NaN and codes 0 (its values
+// must be replaced by 0 before they are multiplied). A row so small that top / amax would overflow
+// is lifted first.
+__device__ __forceinline__ RowCode row_scale(const RowStat& st, float gain, const RowsParams& p,
+                                             long long row, bool writer, bool& bad) {
   const float top = p.code_type == Q8_E4M3 ? 448.0f : 127.0f;
-  const bool bad = st.amax >= 0x7F800000u || !(st.sum < INFINITY);
+  bad = st.amax >= 0x7F800000u || !(st.sum < INFINITY);
   const float amax = __uint_as_float(st.amax);
-  uint8_t* q = p.q + row * p.q_pitch;
-  if (at.tid == 0)
+  if (writer)
     p.scale[row] = bad ? __int_as_float(0x7FC00000) : (amax > 0.0f ? amax * gain / top : 1.0f);
-  float inv = top / amax;
-  if (bad || amax < 0x1p-100f) {  // rows that are no numbers, zeros, or so small that top / amax
-    const bool zero = bad || amax == 0.0f;  // would overflow: those are lifted first
-    inv = zero ? 0.0f : top / (amax * 0x1p100f);
+  RowCode c;
+  c.lift = amax < 0x1p-100f ? 0x1p100f : 1.0f;
+  c.inv = bad || amax == 0.0f ? 0.0f : top / (amax * c.lift);
+  return c;
+}
+
+// Codes and scale of one row whose values the threads hold.
+template <int NV>
+__device__ __forceinline__ void row_write(float (&v)[NV][kChunk], const RowStat& st, float gain,
+                                          const RowsParams& p, long long row, const Place& at) {
+  bool bad;
+  const RowCode rc = row_scale(st, gain, p, row, at.tid == 0, bad);
+  if (bad || rc.lift != 1.0f) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e) v[i][e] = zero ? 0.0f : v[i][e] * 0x1p100f;
+      for (int e = 0; e < kChunk; ++e) v[i][e] = bad ? 0.0f : v[i][e] * rc.lift;
   }
+  uint8_t* q = p.q + row * p.q_pitch;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const uint2 c = p.code_type == Q8_E4M3
-                        ? make_uint2(e4m3_codes(v[i], inv), e4m3_codes(v[i] + 4, inv))
-                        : make_uint2(int8_codes(v[i], inv), int8_codes(v[i] + 4, inv));
+                        ? make_uint2(e4m3_codes(v[i], rc.inv), e4m3_codes(v[i] + 4, rc.inv))
+                        : make_uint2(int8_codes(v[i], rc.inv), int8_codes(v[i] + 4, rc.inv));
     at.store_codes(q, i, c);
   }
 }
 
-// The row this thread works on: one a block, or one a warp when a warp holds a row.
-__device__ __forceinline__ long long my_row(const RowsParams& p) {
-  return p.row_threads == 32 ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
-                             : (long long)blockIdx.x;
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
-template <typename T, int NV, bool kAligned>
-__global__ void __launch_bounds__(NV >= 4 ? 512 : 1024) rmsnorm_q8_kernel(const RowsParams p) {
+// One block (of 32 to 1024 threads) or, for short rows, one warp holds a row, NV chunks a thread, and
+// takes every stride-th row. Up to two chunks a thread the next row's loads are issued before this
+// row is worked on: without that the memory waits for each block's reduction and stores (norm of
+// 8192 x 4096 bf16: 67.5 us with a block a row, FILL us so). Rows past 16384 columns take eight chunks
+// a thread and no look-ahead, which their registers have no room for.
+template <typename T>
+constexpr int rows_max_threads(int nv) {  // 64 registers a thread, or 128
+  return nv == 1 || (nv == 2 && sizeof(T) == 2) ? 1024 : 512;
+}
+
+template <typename T, int NV, bool kNorm>
+__global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const RowsParams p) {
+  constexpr bool kAhead = NV <= 2;
   pdl_wait_primary();
   pdl_launch_dependents();
-  const long long row = my_row(p);
-  if (row >= p.rows) return;  // whole warps, of blocks that hold a row a warp
-  const Place<kAligned> at{p.row_threads == 32 ? (int)(threadIdx.x & 31) : (int)threadIdx.x,
-                           p.row_threads, p.cols};
-  const T* x = static_cast<const T*>(p.a) + row * p.a_pitch;
-  float v[NV][kChunk];
+  const bool warp_rows = p.row_threads == 32;
+  const Place at{warp_rows ? (int)(threadIdx.x & 31) : (int)threadIdx.x, p.row_threads,
+                           p.cols};
+  const long long stride = warp_rows ? (long long)gridDim.x * (blockDim.x >> 5) : gridDim.x;
+  long long row = warp_rows ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                            : (long long)blockIdx.x;
+  const bool two = !kNorm || p.b;  // a second input: the residual, or up
+  Raw<T> ra[NV], rb[NV];
+  auto load_row = [&](long long r) {
+    const T* a = static_cast<const T*>(p.a) + r * p.a_pitch;
+    const T* b = static_cast<const T*>(p.b) + r * p.b_pitch;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) at.load(x, i, v[i]);
-  if (p.b) {
-    const T* res = static_cast<const T*>(p.b) + row * p.b_pitch;
+    for (int i = 0; i < NV; ++i) at.load(a, i, ra[i]);
+    if (two) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) at.load(b, i, rb[i]);
+    }
+  };
+  if (kAhead && row < p.rows) load_row(row);
+  for (int buffer = 0; row < p.rows; row += stride, buffer ^= 1) {
+    if (!kAhead) load_row(row);
+    float v[NV][kChunk];
+    RowStat st{0.0f, 0u};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float b[kChunk];
+      ra[i].values(v[i]);
+      if (two) rb[i].values(b);
+      if (kNorm) {
+        if (two) {
+#pragma unroll
+          for (int e = 0; e < kChunk; ++e) v[i][e] += b[e];
+          // these columns have been read by this thread, if sum_out is x or the residual
+          at.store(static_cast<T*>(p.sum_out) + row * p.sum_pitch, i, v[i]);
+        }
+        float w[kChunk];
+        if (p.weight_type == Q8_F32)
+          at.template values<float>(p.weight, i, w);
+        else if (p.weight_type == Q8_BF16)
+          at.template values<__nv_bfloat16>(p.weight, i, w);
+        else
+          at.template values<__half>(p.weight, i, w);
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+          st.sum = fmaf(v[i][e], v[i][e], st.sum);
+          v[i][e] *= w[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e)
+          v[i][e] = silu_mul(v[i][e], b[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e)
+        st.amax = max(st.amax, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    }
+    if (kAhead && row + stride < p.rows) load_row(row + stride);
+    st = row_reduce(st, p.row_threads, buffer);
+    const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
+    row_write<NV>(v, st, gain, p, row, at);
+  }
+}
+
+// Rows off the 16-byte grid (a base, a pitch or a weight): single elements, consecutive ones by
+// consecutive threads, the row's values kept in shared memory between the two passes.
+constexpr int kLooseThreads = 256;
+template <typename T, bool kNorm>
+__global__ void __launch_bounds__(kLooseThreads) rows_q8_loose_kernel(const RowsParams p) {
+  extern __shared__ float v[];
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  int buffer = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
+    const T* a = static_cast<const T*>(p.a) + row * p.a_pitch;
+    const T* b = p.b ? static_cast<const T*>(p.b) + row * p.b_pitch : nullptr;
     T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch;
-    // all of the residual's loads in flight at once, where registers hold them
-    constexpr int kAhead = kAligned && NV <= 4 ? NV : 1;
-    float r[kAhead][kChunk];
+    RowStat st{0.0f, 0u};
+    constexpr int kBatch = 8;  // loads of one thread in flight
+    for (int c0 = threadIdx.x; c0 < p.cols; c0 += kBatch * kLooseThreads) {
+      float x[kBatch], y[kBatch], w[kBatch];
 #pragma unroll
-    for (int i0 = 0; i0 < NV; i0 += kAhead) {
+      for (int j = 0; j < kBatch; ++j) {
+        const int c = c0 + j * kLooseThreads;
+        const bool in = c < p.cols;
+        x[j] = in ? q8_to_float(a[c]) : 0.0f;
+        y[j] = in && b ? q8_to_float(b[c]) : 0.0f;
+        w[j] = in && kNorm ? q8_load_value(p.weight, p.weight_type, c) : 0.0f;
+      }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) at.load(res, i0 + i, r[i]);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) v[i0 + i][e] += r[i][e];
-        at.store(sum_out, i0 + i, v[i0 + i]);  // columns this thread has read, if x's or residual's
+      for (int j = 0; j < kBatch; ++j) {
+        const int c = c0 + j * kLooseThreads;
+        if (c >= p.cols) break;
+        float f;
+        if (kNorm) {
+          const float h = x[j] + y[j];
+          if (b) sum_out[c] = q8_from_float<T>(h);  // read by this thread, if x or the residual
+          st.sum = fmaf(h, h, st.sum);
+          f = h * w[j];
+        } else {
+          f = silu_mul(x[j], y[j]);
+        }
+        st.amax = max(st.amax, __float_as_uint(f) & 0x7FFFFFFFu);
+        v[c] = f;  // read back by this thread alone
       }
     }
-  }
-  RowStat st{0.0f, 0u};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float w[kChunk];
-    if (p.weight_type == Q8_F32)
-      at.load(static_cast<const float*>(p.weight), i, w);
-    else if (p.weight_type == Q8_BF16)
-      at.load(static_cast<const __nv_bfloat16*>(p.weight), i, w);
-    else
-      at.load(static_cast<const __half*>(p.weight), i, w);
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-      st.sum = fmaf(v[i][e], v[i][e], st.sum);
-      v[i][e] *= w[e];
-      st.amax = max(st.amax, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    st = row_reduce(st, kLooseThreads, buffer);
+    bool bad;
+    const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
+    const RowCode rc = row_scale(st, gain, p, row, threadIdx.x == 0, bad);
+    uint8_t* q = p.q + row * p.q_pitch;
+    for (int c = threadIdx.x; c < p.cols; c += kLooseThreads) {
+      const float f[4] = {bad ? 0.0f : v[c] * rc.lift, 0.0f, 0.0f, 0.0f};
+      q[c] = (uint8_t)(p.code_type == Q8_E4M3 ? e4m3_codes(f, rc.inv) : int8_codes(f, rc.inv));
     }
   }
-  st = row_reduce(st, p.row_threads);
-  row_write<NV, kAligned>(v, st, rsqrtf(st.sum / (float)p.cols + p.eps), p, row, at);
 }
 
-template <typename T, int NV, bool kAligned>
-__global__ void __launch_bounds__(NV >= 4 ? 512 : 1024) silu_mul_q8_kernel(const RowsParams p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const long long row = my_row(p);
-  if (row >= p.rows) return;
-  const Place<kAligned> at{p.row_threads == 32 ? (int)(threadIdx.x & 31) : (int)threadIdx.x,
-                           p.row_threads, p.cols};
-  const T* gate = static_cast<const T*>(p.a) + row * p.a_pitch;
-  const T* up = static_cast<const T*>(p.b) + row * p.b_pitch;
-  float v[NV][kChunk], u[NV][kChunk];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) at.load(gate, i, v[i]);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) at.load(up, i, u[i]);
-  RowStat st{0.0f, 0u};
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) {
-      const float g = v[i][e];
-      v[i][e] = __fdividef(g, 1.0f + __expf(-g)) * u[i][e];
-      st.amax = max(st.amax, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
-    }
-  st = row_reduce(st, p.row_threads);
-  row_write<NV, kAligned>(v, st, 1.0f, p, row, at);
-}
-
-// One row a block of 32..1024 threads, or four rows a block of four warps when a warp holds a row.
+// A persistent grid: as many blocks as the device holds at once, or as the rows need.
 template <typename Kernel>
-static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, cudaStream_t stream) {
-  const bool warp_rows = p.row_threads == 32;
+static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, size_t smem,
+                               cudaStream_t stream) {
+  const long long blocks = p.row_threads == 32 ? (p.rows + 3) / 4 : p.rows;
+  int dev = 0, sms = 0, held = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && blocks > sms)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(warp_rows ? (p.rows + 3) / 4 : p.rows));
-  cfg.blockDim = dim3(warp_rows ? 128 : p.row_threads);
+  cfg.gridDim = dim3((unsigned)std::min<long long>(blocks, (long long)sms * std::max(1, held)));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -281,35 +392,35 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <typename T, bool kAligned>
-static cudaError_t launch_typed(const RowsParams& p, bool norm, int nv, cudaStream_t stream) {
-  if (norm) {
-    if (nv == 1) return launch_rows(rmsnorm_q8_kernel<T, 1, kAligned>, p, stream);
-    if (nv == 2) return launch_rows(rmsnorm_q8_kernel<T, 2, kAligned>, p, stream);
-    if (nv == 4) return launch_rows(rmsnorm_q8_kernel<T, 4, kAligned>, p, stream);
-    return launch_rows(rmsnorm_q8_kernel<T, 8, kAligned>, p, stream);
+template <typename T, bool kNorm>
+static cudaError_t launch_typed(RowsParams& p, bool aligned, cudaStream_t stream) {
+  if (!aligned) {
+    p.row_threads = kLooseThreads;
+    return launch_rows(rows_q8_loose_kernel<T, kNorm>, p, kLooseThreads, p.cols * sizeof(float),
+                       stream);
   }
-  if (nv == 1) return launch_rows(silu_mul_q8_kernel<T, 1, kAligned>, p, stream);
-  if (nv == 2) return launch_rows(silu_mul_q8_kernel<T, 2, kAligned>, p, stream);
-  if (nv == 4) return launch_rows(silu_mul_q8_kernel<T, 4, kAligned>, p, stream);
-  return launch_rows(silu_mul_q8_kernel<T, 8, kAligned>, p, stream);
+  // One chunk a thread where there are few rows, whose time is one row's latency; otherwise two.
+  const int chunks = (p.cols + kChunk - 1) / kChunk;
+  const int nv = chunks > 2 * rows_max_threads<T>(2) ? 8
+                 : chunks > rows_max_threads<T>(1) || (p.rows > 304 && chunks > 32) ? 2
+                                                                                    : 1;
+  p.row_threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
+  const int threads = p.row_threads == 32 ? 128 : p.row_threads;
+  if (nv == 1) return launch_rows(rows_q8_kernel<T, 1, kNorm>, p, threads, 0, stream);
+  if (nv == 2) return launch_rows(rows_q8_kernel<T, 2, kNorm>, p, threads, 0, stream);
+  return launch_rows(rows_q8_kernel<T, 8, kNorm>, p, threads, 0, stream);
 }
 
 cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, bool aligned,
                            cudaStream_t stream) {
-  const int chunks = (p.cols + kChunk - 1) / kChunk;
-  int nv = p.rows <= 304 ? 1 : 4;
-  while (nv > 1 && chunks <= 32 * (nv / 2)) nv >>= 1;
-  while (chunks > (nv >= 4 ? 512 : 1024) * nv) nv <<= 1;  // Q8_MAX_COLS is 8 chunks of 512 threads
-  p.row_threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
   if (value_type == Q8_F32)
-    return aligned ? launch_typed<float, true>(p, norm, nv, stream)
-                   : launch_typed<float, false>(p, norm, nv, stream);
+    return norm ? launch_typed<float, true>(p, aligned, stream)
+                : launch_typed<float, false>(p, aligned, stream);
   if (value_type == Q8_BF16)
-    return aligned ? launch_typed<__nv_bfloat16, true>(p, norm, nv, stream)
-                   : launch_typed<__nv_bfloat16, false>(p, norm, nv, stream);
-  return aligned ? launch_typed<__half, true>(p, norm, nv, stream)
-                 : launch_typed<__half, false>(p, norm, nv, stream);
+    return norm ? launch_typed<__nv_bfloat16, true>(p, aligned, stream)
+                : launch_typed<__nv_bfloat16, false>(p, aligned, stream);
+  return norm ? launch_typed<__half, true>(p, aligned, stream)
+              : launch_typed<__half, false>(p, aligned, stream);
 }
 
 }  // namespace c3d

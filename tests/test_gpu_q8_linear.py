@@ -38,11 +38,12 @@ def case(M, N, K, code_dtype, y_dtype, seed, bias_dtype=None, extra=0):
     return x, sx, w, sw, bias
 
 
-def run(x, sx, w, sw, bias, y_dtype, max_rows=None, y_extra=5):
+def run(x, sx, w, sw, bias, y_dtype, max_rows=None, y_extra=5, **options):
     M, N = x.shape[0], w.shape[0]
     full = torch.full((M + 2, N + y_extra), float("nan"), dtype=y_dtype, device="cuda")
     y = full[1:M + 1, :N]
-    plan = capi.linear_q8_plan(max_rows or M, N, w.shape[1], capi.q8_code_type(w.dtype), 0)
+    plan = capi.linear_q8_plan(max_rows or M, N, w.shape[1], capi.q8_code_type(w.dtype), 0,
+                               **options)
     try:
         capi.linear_q8_run(plan, x, sx, w, sw, y, bias)
         assert capi.linear_q8_check(plan) == capi.CONV3D_OK
@@ -63,11 +64,12 @@ def same_bits(a, b):
     return torch.equal(a.contiguous().view(as_int), b.contiguous().view(as_int))
 
 
-def check(M, N, K, code_dtype, y_dtype, seed, bias_dtype=None, extra=0, max_rows=None):
+def check(M, N, K, code_dtype, y_dtype, seed, bias_dtype=None, extra=0, max_rows=None,
+          y_extra=5, **options):
     x, sx, w, sw, bias = case(M, N, K, code_dtype, y_dtype, seed, bias_dtype, extra)
-    y = run(x, sx, w, sw, bias, y_dtype, max_rows)
+    y = run(x, sx, w, sw, bias, y_dtype, max_rows, y_extra, **options)
     want, mag = linear64(x, sx, w, sw, bias)
-    check_values(y, want, linear_err(mag, K, code_dtype), f"{M}x{N}x{K}")
+    check_values(y, want, linear_err(mag, K, code_dtype), f"{M}x{N}x{K} {options}")
 
 
 # one token, a few, many; widths and lengths around every tile and vector size
@@ -100,6 +102,65 @@ def test_every_short_length(code_dtype, M):
 def test_large(code_dtype):
     check(4096, 4096, 1024, code_dtype, torch.float32, 77)
     check(1111, 8200, 4100, code_dtype, torch.bfloat16, 78, torch.float32)
+
+
+@pytest.mark.parametrize("code_dtype", CODE_TYPES)
+@pytest.mark.parametrize("block_t", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_every_tile(code_dtype, block_t):
+    """Every tile, whole and in slices, on one pair of CTAs and on many, with stores of one channel
+    and of four, and with fewer tokens than a tile."""
+    for M in (block_t - 31, block_t, 3 * block_t - 5):
+        for i, (N, K) in enumerate([(300, 1000), (520, 1536), (256, 130)]):
+            check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, torch.float32, kernel=2,
+                  block_t=block_t, splits=1, y_extra=4 * (i % 2))
+            check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, kernel=2, block_t=block_t,
+                  splits=1, max_ctas=2)
+            for splits in (2, 4):
+                if -(-K // 128) >= splits:
+                    check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, torch.float32, kernel=2,
+                          block_t=block_t, splits=splits, y_extra=4 * (i % 2))
+
+
+@pytest.mark.parametrize("code_dtype", CODE_TYPES)
+def test_few_tokens_on_both_kernels(code_dtype):
+    for M in (1, 5, 8, 9, 16):
+        for kernel in (1, 2):
+            check(M, 777, 1030, code_dtype, torch.float32, 13 * M, kernel=kernel)
+
+
+@pytest.mark.parametrize("code_dtype", CODE_TYPES)
+def test_a_wait_that_runs_out_is_reported(code_dtype):
+    """The loader's first copy left out (a test flag): every wait on it runs out of its 50 ms, the
+    kernel ends, the check reports it once, and the plan's next user is not affected."""
+    x, sx, w, sw, _ = case(100, 300, 1000, code_dtype, torch.float32, 90)
+    for splits in (1, 2):
+        plan = capi.linear_q8_plan(100, 300, 1000, capi.q8_code_type(code_dtype), 0, block_t=64,
+                                   splits=splits, wait_timeout_ms=50, debug_flags=1)
+        y = torch.zeros(100, 300, device="cuda")
+        capi.linear_q8_run(plan, x, sx, w, sw, y)
+        assert capi.linear_q8_check(plan) == capi.CONV3D_EDEVICE
+        assert capi.linear_q8_check(plan) == capi.CONV3D_OK
+        capi.linear_q8_destroy(plan)
+    check(100, 300, 1000, code_dtype, torch.float32, 90)
+
+
+def test_options_that_leave_no_tiling():
+    x, sx, w, sw, _ = case(40, 64, 200, torch.int8, torch.float32, 91)
+    y = torch.zeros(40, 64, device="cuda")
+    for options in (dict(block_t=96), dict(splits=4)):
+        plan = capi.linear_q8_plan(40, 64, 200, capi.Q8_INT8, 0, **options)
+        with pytest.raises(capi.Conv3dFp8Error) as e:
+            capi.linear_q8_run(plan, x, sx, w, sw, y)
+        assert e.value.status == capi.CONV3D_EUNSUPPORTED
+        capi.linear_q8_destroy(plan)
+    for options in (dict(block_t=33), dict(block_t=288), dict(splits=3), dict(kernel=3),
+                    dict(max_ctas=-1), dict(wait_timeout_ms=-1)):
+        with pytest.raises(capi.Conv3dFp8Error) as e:
+            capi.linear_q8_plan(40, 64, 200, capi.Q8_INT8, 0, **options)
+        assert e.value.status == capi.CONV3D_EINVAL
+    with pytest.raises(capi.Conv3dFp8Error) as e:
+        capi.linear_q8_plan(40, 64, 200, capi.Q8_INT8, 0, kernel=1)
+    assert e.value.status == capi.CONV3D_EUNSUPPORTED
 
 
 def test_int8_extremes_are_exact():
