@@ -111,6 +111,24 @@ bool encode_rows(CUtensorMap* map, const void* base, int elem, long long rows, l
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// y, stored in boxes of 128 channels by as many tokens as make 8 KB; what lies outside is dropped.
+bool encode_y(CUtensorMap* map, void* y, int y_type, long long rows, long long cols,
+              long long pitch) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const int elem = value_bytes(y_type);
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(pitch * elem)};
+  const cuuint32_t box[2] = {128, (cuuint32_t)(kTcYBoxBytes / (128 * elem))};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType type = y_type == Q8_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : y_type == Q8_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, type, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Whether every row starts on the grid of the vector accesses. A pitch counts only between rows.
 bool rows_aligned(const RowsParams& p, int vb) {
   const bool one = p.rows <= 1;
@@ -304,7 +322,10 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
   p.status = reinterpret_cast<int*>(plan->workspace + plan->status_off);
   p.timeout_ns = plan->timeout_ns;
   p.debug_flags = plan->debug_flags;
-  CUtensorMap wmap{}, xmap{};
+  CUtensorMap wmap{}, xmap{}, ymap{};
+  const long long y_pitch = p.M > 1 ? p.y_pitch : round_up(p.N, 8);
+  p.y_tma = aligned(p.y, 16) && y_pitch * value_bytes(p.y_type) % 16 == 0;
+  if (p.y_tma && !encode_y(&ymap, p.y, p.y_type, p.M, p.N, y_pitch)) return CONV3D_ECUDA;
   if (!encode_rows(&wmap, p.w, 1, p.N, p.K, p.w_pitch, kTcWBoxRows) ||
       !(int8 ? encode_rows(&xmap, p.xh, 2, p.M, p.K, p.xh_pitch, p.block_t / 2)
              : encode_rows(&xmap, p.x, 1, p.M, p.K, p.x_pitch, p.block_t / 2)))
@@ -313,7 +334,7 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
     const conv3d_status st = launched(launch_linear_expand(p, stream));
     if (st != CONV3D_OK) return st;
   }
-  return launched(launch_linear_tc(p, plan->code_type, wmap, xmap, plan->lim, stream));
+  return launched(launch_linear_tc(p, plan->code_type, wmap, xmap, ymap, plan->lim, stream));
 }
 
 extern "C" conv3d_status linear_q8_check(linear_q8_plan_t plan) {

@@ -42,6 +42,7 @@ struct LinearParams {
   int M, N, K;           // tokens, channels, summed length
   int y_type, bias_type;
   int y_vec;             // four channels of y may be stored at once
+  int y_tma;             // y's tiles may leave by TMA
   // the tensor-core kernel's tiling (linear_tc_decide) and workspace
   int block_t;           // tokens of a tile (a tile has kTcChannels channels)
   int m_tiles, n_tiles, k_blocks;
@@ -71,11 +72,14 @@ struct TcLimits {
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim);
 // Boxes of the tensor maps: rows of w and of x (or xh) one CTA loads at a time.
 constexpr int kTcWBoxRows = 128;
+// The box of y's map: 128 channels of 8 KB's worth of tokens.
+constexpr int kTcYBoxBytes = 8192;
 size_t linear_tc_smem_bytes(const LinearParams& p, int code_type);
 cudaError_t linear_tc_setup();         // the kernels' shared-memory grant
 cudaError_t linear_tc_max_clusters(int (&clusters)[3]);
 cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream);  // x -> xh
 cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
-                             const CUtensorMap& xmap, const TcLimits& lim, cudaStream_t stream);
+                             const CUtensorMap& xmap, const CUtensorMap& ymap, const TcLimits& lim,
+                             cudaStream_t stream);
 
 }  // namespace c3d

@@ -13,19 +13,20 @@
 // up to 2^24. So the product runs as kind::f16, at the f16 rate, on codes turned into f16:
 //   - x, which every channel tile reads again, is expanded to f16 once by a small kernel before
 //     (3 bytes of traffic a code);
-//   - w stays 8 bits wide all the way to shared memory. Eight converter warps (four for each half of
-//     a stage's 128 codes) read 64 codes of a row each thread, turn them into f16 (a byte under the
-//     exponent of 1024, minus 1152 with the sign bit flipped: a permute and a subtraction for each
-//     two codes) and write them to TMEM, from where the MMA takes its A operand. Shared memory then
-//     carries the codes once in and once out, and no f16 copy of w: 96 bytes a cycle at 256 tokens
-//     in place of 192, of the 128 that it moves.
+//   - w stays 8 bits wide all the way to shared memory. Converter warps read 64 codes of a row each
+//     thread, turn them into f16 (a byte under the exponent of 1024, minus 1152 with the sign bit
+//     flipped: a permute and a subtraction for each two codes) and write them to TMEM, from where
+//     the MMA takes its A operand. Shared memory then carries the codes once in and once out, and no
+//     f16 copy of w: 96 bytes a cycle at 256 tokens in place of 192, of the 128 that it moves. One
+//     such step is a chain of about 800 cycles (wait, load, convert, store, publish), so four
+//     groups of four warps take it by turns: two halves of a stage, every other stage.
 //
 // Few tiles: a tile is split along K over the pairs of one cluster (4 or 8 CTAs). Each CTA leaves its
 // partial sums in its own shared memory and adds up its share of the tokens from all of them over
 // distributed shared memory, in the order of the slices: nothing passes through global memory, and
 // a result does not depend on which slice is ready first.
 //
-// Roles of a CTA: warps 0-3 epilogue, 4-11 converters (int8), then TMA and MMA (the leader CTA's).
+// Roles of a CTA: warps 0-3 epilogue, then 16 converters (int8), TMA and MMA (the leader CTA's).
 // Every wait is bounded; one that runs out records a status bit and both CTAs wind down.
 #include <algorithm>
 
@@ -34,8 +35,10 @@
 
 namespace c3d {
 
-constexpr int kTcThreads = 448;
-constexpr int kTcTmaWarp = 12, kTcMmaWarp = 13;
+template <bool kInt8>
+constexpr int kTcTmaWarpOf = kInt8 ? 20 : 4;
+template <bool kInt8>
+constexpr int kTcThreads = (kTcTmaWarpOf<kInt8> + 2) * 32;
 constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // w's codes of one stage: 16 KB a CTA
 constexpr int kTcMaxStages = 8;
 constexpr int kTcSmemBudget = 200 * 1024;
@@ -45,6 +48,7 @@ constexpr int kTcSlotCols = kTcSlotK / 2;           // in 32 columns
 constexpr int kTcMaxSlots = 8;
 constexpr uint64_t kTcAbortSettleNs = 2ull * 1000 * 1000;  // let copies in flight land on abort
 
+constexpr int kTcBoxBytes = kTcYBoxBytes;           // one staging buffer of the epilogue
 constexpr int kTcBars = 3 * kTcMaxStages + 2 * kTcMaxSlots + 5;
 
 // x's bytes of one stage of one CTA (half of the tile's tokens).
@@ -113,7 +117,7 @@ __device__ __forceinline__ void tc_join(const LinearParams& p, const TcTile& t, 
     sc[i] = ScaleBias{__ldg(p.scale_w + c), p.bias ? q8_load_value(p.bias, p.bias_type, c) : 0.0f};
   }
   const int end = min(tokens, (split + 1) * share);
-  for (int c = split * share + (threadIdx.x >> 5); c < end; c += kTcThreads / 32) {
+  for (int c = split * share + (threadIdx.x >> 5); c < end; c += blockDim.x / 32) {
     const uint32_t at = part + (uint32_t)(c * 128 + 4 * lane) * 4u;
     float4 a[4];
 #pragma unroll
@@ -140,10 +144,63 @@ __device__ __forceinline__ void tc_join(const LinearParams& p, const TcTile& t, 
   }
 }
 
+// The epilogue of one tile in one CTA, for its four epilogue warps: thread = channel. 8 KB of the
+// tile at a time (32 tokens of a 16-bit y, 16 of an fp32 one) are staged in shared memory as
+// [token][128 channels], in two buffers by turns (`boxes` counts them), and leave by a TMA store
+// that y's extents bound, or by stores of whole token rows: for a y off the 16-byte grid, and for
+// the last channels of a y whose rows end inside 16 bytes (a TMA store was seen to write the
+// whole of the 16 bytes that hold a row's last element). Stored
+// straight from the accumulator's lanes, 64 bytes a warp, the 67 MB of y of an e4m3 product of 4096 x
+// 8192 x 4096 took 26 of its 105 us. `release` is called once the accumulator has been read.
+template <typename Y, typename Release>
+__device__ __forceinline__ void tc_epilogue(const LinearParams& p, const CUtensorMap* ymap,
+                                            uint32_t trow, const float* scale, ScaleBias sc,
+                                            int tokens, long long m0, int n0, uint8_t* staging,
+                                            uint32_t& boxes, Release release) {
+  constexpr int kRows = kTcBoxBytes / (128 * (int)sizeof(Y));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool by_tma = p.y_tma && (n0 + 128 <= p.N || p.N * (int)sizeof(Y) % 16 == 0);
+  for (int c = 0; c < tokens; c += 32) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(trow + c, r);
+    tmem_ld_wait();
+    if (c + 32 >= tokens) release();
+#pragma unroll
+    for (int h = 0; h < 32; h += kRows) {
+      if (c + h >= tokens) break;
+      uint8_t* buf = staging + (boxes & 1u) * kTcBoxBytes;
+      if (threadIdx.x == 0) bulk_wait_group_read<1>();  // the store from this buffer, two boxes ago
+      named_barrier_sync(1, 128);
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        reinterpret_cast<Y*>(buf)[j * 128 + threadIdx.x] =
+            q8_from_float<Y>(sc(__uint_as_float(r[h + j]), scale[c + h + j]));
+      if (by_tma) fence_proxy_async_smem();
+      named_barrier_sync(1, 128);
+      if (threadIdx.x == 0) {
+        if (by_tma && n0 < p.N) tma_store_2d(ymap, smem_u32(buf), n0, (int)m0 + c + h);
+        bulk_commit_group();  // one a box, empty or not: the wait above counts them
+      }
+      if (!by_tma) {
+        const int rows = min(kRows, tokens - c - h);
+        for (int j = warp; j < rows; j += 4) {
+          Y* dst = static_cast<Y*>(p.y) + (m0 + c + h + j) * p.y_pitch + n0;
+#pragma unroll
+          for (int i = lane; i < 128; i += 32)
+            if (n0 + i < p.N) dst[i] = reinterpret_cast<const Y*>(buf)[j * 128 + i];
+        }
+      }
+      ++boxes;
+    }
+  }
+}
+
 template <bool kInt8>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
     linear_q8_tc_kernel(const __grid_constant__ CUtensorMap wmap,
-                        const __grid_constant__ CUtensorMap xmap, const LinearParams p) {
+                        const __grid_constant__ CUtensorMap xmap,
+                        const __grid_constant__ CUtensorMap ymap, const LinearParams p) {
+  constexpr int kTcTmaWarp = kTcTmaWarpOf<kInt8>, kTcMmaWarp = kTcTmaWarp + 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
@@ -151,7 +208,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t x_bytes = tc_x_bytes(p.block_t, kInt8);
   uint8_t* sW = smem;
   uint8_t* sX = smem + (size_t)S * kTcWBytes;
-  float* sScale = reinterpret_cast<float*>(sX + (size_t)S * x_bytes);  // [4 warps][kTcMaxTokens]
+  uint8_t* sBox = sX + (size_t)S * x_bytes;  // the epilogue's two staging buffers
+  float* sScale = reinterpret_cast<float*>(sBox + 2 * kTcBoxBytes);  // [4 warps][kTcMaxTokens]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + 4 * kTcMaxTokens);
   // bars: full[S] (the leader's; e4m3: both operands, int8: x), empty[S], w_full[S] (int8),
   // slot_full[8] (the leader's), slot_empty[8], acc_full[2], acc_empty[2] (the leader's), drain
@@ -205,6 +263,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == kTcTmaWarp && lane == 0) {
     prefetch_tensormap(&wmap);
     prefetch_tensormap(&xmap);
+    if (p.y_tma) prefetch_tensormap(&ymap);
   }
   tc_fence_before();
   __syncthreads();
@@ -220,39 +279,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------------------------------------ epilogue
     float* scale = sScale + warp * kTcMaxTokens;
     int buf = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, boxes = 0;
     for (int u = first_tile; u < num_tiles; u += tile_step) {
       const TcTile un = tc_tile(p, u);
       const long long n = (long long)un.n_tile * kTcChannels + rank * 128 + threadIdx.x;
-      const bool n_ok = n < p.N;
       const long long m0 = (long long)un.m_tile * p.block_t;
       const int tokens = (int)min((long long)p.block_t, p.M - m0);
       __syncwarp();
       for (int t = lane; t < p.block_t; t += 32) scale[t] = t < tokens ? p.scale_x[m0 + t] : 0.0f;
       ScaleBias sc{0.0f, 0.0f};
-      if (n_ok) {
+      if (n < p.N) {
         sc.w = __ldg(p.scale_w + n);
         if (p.bias) sc.bias = q8_load_value(p.bias, p.bias_type, n);
       }
       __syncwarp();
-      if (!wait_bounded_warp(acc_full(buf), phase, ab, kStatusWaitAccFull)) break;
+      // the four warps go on or stop together: they share the staging buffers
+      const bool ok = wait_bounded_warp(acc_full(buf), phase, ab, kStatusWaitAccFull);
+      if (!named_barrier_and(1, 128, ok)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t)(buf * p.acc_stride) + ((uint32_t)(warp * 32) << 16);
-      if (p.splits == 1) {
-        for (int c = 0; c < p.block_t; c += 32) {
-          if (c >= tokens) break;
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(trow + c, r);
-          tmem_ld_wait();
-          if (n_ok) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c + j < tokens)
-                q8_store_value(p.y, p.y_type, (m0 + c + j) * p.y_pitch + n,
-                               sc(__uint_as_float(r[j]), scale[c + j]));
-          }
-        }
-      } else {
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (acc_empty(buf) - bars_u32));
+      };
+      const int n0 = un.n_tile * kTcChannels + (int)rank * 128;
+      if (p.splits > 1) {
         // the pipeline's stages are free: every copy of this pair has been consumed
         float* part = reinterpret_cast<float*>(sW) + threadIdx.x;
         for (int c = 0; c < p.block_t; c += 32) {
@@ -262,35 +314,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) part[(c + j) * 128] = __uint_as_float(r[j]);
         }
+        release();
+      } else if (p.y_type == Q8_F32) {
+        tc_epilogue<float>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
+      } else if (p.y_type == Q8_BF16) {
+        tc_epilogue<__nv_bfloat16>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
+      } else {
+        tc_epilogue<__half>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (acc_empty(buf) - bars_u32));
       if (++buf == p.acc_bufs) {
         buf = 0;
         phase ^= 1u;
       }
     }
+    if (threadIdx.x == 0) bulk_wait_group_all();  // the stores have read their buffers
   } else if (warp < kTcTmaWarp) {
     // ---------------------------------------------------------------------------- converters
     if (kInt8) {
-      const int quad = warp & 3, half = (warp - 4) >> 2;
+      const int quad = warp & 3, half = ((warp - 4) >> 2) & 1, turn = (warp - 4) >> 3;
       const int row = quad * 32 + lane;
       const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+      const uint32_t slot_shift = p.a_slots == 8 ? 3 : 2;
       Ring ring;
-      Ring slots;
-      slots.stage = half;  // this half's slots are half, half + 2, ...
+      uint32_t it = 0;     // K blocks of all tiles so far; this warp takes those of its turn
       int pending = -1;    // the slot whose store is under way
       auto publish = [&]() {
+        if (pending < 0) return;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (slot_full(pending) - bars_u32));
+        pending = -1;
       };
       bool aborted = false;
       for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
-        const TcTile un = tc_tile(p, u);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next(S)) {
+          if ((it & 1u) != (uint32_t)turn) continue;
+          const uint32_t seq = 2 * it + half;  // halves of stages go through the slots in order
+          const int slot = (int)(seq & (uint32_t)(p.a_slots - 1));
+          const uint32_t slot_phase = (seq >> slot_shift) & 1u;
+          // the store before is published behind this stage's loads, which give it the time to
+          // finish, unless those would have to wait
+          if (!__all_sync(0xFFFFFFFFu, mbar_test(w_full(ring.stage), ring.phase))) publish();
           if (!wait_bounded_warp(w_full(ring.stage), ring.phase, ab, kStatusWaitFull)) {
             aborted = true;
             break;
@@ -300,27 +365,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // 16-byte chunk i of this half, where the swizzle put it
             c[i] = *reinterpret_cast<const uint4*>(src + (((4 * half + i) ^ (row & 7)) << 4));
-          if (pending >= 0) publish();  // the store before has had the loads' time to finish
+          publish();
           uint32_t h[32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) int8_to_f16(c[i], h + 8 * i);
-          if (!wait_bounded_warp(slot_empty(slots.stage), slots.phase ^ 1u, ab,
-                                       kStatusWaitEmpty)) {
+          if (!wait_bounded_warp(slot_empty(slot), slot_phase ^ 1u, ab, kStatusWaitEmpty)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          tmem_st_32x32b_x32(slots_base + lane_base + (uint32_t)(slots.stage * kTcSlotCols), h);
-          pending = slots.stage;
-          ring.next(S);
-          slots.stage += 2;
-          if (slots.stage >= p.a_slots) {
-            slots.stage = half;
-            slots.phase ^= 1u;
-          }
+          tmem_st_32x32b_x32(slots_base + lane_base + (uint32_t)(slot * kTcSlotCols), h);
+          pending = slot;
         }
       }
-      if (pending >= 0) publish();
+      publish();
     }
   } else if (warp == kTcTmaWarp) {
     // ------------------------------------------------------------------------------ TMA loader
@@ -516,16 +574,18 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
 
 size_t linear_tc_smem_bytes(const LinearParams& p, int code_type) {
   return 1024 + (size_t)p.stages * (kTcWBytes + tc_x_bytes(p.block_t, code_type == Q8_INT8)) +
-         4 * kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
+         2 * kTcBoxBytes + 4 * kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
 }
 
+constexpr int kTcMostSmem =
+    1024 + kTcSmemBudget + 2 * kTcBoxBytes + 4 * kTcMaxTokens * 4 + kTcBars * 8 + 16;
+
 cudaError_t linear_tc_setup() {
-  const int most = 1024 + kTcSmemBudget + 4 * kTcMaxTokens * 4 + kTcBars * 8 + 16;
   cudaError_t e = cudaFuncSetAttribute(linear_q8_tc_kernel<true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMostSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(linear_q8_tc_kernel<false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMostSmem);
   return e;
 }
 
@@ -539,8 +599,8 @@ cudaError_t linear_tc_max_clusters(int (&clusters)[3]) {
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.gridDim = dim3(2u << i, 1, 1);
-    cfg.blockDim = dim3(kTcThreads, 1, 1);
-    cfg.dynamicSmemBytes = kTcSmemBudget;
+    cfg.blockDim = dim3(kTcThreads<true>, 1, 1);
+    cfg.dynamicSmemBytes = kTcMostSmem;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const cudaError_t e =
@@ -577,16 +637,17 @@ cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
-                             const CUtensorMap& xmap, const TcLimits& lim, cudaStream_t stream) {
+                             const CUtensorMap& xmap, const CUtensorMap& ymap, const TcLimits& lim,
+                             cudaStream_t stream) {
   const long long tiles = (long long)p.m_tiles * p.n_tiles;
   const int cluster = 2 * p.splits;
   const int grid = cluster * (int)std::min<long long>(tiles, std::max(1, lim.clusters[p.splits / 2]));
   const size_t smem = linear_tc_smem_bytes(p, code_type);
   if (code_type == Q8_INT8)
-    return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads, cluster, smem, stream, wmap, xmap,
-                      p);
-  return launch_pdl(linear_q8_tc_kernel<false>, grid, kTcThreads, cluster, smem, stream, wmap, xmap,
-                    p);
+    return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads<true>, cluster, smem, stream, wmap, xmap,
+                      ymap, p);
+  return launch_pdl(linear_q8_tc_kernel<false>, grid, kTcThreads<false>, cluster, smem, stream, wmap, xmap,
+                    ymap, p);
 }
 
 }  // namespace c3d
