@@ -56,7 +56,7 @@ struct LinearParams {
 };
 
 // Tokens that the kernel for few tokens takes at most; it needs no workspace.
-constexpr int kFewTokens = 16;
+constexpr int kFewTokens = 32;
 cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t stream);
 
 // The tensor-core kernel: CTA pairs, tiles of 256 channels by block_t tokens.

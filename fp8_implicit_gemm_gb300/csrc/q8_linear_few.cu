@@ -2,19 +2,18 @@
 // straight from global memory into registers, and its bytes are what bounds the time. Neither TMEM
 // nor a workspace is used: allocating TMEM alone costs more than these products take.
 //
-// A block takes 16 channels; its warps share K in steps of 128 codes, so that one warp's loads cover
-// 128 consecutive bytes of 8 rows, and add up through shared memory in a fixed order. A warp's
-// product of 16 channels by 8 tokens is mma.sync m16n8k16 on f16, in which every code of either
-// type is exact; the accumulator is fp32. The instruction's order of k is free as long as both
-// operands use the same: thread t of a row takes 16 consecutive bytes, and MMA j of the four they
-// feed takes bytes 4j..4j+3 of each.
+// A block takes 16 or 32 channels; its 8 or 16 warps share K in steps of 128 codes, so that one warp's
+// loads cover 128 consecutive bytes of 8 rows, and add up through shared memory in a fixed order. The
+// loads of a warp's next step are issued before this step's products. A warp's product of 16
+// channels by 8 tokens is mma.sync m16n8k16 on f16, in which every code of either type is exact; the
+// accumulator is fp32. The instruction's order of k is free as long as both operands use the same:
+// thread t of a row takes 16 consecutive bytes, and MMA j of the four they feed takes bytes
+// 4j..4j+3 of each.
 #include "ptx.cuh"
 #include "q8_common.cuh"
 
 namespace c3d {
 
-constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
-constexpr int kFewChannels = 16;
 constexpr int kFewStep = 128;  // codes of K a warp takes at a time
 
 // Two e4m3 codes to f16, exactly.
@@ -49,81 +48,127 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 // The 16 bytes at column k of a row, zero past K (codes behind a row's end are not used, whatever
 // they hold). k is a multiple of 16 and rows start on 16-byte boundaries, so a load that takes in a
 // row's last code stays inside that code's aligned 16 bytes.
-__device__ __forceinline__ uint4 load_codes(const uint8_t* row, int k, int K, bool ok) {
-  if (!ok || k >= K) return make_uint4(0, 0, 0, 0);
-  uint4 c = __ldg(reinterpret_cast<const uint4*>(row + k));
+__device__ __forceinline__ uint4 load_codes_tail(const uint8_t* row, int k, int K) {
+  if (k >= K) return make_uint4(0, 0, 0, 0);
+  const uint4 c = __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t w[4] = {c.x, c.y, c.z, c.w};
   const int left = K - k;
-  if (left < 16) {
-    uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int keep = left - 4 * i;
-      if (keep <= 0)
-        w[i] = 0;
-      else if (keep < 4)
-        w[i] &= (1u << (8 * keep)) - 1u;
-    }
-    c = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) {
+    const int keep = left - 4 * i;
+    if (keep <= 0)
+      w[i] = 0;
+    else if (keep < 4)
+      w[i] &= (1u << (8 * keep)) - 1u;
   }
-  return c;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// kTiles: groups of 8 tokens.
-template <bool kInt8, int kTiles>
-__global__ void __launch_bounds__(kFewThreads) linear_q8_few_kernel(const LinearParams p) {
-  __shared__ float part[kFewWarps][kTiles * 8][kFewChannels + 1];
+// One step's codes of a warp: kCh x 16 channels and kTok x 8 tokens by 128 codes of K.
+template <int kCh, int kTok>
+struct FewStep {
+  uint4 w[kCh][2][2], x[kTok][2];
+};
+
+// kCh: 16-channel groups of a block; kTok: 8-token groups of the product.
+template <bool kInt8, int kCh, int kTok, int kFewWarps>
+__global__ void __launch_bounds__(kFewWarps * 32) linear_q8_few_kernel(const LinearParams p) {
+  constexpr int kChannels = 16 * kCh, kTokens = 8 * kTok;
+  __shared__ float part[kFewWarps][kTokens][kChannels + 1];
   pdl_wait_primary();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const long long n0 = (long long)blockIdx.x * kFewChannels;
-  const bool ok0 = n0 + g < p.N, ok1 = n0 + g + 8 < p.N;
-  const uint8_t* w0 = p.w + (n0 + g) * p.w_pitch;
-  const uint8_t* w1 = w0 + 8 * p.w_pitch;
-  const uint8_t* xr[kTiles];
-  bool xok[kTiles];
+  const long long n0 = (long long)blockIdx.x * kChannels;
+  // Rows past the last channel or token read the last one's codes: what they give is not stored, and
+  // no load depends on a condition, which would make the compiler wait for it at once.
+  const uint8_t* wrow[kCh][2];
+  const uint8_t* xrow[kTok];
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) {
-    xok[i] = 8 * i + g < p.M;
-    xr[i] = p.x + (long long)(8 * i + g) * p.x_pitch;
-  }
-  float acc[kTiles][4] = {};
-  for (int k0 = warp * kFewStep; k0 < p.K; k0 += kFewWarps * kFewStep) {
-    uint4 a[2][2], b[kTiles][2];
+  for (int c = 0; c < kCh; ++c)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      wrow[c][r] = p.w + min(n0 + 16 * c + 8 * r + g, (long long)p.N - 1) * p.w_pitch + 16 * t;
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) xrow[i] = p.x + (long long)min(8 * i + g, p.M - 1) * p.x_pitch + 16 * t;
+  using Step = FewStep<kCh, kTok>;
+  auto load = [&](Step& s, int k0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = k0 + 64 * h + 16 * t;
-      a[0][h] = load_codes(w0, k, p.K, ok0);
-      a[1][h] = load_codes(w1, k, p.K, ok1);
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) b[i][h] = load_codes(xr[i], k, p.K, xok[i]);
+      for (int c = 0; c < kCh; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          s.w[c][r][h] = __ldg(reinterpret_cast<const uint4*>(wrow[c][r] + k0 + 64 * h));
+#pragma unroll
+      for (int i = 0; i < kTok; ++i)
+        s.x[i][h] = __ldg(reinterpret_cast<const uint4*>(xrow[i] + k0 + 64 * h));
     }
+  };
+  float acc[kCh][kTok][4] = {};
+  auto multiply = [&](const Step& s) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t fa[2][8];
-      codes_to_f16<kInt8>(a[0][h], fa[0]);
-      codes_to_f16<kInt8>(a[1][h], fa[1]);
+      uint32_t fx[kTok][8];
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        uint32_t fb[8];
-        codes_to_f16<kInt8>(b[i][h], fb);
+      for (int i = 0; i < kTok; ++i) codes_to_f16<kInt8>(s.x[i][h], fx[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_16816(acc[i], fa[0][2 * j], fa[1][2 * j], fa[0][2 * j + 1], fa[1][2 * j + 1],
-                    fb[2 * j], fb[2 * j + 1]);
+      for (int c = 0; c < kCh; ++c) {
+        uint32_t fw[2][8];
+        codes_to_f16<kInt8>(s.w[c][0][h], fw[0]);
+        codes_to_f16<kInt8>(s.w[c][1][h], fw[1]);
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_16816(acc[c][i], fw[0][2 * j], fw[1][2 * j], fw[0][2 * j + 1], fw[1][2 * j + 1],
+                      fx[i][2 * j], fx[i][2 * j + 1]);
       }
     }
+  };
+  constexpr int kStride = kFewWarps * kFewStep;
+  const int whole = p.K / kFewStep * kFewStep;  // K in whole steps
+  int k0 = warp * kFewStep;
+  if (k0 < whole) {
+    Step a, b;  // one in use, one on its way
+    load(a, k0);
+    while (true) {
+      if (k0 + kStride < whole) load(b, k0 + kStride);
+      multiply(a);
+      k0 += kStride;
+      if (k0 >= whole) break;
+      if (k0 + kStride < whole) load(a, k0 + kStride);
+      multiply(b);
+      k0 += kStride;
+      if (k0 >= whole) break;
+    }
+  }
+  if (k0 == whole && whole < p.K) {  // the last, incomplete step, by the warp whose turn it is
+    Step s;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = whole + 64 * h;  // the rows' pointers are 16 t bytes in
+#pragma unroll
+      for (int c = 0; c < kCh; ++c)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) s.w[c][r][h] = load_codes_tail(wrow[c][r], k, p.K - 16 * t);
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) s.x[i][h] = load_codes_tail(xrow[i], k, p.K - 16 * t);
+    }
+    multiply(s);
   }
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) {
-    part[warp][8 * i + 2 * t][g] = acc[i][0];
-    part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
-    part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
-    part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
-  }
+  for (int c = 0; c < kCh; ++c)
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+      part[warp][8 * i + 2 * t][16 * c + g] = acc[c][i][0];
+      part[warp][8 * i + 2 * t + 1][16 * c + g] = acc[c][i][1];
+      part[warp][8 * i + 2 * t][16 * c + g + 8] = acc[c][i][2];
+      part[warp][8 * i + 2 * t + 1][16 * c + g + 8] = acc[c][i][3];
+    }
   __syncthreads();
-  for (int e = threadIdx.x; e < kTiles * 8 * kFewChannels; e += kFewThreads) {
-    const int c = e & (kFewChannels - 1), m = e / kFewChannels;
+  for (int e = threadIdx.x; e < kTokens * kChannels; e += kFewWarps * 32) {
+    const int c = e % kChannels, m = e / kChannels;
     const long long n = n0 + c;
     if (m >= p.M || n >= p.N) continue;
     float v = part[0][m][c];
@@ -135,22 +180,36 @@ __global__ void __launch_bounds__(kFewThreads) linear_q8_few_kernel(const Linear
   }
 }
 
-cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t stream) {
+template <bool kInt8, int kCh, int kTok, int kFewWarps>
+static cudaError_t launch_one(const LinearParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((p.N + kFewChannels - 1) / kFewChannels));
-  cfg.blockDim = dim3(kFewThreads);
+  cfg.gridDim = dim3((unsigned)((p.N + 16 * kCh - 1) / (16 * kCh)));
+  cfg.blockDim = dim3(kFewWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const bool int8 = code_type == Q8_INT8;
-  if (p.M <= 8)
-    return int8 ? cudaLaunchKernelEx(&cfg, linear_q8_few_kernel<true, 1>, p)
-                : cudaLaunchKernelEx(&cfg, linear_q8_few_kernel<false, 1>, p);
-  return int8 ? cudaLaunchKernelEx(&cfg, linear_q8_few_kernel<true, 2>, p)
-              : cudaLaunchKernelEx(&cfg, linear_q8_few_kernel<false, 2>, p);
+  return cudaLaunchKernelEx(&cfg, linear_q8_few_kernel<kInt8, kCh, kTok, kFewWarps>, p);
+}
+
+template <bool kInt8>
+static cudaError_t launch_few(const LinearParams& p, cudaStream_t stream) {
+  // Up to 8 tokens: 16 channels a block while that leaves SMs idle; 32 (half the reads of x) on 16
+  // warps while one block an SM holds all, on 8 warps, two blocks an SM, beyond. Measured in us, N x
+  // K, 1 token int8: 2048 x 4096 3.0 / 3.6 / 3.5, 4096 x 8192 9.7 / 6.8 / 8.6, 8192 x 4096 12.1 / 8.5
+  // / 6.8. Up to 16 and 32 tokens, whose x takes more registers: 16 channels on 8 warps (16 tokens,
+  // 8192 x 4096: 13.2 / 13.3 / 11.8, and 9.8 so).
+  if (p.M > 16) return launch_one<kInt8, 1, 4, 8>(p, stream);
+  if (p.M > 8) return launch_one<kInt8, 1, 2, 8>(p, stream);
+  if (p.N <= 2432) return launch_one<kInt8, 1, 1, 16>(p, stream);
+  if (p.N <= 4864) return launch_one<kInt8, 2, 1, 16>(p, stream);
+  return launch_one<kInt8, 2, 1, 8>(p, stream);
+}
+
+cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t stream) {
+  return code_type == Q8_INT8 ? launch_few<true>(p, stream) : launch_few<false>(p, stream);
 }
 
 }  // namespace c3d
