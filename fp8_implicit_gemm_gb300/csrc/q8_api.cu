@@ -15,9 +15,12 @@ struct linear_q8_plan_s {
   int few = kFewTokens;            // tokens up to which the kernel for few tokens runs
   unsigned long long timeout_ns = 0;
   int debug_flags = 0;
-  uint8_t* workspace = nullptr;    // x as f16 (int8), status word
-  size_t status_off = 0, workspace_bytes = 0;
+  uint8_t* workspace = nullptr;    // status word; x as f16 (int8, many tokens)
+  size_t workspace_bytes = 0;
 };
+
+constexpr size_t kStatusBytes = 256;  // the workspace's head
+
 
 namespace {
 
@@ -95,8 +98,8 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// A matrix of `rows` rows of `cols` elements (1 byte, or f16), loaded in boxes of 128 bytes by
-// box_rows rows with the 128-byte swizzle; what lies outside reads zero.
+// A matrix of codes (elem 1) or f16 (elem 2), loaded in boxes of 128 bytes by box_rows rows with the
+// 128-byte swizzle; what lies outside reads zero.
 bool encode_rows(CUtensorMap* map, const void* base, int elem, long long rows, long long cols,
                  long long pitch, int box_rows) {
   const EncodeTiledFn enc = encode_tiled();
@@ -251,16 +254,16 @@ extern "C" conv3d_status linear_q8_plan_ex(linear_q8_plan_t* plan, long long max
     // a forced tile no larger than the tokens need, forced slices no more than K has blocks
     pl->lim.block_t = o.block_t;
     pl->lim.splits = o.splits;
-    const long long xh = code_type == Q8_INT8 ? max_rows * round_up(K, 16) * 2 : 0;
-    pl->status_off = (size_t)round_up(xh, 256);
-    pl->workspace_bytes = pl->status_off + 256;
+    pl->workspace_bytes = kStatusBytes;
+    if (code_type == Q8_INT8 && max_rows > kTcXInside)
+      pl->workspace_bytes += (size_t)(max_rows * round_up(K, 16) * 2);
     if (cudaMalloc(&pl->workspace, pl->workspace_bytes) != cudaSuccess) {
       cudaGetLastError();
       delete pl;
       return CONV3D_ENOMEM;
     }
     // the status word is zero between runs; on every stream from here on
-    if (cudaMemset(pl->workspace + pl->status_off, 0, 256) != cudaSuccess ||
+    if (cudaMemset(pl->workspace, 0, kStatusBytes) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
       cudaGetLastError();
       cudaFree(pl->workspace);
@@ -314,23 +317,22 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
   cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
   if (p.M <= plan->few)
     return launched(launch_linear_few(p, plan->code_type, stream));
-  const bool int8 = plan->code_type == Q8_INT8;
   linear_tc_decide(p, plan->code_type, plan->lim);
   if (!p.block_t) return CONV3D_EUNSUPPORTED;  // the options leave no tiling for this many tokens
-  p.xh = reinterpret_cast<uint16_t*>(plan->workspace);
+  p.status = reinterpret_cast<int*>(plan->workspace);
+  p.xh = reinterpret_cast<uint16_t*>(plan->workspace + kStatusBytes);
   p.xh_pitch = round_up(plan->K, 16);
-  p.status = reinterpret_cast<int*>(plan->workspace + plan->status_off);
   p.timeout_ns = plan->timeout_ns;
   p.debug_flags = plan->debug_flags;
-  CUtensorMap wmap{}, xmap{}, ymap{};
   const long long y_pitch = p.M > 1 ? p.y_pitch : round_up(p.N, 8);
   p.y_tma = aligned(p.y, 16) && y_pitch * value_bytes(p.y_type) % 16 == 0;
-  if (p.y_tma && !encode_y(&ymap, p.y, p.y_type, p.M, p.N, y_pitch)) return CONV3D_ECUDA;
+  CUtensorMap wmap{}, xmap{}, ymap{};
   if (!encode_rows(&wmap, p.w, 1, p.N, p.K, p.w_pitch, kTcWBoxRows) ||
-      !(int8 ? encode_rows(&xmap, p.xh, 2, p.M, p.K, p.xh_pitch, p.block_t / 2)
-             : encode_rows(&xmap, p.x, 1, p.M, p.K, p.x_pitch, p.block_t / 2)))
+      !(p.x_expanded ? encode_rows(&xmap, p.xh, 2, p.M, p.K, p.xh_pitch, p.block_t / 2)
+                     : encode_rows(&xmap, p.x, 1, p.M, p.K, p.x_pitch, p.block_t / 2)) ||
+      (p.y_tma && !encode_y(&ymap, p.y, p.y_type, p.M, p.N, y_pitch)))
     return CONV3D_ECUDA;
-  if (int8) {
+  if (p.x_expanded) {
     const conv3d_status st = launched(launch_linear_expand(p, stream));
     if (st != CONV3D_OK) return st;
   }
@@ -344,12 +346,10 @@ extern "C" conv3d_status linear_q8_check(linear_q8_plan_t plan) {
     return CONV3D_ECUDA;
   if (!plan->workspace) return CONV3D_OK;
   int word = 0;
-  if (cudaMemcpy(&word, plan->workspace + plan->status_off, sizeof(int), cudaMemcpyDeviceToHost) !=
-      cudaSuccess)
+  if (cudaMemcpy(&word, plan->workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
     return CONV3D_ECUDA;
   if (word == 0) return CONV3D_OK;
-  if (cudaMemset(plan->workspace + plan->status_off, 0, sizeof(int)) != cudaSuccess)
-    return CONV3D_ECUDA;
+  if (cudaMemset(plan->workspace, 0, sizeof(int)) != cudaSuccess) return CONV3D_ECUDA;
   return CONV3D_EDEVICE;
 }
 

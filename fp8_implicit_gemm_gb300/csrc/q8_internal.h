@@ -47,8 +47,10 @@ struct LinearParams {
   int block_t;           // tokens of a tile (a tile has kTcChannels channels)
   int m_tiles, n_tiles, k_blocks;
   int splits;            // slices of K, one for each pair of a cluster: 1, 2 or 4
-  int stages, acc_bufs, acc_stride, a_slots;
-  uint16_t* xh;          // int8 only: x as f16, [M][xh_pitch]
+  int stages, acc_bufs, acc_stride;
+  // int8 only: K blocks of w in TMEM and of x in shared memory as f16, whether x comes as f16
+  int w_slots, x_slots, x_expanded;
+  uint16_t* xh;          // x as f16, [M][xh_pitch], where it is expanded
   long long xh_pitch;
   int* status;
   unsigned long long timeout_ns;
@@ -70,14 +72,15 @@ struct TcLimits {
 };
 // Fills in the tiling of a product of M, N and K.
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim);
-// Boxes of the tensor maps: rows of w and of x (or xh) one CTA loads at a time.
+// Boxes of the tensor maps: rows of w one CTA loads at a time (of x: half of block_t).
 constexpr int kTcWBoxRows = 128;
 // The box of y's map: 128 channels of 8 KB's worth of tokens.
 constexpr int kTcYBoxBytes = 8192;
-size_t linear_tc_smem_bytes(const LinearParams& p, int code_type);
+// Tokens up to which the kernel turns int8 codes of x into f16 by itself.
+constexpr int kTcXInside = 256;
+cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream);  // x -> xh
 cudaError_t linear_tc_setup();         // the kernels' shared-memory grant
 cudaError_t linear_tc_max_clusters(int (&clusters)[3]);
-cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream);  // x -> xh
 cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
                              const CUtensorMap& xmap, const CUtensorMap& ymap, const TcLimits& lim,
                              cudaStream_t stream);

@@ -11,22 +11,25 @@
 // int8: sm_103a has no fast integer pipe, but an int8 code is exact in f16 (an 11-bit significand),
 // a product of two is an integer of at most 2^14, and the fp32 accumulator holds their sums exactly
 // up to 2^24. So the product runs as kind::f16, at the f16 rate, on codes turned into f16:
-//   - x, which every channel tile reads again, is expanded to f16 once by a small kernel before
-//     (3 bytes of traffic a code);
-//   - w stays 8 bits wide all the way to shared memory. Converter warps read 64 codes of a row each
-//     thread, turn them into f16 (a byte under the exponent of 1024, minus 1152 with the sign bit
-//     flipped: a permute and a subtraction for each two codes) and write them to TMEM, from where
-//     the MMA takes its A operand. Shared memory then carries the codes once in and once out, and no
-//     f16 copy of w: 96 bytes a cycle at 256 tokens in place of 192, of the 128 that it moves. One
-//     such step is a chain of about 800 cycles (wait, load, convert, store, publish), so four
-//     groups of four warps take it by turns: two halves of a stage, every other stage.
+//   - w stays 8 bits wide as far as shared memory. Converter warps read a stage's codes there, half a
+//     row (64 codes) a thread, turn them into f16 (a byte under the exponent of 1024, minus 1152
+//     with the sign bit flipped, a permute and a subtraction for each two codes) and write them to
+//     TMEM, from where the MMA takes its A operand: in shared memory they would come on top of the
+//     codes, x and the MMA's reads, which fill its 128 bytes a cycle at 256 tokens;
+//   - x is expanded to f16 by a small kernel first and loaded as such, 3 bytes of traffic a code, or,
+//     for few tokens, turned by four more warps of this kernel, which saves the launch;
+//   - a K block has one barrier that says that its w and x are there and one commit that frees both,
+//     whatever the depths of their rings: the issuing warp takes about 160 cycles for a wait, 60 for
+//     a commit and 30 for an MMA, and a K block's MMAs take 512 at 128 tokens. With a wait and a
+//     commit for each quarter of a K block it took 2500 cycles.
 //
 // Few tiles: a tile is split along K over the pairs of one cluster (4 or 8 CTAs). Each CTA leaves its
 // partial sums in its own shared memory and adds up its share of the tokens from all of them over
 // distributed shared memory, in the order of the slices: nothing passes through global memory, and
 // a result does not depend on which slice is ready first.
 //
-// Roles of a CTA: warps 0-3 epilogue, then 16 converters (int8), TMA and MMA (the leader CTA's).
+// Roles of a CTA: warps 0-3 epilogue, then 16 converters of w and 4 of x (int8), TMA and MMA (the
+// leader CTA's).
 // Every wait is bounded; one that runs out records a status bit and both CTAs wind down.
 #include <algorithm>
 
@@ -35,25 +38,51 @@
 
 namespace c3d {
 
+constexpr int kTcWWarps = 16, kTcXWarps = 4;        // converters
 template <bool kInt8>
-constexpr int kTcTmaWarpOf = kInt8 ? 20 : 4;
+constexpr int kTcTmaWarpOf = 4 + (kInt8 ? kTcWWarps + kTcXWarps : 0);
 template <bool kInt8>
 constexpr int kTcThreads = (kTcTmaWarpOf<kInt8> + 2) * 32;
 constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // w's codes of one stage: 16 KB a CTA
 constexpr int kTcMaxStages = 8;
-constexpr int kTcSmemBudget = 200 * 1024;
+constexpr int kTcSmemBudget = 208 * 1024;
 constexpr int kTcTmemCols = 512;
-constexpr int kTcSlotK = 64;                        // codes of w a TMEM slot holds as f16
-constexpr int kTcSlotCols = kTcSlotK / 2;           // in 32 columns
-constexpr int kTcMaxSlots = 8;
+constexpr int kTcSlotCols = kTcBlockK / 2;          // a K block of w as f16 in TMEM: 64 columns
+constexpr int kTcDepth = 8;                         // K blocks under way: no ring is deeper
 constexpr uint64_t kTcAbortSettleNs = 2ull * 1000 * 1000;  // let copies in flight land on abort
 
 constexpr int kTcBoxBytes = kTcYBoxBytes;           // one staging buffer of the epilogue
-constexpr int kTcBars = 3 * kTcMaxStages + 2 * kTcMaxSlots + 5;
+constexpr int kTcBars = 2 * kTcMaxStages + 2 * kTcDepth + 5;
 
-// x's bytes of one stage of one CTA (half of the tile's tokens).
-__host__ __device__ inline uint32_t tc_x_bytes(int block_t, bool int8) {
-  return (uint32_t)(block_t / 2) * kTcBlockK * (int8 ? 2 : 1);
+// wait_bounded_warp with less in the way of the next try: the timer, whose read takes several hundred
+// cycles, and the abort flag are looked at after every 64 misses.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const AbortState& ab,
+                                        int code) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xFFFFFFFFu, ok)) {
+    uint64_t t0 = 0;
+    for (uint32_t misses = 1; !ok; ++misses) {
+      ok = mbar_try_wait(bar, parity);
+      if (ok || (misses & 63u) != 0) continue;
+      if (*ab.flag) break;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > ab.timeout_ns) {
+        *ab.flag = 1;
+        atomicOr(ab.status, code);
+        __threadfence();
+        break;
+      }
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+  }
+  return ok;
+}
+
+// x's codes of one stage of one CTA (half of the tile's tokens); as f16 they are twice that.
+__host__ __device__ inline uint32_t tc_x_bytes(int block_t) {
+  return (uint32_t)(block_t / 2) * kTcBlockK;
 }
 
 // One work unit: a tile and a slice [kb0, kb1) of the K blocks. Tiles are taken in groups of
@@ -205,23 +234,29 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
   const int S = p.stages;
-  const uint32_t x_bytes = tc_x_bytes(p.block_t, kInt8);
+  const uint32_t x_bytes = tc_x_bytes(p.block_t);
+  // int8 with x expanded: x's tiles arrive as f16 and a stage holds w's codes alone
+  const bool x_codes = !kInt8 || !p.x_expanded;
   uint8_t* sW = smem;
   uint8_t* sX = smem + (size_t)S * kTcWBytes;
-  uint8_t* sBox = sX + (size_t)S * x_bytes;  // the epilogue's two staging buffers
-  float* sScale = reinterpret_cast<float*>(sBox + 2 * kTcBoxBytes);  // [4 warps][kTcMaxTokens]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + 4 * kTcMaxTokens);
-  // bars: full[S] (the leader's; e4m3: both operands, int8: x), empty[S], w_full[S] (int8),
-  // slot_full[8] (the leader's), slot_empty[8], acc_full[2], acc_empty[2] (the leader's), drain
+  uint8_t* sXh = sX + (x_codes ? (size_t)S * x_bytes : 0);  // x as f16, two 64-code halves a slot
+  uint8_t* sBox = sXh + (kInt8 ? (size_t)p.x_slots * 2 * x_bytes : 0);  // the epilogue's staging
+  float* sScale = reinterpret_cast<float*>(sBox + 2 * kTcBoxBytes);  // [kTcMaxTokens]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kTcMaxTokens);
+  // Barriers (those marked L: the leader's are used). full[S]: a stage's copies have landed (e4m3 L:
+  // both CTAs'; int8: this CTA's). empty[S]: read by the MMAs (e4m3) or the converters (int8).
+  // int8, for K block i of all, at i % kTcDepth: ready L: its w and x are there as f16. done: its MMAs
+  // have completed. acc_full, acc_empty L. drain.
   const uint32_t bars_u32 = smem_u32(bars);
-  auto full = [&](int s) { return bars_u32 + 8u * s; };
-  auto empty = [&](int s) { return bars_u32 + 8u * (kTcMaxStages + s); };
-  auto w_full = [&](int s) { return bars_u32 + 8u * (2 * kTcMaxStages + s); };
-  auto slot_full = [&](int s) { return bars_u32 + 8u * (3 * kTcMaxStages + s); };
-  auto slot_empty = [&](int s) { return bars_u32 + 8u * (3 * kTcMaxStages + kTcMaxSlots + s); };
-  auto acc_full = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 2 * kTcMaxSlots + b); };
-  auto acc_empty = [&](int b) { return bars_u32 + 8u * (3 * kTcMaxStages + 2 * kTcMaxSlots + 2 + b); };
-  const uint32_t drain_bar = bars_u32 + 8u * (kTcBars - 1);
+  auto bar_at = [&](int i) { return bars_u32 + 8u * (uint32_t)i; };
+  auto full = [&](int s) { return bar_at(s); };
+  auto empty = [&](int s) { return bar_at(kTcMaxStages + s); };
+  auto ready = [&](uint32_t i) { return bar_at(2 * kTcMaxStages + (int)(i % kTcDepth)); };
+  auto done = [&](uint32_t i) { return bar_at(2 * kTcMaxStages + kTcDepth + (int)(i % kTcDepth)); };
+  auto parity = [](uint32_t i) { return (i / kTcDepth) & 1u; };
+  auto acc_full = [&](int b) { return bar_at(kTcBars - 5 + b); };
+  auto acc_empty = [&](int b) { return bar_at(kTcBars - 3 + b); };
+  const uint32_t drain_bar = bar_at(kTcBars - 1);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kTcBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -241,12 +276,13 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
-      mbar_init(w_full(s), 1);
+      // an arrival of each converter warp whose turn it is, or a commit's
+      mbar_init(empty(s), kInt8 ? kTcWWarps / 2 + (x_codes ? kTcXWarps : 0) : 1);
     }
-    for (int s = 0; s < kTcMaxSlots; ++s) {
-      mbar_init(slot_full(s), 2 * 4);  // a converter warp's arrival each, of both CTAs
-      mbar_init(slot_empty(s), 1);
+    for (uint32_t i = 0; i < kTcDepth; ++i) {
+      // of both CTAs: the warps of w's two halves, and those of x or the copies of x
+      mbar_init(ready(i), 2 * (kTcWWarps / 2) + (x_codes ? 2 * kTcXWarps : 1));
+      mbar_init(done(i), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full(b), 1);
@@ -277,7 +313,6 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
 
   if (warp < 4) {
     // ------------------------------------------------------------------------------ epilogue
-    float* scale = sScale + warp * kTcMaxTokens;
     int buf = 0;
     uint32_t phase = 0, boxes = 0;
     for (int u = first_tile; u < num_tiles; u += tile_step) {
@@ -285,16 +320,16 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       const long long n = (long long)un.n_tile * kTcChannels + rank * 128 + threadIdx.x;
       const long long m0 = (long long)un.m_tile * p.block_t;
       const int tokens = (int)min((long long)p.block_t, p.M - m0);
-      __syncwarp();
-      for (int t = lane; t < p.block_t; t += 32) scale[t] = t < tokens ? p.scale_x[m0 + t] : 0.0f;
+      // the tile before has been read: its last box's barriers lie behind every warp
+      for (int t = threadIdx.x; t < p.block_t; t += 128)
+        sScale[t] = t < tokens ? p.scale_x[m0 + t] : 0.0f;
       ScaleBias sc{0.0f, 0.0f};
       if (n < p.N) {
         sc.w = __ldg(p.scale_w + n);
         if (p.bias) sc.bias = q8_load_value(p.bias, p.bias_type, n);
       }
-      __syncwarp();
       // the four warps go on or stop together: they share the staging buffers
-      const bool ok = wait_bounded_warp(acc_full(buf), phase, ab, kStatusWaitAccFull);
+      const bool ok = tc_wait(acc_full(buf), phase, ab, kStatusWaitAccFull);
       if (!named_barrier_and(1, 128, ok)) break;
       tc_fence_after();
       const uint32_t trow = tmem_base + (uint32_t)(buf * p.acc_stride) + ((uint32_t)(warp * 32) << 16);
@@ -316,11 +351,11 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         }
         release();
       } else if (p.y_type == Q8_F32) {
-        tc_epilogue<float>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
+        tc_epilogue<float>(p, &ymap, trow, sScale, sc, tokens, m0, n0, sBox, boxes, release);
       } else if (p.y_type == Q8_BF16) {
-        tc_epilogue<__nv_bfloat16>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
+        tc_epilogue<__nv_bfloat16>(p, &ymap, trow, sScale, sc, tokens, m0, n0, sBox, boxes, release);
       } else {
-        tc_epilogue<__half>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
+        tc_epilogue<__half>(p, &ymap, trow, sScale, sc, tokens, m0, n0, sBox, boxes, release);
       }
       if (++buf == p.acc_bufs) {
         buf = 0;
@@ -330,33 +365,18 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
     if (threadIdx.x == 0) bulk_wait_group_all();  // the stores have read their buffers
   } else if (warp < kTcTmaWarp) {
     // ---------------------------------------------------------------------------- converters
-    if (kInt8) {
-      const int quad = warp & 3, half = ((warp - 4) >> 2) & 1, turn = (warp - 4) >> 3;
+    if (kInt8 && warp < 4 + kTcWWarps) {
+      const int quad = warp & 3, half = ((warp - 4) >> 2) & 1;
+      const uint32_t turn = (uint32_t)(warp - 4) >> 3;  // this warp takes every other K block
       const int row = quad * 32 + lane;
-      const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-      const uint32_t slot_shift = p.a_slots == 8 ? 3 : 2;
-      Ring ring;
-      uint32_t it = 0;     // K blocks of all tiles so far; this warp takes those of its turn
-      int pending = -1;    // the slot whose store is under way
-      auto publish = [&]() {
-        if (pending < 0) return;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (slot_full(pending) - bars_u32));
-        pending = -1;
-      };
+      const uint32_t dst0 = slots_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(32 * half);
+      Ring ring, slots;
+      uint32_t it = 0;  // K blocks of all tiles so far
       bool aborted = false;
       for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next(S)) {
-          if ((it & 1u) != (uint32_t)turn) continue;
-          const uint32_t seq = 2 * it + half;  // halves of stages go through the slots in order
-          const int slot = (int)(seq & (uint32_t)(p.a_slots - 1));
-          const uint32_t slot_phase = (seq >> slot_shift) & 1u;
-          // the store before is published behind this stage's loads, which give it the time to
-          // finish, unless those would have to wait
-          if (!__all_sync(0xFFFFFFFFu, mbar_test(w_full(ring.stage), ring.phase))) publish();
-          if (!wait_bounded_warp(w_full(ring.stage), ring.phase, ab, kStatusWaitFull)) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next(S), slots.next(p.w_slots)) {
+          if ((it & 1u) != turn) continue;
+          if (!tc_wait(full(ring.stage), ring.phase, ab, kStatusWaitFull)) {
             aborted = true;
             break;
           }
@@ -365,20 +385,93 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // 16-byte chunk i of this half, where the swizzle put it
             c[i] = *reinterpret_cast<const uint4*>(src + (((4 * half + i) ^ (row & 7)) << 4));
-          publish();
           uint32_t h[32];
 #pragma unroll
           for (int i = 0; i < 4; ++i) int8_to_f16(c[i], h + 8 * i);
-          if (!wait_bounded_warp(slot_empty(slot), slot_phase ^ 1u, ab, kStatusWaitEmpty)) {
+          __syncwarp();  // every lane has its codes
+          if (lane == 0) mbar_arrive(empty(ring.stage));
+          const uint32_t before = it - (uint32_t)p.w_slots;  // the K block that had this slot
+          if (it >= (uint32_t)p.w_slots &&
+              !tc_wait(done(before), parity(before), ab, kStatusWaitEmpty)) {
             aborted = true;
             break;
           }
           tc_fence_after();
-          tmem_st_32x32b_x32(slots_base + lane_base + (uint32_t)(slot * kTcSlotCols), h);
-          pending = slot;
+          tmem_st_32x32b_x32(dst0 + (uint32_t)(slots.stage * kTcSlotCols), h);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0)
+            mbar_arrive_cluster_tmem(leader_bars + (ready(it) - bars_u32));
         }
       }
-      publish();
+    } else if (kInt8 && x_codes) {
+      // x: 16 codes at a time, a row's eight chunks by eight consecutive threads
+      const int thread = threadIdx.x - (4 + kTcWWarps) * 32, chunks = p.block_t / 2 * 8;
+      Ring ring, slots;
+      uint32_t it = 0;
+      bool aborted = false;
+      for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t before = it - (uint32_t)p.x_slots;
+          if (!tc_wait(full(ring.stage), ring.phase, ab, kStatusWaitFull) ||
+              (it >= (uint32_t)p.x_slots &&
+               !tc_wait(done(before), parity(before), ab, kStatusWaitEmpty))) {
+            aborted = true;
+            break;
+          }
+          const uint8_t* src = sX + (size_t)ring.stage * x_bytes;
+          uint8_t* dst = sXh + (size_t)slots.stage * 2 * x_bytes;
+#pragma unroll 4
+          for (int i = thread; i < chunks; i += 32 * kTcXWarps) {
+            const int row = i >> 3, chunk = i & 7, swz = row & 7;
+            const uint4 c =
+                *reinterpret_cast<const uint4*>(src + row * kTcBlockK + ((chunk ^ swz) << 4));
+            uint32_t h[8];
+            int8_to_f16(c, h);
+            // the 16 codes are two 16-byte pieces of a 128-byte row of the half they lie in; the
+            // two halves' threads write theirs in opposite order, on different banks
+            uint8_t* to = dst + (chunk >> 2) * x_bytes + row * 128;
+            const int piece = 2 * (chunk & 3), flip = chunk >> 2;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(to + (((piece + flip) ^ swz) << 4)) = flip ? hi : lo;
+            *reinterpret_cast<uint4*>(to + (((piece + 1 - flip) ^ swz) << 4)) = flip ? lo : hi;
+          }
+          fence_proxy_async_smem();  // the MMA reads them through the async proxy
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(empty(ring.stage));
+            mbar_arrive_cluster_tmem(leader_bars + (ready(it) - bars_u32));
+          }
+          ring.next(S);
+          slots.next(p.x_slots);
+        }
+      }
+    } else if (kInt8 && warp == 4 + kTcWWarps) {
+      // x as f16, for the MMAs of the pair
+      Ring slots;
+      uint32_t it = 0;
+      bool aborted = false;
+      for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
+        const int m0 = tc_tile(p, u).m_tile * p.block_t + (int)rank * (p.block_t / 2);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t before = it - (uint32_t)p.x_slots;
+          if (it >= (uint32_t)p.x_slots &&
+              !tc_wait(done(before), parity(before), ab, kStatusWaitEmpty)) {
+            aborted = true;
+            break;
+          }
+          if (elect_one()) {
+            const uint32_t bar = leader_bars + (ready(it) - bars_u32);
+            const uint32_t dst = smem_u32(sXh) + (uint32_t)slots.stage * 2 * x_bytes;
+            if (leader) mbar_arrive_expect_tx(ready(it), 4 * x_bytes);
+            tma_load_2d_pair(dst, &xmap, bar, kb * kTcBlockK, m0);
+            tma_load_2d_pair(dst + x_bytes, &xmap, bar, kb * kTcBlockK + 64, m0);
+          }
+          __syncwarp();
+          slots.next(p.x_slots);
+        }
+      }
     }
   } else if (warp == kTcTmaWarp) {
     // ------------------------------------------------------------------------------ TMA loader
@@ -392,7 +485,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       const int m0 = un.m_tile * p.block_t + (int)rank * half_t;
       for (int kb = kb0; kb < kb1; ++kb) {
         const int s = ring.stage;
-        if (!wait_bounded_warp(empty(s), ring.phase ^ 1u, ab, kStatusWaitEmpty)) {
+        if (!tc_wait(empty(s), ring.phase ^ 1u, ab, kStatusWaitEmpty)) {
           aborted = true;
           break;
         }
@@ -401,12 +494,10 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
           const uint32_t w_dst = smem_u32(sW) + (uint32_t)s * kTcWBytes;
           const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * x_bytes;
           const int k0 = kb * kTcBlockK;
-          if (kInt8) {
-            mbar_arrive_expect_tx(w_full(s), kTcWBytes);
-            tma_load_2d(w_dst, &wmap, w_full(s), k0, n0);
-            if (leader) mbar_arrive_expect_tx(full(s), 2 * x_bytes);
-            tma_load_2d_pair(x_dst, &xmap, bar, k0, m0);
-            tma_load_2d_pair(x_dst + x_bytes / 2, &xmap, bar, k0 + kTcBlockK / 2, m0);
+          if (kInt8) {  // each CTA's converters wait for its own copies
+            mbar_arrive_expect_tx(full(s), kTcWBytes + (x_codes ? x_bytes : 0));
+            tma_load_2d(w_dst, &wmap, full(s), k0, n0);
+            if (x_codes) tma_load_2d(x_dst, &xmap, full(s), k0, m0);
           } else {
             if (leader) mbar_arrive_expect_tx(full(s), 2 * (kTcWBytes + x_bytes));
             tma_load_2d_pair(w_dst, &wmap, bar, k0, n0);
@@ -423,65 +514,69 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
     const uint32_t idesc = kInt8 ? make_idesc_f16_f32(kTcChannels, (uint32_t)p.block_t)
                                  : make_idesc_e4m3_f32(kTcChannels, (uint32_t)p.block_t);
     const uint64_t wdesc0 = make_sw128_kmajor_desc(smem_u32(sW));
-    const uint64_t xdesc0 = make_sw128_kmajor_desc(smem_u32(sX));
-    Ring ring, slots;
+    const uint64_t xdesc0 = make_sw128_kmajor_desc(smem_u32(kInt8 ? sXh : sX));
+    Ring ring, wslots;  // the stages (e4m3) or x's slots (int8), w's slots
+    const int ring_size = kInt8 ? p.x_slots : S;
+    uint32_t it = 0;
     int buf = 0;
     uint32_t phase = 0;
     bool aborted = false;
     for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
-      const TcTile un = tc_tile(p, u);
-      if (!wait_bounded_warp(acc_empty(buf), phase ^ 1u, ab, kStatusWaitAccEmpty)) break;
+      if (!tc_wait(acc_empty(buf), phase ^ 1u, ab, kStatusWaitAccEmpty)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(buf * p.acc_stride);
       for (int kb = kb0; kb < kb1; ++kb) {
         const int s = ring.stage;
-        if (!wait_bounded_warp(full(s), ring.phase, ab, kStatusWaitFull)) {
+        if (!tc_wait(kInt8 ? ready(it) : full(s), kInt8 ? parity(it) : ring.phase, ab,
+                     kStatusWaitFull)) {
           aborted = true;
           break;
         }
-        const uint32_t acc0 = kb > kb0 ? 1u : 0u;
-        const int rem = p.K - kb * kTcBlockK;  // codes past K are zeros, and mostly left out
-        const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 4));
-        if (kInt8) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!wait_bounded_warp(slot_full(slots.stage), slots.phase, ab,
-                                         kStatusWaitFull)) {
-              aborted = true;
-              break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t acc0 = kb > kb0 ? 1u : 0u;
+          const int rem = p.K - kb * kTcBlockK;  // codes past K are zeros, and mostly left out
+          if (kInt8) {
+            const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 3));
+            const uint64_t xdesc1 = xdesc + (x_bytes >> 4);  // the second 64 codes
+            const uint32_t a = slots_base + (uint32_t)(wslots.stage * kTcSlotCols);
+            if (rem >= kTcBlockK) {
+              mma_f16_pair_tmem_a(d, a, xdesc, idesc, acc0);
+              mma_f16_pair_tmem_a(d, a + 8, xdesc + 2, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 16, xdesc + 4, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 24, xdesc + 6, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 32, xdesc1, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 40, xdesc1 + 2, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 48, xdesc1 + 4, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 56, xdesc1 + 6, idesc, 1u);
+            } else {
+              for (int j = 0; 16 * j < rem; ++j)
+                mma_f16_pair_tmem_a(d, a + 8 * j, (j < 4 ? xdesc : xdesc1) + 2 * (j & 3), idesc,
+                                    j > 0 ? 1u : acc0);
             }
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t a = slots_base + (uint32_t)(slots.stage * kTcSlotCols);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (kTcSlotK * half + 16 * j < rem)
-                  mma_f16_pair_tmem_a(d, a + 8 * j, xdesc + half * (x_bytes >> 5) + 2 * j, idesc,
-                                      half + j > 0 ? 1u : acc0);
-              mma_commit_pair(slot_empty(slots.stage), pair_mask);
-              if (half == 1) {
-                mma_commit_pair(empty(s), pair_mask);
-                if (kb + 1 == kb1) mma_commit_pair(acc_full(buf), pair_mask);
-              }
-            }
-            __syncwarp();
-            slots.next(p.a_slots);
-          }
-          if (aborted) break;
-        } else {
-          tc_fence_after();
-          if (elect_one()) {
+            mma_commit_pair(done(it), pair_mask);
+          } else {
+            const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 4));
             const uint64_t wdesc = wdesc0 + (uint64_t)((uint32_t)s * (kTcWBytes >> 4));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (32 * j < rem)
+            if (rem >= kTcBlockK) {
+              mma_f8f6f4_pair(d, wdesc, xdesc, idesc, acc0);
+              mma_f8f6f4_pair(d, wdesc + 2, xdesc + 2, idesc, 1u);
+              mma_f8f6f4_pair(d, wdesc + 4, xdesc + 4, idesc, 1u);
+              mma_f8f6f4_pair(d, wdesc + 6, xdesc + 6, idesc, 1u);
+            } else {
+              for (int j = 0; 32 * j < rem; ++j)
                 mma_f8f6f4_pair(d, wdesc + 2 * j, xdesc + 2 * j, idesc, j > 0 ? 1u : acc0);
+            }
             mma_commit_pair(empty(s), pair_mask);
-            if (kb + 1 == kb1) mma_commit_pair(acc_full(buf), pair_mask);
           }
-          __syncwarp();
+          if (kb + 1 == kb1) mma_commit_pair(acc_full(buf), pair_mask);
         }
-        ring.next(S);
+        __syncwarp();
+        ring.next(ring_size);
+        if (kInt8) {
+          wslots.next(p.w_slots);
+          ++it;
+        }
       }
       if (++buf == p.acc_bufs) {
         buf = 0;
@@ -507,11 +602,12 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   if (warp == kTcMmaWarp) tmem_dealloc_pair(tmem_base, kTcTmemCols);
 }
 
-// x's int8 codes as f16, 16 a thread and step.
+// x's int8 codes as f16, 16 a thread and step. The codes between K and the pitch's 16 are not read
+// later: the f16 matrix's map ends at K.
 __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int per_row = (p.K + 15) / 16;  // the codes past K, inside the pitch, are not read later
+  const int per_row = (p.K + 15) / 16;
   const long long total = (long long)p.M * per_row;
   for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
     const long long m = i / per_row;
@@ -523,6 +619,9 @@ __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p
     dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
   }
 }
+
+// Whether TMEM holds two accumulators of t tokens, beside two slots of w.
+static bool two_accumulators(bool int8, int t) { return !int8 || t <= 192; }
 
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
   const bool int8 = code_type == Q8_INT8;
@@ -547,9 +646,8 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
       const double ctas = 2.0 * splits * (double)std::min(tiles, held);
       const double arrive = kTcWBytes / std::min(40.0, 3570.0 / ctas);
       const double kb = std::max((int8 ? 4.0 : 2.0) * t, arrive);
-      const bool two = !int8 || t <= 192;
       const double unit =
-          (double)((p.k_blocks + splits - 1) / splits) * kb + (two ? 0.0 : 8.0 * t);
+          (double)((p.k_blocks + splits - 1) / splits) * kb + (two_accumulators(int8, t) ? 0.0 : 8.0 * t);
       const double cost = (double)waves * unit + (splits > 1 ? 20.0 * t + 2500.0 : 8.0 * t);
       if (cost < best) {
         best = cost;
@@ -559,26 +657,29 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
       }
     }
   }
-  if (!int8) {
-    p.acc_bufs = 2;
-    p.acc_stride = kTcMaxTokens;
-    p.a_slots = 1;
-  } else {
-    p.acc_bufs = p.block_t <= 192 ? 2 : 1;
-    p.acc_stride = p.block_t <= 128 ? 128 : (p.block_t <= 192 ? 192 : 256);
-    p.a_slots = (kTcTmemCols - p.acc_bufs * p.acc_stride) / kTcSlotCols;  // 8 or 4
+  const int x_bytes = (int)tc_x_bytes(p.block_t);
+  p.acc_bufs = two_accumulators(int8, p.block_t) ? 2 : 1;
+  p.acc_stride = (p.block_t + 31) / 32 * 32;
+  p.x_expanded = int8 && p.M > kTcXInside;
+  p.w_slots = p.x_slots = 0;
+  if (int8) {
+    p.w_slots = std::min(kTcDepth, (kTcTmemCols - p.acc_bufs * p.acc_stride) / kTcSlotCols);
+    // x's copies take longer than w's way through TMEM, so x gets most of shared memory if it comes as
+    // f16, and half of it otherwise
+    p.x_slots = std::min(kTcDepth, kTcSmemBudget * (p.x_expanded ? 5 : 4) / 8 / (2 * x_bytes));
   }
-  const int stage = kTcWBytes + (int)tc_x_bytes(p.block_t, int8);
-  p.stages = std::min(kTcMaxStages, kTcSmemBudget / stage);
+  p.stages = std::min(kTcMaxStages, (kTcSmemBudget - p.x_slots * 2 * x_bytes) /
+                                        (kTcWBytes + (p.x_expanded ? 0 : x_bytes)));
 }
 
-size_t linear_tc_smem_bytes(const LinearParams& p, int code_type) {
-  return 1024 + (size_t)p.stages * (kTcWBytes + tc_x_bytes(p.block_t, code_type == Q8_INT8)) +
-         2 * kTcBoxBytes + 4 * kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
+size_t linear_tc_smem_bytes(const LinearParams& p) {
+  const size_t x_bytes = tc_x_bytes(p.block_t);
+  return 1024 + p.stages * (kTcWBytes + (p.x_expanded ? 0 : x_bytes)) + p.x_slots * 2 * x_bytes +
+         2 * kTcBoxBytes + kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
 }
 
 constexpr int kTcMostSmem =
-    1024 + kTcSmemBudget + 2 * kTcBoxBytes + 4 * kTcMaxTokens * 4 + kTcBars * 8 + 16;
+    1024 + kTcSmemBudget + 2 * kTcBoxBytes + kTcMaxTokens * 4 + kTcBars * 8 + 16;
 
 cudaError_t linear_tc_setup() {
   cudaError_t e = cudaFuncSetAttribute(linear_q8_tc_kernel<true>,
@@ -642,7 +743,7 @@ cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtenso
   const long long tiles = (long long)p.m_tiles * p.n_tiles;
   const int cluster = 2 * p.splits;
   const int grid = cluster * (int)std::min<long long>(tiles, std::max(1, lim.clusters[p.splits / 2]));
-  const size_t smem = linear_tc_smem_bytes(p, code_type);
+  const size_t smem = linear_tc_smem_bytes(p);
   if (code_type == Q8_INT8)
     return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads<true>, cluster, smem, stream, wmap, xmap,
                       ymap, p);
