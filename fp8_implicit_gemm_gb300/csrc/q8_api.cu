@@ -15,7 +15,7 @@ struct linear_q8_plan_s {
   int few = kFewTokens;            // tokens up to which the kernel for few tokens runs
   unsigned long long timeout_ns = 0;
   int debug_flags = 0;
-  uint8_t* workspace = nullptr;    // status word; x as f16 (int8, many tokens)
+  uint8_t* workspace = nullptr;    // status word; x as f16 (int8)
   size_t workspace_bytes = 0;
 };
 
@@ -225,7 +225,7 @@ extern "C" conv3d_status linear_q8_plan_ex(linear_q8_plan_t* plan, long long max
   linear_q8_options o{};
   if (opts) o = *opts;
   if (o.kernel < 0 || o.kernel > 2 || o.block_t < 0 || o.block_t > kTcMaxTokens ||
-      o.block_t % 32 != 0 || (o.splits != 0 && o.splits != 1 && o.splits != 2 && o.splits != 4) ||
+      o.block_t % 32 != 0 || o.splits < 0 || o.splits > kTcMaxSplits ||
       o.max_ctas < 0 || o.wait_timeout_ms < 0)
     return CONV3D_EINVAL;
   if (max_rows >= (1LL << 30) || N >= (1LL << 30) || K >= (1LL << 30)) return CONV3D_EUNSUPPORTED;
@@ -248,14 +248,13 @@ extern "C" conv3d_status linear_q8_plan_ex(linear_q8_plan_t* plan, long long max
       delete pl;
       return CONV3D_ECUDA;
     }
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < kTcMaxSplits; ++i)
       if (o.max_ctas > 0)
-        pl->lim.clusters[i] = std::min(pl->lim.clusters[i], o.max_ctas / (2 << i));
-    // a forced tile no larger than the tokens need, forced slices no more than K has blocks
+        pl->lim.clusters[i] = std::min(pl->lim.clusters[i], o.max_ctas / (2 * (i + 1)));
     pl->lim.block_t = o.block_t;
     pl->lim.splits = o.splits;
     pl->workspace_bytes = kStatusBytes;
-    if (code_type == Q8_INT8 && max_rows > kTcXInside)
+    if (code_type == Q8_INT8)
       pl->workspace_bytes += (size_t)(max_rows * round_up(K, 16) * 2);
     if (cudaMalloc(&pl->workspace, pl->workspace_bytes) != cudaSuccess) {
       cudaGetLastError();
@@ -326,13 +325,14 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
   p.debug_flags = plan->debug_flags;
   const long long y_pitch = p.M > 1 ? p.y_pitch : round_up(p.N, 8);
   p.y_tma = aligned(p.y, 16) && y_pitch * value_bytes(p.y_type) % 16 == 0;
+  const bool int8 = plan->code_type == Q8_INT8;
   CUtensorMap wmap{}, xmap{}, ymap{};
   if (!encode_rows(&wmap, p.w, 1, p.N, p.K, p.w_pitch, kTcWBoxRows) ||
-      !(p.x_expanded ? encode_rows(&xmap, p.xh, 2, p.M, p.K, p.xh_pitch, p.block_t / 2)
+      !(int8 ? encode_rows(&xmap, p.xh, 2, p.M, p.K, p.xh_pitch, p.block_t / 2)
                      : encode_rows(&xmap, p.x, 1, p.M, p.K, p.x_pitch, p.block_t / 2)) ||
       (p.y_tma && !encode_y(&ymap, p.y, p.y_type, p.M, p.N, y_pitch)))
     return CONV3D_ECUDA;
-  if (p.x_expanded) {
+  if (int8) {
     const conv3d_status st = launched(launch_linear_expand(p, stream));
     if (st != CONV3D_OK) return st;
   }

@@ -46,11 +46,10 @@ struct LinearParams {
   // the tensor-core kernel's tiling (linear_tc_decide) and workspace
   int block_t;           // tokens of a tile (a tile has kTcChannels channels)
   int m_tiles, n_tiles, k_blocks;
-  int splits;            // slices of K, one for each pair of a cluster: 1, 2 or 4
-  int stages, acc_bufs, acc_stride;
-  // int8 only: K blocks of w in TMEM and of x in shared memory as f16, whether x comes as f16
-  int w_slots, x_slots, x_expanded;
-  uint16_t* xh;          // x as f16, [M][xh_pitch], where it is expanded
+  int splits;            // slices of K, one for each pair of a cluster: 1 to kTcMaxSplits
+  int stages;
+  int w_slots, x_slots;  // int8 only: K blocks of w in TMEM and of x in shared memory as f16
+  uint16_t* xh;          // int8 only: x as f16, [M][xh_pitch]
   long long xh_pitch;
   int* status;
   unsigned long long timeout_ns;
@@ -65,9 +64,10 @@ cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t
 constexpr int kTcChannels = 256;
 constexpr int kTcBlockK = 128;         // codes of K a pipeline stage holds
 constexpr int kTcMaxTokens = 256;
+constexpr int kTcMaxSplits = 4;
 // What a plan's device and options allow.
 struct TcLimits {
-  int clusters[3];       // clusters of 2, 4 and 8 CTAs held at once
+  int clusters[kTcMaxSplits];  // clusters of 2, 4, 6 and 8 CTAs held at once
   int block_t, splits;   // 0: the choice of linear_tc_decide
 };
 // Fills in the tiling of a product of M, N and K.
@@ -76,11 +76,9 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim);
 constexpr int kTcWBoxRows = 128;
 // The box of y's map: 128 channels of 8 KB's worth of tokens.
 constexpr int kTcYBoxBytes = 8192;
-// Tokens up to which the kernel turns int8 codes of x into f16 by itself.
-constexpr int kTcXInside = 256;
 cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream);  // x -> xh
 cudaError_t linear_tc_setup();         // the kernels' shared-memory grant
-cudaError_t linear_tc_max_clusters(int (&clusters)[3]);
+cudaError_t linear_tc_max_clusters(int (&clusters)[kTcMaxSplits]);
 cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtensorMap& wmap,
                              const CUtensorMap& xmap, const CUtensorMap& ymap, const TcLimits& lim,
                              cudaStream_t stream);

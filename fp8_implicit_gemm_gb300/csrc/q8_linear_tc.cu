@@ -16,20 +16,22 @@
 //     with the sign bit flipped, a permute and a subtraction for each two codes) and write them to
 //     TMEM, from where the MMA takes its A operand: in shared memory they would come on top of the
 //     codes, x and the MMA's reads, which fill its 128 bytes a cycle at 256 tokens;
-//   - x is expanded to f16 by a small kernel first and loaded as such, 3 bytes of traffic a code, or,
-//     for few tokens, turned by four more warps of this kernel, which saves the launch;
+//   - x is expanded to f16 by a small kernel first, 3 bytes of traffic a code, and loaded as such.
+//     Turned by four or eight more warps of this kernel it is read back into shared memory next to
+//     everything else: 256 x 6144 x 4096 takes 26 us so and 22 with the expansion, 64 x 8192 x 4096
+//     15.3 and 14.4, 8192 x 4096 x 8192 408 and 328;
 //   - a K block has one barrier that says that its w and x are there and one commit that frees both,
 //     whatever the depths of their rings: the issuing warp takes about 160 cycles for a wait, 60 for
 //     a commit and 30 for an MMA, and a K block's MMAs take 512 at 128 tokens. With a wait and a
 //     commit for each quarter of a K block it took 2500 cycles.
 //
-// Few tiles: a tile is split along K over the pairs of one cluster (4 or 8 CTAs). Each CTA leaves its
+// Few tiles: a tile is split along K over the pairs of one cluster (4, 6 or 8 CTAs). Each CTA leaves its
 // partial sums in its own shared memory and adds up its share of the tokens from all of them over
 // distributed shared memory, in the order of the slices: nothing passes through global memory, and
 // a result does not depend on which slice is ready first.
 //
-// Roles of a CTA: warps 0-3 epilogue, then 16 converters of w and 4 of x (int8), TMA and MMA (the
-// leader CTA's).
+// Roles of a CTA: warps 0-3 epilogue, then 16 converters of w and the copies of x (int8), the other
+// copies, and the MMAs (the leader CTA's).
 // Every wait is bounded; one that runs out records a status bit and both CTAs wind down.
 #include <algorithm>
 
@@ -38,9 +40,10 @@
 
 namespace c3d {
 
-constexpr int kTcWWarps = 16, kTcXWarps = 4;        // converters
+constexpr int kTcWWarps = 16;                       // converters (int8)
+constexpr int kTcXWarp = 4 + kTcWWarps;             // x's copies (int8)
 template <bool kInt8>
-constexpr int kTcTmaWarpOf = 4 + (kInt8 ? kTcWWarps + kTcXWarps : 0);
+constexpr int kTcTmaWarpOf = kInt8 ? kTcXWarp + 1 : 4;
 template <bool kInt8>
 constexpr int kTcThreads = (kTcTmaWarpOf<kInt8> + 2) * 32;
 constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // w's codes of one stage: 16 KB a CTA
@@ -136,7 +139,7 @@ __device__ __forceinline__ void tc_join(const LinearParams& p, const TcTile& t, 
   const long long n = (long long)t.n_tile * kTcChannels + rank * 128 + 4 * lane;
   const long long m0 = (long long)t.m_tile * p.block_t;
   const int tokens = (int)min((long long)p.block_t, p.M - m0);
-  const int share = p.block_t / p.splits;
+  const int share = (p.block_t + p.splits - 1) / p.splits;
   if (n >= p.N) return;
   const int have = (int)min(4LL, p.N - n);
   ScaleBias sc[4];
@@ -148,12 +151,12 @@ __device__ __forceinline__ void tc_join(const LinearParams& p, const TcTile& t, 
   const int end = min(tokens, (split + 1) * share);
   for (int c = split * share + (threadIdx.x >> 5); c < end; c += blockDim.x / 32) {
     const uint32_t at = part + (uint32_t)(c * 128 + 4 * lane) * 4u;
-    float4 a[4];
+    float4 a[kTcMaxSplits];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < kTcMaxSplits; ++s)
       if (s < p.splits) a[s] = ld_cluster_f4(map_to_cta(at, 2u * s + rank));
 #pragma unroll
-    for (int s = 1; s < 4; ++s)
+    for (int s = 1; s < kTcMaxSplits; ++s)
       if (s < p.splits) {
         a[0].x += a[s].x;
         a[0].y += a[s].y;
@@ -201,9 +204,14 @@ __device__ __forceinline__ void tc_epilogue(const LinearParams& p, const CUtenso
       if (threadIdx.x == 0) bulk_wait_group_read<1>();  // the store from this buffer, two boxes ago
       named_barrier_sync(1, 128);
 #pragma unroll
-      for (int j = 0; j < kRows; ++j)
-        reinterpret_cast<Y*>(buf)[j * 128 + threadIdx.x] =
-            q8_from_float<Y>(sc(__uint_as_float(r[h + j]), scale[c + h + j]));
+      for (int j = 0; j < kRows; j += 4) {
+        const float4 sx = *reinterpret_cast<const float4*>(scale + c + h + j);
+        Y* to = reinterpret_cast<Y*>(buf) + j * 128 + threadIdx.x;
+        to[0] = q8_from_float<Y>(sc(__uint_as_float(r[h + j]), sx.x));
+        to[128] = q8_from_float<Y>(sc(__uint_as_float(r[h + j + 1]), sx.y));
+        to[256] = q8_from_float<Y>(sc(__uint_as_float(r[h + j + 2]), sx.z));
+        to[384] = q8_from_float<Y>(sc(__uint_as_float(r[h + j + 3]), sx.w));
+      }
       if (by_tma) fence_proxy_async_smem();
       named_barrier_sync(1, 128);
       if (threadIdx.x == 0) {
@@ -235,12 +243,10 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
   const int S = p.stages;
   const uint32_t x_bytes = tc_x_bytes(p.block_t);
-  // int8 with x expanded: x's tiles arrive as f16 and a stage holds w's codes alone
-  const bool x_codes = !kInt8 || !p.x_expanded;
   uint8_t* sW = smem;
   uint8_t* sX = smem + (size_t)S * kTcWBytes;
-  uint8_t* sXh = sX + (x_codes ? (size_t)S * x_bytes : 0);  // x as f16, two 64-code halves a slot
-  uint8_t* sBox = sXh + (kInt8 ? (size_t)p.x_slots * 2 * x_bytes : 0);  // the epilogue's staging
+  // x's tiles: codes in the stages (e4m3), or f16 in slots of their own, two 64-code halves each
+  uint8_t* sBox = sX + (size_t)(kInt8 ? 2 * p.x_slots : S) * x_bytes;  // the epilogue's staging
   float* sScale = reinterpret_cast<float*>(sBox + 2 * kTcBoxBytes);  // [kTcMaxTokens]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kTcMaxTokens);
   // Barriers (those marked L: the leader's are used). full[S]: a stage's copies have landed (e4m3 L:
@@ -277,11 +283,11 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 1);
       // an arrival of each converter warp whose turn it is, or a commit's
-      mbar_init(empty(s), kInt8 ? kTcWWarps / 2 + (x_codes ? kTcXWarps : 0) : 1);
+      mbar_init(empty(s), kInt8 ? kTcWWarps / 2 : 1);
     }
     for (uint32_t i = 0; i < kTcDepth; ++i) {
-      // of both CTAs: the warps of w's two halves, and those of x or the copies of x
-      mbar_init(ready(i), 2 * (kTcWWarps / 2) + (x_codes ? 2 * kTcXWarps : 1));
+      // of both CTAs: the warps of w's two halves, and the copies of x
+      mbar_init(ready(i), 2 * (kTcWWarps / 2) + 1);
       mbar_init(done(i), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -306,15 +312,15 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   cluster_sync();  // both CTAs' barriers exist before anyone signals across the pair
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t slots_base = tmem_base + (uint32_t)(p.acc_bufs * p.acc_stride);
+  const uint32_t slots_base = tmem_base + (uint32_t)(2 * p.block_t);
   pdl_wait_primary();
   pdl_launch_dependents();
   const AbortState ab{abort_flag, p.status, p.timeout_ns};
 
   if (warp < 4) {
     // ------------------------------------------------------------------------------ epilogue
-    int buf = 0;
-    uint32_t phase = 0, boxes = 0;
+    Ring acc;
+    uint32_t boxes = 0;
     for (int u = first_tile; u < num_tiles; u += tile_step) {
       const TcTile un = tc_tile(p, u);
       const long long n = (long long)un.n_tile * kTcChannels + rank * 128 + threadIdx.x;
@@ -329,14 +335,15 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         if (p.bias) sc.bias = q8_load_value(p.bias, p.bias_type, n);
       }
       // the four warps go on or stop together: they share the staging buffers
-      const bool ok = tc_wait(acc_full(buf), phase, ab, kStatusWaitAccFull);
+      const bool ok = tc_wait(acc_full(acc.stage), acc.phase, ab, kStatusWaitAccFull);
       if (!named_barrier_and(1, 128, ok)) break;
       tc_fence_after();
-      const uint32_t trow = tmem_base + (uint32_t)(buf * p.acc_stride) + ((uint32_t)(warp * 32) << 16);
+      const uint32_t trow = tmem_base + (uint32_t)(acc.stage * p.block_t) + ((uint32_t)(warp * 32) << 16);
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (acc_empty(buf) - bars_u32));
+        if (lane == 0)
+          mbar_arrive_cluster_tmem(leader_bars + (acc_empty(acc.stage) - bars_u32));
       };
       const int n0 = un.n_tile * kTcChannels + (int)rank * 128;
       if (p.splits > 1) {
@@ -357,15 +364,12 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       } else {
         tc_epilogue<__half>(p, &ymap, trow, sScale, sc, tokens, m0, n0, sBox, boxes, release);
       }
-      if (++buf == p.acc_bufs) {
-        buf = 0;
-        phase ^= 1u;
-      }
+      acc.next(2);
     }
     if (threadIdx.x == 0) bulk_wait_group_all();  // the stores have read their buffers
   } else if (warp < kTcTmaWarp) {
     // ---------------------------------------------------------------------------- converters
-    if (kInt8 && warp < 4 + kTcWWarps) {
+    if (kInt8 && warp < kTcXWarp) {
       const int quad = warp & 3, half = ((warp - 4) >> 2) & 1;
       const uint32_t turn = (uint32_t)(warp - 4) >> 3;  // this warp takes every other K block
       const int row = quad * 32 + lane;
@@ -405,49 +409,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
             mbar_arrive_cluster_tmem(leader_bars + (ready(it) - bars_u32));
         }
       }
-    } else if (kInt8 && x_codes) {
-      // x: 16 codes at a time, a row's eight chunks by eight consecutive threads
-      const int thread = threadIdx.x - (4 + kTcWWarps) * 32, chunks = p.block_t / 2 * 8;
-      Ring ring, slots;
-      uint32_t it = 0;
-      bool aborted = false;
-      for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const uint32_t before = it - (uint32_t)p.x_slots;
-          if (!tc_wait(full(ring.stage), ring.phase, ab, kStatusWaitFull) ||
-              (it >= (uint32_t)p.x_slots &&
-               !tc_wait(done(before), parity(before), ab, kStatusWaitEmpty))) {
-            aborted = true;
-            break;
-          }
-          const uint8_t* src = sX + (size_t)ring.stage * x_bytes;
-          uint8_t* dst = sXh + (size_t)slots.stage * 2 * x_bytes;
-#pragma unroll 4
-          for (int i = thread; i < chunks; i += 32 * kTcXWarps) {
-            const int row = i >> 3, chunk = i & 7, swz = row & 7;
-            const uint4 c =
-                *reinterpret_cast<const uint4*>(src + row * kTcBlockK + ((chunk ^ swz) << 4));
-            uint32_t h[8];
-            int8_to_f16(c, h);
-            // the 16 codes are two 16-byte pieces of a 128-byte row of the half they lie in; the
-            // two halves' threads write theirs in opposite order, on different banks
-            uint8_t* to = dst + (chunk >> 2) * x_bytes + row * 128;
-            const int piece = 2 * (chunk & 3), flip = chunk >> 2;
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4*>(to + (((piece + flip) ^ swz) << 4)) = flip ? hi : lo;
-            *reinterpret_cast<uint4*>(to + (((piece + 1 - flip) ^ swz) << 4)) = flip ? lo : hi;
-          }
-          fence_proxy_async_smem();  // the MMA reads them through the async proxy
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(empty(ring.stage));
-            mbar_arrive_cluster_tmem(leader_bars + (ready(it) - bars_u32));
-          }
-          ring.next(S);
-          slots.next(p.x_slots);
-        }
-      }
-    } else if (kInt8 && warp == 4 + kTcWWarps) {
+    } else if (kInt8) {
       // x as f16, for the MMAs of the pair
       Ring slots;
       uint32_t it = 0;
@@ -463,7 +425,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
           }
           if (elect_one()) {
             const uint32_t bar = leader_bars + (ready(it) - bars_u32);
-            const uint32_t dst = smem_u32(sXh) + (uint32_t)slots.stage * 2 * x_bytes;
+            const uint32_t dst = smem_u32(sX) + (uint32_t)slots.stage * 2 * x_bytes;
             if (leader) mbar_arrive_expect_tx(ready(it), 4 * x_bytes);
             tma_load_2d_pair(dst, &xmap, bar, kb * kTcBlockK, m0);
             tma_load_2d_pair(dst + x_bytes, &xmap, bar, kb * kTcBlockK + 64, m0);
@@ -495,9 +457,8 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
           const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * x_bytes;
           const int k0 = kb * kTcBlockK;
           if (kInt8) {  // each CTA's converters wait for its own copies
-            mbar_arrive_expect_tx(full(s), kTcWBytes + (x_codes ? x_bytes : 0));
+            mbar_arrive_expect_tx(full(s), kTcWBytes);
             tma_load_2d(w_dst, &wmap, full(s), k0, n0);
-            if (x_codes) tma_load_2d(x_dst, &xmap, full(s), k0, m0);
           } else {
             if (leader) mbar_arrive_expect_tx(full(s), 2 * (kTcWBytes + x_bytes));
             tma_load_2d_pair(w_dst, &wmap, bar, k0, n0);
@@ -514,17 +475,16 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
     const uint32_t idesc = kInt8 ? make_idesc_f16_f32(kTcChannels, (uint32_t)p.block_t)
                                  : make_idesc_e4m3_f32(kTcChannels, (uint32_t)p.block_t);
     const uint64_t wdesc0 = make_sw128_kmajor_desc(smem_u32(sW));
-    const uint64_t xdesc0 = make_sw128_kmajor_desc(smem_u32(kInt8 ? sXh : sX));
+    const uint64_t xdesc0 = make_sw128_kmajor_desc(smem_u32(sX));
     Ring ring, wslots;  // the stages (e4m3) or x's slots (int8), w's slots
     const int ring_size = kInt8 ? p.x_slots : S;
     uint32_t it = 0;
-    int buf = 0;
-    uint32_t phase = 0;
+    Ring acc;
     bool aborted = false;
     for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
-      if (!tc_wait(acc_empty(buf), phase ^ 1u, ab, kStatusWaitAccEmpty)) break;
+      if (!tc_wait(acc_empty(acc.stage), acc.phase ^ 1u, ab, kStatusWaitAccEmpty)) break;
       tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)(buf * p.acc_stride);
+      const uint32_t d = tmem_base + (uint32_t)(acc.stage * p.block_t);
       for (int kb = kb0; kb < kb1; ++kb) {
         const int s = ring.stage;
         if (!tc_wait(kInt8 ? ready(it) : full(s), kInt8 ? parity(it) : ring.phase, ab,
@@ -569,7 +529,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
             }
             mma_commit_pair(empty(s), pair_mask);
           }
-          if (kb + 1 == kb1) mma_commit_pair(acc_full(buf), pair_mask);
+          if (kb + 1 == kb1) mma_commit_pair(acc_full(acc.stage), pair_mask);
         }
         __syncwarp();
         ring.next(ring_size);
@@ -578,10 +538,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
           ++it;
         }
       }
-      if (++buf == p.acc_bufs) {
-        buf = 0;
-        phase ^= 1u;
-      }
+      acc.next(2);
     }
     // every MMA of the pair is complete before TMEM is released
     if (elect_one()) mma_commit_pair(drain_bar, (uint16_t)(1u << cluster_rank));
@@ -620,35 +577,32 @@ __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p
   }
 }
 
-// Whether TMEM holds two accumulators of t tokens, beside two slots of w.
-static bool two_accumulators(bool int8, int t) { return !int8 || t <= 192; }
+// The most tokens of a tile: TMEM holds two accumulators, and for int8 two K blocks of w beside them.
+// (One accumulator of 256 tokens and four K blocks took 193 us for 4096 x 8192 x 4096, where two of 160
+// or 192 take 160: the epilogue's 8 us a tile are then not hidden.)
+static int tc_most_tokens(bool int8) { return int8 ? 192 : kTcMaxTokens; }
 
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
   const bool int8 = code_type == Q8_INT8;
   p.n_tiles = (p.N + kTcChannels - 1) / kTcChannels;
   p.k_blocks = (p.K + kTcBlockK - 1) / kTcBlockK;
   // Tokens of a tile and slices of K: the choice whose waves of tiles are estimated to take the
-  // fewest cycles. A K block of a 256 x t tile takes 4t cycles of f16 MMAs (2t of e4m3's), and never
-  // less than w's 16 KB a CTA take to arrive: the memory's 6.8 TB/s (3570 bytes a cycle) shared by
-  // the CTAs at work, up to 40 bytes a cycle each. An epilogue that no second accumulator hides
-  // costs about 8 cycles a token, so does a kernel's last one; joining slices about 20 a token and
-  // 2500 for the cluster's barriers.
+  // fewest cycles. Measured on whole products, at 1.9 GHz: a K block of a tile of t tokens takes 430 +
+  // 2.3t cycles (int8) or 2.9t (e4m3), and at least 690 or 415, what its chain of waits and copies
+  // takes; the last epilogue about 8 a token, joining slices about 20 a token and 2500 for the
+  // cluster's barriers.
   double best = 1e300;
-  for (int t = 32; t <= kTcMaxTokens && t < p.M + 32; t += 32) {
+  for (int t = 32; t <= tc_most_tokens(int8) && t < p.M + 32; t += 32) {
     if (lim.block_t && t != lim.block_t) continue;
     const long long m_tiles = (p.M + t - 1) / t, tiles = m_tiles * p.n_tiles;
-    for (int i = 0; i < 3; ++i) {
-      const int splits = 1 << i;
+    const double kb = int8 ? std::max(430.0 + 2.3 * t, 690.0) : std::max(2.9 * t, 415.0);
+    for (int splits = 1; splits <= kTcMaxSplits; ++splits) {
       if (lim.splits ? splits != lim.splits : splits > 1 && p.k_blocks < 2 * splits) continue;
-      if (splits > p.k_blocks || (splits > 1 && tiles > lim.clusters[i])) continue;
-      const long long held = std::max(1, lim.clusters[i]);
+      if (splits > p.k_blocks || (splits > 1 && tiles > lim.clusters[splits - 1])) continue;
+      const long long held = std::max(1, lim.clusters[splits - 1]);
       const long long waves = (tiles + held - 1) / held;
-      const double ctas = 2.0 * splits * (double)std::min(tiles, held);
-      const double arrive = kTcWBytes / std::min(40.0, 3570.0 / ctas);
-      const double kb = std::max((int8 ? 4.0 : 2.0) * t, arrive);
-      const double unit =
-          (double)((p.k_blocks + splits - 1) / splits) * kb + (two_accumulators(int8, t) ? 0.0 : 8.0 * t);
-      const double cost = (double)waves * unit + (splits > 1 ? 20.0 * t + 2500.0 : 8.0 * t);
+      const double cost = (double)waves * ((p.k_blocks + splits - 1) / splits) * kb +
+                          (splits > 1 ? 20.0 * t + 2500.0 : 8.0 * t);
       if (cost < best) {
         best = cost;
         p.block_t = t;
@@ -658,23 +612,20 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
     }
   }
   const int x_bytes = (int)tc_x_bytes(p.block_t);
-  p.acc_bufs = two_accumulators(int8, p.block_t) ? 2 : 1;
-  p.acc_stride = (p.block_t + 31) / 32 * 32;
-  p.x_expanded = int8 && p.M > kTcXInside;
   p.w_slots = p.x_slots = 0;
   if (int8) {
-    p.w_slots = std::min(kTcDepth, (kTcTmemCols - p.acc_bufs * p.acc_stride) / kTcSlotCols);
-    // x's copies take longer than w's way through TMEM, so x gets most of shared memory if it comes as
-    // f16, and half of it otherwise
-    p.x_slots = std::min(kTcDepth, kTcSmemBudget * (p.x_expanded ? 5 : 4) / 8 / (2 * x_bytes));
+    p.w_slots = std::min(kTcDepth, (kTcTmemCols - 2 * p.block_t) / kTcSlotCols);
+    // x's copies take longer than w's way through TMEM: x gets most of shared memory
+    p.x_slots = std::min(kTcDepth, kTcSmemBudget * 5 / 8 / (2 * x_bytes));
+    p.stages = std::min(kTcMaxStages, (kTcSmemBudget - p.x_slots * 2 * x_bytes) / kTcWBytes);
+  } else {
+    p.stages = std::min(kTcMaxStages, kTcSmemBudget / (kTcWBytes + x_bytes));
   }
-  p.stages = std::min(kTcMaxStages, (kTcSmemBudget - p.x_slots * 2 * x_bytes) /
-                                        (kTcWBytes + (p.x_expanded ? 0 : x_bytes)));
 }
 
 size_t linear_tc_smem_bytes(const LinearParams& p) {
   const size_t x_bytes = tc_x_bytes(p.block_t);
-  return 1024 + p.stages * (kTcWBytes + (p.x_expanded ? 0 : x_bytes)) + p.x_slots * 2 * x_bytes +
+  return 1024 + p.stages * kTcWBytes + (p.x_slots ? 2 * p.x_slots : p.stages) * x_bytes +
          2 * kTcBoxBytes + kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
 }
 
@@ -690,16 +641,16 @@ cudaError_t linear_tc_setup() {
   return e;
 }
 
-// Clusters of 2, 4 and 8 CTAs that the current device holds at once.
-cudaError_t linear_tc_max_clusters(int (&clusters)[3]) {
-  for (int i = 0; i < 3; ++i) {
+// Clusters of 2, 4, 6 and 8 CTAs that the current device holds at once.
+cudaError_t linear_tc_max_clusters(int (&clusters)[kTcMaxSplits]) {
+  for (int i = 0; i < kTcMaxSplits; ++i) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2u << i;
+    attr.val.clusterDim.x = 2 * (i + 1);
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2u << i, 1, 1);
+    cfg.gridDim = dim3(2 * (i + 1), 1, 1);
     cfg.blockDim = dim3(kTcThreads<true>, 1, 1);
     cfg.dynamicSmemBytes = kTcMostSmem;
     cfg.attrs = &attr;
@@ -742,7 +693,7 @@ cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtenso
                              cudaStream_t stream) {
   const long long tiles = (long long)p.m_tiles * p.n_tiles;
   const int cluster = 2 * p.splits;
-  const int grid = cluster * (int)std::min<long long>(tiles, std::max(1, lim.clusters[p.splits / 2]));
+  const int grid = cluster * (int)std::min<long long>(tiles, std::max(1, lim.clusters[p.splits - 1]));
   const size_t smem = linear_tc_smem_bytes(p);
   if (code_type == Q8_INT8)
     return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads<true>, cluster, smem, stream, wmap, xmap,

@@ -109,13 +109,15 @@ def test_large(code_dtype):
 def test_every_tile(code_dtype, block_t):
     """Every tile, whole and in slices, on one pair of CTAs and on many, with stores of one channel
     and of four, and with fewer tokens than a tile."""
+    if code_dtype == torch.int8 and block_t > 192:
+        pytest.skip("int8 tiles have up to 192 tokens")
     for M in (block_t - 31, block_t, 3 * block_t - 5):
         for i, (N, K) in enumerate([(300, 1000), (520, 1536), (256, 130)]):
             check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, torch.float32, kernel=2,
                   block_t=block_t, splits=1, y_extra=4 * (i % 2))
             check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, kernel=2, block_t=block_t,
                   splits=1, max_ctas=2)
-            for splits in (2, 4):
+            for splits in (2, 3, 4):
                 if -(-K // 128) >= splits:
                     check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, torch.float32, kernel=2,
                           block_t=block_t, splits=splits, y_extra=4 * (i % 2))
@@ -153,7 +155,7 @@ def test_options_that_leave_no_tiling():
             capi.linear_q8_run(plan, x, sx, w, sw, y)
         assert e.value.status == capi.CONV3D_EUNSUPPORTED
         capi.linear_q8_destroy(plan)
-    for options in (dict(block_t=33), dict(block_t=288), dict(splits=3), dict(kernel=3),
+    for options in (dict(block_t=33), dict(block_t=288), dict(splits=5), dict(kernel=3),
                     dict(max_ctas=-1), dict(wait_timeout_ms=-1)):
         with pytest.raises(capi.Conv3dFp8Error) as e:
             capi.linear_q8_plan(40, 64, 200, capi.Q8_INT8, 0, **options)
