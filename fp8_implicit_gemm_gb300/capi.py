@@ -453,28 +453,31 @@ Q8_F32, Q8_BF16, Q8_F16 = 1, 2, 3
 Q8_INT8, Q8_E4M3 = 1, 2
 
 # The argument structs of include/q8.h, packed as C lays them out on a 64-bit host: one bytes object
-# crosses the boundary, which costs less than a dozen converted arguments.
+# crosses the boundary. These calls run once or more a layer and token, so what they check of a tensor
+# is asked for once and compared in as few steps as possible.
 _RMSNORM_ARGS = struct.Struct("@6P4q2qP4ifi")
 _SILU_MUL_ARGS = struct.Struct("@4P3q2qP4i")
 _LINEAR_ARGS = struct.Struct("@6P6qP4i")
 
 _value_types = {}
 _code_types = {}
-_f32 = None  # torch.float32, once torch is imported
+_q8 = None  # the library, once its first call has loaded it
 
 
-def _q8_types():
-    global _f32
+def _q8_setup():
+    global _q8
     import torch
-    _f32 = torch.float32
+    lib = load()
     _value_types.update({torch.float32: Q8_F32, torch.bfloat16: Q8_BF16, torch.float16: Q8_F16})
     _code_types.update({torch.int8: Q8_INT8, torch.uint8: Q8_E4M3, torch.float8_e4m3fn: Q8_E4M3})
+    _q8 = lib
+    return lib
 
 
 def q8_code_type(dtype) -> int:
     """Q8_INT8 for torch.int8, Q8_E4M3 for torch.float8_e4m3fn or torch.uint8 (e4m3 bytes)."""
     if not _code_types:
-        _q8_types()
+        _q8_setup()
     t = _code_types.get(dtype)
     if t is None:
         raise ValueError(f"codes are int8, float8_e4m3fn or uint8 (e4m3 bytes), not {dtype}")
@@ -482,84 +485,100 @@ def q8_code_type(dtype) -> int:
 
 
 def _q8_value_type(t, name) -> int:
-    if not _value_types:
-        _q8_types()
     v = _value_types.get(t.dtype)
     if v is None:
         raise ValueError(f"{name} holds fp32, bfloat16 or float16 values, not {t.dtype}")
     return v
 
 
-def _q8_matrix(t, name, shape=None, dtype=None):
-    """Pitch of a CUDA matrix whose rows are contiguous."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name}: expected a matrix with contiguous rows")
-    if shape is not None and t.shape != shape:
+def _q8_pitch(t, name, shape, device) -> int:
+    """Pitch of a matrix of this shape and device whose rows are contiguous."""
+    if t.shape != shape:
         raise ValueError(f"{name}: expected the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    return t.stride(0)
+    pitch, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on CUDA device {device}")
+    return pitch
 
 
-def _q8_vector(t, name, size, dtype=None):
+def _q8_vector(t, name, size, device, dtype=None) -> int:
+    """Address of a contiguous vector of this size and device."""
     if t.dim() != 1 or t.shape[0] != size or (size > 1 and t.stride(0) != 1):
         raise ValueError(f"{name}: expected {size} contiguous elements")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on CUDA device {device}")
     return t.data_ptr()
 
 
-def _q8_device(*tensors) -> int:
-    d = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != d:
-            raise ValueError("expected tensors of one device")
-    return d
+def _q8_head(t, name):
+    """Shape and device of a call's first matrix."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.shape, device
+
+
+def _q8_stream(stream, device) -> int:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def rmsnorm_q8_run(x, weight, q, scale, eps, residual=None, residual_out=None,
                    stream=None) -> None:
     """h = x + residual; residual_out = h; q, scale = the codes of h / rms(h) * weight, a scale a
     row. Matrices [rows, cols] with contiguous rows (any pitch); the codes' type is q's."""
-    shape = x.shape
-    value_type = _q8_value_type(x, "x")
-    x_pitch = _q8_matrix(x, "x")
+    lib = _q8 or _q8_setup()
+    shape, device = _q8_head(x, "x")
     rows, cols = shape
-    code_type = q8_code_type(q.dtype)
-    q_pitch = _q8_matrix(q, "q", shape)
+    value_type = _q8_value_type(x, "x")
     r_ptr = out_ptr = r_pitch = out_pitch = 0
     if residual is not None:
-        r_pitch, r_ptr = _q8_matrix(residual, "residual", shape, x.dtype), residual.data_ptr()
+        if residual.dtype != x.dtype:
+            raise ValueError(f"residual: expected {x.dtype}, got {residual.dtype}")
+        r_pitch, r_ptr = _q8_pitch(residual, "residual", shape, device), residual.data_ptr()
     if residual_out is not None:
-        out_pitch = _q8_matrix(residual_out, "residual_out", shape, x.dtype)
+        if residual_out.dtype != x.dtype:
+            raise ValueError(f"residual_out: expected {x.dtype}, got {residual_out.dtype}")
+        out_pitch = _q8_pitch(residual_out, "residual_out", shape, device)
         out_ptr = residual_out.data_ptr()
-    args = _RMSNORM_ARGS.pack(
-        x.data_ptr(), r_ptr, _q8_vector(weight, "weight", cols), out_ptr, q.data_ptr(),
-        _q8_vector(scale, "scale", rows, _f32), x_pitch, r_pitch, out_pitch, q_pitch,
-        rows, cols, _stream(stream), value_type, _q8_value_type(weight, "weight"), code_type,
-        _q8_device(x, weight, q, scale, residual, residual_out), eps, 0)
-    _raise(load().rmsnorm_q8_run(args), "rmsnorm_q8_run")
+    status = lib.rmsnorm_q8_run(_RMSNORM_ARGS.pack(
+        x.data_ptr(), r_ptr, _q8_vector(weight, "weight", cols, device), out_ptr, q.data_ptr(),
+        _q8_vector(scale, "scale", rows, device, _f32()), _q8_pitch(x, "x", shape, device), r_pitch,
+        out_pitch, _q8_pitch(q, "q", shape, device), rows, cols, _q8_stream(stream, device),
+        value_type, _q8_value_type(weight, "weight"), q8_code_type(q.dtype), device, eps, 0))
+    if status:
+        _raise(status, "rmsnorm_q8_run")
 
 
 def silu_mul_q8_run(gate, up, q, scale, stream=None) -> None:
     """q, scale = the codes of silu(gate) * up, a scale a row. Matrices [rows, cols] with contiguous
     rows (any pitch; gate and up may be two halves of one matrix); the codes' type is q's."""
-    shape = gate.shape
-    value_type = _q8_value_type(gate, "gate")
-    gate_pitch = _q8_matrix(gate, "gate")
-    up_pitch = _q8_matrix(up, "up", shape, gate.dtype)
-    code_type = q8_code_type(q.dtype)
-    q_pitch = _q8_matrix(q, "q", shape)
+    lib = _q8 or _q8_setup()
+    shape, device = _q8_head(gate, "gate")
     rows, cols = shape
-    args = _SILU_MUL_ARGS.pack(
+    value_type = _q8_value_type(gate, "gate")
+    if up.dtype != gate.dtype:
+        raise ValueError(f"up: expected {gate.dtype}, got {up.dtype}")
+    status = lib.silu_mul_q8_run(_SILU_MUL_ARGS.pack(
         gate.data_ptr(), up.data_ptr(), q.data_ptr(),
-        _q8_vector(scale, "scale", rows, _f32), gate_pitch, up_pitch, q_pitch, rows, cols,
-        _stream(stream), value_type, code_type, _q8_device(gate, up, q, scale), 0)
-    _raise(load().silu_mul_q8_run(args), "silu_mul_q8_run")
+        _q8_vector(scale, "scale", rows, device, _f32()), _q8_pitch(gate, "gate", shape, device),
+        _q8_pitch(up, "up", shape, device), _q8_pitch(q, "q", shape, device), rows, cols,
+        _q8_stream(stream, device), value_type, q8_code_type(q.dtype), device, 0))
+    if status:
+        _raise(status, "silu_mul_q8_run")
+
+
+def _f32():
+    import torch
+    return torch.float32
 
 
 def linear_q8_plan(max_rows, N, K, code_type, device=0, **options) -> int:
@@ -581,25 +600,28 @@ def linear_q8_plan(max_rows, N, K, code_type, device=0, **options) -> int:
 def linear_q8_run(plan, x, scale_x, w, scale_w, y, bias=None, stream=None) -> None:
     """y[m, n] = scale_x[m] * scale_w[n] * sum_k x[m, k] * w[n, k] + bias[n]. x [rows, K] and
     w [N, K] are codes of one type with row pitches that are multiples of 16, y is [rows, N]."""
-    if x.dim() != 2 or w.dim() != 2:
-        raise ValueError("x and w: expected matrices")
-    rows, K = x.shape
+    lib = _q8 or _q8_setup()
+    x_shape, device = _q8_head(x, "x")
+    rows, K = x_shape
+    if w.dim() != 2:
+        raise ValueError("w: expected a matrix")
     N = w.shape[0]
     code_type = q8_code_type(x.dtype)
     if code_type != q8_code_type(w.dtype):
         raise ValueError(f"x and w hold codes of one type, not {x.dtype} and {w.dtype}")
-    x_pitch = _q8_matrix(x, "x")
-    w_pitch = _q8_matrix(w, "w", (N, K))
-    y_pitch = _q8_matrix(y, "y", (rows, N))
     b_ptr = b_type = 0
     if bias is not None:
-        b_ptr, b_type = _q8_vector(bias, "bias", N), _q8_value_type(bias, "bias")
-    _q8_device(x, scale_x, w, scale_w, y, bias)
-    args = _LINEAR_ARGS.pack(
-        x.data_ptr(), _q8_vector(scale_x, "scale_x", rows, _f32), w.data_ptr(),
-        _q8_vector(scale_w, "scale_w", N, _f32), b_ptr, y.data_ptr(), x_pitch, w_pitch,
-        y_pitch, rows, N, K, _stream(stream), _q8_value_type(y, "y"), b_type, code_type, 0)
-    _raise(load().linear_q8_run(plan, args), "linear_q8_run")
+        b_ptr = _q8_vector(bias, "bias", N, device)
+        b_type = _q8_value_type(bias, "bias")
+    f32 = _f32()
+    status = lib.linear_q8_run(plan, _LINEAR_ARGS.pack(
+        x.data_ptr(), _q8_vector(scale_x, "scale_x", rows, device, f32), w.data_ptr(),
+        _q8_vector(scale_w, "scale_w", N, device, f32), b_ptr, y.data_ptr(),
+        _q8_pitch(x, "x", x_shape, device), _q8_pitch(w, "w", (N, K), device),
+        _q8_pitch(y, "y", (rows, N), device), rows, N, K, _q8_stream(stream, device),
+        _q8_value_type(y, "y"), b_type, code_type, 0))
+    if status:
+        _raise(status, "linear_q8_run")
 
 
 def linear_q8_check(plan) -> int:

@@ -12,7 +12,7 @@ struct linear_q8_plan_s {
   int code_type = 0;
   long long max_rows = 0, N = 0, K = 0;
   TcLimits lim{};
-  int few = kFewTokens;            // tokens up to which the kernel for few tokens runs
+  int kernel = 0;                  // as in the options
   unsigned long long timeout_ns = 0;
   int debug_flags = 0;
   uint8_t* workspace = nullptr;    // status word; x as f16 (int8)
@@ -229,7 +229,7 @@ extern "C" conv3d_status linear_q8_plan_ex(linear_q8_plan_t* plan, long long max
       o.max_ctas < 0 || o.wait_timeout_ms < 0)
     return CONV3D_EINVAL;
   if (max_rows >= (1LL << 30) || N >= (1LL << 30) || K >= (1LL << 30)) return CONV3D_EUNSUPPORTED;
-  if (o.kernel == 1 && max_rows > kFewTokens) return CONV3D_EUNSUPPORTED;
+  if (o.kernel == 1 && max_rows > few_tokens(code_type)) return CONV3D_EUNSUPPORTED;
   const conv3d_status st = check_device(device);
   if (st != CONV3D_OK) return st;
   linear_q8_plan_s* pl = new (std::nothrow) linear_q8_plan_s();
@@ -239,10 +239,11 @@ extern "C" conv3d_status linear_q8_plan_ex(linear_q8_plan_t* plan, long long max
   pl->max_rows = max_rows;
   pl->N = N;
   pl->K = K;
-  pl->few = o.kernel == 2 ? 0 : kFewTokens;
+  pl->kernel = o.kernel;
   pl->timeout_ns = o.wait_timeout_ms > 0 ? o.wait_timeout_ms * 1000000ull : kLinearTimeoutNs;
   pl->debug_flags = o.debug_flags;
-  if (max_rows > pl->few) {
+  // few tokens need no workspace; a product of fewer tokens than max_rows is not dearer to them
+  if (o.kernel != 1 && (o.kernel == 2 || !prefer_few(max_rows, N, K, code_type))) {
     if (linear_tc_setup() != cudaSuccess || linear_tc_max_clusters(pl->lim.clusters) != cudaSuccess) {
       cudaGetLastError();
       delete pl;
@@ -314,7 +315,8 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
   const int yb = value_bytes(a->y_type);
   p.y_vec = aligned(a->y, 4 * yb) && (p.M <= 1 || p.y_pitch % 4 == 0);
   cudaStream_t stream = static_cast<cudaStream_t>(a->stream);
-  if (p.M <= plan->few)
+  if (plan->kernel == 1 || !plan->workspace ||
+      (plan->kernel == 0 && prefer_few(p.M, p.N, p.K, plan->code_type)))
     return launched(launch_linear_few(p, plan->code_type, stream));
   linear_tc_decide(p, plan->code_type, plan->lim);
   if (!p.block_t) return CONV3D_EUNSUPPORTED;  // the options leave no tiling for this many tokens

@@ -56,13 +56,22 @@ struct LinearParams {
   int debug_flags;
 };
 
-// Tokens that the kernel for few tokens takes at most; it needs no workspace.
-constexpr int kFewTokens = 32;
+// The kernel for few tokens takes up to this many; it needs no workspace.
+constexpr int few_tokens(int code_type) { return code_type == Q8_INT8 ? 32 : 16; }
+// Whether it is the faster one. Measured, us, few tokens / tensor cores: int8 16 tokens 4096 x 16384
+// 16.4 / 23.1, 16384 x 4096 19.8 / 18.9; 32 tokens 4096 x 4096 9.0 / 10.5, 1024 x 16384 12.6 / 17.6, 8192
+// x 4096 19.9 / 13.3, 4096 x 8192 18.4 / 15.1. e4m3 8 tokens 16384 x 4096 15.9 / 14.2, 4096 x 16384 14.1
+// / 15.8; 16 tokens 4096 x 4096 5.6 / 6.8, 1024 x 16384 9.2 / 10.5, 8192 x 4096 11.4 / 9.3, 4096 x 8192
+// 11.0 / 9.7.
+inline bool prefer_few(long long M, long long N, long long K, int code_type) {
+  const bool small = N * K <= 20 * 1000 * 1000;
+  return M <= 8 || (M <= few_tokens(code_type) && (small || (code_type == Q8_INT8 && M <= 16)));
+}
 cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t stream);
 
 // The tensor-core kernel: CTA pairs, tiles of 256 channels by block_t tokens.
 constexpr int kTcChannels = 256;
-constexpr int kTcBlockK = 128;         // codes of K a pipeline stage holds
+constexpr int kTcBlockK = 128;         // codes of K in a box
 constexpr int kTcMaxTokens = 256;
 constexpr int kTcMaxSplits = 4;
 // What a plan's device and options allow.

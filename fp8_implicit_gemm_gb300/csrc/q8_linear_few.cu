@@ -199,9 +199,10 @@ static cudaError_t launch_few(const LinearParams& p, cudaStream_t stream) {
   // Up to 8 tokens: 16 channels a block while that leaves SMs idle; 32 (half the reads of x) on 16
   // warps while one block an SM holds all, on 8 warps, two blocks an SM, beyond. Measured in us, N x
   // K, 1 token int8: 2048 x 4096 3.0 / 3.6 / 3.5, 4096 x 8192 9.7 / 6.8 / 8.6, 8192 x 4096 12.1 / 8.5
-  // / 6.8. Up to 16 and 32 tokens, whose x takes more registers: 16 channels on 8 warps (16 tokens,
+  // / 6.8. Up to 16 (and 32 int8) tokens, whose x takes more registers: 16 channels on 8 warps (16 tokens,
   // 8192 x 4096: 13.2 / 13.3 / 11.8, and 9.8 so).
-  if (p.M > 16) return launch_one<kInt8, 1, 4, 8>(p, stream);
+  if constexpr (kInt8)
+    if (p.M > 16) return launch_one<kInt8, 1, 4, 8>(p, stream);
   if (p.M > 8) return launch_one<kInt8, 1, 2, 8>(p, stream);
   if (p.N <= 2432) return launch_one<kInt8, 1, 1, 16>(p, stream);
   if (p.N <= 4864) return launch_one<kInt8, 2, 1, 16>(p, stream);

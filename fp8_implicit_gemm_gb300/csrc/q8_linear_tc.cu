@@ -6,7 +6,9 @@
 // channel in each TMEM lane and a token in each column, and a warp's stores of one token cover 32
 // consecutive channels of y.
 //
-// e4m3: both operands go from global memory to shared memory by TMA and into kind::f8f6f4.
+// e4m3: both operands go from global memory to shared memory by TMA and into kind::f8f6f4. A stage
+// holds 256 codes of K: with 128 the issuing warp's 520 cycles a stage (a wait 160, the MMAs 30 each,
+// a commit 60) were as long as the stage's MMAs take at 256 tokens.
 //
 // int8: sm_103a has no fast integer pipe, but an int8 code is exact in f16 (an 11-bit significand),
 // a product of two is an integer of at most 2^14, and the fp32 accumulator holds their sums exactly
@@ -46,7 +48,9 @@ template <bool kInt8>
 constexpr int kTcTmaWarpOf = kInt8 ? kTcXWarp + 1 : 4;
 template <bool kInt8>
 constexpr int kTcThreads = (kTcTmaWarpOf<kInt8> + 2) * 32;
-constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // w's codes of one stage: 16 KB a CTA
+template <bool kInt8>
+constexpr int kTcStepBoxes = kInt8 ? 1 : 2;         // boxes of 128 codes that make a K block
+constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // a box of w's codes: 16 KB a CTA
 constexpr int kTcMaxStages = 8;
 constexpr int kTcSmemBudget = 208 * 1024;
 constexpr int kTcTmemCols = 512;
@@ -83,7 +87,8 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const Abo
   return ok;
 }
 
-// x's codes of one stage of one CTA (half of the tile's tokens); as f16 they are twice that.
+// A box of x's codes of one CTA (half of the tile's tokens), or of half as many as f16. Either way a
+// stage (e4m3) or a slot (int8) of x is two.
 __host__ __device__ inline uint32_t tc_x_bytes(int block_t) {
   return (uint32_t)(block_t / 2) * kTcBlockK;
 }
@@ -242,11 +247,13 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
   const int S = p.stages;
+  constexpr int kBoxes = kTcStepBoxes<kInt8>;
+  constexpr uint32_t kWStage = kBoxes * kTcWBytes;
   const uint32_t x_bytes = tc_x_bytes(p.block_t);
   uint8_t* sW = smem;
-  uint8_t* sX = smem + (size_t)S * kTcWBytes;
-  // x's tiles: codes in the stages (e4m3), or f16 in slots of their own, two 64-code halves each
-  uint8_t* sBox = sX + (size_t)(kInt8 ? 2 * p.x_slots : S) * x_bytes;  // the epilogue's staging
+  uint8_t* sX = smem + (size_t)S * kWStage;
+  // x's tiles: codes in the stages (e4m3), or f16 in slots of their own
+  uint8_t* sBox = sX + (size_t)(kInt8 ? p.x_slots : S) * 2 * x_bytes;  // the epilogue's staging
   float* sScale = reinterpret_cast<float*>(sBox + 2 * kTcBoxBytes);  // [kTcMaxTokens]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kTcMaxTokens);
   // Barriers (those marked L: the leader's are used). full[S]: a stage's copies have landed (e4m3 L:
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
             aborted = true;
             break;
           }
-          const uint8_t* src = sW + (size_t)ring.stage * kTcWBytes + row * kTcBlockK;
+          const uint8_t* src = sW + (size_t)ring.stage * kWStage + row * kTcBlockK;
           uint4 c[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // 16-byte chunk i of this half, where the swizzle put it
@@ -453,16 +460,21 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         }
         if (!skip && elect_one()) {
           const uint32_t bar = leader_bars + (full(s) - bars_u32);
-          const uint32_t w_dst = smem_u32(sW) + (uint32_t)s * kTcWBytes;
-          const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * x_bytes;
-          const int k0 = kb * kTcBlockK;
+          const uint32_t w_dst = smem_u32(sW) + (uint32_t)s * kWStage;
+          const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * 2 * x_bytes;
+          const int k0 = kb * kBoxes * kTcBlockK;
           if (kInt8) {  // each CTA's converters wait for its own copies
             mbar_arrive_expect_tx(full(s), kTcWBytes);
             tma_load_2d(w_dst, &wmap, full(s), k0, n0);
           } else {
-            if (leader) mbar_arrive_expect_tx(full(s), 2 * (kTcWBytes + x_bytes));
+            const bool both = k0 + kTcBlockK < p.K;  // K may end with the first box
+            if (leader) mbar_arrive_expect_tx(full(s), (both ? 4u : 2u) * (kTcWBytes + x_bytes));
             tma_load_2d_pair(w_dst, &wmap, bar, k0, n0);
             tma_load_2d_pair(x_dst, &xmap, bar, k0, m0);
+            if (both) {
+              tma_load_2d_pair(w_dst + kTcWBytes, &wmap, bar, k0 + kTcBlockK, n0);
+              tma_load_2d_pair(x_dst + x_bytes, &xmap, bar, k0 + kTcBlockK, m0);
+            }
           }
         }
         skip = false;
@@ -495,10 +507,11 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         tc_fence_after();
         if (elect_one()) {
           const uint32_t acc0 = kb > kb0 ? 1u : 0u;
-          const int rem = p.K - kb * kTcBlockK;  // codes past K are zeros, and mostly left out
+          // codes past K are zeros, and mostly left out
+          const int rem = p.K - kb * kBoxes * kTcBlockK;
+          const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 3));
+          const uint64_t xdesc1 = xdesc + (x_bytes >> 4);  // the second box
           if (kInt8) {
-            const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 3));
-            const uint64_t xdesc1 = xdesc + (x_bytes >> 4);  // the second 64 codes
             const uint32_t a = slots_base + (uint32_t)(wslots.stage * kTcSlotCols);
             if (rem >= kTcBlockK) {
               mma_f16_pair_tmem_a(d, a, xdesc, idesc, acc0);
@@ -516,16 +529,21 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
             }
             mma_commit_pair(done(it), pair_mask);
           } else {
-            const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 4));
-            const uint64_t wdesc = wdesc0 + (uint64_t)((uint32_t)s * (kTcWBytes >> 4));
-            if (rem >= kTcBlockK) {
+            const uint64_t wdesc = wdesc0 + (uint64_t)((uint32_t)s * (kWStage >> 4));
+            const uint64_t wdesc1 = wdesc + (kTcWBytes >> 4);
+            if (rem >= 2 * kTcBlockK) {
               mma_f8f6f4_pair(d, wdesc, xdesc, idesc, acc0);
               mma_f8f6f4_pair(d, wdesc + 2, xdesc + 2, idesc, 1u);
               mma_f8f6f4_pair(d, wdesc + 4, xdesc + 4, idesc, 1u);
               mma_f8f6f4_pair(d, wdesc + 6, xdesc + 6, idesc, 1u);
+              mma_f8f6f4_pair(d, wdesc1, xdesc1, idesc, 1u);
+              mma_f8f6f4_pair(d, wdesc1 + 2, xdesc1 + 2, idesc, 1u);
+              mma_f8f6f4_pair(d, wdesc1 + 4, xdesc1 + 4, idesc, 1u);
+              mma_f8f6f4_pair(d, wdesc1 + 6, xdesc1 + 6, idesc, 1u);
             } else {
               for (int j = 0; 32 * j < rem; ++j)
-                mma_f8f6f4_pair(d, wdesc + 2 * j, xdesc + 2 * j, idesc, j > 0 ? 1u : acc0);
+                mma_f8f6f4_pair(d, (j < 4 ? wdesc : wdesc1) + 2 * (j & 3),
+                                (j < 4 ? xdesc : xdesc1) + 2 * (j & 3), idesc, j > 0 ? 1u : acc0);
             }
             mma_commit_pair(empty(s), pair_mask);
           }
@@ -585,24 +603,24 @@ static int tc_most_tokens(bool int8) { return int8 ? 192 : kTcMaxTokens; }
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
   const bool int8 = code_type == Q8_INT8;
   p.n_tiles = (p.N + kTcChannels - 1) / kTcChannels;
-  p.k_blocks = (p.K + kTcBlockK - 1) / kTcBlockK;
+  const int step_k = (int8 ? kTcStepBoxes<true> : kTcStepBoxes<false>) * kTcBlockK;
+  p.k_blocks = (p.K + step_k - 1) / step_k;
   // Tokens of a tile and slices of K: the choice whose waves of tiles are estimated to take the
   // fewest cycles. Measured on whole products, at 1.9 GHz: a K block of a tile of t tokens takes 430 +
-  // 2.3t cycles (int8) or 2.9t (e4m3), and at least 690 or 415, what its chain of waits and copies
-  // takes; the last epilogue about 8 a token, joining slices about 20 a token and 2500 for the
-  // cluster's barriers.
+  // 2.3t cycles and at least 690 (int8), or 380 + 2.3t and at least 5.6t (e4m3, 256 codes); the last
+  // epilogue about 8 a token; joining slices about 20 a token and 3500 for the cluster's barriers.
   double best = 1e300;
   for (int t = 32; t <= tc_most_tokens(int8) && t < p.M + 32; t += 32) {
     if (lim.block_t && t != lim.block_t) continue;
     const long long m_tiles = (p.M + t - 1) / t, tiles = m_tiles * p.n_tiles;
-    const double kb = int8 ? std::max(430.0 + 2.3 * t, 690.0) : std::max(2.9 * t, 415.0);
+    const double kb = int8 ? std::max(430.0 + 2.3 * t, 690.0) : std::max(380.0 + 2.3 * t, 5.6 * t);
     for (int splits = 1; splits <= kTcMaxSplits; ++splits) {
       if (lim.splits ? splits != lim.splits : splits > 1 && p.k_blocks < 2 * splits) continue;
       if (splits > p.k_blocks || (splits > 1 && tiles > lim.clusters[splits - 1])) continue;
       const long long held = std::max(1, lim.clusters[splits - 1]);
       const long long waves = (tiles + held - 1) / held;
       const double cost = (double)waves * ((p.k_blocks + splits - 1) / splits) * kb +
-                          (splits > 1 ? 20.0 * t + 2500.0 : 8.0 * t);
+                          (splits > 1 ? 20.0 * t + 3500.0 : 8.0 * t);
       if (cost < best) {
         best = cost;
         p.block_t = t;
@@ -619,14 +637,15 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
     p.x_slots = std::min(kTcDepth, kTcSmemBudget * 5 / 8 / (2 * x_bytes));
     p.stages = std::min(kTcMaxStages, (kTcSmemBudget - p.x_slots * 2 * x_bytes) / kTcWBytes);
   } else {
-    p.stages = std::min(kTcMaxStages, kTcSmemBudget / (kTcWBytes + x_bytes));
+    p.stages = std::min(kTcMaxStages, kTcSmemBudget / (2 * (kTcWBytes + x_bytes)));
   }
 }
 
-size_t linear_tc_smem_bytes(const LinearParams& p) {
-  const size_t x_bytes = tc_x_bytes(p.block_t);
-  return 1024 + p.stages * kTcWBytes + (p.x_slots ? 2 * p.x_slots : p.stages) * x_bytes +
-         2 * kTcBoxBytes + kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
+size_t linear_tc_smem_bytes(const LinearParams& p, int code_type) {
+  const size_t x = 2 * tc_x_bytes(p.block_t);
+  const size_t tiles = code_type == Q8_INT8 ? p.stages * kTcWBytes + p.x_slots * x
+                                            : p.stages * (2 * kTcWBytes + x);
+  return 1024 + tiles + 2 * kTcBoxBytes + kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
 }
 
 constexpr int kTcMostSmem =
@@ -694,7 +713,7 @@ cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtenso
   const long long tiles = (long long)p.m_tiles * p.n_tiles;
   const int cluster = 2 * p.splits;
   const int grid = cluster * (int)std::min<long long>(tiles, std::max(1, lim.clusters[p.splits - 1]));
-  const size_t smem = linear_tc_smem_bytes(p);
+  const size_t smem = linear_tc_smem_bytes(p, code_type);
   if (code_type == Q8_INT8)
     return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads<true>, cluster, smem, stream, wmap, xmap,
                       ymap, p);
