@@ -45,10 +45,11 @@ struct LinearParams {
   int y_tma;             // y's tiles may leave by TMA
   // the tensor-core kernel's tiling (linear_tc_decide) and workspace
   int block_t;           // tokens of a tile (a tile has kTcChannels channels)
-  int m_tiles, n_tiles, k_blocks;
+  int m_tiles, n_tiles;
+  int boxes, k_blocks;   // a K block is `boxes` boxes of kTcBlockK codes
   int splits;            // slices of K, one for each pair of a cluster: 1 to kTcMaxSplits
   int stages;
-  int w_slots, x_slots;  // int8 only: K blocks of w in TMEM and of x in shared memory as f16
+  int w_slots, x_slots;  // int8 only: boxes of w in TMEM and K blocks of x in shared memory, as f16
   uint16_t* xh;          // int8 only: x as f16, [M][xh_pitch]
   long long xh_pitch;
   int* status;

@@ -13,19 +13,22 @@
 // int8: sm_103a has no fast integer pipe, but an int8 code is exact in f16 (an 11-bit significand),
 // a product of two is an integer of at most 2^14, and the fp32 accumulator holds their sums exactly
 // up to 2^24. So the product runs as kind::f16, at the f16 rate, on codes turned into f16:
-//   - w stays 8 bits wide as far as shared memory. Converter warps read a stage's codes there, half a
-//     row (64 codes) a thread, turn them into f16 (a byte under the exponent of 1024, minus 1152
-//     with the sign bit flipped, a permute and a subtraction for each two codes) and write them to
-//     TMEM, from where the MMA takes its A operand: in shared memory they would come on top of the
-//     codes, x and the MMA's reads, which fill its 128 bytes a cycle at 256 tokens;
+//   - w stays 8 bits wide as far as shared memory. Converter warps read a stage's codes there, turn
+//     them into f16 (a byte under the exponent of 1024, minus 1152 with the sign bit flipped, a
+//     permute and a subtraction for each two codes) and write them to TMEM, from where the MMA takes
+//     its A operand: in shared memory they would come on top of the codes, x and the MMA's reads,
+//     which fill its 128 bytes a cycle at 256 tokens;
 //   - x is expanded to f16 by a small kernel first, 3 bytes of traffic a code, and loaded as such.
 //     Turned by four or eight more warps of this kernel it is read back into shared memory next to
 //     everything else: 256 x 6144 x 4096 takes 26 us so and 22 with the expansion, 64 x 8192 x 4096
 //     15.3 and 14.4, 8192 x 4096 x 8192 408 and 328;
 //   - a K block has one barrier that says that its w and x are there and one commit that frees both,
-//     whatever the depths of their rings: the issuing warp takes about 160 cycles for a wait, 60 for
-//     a commit and 30 for an MMA, and a K block's MMAs take 512 at 128 tokens. With a wait and a
-//     commit for each quarter of a K block it took 2500 cycles.
+//     whatever the depths of their rings, and holds 256 codes in tiles of up to 128 tokens: the
+//     issuing warp takes about 160 cycles for a wait, 60 for a commit and 30 for an MMA, as long as
+//     those MMAs take. (With a wait and a commit for each 32 codes a box of 128 took 2500 cycles.) For
+//     the same reason a converter's visit covers a whole row of a box there, and four groups of four
+//     warps take the boxes by turns; in larger tiles, where TMEM holds two or three boxes of w, the
+//     shorter way of half a row a thread matters more, and two groups of eight take turns.
 //
 // Few tiles: a tile is split along K over the pairs of one cluster (4, 6 or 8 CTAs). Each CTA leaves its
 // partial sums in its own shared memory and adds up its share of the tokens from all of them over
@@ -48,13 +51,16 @@ template <bool kInt8>
 constexpr int kTcTmaWarpOf = kInt8 ? kTcXWarp + 1 : 4;
 template <bool kInt8>
 constexpr int kTcThreads = (kTcTmaWarpOf<kInt8> + 2) * 32;
-template <bool kInt8>
-constexpr int kTcStepBoxes = kInt8 ? 1 : 2;         // boxes of 128 codes that make a K block
+// Warps quartets that share a box's rows by halves, and converter groups that take the boxes by turns.
+template <int kBoxes>
+constexpr int kTcParts = kBoxes == 1 ? 2 : 1;
+template <int kBoxes>
+constexpr int kTcGroups = kTcWWarps / 4 / kTcParts<kBoxes>;
 constexpr int kTcWBytes = kTcWBoxRows * kTcBlockK;  // a box of w's codes: 16 KB a CTA
 constexpr int kTcMaxStages = 8;
 constexpr int kTcSmemBudget = 208 * 1024;
 constexpr int kTcTmemCols = 512;
-constexpr int kTcSlotCols = kTcBlockK / 2;          // a K block of w as f16 in TMEM: 64 columns
+constexpr int kTcSlotCols = kTcBlockK / 2;          // a box of w as f16 in TMEM: 64 columns
 constexpr int kTcDepth = 8;                         // K blocks under way: no ring is deeper
 constexpr uint64_t kTcAbortSettleNs = 2ull * 1000 * 1000;  // let copies in flight land on abort
 
@@ -237,7 +243,8 @@ __device__ __forceinline__ void tc_epilogue(const LinearParams& p, const CUtenso
   }
 }
 
-template <bool kInt8>
+// kBoxes: boxes of 128 codes that make a K block.
+template <bool kInt8, int kBoxes>
 __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
     linear_q8_tc_kernel(const __grid_constant__ CUtensorMap wmap,
                         const __grid_constant__ CUtensorMap xmap,
@@ -247,13 +254,14 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   const uint32_t raw_u32 = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_u32 & 1023u)) & 1023u);
   const int S = p.stages;
-  constexpr int kBoxes = kTcStepBoxes<kInt8>;
-  constexpr uint32_t kWStage = kBoxes * kTcWBytes;
+  // a stage of w's codes is a box (int8) or a K block (e4m3)
+  constexpr uint32_t kWStage = kInt8 ? kTcWBytes : 2 * kTcWBytes;
+  const uint32_t x_step = (uint32_t)kBoxes * (kInt8 ? 2u : 1u) * tc_x_bytes(p.block_t);
   const uint32_t x_bytes = tc_x_bytes(p.block_t);
   uint8_t* sW = smem;
   uint8_t* sX = smem + (size_t)S * kWStage;
   // x's tiles: codes in the stages (e4m3), or f16 in slots of their own
-  uint8_t* sBox = sX + (size_t)(kInt8 ? p.x_slots : S) * 2 * x_bytes;  // the epilogue's staging
+  uint8_t* sBox = sX + (size_t)(kInt8 ? p.x_slots : S) * x_step;  // the epilogue's staging
   float* sScale = reinterpret_cast<float*>(sBox + 2 * kTcBoxBytes);  // [kTcMaxTokens]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kTcMaxTokens);
   // Barriers (those marked L: the leader's are used). full[S]: a stage's copies have landed (e4m3 L:
@@ -289,12 +297,11 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), 1);
-      // an arrival of each converter warp whose turn it is, or a commit's
-      mbar_init(empty(s), kInt8 ? kTcWWarps / 2 : 1);
+      mbar_init(empty(s), kInt8 ? 4 * kTcParts<kBoxes> : 1);  // a converter group, or a commit
     }
     for (uint32_t i = 0; i < kTcDepth; ++i) {
-      // of both CTAs: the warps of w's two halves, and the copies of x
-      mbar_init(ready(i), 2 * (kTcWWarps / 2) + 1);
+      // both CTAs' converters, and the copies of x
+      mbar_init(ready(i), 2 * 4 * kTcParts<kBoxes> * kBoxes + 1);
       mbar_init(done(i), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -377,43 +384,63 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   } else if (warp < kTcTmaWarp) {
     // ---------------------------------------------------------------------------- converters
     if (kInt8 && warp < kTcXWarp) {
-      const int quad = warp & 3, half = ((warp - 4) >> 2) & 1;
-      const uint32_t turn = (uint32_t)(warp - 4) >> 3;  // this warp takes every other K block
+      const int quad = warp & 3;
+      constexpr uint32_t kGroups = kTcGroups<kBoxes>;
+      constexpr int kParts = kTcParts<kBoxes>, kChunks = 8 / kParts;
+      const uint32_t group = (uint32_t)(warp - 4) >> (kParts == 2 ? 3 : 2);
+      const int part = kParts == 2 ? ((warp - 4) >> 2) & 1 : 0;
       const int row = quad * 32 + lane;
-      const uint32_t dst0 = slots_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(32 * half);
-      Ring ring, slots;
-      uint32_t it = 0;  // K blocks of all tiles so far
+      const uint32_t dst0 = slots_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(32 * part);
+      const uint32_t num_boxes = (uint32_t)((kb1 - kb0) * kBoxes);  // of a tile
+      const uint32_t w_slots = (uint32_t)p.w_slots;
+      // The boxes of all tiles are counted through; this group takes every kGroups-th. The number of
+      // stages is a multiple of that, so a stage is always the same group's: were it another's next,
+      // that group could come to wait for a phase two ahead of the barrier's, which a parity cannot
+      // tell from one that is over.
+      uint32_t box = group, stage = group, stage_phase = 0, slot = group % w_slots;
+      uint32_t end = 0;
       bool aborted = false;
       for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++it, ring.next(S), slots.next(p.w_slots)) {
-          if ((it & 1u) != turn) continue;
-          if (!tc_wait(full(ring.stage), ring.phase, ab, kStatusWaitFull)) {
+        end += num_boxes;
+        for (; box < end; box += kGroups) {
+          const uint32_t step = box / kBoxes;
+          if (!tc_wait(full((int)stage), stage_phase, ab, kStatusWaitFull)) {
             aborted = true;
             break;
           }
-          const uint8_t* src = sW + (size_t)ring.stage * kWStage + row * kTcBlockK;
-          uint4 c[4];
+          const uint8_t* src = sW + stage * kWStage + row * kTcBlockK;
+          uint4 c[kChunks];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)  // 16-byte chunk i of this half, where the swizzle put it
-            c[i] = *reinterpret_cast<const uint4*>(src + (((4 * half + i) ^ (row & 7)) << 4));
-          uint32_t h[32];
+          for (int i = 0; i < kChunks; ++i)  // 16-byte chunk i, where the swizzle put it
+            c[i] = *reinterpret_cast<const uint4*>(src + (((kChunks * part + i) ^ (row & 7)) << 4));
+          uint32_t h[kChunks / 4][32];  // the codes as f16, before their slot is free
 #pragma unroll
-          for (int i = 0; i < 4; ++i) int8_to_f16(c[i], h + 8 * i);
+          for (int i = 0; i < kChunks; ++i) int8_to_f16(c[i], h[i / 4] + 8 * (i % 4));
           __syncwarp();  // every lane has its codes
-          if (lane == 0) mbar_arrive(empty(ring.stage));
-          const uint32_t before = it - (uint32_t)p.w_slots;  // the K block that had this slot
-          if (it >= (uint32_t)p.w_slots &&
-              !tc_wait(done(before), parity(before), ab, kStatusWaitEmpty)) {
-            aborted = true;
-            break;
+          if (lane == 0) mbar_arrive(empty((int)stage));
+          // the K block that had this slot
+          if (box >= w_slots) {
+            const uint32_t before = (box - w_slots) / kBoxes;
+            if (!tc_wait(done(before), parity(before), ab, kStatusWaitEmpty)) {
+              aborted = true;
+              break;
+            }
           }
           tc_fence_after();
-          tmem_st_32x32b_x32(dst0 + (uint32_t)(slots.stage * kTcSlotCols), h);
+#pragma unroll
+          for (int i = 0; i < kChunks / 4; ++i)
+            tmem_st_32x32b_x32(dst0 + slot * kTcSlotCols + 32 * i, h[i]);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0)
-            mbar_arrive_cluster_tmem(leader_bars + (ready(it) - bars_u32));
+          if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (ready(step) - bars_u32));
+          stage += kGroups;
+          if (stage >= (uint32_t)S) {
+            stage -= (uint32_t)S;
+            stage_phase ^= 1u;
+          }
+          slot += kGroups;
+          while (slot >= w_slots) slot -= w_slots;
         }
       }
     } else if (kInt8) {
@@ -432,10 +459,12 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
           }
           if (elect_one()) {
             const uint32_t bar = leader_bars + (ready(it) - bars_u32);
-            const uint32_t dst = smem_u32(sX) + (uint32_t)slots.stage * 2 * x_bytes;
-            if (leader) mbar_arrive_expect_tx(ready(it), 4 * x_bytes);
-            tma_load_2d_pair(dst, &xmap, bar, kb * kTcBlockK, m0);
-            tma_load_2d_pair(dst + x_bytes, &xmap, bar, kb * kTcBlockK + 64, m0);
+            const uint32_t dst = smem_u32(sX) + (uint32_t)slots.stage * x_step;
+            if (leader) mbar_arrive_expect_tx(ready(it), 2 * x_step);
+#pragma unroll
+            for (int i = 0; i < 2 * kBoxes; ++i)  // 64 f16 wide
+              tma_load_2d_pair(dst + (uint32_t)i * x_bytes, &xmap, bar,
+                               kb * kBoxes * kTcBlockK + 64 * i, m0);
           }
           __syncwarp();
           slots.next(p.x_slots);
@@ -452,7 +481,8 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       const TcTile un = tc_tile(p, u);
       const int n0 = un.n_tile * kTcChannels + (int)rank * 128;
       const int m0 = un.m_tile * p.block_t + (int)rank * half_t;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      constexpr int per = kInt8 ? kBoxes : 1;  // stages of a K block
+      for (int i = kb0 * per; i < kb1 * per; ++i) {
         const int s = ring.stage;
         if (!tc_wait(empty(s), ring.phase ^ 1u, ab, kStatusWaitEmpty)) {
           aborted = true;
@@ -461,8 +491,8 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         if (!skip && elect_one()) {
           const uint32_t bar = leader_bars + (full(s) - bars_u32);
           const uint32_t w_dst = smem_u32(sW) + (uint32_t)s * kWStage;
-          const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * 2 * x_bytes;
-          const int k0 = kb * kBoxes * kTcBlockK;
+          const uint32_t x_dst = smem_u32(sX) + (uint32_t)s * x_step;
+          const int k0 = i * (kInt8 ? kTcBlockK : 2 * kTcBlockK);
           if (kInt8) {  // each CTA's converters wait for its own copies
             mbar_arrive_expect_tx(full(s), kTcWBytes);
             tma_load_2d(w_dst, &wmap, full(s), k0, n0);
@@ -509,28 +539,36 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
           const uint32_t acc0 = kb > kb0 ? 1u : 0u;
           // codes past K are zeros, and mostly left out
           const int rem = p.K - kb * kBoxes * kTcBlockK;
-          const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_bytes >> 3));
-          const uint64_t xdesc1 = xdesc + (x_bytes >> 4);  // the second box
+          const uint64_t xdesc = xdesc0 + (uint64_t)((uint32_t)s * (x_step >> 4));
+          const uint32_t half = x_bytes >> 4;  // 64 f16, or the second box of e4m3
           if (kInt8) {
-            const uint32_t a = slots_base + (uint32_t)(wslots.stage * kTcSlotCols);
-            if (rem >= kTcBlockK) {
-              mma_f16_pair_tmem_a(d, a, xdesc, idesc, acc0);
-              mma_f16_pair_tmem_a(d, a + 8, xdesc + 2, idesc, 1u);
-              mma_f16_pair_tmem_a(d, a + 16, xdesc + 4, idesc, 1u);
-              mma_f16_pair_tmem_a(d, a + 24, xdesc + 6, idesc, 1u);
-              mma_f16_pair_tmem_a(d, a + 32, xdesc1, idesc, 1u);
-              mma_f16_pair_tmem_a(d, a + 40, xdesc1 + 2, idesc, 1u);
-              mma_f16_pair_tmem_a(d, a + 48, xdesc1 + 4, idesc, 1u);
-              mma_f16_pair_tmem_a(d, a + 56, xdesc1 + 6, idesc, 1u);
+            const uint32_t a0 = slots_base + (uint32_t)(wslots.stage * kTcSlotCols);
+            const int next_slot = wslots.stage + 1 == p.w_slots ? 0 : wslots.stage + 1;
+            const uint32_t a1 = slots_base + (uint32_t)(next_slot * kTcSlotCols);
+            auto issue_box = [&](uint32_t a, uint64_t x, uint32_t acc) {
+              mma_f16_pair_tmem_a(d, a, x, idesc, acc);
+              mma_f16_pair_tmem_a(d, a + 8, x + 2, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 16, x + 4, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 24, x + 6, idesc, 1u);
+              x += half;
+              mma_f16_pair_tmem_a(d, a + 32, x, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 40, x + 2, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 48, x + 4, idesc, 1u);
+              mma_f16_pair_tmem_a(d, a + 56, x + 6, idesc, 1u);
+            };
+            if (rem >= kBoxes * kTcBlockK) {
+              issue_box(a0, xdesc, acc0);
+              if (kBoxes == 2) issue_box(a1, xdesc + 2 * half, 1u);
             } else {
-              for (int j = 0; 16 * j < rem; ++j)
-                mma_f16_pair_tmem_a(d, a + 8 * j, (j < 4 ? xdesc : xdesc1) + 2 * (j & 3), idesc,
+              for (int j = 0; 16 * j < rem; ++j)  // K = 16 each, four to a half
+                mma_f16_pair_tmem_a(d, (j < 8 ? a0 : a1) + 8 * (j & 7),
+                                    xdesc + (uint32_t)(j >> 2) * half + 2 * (j & 3), idesc,
                                     j > 0 ? 1u : acc0);
             }
             mma_commit_pair(done(it), pair_mask);
           } else {
             const uint64_t wdesc = wdesc0 + (uint64_t)((uint32_t)s * (kWStage >> 4));
-            const uint64_t wdesc1 = wdesc + (kTcWBytes >> 4);
+            const uint64_t wdesc1 = wdesc + (kTcWBytes >> 4), xdesc1 = xdesc + half;
             if (rem >= 2 * kTcBlockK) {
               mma_f8f6f4_pair(d, wdesc, xdesc, idesc, acc0);
               mma_f8f6f4_pair(d, wdesc + 2, xdesc + 2, idesc, 1u);
@@ -552,7 +590,8 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         __syncwarp();
         ring.next(ring_size);
         if (kInt8) {
-          wslots.next(p.w_slots);
+          wslots.stage += kBoxes;
+          if (wslots.stage >= p.w_slots) wslots.stage -= p.w_slots;
           ++it;
         }
       }
@@ -600,31 +639,39 @@ __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p
 // or 192 take 160: the epilogue's 8 us a tile are then not hidden.)
 static int tc_most_tokens(bool int8) { return int8 ? 192 : kTcMaxTokens; }
 
+// Boxes of 128 codes of a K block: two, where TMEM has room for two K blocks of w (int8).
+static int tc_boxes(bool int8, int t) { return int8 && t > 128 ? 1 : 2; }
+
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
   const bool int8 = code_type == Q8_INT8;
   p.n_tiles = (p.N + kTcChannels - 1) / kTcChannels;
-  const int step_k = (int8 ? kTcStepBoxes<true> : kTcStepBoxes<false>) * kTcBlockK;
-  p.k_blocks = (p.K + step_k - 1) / step_k;
   // Tokens of a tile and slices of K: the choice whose waves of tiles are estimated to take the
-  // fewest cycles. Measured on whole products, at 1.9 GHz: a K block of a tile of t tokens takes 430 +
-  // 2.3t cycles and at least 690 (int8), or 380 + 2.3t and at least 5.6t (e4m3, 256 codes); the last
-  // epilogue about 8 a token; joining slices about 20 a token and 3500 for the cluster's barriers.
+  // fewest cycles. Measured on whole products, at 1.9 GHz: a K block of a tile of t tokens takes 4.7t
+  // cycles (int8, 128 codes), 780 + 2.1t and at least 9.4t (int8, 256 codes), or 380 + 2.3t and at
+  // least 5.6t (e4m3, 256 codes); the last epilogue about 8 a token; joining slices about 20 a token
+  // and 3500 for the cluster's barriers.
   double best = 1e300;
   for (int t = 32; t <= tc_most_tokens(int8) && t < p.M + 32; t += 32) {
     if (lim.block_t && t != lim.block_t) continue;
     const long long m_tiles = (p.M + t - 1) / t, tiles = m_tiles * p.n_tiles;
-    const double kb = int8 ? std::max(430.0 + 2.3 * t, 690.0) : std::max(380.0 + 2.3 * t, 5.6 * t);
+    const int boxes = tc_boxes(int8, t);
+    const double kb = boxes == 1 ? 4.7 * t
+                      : int8     ? std::max(780.0 + 2.1 * t, 9.4 * t)
+                                 : std::max(380.0 + 2.3 * t, 5.6 * t);
+    const int k_blocks = (p.K + boxes * kTcBlockK - 1) / (boxes * kTcBlockK);
     for (int splits = 1; splits <= kTcMaxSplits; ++splits) {
-      if (lim.splits ? splits != lim.splits : splits > 1 && p.k_blocks < 2 * splits) continue;
-      if (splits > p.k_blocks || (splits > 1 && tiles > lim.clusters[splits - 1])) continue;
+      if (lim.splits ? splits != lim.splits : splits > 1 && k_blocks < 2 * splits) continue;
+      if (splits > k_blocks || (splits > 1 && tiles > lim.clusters[splits - 1])) continue;
       const long long held = std::max(1, lim.clusters[splits - 1]);
       const long long waves = (tiles + held - 1) / held;
-      const double cost = (double)waves * ((p.k_blocks + splits - 1) / splits) * kb +
+      const double cost = (double)waves * ((k_blocks + splits - 1) / splits) * kb +
                           (splits > 1 ? 20.0 * t + 3500.0 : 8.0 * t);
       if (cost < best) {
         best = cost;
         p.block_t = t;
         p.m_tiles = (int)m_tiles;
+        p.k_blocks = k_blocks;
+        p.boxes = boxes;
         p.splits = splits;
       }
     }
@@ -632,19 +679,22 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
   const int x_bytes = (int)tc_x_bytes(p.block_t);
   p.w_slots = p.x_slots = 0;
   if (int8) {
-    p.w_slots = std::min(kTcDepth, (kTcTmemCols - 2 * p.block_t) / kTcSlotCols);
-    // x's copies take longer than w's way through TMEM: x gets most of shared memory
-    p.x_slots = std::min(kTcDepth, kTcSmemBudget * 5 / 8 / (2 * x_bytes));
-    p.stages = std::min(kTcMaxStages, (kTcSmemBudget - p.x_slots * 2 * x_bytes) / kTcWBytes);
+    p.w_slots = std::min(8, (kTcTmemCols - 2 * p.block_t) / kTcSlotCols);
+    // w gets as many stages for each converter group as leave x five K blocks, x the rest
+    const int x_step = p.boxes * 2 * x_bytes;
+    const int groups = p.boxes == 1 ? kTcGroups<1> : kTcGroups<2>;
+    p.stages = (kTcSmemBudget - 5 * x_step) / kTcWBytes / groups * groups;
+    p.stages = std::max(groups, std::min(kTcMaxStages, p.stages));
+    p.x_slots = std::min(kTcDepth, (kTcSmemBudget - p.stages * kTcWBytes) / x_step);
   } else {
     p.stages = std::min(kTcMaxStages, kTcSmemBudget / (2 * (kTcWBytes + x_bytes)));
   }
 }
 
 size_t linear_tc_smem_bytes(const LinearParams& p, int code_type) {
-  const size_t x = 2 * tc_x_bytes(p.block_t);
-  const size_t tiles = code_type == Q8_INT8 ? p.stages * kTcWBytes + p.x_slots * x
-                                            : p.stages * (2 * kTcWBytes + x);
+  const size_t x = tc_x_bytes(p.block_t);
+  const size_t tiles = code_type == Q8_INT8 ? p.stages * kTcWBytes + p.x_slots * p.boxes * 2 * x
+                                            : p.stages * 2 * (kTcWBytes + x);
   return 1024 + tiles + 2 * kTcBoxBytes + kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
 }
 
@@ -652,11 +702,13 @@ constexpr int kTcMostSmem =
     1024 + kTcSmemBudget + 2 * kTcBoxBytes + kTcMaxTokens * 4 + kTcBars * 8 + 16;
 
 cudaError_t linear_tc_setup() {
-  cudaError_t e = cudaFuncSetAttribute(linear_q8_tc_kernel<true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMostSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(linear_q8_tc_kernel<false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMostSmem);
+  cudaError_t e = cudaSuccess;
+  const void* kernels[] = {(const void*)linear_q8_tc_kernel<true, 1>,
+                           (const void*)linear_q8_tc_kernel<true, 2>,
+                           (const void*)linear_q8_tc_kernel<false, 2>};
+  for (const void* k : kernels)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcMostSmem);
   return e;
 }
 
@@ -675,7 +727,7 @@ cudaError_t linear_tc_max_clusters(int (&clusters)[kTcMaxSplits]) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const cudaError_t e =
-        cudaOccupancyMaxActiveClusters(&clusters[i], linear_q8_tc_kernel<true>, &cfg);
+        cudaOccupancyMaxActiveClusters(&clusters[i], linear_q8_tc_kernel<true, 1>, &cfg);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -714,11 +766,12 @@ cudaError_t launch_linear_tc(const LinearParams& p, int code_type, const CUtenso
   const int cluster = 2 * p.splits;
   const int grid = cluster * (int)std::min<long long>(tiles, std::max(1, lim.clusters[p.splits - 1]));
   const size_t smem = linear_tc_smem_bytes(p, code_type);
-  if (code_type == Q8_INT8)
-    return launch_pdl(linear_q8_tc_kernel<true>, grid, kTcThreads<true>, cluster, smem, stream, wmap, xmap,
-                      ymap, p);
-  return launch_pdl(linear_q8_tc_kernel<false>, grid, kTcThreads<false>, cluster, smem, stream, wmap, xmap,
-                    ymap, p);
+  auto launch = [&](auto kernel, int threads) {
+    return launch_pdl(kernel, grid, threads, cluster, smem, stream, wmap, xmap, ymap, p);
+  };
+  if (code_type == Q8_E4M3) return launch(linear_q8_tc_kernel<false, 2>, kTcThreads<false>);
+  return p.boxes == 1 ? launch(linear_q8_tc_kernel<true, 1>, kTcThreads<true>)
+                      : launch(linear_q8_tc_kernel<true, 2>, kTcThreads<true>);
 }
 
 }  // namespace c3d

@@ -111,8 +111,8 @@ typedef struct {
     int block_t;         /* 0: the library chooses; else the tokens of a tensor-core tile, a multiple
                             of 32 up to 256 (int8: 192), and less than the run's rows + 32 */
     int splits;          /* 0: the library chooses; 1 to 4: slices of K (no more than K has blocks of
-                            128 codes, e4m3: 256; with more than one, all tiles must be held by the
-                            device at once) */
+                            256 codes; with more than one, all tiles must be held by the device at
+                            once) */
     int max_ctas;        /* 0: all the device holds; else an upper bound on the grid */
     int wait_timeout_ms; /* 0: 2000 ms; a bounded wait inside a kernel gives up after this long */
     int debug_flags;     /* test-only: bit 0 makes the loader skip its first copy, so the waits on it

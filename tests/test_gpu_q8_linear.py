@@ -118,7 +118,7 @@ def test_every_tile(code_dtype, block_t):
             check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, kernel=2, block_t=block_t,
                   splits=1, max_ctas=2)
             for splits in (2, 3, 4):
-                if -(-K // (128 if code_dtype == torch.int8 else 256)) >= splits:
+                if -(-K // 256) >= splits:
                     check(M, N, K, code_dtype, VALUE_TYPES[i], 31 * M + i, torch.float32, kernel=2,
                           block_t=block_t, splits=splits, y_extra=4 * (i % 2))
 

@@ -80,7 +80,29 @@ def test_norm_any_alignment(offset):
         assert float(buf[:, :offset].abs().max()) == 0.0
 
 
-@pytest.mark.parametrize("cols", [64, 1000, 4096, 8192])
+@pytest.mark.parametrize("cols", [5, 255, 257, 4099, 12501, 25001, 32765])
+@pytest.mark.parametrize("dtype", VALUE_TYPES)
+def test_loose_rows(dtype, cols):
+    """Rows of odd pitches, on every offset inside 16 bytes, narrow and too wide for two copies."""
+    x = values(1, 9 * (cols + 3), dtype, 20)[0].view(9, cols + 3)[:, :cols]
+    r = values(1, 9 * (cols + 1), dtype, 21)[0].view(9, cols + 1)[:, :cols]
+    weight = values(1, cols + 1, dtype, 22)[0, 1:]
+    for residual in (None, r):
+        q, scale, out = run_norm(x, weight, torch.float8_e4m3fn, residual)
+        h, y = norm64(x, weight, EPS, residual)
+        check_codes(q, scale, y, CODE_ERR, 2.0 ** -17, f"{cols}")
+        if residual is not None:
+            check_values(out, h, h.abs() * U)
+    q, scale, full = outputs(9, cols, torch.int8)
+    flat = values(1, 18 * cols + 1, dtype, 23)[0, 1:]
+    gate, up = flat[:9 * cols].view(9, cols), flat[9 * cols:].view(9, cols)
+    capi.silu_mul_q8_run(gate, up, q, scale)
+    check_guard(full, cols)
+    err = 2 * (float(gate.abs().max()) + 4) * U + 16 * U
+    check_codes(q, scale, act64(gate, up), 2 * err, err)
+
+
+@pytest.mark.parametrize("cols", [64, 1000, 1001, 4096, 8192])
 def test_norm_in_place(cols):
     """residual_out may be the residual or x itself."""
     for dtype in VALUE_TYPES:
