@@ -237,7 +237,7 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 // One block (of 32 to 1024 threads) or, for short rows, one warp holds a row, NV chunks a thread, and
 // takes every stride-th row. Up to two chunks a thread the next row's loads are issued before this
 // row is worked on: without that the memory waits for each block's reduction and stores (norm of
-// 8192 x 4096 bf16: 67.5 us with a block a row, FILL us so). Rows past 16384 columns take eight chunks
+// 8192 x 4096 bf16: 67.5 us with a block a row, 37.3 so). Rows past 16384 columns take eight chunks
 // a thread and no look-ahead, which their registers have no room for.
 template <typename T>
 constexpr int rows_max_threads(int nv) {  // 64 registers a thread, or 128
@@ -312,88 +312,82 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
   }
 }
 
-// Rows off the 16-byte grid (a base, a pitch or a weight). The aligned 16 bytes that hold a row's
-// first element up to those that hold its last are copied to shared memory asynchronously, one row
-// ahead, and read there element by element, consecutive ones by consecutive threads; what else those
-// bytes hold is not used (and they lie in the pages the row lies in). Read straight from global
-// memory by single elements, 1501 x 5001 fp32 took 16.6 us, FILL so.
-constexpr int kLooseThreads = 256;
-constexpr int kLooseMostSmem = 200 * 1024;
-
-template <typename T>
-__host__ __device__ inline int loose_window(int cols) {  // bytes of one row's copy
-  return (int)((cols * sizeof(T) + 15 + 15) / 16 * 16);
-}
-
+// Rows off the 16-byte grid (a base, a pitch or a weight): single elements, consecutive ones by
+// consecutive threads, kLoose a thread, held in registers and loaded one row ahead as above. A thread's
+// columns are the same in every row, so its weights are loaded once. (1501 x 5001 fp32: 16.6 us by the
+// kernel for wider rows below, 21 by 16-byte accesses shifted into place, 27 by asynchronous copies to
+// shared memory, 14.7 so: these rows are bound by instructions and the latency of one row's steps.)
+constexpr int kLoose = 8;
 template <typename T, bool kNorm>
-__global__ void __launch_bounds__(kLooseThreads) rows_q8_loose_kernel(const RowsParams p) {
-  extern __shared__ __align__(16) uint8_t loose_smem[];
+__global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const bool two = p.b != nullptr;
-  const int window = loose_window<T>(p.cols), buffer_bytes = two ? 2 * window : window;
-  // buffer i holds row blockIdx.x + j * gridDim.x for j = i, i + 2, ...
-  auto fetch = [&](const void* base, long long pitch, long long row, uint8_t* to) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * pitch);
-    const uintptr_t first = at & ~(uintptr_t)15;
-    const int n = (int)((at + p.cols * sizeof(T) + 15 - first) / 16);
-    for (int i = threadIdx.x; i < n; i += kLooseThreads)
-      cp_async_16_zfill(smem_u32(to + 16 * i), reinterpret_cast<const void*>(first + 16 * i), 16);
-  };
-  auto fetch_row = [&](long long row, int buffer) {
-    uint8_t* to = loose_smem + buffer * buffer_bytes;
-    fetch(p.a, p.a_pitch, row, to);
-    if (two) fetch(p.b, p.b_pitch, row, to + window);
-  };
-  auto in_buffer = [&](const void* base, long long pitch, long long row, const uint8_t* to) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * pitch);
-    return reinterpret_cast<const T*>(to + (at & 15));
-  };
-  int buffer = 0;
-  if (blockIdx.x < p.rows) fetch_row(blockIdx.x, 0);
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
-    cp_async_wait_all();
-    __syncthreads();  // this row is there, and nobody reads the other buffer's any more
-    if (row + gridDim.x < p.rows) fetch_row(row + gridDim.x, buffer ^ 1);
-    const uint8_t* from = loose_smem + buffer * buffer_bytes;
-    const T* a = in_buffer(p.a, p.a_pitch, row, from);
-    const T* b = in_buffer(p.b, p.b_pitch, row, from + window);
-    T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch;
-    // the value whose codes are written, from the copies: h * weight, or silu(gate) * up
-    auto value = [&](int c, float& h) {
-      h = q8_to_float(a[c]);
-      if (!kNorm) return silu_mul(h, q8_to_float(b[c]));
-      if (two) h += q8_to_float(b[c]);
-      return h * q8_load_value(p.weight, p.weight_type, c);
-    };
-    RowStat st{0.0f, 0u};
-#pragma unroll 4
-    for (int c = threadIdx.x; c < p.cols; c += kLooseThreads) {
-      float h;
-      st.amax = max(st.amax, __float_as_uint(value(c, h)) & 0x7FFFFFFFu);
-      if (kNorm) {
-        st.sum = fmaf(h, h, st.sum);
-        if (two) sum_out[c] = q8_from_float<T>(h);
-      }
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int mine = tid < p.cols ? (p.cols - tid + threads - 1) / threads : 0;  // columns
+  const bool two = !kNorm || p.b;
+  float w[kLoose];
+  if (kNorm) {
+#pragma unroll
+    for (int e = 0; e < kLoose; ++e)
+      w[e] = e < mine ? q8_load_value(p.weight, p.weight_type, tid + e * threads) : 0.0f;
+  }
+  T ra[kLoose], rb[kLoose];
+  auto load_row = [&](long long r) {
+    const T* a = static_cast<const T*>(p.a) + r * p.a_pitch + tid;
+    const T* b = static_cast<const T*>(p.b) + r * p.b_pitch + tid;
+#pragma unroll
+    for (int e = 0; e < kLoose; ++e) ra[e] = e < mine ? a[e * threads] : q8_from_float<T>(0.0f);
+    if (two) {
+#pragma unroll
+      for (int e = 0; e < kLoose; ++e) rb[e] = e < mine ? b[e * threads] : q8_from_float<T>(0.0f);
     }
-    st = row_reduce(st, kLooseThreads, buffer);
+  };
+  long long row = blockIdx.x;
+  if (row < p.rows) load_row(row);
+  for (int buffer = 0; row < p.rows; row += gridDim.x, buffer ^= 1) {
+    float v[kLoose];
+    RowStat st{0.0f, 0u};
+    T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch + tid;
+#pragma unroll
+    for (int e = 0; e < kLoose; ++e) {
+      v[e] = q8_to_float(ra[e]);
+      if (kNorm) {
+        if (two) {
+          v[e] += q8_to_float(rb[e]);
+          // this thread has read the column, if sum_out is x or the residual
+          if (e < mine) sum_out[e * threads] = q8_from_float<T>(v[e]);
+        }
+        st.sum = fmaf(v[e], v[e], st.sum);
+        v[e] *= w[e];
+      } else {
+        v[e] = silu_mul(v[e], q8_to_float(rb[e]));
+      }
+      st.amax = max(st.amax, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    }
+    if (row + gridDim.x < p.rows) load_row(row + gridDim.x);
+    st = row_reduce(st, threads, buffer);
     bool bad;
     const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
-    const RowCode rc = row_scale(st, gain, p, row, threadIdx.x == 0, bad);
-    uint8_t* q = p.q + row * p.q_pitch;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < p.cols; c += kLooseThreads) {
-      float h;
-      const float f[4] = {bad ? 0.0f : value(c, h) * rc.lift, 0.0f, 0.0f, 0.0f};
-      q[c] = (uint8_t)(p.code_type == Q8_E4M3 ? e4m3_codes(f, rc.inv) : int8_codes(f, rc.inv));
+    const RowCode rc = row_scale(st, gain, p, row, tid == 0, bad);
+    uint8_t* q = p.q + row * p.q_pitch + tid;
+#pragma unroll
+    for (int e = 0; e < kLoose; e += 4) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = bad ? 0.0f : v[e + i] * rc.lift;
+      const uint32_t codes = p.code_type == Q8_E4M3 ? e4m3_codes(f, rc.inv) : int8_codes(f, rc.inv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < mine) q[(e + i) * threads] = (uint8_t)(codes >> (8 * i));
     }
   }
 }
 
-// Such rows too wide for two copies in shared memory: single elements from global memory, the row's
-// values kept in shared memory between the two passes.
+// Such rows of more than 8192 columns: the row's values kept in shared memory between the two
+// passes.
+constexpr int kWideThreads = 256;
 template <typename T, bool kNorm>
-__global__ void __launch_bounds__(kLooseThreads) rows_q8_wide_loose_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kWideThreads) rows_q8_wide_loose_kernel(const RowsParams p) {
   extern __shared__ float v[];
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -404,11 +398,11 @@ __global__ void __launch_bounds__(kLooseThreads) rows_q8_wide_loose_kernel(const
     T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch;
     RowStat st{0.0f, 0u};
     constexpr int kBatch = 8;  // loads of one thread in flight
-    for (int c0 = threadIdx.x; c0 < p.cols; c0 += kBatch * kLooseThreads) {
+    for (int c0 = threadIdx.x; c0 < p.cols; c0 += kBatch * kWideThreads) {
       float x[kBatch], y[kBatch], w[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int c = c0 + j * kLooseThreads;
+        const int c = c0 + j * kWideThreads;
         const bool in = c < p.cols;
         x[j] = in ? q8_to_float(a[c]) : 0.0f;
         y[j] = in && b ? q8_to_float(b[c]) : 0.0f;
@@ -416,7 +410,7 @@ __global__ void __launch_bounds__(kLooseThreads) rows_q8_wide_loose_kernel(const
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const int c = c0 + j * kLooseThreads;
+        const int c = c0 + j * kWideThreads;
         if (c >= p.cols) break;
         float f;
         if (kNorm) {
@@ -431,12 +425,12 @@ __global__ void __launch_bounds__(kLooseThreads) rows_q8_wide_loose_kernel(const
         v[c] = f;  // read back by this thread alone
       }
     }
-    st = row_reduce(st, kLooseThreads, buffer);
+    st = row_reduce(st, kWideThreads, buffer);
     bool bad;
     const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
     const RowCode rc = row_scale(st, gain, p, row, threadIdx.x == 0, bad);
     uint8_t* q = p.q + row * p.q_pitch;
-    for (int c = threadIdx.x; c < p.cols; c += kLooseThreads) {
+    for (int c = threadIdx.x; c < p.cols; c += kWideThreads) {
       const float f[4] = {bad ? 0.0f : v[c] * rc.lift, 0.0f, 0.0f, 0.0f};
       q[c] = (uint8_t)(p.code_type == Q8_E4M3 ? e4m3_codes(f, rc.inv) : int8_codes(f, rc.inv));
     }
@@ -472,11 +466,12 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, 
 template <typename T, bool kNorm>
 static cudaError_t launch_typed(RowsParams& p, bool aligned, cudaStream_t stream) {
   if (!aligned) {
-    p.row_threads = kLooseThreads;
-    const int copies = 2 * (p.b ? 2 : 1) * loose_window<T>(p.cols);
-    if (copies <= kLooseMostSmem)
-      return launch_rows(rows_q8_loose_kernel<T, kNorm>, p, kLooseThreads, copies, stream);
-    return launch_rows(rows_q8_wide_loose_kernel<T, kNorm>, p, kLooseThreads,
+    if (p.cols <= 1024 * kLoose) {
+      p.row_threads = std::max(64, (p.cols + 32 * kLoose - 1) / (32 * kLoose) * 32);  // one row a block
+      return launch_rows(rows_q8_loose_kernel<T, kNorm>, p, p.row_threads, 0, stream);
+    }
+    p.row_threads = kWideThreads;
+    return launch_rows(rows_q8_wide_loose_kernel<T, kNorm>, p, kWideThreads,
                        p.cols * sizeof(float), stream);
   }
   // One chunk a thread where there are few rows, whose time is one row's latency; otherwise two.
