@@ -39,21 +39,23 @@ __device__ __forceinline__ void q8_store_value(void* p, int type, long long i, f
     static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// Sixteen int8 codes as f16 pairs in order. A code's byte with the sign bit flipped is u = code +
-// 128; under the exponent byte 0x64 it is the f16 1024 + u, and 1024 + u - 1152 = code exactly.
-__device__ __forceinline__ void int8_to_f16(const uint4& c, uint32_t* h) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+// Four int8 codes as f16 pairs in order. A code's byte with the sign bit flipped is u = code + 128;
+// under the exponent byte 0x64 it is the f16 1024 + u, and 1024 + u - 1152 = code exactly.
+__device__ __forceinline__ void int8_to_f16(uint32_t codes, uint32_t* h) {
   const __half2 bias = __floats2half2_rn(1152.0f, 1152.0f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = w[i] ^ 0x80808080u;
-    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140);
-    uint32_t hi = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
-    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
-    h[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
-    h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
-  }
+  const uint32_t u = codes ^ 0x80808080u;
+  const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140);
+  const uint32_t hi = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
+  const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
+  h[0] = *reinterpret_cast<const uint32_t*>(&a);
+  h[1] = *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void int8_to_f16(const uint4& c, uint32_t* h) {
+  int8_to_f16(c.x, h);
+  int8_to_f16(c.y, h + 2);
+  int8_to_f16(c.z, h + 4);
+  int8_to_f16(c.w, h + 6);
 }
 
 // y's element from its sum: scaled by token and channel, the bias added (0 without one).

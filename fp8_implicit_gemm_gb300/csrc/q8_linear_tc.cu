@@ -202,7 +202,7 @@ __device__ __forceinline__ void tc_epilogue(const LinearParams& p, const CUtenso
                                             uint32_t& boxes, Release release) {
   constexpr int kRows = kTcBoxBytes / (128 * (int)sizeof(Y));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool by_tma = p.y_tma && (n0 + 128 <= p.N || p.N * (int)sizeof(Y) % 16 == 0);
+  const bool by_tma = p.y_tma && (n0 + 128 <= p.N || (long long)p.N * (int)sizeof(Y) % 16 == 0);
   for (int c = 0; c < tokens; c += 32) {
     uint32_t r[32];
     tmem_ld_32x32b_x32(trow + c, r);
@@ -616,21 +616,33 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   if (warp == kTcMmaWarp) tmem_dealloc_pair(tmem_base, kTcTmemCols);
 }
 
-// x's int8 codes as f16, 16 a thread and step. The codes between K and the pitch's 16 are not read
-// later: the f16 matrix's map ends at K.
+// x's int8 codes as f16. A thread turns 8 codes into 16 bytes, so that a warp's stores fill whole
+// sectors, and has kExpand such loads on their way: bound by its 3 bytes of traffic a code. The codes
+// between K and the pitch's 16 are not read later: the f16 matrix's map ends at K.
+constexpr int kExpand = 4;
 __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int per_row = (p.K + 15) / 16;
-  const long long total = (long long)p.M * per_row;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-    const long long m = i / per_row;
-    const int c = (int)(i - m * per_row);
-    uint32_t h[8];
-    int8_to_f16(__ldg(reinterpret_cast<const uint4*>(p.x + m * p.x_pitch) + c), h);
-    uint4* dst = reinterpret_cast<uint4*>(p.xh + m * p.xh_pitch) + 2 * c;
-    dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  const int per_row = (p.K + 15) / 16 * 2;
+  const int row_blocks = (per_row + 256 * kExpand - 1) / (256 * kExpand);
+  const long long blocks = (long long)p.M * row_blocks;
+  for (long long i = blockIdx.x; i < blocks; i += gridDim.x) {
+    const long long m = i / row_blocks;
+    const int c0 = (int)(i - m * row_blocks) * 256 * kExpand + (int)threadIdx.x;
+    const uint2* from = reinterpret_cast<const uint2*>(p.x + m * p.x_pitch);
+    uint4* to = reinterpret_cast<uint4*>(p.xh + m * p.xh_pitch);
+    uint2 c[kExpand];
+#pragma unroll
+    for (int j = 0; j < kExpand; ++j)
+      c[j] = c0 + 256 * j < per_row ? __ldg(from + c0 + 256 * j) : make_uint2(0, 0);
+#pragma unroll
+    for (int j = 0; j < kExpand; ++j) {
+      if (c0 + 256 * j >= per_row) break;
+      uint32_t h[4];
+      int8_to_f16(c[j].x, h);
+      int8_to_f16(c[j].y, h + 2);
+      to[c0 + 256 * j] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
   }
 }
 
@@ -754,8 +766,9 @@ static cudaError_t launch_pdl(Kernel kernel, int grid, int block, int cluster, s
 }
 
 cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream) {
-  const long long total = (long long)p.M * ((p.K + 15) / 16);
-  const int grid = (int)std::min<long long>((total + 255) / 256, 152 * 8);
+  const long long per_row = (p.K + 15) / 16 * 2;
+  const long long blocks = p.M * ((per_row + 256 * kExpand - 1) / (256 * kExpand));
+  const int grid = (int)std::min<long long>(blocks, 152 * 8);
   return launch_pdl(linear_expand_kernel, grid, 256, 1, 0, stream, p);
 }
 
