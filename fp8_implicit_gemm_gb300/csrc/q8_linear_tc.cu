@@ -327,7 +327,9 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t slots_base = tmem_base + (uint32_t)(2 * p.block_t);
-  pdl_wait_primary();
+  // int8: the kernel before is the expansion of x, whose blocks let this one start only after they have
+  // waited for everything before them: w, the scales and y are ready, and only x's copies wait for it.
+  if (!kInt8) pdl_wait_primary();
   pdl_launch_dependents();
   const AbortState ab{abort_flag, p.status, p.timeout_ns};
 
@@ -445,6 +447,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       }
     } else if (kInt8) {
       // x as f16, for the MMAs of the pair
+      pdl_wait_primary();
       Ring slots;
       uint32_t it = 0;
       bool aborted = false;
