@@ -51,7 +51,7 @@ template <bool kInt8>
 constexpr int kTcTmaWarpOf = kInt8 ? kTcXWarp + 1 : 4;
 template <bool kInt8>
 constexpr int kTcThreads = (kTcTmaWarpOf<kInt8> + 2) * 32;
-// Warps quartets that share a box's rows by halves, and converter groups that take the boxes by turns.
+// Quartets of warps that share a box's rows by halves, and converter groups that take boxes by turns.
 template <int kBoxes>
 constexpr int kTcParts = kBoxes == 1 ? 2 : 1;
 template <int kBoxes>
@@ -327,9 +327,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t slots_base = tmem_base + (uint32_t)(2 * p.block_t);
-  // int8: the kernel before is the expansion of x, whose blocks let this one start only after they have
-  // waited for everything before them: w, the scales and y are ready, and only x's copies wait for it.
-  if (!kInt8) pdl_wait_primary();
+  pdl_wait_primary();
   pdl_launch_dependents();
   const AbortState ab{abort_flag, p.status, p.timeout_ns};
 
@@ -447,7 +445,6 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       }
     } else if (kInt8) {
       // x as f16, for the MMAs of the pair
-      pdl_wait_primary();
       Ring slots;
       uint32_t it = 0;
       bool aborted = false;
@@ -624,8 +621,8 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
 // between K and the pitch's 16 are not read later: the f16 matrix's map ends at K.
 constexpr int kExpand = 4;
 __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p) {
+  pdl_launch_dependents();  // the product's kernel sets itself up meanwhile
   pdl_wait_primary();
-  pdl_launch_dependents();
   const int per_row = (p.K + 15) / 16 * 2;
   const int row_blocks = (per_row + 256 * kExpand - 1) / (256 * kExpand);
   const long long blocks = (long long)p.M * row_blocks;
