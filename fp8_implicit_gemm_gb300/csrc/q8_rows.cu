@@ -312,73 +312,130 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
   }
 }
 
-// Rows off the 16-byte grid (a base, a pitch or a weight): single elements, consecutive ones by
-// consecutive threads, kLoose a thread, held in registers and loaded one row ahead as above. A thread's
-// columns are the same in every row, so its weights are loaded once. (1501 x 5001 fp32: 16.6 us by the
-// kernel for wider rows below, 21 by 16-byte accesses shifted into place, 27 by asynchronous copies to
-// shared memory, 14.7 so: these rows are bound by instructions and the latency of one row's steps.)
+// Rows off the 16-byte grid (a base, a pitch or a weight): single elements, 32 consecutive ones by a
+// warp at a time, kLoose a thread, held in registers and loaded one row ahead as above. A warp's columns
+// are a run of 32 * kLoose, the same in every row: its accesses are one address and constant offsets,
+// without a mask in all warps but the row's last, and its weights are loaded once. Bound by the issue of
+// instructions (1501 x 5001 fp32: 27 us by asynchronous copies to shared memory, 21 by 16-byte accesses
+// shifted into place, 14.7 with a block's whole width between a thread's elements, each address and mask
+// worked out, 11.1 so; 8192 x 4097 bf16 with a residual 117 -> 63 us, 3.7 TB/s).
 constexpr int kLoose = 8;
+
+// One element as it lies in memory, in a register of its own.
+template <typename T>
+struct LooseRaw {
+  uint32_t bits;
+  __device__ __forceinline__ void load(const T* p) {
+    if (sizeof(T) == 4)
+      bits = *reinterpret_cast<const uint32_t*>(p);
+    else
+      bits = *reinterpret_cast<const uint16_t*>(p);
+  }
+  __device__ __forceinline__ float value() const;
+};
+template <>
+__device__ __forceinline__ float LooseRaw<float>::value() const { return __uint_as_float(bits); }
+template <>
+__device__ __forceinline__ float LooseRaw<__nv_bfloat16>::value() const {
+  return __uint_as_float(bits << 16);
+}
+template <>
+__device__ __forceinline__ float LooseRaw<__half>::value() const {
+  return __half2float(__ushort_as_half((unsigned short)bits));
+}
+
 template <typename T, bool kNorm>
 __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int tid = threadIdx.x, threads = blockDim.x;
-  const int mine = tid < p.cols ? (p.cols - tid + threads - 1) / threads : 0;  // columns
+  const int col = (tid >> 5) * (32 * kLoose) + (tid & 31);
+  const int left = p.cols - col;                                      // e is in the row if 32 e < left
+  const bool whole = ((tid >> 5) + 1) * (32 * kLoose) <= p.cols;      // the same for a warp
   const bool two = !kNorm || p.b;
   float w[kLoose];
   if (kNorm) {
 #pragma unroll
     for (int e = 0; e < kLoose; ++e)
-      w[e] = e < mine ? q8_load_value(p.weight, p.weight_type, tid + e * threads) : 0.0f;
+      w[e] = 32 * e < left ? q8_load_value(p.weight, p.weight_type, col + 32 * e) : 0.0f;
   }
-  T ra[kLoose], rb[kLoose];
-  auto load_row = [&](long long r) {
-    const T* a = static_cast<const T*>(p.a) + r * p.a_pitch + tid;
-    const T* b = static_cast<const T*>(p.b) + r * p.b_pitch + tid;
+  LooseRaw<T> ra[kLoose] = {}, rb[kLoose] = {};  // 0 past the row's end, in every row
+  auto load_run = [&](const T* src, LooseRaw<T>(&r)[kLoose]) {
+    if (whole) {
 #pragma unroll
-    for (int e = 0; e < kLoose; ++e) ra[e] = e < mine ? a[e * threads] : q8_from_float<T>(0.0f);
-    if (two) {
+      for (int e = 0; e < kLoose; ++e) r[e].load(src + 32 * e);
+    } else {
 #pragma unroll
-      for (int e = 0; e < kLoose; ++e) rb[e] = e < mine ? b[e * threads] : q8_from_float<T>(0.0f);
+      for (int e = 0; e < kLoose; ++e)
+        if (32 * e < left) r[e].load(src + 32 * e);
     }
+  };
+  auto load_row = [&](long long r) {
+    load_run(static_cast<const T*>(p.a) + r * p.a_pitch + col, ra);
+    if (two) load_run(static_cast<const T*>(p.b) + r * p.b_pitch + col, rb);
   };
   long long row = blockIdx.x;
   if (row < p.rows) load_row(row);
   for (int buffer = 0; row < p.rows; row += gridDim.x, buffer ^= 1) {
     float v[kLoose];
     RowStat st{0.0f, 0u};
-    T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch + tid;
 #pragma unroll
-    for (int e = 0; e < kLoose; ++e) {
-      v[e] = q8_to_float(ra[e]);
-      if (kNorm) {
-        if (two) {
-          v[e] += q8_to_float(rb[e]);
-          // this thread has read the column, if sum_out is x or the residual
-          if (e < mine) sum_out[e * threads] = q8_from_float<T>(v[e]);
+    for (int e = 0; e < kLoose; ++e) v[e] = ra[e].value();
+    if (kNorm) {
+      if (two) {
+        T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch + col;
+#pragma unroll
+        for (int e = 0; e < kLoose; ++e) v[e] += rb[e].value();
+        // this thread has read these columns, if sum_out is x or the residual
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < kLoose; ++e) sum_out[32 * e] = q8_from_float<T>(v[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kLoose; ++e)
+            if (32 * e < left) sum_out[32 * e] = q8_from_float<T>(v[e]);
         }
+      }
+#pragma unroll
+      for (int e = 0; e < kLoose; ++e) {
         st.sum = fmaf(v[e], v[e], st.sum);
         v[e] *= w[e];
-      } else {
-        v[e] = silu_mul(v[e], q8_to_float(rb[e]));
       }
-      st.amax = max(st.amax, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLoose; ++e) v[e] = silu_mul(v[e], rb[e].value());
     }
+#pragma unroll
+    for (int e = 0; e < kLoose; ++e) st.amax = max(st.amax, __float_as_uint(v[e]) & 0x7FFFFFFFu);
     if (row + gridDim.x < p.rows) load_row(row + gridDim.x);
     st = row_reduce(st, threads, buffer);
     bool bad;
     const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
     const RowCode rc = row_scale(st, gain, p, row, tid == 0, bad);
-    uint8_t* q = p.q + row * p.q_pitch + tid;
+    if (bad) {
 #pragma unroll
-    for (int e = 0; e < kLoose; e += 4) {
-      float f[4];
+      for (int e = 0; e < kLoose; ++e) v[e] = 0.0f;
+    }
+    if (rc.lift != 1.0f) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = bad ? 0.0f : v[e + i] * rc.lift;
-      const uint32_t codes = p.code_type == Q8_E4M3 ? e4m3_codes(f, rc.inv) : int8_codes(f, rc.inv);
+      for (int e = 0; e < kLoose; ++e) v[e] *= rc.lift;
+    }
+    uint32_t codes[kLoose / 4];
+    if (p.code_type == Q8_E4M3) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (e + i < mine) q[(e + i) * threads] = (uint8_t)(codes >> (8 * i));
+      for (int e = 0; e < kLoose; e += 4) codes[e / 4] = e4m3_codes(v + e, rc.inv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLoose; e += 4) codes[e / 4] = int8_codes(v + e, rc.inv);
+    }
+    uint8_t* q = p.q + row * p.q_pitch + col;
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e < kLoose; ++e) q[32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3)));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLoose; ++e)
+        if (32 * e < left) q[32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3)));
     }
   }
 }
