@@ -344,6 +344,33 @@ __device__ __forceinline__ float LooseRaw<__half>::value() const {
   return __half2float(__ushort_as_half((unsigned short)bits));
 }
 
+// f(e) for a thread's elements of a run of which `left` columns from its first one on are in the row;
+// the mask only where the run holds the row's end.
+template <bool kWhole, typename F>
+__device__ __forceinline__ void for_run(int left, F f) {
+#pragma unroll
+  for (int e = 0; e < kLoose; ++e)
+    if (kWhole || 32 * e < left) f(e);
+}
+template <typename F>
+__device__ __forceinline__ void for_run(bool whole, int left, F f) {
+  if (whole)
+    for_run<true>(left, f);
+  else
+    for_run<false>(left, f);
+}
+
+__device__ __forceinline__ void loose_codes(const float* f, int code_type, float inv,
+                                            uint32_t* codes) {
+  if (code_type == Q8_E4M3) {
+#pragma unroll
+    for (int e = 0; e < kLoose; e += 4) codes[e / 4] = e4m3_codes(f + e, inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kLoose; e += 4) codes[e / 4] = int8_codes(f + e, inv);
+  }
+}
+
 template <typename T, bool kNorm>
 __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p) {
   pdl_wait_primary();
@@ -361,14 +388,7 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
   }
   LooseRaw<T> ra[kLoose] = {}, rb[kLoose] = {};  // 0 past the row's end, in every row
   auto load_run = [&](const T* src, LooseRaw<T>(&r)[kLoose]) {
-    if (whole) {
-#pragma unroll
-      for (int e = 0; e < kLoose; ++e) r[e].load(src + 32 * e);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kLoose; ++e)
-        if (32 * e < left) r[e].load(src + 32 * e);
-    }
+    for_run(whole, left, [&](int e) { r[e].load(src + 32 * e); });
   };
   auto load_row = [&](long long r) {
     load_run(static_cast<const T*>(p.a) + r * p.a_pitch + col, ra);
@@ -387,14 +407,7 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
 #pragma unroll
         for (int e = 0; e < kLoose; ++e) v[e] += rb[e].value();
         // this thread has read these columns, if sum_out is x or the residual
-        if (whole) {
-#pragma unroll
-          for (int e = 0; e < kLoose; ++e) sum_out[32 * e] = q8_from_float<T>(v[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kLoose; ++e)
-            if (32 * e < left) sum_out[32 * e] = q8_from_float<T>(v[e]);
-        }
+        for_run(whole, left, [&](int e) { sum_out[32 * e] = q8_from_float<T>(v[e]); });
       }
 #pragma unroll
       for (int e = 0; e < kLoose; ++e) {
@@ -421,75 +434,97 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
       for (int e = 0; e < kLoose; ++e) v[e] *= rc.lift;
     }
     uint32_t codes[kLoose / 4];
-    if (p.code_type == Q8_E4M3) {
-#pragma unroll
-      for (int e = 0; e < kLoose; e += 4) codes[e / 4] = e4m3_codes(v + e, rc.inv);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kLoose; e += 4) codes[e / 4] = int8_codes(v + e, rc.inv);
-    }
+    loose_codes(v, p.code_type, rc.inv, codes);
     uint8_t* q = p.q + row * p.q_pitch + col;
-    if (whole) {
-#pragma unroll
-      for (int e = 0; e < kLoose; ++e) q[32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3)));
-    } else {
-#pragma unroll
-      for (int e = 0; e < kLoose; ++e)
-        if (32 * e < left) q[32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3)));
-    }
+    for_run(whole, left, [&](int e) { q[32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3))); });
   }
 }
 
 // Such rows of more than 8192 columns: the row's values kept in shared memory between the two
-// passes.
-constexpr int kWideThreads = 256;
+// passes, a warp working on runs of 32 * kLoose columns as above (2000 x 12001 bf16 with a residual 143 us
+// with single elements of a block's whole width, 47 so, 3.6 TB/s; 60 with 1024 threads, which leave one
+// block an SM; with 256 threads wide rows leave too few warps: 16383 columns 75 us against 56).
+constexpr int kWideThreads = 512;
+
+template <typename T, bool kNorm, bool kWhole>
+__device__ __forceinline__ void wide_run(const T* a, const T* b, T* sum_out, const RowsParams& p,
+                                         int col, float* v, RowStat& st) {
+  const int left = p.cols - col;
+  LooseRaw<T> ra[kLoose] = {}, rb[kLoose] = {};
+  float w[kLoose];
+  for_run<kWhole>(left, [&](int e) { ra[e].load(a + col + 32 * e); });
+  if (b) for_run<kWhole>(left, [&](int e) { rb[e].load(b + col + 32 * e); });
+  if (kNorm) {
+    if (p.weight_type == Q8_F32) {
+      const float* g = static_cast<const float*>(p.weight) + col;
+      for_run<kWhole>(left, [&](int e) { w[e] = g[32 * e]; });
+    } else if (p.weight_type == Q8_BF16) {
+      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.weight) + col;
+      for_run<kWhole>(left, [&](int e) { w[e] = q8_to_float(g[32 * e]); });
+    } else {
+      const __half* g = static_cast<const __half*>(p.weight) + col;
+      for_run<kWhole>(left, [&](int e) { w[e] = q8_to_float(g[32 * e]); });
+    }
+  }
+  for_run<kWhole>(left, [&](int e) {
+    float f = ra[e].value();
+    if (kNorm) {
+      if (b) {
+        f += rb[e].value();
+        sum_out[col + 32 * e] = q8_from_float<T>(f);  // read by this thread, if x or the residual
+      }
+      st.sum = fmaf(f, f, st.sum);
+      f *= w[e];
+    } else {
+      f = silu_mul(f, rb[e].value());
+    }
+    st.amax = max(st.amax, __float_as_uint(f) & 0x7FFFFFFFu);
+    v[col + 32 * e] = f;  // read back by this thread alone
+  });
+}
+
+template <bool kWhole>
+__device__ __forceinline__ void wide_codes(uint8_t* q, const RowsParams& p, int col, const float* v,
+                                           bool bad, const RowCode& rc) {
+  const int left = p.cols - col;
+  float f[kLoose] = {};
+  for_run<kWhole>(left, [&](int e) { f[e] = bad ? 0.0f : v[col + 32 * e] * rc.lift; });
+  uint32_t codes[kLoose / 4];
+  loose_codes(f, p.code_type, rc.inv, codes);
+  for_run<kWhole>(left, [&](int e) {
+    q[col + 32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3)));
+  });
+}
+
 template <typename T, bool kNorm>
 __global__ void __launch_bounds__(kWideThreads) rows_q8_wide_loose_kernel(const RowsParams p) {
   extern __shared__ float v[];
   pdl_wait_primary();
   pdl_launch_dependents();
+  constexpr int kRun = 32 * kLoose;
+  const int first = (threadIdx.x >> 5) * kRun, lane = threadIdx.x & 31;
   int buffer = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
     const T* a = static_cast<const T*>(p.a) + row * p.a_pitch;
     const T* b = p.b ? static_cast<const T*>(p.b) + row * p.b_pitch : nullptr;
     T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch;
     RowStat st{0.0f, 0u};
-    constexpr int kBatch = 8;  // loads of one thread in flight
-    for (int c0 = threadIdx.x; c0 < p.cols; c0 += kBatch * kWideThreads) {
-      float x[kBatch], y[kBatch], w[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int c = c0 + j * kWideThreads;
-        const bool in = c < p.cols;
-        x[j] = in ? q8_to_float(a[c]) : 0.0f;
-        y[j] = in && b ? q8_to_float(b[c]) : 0.0f;
-        w[j] = in && kNorm ? q8_load_value(p.weight, p.weight_type, c) : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int c = c0 + j * kWideThreads;
-        if (c >= p.cols) break;
-        float f;
-        if (kNorm) {
-          const float h = x[j] + y[j];
-          if (b) sum_out[c] = q8_from_float<T>(h);  // read by this thread, if x or the residual
-          st.sum = fmaf(h, h, st.sum);
-          f = h * w[j];
-        } else {
-          f = silu_mul(x[j], y[j]);
-        }
-        st.amax = max(st.amax, __float_as_uint(f) & 0x7FFFFFFFu);
-        v[c] = f;  // read back by this thread alone
-      }
+    for (int c = first; c < p.cols; c += kWideThreads * kLoose) {
+      if (c + kRun <= p.cols)
+        wide_run<T, kNorm, true>(a, b, sum_out, p, c + lane, v, st);
+      else
+        wide_run<T, kNorm, false>(a, b, sum_out, p, c + lane, v, st);
     }
     st = row_reduce(st, kWideThreads, buffer);
     bool bad;
     const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
     const RowCode rc = row_scale(st, gain, p, row, threadIdx.x == 0, bad);
     uint8_t* q = p.q + row * p.q_pitch;
-    for (int c = threadIdx.x; c < p.cols; c += kWideThreads) {
-      const float f[4] = {bad ? 0.0f : v[c] * rc.lift, 0.0f, 0.0f, 0.0f};
-      q[c] = (uint8_t)(p.code_type == Q8_E4M3 ? e4m3_codes(f, rc.inv) : int8_codes(f, rc.inv));
+    for (int c = first; c < p.cols; c += kWideThreads * kLoose) {
+      if (c + kRun <= p.cols)
+        wide_codes<true>(q, p, c + lane, v, bad, rc);
+      else
+        wide_codes<false>(q, p, c + lane, v, bad, rc);
     }
   }
 }
