@@ -114,7 +114,7 @@ bool encode_rows(CUtensorMap* map, const void* base, int elem, long long rows, l
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// y, stored in boxes of 128 channels by as many tokens as make 8 KB; what lies outside is dropped.
+// y, stored in boxes of 32 channels by as many tokens as make 2 KB; what lies outside is dropped.
 bool encode_y(CUtensorMap* map, void* y, int y_type, long long rows, long long cols,
               long long pitch) {
   const EncodeTiledFn enc = encode_tiled();
@@ -122,7 +122,7 @@ bool encode_y(CUtensorMap* map, void* y, int y_type, long long rows, long long c
   const int elem = value_bytes(y_type);
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(pitch * elem)};
-  const cuuint32_t box[2] = {128, (cuuint32_t)(kTcYBoxBytes / (128 * elem))};
+  const cuuint32_t box[2] = {32, (cuuint32_t)(kTcYBoxBytes / (32 * elem))};
   const cuuint32_t estr[2] = {1, 1};
   const CUtensorMapDataType type = y_type == Q8_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : y_type == Q8_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

@@ -84,8 +84,8 @@ struct TcLimits {
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim);
 // Boxes of the tensor maps: rows of w one CTA loads at a time (of x: half of block_t).
 constexpr int kTcWBoxRows = 128;
-// The box of y's map: 128 channels of 8 KB's worth of tokens.
-constexpr int kTcYBoxBytes = 8192;
+// The box of y's map: 32 channels (a warp) of 2 KB worth of tokens.
+constexpr int kTcYBoxBytes = 2048;
 cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream);  // x -> xh
 cudaError_t linear_tc_setup();         // the kernels' shared-memory grant
 cudaError_t linear_tc_max_clusters(int (&clusters)[kTcMaxSplits]);

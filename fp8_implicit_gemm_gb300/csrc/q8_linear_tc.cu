@@ -64,8 +64,11 @@ constexpr int kTcSlotCols = kTcBlockK / 2;          // a box of w as f16 in TMEM
 constexpr int kTcDepth = 8;                         // K blocks under way: no ring is deeper
 constexpr uint64_t kTcAbortSettleNs = 2ull * 1000 * 1000;  // let copies in flight land on abort
 
-constexpr int kTcBoxBytes = kTcYBoxBytes;           // one staging buffer of the epilogue
+constexpr int kTcBoxBytes = kTcYBoxBytes;           // one staging buffer of an epilogue warp
+constexpr int kTcStaging = 4 * 2 * kTcBoxBytes;     // (two boxes of 4 KB and 16 bytes a row otherwise)
 constexpr int kTcBars = 2 * kTcMaxStages + 2 * kTcDepth + 5;
+constexpr int kTcBarBytes = 512;                    // barriers, the TMEM address, the abort flag
+static_assert(kTcBars * 8 + 8 <= kTcBarBytes);
 
 // wait_bounded_warp with less in the way of the next try: the timer, whose read takes several hundred
 // cycles, and the abort flag are looked at after every 64 misses.
@@ -97,6 +100,12 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const Abo
 // stage (e4m3) or a slot (int8) of x is two.
 __host__ __device__ inline uint32_t tc_x_bytes(int block_t) {
   return (uint32_t)(block_t / 2) * kTcBlockK;
+}
+
+// What lies in shared memory before the stages, which start on 1024 bytes: the barriers, the staging
+// of the epilogue, the scales of two tiles' tokens.
+__host__ __device__ inline uint32_t tc_head_bytes(int block_t) {
+  return (uint32_t)(kTcBarBytes + kTcStaging + 2 * block_t * 4 + 1023) & ~1023u;
 }
 
 // One work unit: a tile and a slice [kb0, kb1) of the K blocks. Tiles are taken in groups of
@@ -187,58 +196,117 @@ __device__ __forceinline__ void tc_join(const LinearParams& p, const TcTile& t, 
   }
 }
 
-// The epilogue of one tile in one CTA, for its four epilogue warps: thread = channel. 8 KB of the
-// tile at a time (32 tokens of a 16-bit y, 16 of an fp32 one) are staged in shared memory as
-// [token][128 channels], in two buffers by turns (`boxes` counts them), and leave by a TMA store
-// that y's extents bound, or by stores of whole token rows: for a y off the 16-byte grid, and for
-// the last channels of a y whose rows end inside 16 bytes (a TMA store was seen to write the
-// whole of the 16 bytes that hold a row's last element). Stored
-// straight from the accumulator's lanes, 64 bytes a warp, the 67 MB of y of an e4m3 product of 4096 x
-// 8192 x 4096 took 26 of its 105 us. `release` is called once the accumulator has been read.
+// `rows` rows of y from the staging of the four epilogue warps, for a y off the 16-byte grid. A row's
+// 128 channels are staged kShiftPitch bytes apart, as far behind a 16-byte boundary as in y, so that
+// both divide into the same 16-byte chunks: one at each end that the row shares with its neighbours
+// (as many elements as one chunk together, stored one by one) and those between.
+template <typename Y>
+constexpr int kShiftPitch = 128 * (int)sizeof(Y) + 16;
+template <typename Y>
+constexpr int kShiftRows = 4096 / (128 * (int)sizeof(Y));
+__device__ __forceinline__ uint32_t behind16(const void* p) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+}
+template <typename Y>
+__device__ __forceinline__ void store_shifted(Y* first, long long pitch, int rows,
+                                              const uint8_t* buf) {
+  constexpr int kEdge = 16 / (int)sizeof(Y), kChunks = 128 / kEdge;
+#pragma unroll
+  for (int i = threadIdx.x; i < kShiftRows<Y> * kChunks; i += 128) {
+    const int j = i / kChunks, chunk = i % kChunks;
+    if (j >= rows || chunk == 0) continue;
+    uint8_t* row = reinterpret_cast<uint8_t*>(first + j * pitch);
+    *reinterpret_cast<uint4*>(row - behind16(row) + 16 * chunk) =
+        *reinterpret_cast<const uint4*>(buf + j * kShiftPitch<Y> + 16 * chunk);
+  }
+#pragma unroll
+  for (int i = threadIdx.x; i < kShiftRows<Y> * kEdge; i += 128) {
+    const int j = i / kEdge, e = i % kEdge;
+    if (j >= rows) continue;
+    Y* row = first + j * pitch;
+    const int behind = (int)behind16(row);
+    const int channel = e * (int)sizeof(Y) < 16 - behind ? e : 128 - kEdge + e;
+    row[channel] = *reinterpret_cast<const Y*>(buf + j * kShiftPitch<Y> + behind +
+                                               channel * (int)sizeof(Y));
+  }
+}
+
+// One warp's part of the epilogue of a tile: a channel a lane, channels n0 .. n0 + 31. 32 tokens of a
+// 16-bit y, 16 of an fp32 one, are staged in shared memory as [token][32 channels], in the warp's two
+// buffers by turns (`boxes` counts them), and leave by a TMA store that y's extents bound. A y off the
+// 16-byte grid is staged by the four warps together and stored as above; the last channels of a y
+// whose rows end inside 16 bytes leave straight from the lanes (a TMA store was seen to write the
+// whole of the 16 bytes that hold a row's last element). With all of y stored from the lanes, 64 bytes
+// a warp, the 67 MB of an e4m3 product of 4096 x 8192 x 4096 took 26 of its 105 us. `release` is called
+// once the accumulator has been read.
 template <typename Y, typename Release>
 __device__ __forceinline__ void tc_epilogue(const LinearParams& p, const CUtensorMap* ymap,
                                             uint32_t trow, const float* scale, ScaleBias sc,
                                             int tokens, long long m0, int n0, uint8_t* staging,
                                             uint32_t& boxes, Release release) {
-  constexpr int kRows = kTcBoxBytes / (128 * (int)sizeof(Y));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool by_tma = p.y_tma && (n0 + 128 <= p.N || (long long)p.N * (int)sizeof(Y) % 16 == 0);
+  constexpr int kRows = kTcBoxBytes / (32 * (int)sizeof(Y));
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const bool by_tma = p.y_tma && (n0 + 32 <= p.N || (long long)p.N * (int)sizeof(Y) % 16 == 0);
+  const bool shifted = !p.y_tma && n0 - 32 * warp + 128 <= p.N;  // the same for the four warps
+  uint8_t* own = staging + warp * 2 * kTcBoxBytes;
   for (int c = 0; c < tokens; c += 32) {
     uint32_t r[32];
     tmem_ld_32x32b_x32(trow + c, r);
     tmem_ld_wait();
     if (c + 32 >= tokens) release();
+    if (n0 >= p.N) continue;
+    float v[32];  // before the first store: the compiler cannot tell the staging from the scales
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 sx = *reinterpret_cast<const float4*>(scale + c + j);
+      v[j] = sc(__uint_as_float(r[j]), sx.x);
+      v[j + 1] = sc(__uint_as_float(r[j + 1]), sx.y);
+      v[j + 2] = sc(__uint_as_float(r[j + 2]), sx.z);
+      v[j + 3] = sc(__uint_as_float(r[j + 3]), sx.w);
+    }
+    if (shifted) {
+      constexpr int kStep = kShiftRows<Y>;
+      Y* first = static_cast<Y*>(p.y) + (m0 + c) * p.y_pitch + (n0 - 32 * warp);
+#pragma unroll
+      for (int h = 0; h < 32; h += kStep) {
+        if (c + h >= tokens) break;
+        uint8_t* buf = staging + (boxes++ & 1u) * (kStep * kShiftPitch<Y>);
+#pragma unroll
+        for (int j = 0; j < kStep; ++j)
+          *reinterpret_cast<Y*>(buf + j * kShiftPitch<Y> + behind16(first + (h + j) * p.y_pitch) +
+                                threadIdx.x * (int)sizeof(Y)) = q8_from_float<Y>(v[h + j]);
+        // the other buffer is written once every warp is past this barrier, and so has read it
+        named_barrier_sync(1, 128);
+        store_shifted<Y>(first + h * p.y_pitch, p.y_pitch, min(kStep, tokens - c - h), buf);
+      }
+      continue;
+    }
+    if (!by_tma) {
+      Y* dst = static_cast<Y*>(p.y) + (m0 + c) * p.y_pitch + n0 + lane;
+      if (n0 + lane < p.N) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (c + j < tokens)
+            dst[j * p.y_pitch] = q8_from_float<Y>(v[j]);
+      }
+      continue;
+    }
 #pragma unroll
     for (int h = 0; h < 32; h += kRows) {
       if (c + h >= tokens) break;
-      uint8_t* buf = staging + (boxes & 1u) * kTcBoxBytes;
-      if (threadIdx.x == 0) bulk_wait_group_read<1>();  // the store from this buffer, two boxes ago
-      named_barrier_sync(1, 128);
+      uint8_t* buf = own + (boxes++ & 1u) * kTcBoxBytes;
+      if (lane == 0) bulk_wait_group_read<1>();  // the store from this buffer, two boxes ago
+      __syncwarp();
+      Y* to = reinterpret_cast<Y*>(buf) + lane;
 #pragma unroll
-      for (int j = 0; j < kRows; j += 4) {
-        const float4 sx = *reinterpret_cast<const float4*>(scale + c + h + j);
-        Y* to = reinterpret_cast<Y*>(buf) + j * 128 + threadIdx.x;
-        to[0] = q8_from_float<Y>(sc(__uint_as_float(r[h + j]), sx.x));
-        to[128] = q8_from_float<Y>(sc(__uint_as_float(r[h + j + 1]), sx.y));
-        to[256] = q8_from_float<Y>(sc(__uint_as_float(r[h + j + 2]), sx.z));
-        to[384] = q8_from_float<Y>(sc(__uint_as_float(r[h + j + 3]), sx.w));
+      for (int j = 0; j < kRows; ++j) to[32 * j] = q8_from_float<Y>(v[h + j]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(ymap, smem_u32(buf), n0, (int)m0 + c + h);
+        bulk_commit_group();
       }
-      if (by_tma) fence_proxy_async_smem();
-      named_barrier_sync(1, 128);
-      if (threadIdx.x == 0) {
-        if (by_tma && n0 < p.N) tma_store_2d(ymap, smem_u32(buf), n0, (int)m0 + c + h);
-        bulk_commit_group();  // one a box, empty or not: the wait above counts them
-      }
-      if (!by_tma) {
-        const int rows = min(kRows, tokens - c - h);
-        for (int j = warp; j < rows; j += 4) {
-          Y* dst = static_cast<Y*>(p.y) + (m0 + c + h + j) * p.y_pitch + n0;
-#pragma unroll
-          for (int i = lane; i < 128; i += 32)
-            if (n0 + i < p.N) dst[i] = reinterpret_cast<const Y*>(buf)[j * 128 + i];
-        }
-      }
-      ++boxes;
     }
   }
 }
@@ -258,12 +326,12 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
   constexpr uint32_t kWStage = kInt8 ? kTcWBytes : 2 * kTcWBytes;
   const uint32_t x_step = (uint32_t)kBoxes * (kInt8 ? 2u : 1u) * tc_x_bytes(p.block_t);
   const uint32_t x_bytes = tc_x_bytes(p.block_t);
-  uint8_t* sW = smem;
-  uint8_t* sX = smem + (size_t)S * kWStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+  uint8_t* sBox = smem + kTcBarBytes;                                // the epilogue's staging
+  float* sScale = reinterpret_cast<float*>(sBox + kTcStaging);       // [2][block_t]
+  uint8_t* sW = smem + tc_head_bytes(p.block_t);
   // x's tiles: codes in the stages (e4m3), or f16 in slots of their own
-  uint8_t* sBox = sX + (size_t)(kInt8 ? p.x_slots : S) * x_step;  // the epilogue's staging
-  float* sScale = reinterpret_cast<float*>(sBox + 2 * kTcBoxBytes);  // [kTcMaxTokens]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sScale + kTcMaxTokens);
+  uint8_t* sX = sW + (size_t)S * kWStage;
   // Barriers (those marked L: the leader's are used). full[S]: a stage's copies have landed (e4m3 L:
   // both CTAs'; int8: this CTA's). empty[S]: read by the MMAs (e4m3) or the converters (int8).
   // int8, for K block i of all, at i % kTcDepth: ready L: its w and x are there as f16. done: its MMAs
@@ -340,15 +408,17 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       const long long n = (long long)un.n_tile * kTcChannels + rank * 128 + threadIdx.x;
       const long long m0 = (long long)un.m_tile * p.block_t;
       const int tokens = (int)min((long long)p.block_t, p.M - m0);
-      // the tile before has been read: its last box's barriers lie behind every warp
+      // the scales of the tile before the last: that tile lies behind every warp that has come to
+      // the last one's barrier
+      float* scale = sScale + acc.stage * p.block_t;
       for (int t = threadIdx.x; t < p.block_t; t += 128)
-        sScale[t] = t < tokens ? p.scale_x[m0 + t] : 0.0f;
+        scale[t] = t < tokens ? p.scale_x[m0 + t] : 0.0f;
       ScaleBias sc{0.0f, 0.0f};
       if (n < p.N) {
         sc.w = __ldg(p.scale_w + n);
         if (p.bias) sc.bias = q8_load_value(p.bias, p.bias_type, n);
       }
-      // the four warps go on or stop together: they share the staging buffers
+      // the four warps go on or stop together: they share the tokens' scales
       const bool ok = tc_wait(acc_full(acc.stage), acc.phase, ab, kStatusWaitAccFull);
       if (!named_barrier_and(1, 128, ok)) break;
       tc_fence_after();
@@ -359,7 +429,7 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         if (lane == 0)
           mbar_arrive_cluster_tmem(leader_bars + (acc_empty(acc.stage) - bars_u32));
       };
-      const int n0 = un.n_tile * kTcChannels + (int)rank * 128;
+      const int n0 = un.n_tile * kTcChannels + (int)rank * 128 + warp * 32;
       if (p.splits > 1) {
         // the pipeline's stages are free: every copy of this pair has been consumed
         float* part = reinterpret_cast<float*>(sW) + threadIdx.x;
@@ -372,15 +442,15 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
         }
         release();
       } else if (p.y_type == Q8_F32) {
-        tc_epilogue<float>(p, &ymap, trow, sScale, sc, tokens, m0, n0, sBox, boxes, release);
+        tc_epilogue<float>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
       } else if (p.y_type == Q8_BF16) {
-        tc_epilogue<__nv_bfloat16>(p, &ymap, trow, sScale, sc, tokens, m0, n0, sBox, boxes, release);
+        tc_epilogue<__nv_bfloat16>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
       } else {
-        tc_epilogue<__half>(p, &ymap, trow, sScale, sc, tokens, m0, n0, sBox, boxes, release);
+        tc_epilogue<__half>(p, &ymap, trow, scale, sc, tokens, m0, n0, sBox, boxes, release);
       }
       acc.next(2);
     }
-    if (threadIdx.x == 0) bulk_wait_group_all();  // the stores have read their buffers
+    if (lane == 0) bulk_wait_group_all();  // the stores have read their buffers
   } else if (warp < kTcTmaWarp) {
     // ---------------------------------------------------------------------------- converters
     if (kInt8 && warp < kTcXWarp) {
@@ -391,57 +461,48 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
       const int part = kParts == 2 ? ((warp - 4) >> 2) & 1 : 0;
       const int row = quad * 32 + lane;
       const uint32_t dst0 = slots_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(32 * part);
-      const uint32_t num_boxes = (uint32_t)((kb1 - kb0) * kBoxes);  // of a tile
       const uint32_t w_slots = (uint32_t)p.w_slots;
       // The boxes of all tiles are counted through; this group takes every kGroups-th. The number of
       // stages is a multiple of that, so a stage is always the same group's: were it another's next,
       // that group could come to wait for a phase two ahead of the barrier's, which a parity cannot
       // tell from one that is over.
       uint32_t box = group, stage = group, stage_phase = 0, slot = group % w_slots;
-      uint32_t end = 0;
-      bool aborted = false;
-      for (int u = first_tile; u < num_tiles && !aborted; u += tile_step) {
-        end += num_boxes;
-        for (; box < end; box += kGroups) {
-          const uint32_t step = box / kBoxes;
-          if (!tc_wait(full((int)stage), stage_phase, ab, kStatusWaitFull)) {
-            aborted = true;
-            break;
-          }
-          const uint8_t* src = sW + stage * kWStage + row * kTcBlockK;
-          uint4 c[kChunks];
+      const uint32_t tiles =
+          first_tile < num_tiles ? (uint32_t)((num_tiles - 1 - first_tile) / tile_step + 1) : 0u;
+      const uint32_t end = tiles * (uint32_t)((kb1 - kb0) * kBoxes);
+      for (; box < end; box += kGroups) {
+        const uint32_t step = box / kBoxes;
+        if (!tc_wait(full((int)stage), stage_phase, ab, kStatusWaitFull)) break;
+        const uint8_t* src = sW + stage * kWStage + row * kTcBlockK;
+        uint4 c[kChunks];
 #pragma unroll
-          for (int i = 0; i < kChunks; ++i)  // 16-byte chunk i, where the swizzle put it
-            c[i] = *reinterpret_cast<const uint4*>(src + (((kChunks * part + i) ^ (row & 7)) << 4));
-          uint32_t h[kChunks / 4][32];  // the codes as f16, before their slot is free
+        for (int i = 0; i < kChunks; ++i)  // 16-byte chunk i, where the swizzle put it
+          c[i] = *reinterpret_cast<const uint4*>(src + (((kChunks * part + i) ^ (row & 7)) << 4));
+        uint32_t h[kChunks / 4][32];  // the codes as f16, before their slot is free
 #pragma unroll
-          for (int i = 0; i < kChunks; ++i) int8_to_f16(c[i], h[i / 4] + 8 * (i % 4));
-          __syncwarp();  // every lane has its codes
-          if (lane == 0) mbar_arrive(empty((int)stage));
-          // the K block that had this slot
-          if (box >= w_slots) {
-            const uint32_t before = (box - w_slots) / kBoxes;
-            if (!tc_wait(done(before), parity(before), ab, kStatusWaitEmpty)) {
-              aborted = true;
-              break;
-            }
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < kChunks / 4; ++i)
-            tmem_st_32x32b_x32(dst0 + slot * kTcSlotCols + 32 * i, h[i]);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (ready(step) - bars_u32));
-          stage += kGroups;
-          if (stage >= (uint32_t)S) {
-            stage -= (uint32_t)S;
-            stage_phase ^= 1u;
-          }
-          slot += kGroups;
-          while (slot >= w_slots) slot -= w_slots;
+        for (int i = 0; i < kChunks; ++i) int8_to_f16(c[i], h[i / 4] + 8 * (i % 4));
+        __syncwarp();  // every lane has its codes
+        if (lane == 0) mbar_arrive(empty((int)stage));
+        // the K block that had this slot
+        if (box >= w_slots) {
+          const uint32_t before = (box - w_slots) / kBoxes;
+          if (!tc_wait(done(before), parity(before), ab, kStatusWaitEmpty)) break;
         }
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < kChunks / 4; ++i)
+          tmem_st_32x32b_x32(dst0 + slot * kTcSlotCols + 32 * i, h[i]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_tmem(leader_bars + (ready(step) - bars_u32));
+        stage += kGroups;
+        if (stage >= (uint32_t)S) {
+          stage -= (uint32_t)S;
+          stage_phase ^= 1u;
+        }
+        slot += kGroups;
+        while (slot >= w_slots) slot -= w_slots;
       }
     } else if (kInt8) {
       // x as f16, for the MMAs of the pair
@@ -707,11 +768,13 @@ size_t linear_tc_smem_bytes(const LinearParams& p, int code_type) {
   const size_t x = tc_x_bytes(p.block_t);
   const size_t tiles = code_type == Q8_INT8 ? p.stages * kTcWBytes + p.x_slots * p.boxes * 2 * x
                                             : p.stages * 2 * (kTcWBytes + x);
-  return 1024 + tiles + 2 * kTcBoxBytes + kTcMaxTokens * sizeof(float) + kTcBars * 8 + 16;
+  return 1024 + tc_head_bytes(p.block_t) + tiles;
 }
 
-constexpr int kTcMostSmem =
-    1024 + kTcSmemBudget + 2 * kTcBoxBytes + kTcMaxTokens * 4 + kTcBars * 8 + 16;
+constexpr int kTcMostSmem = 227 * 1024;  // all that a CTA may have
+// tiles of more than 192 tokens have stages of 60 and 64 KB, and so leave room for more scales
+static_assert(1024 + 18 * 1024 + kTcSmemBudget <= kTcMostSmem &&
+              kTcBarBytes + kTcStaging + 2 * 192 * 4 <= 18 * 1024);
 
 cudaError_t linear_tc_setup() {
   cudaError_t e = cudaSuccess;
