@@ -11,9 +11,11 @@ from . import capi
 
 
 def empty_codes(rows: int, cols: int, dtype=torch.int8, device="cuda") -> torch.Tensor:
-    """An uninitialised [rows, cols] matrix of codes whose row pitch is a multiple of 16 bytes, as
-    the linear layers take it."""
-    return torch.empty(rows, -(-cols // 16) * 16, dtype=dtype, device=device)[:, :cols]
+    """An uninitialised [rows, cols] matrix of codes whose row pitch is a multiple of 32 bytes. The
+    linear layers take multiples of 16, but a row that starts inside a 32-byte sector costs them a
+    sector more for every 128 codes: 4096 x 8192 x 1001 e4m3 takes 56 us with both matrices on 16
+    bytes, 40 on 32."""
+    return torch.empty(rows, -(-cols // 32) * 32, dtype=dtype, device=device)[:, :cols]
 
 
 def quantise_rows(v: torch.Tensor, dtype=torch.int8) -> tuple[torch.Tensor, torch.Tensor]:
@@ -31,13 +33,13 @@ def quantise_rows(v: torch.Tensor, dtype=torch.int8) -> tuple[torch.Tensor, torc
 
 class LinearQ8:
     """y = (x * w^T) scaled by token and channel, plus a bias. Owns a plan for up to max_rows tokens
-    and keeps the weights' codes (copied once if their rows are not laid out as the kernels read
-    them). One call at a time: a plan's workspace is shared by its runs."""
+    and keeps the weights' codes (copied once if their rows do not lie on 32-byte boundaries, as the
+    kernels read them fastest). One call at a time: a plan's workspace is shared by its runs."""
 
     def __init__(self, w: torch.Tensor, scale_w: torch.Tensor, bias: torch.Tensor | None = None,
                  max_rows: int = 8192):
         self._plan = 0
-        if w.stride(1) != 1 or w.stride(0) % 16 or w.data_ptr() % 16:
+        if w.stride(1) != 1 or w.stride(0) % 32 or w.data_ptr() % 32:
             w = empty_codes(*w.shape, dtype=w.dtype, device=w.device).copy_(w)
         self.w, self.scale_w, self.bias = w, scale_w, bias
         self.max_rows = max_rows
