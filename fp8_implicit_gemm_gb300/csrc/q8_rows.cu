@@ -23,6 +23,41 @@ struct RowStat {
   unsigned amax;
 };
 
+// Two fp32 operations by one instruction: these kernels are bound by their issue.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// amax with |a| and |b| taken in, a NaN kept (max.NaN gives the positive one).
+__device__ __forceinline__ unsigned amax_with(unsigned amax, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;"
+      : "=f"(r)
+      : "f"(a), "f"(b), "f"(__uint_as_float(amax)));
+  return __float_as_uint(r);
+}
+
 __device__ __forceinline__ RowStat warp_reduce(RowStat s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s.sum += __shfl_xor_sync(0xFFFFFFFFu, s.sum, o);
@@ -175,13 +210,18 @@ struct Place {
 __device__ __forceinline__ uint32_t int8_codes(const float* v, float inv) {
   uint32_t n[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) n[i] = __float_as_uint(fmaf(v[i], inv, 12582912.0f));
+  for (int i = 0; i < 4; i += 2) {
+    const float2 r = fma2(make_float2(v[i], v[i + 1]), make_float2(inv, inv),
+                          make_float2(12582912.0f, 12582912.0f));
+    n[i] = __float_as_uint(r.x);
+    n[i + 1] = __float_as_uint(r.y);
+  }
   return __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
 }
 __device__ __forceinline__ uint32_t e4m3_codes(const float* v, float inv) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv),
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[0], v[1]), make_float2(inv, inv)),
                                                __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv),
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[2], v[3]), make_float2(inv, inv)),
                                                __NV_SATFINITE, __NV_E4M3);
   return (lo & 0xFFFFu) | (hi << 16);
 }
@@ -191,17 +231,20 @@ struct RowCode {
   float lift, inv;
 };
 
-// The row's scale, written by one thread, and its codes' factors; `gain` is what the scale is
-// multiplied by (the norm's r). A row that is not finite gets the scale NaN and codes 0 (its values
+// The row's scale, written by one thread, and its codes' factors. The norm's r goes into the scale
+// alone, so only that thread works it out. A row that is not finite gets the scale NaN and codes 0 (its values
 // must be replaced by 0 before they are multiplied). A row so small that top / amax would overflow
 // is lifted first.
-__device__ __forceinline__ RowCode row_scale(const RowStat& st, float gain, const RowsParams& p,
-                                             long long row, bool writer, bool& bad) {
+template <bool kNorm>
+__device__ __forceinline__ RowCode row_scale(const RowStat& st, const RowsParams& p, long long row,
+                                             bool writer, bool& bad) {
   const float top = p.code_type == Q8_E4M3 ? 448.0f : 127.0f;
   bad = st.amax >= 0x7F800000u || !(st.sum < INFINITY);
   const float amax = __uint_as_float(st.amax);
-  if (writer)
+  if (writer) {
+    const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
     p.scale[row] = bad ? __int_as_float(0x7FC00000) : (amax > 0.0f ? amax * gain / top : 1.0f);
+  }
   RowCode c;
   c.lift = amax < 0x1p-100f ? 0x1p100f : 1.0f;
   c.inv = bad || amax == 0.0f ? 0.0f : top / (amax * c.lift);
@@ -209,11 +252,11 @@ __device__ __forceinline__ RowCode row_scale(const RowStat& st, float gain, cons
 }
 
 // Codes and scale of one row whose values the threads hold.
-template <int NV>
-__device__ __forceinline__ void row_write(float (&v)[NV][kChunk], const RowStat& st, float gain,
+template <int NV, bool kNorm>
+__device__ __forceinline__ void row_write(float (&v)[NV][kChunk], const RowStat& st,
                                           const RowsParams& p, long long row, const Place& at) {
   bool bad;
-  const RowCode rc = row_scale(st, gain, p, row, at.tid == 0, bad);
+  const RowCode rc = row_scale<kNorm>(st, p, row, at.tid == 0, bad);
   if (bad || rc.lift != 1.0f) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -272,6 +315,7 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
     if (!kAhead) load_row(row);
     float v[NV][kChunk];
     RowStat st{0.0f, 0u};
+    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float b[kChunk];
@@ -280,7 +324,11 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
       if (kNorm) {
         if (two) {
 #pragma unroll
-          for (int e = 0; e < kChunk; ++e) v[i][e] += b[e];
+          for (int e = 0; e < kChunk; e += 2) {
+            const float2 h = add2(make_float2(v[i][e], v[i][e + 1]), make_float2(b[e], b[e + 1]));
+            v[i][e] = h.x;
+            v[i][e + 1] = h.y;
+          }
           // these columns have been read by this thread, if sum_out is x or the residual
           at.store(static_cast<T*>(p.sum_out) + row * p.sum_pitch, i, v[i]);
         }
@@ -292,9 +340,12 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
         else
           at.template values<__half>(p.weight, i, w);
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-          st.sum = fmaf(v[i][e], v[i][e], st.sum);
-          v[i][e] *= w[e];
+        for (int e = 0; e < kChunk; e += 2) {
+          const float2 h = make_float2(v[i][e], v[i][e + 1]);
+          sum = fma2(h, h, sum);
+          const float2 y = mul2(h, make_float2(w[e], w[e + 1]));
+          v[i][e] = y.x;
+          v[i][e + 1] = y.y;
         }
       } else {
 #pragma unroll
@@ -302,13 +353,12 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
           v[i][e] = silu_mul(v[i][e], b[e]);
       }
 #pragma unroll
-      for (int e = 0; e < kChunk; ++e)
-        st.amax = max(st.amax, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < kChunk; e += 2) st.amax = amax_with(st.amax, v[i][e], v[i][e + 1]);
     }
     if (kAhead && row + stride < p.rows) load_row(row + stride);
+    st.sum = sum.x + sum.y;
     st = row_reduce(st, p.row_threads, buffer);
-    const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
-    row_write<NV>(v, st, gain, p, row, at);
+    row_write<NV, kNorm>(v, st, p, row, at);
   }
 }
 
@@ -419,12 +469,11 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
       for (int e = 0; e < kLoose; ++e) v[e] = silu_mul(v[e], rb[e].value());
     }
 #pragma unroll
-    for (int e = 0; e < kLoose; ++e) st.amax = max(st.amax, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < kLoose; e += 2) st.amax = amax_with(st.amax, v[e], v[e + 1]);
     if (row + gridDim.x < p.rows) load_row(row + gridDim.x);
     st = row_reduce(st, threads, buffer);
     bool bad;
-    const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
-    const RowCode rc = row_scale(st, gain, p, row, tid == 0, bad);
+    const RowCode rc = row_scale<kNorm>(st, p, row, tid == 0, bad);
     if (bad) {
 #pragma unroll
       for (int e = 0; e < kLoose; ++e) v[e] = 0.0f;
@@ -478,7 +527,7 @@ __device__ __forceinline__ void wide_run(const T* a, const T* b, T* sum_out, con
     } else {
       f = silu_mul(f, rb[e].value());
     }
-    st.amax = max(st.amax, __float_as_uint(f) & 0x7FFFFFFFu);
+    st.amax = amax_with(st.amax, f, 0.0f);
     v[col + 32 * e] = f;  // read back by this thread alone
   });
 }
@@ -517,8 +566,7 @@ __global__ void __launch_bounds__(kWideThreads) rows_q8_wide_loose_kernel(const 
     }
     st = row_reduce(st, kWideThreads, buffer);
     bool bad;
-    const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
-    const RowCode rc = row_scale(st, gain, p, row, threadIdx.x == 0, bad);
+    const RowCode rc = row_scale<kNorm>(st, p, row, threadIdx.x == 0, bad);
     uint8_t* q = p.q + row * p.q_pitch;
     for (int c = first; c < p.cols; c += kWideThreads * kLoose) {
       if (c + kRun <= p.cols)
