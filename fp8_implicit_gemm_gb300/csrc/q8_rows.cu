@@ -8,6 +8,7 @@
 // input is read once, every output written once, which is the operator's floor (both are bound by
 // the memory's bandwidth, and by one row's latency when there are few rows).
 #include <algorithm>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "q8_common.cuh"
@@ -160,43 +161,43 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[kChunk]) {
 }
 
 // Where a thread's kChunk values of step i lie in rows on the 16-byte grid: consecutive columns,
-// moved by 16-byte accesses (the row's last, incomplete chunk by single elements).
+// moved by 16-byte accesses. Only a warp that holds a row's last, incomplete chunk (kTail) has code
+// for single elements; in the others a chunk is in the row or not.
 struct Place {
   int tid, threads, cols;
   __device__ __forceinline__ int col(int i) const { return (i * threads + tid) * kChunk; }
   __device__ __forceinline__ bool whole(int i) const { return col(i) + kChunk <= cols; }
+  __device__ __forceinline__ bool partial(int i) const { return !whole(i) && col(i) < cols; }
   // Columns past the row's end read 0, which changes neither a sum of squares nor an amax.
-  template <typename T>
+  template <bool kTail, typename T>
   __device__ __forceinline__ void load(const T* row, int i, Raw<T>& r) const {
-    if (whole(i)) {
-      r.load8(row + col(i));
-    } else {
-      r.clear();
+    r.clear();
+    if (whole(i)) r.load8(row + col(i));
+    if (kTail && partial(i)) {
 #pragma unroll
       for (int e = 0; e < kChunk - 1; ++e)
         if (col(i) + e < cols) r.load1(e, row + col(i) + e);
     }
   }
-  template <typename T>
+  template <typename T, bool kTail>
   __device__ __forceinline__ void values(const void* row, int i, float (&v)[kChunk]) const {
     Raw<T> r;
-    load(static_cast<const T*>(row), i, r);
+    load<kTail>(static_cast<const T*>(row), i, r);
     r.values(v);
   }
-  template <typename T>
+  template <bool kTail, typename T>
   __device__ __forceinline__ void store(T* row, int i, const float (&v)[kChunk]) const {
-    if (whole(i)) {
-      store8(row + col(i), v);
-    } else {
+    if (whole(i)) store8(row + col(i), v);
+    if (kTail && partial(i)) {
 #pragma unroll
       for (int e = 0; e < kChunk - 1; ++e)
         if (col(i) + e < cols) row[col(i) + e] = q8_from_float<T>(v[e]);
     }
   }
+  template <bool kTail>
   __device__ __forceinline__ void store_codes(uint8_t* row, int i, uint2 c) const {
-    if (whole(i)) {
-      *reinterpret_cast<uint2*>(row + col(i)) = c;
-    } else {
+    if (whole(i)) *reinterpret_cast<uint2*>(row + col(i)) = c;
+    if (kTail && partial(i)) {
 #pragma unroll
       for (int e = 0; e < kChunk - 1; ++e)
         if (col(i) + e < cols)
@@ -204,6 +205,15 @@ struct Place {
     }
   }
 };
+
+// f with std::true_type or std::false_type.
+template <typename F>
+__device__ __forceinline__ void with_flag(bool flag, F f) {
+  if (flag)
+    f(std::true_type{});
+  else
+    f(std::false_type{});
+}
 
 // Four int8 codes of values |v * inv| <= 127 (and a rounding error): adding 1.5 * 2^23 rounds the
 // fused product to an integer, ties to even, whose low byte is the code.
@@ -254,7 +264,8 @@ __device__ __forceinline__ RowCode row_scale(const RowStat& st, const RowsParams
 // Codes and scale of one row whose values the threads hold.
 template <int NV, bool kNorm>
 __device__ __forceinline__ void row_write(float (&v)[NV][kChunk], const RowStat& st,
-                                          const RowsParams& p, long long row, const Place& at) {
+                                          const RowsParams& p, long long row, const Place& at,
+                                          bool tail) {
   bool bad;
   const RowCode rc = row_scale<kNorm>(st, p, row, at.tid == 0, bad);
   if (bad || rc.lift != 1.0f) {
@@ -264,13 +275,20 @@ __device__ __forceinline__ void row_write(float (&v)[NV][kChunk], const RowStat&
       for (int e = 0; e < kChunk; ++e) v[i][e] = bad ? 0.0f : v[i][e] * rc.lift;
   }
   uint8_t* q = p.q + row * p.q_pitch;
+  uint2 c[NV];
+  if (p.code_type == Q8_E4M3) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint2 c = p.code_type == Q8_E4M3
-                        ? make_uint2(e4m3_codes(v[i], rc.inv), e4m3_codes(v[i] + 4, rc.inv))
-                        : make_uint2(int8_codes(v[i], rc.inv), int8_codes(v[i] + 4, rc.inv));
-    at.store_codes(q, i, c);
+    for (int i = 0; i < NV; ++i)
+      c[i] = make_uint2(e4m3_codes(v[i], rc.inv), e4m3_codes(v[i] + 4, rc.inv));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      c[i] = make_uint2(int8_codes(v[i], rc.inv), int8_codes(v[i] + 4, rc.inv));
   }
+  with_flag(tail, [&](auto t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) at.template store_codes<decltype(t)::value>(q, i, c[i]);
+  });
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -299,16 +317,22 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
   long long row = warp_rows ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
                             : (long long)blockIdx.x;
   const bool two = !kNorm || p.b;  // a second input: the residual, or up
+  bool partial = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) partial |= at.partial(i);
+  const bool tail = __any_sync(0xFFFFFFFFu, partial);
   Raw<T> ra[NV], rb[NV];
   auto load_row = [&](long long r) {
     const T* a = static_cast<const T*>(p.a) + r * p.a_pitch;
     const T* b = static_cast<const T*>(p.b) + r * p.b_pitch;
+    with_flag(tail, [&](auto t) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) at.load(a, i, ra[i]);
-    if (two) {
+      for (int i = 0; i < NV; ++i) at.template load<decltype(t)::value>(a, i, ra[i]);
+      if (two) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) at.load(b, i, rb[i]);
-    }
+        for (int i = 0; i < NV; ++i) at.template load<decltype(t)::value>(b, i, rb[i]);
+      }
+    });
   };
   if (kAhead && row < p.rows) load_row(row);
   for (int buffer = 0; row < p.rows; row += stride, buffer ^= 1) {
@@ -316,49 +340,51 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
     float v[NV][kChunk];
     RowStat st{0.0f, 0u};
     float2 sum = make_float2(0.0f, 0.0f);
+    with_flag(tail, [&](auto t) {
+      constexpr bool kTail = decltype(t)::value;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float b[kChunk];
-      ra[i].values(v[i]);
-      if (two) rb[i].values(b);
-      if (kNorm) {
-        if (two) {
+      for (int i = 0; i < NV; ++i) {
+        float b[kChunk];
+        ra[i].values(v[i]);
+        if (two) rb[i].values(b);
+        if (kNorm) {
+          if (two) {
+#pragma unroll
+            for (int e = 0; e < kChunk; e += 2) {
+              const float2 h = add2(make_float2(v[i][e], v[i][e + 1]), make_float2(b[e], b[e + 1]));
+              v[i][e] = h.x;
+              v[i][e + 1] = h.y;
+            }
+            // these columns have been read by this thread, if sum_out is x or the residual
+            at.template store<kTail>(static_cast<T*>(p.sum_out) + row * p.sum_pitch, i, v[i]);
+          }
+          float w[kChunk];
+          if (p.weight_type == Q8_F32)
+            at.template values<float, kTail>(p.weight, i, w);
+          else if (p.weight_type == Q8_BF16)
+            at.template values<__nv_bfloat16, kTail>(p.weight, i, w);
+          else
+            at.template values<__half, kTail>(p.weight, i, w);
 #pragma unroll
           for (int e = 0; e < kChunk; e += 2) {
-            const float2 h = add2(make_float2(v[i][e], v[i][e + 1]), make_float2(b[e], b[e + 1]));
-            v[i][e] = h.x;
-            v[i][e + 1] = h.y;
+            const float2 h = make_float2(v[i][e], v[i][e + 1]);
+            sum = fma2(h, h, sum);
+            const float2 y = mul2(h, make_float2(w[e], w[e + 1]));
+            v[i][e] = y.x;
+            v[i][e + 1] = y.y;
           }
-          // these columns have been read by this thread, if sum_out is x or the residual
-          at.store(static_cast<T*>(p.sum_out) + row * p.sum_pitch, i, v[i]);
-        }
-        float w[kChunk];
-        if (p.weight_type == Q8_F32)
-          at.template values<float>(p.weight, i, w);
-        else if (p.weight_type == Q8_BF16)
-          at.template values<__nv_bfloat16>(p.weight, i, w);
-        else
-          at.template values<__half>(p.weight, i, w);
+        } else {
 #pragma unroll
-        for (int e = 0; e < kChunk; e += 2) {
-          const float2 h = make_float2(v[i][e], v[i][e + 1]);
-          sum = fma2(h, h, sum);
-          const float2 y = mul2(h, make_float2(w[e], w[e + 1]));
-          v[i][e] = y.x;
-          v[i][e + 1] = y.y;
+          for (int e = 0; e < kChunk; ++e) v[i][e] = silu_mul(v[i][e], b[e]);
         }
-      } else {
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e)
-          v[i][e] = silu_mul(v[i][e], b[e]);
+        for (int e = 0; e < kChunk; e += 2) st.amax = amax_with(st.amax, v[i][e], v[i][e + 1]);
       }
-#pragma unroll
-      for (int e = 0; e < kChunk; e += 2) st.amax = amax_with(st.amax, v[i][e], v[i][e + 1]);
-    }
+    });
     if (kAhead && row + stride < p.rows) load_row(row + stride);
     st.sum = sum.x + sum.y;
     st = row_reduce(st, p.row_threads, buffer);
-    row_write<NV, kNorm>(v, st, p, row, at);
+    row_write<NV, kNorm>(v, st, p, row, at, tail);
   }
 }
 
