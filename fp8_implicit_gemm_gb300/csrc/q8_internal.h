@@ -59,14 +59,24 @@ struct LinearParams {
 
 // The kernel for few tokens takes up to this many; it needs no workspace.
 constexpr int few_tokens(int code_type) { return code_type == Q8_INT8 ? 32 : 16; }
-// Whether it is the faster one. Measured, us, few tokens / tensor cores: int8 16 tokens 4096 x 16384
-// 16.4 / 23.1, 16384 x 4096 19.8 / 18.9; 32 tokens 4096 x 4096 9.0 / 10.5, 1024 x 16384 12.6 / 17.6, 8192
-// x 4096 19.9 / 13.3, 4096 x 8192 18.4 / 15.1. e4m3 8 tokens 16384 x 4096 15.9 / 14.2, 4096 x 16384 14.1
-// / 15.8; 16 tokens 4096 x 4096 5.6 / 6.8, 1024 x 16384 9.2 / 10.5, 8192 x 4096 11.4 / 9.3, 4096 x 8192
-// 11.0 / 9.7.
+// Whether it is the faster one, from sweeps of K = 256 to 16384 and N = 512 to 28672. us, few tokens /
+// tensor cores, N x K: e4m3 8 tokens 4096 x 8192 7.8 / 7.9, 10240 x 2048 5.9 / 5.8, 16384 x 2048 8.5 / 7.3,
+// 10240 x 4096 12.3 / 10.1; 16 tokens 4096 x 4096 5.5 / 6.1, 4096 x 8192 11.1 / 8.3, 10240 x 512 3.5 / 3.8,
+// 16384 x 1024 5.8 / 4.8. int8 8 tokens 28672 x 8192 39.0 / 44.4; 16 tokens 4096 x 8192 8.7 / 12.4,
+// 8192 x 8192 16.1 / 17.8, 16384 x 4096 17.4 / 16.3; 24 tokens 4096 x 4096 6.7 / 8.8, 4096 x 8192 12.4 /
+// 12.6; 32 tokens 4096 x 4096 8.1 / 8.9, 4096 x 8192 18.2 / 12.5, 10240 x 512 5.9 / 5.7.
 inline bool prefer_few(long long M, long long N, long long K, int code_type) {
-  const bool small = N * K <= 20 * 1000 * 1000;
-  return M <= 8 || (M <= few_tokens(code_type) && (small || (code_type == Q8_INT8 && M <= 16)));
+  if (M > few_tokens(code_type)) return false;
+  const double codes = (double)N * (double)K;
+  const bool long_n = N > 9728;  // more than a wave of blocks
+  if (code_type == Q8_E4M3) {
+    if (M <= 8) return codes <= (long_n ? 15e6 : 24e6);
+    return codes <= (N > 4864 ? 10e6 : 20e6);
+  }
+  if (M <= 8) return true;
+  if (M <= 16) return codes <= (long_n ? 60e6 : 70e6);
+  if (M <= 24) return codes <= (long_n ? 10e6 : 20e6);
+  return codes <= 20e6 && !long_n;
 }
 cudaError_t launch_linear_few(const LinearParams& p, int code_type, cudaStream_t stream);
 

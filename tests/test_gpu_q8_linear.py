@@ -384,3 +384,27 @@ def test_refusals():
         refused(capi.Conv3dFp8Error, plan, e4[0], sx, e4[1], sw, y)  # a plan for int8 codes
     finally:
         capi.linear_q8_destroy(plan)
+
+
+# every way the kernel for few tokens divides the channels, the warps and the tokens
+@pytest.mark.parametrize("code_dtype", CODE_TYPES)
+@pytest.mark.parametrize("M,N,K", [(3, 100, 200), (1, 2432, 1024), (3, 70, 1300), (5, 2500, 300),
+                                   (7, 4864, 2050), (8, 4900, 2100), (5, 9731, 130), (2, 9731, 600),
+                                   (12, 80, 8300), (9, 2500, 200), (16, 4900, 200), (13, 9731, 200)])
+def test_few_tokens_of_every_shape(code_dtype, M, N, K):
+    check(M, N, K, code_dtype, torch.bfloat16, seed=M + N, bias_dtype=torch.float32, kernel=1)
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 100, 300), (24, 4864, 150), (21, 4900, 1200), (25, 100, 300),
+                                   (32, 2432, 150), (29, 2500, 1200), (27, 9731, 60)])
+def test_few_tokens_of_every_shape_int8(M, N, K):
+    check(M, N, K, torch.int8, torch.float16, seed=M + N, kernel=1)
+
+
+# y's rows anywhere on the 16-byte grid, whole tiles and ragged ones of channels and tokens
+@pytest.mark.parametrize("y_dtype", VALUE_TYPES)
+@pytest.mark.parametrize("y_extra", range(8))
+def test_any_alignment_of_y(y_dtype, y_extra):
+    for M, N in ((40, 256), (77, 300), (33, 129), (130, 511)):
+        check(M, N, 150, torch.int8, y_dtype, seed=M, y_extra=y_extra, kernel=2, splits=1)
+        check(M, N, 150, torch.float8_e4m3fn, y_dtype, seed=M, y_extra=y_extra, kernel=2, splits=1)
