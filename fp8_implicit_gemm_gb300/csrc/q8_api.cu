@@ -114,7 +114,8 @@ bool encode_rows(CUtensorMap* map, const void* base, int elem, long long rows, l
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// y, stored in boxes of 32 channels by as many tokens as make 2 KB; what lies outside is dropped.
+// y, stored in boxes of 32 channels by as many tokens as make 2 KB; what lies outside is dropped. The
+// boxes of a 16-bit y are swizzled, for the matrix stores that fill them.
 bool encode_y(CUtensorMap* map, void* y, int y_type, long long rows, long long cols,
               long long pitch) {
   const EncodeTiledFn enc = encode_tiled();
@@ -128,8 +129,8 @@ bool encode_y(CUtensorMap* map, void* y, int y_type, long long rows, long long c
                                    : y_type == Q8_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   return enc(map, type, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             elem == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Whether every row starts on the grid of the vector accesses. A pitch counts only between rows.

@@ -231,14 +231,67 @@ __device__ __forceinline__ void store_shifted(Y* first, long long pitch, int row
   }
 }
 
-// One warp's part of the epilogue of a tile: a channel a lane, channels n0 .. n0 + 31. 32 tokens of a
-// 16-bit y, 16 of an fp32 one, are staged in shared memory as [token][32 channels], in the warp's two
-// buffers by turns (`boxes` counts them), and leave by a TMA store that y's extents bound. A y off the
-// 16-byte grid is staged by the four warps together and stored as above; the last channels of a y
-// whose rows end inside 16 bytes leave straight from the lanes (a TMA store was seen to write the
-// whole of the 16 bytes that hold a row's last element). With all of y stored from the lanes, 64 bytes
-// a warp, the 67 MB of an e4m3 product of 4096 x 8192 x 4096 took 26 of its 105 us. `release` is called
-// once the accumulator has been read.
+// One warp's part of the epilogue of a tile of a 16-bit y on the 16-byte grid: channels n0 .. n0 + 31,
+// 32 tokens at a time. TMEM is read by 16 lanes x 8 columns, which leaves two tokens of four channels
+// with each thread of eight: as pairs they are scaled and rounded two by one instruction, and stmatrix
+// transposes them on their way to the staging, eight tokens of the 32 channels by one instruction. A
+// thread that held a channel's 32 tokens took 32 two-byte stores and as many roundings for them: 4096 x
+// 8192 x 128 e4m3 28.0 us. The staging is a box of y's map, [token][32 channels] with the map's
+// 64-byte swizzle (without it the eight rows of a matrix meet in two banks of 16 bytes).
+template <typename Y, typename Release>
+__device__ __forceinline__ void tc_epilogue16(const LinearParams& p, const CUtensorMap* ymap,
+                                              uint32_t trow, const float* scale, ScaleBias sc,
+                                              int tokens, long long m0, int n0, uint8_t* own,
+                                              uint32_t& boxes, Release release) {
+  const int lane = threadIdx.x & 31;
+  float2 w[4], bias[4];  // of the channels n0 + 8 q + lane / 4
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float a = __shfl_sync(0xFFFFFFFFu, sc.w, 8 * q + lane / 4);
+    const float b = __shfl_sync(0xFFFFFFFFu, sc.bias, 8 * q + lane / 4);
+    w[q] = make_float2(a, a);
+    bias[q] = make_float2(b, b);
+  }
+  // this thread's row of the matrix that it addresses: token lane % 8, channels 8 (lane / 8) and on
+  const uint32_t row = (uint32_t)((lane % 8) * 64 + (((lane / 8) ^ ((lane % 8) >> 1)) << 4));
+  for (int c = 0; c < tokens; c += 32) {
+    uint32_t r[2][16];
+    tmem_ld_16x256b_x4(trow + c, r[0]);
+    tmem_ld_16x256b_x4(trow + c + (16u << 16), r[1]);
+    tmem_ld_wait();
+    if (c + 32 >= tokens) release();
+    const uint32_t buf = smem_u32(own + (boxes++ & 1u) * kTcBoxBytes);
+    if (lane == 0) bulk_wait_group_read<1>();  // the store from this buffer, two boxes ago
+    __syncwarp();
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {  // of eight tokens
+      const float2 sx = *reinterpret_cast<const float2*>(scale + c + 8 * g + 2 * (lane % 4));
+      uint32_t h[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t* acc = r[q / 2] + 4 * g + 2 * (q % 2);
+        const float2 a = make_float2(__uint_as_float(acc[0]), __uint_as_float(acc[1]));
+        h[q] = q8_pack2<Y>(q8_fma2(q8_mul2(a, sx), w[q], bias[q]));
+      }
+      stmatrix_x4_trans(buf + 512u * g + row, h);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(ymap, buf, n0, (int)m0 + c);
+      bulk_commit_group();
+    }
+  }
+}
+
+// One warp's part of the epilogue of a tile: a channel a lane, channels n0 .. n0 + 31. A 16-bit y on the
+// 16-byte grid goes as above. Of an fp32 one 16 tokens are staged in shared memory as [token][32
+// channels], in the warp's two buffers by turns (`boxes` counts them), and leave by a TMA store that
+// y's extents bound. A y off the 16-byte grid is staged by the four warps together and stored as
+// above; the last channels of a y whose rows end inside 16 bytes leave straight from the lanes (a TMA
+// store was seen to write the whole of the 16 bytes that hold a row's last element). With all of y
+// stored from the lanes the 67 MB of an e4m3 product of 4096 x 8192 x 4096 took 26 of its 105 us, and
+// 6621 x 8192 x 640 to fp32 123 us instead of 81. `release` is called once the accumulator has been read.
 template <typename Y, typename Release>
 __device__ __forceinline__ void tc_epilogue(const LinearParams& p, const CUtensorMap* ymap,
                                             uint32_t trow, const float* scale, ScaleBias sc,
@@ -247,9 +300,16 @@ __device__ __forceinline__ void tc_epilogue(const LinearParams& p, const CUtenso
   constexpr int kRows = kTcBoxBytes / (32 * (int)sizeof(Y));
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
-  const bool by_tma = p.y_tma && (n0 + 32 <= p.N || (long long)p.N * (int)sizeof(Y) % 16 == 0);
+  const bool by_tma = p.y_tma && n0 < p.N &&
+                      (n0 + 32 <= p.N || (long long)p.N * (int)sizeof(Y) % 16 == 0);
   const bool shifted = !p.y_tma && n0 - 32 * warp + 128 <= p.N;  // the same for the four warps
   uint8_t* own = staging + warp * 2 * kTcBoxBytes;
+  if constexpr (sizeof(Y) == 2) {
+    if (by_tma) {
+      tc_epilogue16<Y>(p, ymap, trow, scale, sc, tokens, m0, n0, own, boxes, release);
+      return;
+    }
+  }
   for (int c = 0; c < tokens; c += 32) {
     uint32_t r[32];
     tmem_ld_32x32b_x32(trow + c, r);
@@ -403,21 +463,39 @@ __global__ void __launch_bounds__(kTcThreads<kInt8>, 1)
     // ------------------------------------------------------------------------------ epilogue
     Ring acc;
     uint32_t boxes = 0;
-    for (int u = first_tile; u < num_tiles; u += tile_step) {
+    // The scales and biases of the next tile are loaded while this one's sums are stored: a tile of
+    // few K blocks otherwise waits for them (4096 x 8192 x 128 e4m3 25.7 us, 24.7 so). For int8 that
+    // makes registers spill (36.8 us, 38.1 so).
+    constexpr bool kAhead = !kInt8;
+    float next_x[2], next_w, next_bias;
+    auto load_scales = [&](int u) {
       const TcTile un = tc_tile(p, u);
       const long long n = (long long)un.n_tile * kTcChannels + rank * 128 + threadIdx.x;
+      const long long m = (long long)un.m_tile * p.block_t + threadIdx.x;
+      const long long end = min((long long)un.m_tile * p.block_t + p.block_t, (long long)p.M);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        next_x[i] = m + 128 * i < end ? __ldg(p.scale_x + m + 128 * i) : 0.0f;
+      next_w = next_bias = 0.0f;
+      if (n < p.N) {
+        next_w = __ldg(p.scale_w + n);
+        if (p.bias) next_bias = q8_load_value(p.bias, p.bias_type, n);
+      }
+    };
+    if (kAhead && first_tile < num_tiles) load_scales(first_tile);
+    for (int u = first_tile; u < num_tiles; u += tile_step) {
+      const TcTile un = tc_tile(p, u);
       const long long m0 = (long long)un.m_tile * p.block_t;
       const int tokens = (int)min((long long)p.block_t, p.M - m0);
+      if (!kAhead) load_scales(u);
       // the scales of the tile before the last: that tile lies behind every warp that has come to
       // the last one's barrier
       float* scale = sScale + acc.stage * p.block_t;
-      for (int t = threadIdx.x; t < p.block_t; t += 128)
-        scale[t] = t < tokens ? p.scale_x[m0 + t] : 0.0f;
-      ScaleBias sc{0.0f, 0.0f};
-      if (n < p.N) {
-        sc.w = __ldg(p.scale_w + n);
-        if (p.bias) sc.bias = q8_load_value(p.bias, p.bias_type, n);
-      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if ((int)threadIdx.x + 128 * i < p.block_t) scale[threadIdx.x + 128 * i] = next_x[i];
+      const ScaleBias sc{next_w, next_bias};
+      if (kAhead && u + tile_step < num_tiles) load_scales(u + tile_step);
       // the four warps go on or stop together: they share the tokens' scales
       const bool ok = tc_wait(acc_full(acc.stage), acc.phase, ab, kStatusWaitAccFull);
       if (!named_barrier_and(1, 128, ok)) break;

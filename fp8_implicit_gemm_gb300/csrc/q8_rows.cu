@@ -24,32 +24,6 @@ struct RowStat {
   unsigned amax;
 };
 
-// Two fp32 operations by one instruction: these kernels are bound by their issue.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-
 // amax with |a| and |b| taken in, a NaN kept (max.NaN gives the positive one).
 __device__ __forceinline__ unsigned amax_with(unsigned amax, float a, float b) {
   float r;
@@ -221,7 +195,7 @@ __device__ __forceinline__ uint32_t int8_codes(const float* v, float inv) {
   uint32_t n[4];
 #pragma unroll
   for (int i = 0; i < 4; i += 2) {
-    const float2 r = fma2(make_float2(v[i], v[i + 1]), make_float2(inv, inv),
+    const float2 r = q8_fma2(make_float2(v[i], v[i + 1]), make_float2(inv, inv),
                           make_float2(12582912.0f, 12582912.0f));
     n[i] = __float_as_uint(r.x);
     n[i + 1] = __float_as_uint(r.y);
@@ -229,9 +203,9 @@ __device__ __forceinline__ uint32_t int8_codes(const float* v, float inv) {
   return __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
 }
 __device__ __forceinline__ uint32_t e4m3_codes(const float* v, float inv) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[0], v[1]), make_float2(inv, inv)),
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(q8_mul2(make_float2(v[0], v[1]), make_float2(inv, inv)),
                                                __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul2(make_float2(v[2], v[3]), make_float2(inv, inv)),
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(q8_mul2(make_float2(v[2], v[3]), make_float2(inv, inv)),
                                                __NV_SATFINITE, __NV_E4M3);
   return (lo & 0xFFFFu) | (hi << 16);
 }
@@ -351,7 +325,7 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
           if (two) {
 #pragma unroll
             for (int e = 0; e < kChunk; e += 2) {
-              const float2 h = add2(make_float2(v[i][e], v[i][e + 1]), make_float2(b[e], b[e + 1]));
+              const float2 h = q8_add2(make_float2(v[i][e], v[i][e + 1]), make_float2(b[e], b[e + 1]));
               v[i][e] = h.x;
               v[i][e + 1] = h.y;
             }
@@ -368,8 +342,8 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
 #pragma unroll
           for (int e = 0; e < kChunk; e += 2) {
             const float2 h = make_float2(v[i][e], v[i][e + 1]);
-            sum = fma2(h, h, sum);
-            const float2 y = mul2(h, make_float2(w[e], w[e + 1]));
+            sum = q8_fma2(h, h, sum);
+            const float2 y = q8_mul2(h, make_float2(w[e], w[e + 1]));
             v[i][e] = y.x;
             v[i][e + 1] = y.y;
           }
