@@ -133,14 +133,19 @@ bool encode_y(CUtensorMap* map, void* y, int y_type, long long rows, long long c
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether every row starts on the grid of the vector accesses. A pitch counts only between rows.
-bool rows_aligned(const RowsParams& p, int vb) {
-  const bool one = p.rows <= 1;
-  auto on = [&](const void* m, long long pitch, int grid, int elem) {
-    return !m || (aligned(m, grid) && (one || pitch * elem % grid == 0));
+// Where the rows start. A pitch counts only between rows.
+RowsGrid rows_grid(const RowsParams& p, int vb, int weight_bytes) {
+  auto all_on = [&](int value_grid, int code_grid, int weight_grid) {
+    auto on = [&](const void* m, long long pitch, int grid, int elem) {
+      return !m || (aligned(m, grid) && (p.rows <= 1 || pitch * elem % grid == 0));
+    };
+    return on(p.a, p.a_pitch, value_grid, vb) && on(p.b, p.b_pitch, value_grid, vb) &&
+           on(p.sum_out, p.sum_pitch, value_grid, vb) && on(p.q, p.q_pitch, code_grid, 1) &&
+           aligned(p.weight, weight_grid);
   };
-  return on(p.a, p.a_pitch, 16, vb) && on(p.b, p.b_pitch, 16, vb) &&
-         on(p.sum_out, p.sum_pitch, 16, vb) && on(p.q, p.q_pitch, 8, 1);
+  if (all_on(16, 8, 16)) return RowsGrid::kChunk;
+  if (p.cols % 2 == 0 && all_on(2 * vb, 2, 2 * weight_bytes)) return RowsGrid::kPair;
+  return RowsGrid::kElement;
 }
 
 }  // namespace
@@ -180,9 +185,9 @@ extern "C" conv3d_status rmsnorm_q8_run(const rmsnorm_q8_args* a) {
   p.code_type = a->code_type;
   p.weight_type = a->weight_type;
   p.eps = a->eps;
-  const bool vec = rows_aligned(p, vb) && aligned(p.weight, 16);
+  const RowsGrid grid = rows_grid(p, vb, value_bytes(a->weight_type));
   return launched(
-      launch_rows_q8(p, a->value_type, true, vec, static_cast<cudaStream_t>(a->stream)));
+      launch_rows_q8(p, a->value_type, true, grid, static_cast<cudaStream_t>(a->stream)));
 }
 
 extern "C" conv3d_status silu_mul_q8_run(const silu_mul_q8_args* a) {
@@ -208,7 +213,7 @@ extern "C" conv3d_status silu_mul_q8_run(const silu_mul_q8_args* a) {
   p.rows = a->rows;
   p.cols = (int)a->cols;
   p.code_type = a->code_type;
-  return launched(launch_rows_q8(p, a->value_type, false, rows_aligned(p, vb),
+  return launched(launch_rows_q8(p, a->value_type, false, rows_grid(p, vb, 1),
                                  static_cast<cudaStream_t>(a->stream)));
 }
 

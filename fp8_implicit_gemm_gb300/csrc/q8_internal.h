@@ -25,9 +25,10 @@ struct RowsParams {
   float eps;
 };
 
-// `aligned`: every base and pitch lies on the grid of 8 elements' accesses (16 bytes of values, 8 of
-// codes).
-cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, bool aligned,
+// Where every row of all matrices starts: on 16 bytes (codes on 8), on a pair of elements with an even
+// number of columns, or anywhere.
+enum class RowsGrid { kChunk, kPair, kElement };
+cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, RowsGrid grid,
                            cudaStream_t stream);
 
 // One product y = scale_x * scale_w * (x * w^T) + bias.

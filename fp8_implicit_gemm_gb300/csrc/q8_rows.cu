@@ -362,52 +362,77 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
   }
 }
 
-// Rows off the 16-byte grid (a base, a pitch or a weight): single elements, 32 consecutive ones by a
-// warp at a time, kLoose a thread, held in registers and loaded one row ahead as above. A warp's columns
-// are a run of 32 * kLoose, the same in every row: its accesses are one address and constant offsets,
-// without a mask in all warps but the row's last, and its weights are loaded once. Bound by the issue of
-// instructions (1501 x 5001 fp32: 27 us by asynchronous copies to shared memory, 21 by 16-byte accesses
-// shifted into place, 14.7 with a block's whole width between a thread's elements, each address and mask
-// worked out, 11.1 so; 8192 x 4097 bf16 with a residual 117 -> 63 us, 3.7 TB/s).
+// Rows off the 16-byte grid (a base, a pitch or a weight): elements one by one, or by pairs where every
+// row starts on a pair (kPair), consecutive ones by a warp's lanes, kLoose a thread, held in registers
+// and loaded one row ahead as above. A warp's columns are a run of 32 * kLoose, the same in every row:
+// its accesses are one address and constant offsets, without a mask in all warps but the row's last,
+// and its weights are loaded once. Bound by the issue of instructions (1501 x 5001 fp32: 27 us by
+// asynchronous copies to shared memory, 21 by 16-byte accesses shifted into place, 14.7 with a block's
+// whole width between a thread's elements, each address and mask worked out, 10.6 so; 8192 x 4097 bf16
+// with a residual 117 -> 61 us, 3.9 TB/s, and by pairs 8192 x 4098 42 us, 5.6 TB/s).
 constexpr int kLoose = 8;
+constexpr int kRun = 32 * kLoose;
 
-// One element as it lies in memory, in a register of its own.
-template <typename T>
+// kPair consecutive elements as they lie in memory, in registers of their own.
+template <typename T, int kPair>
 struct LooseRaw {
-  uint32_t bits;
+  static constexpr bool kWords = sizeof(T) == 4 && kPair == 2;
+  uint32_t w[kWords ? 2 : 1];
   __device__ __forceinline__ void load(const T* p) {
-    if (sizeof(T) == 4)
-      bits = *reinterpret_cast<const uint32_t*>(p);
-    else
-      bits = *reinterpret_cast<const uint16_t*>(p);
+    if constexpr (kWords) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else if constexpr (sizeof(T) * kPair == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
   }
-  __device__ __forceinline__ float value() const;
+  __device__ __forceinline__ float value(int j) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[j]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return __uint_as_float(j ? w[0] & 0xFFFF0000u : w[0] << 16);
+    } else {
+      return __half2float(__ushort_as_half((unsigned short)(j ? w[0] >> 16 : w[0])));
+    }
+  }
 };
-template <>
-__device__ __forceinline__ float LooseRaw<float>::value() const { return __uint_as_float(bits); }
-template <>
-__device__ __forceinline__ float LooseRaw<__nv_bfloat16>::value() const {
-  return __uint_as_float(bits << 16);
+template <int kPair, typename T>
+__device__ __forceinline__ void loose_store(T* p, const float* v) {
+  if constexpr (kPair == 1)
+    *p = q8_from_float<T>(v[0]);
+  else if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p) = q8_pack2<T>(make_float2(v[0], v[1]));
 }
-template <>
-__device__ __forceinline__ float LooseRaw<__half>::value() const {
-  return __half2float(__ushort_as_half((unsigned short)bits));
+// The codes e .. e + kPair - 1 of kLoose.
+template <int kPair>
+__device__ __forceinline__ void loose_store_codes(uint8_t* p, const uint32_t* codes, int e) {
+  const uint32_t c = codes[e / 4] >> (8 * (e & 3));
+  if constexpr (kPair == 1)
+    *p = (uint8_t)c;
+  else
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)c;
 }
 
-// f(e) for a thread's elements of a run of which `left` columns from its first one on are in the row;
-// the mask only where the run holds the row's end.
-template <bool kWhole, typename F>
+// f(e, offset) for the first of each kPair of a thread's kLoose elements, which lies `offset` columns
+// behind the thread's first one, `left` columns before the row's end; the mask only where the run
+// holds that end.
+template <bool kWhole, int kPair, typename F>
 __device__ __forceinline__ void for_run(int left, F f) {
 #pragma unroll
-  for (int e = 0; e < kLoose; ++e)
-    if (kWhole || 32 * e < left) f(e);
+  for (int e = 0; e < kLoose; e += kPair)
+    if (kWhole || 32 * e < left) f(e, 32 * e);
 }
-template <typename F>
+template <int kPair, typename F>
 __device__ __forceinline__ void for_run(bool whole, int left, F f) {
   if (whole)
-    for_run<true>(left, f);
+    for_run<true, kPair>(left, f);
   else
-    for_run<false>(left, f);
+    for_run<false, kPair>(left, f);
 }
 
 __device__ __forceinline__ void loose_codes(const float* f, int code_type, float inv,
@@ -421,28 +446,28 @@ __device__ __forceinline__ void loose_codes(const float* f, int code_type, float
   }
 }
 
-template <typename T, bool kNorm>
+template <typename T, bool kNorm, int kPair>
 __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int tid = threadIdx.x, threads = blockDim.x;
-  const int col = (tid >> 5) * (32 * kLoose) + (tid & 31);
-  const int left = p.cols - col;                                      // e is in the row if 32 e < left
-  const bool whole = ((tid >> 5) + 1) * (32 * kLoose) <= p.cols;      // the same for a warp
+  const int col = (tid >> 5) * kRun + (tid & 31) * kPair;
+  const int left = p.cols - col;
+  const bool whole = ((tid >> 5) + 1) * kRun <= p.cols;  // the same for a warp
   const bool two = !kNorm || p.b;
-  float w[kLoose];
-  if (kNorm) {
+  float w[kLoose] = {};
+  if (kNorm)
+    for_run<false, kPair>(left, [&](int e, int o) {
 #pragma unroll
-    for (int e = 0; e < kLoose; ++e)
-      w[e] = 32 * e < left ? q8_load_value(p.weight, p.weight_type, col + 32 * e) : 0.0f;
-  }
-  LooseRaw<T> ra[kLoose] = {}, rb[kLoose] = {};  // 0 past the row's end, in every row
-  auto load_run = [&](const T* src, LooseRaw<T>(&r)[kLoose]) {
-    for_run(whole, left, [&](int e) { r[e].load(src + 32 * e); });
-  };
+      for (int j = 0; j < kPair; ++j)
+        w[e + j] = q8_load_value(p.weight, p.weight_type, col + o + j);
+    });
+  LooseRaw<T, kPair> ra[kLoose / kPair] = {}, rb[kLoose / kPair] = {};  // 0 past the row's end, in every row
   auto load_row = [&](long long r) {
-    load_run(static_cast<const T*>(p.a) + r * p.a_pitch + col, ra);
-    if (two) load_run(static_cast<const T*>(p.b) + r * p.b_pitch + col, rb);
+    const T* a = static_cast<const T*>(p.a) + r * p.a_pitch + col;
+    const T* b = static_cast<const T*>(p.b) + r * p.b_pitch + col;
+    for_run<kPair>(whole, left, [&](int e, int o) { ra[e / kPair].load(a + o); });
+    if (two) for_run<kPair>(whole, left, [&](int e, int o) { rb[e / kPair].load(b + o); });
   };
   long long row = blockIdx.x;
   if (row < p.rows) load_row(row);
@@ -450,14 +475,14 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
     float v[kLoose];
     RowStat st{0.0f, 0u};
 #pragma unroll
-    for (int e = 0; e < kLoose; ++e) v[e] = ra[e].value();
+    for (int e = 0; e < kLoose; ++e) v[e] = ra[e / kPair].value(e % kPair);
     if (kNorm) {
       if (two) {
         T* sum_out = static_cast<T*>(p.sum_out) + row * p.sum_pitch + col;
 #pragma unroll
-        for (int e = 0; e < kLoose; ++e) v[e] += rb[e].value();
+        for (int e = 0; e < kLoose; ++e) v[e] += rb[e / kPair].value(e % kPair);
         // this thread has read these columns, if sum_out is x or the residual
-        for_run(whole, left, [&](int e) { sum_out[32 * e] = q8_from_float<T>(v[e]); });
+        for_run<kPair>(whole, left, [&](int e, int o) { loose_store<kPair>(sum_out + o, v + e); });
       }
 #pragma unroll
       for (int e = 0; e < kLoose; ++e) {
@@ -466,7 +491,7 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < kLoose; ++e) v[e] = silu_mul(v[e], rb[e].value());
+      for (int e = 0; e < kLoose; ++e) v[e] = silu_mul(v[e], rb[e / kPair].value(e % kPair));
     }
 #pragma unroll
     for (int e = 0; e < kLoose; e += 2) st.amax = amax_with(st.amax, v[e], v[e + 1]);
@@ -485,73 +510,88 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
     uint32_t codes[kLoose / 4];
     loose_codes(v, p.code_type, rc.inv, codes);
     uint8_t* q = p.q + row * p.q_pitch + col;
-    for_run(whole, left, [&](int e) { q[32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3))); });
+    for_run<kPair>(whole, left, [&](int e, int o) { loose_store_codes<kPair>(q + o, codes, e); });
   }
 }
 
 // Such rows of more than 8192 columns: the row's values kept in shared memory between the two
-// passes, a warp working on runs of 32 * kLoose columns as above (2000 x 12001 bf16 with a residual 143 us
-// with single elements of a block's whole width, 47 so, 3.6 TB/s; 60 with 1024 threads, which leave one
-// block an SM; with 256 threads wide rows leave too few warps: 16383 columns 75 us against 56).
+// passes, a warp working on runs of kRun columns as above (2000 x 12001 bf16 with a residual 143 us with
+// single elements of a block's whole width, 46 so, 36 by pairs; 60 with 1024 threads, which leave
+// one block an SM; with 256 threads wide rows leave too few warps: 16383 columns 75 us against 56).
 constexpr int kWideThreads = 512;
 
-template <typename T, bool kNorm, bool kWhole>
-__device__ __forceinline__ void wide_run(const T* a, const T* b, T* sum_out, const RowsParams& p,
-                                         int col, float* v, RowStat& st) {
-  const int left = p.cols - col;
-  LooseRaw<T> ra[kLoose] = {}, rb[kLoose] = {};
-  float w[kLoose];
-  for_run<kWhole>(left, [&](int e) { ra[e].load(a + col + 32 * e); });
-  if (b) for_run<kWhole>(left, [&](int e) { rb[e].load(b + col + 32 * e); });
-  if (kNorm) {
-    if (p.weight_type == Q8_F32) {
-      const float* g = static_cast<const float*>(p.weight) + col;
-      for_run<kWhole>(left, [&](int e) { w[e] = g[32 * e]; });
-    } else if (p.weight_type == Q8_BF16) {
-      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.weight) + col;
-      for_run<kWhole>(left, [&](int e) { w[e] = q8_to_float(g[32 * e]); });
-    } else {
-      const __half* g = static_cast<const __half*>(p.weight) + col;
-      for_run<kWhole>(left, [&](int e) { w[e] = q8_to_float(g[32 * e]); });
-    }
-  }
-  for_run<kWhole>(left, [&](int e) {
-    float f = ra[e].value();
-    if (kNorm) {
-      if (b) {
-        f += rb[e].value();
-        sum_out[col + 32 * e] = q8_from_float<T>(f);  // read by this thread, if x or the residual
-      }
-      st.sum = fmaf(f, f, st.sum);
-      f *= w[e];
-    } else {
-      f = silu_mul(f, rb[e].value());
-    }
-    st.amax = amax_with(st.amax, f, 0.0f);
-    v[col + 32 * e] = f;  // read back by this thread alone
+template <typename W, bool kWhole, int kPair>
+__device__ __forceinline__ void wide_weights(const void* weight, int col, int left, float* w) {
+  const W* g = static_cast<const W*>(weight) + col;
+  for_run<kWhole, kPair>(left, [&](int e, int o) {
+    LooseRaw<W, kPair> r;
+    r.load(g + o);
+#pragma unroll
+    for (int j = 0; j < kPair; ++j) w[e + j] = r.value(j);
   });
 }
 
-template <bool kWhole>
+template <typename T, bool kNorm, bool kWhole, int kPair>
+__device__ __forceinline__ void wide_run(const T* a, const T* b, T* sum_out, const RowsParams& p,
+                                         int col, float* v, RowStat& st) {
+  const int left = p.cols - col;
+  LooseRaw<T, kPair> ra[kLoose / kPair] = {}, rb[kLoose / kPair] = {};
+  float w[kLoose];
+  for_run<kWhole, kPair>(left, [&](int e, int o) { ra[e / kPair].load(a + col + o); });
+  if (b) for_run<kWhole, kPair>(left, [&](int e, int o) { rb[e / kPair].load(b + col + o); });
+  if (kNorm) {
+    if (p.weight_type == Q8_F32)
+      wide_weights<float, kWhole, kPair>(p.weight, col, left, w);
+    else if (p.weight_type == Q8_BF16)
+      wide_weights<__nv_bfloat16, kWhole, kPair>(p.weight, col, left, w);
+    else
+      wide_weights<__half, kWhole, kPair>(p.weight, col, left, w);
+  }
+  for_run<kWhole, kPair>(left, [&](int e, int o) {
+    float f[kPair];
+#pragma unroll
+    for (int j = 0; j < kPair; ++j) f[j] = ra[e / kPair].value(j);
+    if (kNorm) {
+      if (b) {
+#pragma unroll
+        for (int j = 0; j < kPair; ++j) f[j] += rb[e / kPair].value(j);
+        loose_store<kPair>(sum_out + col + o, f);  // read by this thread, if x or the residual
+      }
+#pragma unroll
+      for (int j = 0; j < kPair; ++j) {
+        st.sum = fmaf(f[j], f[j], st.sum);
+        f[j] *= w[e + j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPair; ++j) f[j] = silu_mul(f[j], rb[e / kPair].value(j));
+    }
+    st.amax = amax_with(st.amax, f[0], f[kPair - 1]);
+    loose_store<kPair>(v + col + o, f);  // read back by this thread alone
+  });
+}
+
+template <bool kWhole, int kPair>
 __device__ __forceinline__ void wide_codes(uint8_t* q, const RowsParams& p, int col, const float* v,
                                            bool bad, const RowCode& rc) {
   const int left = p.cols - col;
   float f[kLoose] = {};
-  for_run<kWhole>(left, [&](int e) { f[e] = bad ? 0.0f : v[col + 32 * e] * rc.lift; });
+  for_run<kWhole, kPair>(left, [&](int e, int o) {
+#pragma unroll
+    for (int j = 0; j < kPair; ++j) f[e + j] = bad ? 0.0f : v[col + o + j] * rc.lift;
+  });
   uint32_t codes[kLoose / 4];
   loose_codes(f, p.code_type, rc.inv, codes);
-  for_run<kWhole>(left, [&](int e) {
-    q[col + 32 * e] = (uint8_t)(codes[e / 4] >> (8 * (e & 3)));
-  });
+  for_run<kWhole, kPair>(left,
+                         [&](int e, int o) { loose_store_codes<kPair>(q + col + o, codes, e); });
 }
 
-template <typename T, bool kNorm>
+template <typename T, bool kNorm, int kPair>
 __global__ void __launch_bounds__(kWideThreads) rows_q8_wide_loose_kernel(const RowsParams p) {
-  extern __shared__ float v[];
+  extern __shared__ __align__(16) float v[];
   pdl_wait_primary();
   pdl_launch_dependents();
-  constexpr int kRun = 32 * kLoose;
-  const int first = (threadIdx.x >> 5) * kRun, lane = threadIdx.x & 31;
+  const int first = (threadIdx.x >> 5) * kRun, lane = (threadIdx.x & 31) * kPair;
   int buffer = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, buffer ^= 1) {
     const T* a = static_cast<const T*>(p.a) + row * p.a_pitch;
@@ -560,9 +600,9 @@ __global__ void __launch_bounds__(kWideThreads) rows_q8_wide_loose_kernel(const 
     RowStat st{0.0f, 0u};
     for (int c = first; c < p.cols; c += kWideThreads * kLoose) {
       if (c + kRun <= p.cols)
-        wide_run<T, kNorm, true>(a, b, sum_out, p, c + lane, v, st);
+        wide_run<T, kNorm, true, kPair>(a, b, sum_out, p, c + lane, v, st);
       else
-        wide_run<T, kNorm, false>(a, b, sum_out, p, c + lane, v, st);
+        wide_run<T, kNorm, false, kPair>(a, b, sum_out, p, c + lane, v, st);
     }
     st = row_reduce(st, kWideThreads, buffer);
     bool bad;
@@ -570,9 +610,9 @@ __global__ void __launch_bounds__(kWideThreads) rows_q8_wide_loose_kernel(const 
     uint8_t* q = p.q + row * p.q_pitch;
     for (int c = first; c < p.cols; c += kWideThreads * kLoose) {
       if (c + kRun <= p.cols)
-        wide_codes<true>(q, p, c + lane, v, bad, rc);
+        wide_codes<true, kPair>(q, p, c + lane, v, bad, rc);
       else
-        wide_codes<false>(q, p, c + lane, v, bad, rc);
+        wide_codes<false, kPair>(q, p, c + lane, v, bad, rc);
     }
   }
 }
@@ -603,17 +643,21 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, 
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <typename T, bool kNorm>
-static cudaError_t launch_typed(RowsParams& p, bool aligned, cudaStream_t stream) {
-  if (!aligned) {
-    if (p.cols <= 1024 * kLoose) {
-      p.row_threads = std::max(64, (p.cols + 32 * kLoose - 1) / (32 * kLoose) * 32);  // one row a block
-      return launch_rows(rows_q8_loose_kernel<T, kNorm>, p, p.row_threads, 0, stream);
-    }
-    p.row_threads = kWideThreads;
-    return launch_rows(rows_q8_wide_loose_kernel<T, kNorm>, p, kWideThreads,
-                       p.cols * sizeof(float), stream);
+template <typename T, bool kNorm, int kPair>
+static cudaError_t launch_loose(RowsParams& p, cudaStream_t stream) {
+  if (p.cols <= 1024 * kLoose) {
+    p.row_threads = std::max(64, (p.cols + kRun - 1) / kRun * 32);  // one row a block
+    return launch_rows(rows_q8_loose_kernel<T, kNorm, kPair>, p, p.row_threads, 0, stream);
   }
+  p.row_threads = kWideThreads;
+  return launch_rows(rows_q8_wide_loose_kernel<T, kNorm, kPair>, p, kWideThreads,
+                     p.cols * sizeof(float), stream);
+}
+
+template <typename T, bool kNorm>
+static cudaError_t launch_typed(RowsParams& p, RowsGrid grid, cudaStream_t stream) {
+  if (grid == RowsGrid::kElement) return launch_loose<T, kNorm, 1>(p, stream);
+  if (grid == RowsGrid::kPair) return launch_loose<T, kNorm, 2>(p, stream);
   // One chunk a thread where there are few rows, whose time is one row's latency; otherwise two.
   const int chunks = (p.cols + kChunk - 1) / kChunk;
   const int nv = chunks > 2 * rows_max_threads<T>(2) ? 8
@@ -626,16 +670,16 @@ static cudaError_t launch_typed(RowsParams& p, bool aligned, cudaStream_t stream
   return launch_rows(rows_q8_kernel<T, 8, kNorm>, p, threads, 0, stream);
 }
 
-cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, bool aligned,
+cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, RowsGrid grid,
                            cudaStream_t stream) {
   if (value_type == Q8_F32)
-    return norm ? launch_typed<float, true>(p, aligned, stream)
-                : launch_typed<float, false>(p, aligned, stream);
+    return norm ? launch_typed<float, true>(p, grid, stream)
+                : launch_typed<float, false>(p, grid, stream);
   if (value_type == Q8_BF16)
-    return norm ? launch_typed<__nv_bfloat16, true>(p, aligned, stream)
-                : launch_typed<__nv_bfloat16, false>(p, aligned, stream);
-  return norm ? launch_typed<__half, true>(p, aligned, stream)
-              : launch_typed<__half, false>(p, aligned, stream);
+    return norm ? launch_typed<__nv_bfloat16, true>(p, grid, stream)
+                : launch_typed<__nv_bfloat16, false>(p, grid, stream);
+  return norm ? launch_typed<__half, true>(p, grid, stream)
+              : launch_typed<__half, false>(p, grid, stream);
 }
 
 }  // namespace c3d

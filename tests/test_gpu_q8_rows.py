@@ -102,6 +102,29 @@ def test_loose_rows(dtype, cols):
     check_codes(q, scale, act64(gate, up), 2 * err, err)
 
 
+@pytest.mark.parametrize("cols", [6, 254, 258, 2050, 4098, 8194, 12502, 32766])
+@pytest.mark.parametrize("dtype", VALUE_TYPES)
+def test_pair_rows(dtype, cols):
+    """Rows that start on pairs of elements, but not on 16 bytes."""
+    x = values(1, 9 * (cols + 4), dtype, 30)[0].view(9, cols + 4)[:, 2:cols + 2]
+    r = values(1, 9 * (cols + 2), dtype, 31)[0].view(9, cols + 2)[:, :cols]
+    weight = values(1, cols + 2, dtype, 32)[0, 2:]
+    for residual in (None, r):
+        for code_dtype in CODE_TYPES:
+            q, scale, out = run_norm(x, weight, code_dtype, residual)
+            h, y = norm64(x, weight, EPS, residual)
+            check_codes(q, scale, y, CODE_ERR, 2.0 ** -17, f"{cols}")
+            if residual is not None:
+                check_values(out, h, h.abs() * U)
+    q, scale, full = outputs(9, cols, torch.int8)
+    flat = values(1, 18 * cols + 2, dtype, 33)[0, 2:]
+    gate, up = flat[:9 * cols].view(9, cols), flat[9 * cols:].view(9, cols)
+    capi.silu_mul_q8_run(gate, up, q, scale)
+    check_guard(full, cols)
+    err = 2 * (float(gate.abs().max()) + 4) * U + 16 * U
+    check_codes(q, scale, act64(gate, up), 2 * err, err)
+
+
 @pytest.mark.parametrize("cols", [64, 1000, 1001, 4096, 8192])
 def test_norm_in_place(cols):
     """residual_out may be the residual or x itself."""
