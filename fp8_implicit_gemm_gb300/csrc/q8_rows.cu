@@ -272,8 +272,9 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 // One block (of 32 to 1024 threads) or, for short rows, one warp holds a row, NV chunks a thread, and
 // takes every stride-th row. Up to two chunks a thread the next row's loads are issued before this
 // row is worked on: without that the memory waits for each block's reduction and stores (norm of
-// 8192 x 4096 bf16: 67.5 us with a block a row, 37.3 so). Rows past 16384 columns take eight chunks
-// a thread and no look-ahead, which their registers have no room for.
+// 8192 x 4096 bf16: 67.5 us with a block a row, 37.3 so). 16-bit rows past 16384 columns take eight
+// chunks a thread and no look-ahead, which their registers have no room for (1000 x 32768 32.7 us, 50.4
+// by the wide kernel below; fp32 rows past 8192 go there: 2368 x 13256 with a residual 66 us, 95 so).
 template <typename T>
 constexpr int rows_max_threads(int nv) {  // 64 registers a thread, or 128
   return nv == 1 || (nv == 2 && sizeof(T) == 2) ? 1024 : 512;
@@ -373,17 +374,23 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
 constexpr int kLoose = 8;
 constexpr int kRun = 32 * kLoose;
 
-// kPair consecutive elements as they lie in memory, in registers of their own.
+// kPair (1, 2 or 4) consecutive elements as they lie in memory, in registers of their own.
 template <typename T, int kPair>
 struct LooseRaw {
-  static constexpr bool kWords = sizeof(T) == 4 && kPair == 2;
-  uint32_t w[kWords ? 2 : 1];
+  static constexpr int kBytes = kPair * (int)sizeof(T);
+  uint32_t w[(kBytes + 3) / 4];
   __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kWords) {
+    if constexpr (kBytes == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else if constexpr (kBytes == 8) {
       const uint2 v = *reinterpret_cast<const uint2*>(p);
       w[0] = v.x;
       w[1] = v.y;
-    } else if constexpr (sizeof(T) * kPair == 4) {
+    } else if constexpr (kBytes == 4) {
       w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
       w[0] = *reinterpret_cast<const uint16_t*>(p);
@@ -393,20 +400,28 @@ struct LooseRaw {
     if constexpr (sizeof(T) == 4) {
       return __uint_as_float(w[j]);
     } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-      return __uint_as_float(j ? w[0] & 0xFFFF0000u : w[0] << 16);
+      return __uint_as_float(j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
     } else {
-      return __half2float(__ushort_as_half((unsigned short)(j ? w[0] >> 16 : w[0])));
+      return __half2float(__ushort_as_half((unsigned short)(j % 2 ? w[j / 2] >> 16 : w[j / 2])));
     }
   }
 };
 template <int kPair, typename T>
 __device__ __forceinline__ void loose_store(T* p, const float* v) {
-  if constexpr (kPair == 1)
+  if constexpr (kPair == 1) {
     *p = q8_from_float<T>(v[0]);
-  else if constexpr (sizeof(T) == 4)
-    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
-  else
-    *reinterpret_cast<uint32_t*>(p) = q8_pack2<T>(make_float2(v[0], v[1]));
+  } else if constexpr (sizeof(T) == 4) {
+    if constexpr (kPair == 2)
+      *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    const uint32_t lo = q8_pack2<T>(make_float2(v[0], v[1]));
+    if constexpr (kPair == 2)
+      *reinterpret_cast<uint32_t*>(p) = lo;
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(lo, q8_pack2<T>(make_float2(v[2], v[3])));
+  }
 }
 // The codes e .. e + kPair - 1 of kLoose.
 template <int kPair>
@@ -414,8 +429,10 @@ __device__ __forceinline__ void loose_store_codes(uint8_t* p, const uint32_t* co
   const uint32_t c = codes[e / 4] >> (8 * (e & 3));
   if constexpr (kPair == 1)
     *p = (uint8_t)c;
-  else
+  else if constexpr (kPair == 2)
     *reinterpret_cast<uint16_t*>(p) = (uint16_t)c;
+  else
+    *reinterpret_cast<uint32_t*>(p) = c;
 }
 
 // f(e, offset) for the first of each kPair of a thread's kLoose elements, which lies `offset` columns
@@ -514,8 +531,8 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
   }
 }
 
-// Such rows of more than 8192 columns: the row's values kept in shared memory between the two
-// passes, a warp working on runs of kRun columns as above (2000 x 12001 bf16 with a residual 143 us with
+// Such rows of more than 8192 columns, and fp32 rows of more on the 16-byte grid (by fours): the row's
+// values kept in shared memory between the two passes, a warp working on runs of kRun columns as above (2000 x 12001 bf16 with a residual 143 us with
 // single elements of a block's whole width, 46 so, 36 by pairs; 60 with 1024 threads, which leave
 // one block an SM; with 256 threads wide rows leave too few warps: 16383 columns 75 us against 56).
 constexpr int kWideThreads = 512;
@@ -567,6 +584,7 @@ __device__ __forceinline__ void wide_run(const T* a, const T* b, T* sum_out, con
       for (int j = 0; j < kPair; ++j) f[j] = silu_mul(f[j], rb[e / kPair].value(j));
     }
     st.amax = amax_with(st.amax, f[0], f[kPair - 1]);
+    if constexpr (kPair == 4) st.amax = amax_with(st.amax, f[1], f[2]);
     loose_store<kPair>(v + col + o, f);  // read back by this thread alone
   });
 }
@@ -577,8 +595,10 @@ __device__ __forceinline__ void wide_codes(uint8_t* q, const RowsParams& p, int 
   const int left = p.cols - col;
   float f[kLoose] = {};
   for_run<kWhole, kPair>(left, [&](int e, int o) {
+    LooseRaw<float, kPair> r;
+    r.load(v + col + o);
 #pragma unroll
-    for (int j = 0; j < kPair; ++j) f[e + j] = bad ? 0.0f : v[col + o + j] * rc.lift;
+    for (int j = 0; j < kPair; ++j) f[e + j] = bad ? 0.0f : r.value(j) * rc.lift;
   });
   uint32_t codes[kLoose / 4];
   loose_codes(f, p.code_type, rc.inv, codes);
@@ -587,7 +607,7 @@ __device__ __forceinline__ void wide_codes(uint8_t* q, const RowsParams& p, int 
 }
 
 template <typename T, bool kNorm, int kPair>
-__global__ void __launch_bounds__(kWideThreads) rows_q8_wide_loose_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kWideThreads) rows_q8_wide_kernel(const RowsParams p) {
   extern __shared__ __align__(16) float v[];
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -644,30 +664,37 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, 
 }
 
 template <typename T, bool kNorm, int kPair>
-static cudaError_t launch_loose(RowsParams& p, cudaStream_t stream) {
-  if (p.cols <= 1024 * kLoose) {
-    p.row_threads = std::max(64, (p.cols + kRun - 1) / kRun * 32);  // one row a block
-    return launch_rows(rows_q8_loose_kernel<T, kNorm, kPair>, p, p.row_threads, 0, stream);
-  }
+static cudaError_t launch_wide(RowsParams& p, cudaStream_t stream) {
   p.row_threads = kWideThreads;
-  return launch_rows(rows_q8_wide_loose_kernel<T, kNorm, kPair>, p, kWideThreads,
-                     p.cols * sizeof(float), stream);
+  return launch_rows(rows_q8_wide_kernel<T, kNorm, kPair>, p, kWideThreads, p.cols * sizeof(float),
+                     stream);
+}
+template <typename T, bool kNorm, int kPair>
+static cudaError_t launch_loose(RowsParams& p, cudaStream_t stream) {
+  if (p.cols > 1024 * kLoose) return launch_wide<T, kNorm, kPair>(p, stream);
+  p.row_threads = std::max(64, (p.cols + kRun - 1) / kRun * 32);  // one row a block
+  return launch_rows(rows_q8_loose_kernel<T, kNorm, kPair>, p, p.row_threads, 0, stream);
 }
 
 template <typename T, bool kNorm>
 static cudaError_t launch_typed(RowsParams& p, RowsGrid grid, cudaStream_t stream) {
   if (grid == RowsGrid::kElement) return launch_loose<T, kNorm, 1>(p, stream);
   if (grid == RowsGrid::kPair) return launch_loose<T, kNorm, 2>(p, stream);
-  // One chunk a thread where there are few rows, whose time is one row's latency; otherwise two.
   const int chunks = (p.cols + kChunk - 1) / kChunk;
-  const int nv = chunks > 2 * rows_max_threads<T>(2) ? 8
-                 : chunks > rows_max_threads<T>(1) || (p.rows > 304 && chunks > 32) ? 2
-                                                                                    : 1;
+  const bool wide = chunks > 2 * rows_max_threads<T>(2);
+  if constexpr (sizeof(T) == 4)
+    if (wide)
+      return p.cols % 4 == 0   ? launch_wide<T, kNorm, 4>(p, stream)
+             : p.cols % 2 == 0 ? launch_wide<T, kNorm, 2>(p, stream)
+                               : launch_wide<T, kNorm, 1>(p, stream);
+  // One chunk a thread where there are few rows, whose time is one row's latency; otherwise two.
+  const int nv = wide ? 8 : chunks > rows_max_threads<T>(1) || (p.rows > 304 && chunks > 32) ? 2 : 1;
   p.row_threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
   const int threads = p.row_threads == 32 ? 128 : p.row_threads;
   if (nv == 1) return launch_rows(rows_q8_kernel<T, 1, kNorm>, p, threads, 0, stream);
-  if (nv == 2) return launch_rows(rows_q8_kernel<T, 2, kNorm>, p, threads, 0, stream);
-  return launch_rows(rows_q8_kernel<T, 8, kNorm>, p, threads, 0, stream);
+  if constexpr (sizeof(T) == 2)
+    if (wide) return launch_rows(rows_q8_kernel<T, 8, kNorm>, p, threads, 0, stream);
+  return launch_rows(rows_q8_kernel<T, 2, kNorm>, p, threads, 0, stream);
 }
 
 cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, RowsGrid grid,
