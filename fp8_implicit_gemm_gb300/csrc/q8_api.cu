@@ -159,7 +159,8 @@ extern "C" conv3d_status rmsnorm_q8_run(const rmsnorm_q8_args* a) {
     return CONV3D_EINVAL;
   const int vb = value_bytes(a->value_type);
   if (a->rows > 0) {
-    if (!matrix_ok(a->x, vb, a->rows, a->x_pitch, a->cols) || !matrix_ok(a->q, 1, a->rows, a->q_pitch, a->cols) ||
+    if (!matrix_ok(a->x, vb, a->rows, a->x_pitch, a->cols) ||
+        !matrix_ok(a->q, 1, a->rows, a->q_pitch, a->cols) ||
         !a->scale || !aligned(a->scale, 4) || !a->weight ||
         !aligned(a->weight, value_bytes(a->weight_type)))
       return CONV3D_EINVAL;
@@ -197,7 +198,8 @@ extern "C" conv3d_status silu_mul_q8_run(const silu_mul_q8_args* a) {
   const int vb = value_bytes(a->value_type);
   if (a->rows > 0 &&
       (!matrix_ok(a->gate, vb, a->rows, a->gate_pitch, a->cols) ||
-       !matrix_ok(a->up, vb, a->rows, a->up_pitch, a->cols) || !matrix_ok(a->q, 1, a->rows, a->q_pitch, a->cols) ||
+       !matrix_ok(a->up, vb, a->rows, a->up_pitch, a->cols) ||
+       !matrix_ok(a->q, 1, a->rows, a->q_pitch, a->cols) ||
        !a->scale || !aligned(a->scale, 4)))
     return CONV3D_EINVAL;
   st = check_device(a->device);
@@ -289,7 +291,8 @@ extern "C" conv3d_status linear_q8_run(linear_q8_plan_t plan, const linear_q8_ar
   if (a->bias && (!value_type_ok(a->bias_type) || !aligned(a->bias, value_bytes(a->bias_type))))
     return CONV3D_EINVAL;
   if (a->rows > 0) {
-    if (!matrix_ok(a->x, 16, a->rows, a->x_pitch, plan->K) || !matrix_ok(a->w, 16, plan->N, a->w_pitch, plan->K) ||
+    if (!matrix_ok(a->x, 16, a->rows, a->x_pitch, plan->K) ||
+        !matrix_ok(a->w, 16, plan->N, a->w_pitch, plan->K) ||
         !matrix_ok(a->y, value_bytes(a->y_type), a->rows, a->y_pitch, plan->N) || !a->scale_x ||
         !aligned(a->scale_x, 4) || !a->scale_w || !aligned(a->scale_w, 4))
       return CONV3D_EINVAL;

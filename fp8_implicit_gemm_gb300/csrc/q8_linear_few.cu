@@ -199,21 +199,24 @@ static cudaError_t launch_few(const LinearParams& p, cudaStream_t stream) {
   // Channels and warps of a block, from sweeps of K = 256 to 16384 and N = 512 to 28672. 4864 and 9728
   // channels are a wave of 32-channel blocks, one and two an SM. Up to a wave, more warps share K where
   // it is long; past it, the last blocks of a wave leave SMs idle, the less the smaller a block is.
-  // Up to 8 tokens, us, N x K int8, 16 channels on 4 warps / 32 on 4 / 32 on 8 / 32 on 16: 4096 x 512 1.9 /
-  // 1.9 / 1.9 / 2.2, 4096 x 8192 13.1 / 14.2 / 8.5 / 6.7, 8192 x 2048 3.6 / 3.5 / 3.6 / 5.2, 8192 x 4096 8.0 / 8.6
-  // / 6.7 / 8.3, 10240 x 1024 3.1 / 3.4 / 3.9 / 5.8, 16384 x 4096 13.0 / 13.4 / 14.4 / 18.1; 16 channels on 16
-  // warps: 2048 x 4096 3.2, and 3.8 / 4.3 / 3.5 / 3.7.
+  // Up to 8 tokens, us, N x K int8, 16 channels on 4 warps / 32 on 4 / 32 on 8 / 32 on 16:
+  //   4096 x 512  1.9 / 1.9 / 1.9 / 2.2      8192 x 2048  3.6 / 3.5 / 3.6 / 5.2
+  //   4096 x 8192 13.1 / 14.2 / 8.5 / 6.7    8192 x 4096  8.0 / 8.6 / 6.7 / 8.3
+  //   10240 x 1024 3.1 / 3.4 / 3.9 / 5.8     16384 x 4096 13.0 / 13.4 / 14.4 / 18.1
+  // and 16 channels on 16 warps 2048 x 4096 3.2, where those take 3.8 / 4.3 / 3.5 / 3.7.
   const bool long_n = p.N > 9728;
   if (p.M <= 8) {
     if (p.N <= 2432)
-      return p.K <= 1024 ? launch_one<kInt8, 1, 1, 4>(p, stream) : launch_one<kInt8, 1, 1, 16>(p, stream);
+      return p.K <= 1024 ? launch_one<kInt8, 1, 1, 4>(p, stream)
+                         : launch_one<kInt8, 1, 1, 16>(p, stream);
     if (long_n && (kInt8 || p.K <= 512)) return launch_one<kInt8, 1, 1, 4>(p, stream);
     if (long_n || p.K <= 2048) return launch_one<kInt8, 2, 1, 4>(p, stream);
     return p.N <= 4864 ? launch_one<kInt8, 2, 1, 16>(p, stream) : launch_one<kInt8, 2, 1, 8>(p, stream);
   }
-  // More tokens, whose x takes registers. 16 tokens, 16 channels on 4 warps / 16 on 8 / 32 on 4: 4096 x 4096
-  // 4.7 / 4.5 / 5.1, 8192 x 1024 3.4 / 4.4 / 3.9, 10240 x 4096 15.6 / 14.4 / 11.4; 16 on 8 / 16 on 16:
-  // 2048 x 16384 13.4 / 8.9. 32 tokens, 16 on 8 / 32 on 4: 2048 x 4096 5.0 / 8.0, 8192 x 1024 8.4 / 4.9.
+  // More tokens, whose x takes registers. 16 tokens, 16 channels on 4 warps / 16 on 8 / 32 on 4:
+  //   4096 x 4096 4.7 / 4.5 / 5.1    8192 x 1024 3.4 / 4.4 / 3.9    10240 x 4096 15.6 / 14.4 / 11.4
+  // and 2048 x 16384 16 on 8 / 16 on 16 13.4 / 8.9. 32 tokens, 16 on 8 / 32 on 4: 2048 x 4096 5.0 / 8.0,
+  // 8192 x 1024 8.4 / 4.9.
   if (p.M <= 16) {
     if (p.N <= 2432 && p.K > 8192) return launch_one<kInt8, 1, 2, 16>(p, stream);
     if (p.N <= 4864) return launch_one<kInt8, 1, 2, 8>(p, stream);
@@ -223,7 +226,8 @@ static cudaError_t launch_few(const LinearParams& p, cudaStream_t stream) {
   }
   if constexpr (kInt8) {
     if (p.M <= 24)
-      return p.N <= 4864 ? launch_one<kInt8, 1, 3, 8>(p, stream) : launch_one<kInt8, 1, 3, 4>(p, stream);
+      return p.N <= 4864 ? launch_one<kInt8, 1, 3, 8>(p, stream)
+                         : launch_one<kInt8, 1, 3, 4>(p, stream);
     return p.N <= 2432 ? launch_one<kInt8, 1, 4, 8>(p, stream) : launch_one<kInt8, 2, 4, 4>(p, stream);
   }
   return cudaErrorInvalidValue;  // more than few_tokens

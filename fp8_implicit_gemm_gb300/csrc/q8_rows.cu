@@ -216,9 +216,9 @@ struct RowCode {
 };
 
 // The row's scale, written by one thread, and its codes' factors. The norm's r goes into the scale
-// alone, so only that thread works it out. A row that is not finite gets the scale NaN and codes 0 (its values
-// must be replaced by 0 before they are multiplied). A row so small that top / amax would overflow
-// is lifted first.
+// alone, so only that thread works it out. A row that is not finite gets the scale NaN and codes 0
+// (its values must be replaced by 0 before they are multiplied). A row so small that top / amax would
+// overflow is lifted first.
 template <bool kNorm>
 __device__ __forceinline__ RowCode row_scale(const RowStat& st, const RowsParams& p, long long row,
                                              bool writer, bool& bad) {
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
       for (int j = 0; j < kPair; ++j)
         w[e + j] = q8_load_value(p.weight, p.weight_type, col + o + j);
     });
-  LooseRaw<T, kPair> ra[kLoose / kPair] = {}, rb[kLoose / kPair] = {};  // 0 past the row's end, in every row
+  // 0 past the row's end, in every row
+  LooseRaw<T, kPair> ra[kLoose / kPair] = {}, rb[kLoose / kPair] = {};
   auto load_row = [&](long long r) {
     const T* a = static_cast<const T*>(p.a) + r * p.a_pitch + col;
     const T* b = static_cast<const T*>(p.b) + r * p.b_pitch + col;
@@ -532,9 +533,10 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
 }
 
 // Such rows of more than 8192 columns, and fp32 rows of more on the 16-byte grid (by fours): the row's
-// values kept in shared memory between the two passes, a warp working on runs of kRun columns as above (2000 x 12001 bf16 with a residual 143 us with
-// single elements of a block's whole width, 46 so, 36 by pairs; 60 with 1024 threads, which leave
-// one block an SM; with 256 threads wide rows leave too few warps: 16383 columns 75 us against 56).
+// values kept in shared memory between the two passes, a warp working on runs of kRun columns as
+// above. 2000 x 12001 bf16 with a residual takes 143 us with single elements of a block's whole width,
+// 46 so, 36 by pairs; 60 with 1024 threads, which leave one block an SM; with 256 threads wide rows leave
+// too few warps (16383 fp32 columns 75 us against 56).
 constexpr int kWideThreads = 512;
 
 template <typename W, bool kWhole, int kPair>

@@ -96,7 +96,9 @@ conv3d_status silu_mul_q8_run(const silu_mul_q8_args *args);
 typedef struct linear_q8_plan_s *linear_q8_plan_t; /* opaque, owned by the library */
 
 /*
- * Plan products of up to max_rows tokens by an [N][K] weight on `device`. Allocates the workspace.
+ * Plan products of up to max_rows tokens by an [N][K] weight on `device`. Allocates the workspace: a
+ * status word and, for int8 codes, x as f16 (2 * max_rows * K bytes); nothing where max_rows and the
+ * sizes leave all runs to the kernel for few tokens.
  * Errors: EINVAL (a size below 1, an unknown code type), EUNSUPPORTED (sizes of 2^30 or more, a
  * device that is not sm_103), ENOMEM, ECUDA. On error *plan is set to NULL.
  */
@@ -107,7 +109,8 @@ conv3d_status linear_q8_plan(linear_q8_plan_t *plan, long long max_rows, long lo
  * computed beyond the order of a sum's additions. */
 typedef struct {
     int kernel;          /* 0: the library chooses; 1: the kernel for few tokens (EUNSUPPORTED for
-                            max_rows above 32 (int8) or 16 (e4m3)); 2: the tensor-core kernel for any number */
+                            max_rows above 32 (int8) or 16 (e4m3)); 2: the tensor-core kernel for
+                            any number */
     int block_t;         /* 0: the library chooses; else the tokens of a tensor-core tile, a multiple
                             of 32 up to 256 (int8: 192), and less than the run's rows + 32 */
     int splits;          /* 0: the library chooses; 1 to 4: slices of K (no more than K has blocks of
@@ -128,9 +131,9 @@ conv3d_status linear_q8_plan_ex(linear_q8_plan_t *plan, long long max_rows, long
  * One product, asynchronously on `stream`. A plan's workspace is shared by its runs: at most one run
  * of a plan may be in flight at a time (one plan for each concurrent stream). Every element of y is
  * written exactly once and nothing outside it. A row or channel whose scale is NaN is NaN in y.
- * Errors: EINVAL (a NULL pointer with rows > 0, rows < 0 or above max_rows, N, K
- * or a code type other than the plan's, a pitch too small, x or
- * w not 16-byte aligned or with a pitch that is not a multiple of 16, an unknown type, a pointer that
+ * Rows of codes on 32-byte boundaries are read fastest. Errors: EINVAL (a NULL pointer with rows > 0,
+ * rows < 0 or above max_rows, N, K or a code type other than the plan's, a pitch too small, x or w not
+ * 16-byte aligned or with a pitch that is not a multiple of 16, an unknown type, a pointer that
  * is not aligned to its element, the wrong current device), ECUDA. Device errors are reported later,
  * by linear_q8_check. rows == 0 does nothing.
  */
