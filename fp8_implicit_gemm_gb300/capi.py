@@ -461,13 +461,16 @@ _LINEAR_ARGS = struct.Struct("@6P6qP4i")
 
 _value_types = {}
 _code_types = {}
-_q8 = None  # the library, once its first call has loaded it
+# Set by the first call: the library, torch's fp32 and its current stream's handle. These calls cost
+# the host more than the GPU where there are few tokens, so nothing is looked up twice in them.
+_q8 = _f32 = _raw_stream = None
 
 
 def _q8_setup():
-    global _q8
+    global _q8, _f32, _raw_stream
     import torch
     lib = load()
+    _f32, _raw_stream = torch.float32, torch._C._cuda_getCurrentRawStream
     _value_types.update({torch.float32: Q8_F32, torch.bfloat16: Q8_BF16, torch.float16: Q8_F16})
     _code_types.update({torch.int8: Q8_INT8, torch.uint8: Q8_E4M3, torch.float8_e4m3fn: Q8_E4M3})
     _q8 = lib
@@ -476,9 +479,10 @@ def _q8_setup():
 
 def q8_code_type(dtype) -> int:
     """Q8_INT8 for torch.int8, Q8_E4M3 for torch.float8_e4m3fn or torch.uint8 (e4m3 bytes)."""
-    if not _code_types:
-        _q8_setup()
     t = _code_types.get(dtype)
+    if t is None and not _code_types:
+        _q8_setup()
+        t = _code_types.get(dtype)
     if t is None:
         raise ValueError(f"codes are int8, float8_e4m3fn or uint8 (e4m3 bytes), not {dtype}")
     return t
@@ -496,7 +500,7 @@ def _q8_pitch(t, name, shape, device) -> int:
     if t.shape != shape:
         raise ValueError(f"{name}: expected the shape {tuple(shape)}, got {tuple(t.shape)}")
     pitch, step = t.stride()
-    if step != 1 and shape[1] > 1:
+    if step != 1 and t.shape[1] > 1:
         raise ValueError(f"{name}: expected contiguous rows")
     if t.get_device() != device:
         raise ValueError(f"{name}: expected a tensor on CUDA device {device}")
@@ -505,7 +509,7 @@ def _q8_pitch(t, name, shape, device) -> int:
 
 def _q8_vector(t, name, size, device, dtype=None) -> int:
     """Address of a contiguous vector of this size and device."""
-    if t.dim() != 1 or t.shape[0] != size or (size > 1 and t.stride(0) != 1):
+    if t.shape != (size,) or not t.is_contiguous():
         raise ValueError(f"{name}: expected {size} contiguous elements")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -516,18 +520,17 @@ def _q8_vector(t, name, size, device, dtype=None) -> int:
 
 def _q8_head(t, name):
     """Shape and device of a call's first matrix."""
-    if t.dim() != 2:
+    shape, device = t.shape, t.get_device()
+    if len(shape) != 2:
         raise ValueError(f"{name}: expected a matrix")
-    device = t.get_device()
     if device < 0:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    return t.shape, device
+    return shape, device
 
 
 def _q8_stream(stream, device) -> int:
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -551,7 +554,7 @@ def rmsnorm_q8_run(x, weight, q, scale, eps, residual=None, residual_out=None,
         out_ptr = residual_out.data_ptr()
     status = lib.rmsnorm_q8_run(_RMSNORM_ARGS.pack(
         x.data_ptr(), r_ptr, _q8_vector(weight, "weight", cols, device), out_ptr, q.data_ptr(),
-        _q8_vector(scale, "scale", rows, device, _f32()), _q8_pitch(x, "x", shape, device), r_pitch,
+        _q8_vector(scale, "scale", rows, device, _f32), _q8_pitch(x, "x", shape, device), r_pitch,
         out_pitch, _q8_pitch(q, "q", shape, device), rows, cols, _q8_stream(stream, device),
         value_type, _q8_value_type(weight, "weight"), q8_code_type(q.dtype), device, eps, 0))
     if status:
@@ -569,16 +572,11 @@ def silu_mul_q8_run(gate, up, q, scale, stream=None) -> None:
         raise ValueError(f"up: expected {gate.dtype}, got {up.dtype}")
     status = lib.silu_mul_q8_run(_SILU_MUL_ARGS.pack(
         gate.data_ptr(), up.data_ptr(), q.data_ptr(),
-        _q8_vector(scale, "scale", rows, device, _f32()), _q8_pitch(gate, "gate", shape, device),
+        _q8_vector(scale, "scale", rows, device, _f32), _q8_pitch(gate, "gate", shape, device),
         _q8_pitch(up, "up", shape, device), _q8_pitch(q, "q", shape, device), rows, cols,
         _q8_stream(stream, device), value_type, q8_code_type(q.dtype), device, 0))
     if status:
         _raise(status, "silu_mul_q8_run")
-
-
-def _f32():
-    import torch
-    return torch.float32
 
 
 def linear_q8_plan(max_rows, N, K, code_type, device=0, **options) -> int:
@@ -597,31 +595,45 @@ def linear_q8_plan(max_rows, N, K, code_type, device=0, **options) -> int:
     return h.value
 
 
-def linear_q8_run(plan, x, scale_x, w, scale_w, y, bias=None, stream=None) -> None:
-    """y[m, n] = scale_x[m] * scale_w[n] * sum_k x[m, k] * w[n, k] + bias[n]. x [rows, K] and
-    w [N, K] are codes of one type with row pitches that are multiples of 16, y is [rows, N]."""
-    lib = _q8 or _q8_setup()
-    x_shape, device = _q8_head(x, "x")
-    rows, K = x_shape
-    if w.dim() != 2:
-        raise ValueError("w: expected a matrix")
-    N = w.shape[0]
-    code_type = q8_code_type(x.dtype)
-    if code_type != q8_code_type(w.dtype):
-        raise ValueError(f"x and w hold codes of one type, not {x.dtype} and {w.dtype}")
+def linear_q8_weights(w, scale_w, bias=None) -> tuple:
+    """What linear_q8_run_weights needs of a layer's weights w [N, K], scale_w [N] and bias [N],
+    checked once. The caller keeps the tensors alive and where they are."""
+    _q8 or _q8_setup()
+    shape, device = _q8_head(w, "w")
+    N, K = shape
     b_ptr = b_type = 0
     if bias is not None:
         b_ptr = _q8_vector(bias, "bias", N, device)
         b_type = _q8_value_type(bias, "bias")
-    f32 = _f32()
-    status = lib.linear_q8_run(plan, _LINEAR_ARGS.pack(
-        x.data_ptr(), _q8_vector(scale_x, "scale_x", rows, device, f32), w.data_ptr(),
-        _q8_vector(scale_w, "scale_w", N, device, f32), b_ptr, y.data_ptr(),
-        _q8_pitch(x, "x", x_shape, device), _q8_pitch(w, "w", (N, K), device),
+    return (w.data_ptr(), _q8_pitch(w, "w", shape, device),
+            _q8_vector(scale_w, "scale_w", N, device, _f32), b_ptr, b_type, N, K,
+            q8_code_type(w.dtype), device)
+
+
+def linear_q8_run_weights(plan, x, scale_x, weights, y, stream=None) -> None:
+    """linear_q8_run on weights checked before: for few tokens the checks of all tensors take the
+    host as long as the rest of the call."""
+    w_ptr, w_pitch, scale_w_ptr, b_ptr, b_type, N, K, code_type, device = weights
+    x_shape, x_device = _q8_head(x, "x")
+    rows = x_shape[0]
+    if x_shape[1] != K or x_device != device:
+        raise ValueError(f"x: expected {K} columns on CUDA device {device}, got {x_shape[1]} on "
+                         f"{x_device}")
+    if q8_code_type(x.dtype) != code_type:
+        raise ValueError(f"x and w hold codes of one type, not {x.dtype} and another")
+    status = _q8.linear_q8_run(plan, _LINEAR_ARGS.pack(
+        x.data_ptr(), _q8_vector(scale_x, "scale_x", rows, device, _f32), w_ptr, scale_w_ptr, b_ptr,
+        y.data_ptr(), _q8_pitch(x, "x", x_shape, device), w_pitch,
         _q8_pitch(y, "y", (rows, N), device), rows, N, K, _q8_stream(stream, device),
         _q8_value_type(y, "y"), b_type, code_type, 0))
     if status:
         _raise(status, "linear_q8_run")
+
+
+def linear_q8_run(plan, x, scale_x, w, scale_w, y, bias=None, stream=None) -> None:
+    """y[m, n] = scale_x[m] * scale_w[n] * sum_k x[m, k] * w[n, k] + bias[n]. x [rows, K] and
+    w [N, K] are codes of one type with row pitches that are multiples of 16, y is [rows, N]."""
+    linear_q8_run_weights(plan, x, scale_x, linear_q8_weights(w, scale_w, bias), y, stream)
 
 
 def linear_q8_check(plan) -> int:

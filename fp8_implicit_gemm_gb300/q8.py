@@ -41,14 +41,18 @@ class LinearQ8:
         self._plan = 0
         if w.stride(1) != 1 or w.stride(0) % 32 or w.data_ptr() % 32:
             w = empty_codes(*w.shape, dtype=w.dtype, device=w.device).copy_(w)
-        self.w, self.scale_w, self.bias = w, scale_w, bias
+        # tensors of its own on the same memory: what the caller does to its own ones later frees none
+        # of what the calls read
+        self.w, self.scale_w = w.detach(), scale_w.detach()
+        self.bias = None if bias is None else bias.detach()
+        self._weights = capi.linear_q8_weights(self.w, self.scale_w, self.bias)
         self.max_rows = max_rows
         self._plan = capi.linear_q8_plan(max_rows, w.shape[0], w.shape[1],
                                          capi.q8_code_type(w.dtype), w.get_device())
 
     def __call__(self, x: torch.Tensor, scale_x: torch.Tensor, y: torch.Tensor,
                  stream=None) -> torch.Tensor:
-        capi.linear_q8_run(self._plan, x, scale_x, self.w, self.scale_w, y, self.bias, stream)
+        capi.linear_q8_run_weights(self._plan, x, scale_x, self._weights, y, stream)
         return y
 
     def check(self) -> int:

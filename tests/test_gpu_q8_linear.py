@@ -408,3 +408,25 @@ def test_any_alignment_of_y(y_dtype, y_extra):
     for M, N in ((40, 256), (77, 300), (33, 129), (130, 511)):
         check(M, N, 150, torch.int8, y_dtype, seed=M, y_extra=y_extra, kernel=2, splits=1)
         check(M, N, 150, torch.float8_e4m3fn, y_dtype, seed=M, y_extra=y_extra, kernel=2, splits=1)
+
+
+def test_layer_holds_its_weights():
+    """A layer reads the memory it was made with, whatever becomes of the caller's tensors."""
+    x, sx, w, sw, bias = case(20, 300, 256, torch.int8, torch.float32, 90, torch.float32)
+    want, mag = linear64(x, sx, w, sw, bias)
+    w = w.clone(memory_format=torch.contiguous_format)
+    layer = q8.LinearQ8(w, sw, bias=bias, max_rows=20)
+    w.data = torch.zeros(1, 1, dtype=torch.int8, device="cuda")
+    sw.data = torch.zeros(1, device="cuda")
+    del bias
+    fill = [torch.full((300, 256), 55, dtype=torch.int8, device="cuda") for _ in range(4)]
+    y = layer(x, sx, torch.empty(20, 300, device="cuda"))
+    assert layer.check() == capi.CONV3D_OK and len(fill) == 4
+    check_values(y, want, linear_err(mag, 256, torch.int8), "held")
+    with pytest.raises(ValueError):
+        layer(x[:, :255], sx, y)
+    with pytest.raises(ValueError):
+        layer(x.view(torch.float8_e4m3fn), sx, y)
+    with pytest.raises(ValueError):
+        layer(x, sx, y[:, :299])
+    layer.close()
