@@ -519,13 +519,16 @@ def _q8_vector(t, name, size, device, dtype=None) -> int:
 
 
 def _q8_head(t, name):
-    """Shape and device of a call's first matrix."""
+    """Shape, device and pitch of a call's first matrix."""
     shape, device = t.shape, t.get_device()
     if len(shape) != 2:
         raise ValueError(f"{name}: expected a matrix")
     if device < 0:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    return shape, device
+    pitch, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    return shape, device, pitch
 
 
 def _q8_stream(stream, device) -> int:
@@ -539,7 +542,7 @@ def rmsnorm_q8_run(x, weight, q, scale, eps, residual=None, residual_out=None,
     """h = x + residual; residual_out = h; q, scale = the codes of h / rms(h) * weight, a scale a
     row. Matrices [rows, cols] with contiguous rows (any pitch); the codes' type is q's."""
     lib = _q8 or _q8_setup()
-    shape, device = _q8_head(x, "x")
+    shape, device, x_pitch = _q8_head(x, "x")
     rows, cols = shape
     value_type = _q8_value_type(x, "x")
     r_ptr = out_ptr = r_pitch = out_pitch = 0
@@ -547,15 +550,17 @@ def rmsnorm_q8_run(x, weight, q, scale, eps, residual=None, residual_out=None,
         if residual.dtype != x.dtype:
             raise ValueError(f"residual: expected {x.dtype}, got {residual.dtype}")
         r_pitch, r_ptr = _q8_pitch(residual, "residual", shape, device), residual.data_ptr()
-    if residual_out is not None:
+    if residual_out is residual:
+        out_pitch, out_ptr = r_pitch, r_ptr
+    elif residual_out is not None:
         if residual_out.dtype != x.dtype:
             raise ValueError(f"residual_out: expected {x.dtype}, got {residual_out.dtype}")
         out_pitch = _q8_pitch(residual_out, "residual_out", shape, device)
         out_ptr = residual_out.data_ptr()
     status = lib.rmsnorm_q8_run(_RMSNORM_ARGS.pack(
         x.data_ptr(), r_ptr, _q8_vector(weight, "weight", cols, device), out_ptr, q.data_ptr(),
-        _q8_vector(scale, "scale", rows, device, _f32), _q8_pitch(x, "x", shape, device), r_pitch,
-        out_pitch, _q8_pitch(q, "q", shape, device), rows, cols, _q8_stream(stream, device),
+        _q8_vector(scale, "scale", rows, device, _f32), x_pitch, r_pitch, out_pitch,
+        _q8_pitch(q, "q", shape, device), rows, cols, _q8_stream(stream, device),
         value_type, _q8_value_type(weight, "weight"), q8_code_type(q.dtype), device, eps, 0))
     if status:
         _raise(status, "rmsnorm_q8_run")
@@ -565,14 +570,14 @@ def silu_mul_q8_run(gate, up, q, scale, stream=None) -> None:
     """q, scale = the codes of silu(gate) * up, a scale a row. Matrices [rows, cols] with contiguous
     rows (any pitch; gate and up may be two halves of one matrix); the codes' type is q's."""
     lib = _q8 or _q8_setup()
-    shape, device = _q8_head(gate, "gate")
+    shape, device, gate_pitch = _q8_head(gate, "gate")
     rows, cols = shape
     value_type = _q8_value_type(gate, "gate")
     if up.dtype != gate.dtype:
         raise ValueError(f"up: expected {gate.dtype}, got {up.dtype}")
     status = lib.silu_mul_q8_run(_SILU_MUL_ARGS.pack(
         gate.data_ptr(), up.data_ptr(), q.data_ptr(),
-        _q8_vector(scale, "scale", rows, device, _f32), _q8_pitch(gate, "gate", shape, device),
+        _q8_vector(scale, "scale", rows, device, _f32), gate_pitch,
         _q8_pitch(up, "up", shape, device), _q8_pitch(q, "q", shape, device), rows, cols,
         _q8_stream(stream, device), value_type, q8_code_type(q.dtype), device, 0))
     if status:
@@ -599,22 +604,21 @@ def linear_q8_weights(w, scale_w, bias=None) -> tuple:
     """What linear_q8_run_weights needs of a layer's weights w [N, K], scale_w [N] and bias [N],
     checked once. The caller keeps the tensors alive and where they are."""
     _q8 or _q8_setup()
-    shape, device = _q8_head(w, "w")
+    shape, device, w_pitch = _q8_head(w, "w")
     N, K = shape
     b_ptr = b_type = 0
     if bias is not None:
         b_ptr = _q8_vector(bias, "bias", N, device)
         b_type = _q8_value_type(bias, "bias")
-    return (w.data_ptr(), _q8_pitch(w, "w", shape, device),
-            _q8_vector(scale_w, "scale_w", N, device, _f32), b_ptr, b_type, N, K,
-            q8_code_type(w.dtype), device)
+    return (w.data_ptr(), w_pitch, _q8_vector(scale_w, "scale_w", N, device, _f32), b_ptr, b_type,
+            N, K, q8_code_type(w.dtype), device)
 
 
 def linear_q8_run_weights(plan, x, scale_x, weights, y, stream=None) -> None:
     """linear_q8_run on weights checked before: for few tokens the checks of all tensors take the
     host as long as the rest of the call."""
     w_ptr, w_pitch, scale_w_ptr, b_ptr, b_type, N, K, code_type, device = weights
-    x_shape, x_device = _q8_head(x, "x")
+    x_shape, x_device, x_pitch = _q8_head(x, "x")
     rows = x_shape[0]
     if x_shape[1] != K or x_device != device:
         raise ValueError(f"x: expected {K} columns on CUDA device {device}, got {x_shape[1]} on "
@@ -623,9 +627,8 @@ def linear_q8_run_weights(plan, x, scale_x, weights, y, stream=None) -> None:
         raise ValueError(f"x and w hold codes of one type, not {x.dtype} and another")
     status = _q8.linear_q8_run(plan, _LINEAR_ARGS.pack(
         x.data_ptr(), _q8_vector(scale_x, "scale_x", rows, device, _f32), w_ptr, scale_w_ptr, b_ptr,
-        y.data_ptr(), _q8_pitch(x, "x", x_shape, device), w_pitch,
-        _q8_pitch(y, "y", (rows, N), device), rows, N, K, _q8_stream(stream, device),
-        _q8_value_type(y, "y"), b_type, code_type, 0))
+        y.data_ptr(), x_pitch, w_pitch, _q8_pitch(y, "y", (rows, N), device), rows, N, K,
+        _q8_stream(stream, device), _q8_value_type(y, "y"), b_type, code_type, 0))
     if status:
         _raise(status, "linear_q8_run")
 
