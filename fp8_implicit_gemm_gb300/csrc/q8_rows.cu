@@ -639,7 +639,9 @@ __global__ void __launch_bounds__(kWideThreads) rows_q8_wide_kernel(const RowsPa
   }
 }
 
-// A persistent grid: as many blocks as the device holds at once, or as the rows need.
+// A persistent grid: as many blocks as the device holds at once, or as the rows need. A kernel with
+// `smem` bytes for a row's values has those of row_reduce beside them, and the limit that a block has
+// unless it is raised counts both.
 template <typename Kernel>
 static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, size_t smem,
                                cudaStream_t stream) {
@@ -647,7 +649,7 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, 
   int dev = 0, sms = 0, held = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && smem > 48 * 1024)
+  if (e == cudaSuccess && smem > 0)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess && blocks > sms)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, threads, smem);
