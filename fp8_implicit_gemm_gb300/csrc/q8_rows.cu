@@ -639,9 +639,7 @@ __global__ void __launch_bounds__(kWideThreads) rows_q8_wide_kernel(const RowsPa
   }
 }
 
-// A persistent grid: as many blocks as the device holds at once, or as the rows need. A kernel with
-// `smem` bytes for a row's values has those of row_reduce beside them, and the limit that a block has
-// unless it is raised counts both.
+// A persistent grid: as many blocks as the device holds at once, or as the rows need.
 template <typename Kernel>
 static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, size_t smem,
                                cudaStream_t stream) {
@@ -649,8 +647,6 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, 
   int dev = 0, sms = 0, held = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && smem > 0)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess && blocks > sms)
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&held, kernel, threads, smem);
   if (e != cudaSuccess) return e;
@@ -667,11 +663,18 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, 
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// The kernel's shared-memory limit is raised to what the widest row needs whatever this row does: the
+// limit belongs to the kernel, so were it set to a call's own size, another host thread's call could
+// lower it between that and the launch. (A row's values have row_reduce's 512 bytes beside them, and
+// the limit that holds unless it is raised counts both.)
 template <typename T, bool kNorm, int kPair>
 static cudaError_t launch_wide(RowsParams& p, cudaStream_t stream) {
+  constexpr auto kernel = rows_q8_wide_kernel<T, kNorm, kPair>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             Q8_MAX_COLS * (int)sizeof(float));
+  if (e != cudaSuccess) return e;
   p.row_threads = kWideThreads;
-  return launch_rows(rows_q8_wide_kernel<T, kNorm, kPair>, p, kWideThreads, p.cols * sizeof(float),
-                     stream);
+  return launch_rows(kernel, p, kWideThreads, p.cols * sizeof(float), stream);
 }
 template <typename T, bool kNorm, int kPair>
 static cudaError_t launch_loose(RowsParams& p, cudaStream_t stream) {
