@@ -91,7 +91,7 @@ struct TcLimits {
   int clusters[kTcMaxSplits];  // clusters of 2, 4, 6 and 8 CTAs held at once
   int block_t, splits;   // 0: the choice of linear_tc_decide
 };
-// Fills in the tiling of a product of M, N and K.
+// Fills in the tiling of a product of M, N and K; block_t stays 0 where the limits leave none.
 void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim);
 // Boxes of the tensor maps: rows of w one CTA loads at a time (of x: half of block_t).
 constexpr int kTcWBoxRows = 128;

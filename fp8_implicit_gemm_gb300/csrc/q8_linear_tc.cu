@@ -827,6 +827,7 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
       }
     }
   }
+  if (!p.block_t) return;  // the limits leave none
   const int x_bytes = (int)tc_x_bytes(p.block_t);
   p.w_slots = p.x_slots = 0;
   if (int8) {

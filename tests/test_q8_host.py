@@ -1,0 +1,72 @@
+"""The host side of the 8-bit products' planning, as far as it goes without a GPU."""
+import os
+import subprocess
+
+import pytest
+
+from fp8_implicit_gemm_gb300 import build
+
+# Asks for the tiling of M x N x K, with room for 76 clusters of each size.
+DECIDE = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "q8_internal.h"
+int main(int argc, char** argv) {
+  c3d::LinearParams p{};
+  c3d::TcLimits lim{};
+  p.M = atoi(argv[1]);
+  p.N = atoi(argv[2]);
+  p.K = atoi(argv[3]);
+  lim.block_t = atoi(argv[5]);
+  lim.splits = atoi(argv[6]);
+  for (int& c : lim.clusters) c = 76;
+  c3d::linear_tc_decide(p, atoi(argv[4]), lim);
+  printf("%d %d %d %d\n", p.block_t, p.splits, p.stages, p.x_slots);
+}
+"""
+INT8, E4M3 = 1, 2
+
+
+@pytest.fixture(scope="module")
+def decide(tmp_path_factory):
+    build.build()
+    d = tmp_path_factory.mktemp("decide")
+    src, exe = d / "decide.cpp", d / "decide"
+    src.write_text(DECIDE)
+    cuda = os.path.dirname(os.path.dirname(build._nvcc()))
+    subprocess.run(["g++", "-std=c++17", "-I", build.CSRC, "-I", build.INCLUDE, "-I",
+                    os.path.join(cuda, "include"), str(src), build.LIB_PATH, "-o", str(exe),
+                    f"-Wl,-rpath,{os.path.dirname(build.LIB_PATH)}"], check=True)
+
+    def run(*args):
+        r = subprocess.run([str(exe)] + [str(a) for a in args], capture_output=True, text=True)
+        assert r.returncode == 0, (args, r.returncode, r.stderr)
+        return [int(v) for v in r.stdout.split()]
+    return run
+
+
+@pytest.mark.parametrize("code_type", [INT8, E4M3])
+@pytest.mark.parametrize("M,N,K,block_t,splits", [
+    (40, 64, 200, 96, 0),          # a tile of more tokens than there are
+    (40, 64, 200, 0, 4),           # more slices than K has blocks
+    (4096, 4096, 4096, 128, 4)])   # more tiles than clusters of eight are held
+def test_options_that_leave_no_tiling_end_in_none(decide, code_type, M, N, K, block_t, splits):
+    """The run then reports it; the choice itself must not divide by what it has not found."""
+    assert decide(M, N, K, code_type, block_t, splits)[0] == 0
+
+
+@pytest.mark.parametrize("block_t", [224, 256])
+def test_int8_has_no_tile_of_more_than_192_tokens(decide, block_t):
+    assert decide(1000, 64, 200, INT8, block_t, 0)[0] == 0
+    assert decide(1000, 64, 200, E4M3, block_t, 0)[0] == block_t
+
+
+@pytest.mark.parametrize("code_type", [INT8, E4M3])
+def test_free_choice_always_finds_a_tiling(decide, code_type):
+    for M in (1, 33, 256, 5000):
+        for N in (1, 300, 20000):
+            for K in (1, 129, 1000, 30000):
+                block_t, splits, stages, x_slots = decide(M, N, K, code_type, 0, 0)
+                assert block_t % 32 == 0 and 32 <= block_t < M + 32
+                assert 1 <= splits <= 4 and stages >= 2
+                assert x_slots >= 2 if code_type == INT8 else x_slots == 0
