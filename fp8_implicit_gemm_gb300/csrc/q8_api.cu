@@ -232,7 +232,7 @@ extern "C" conv3d_status linear_q8_plan_ex(linear_q8_plan_t* plan, long long max
   if (max_rows < 1 || N < 1 || K < 1 || !code_type_ok(code_type)) return CONV3D_EINVAL;
   linear_q8_options o{};
   if (opts) o = *opts;
-  if (o.kernel < 0 || o.kernel > 2 || o.block_t < 0 || o.block_t > kTcMaxTokens ||
+  if (o.kernel < 0 || o.kernel > 2 || o.block_t < 0 || o.block_t > tc_most_tokens(code_type) ||
       o.block_t % 32 != 0 || o.splits < 0 || o.splits > kTcMaxSplits ||
       o.max_ctas < 0 || o.wait_timeout_ms < 0)
     return CONV3D_EINVAL;

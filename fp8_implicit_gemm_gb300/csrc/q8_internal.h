@@ -86,6 +86,10 @@ constexpr int kTcChannels = 256;
 constexpr int kTcBlockK = 128;         // codes of K in a box
 constexpr int kTcMaxTokens = 256;
 constexpr int kTcMaxSplits = 4;
+// The most tokens of a tile: TMEM holds two accumulators, and for int8 two K blocks of w beside them.
+// (One accumulator of 256 tokens and four K blocks took 193 us for 4096 x 8192 x 4096, where two of 160
+// or 192 take 160: the epilogue's 8 us a tile are then not hidden.)
+constexpr int tc_most_tokens(int code_type) { return code_type == Q8_INT8 ? 192 : kTcMaxTokens; }
 // What a plan's device and options allow.
 struct TcLimits {
   int clusters[kTcMaxSplits];  // clusters of 2, 4, 6 and 8 CTAs held at once

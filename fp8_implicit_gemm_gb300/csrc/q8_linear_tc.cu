@@ -785,11 +785,6 @@ __global__ void __launch_bounds__(256) linear_expand_kernel(const LinearParams p
   }
 }
 
-// The most tokens of a tile: TMEM holds two accumulators, and for int8 two K blocks of w beside them.
-// (One accumulator of 256 tokens and four K blocks took 193 us for 4096 x 8192 x 4096, where two of 160
-// or 192 take 160: the epilogue's 8 us a tile are then not hidden.)
-static int tc_most_tokens(bool int8) { return int8 ? 192 : kTcMaxTokens; }
-
 // Boxes of 128 codes of a K block: two, where TMEM has room for two K blocks of w (int8).
 static int tc_boxes(bool int8, int t) { return int8 && t > 128 ? 1 : 2; }
 
@@ -802,7 +797,7 @@ void linear_tc_decide(LinearParams& p, int code_type, const TcLimits& lim) {
   // least 5.6t (e4m3, 256 codes); the last epilogue about 8 a token; joining slices about 20 a token
   // and 3500 for the cluster's barriers.
   double best = 1e300;
-  for (int t = 32; t <= tc_most_tokens(int8) && t < p.M + 32; t += 32) {
+  for (int t = 32; t <= tc_most_tokens(code_type) && t < p.M + 32; t += 32) {
     if (lim.block_t && t != lim.block_t) continue;
     const long long m_tiles = (p.M + t - 1) / t, tiles = m_tiles * p.n_tiles;
     const int boxes = tc_boxes(int8, t);

@@ -1,10 +1,11 @@
 """The host side of the 8-bit products' planning, as far as it goes without a GPU."""
+import ctypes
 import os
 import subprocess
 
 import pytest
 
-from fp8_implicit_gemm_gb300 import build
+from fp8_implicit_gemm_gb300 import build, capi
 
 # Asks for the tiling of M x N x K, with room for 76 clusters of each size.
 DECIDE = r"""
@@ -70,3 +71,10 @@ def test_free_choice_always_finds_a_tiling(decide, code_type):
                 assert block_t % 32 == 0 and 32 <= block_t < M + 32
                 assert 1 <= splits <= 4 and stages >= 2
                 assert x_slots >= 2 if code_type == INT8 else x_slots == 0
+
+
+@pytest.mark.parametrize("block_t", [224, 256])
+def test_plan_refuses_int8_tiles_of_more_than_192_tokens(block_t):
+    h, o = ctypes.c_void_p(1), capi.LinearOptions(block_t=block_t)
+    st = capi.load().linear_q8_plan_ex(ctypes.byref(h), 1000, 64, 200, INT8, 0, ctypes.byref(o))
+    assert st == capi.CONV3D_EINVAL and h.value is None
