@@ -107,7 +107,8 @@ class MlpQ8:
         return self.down(h, scale_h, y, stream)
 
     def check(self) -> int:
-        return self.gate_up.check() or self.down.check()
+        first, second = self.gate_up.check(), self.down.check()  # each clears what it reports
+        return first or second
 
     def close(self) -> None:
         self.gate_up.close()

@@ -5,7 +5,7 @@ import subprocess
 
 import pytest
 
-from fp8_implicit_gemm_gb300 import build, capi
+from fp8_implicit_gemm_gb300 import build, capi, q8
 
 # Asks for the tiling of M x N x K, with room for 76 clusters of each size.
 DECIDE = r"""
@@ -78,3 +78,24 @@ def test_plan_refuses_int8_tiles_of_more_than_192_tokens(block_t):
     h, o = ctypes.c_void_p(1), capi.LinearOptions(block_t=block_t)
     st = capi.load().linear_q8_plan_ex(ctypes.byref(h), 1000, 64, 200, INT8, 0, ctypes.byref(o))
     assert st == capi.CONV3D_EINVAL and h.value is None
+
+
+def test_block_check_reports_and_clears_both_products():
+    """A status is reported once: what the second product has to report is not left for a later
+    check when the first has something to report too."""
+    class Layer:
+        def __init__(self, *statuses):
+            self.statuses = list(statuses)
+
+        def check(self):
+            return self.statuses.pop(0) if self.statuses else capi.CONV3D_OK
+
+    mlp = q8.MlpQ8.__new__(q8.MlpQ8)
+    for first, second in ((capi.CONV3D_EDEVICE, capi.CONV3D_EDEVICE),
+                          (capi.CONV3D_EDEVICE, capi.CONV3D_OK),
+                          (capi.CONV3D_OK, capi.CONV3D_EDEVICE)):
+        mlp.gate_up, mlp.down = Layer(first), Layer(second)
+        assert mlp.check() == capi.CONV3D_EDEVICE
+        assert mlp.check() == capi.CONV3D_OK
+    mlp.gate_up, mlp.down = Layer(), Layer(capi.CONV3D_ECUDA)
+    assert mlp.check() == capi.CONV3D_ECUDA
