@@ -20,13 +20,16 @@ def empty_codes(rows: int, cols: int, dtype=torch.int8, device="cuda") -> torch.
 
 def quantise_rows(v: torch.Tensor, dtype=torch.int8) -> tuple[torch.Tensor, torch.Tensor]:
     """Codes and scales of a matrix's rows by torch operations, for weights, which are laid out
-    once (a step's activations get theirs from the norm or the activation)."""
+    once (a step's activations get theirs from the norm or the activation). A row that is not
+    finite gets the scale NaN and codes 0, as it does there."""
     top = 127.0 if dtype == torch.int8 else 448.0
     v = v.float()
     amax = v.abs().amax(dim=1)
     scale = torch.where(amax > 0, amax / top, torch.ones_like(amax))
+    finite = torch.isfinite(amax)
     q = empty_codes(*v.shape, dtype=dtype, device=v.device)
-    v = v / scale[:, None]
+    v = torch.where(finite[:, None], v / scale[:, None], 0.0)
+    scale = torch.where(finite, scale, torch.nan)
     q.copy_(v.round() if dtype == torch.int8 else v.clamp(-top, top))
     return q, scale
 

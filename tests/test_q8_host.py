@@ -4,6 +4,7 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 from fp8_implicit_gemm_gb300 import build, capi, q8
 
@@ -99,3 +100,17 @@ def test_block_check_reports_and_clears_both_products():
         assert mlp.check() == capi.CONV3D_OK
     mlp.gate_up, mlp.down = Layer(), Layer(capi.CONV3D_ECUDA)
     assert mlp.check() == capi.CONV3D_ECUDA
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.float8_e4m3fn])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_rows_that_are_not_finite_have_the_scale_nan_and_codes_0(dtype, bad):
+    """As the norm and the activation mark them, so that a product of such a row is NaN."""
+    v = torch.randn(4, 70, generator=torch.Generator().manual_seed(1))
+    q0, s0 = q8.quantise_rows(v, dtype)
+    v[2, 33] = bad
+    q, s = q8.quantise_rows(v, dtype)
+    keep = [0, 1, 3]
+    assert torch.equal(s[keep], s0[keep])
+    assert torch.equal(q[keep].view(torch.uint8), q0[keep].view(torch.uint8))
+    assert bool(torch.isnan(s[2])) and float(q[2].float().abs().max()) == 0.0
