@@ -28,7 +28,10 @@ def quantise_rows(v: torch.Tensor, dtype=torch.int8) -> tuple[torch.Tensor, torc
     scale = torch.where(amax > 0, amax / top, torch.ones_like(amax))
     finite = torch.isfinite(amax)
     q = empty_codes(*v.shape, dtype=dtype, device=v.device)
-    v = torch.where(finite[:, None], v / scale[:, None], 0.0)
+    # a row so small that its scale rounds coarsely, or to 0, is lifted for its quotients
+    lift = torch.where((amax > 0) & (amax < 2.0 ** -100), 2.0 ** 100, 1.0)
+    by = torch.where(amax > 0, amax * lift / top, torch.ones_like(amax))
+    v = torch.where(finite[:, None], v * lift[:, None] / by[:, None], 0.0)
     scale = torch.where(finite, scale, torch.nan)
     q.copy_(v.round() if dtype == torch.int8 else v.clamp(-top, top))
     return q, scale

@@ -114,3 +114,16 @@ def test_rows_that_are_not_finite_have_the_scale_nan_and_codes_0(dtype, bad):
     assert torch.equal(s[keep], s0[keep])
     assert torch.equal(q[keep].view(torch.uint8), q0[keep].view(torch.uint8))
     assert bool(torch.isnan(s[2])) and float(q[2].float().abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("dtype,top", [(torch.int8, 127.0), (torch.float8_e4m3fn, 448.0)])
+@pytest.mark.parametrize("size", [2.0 ** -126, 2.0 ** -135, 2.0 ** -142, 2.0 ** -149])
+def test_rows_whose_scale_is_subnormal_keep_their_codes(dtype, top, size):
+    """amax / top is then rounded coarsely, or to 0: the codes are those of the exact quotient all the
+    same. The values are powers of two, which every type holds, so that quotient is one of
+    top * 2^-k; the nearest code to it is within half a step (int8: 0.5, e4m3: 2^-4 of it)."""
+    v = torch.tensor([[1.0, -0.5, 0.25, 0.0]]) * size
+    q, _ = q8.quantise_rows(v, dtype)
+    t = v.double() / (size / top)
+    step = 0.5 if dtype == torch.int8 else t.abs() * 2.0 ** -4
+    assert bool(((q.float().double() - t).abs() <= step).all()), q.float().tolist()
