@@ -22,6 +22,9 @@ def quantise_rows(v: torch.Tensor, dtype=torch.int8) -> tuple[torch.Tensor, torc
     """Codes and scales of a matrix's rows by torch operations, for weights, which are laid out
     once (a step's activations get theirs from the norm or the activation). A row that is not
     finite gets the scale NaN and codes 0, as it does there."""
+    if capi.q8_code_type(dtype) == capi.Q8_E4M3 and dtype != torch.float8_e4m3fn:  # e4m3 bytes
+        q, scale = quantise_rows(v, torch.float8_e4m3fn)
+        return q.view(dtype), scale
     top = 127.0 if dtype == torch.int8 else 448.0
     v = v.float()
     amax = v.abs().amax(dim=1)

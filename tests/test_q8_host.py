@@ -127,3 +127,15 @@ def test_rows_whose_scale_is_subnormal_keep_their_codes(dtype, top, size):
     t = v.double() / (size / top)
     step = 0.5 if dtype == torch.int8 else t.abs() * 2.0 ** -4
     assert bool(((q.float().double() - t).abs() <= step).all()), q.float().tolist()
+
+
+def test_codes_as_bytes_are_e4m3():
+    """uint8 stands for e4m3 bytes, as it does in every call that takes codes; other types are refused."""
+    v = torch.randn(5, 70, generator=torch.Generator().manual_seed(2))
+    want, s0 = q8.quantise_rows(v, torch.float8_e4m3fn)
+    q, s = q8.quantise_rows(v, torch.uint8)
+    assert q.dtype == torch.uint8 and q.stride() == want.stride()
+    assert torch.equal(q, want.view(torch.uint8)) and torch.equal(s, s0)
+    for dtype in (torch.float16, torch.int32, torch.float8_e5m2):
+        with pytest.raises(ValueError):
+            q8.quantise_rows(v, dtype)
