@@ -32,7 +32,7 @@ def quantise_rows(v: torch.Tensor, dtype=torch.int8) -> tuple[torch.Tensor, torc
     finite = torch.isfinite(amax)
     q = empty_codes(*v.shape, dtype=dtype, device=v.device)
     # a row so small that its scale rounds coarsely, or to 0, is lifted for its quotients
-    lift = torch.where((amax > 0) & (amax < 2.0 ** -100), 2.0 ** 100, 1.0)
+    lift = torch.ones_like(amax).masked_fill_((amax > 0) & (amax < 2.0 ** -100), 2.0 ** 100)
     by = torch.where(amax > 0, amax * lift / top, torch.ones_like(amax))
     v = torch.where(finite[:, None], v * lift[:, None] / by[:, None], 0.0)
     scale = torch.where(finite, scale, torch.nan)

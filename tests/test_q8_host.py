@@ -139,3 +139,15 @@ def test_codes_as_bytes_are_e4m3():
     for dtype in (torch.float16, torch.int32, torch.float8_e5m2):
         with pytest.raises(ValueError):
             q8.quantise_rows(v, dtype)
+
+
+def test_codes_do_not_depend_on_the_default_type():
+    v = torch.randn(3, 40, generator=torch.Generator().manual_seed(3))
+    v[1] *= 1e-43
+    want = q8.quantise_rows(v)
+    torch.set_default_dtype(torch.float16)
+    try:
+        got = q8.quantise_rows(v)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
