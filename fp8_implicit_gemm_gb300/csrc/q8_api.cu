@@ -370,10 +370,10 @@ extern "C" size_t linear_q8_workspace_size(linear_q8_plan_t plan) {
 
 extern "C" void linear_q8_destroy(linear_q8_plan_t plan) {
   if (!plan) return;
-  if (plan->workspace) {
+  {
     DeviceRestore restore;
     if (cudaSetDevice(plan->device) == cudaSuccess) {
-      cudaDeviceSynchronize();
+      cudaDeviceSynchronize();  // without a workspace too: the runs read the caller's memory
       cudaFree(plan->workspace);
     }
     cudaGetLastError();
