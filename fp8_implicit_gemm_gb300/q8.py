@@ -50,6 +50,8 @@ class LinearQ8:
         self._plan = 0
         if w.stride(1) != 1 or w.stride(0) % 32 or w.data_ptr() % 32:
             w = empty_codes(*w.shape, dtype=w.dtype, device=w.device).copy_(w)
+            if w.is_cuda:  # in place for calls on every stream
+                torch.cuda.current_stream(w.device).synchronize()
         # tensors of its own on the same memory: what the caller does to its own ones later frees none
         # of what the calls read
         self.w, self.scale_w = w.detach(), scale_w.detach()
@@ -94,6 +96,7 @@ class MlpQ8:
         self.gate_up = LinearQ8(*quantise_rows(w_gate_up, codes), max_rows=max_rows)
         self.down = LinearQ8(*quantise_rows(w_down, codes), max_rows=max_rows)
         dev = w_down.device
+        torch.cuda.current_stream(dev).synchronize()  # the codes are in place for calls on every stream
         self._a = empty_codes(max_rows, dim, codes, dev)
         self._h = empty_codes(max_rows, inner, codes, dev)
         self._scale_a = torch.empty(max_rows, dtype=torch.float32, device=dev)
