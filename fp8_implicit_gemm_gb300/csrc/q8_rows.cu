@@ -17,6 +17,14 @@ namespace c3d {
 
 constexpr int kChunk = 8;  // values a thread takes at a time: 16 bytes of a 16-bit type
 
+// Squares of values below about 2^-50 lose bits in fp32, or all of them. Beside an eps of kSmallEps or more
+// that changes nothing. With a smaller one (0, mostly) small_rows_kernel first takes the sum of values
+// lifted by kRowLift, and it counts (kSmall) for rows whose plain sum is below kLiftBelow, where no lifted
+// square overflows. It is a launch of its own (1 x 4096 bf16 2.1 -> 3.1 us, 8192 x 4096 37.4 -> 39.4, 40000 x
+// 256 13.6 -> 18.9): taken in the norm's kernels, under a condition that other calls do not meet, it
+// cost those their registers (8192 x 4098 bf16 42 -> 57 us).
+constexpr float kSmallEps = 0x1p-120f, kRowLift = 0x1p100f, kLiftBelow = 0x1p-100f;
+
 // amax(|v|) as bits: unsigned order is the order of the magnitudes, and a NaN is above them all, so
 // that one NaN or infinity marks the row.
 struct RowStat {
@@ -219,29 +227,33 @@ struct RowCode {
 // alone, so only that thread works it out. A row that is not finite gets the scale NaN and codes 0
 // (its values must be replaced by 0 before they are multiplied). A row so small that top / amax would
 // overflow is lifted first.
-template <bool kNorm>
+template <bool kNorm, bool kSmall>
 __device__ __forceinline__ RowCode row_scale(const RowStat& st, const RowsParams& p, long long row,
                                              bool writer, bool& bad) {
   const float top = p.code_type == Q8_E4M3 ? 448.0f : 127.0f;
   bad = st.amax >= 0x7F800000u || !(st.sum < INFINITY);
   const float amax = __uint_as_float(st.amax);
   if (writer) {
-    const float gain = kNorm ? rsqrtf(st.sum / (float)p.cols + p.eps) : 1.0f;
-    p.scale[row] = bad ? __int_as_float(0x7FC00000) : (amax > 0.0f ? amax * gain / top : 1.0f);
+    float root = kNorm ? amax * rsqrtf(st.sum / (float)p.cols + p.eps) : amax;
+    if (kSmall && st.sum < kLiftBelow) {
+      const float gain = rsqrtf(p.scale[row] / (float)p.cols + p.eps * kRowLift * kRowLift);
+      root = amax < 1.0f ? amax * kRowLift * gain : amax * gain * kRowLift;
+    }
+    p.scale[row] = bad ? __int_as_float(0x7FC00000) : (amax > 0.0f ? root / top : 1.0f);
   }
   RowCode c;
-  c.lift = amax < 0x1p-100f ? 0x1p100f : 1.0f;
+  c.lift = amax < 0x1p-100f ? kRowLift : 1.0f;
   c.inv = bad || amax == 0.0f ? 0.0f : top / (amax * c.lift);
   return c;
 }
 
 // Codes and scale of one row whose values the threads hold.
-template <int NV, bool kNorm>
+template <int NV, bool kNorm, bool kSmall>
 __device__ __forceinline__ void row_write(float (&v)[NV][kChunk], const RowStat& st,
                                           const RowsParams& p, long long row, const Place& at,
                                           bool tail) {
   bool bad;
-  const RowCode rc = row_scale<kNorm>(st, p, row, at.tid == 0, bad);
+  const RowCode rc = row_scale<kNorm, kSmall>(st, p, row, at.tid == 0, bad);
   if (bad || rc.lift != 1.0f) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -315,7 +327,7 @@ constexpr int rows_max_threads(int nv) {  // 64 registers a thread, or 128
   return nv == 1 || (nv == 2 && sizeof(T) == 2) ? 1024 : 512;
 }
 
-template <typename T, int NV, bool kNorm>
+template <typename T, int NV, bool kNorm, bool kSmall>
 __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const RowsParams p) {
   constexpr bool kAhead = NV <= 2;
   pdl_wait_primary();
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(rows_max_threads<T>(NV)) rows_q8_kernel(const 
     if (kAhead && row + stride < p.rows) load_row(row + stride);
     st.sum = sum.x + sum.y;
     st = row_reduce(st, p.row_threads, buffer);
-    row_write<NV, kNorm>(v, st, p, row, at, tail);
+    row_write<NV, kNorm, kSmall>(v, st, p, row, at, tail);
   }
 }
 
@@ -497,7 +509,7 @@ __device__ __forceinline__ void loose_codes(const float* f, int code_type, float
   }
 }
 
-template <typename T, bool kNorm, int kPair>
+template <typename T, bool kNorm, bool kSmall, int kPair>
 __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(1024) rows_q8_loose_kernel(const RowsParams p)
     if (row + gridDim.x < p.rows) load_row(row + gridDim.x);
     st = row_reduce(st, threads, buffer);
     bool bad;
-    const RowCode rc = row_scale<kNorm>(st, p, row, tid == 0, bad);
+    const RowCode rc = row_scale<kNorm, kSmall>(st, p, row, tid == 0, bad);
     if (bad) {
 #pragma unroll
       for (int e = 0; e < kLoose; ++e) v[e] = 0.0f;
@@ -649,7 +661,7 @@ __device__ __forceinline__ void wide_codes(uint8_t* q, const RowsParams& p, int 
 
 // (The activation is held to the 32 registers that let four blocks share an SM: 4096 x 12002 bf16 48 us,
 // 51 with the 40 it takes otherwise.)
-template <typename T, bool kNorm, int kPair>
+template <typename T, bool kNorm, bool kSmall, int kPair>
 __global__ void __launch_bounds__(kWideThreads, kNorm ? 0 : 4) rows_q8_wide_kernel(const RowsParams p) {
   extern __shared__ __align__(16) float v[];
   pdl_wait_primary();
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(kWideThreads, kNorm ? 0 : 4) rows_q8_wide_kern
     }
     st = row_reduce(st, kWideThreads, buffer);
     bool bad;
-    const RowCode rc = row_scale<kNorm>(st, p, row, threadIdx.x == 0, bad);
+    const RowCode rc = row_scale<kNorm, kSmall>(st, p, row, threadIdx.x == 0, bad);
     uint8_t* q = p.q + row * p.q_pitch;
     for (int c = first; c < p.cols; c += kWideThreads * kLoose) {
       if (c + kRun <= p.cols)
@@ -677,6 +689,35 @@ __global__ void __launch_bounds__(kWideThreads, kNorm ? 0 : 4) rows_q8_wide_kern
       else
         wide_codes<false, kPair>(q, p, c + lane, v, bad, rc);
     }
+  }
+}
+
+// For each row of small values, the sum of their lifted squares in place of its scale, where row_scale
+// finds it. A warp takes a row and leaves it at the first value whose square alone makes the plain sum
+// good: of ordinary rows no more than the first columns are read.
+template <typename T>
+__global__ void __launch_bounds__(128) small_rows_kernel(const RowsParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long stride = (long long)gridDim.x * 4;
+  for (long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); row < p.rows; row += stride) {
+    const T* a = static_cast<const T*>(p.a) + row * p.a_pitch;
+    const T* b = p.b ? static_cast<const T*>(p.b) + row * p.b_pitch : nullptr;
+    float sum = 0.0f;
+    bool small = true;
+    for (int c0 = 0, end = 32; small && c0 < p.cols; c0 = end, end += 1024) {
+      bool mine = true;
+#pragma unroll 8
+      for (int c = c0 + lane; c < min(end, p.cols); c += 32) {
+        const float h = q8_to_float(a[c]) + (b ? q8_to_float(b[c]) : 0.0f);
+        mine = mine && fabsf(h) < 0x1p-49f;
+        sum = fmaf(h * kRowLift, h * kRowLift, sum);
+      }
+      small = __all_sync(0xFFFFFFFFu, mine);
+    }
+    const RowStat st = warp_reduce(RowStat{sum, 0u});
+    if (small && lane == 0) p.scale[row] = st.sum;
   }
 }
 
@@ -708,53 +749,57 @@ static cudaError_t launch_rows(Kernel kernel, const RowsParams& p, int threads, 
 // limit belongs to the kernel, so were it set to a call's own size, another host thread's call could
 // lower it between that and the launch. (A row's values have row_reduce's 512 bytes beside them, and
 // the limit that holds unless it is raised counts both.)
-template <typename T, bool kNorm, int kPair>
+template <typename T, bool kNorm, bool kSmall, int kPair>
 static cudaError_t launch_wide(RowsParams& p, cudaStream_t stream) {
-  constexpr auto kernel = rows_q8_wide_kernel<T, kNorm, kPair>;
+  constexpr auto kernel = rows_q8_wide_kernel<T, kNorm, kSmall, kPair>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              Q8_MAX_COLS * (int)sizeof(float));
   if (e != cudaSuccess) return e;
   p.row_threads = kWideThreads;
   return launch_rows(kernel, p, kWideThreads, p.cols * sizeof(float), stream);
 }
-template <typename T, bool kNorm, int kPair>
+template <typename T, bool kNorm, bool kSmall, int kPair>
 static cudaError_t launch_loose(RowsParams& p, cudaStream_t stream) {
-  if (p.cols > 1024 * kLoose) return launch_wide<T, kNorm, kPair>(p, stream);
+  if (p.cols > 1024 * kLoose) return launch_wide<T, kNorm, kSmall, kPair>(p, stream);
   p.row_threads = std::max(64, (p.cols + kRun - 1) / kRun * 32);  // one row a block
-  return launch_rows(rows_q8_loose_kernel<T, kNorm, kPair>, p, p.row_threads, 0, stream);
+  return launch_rows(rows_q8_loose_kernel<T, kNorm, kSmall, kPair>, p, p.row_threads, 0, stream);
 }
 
-template <typename T, bool kNorm>
+template <typename T, bool kNorm, bool kSmall>
 static cudaError_t launch_typed(RowsParams& p, RowsGrid grid, cudaStream_t stream) {
-  if (grid == RowsGrid::kElement) return launch_loose<T, kNorm, 1>(p, stream);
-  if (grid == RowsGrid::kPair) return launch_loose<T, kNorm, 2>(p, stream);
+  if (grid == RowsGrid::kElement) return launch_loose<T, kNorm, kSmall, 1>(p, stream);
+  if (grid == RowsGrid::kPair) return launch_loose<T, kNorm, kSmall, 2>(p, stream);
   const int chunks = (p.cols + kChunk - 1) / kChunk;
   const bool wide = chunks > 2 * rows_max_threads<T>(2);
   if constexpr (sizeof(T) == 4)
     if (wide)
-      return p.cols % 4 == 0   ? launch_wide<T, kNorm, 4>(p, stream)
-             : p.cols % 2 == 0 ? launch_wide<T, kNorm, 2>(p, stream)
-                               : launch_wide<T, kNorm, 1>(p, stream);
+      return p.cols % 4 == 0   ? launch_wide<T, kNorm, kSmall, 4>(p, stream)
+             : p.cols % 2 == 0 ? launch_wide<T, kNorm, kSmall, 2>(p, stream)
+                               : launch_wide<T, kNorm, kSmall, 1>(p, stream);
   // One chunk a thread where there are few rows, whose time is one row's latency; otherwise two.
   const int nv = wide ? 8 : chunks > rows_max_threads<T>(1) || (p.rows > 304 && chunks > 32) ? 2 : 1;
   p.row_threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
   const int threads = p.row_threads == 32 ? 128 : p.row_threads;
-  if (nv == 1) return launch_rows(rows_q8_kernel<T, 1, kNorm>, p, threads, 0, stream);
+  if (nv == 1) return launch_rows(rows_q8_kernel<T, 1, kNorm, kSmall>, p, threads, 0, stream);
   if constexpr (sizeof(T) == 2)
-    if (wide) return launch_rows(rows_q8_kernel<T, 8, kNorm>, p, threads, 0, stream);
-  return launch_rows(rows_q8_kernel<T, 2, kNorm>, p, threads, 0, stream);
+    if (wide) return launch_rows(rows_q8_kernel<T, 8, kNorm, kSmall>, p, threads, 0, stream);
+  return launch_rows(rows_q8_kernel<T, 2, kNorm, kSmall>, p, threads, 0, stream);
+}
+
+template <typename T>
+static cudaError_t launch_type(RowsParams& p, bool norm, RowsGrid grid, cudaStream_t stream) {
+  if (!norm) return launch_typed<T, false, false>(p, grid, stream);
+  if (p.eps >= kSmallEps) return launch_typed<T, true, false>(p, grid, stream);
+  p.row_threads = 32;
+  const cudaError_t e = launch_rows(small_rows_kernel<T>, p, 128, 0, stream);
+  return e != cudaSuccess ? e : launch_typed<T, true, true>(p, grid, stream);
 }
 
 cudaError_t launch_rows_q8(RowsParams p, int value_type, bool norm, RowsGrid grid,
                            cudaStream_t stream) {
-  if (value_type == Q8_F32)
-    return norm ? launch_typed<float, true>(p, grid, stream)
-                : launch_typed<float, false>(p, grid, stream);
-  if (value_type == Q8_BF16)
-    return norm ? launch_typed<__nv_bfloat16, true>(p, grid, stream)
-                : launch_typed<__nv_bfloat16, false>(p, grid, stream);
-  return norm ? launch_typed<__half, true>(p, grid, stream)
-              : launch_typed<__half, false>(p, grid, stream);
+  if (value_type == Q8_F32) return launch_type<float>(p, norm, grid, stream);
+  if (value_type == Q8_BF16) return launch_type<__nv_bfloat16>(p, norm, grid, stream);
+  return launch_type<__half>(p, norm, grid, stream);
 }
 
 }  // namespace c3d

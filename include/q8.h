@@ -43,7 +43,8 @@ typedef enum { Q8_INT8 = 1, Q8_E4M3 = 2 } q8_code_type;
  *   h = x + residual (in fp32; h = x without a residual), residual_out = h rounded to value_type,
  *   y = h / sqrt(sum(h^2) / cols + eps) * weight, q and scale = the codes of y.
  * y is taken from the unrounded h. residual_out may be x or residual itself (same pitch); apart
- * from that no output may overlap an input.
+ * from that no output may overlap an input. With an eps below 2^-120 (0, mostly) the squares of small
+ * values would underflow beside it: their sum is then taken of lifted values, by a second launch.
  * Errors: EINVAL (NULL x, weight, q or scale with rows > 0; a residual without residual_out or the
  * reverse; rows < 0, cols < 1, a pitch below cols, an unknown type, a pointer that is not aligned to
  * its element, eps negative or not finite, `device` not the current device), EUNSUPPORTED
