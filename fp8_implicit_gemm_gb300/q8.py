@@ -110,6 +110,9 @@ class MlpQ8:
         rows = x.shape[0]
         if rows > self.max_rows:
             raise ValueError(f"{rows} rows, planned for up to {self.max_rows}")
+        # y is the last call's argument: refused here, before the first one has updated the residual
+        capi._q8_pitch(y, "y", x.shape, x.get_device())
+        capi._q8_value_type(y, "y")
         a, scale_a, gu = self._a[:rows], self._scale_a[:rows], self._gu[:rows]
         h, scale_h = self._h[:rows], self._scale_h[:rows]
         capi.rmsnorm_q8_run(x, self.norm_weight, a, scale_a, self.eps, residual=residual,
