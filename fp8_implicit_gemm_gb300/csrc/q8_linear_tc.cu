@@ -905,7 +905,7 @@ static cudaError_t launch_pdl(Kernel kernel, int grid, int block, int cluster, s
 cudaError_t launch_linear_expand(const LinearParams& p, cudaStream_t stream) {
   const long long per_row = (p.K + 15) / 16 * 2;
   const long long blocks = p.M * ((per_row + 256 * kExpand - 1) / (256 * kExpand));
-  const int grid = (int)std::min<long long>(blocks, 152 * 8);
+  const int grid = (int)std::min<long long>(blocks, 152 * 8);  // eight blocks an SM of this device
   return launch_pdl(linear_expand_kernel, grid, 256, 1, 0, stream, p);
 }
 

@@ -43,7 +43,9 @@ def quantise_rows(v: torch.Tensor, dtype=torch.int8) -> tuple[torch.Tensor, torc
 class LinearQ8:
     """y = (x * w^T) scaled by token and channel, plus a bias. Owns a plan for up to max_rows tokens
     and keeps the weights' codes (copied once if their rows do not lie on 32-byte boundaries, as the
-    kernels read them fastest). One call at a time: a plan's workspace is shared by its runs."""
+    kernels read them fastest: what the caller changes in its own tensor later then does not reach the
+    layer; scales and bias, and codes laid out so, stay the caller's memory). One call at a time: a
+    plan's workspace is shared by its runs. For int8 codes it takes 2 * max_rows * K bytes."""
 
     def __init__(self, w: torch.Tensor, scale_w: torch.Tensor, bias: torch.Tensor | None = None,
                  max_rows: int = 8192):
@@ -85,7 +87,8 @@ class MlpQ8:
 
         residual += x;  a = norm(residual);  g, u = a * w_gate_up^T;  y = (silu(g) * u) * w_down^T
 
-    four launches of the library a call, in the caller's buffers and its own (made once)."""
+    four calls of the library, in the caller's buffers and its own (made once): as many launches, and one
+    more for each product of int8 codes on the tensor cores."""
 
     def __init__(self, norm_weight, w_gate_up, w_down, max_rows=8192, codes=torch.int8, eps=1e-6):
         dim, inner = w_down.shape
