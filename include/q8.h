@@ -49,7 +49,8 @@ typedef enum { Q8_INT8 = 1, Q8_E4M3 = 2 } q8_code_type;
  * Errors: EINVAL (NULL x, weight, q or scale with rows > 0; a residual without residual_out or the
  * reverse; rows < 0, cols < 1, a pitch below cols, an unknown type, a pointer that is not aligned to
  * its element, eps negative or not finite, `device` not the current device), EUNSUPPORTED
- * (cols > Q8_MAX_COLS, a device that is not sm_103), ECUDA. rows == 0 does nothing.
+ * (cols > Q8_MAX_COLS, rows of 2^31 or more, a device that is not sm_103), ECUDA. rows == 0 does
+ * nothing.
  */
 typedef struct {
     const void *x;              /* [rows][cols] value_type */
