@@ -1,5 +1,5 @@
-"""ctypes binding of the C ABI in ``include/conv3d_fp8.h`` and ``include/q8.h`` (argument
-marshalling only).
+"""ctypes binding of the C ABI in ``include/conv3d_fp8.h``, ``include/q8.h`` and
+``include/q8_attention.h`` (argument marshalling only).
 
 Every entry point keeps its C name. Tensors are passed as raw device pointers (``data_ptr()``);
 torch is only used for device memory and streams. There is no fallback of any kind: if the CUDA
@@ -145,6 +145,24 @@ def load() -> ctypes.CDLL:
             lib.linear_q8_workspace_size.argtypes = [vp]
             lib.linear_q8_destroy.restype = None
             lib.linear_q8_destroy.argtypes = [vp]
+            for name in ("heads_q8_run", "cache_q8_read_run"):
+                getattr(lib, name).restype = ci
+                getattr(lib, name).argtypes = [ctypes.c_char_p]
+            lib.attn_q8_plan.restype = ci
+            lib.attn_q8_plan.argtypes = [ctypes.POINTER(vp), cq] + [ci] * 6
+            lib.attn_prompt_plan.restype = ci
+            lib.attn_prompt_plan.argtypes = [ctypes.POINTER(vp), ci]
+            for name in ("attn_q8_run", "attn_prompt_run"):
+                getattr(lib, name).restype = ci
+                getattr(lib, name).argtypes = [vp, ctypes.c_char_p]
+            for name in ("attn_q8_check", "attn_prompt_check"):
+                getattr(lib, name).restype = ci
+                getattr(lib, name).argtypes = [vp]
+            lib.attn_q8_workspace_size.restype = ctypes.c_size_t
+            lib.attn_q8_workspace_size.argtypes = [vp]
+            for name in ("attn_q8_destroy", "attn_prompt_destroy"):
+                getattr(lib, name).restype = None
+                getattr(lib, name).argtypes = [vp]
             _lib = lib
     return _lib
 
@@ -651,3 +669,276 @@ def linear_q8_workspace_size(plan) -> int:
 def linear_q8_destroy(plan) -> None:
     if plan:
         load().linear_q8_destroy(plan)
+
+
+# -------------------------------------- heads, caches and attention (include/q8_attention.h)
+Q8_INT4 = 3
+
+_CACHE = struct.Struct("@4Pq4i")
+_HEADS_ARGS = struct.Struct("@12P12qP9if")
+_CACHE_READ_ARGS = struct.Struct("@4P5qP2i")
+_ATTN_ARGS = struct.Struct("@5P7qP3if")
+_ATTN_PROMPT_ARGS = struct.Struct("@6P11qP5if")
+
+
+def cache_q8(k_codes, k_scale, v_codes, v_scale) -> tuple:
+    """What the calls on a cache need of its tensors, checked once: codes [pages, kv_heads, page_size,
+    head_dim] (int8, float8_e4m3fn, or uint8 e4m3 bytes) with scales [pages, kv_heads, page_size], or 4-bit codes
+    [.., head_dim / 2] uint8 with scales [pages, kv_heads, page_size, 2]. The caller keeps the tensors alive
+    and where they are, and the tuple as long as it is used."""
+    _q8 or _q8_setup()
+    shape, device = k_codes.shape, k_codes.get_device()
+    if len(shape) != 4:
+        raise ValueError("k_codes: expected [pages, kv_heads, page_size, head_dim]")
+    if device < 0:
+        raise ValueError("k_codes: expected a CUDA tensor")
+    pages, kv_heads, page_size, width = shape
+    four = k_scale.dim() == 4
+    if four:
+        import torch
+        if k_codes.dtype != torch.uint8:
+            raise ValueError(f"k_codes: 4-bit codes lie in uint8 bytes, not {k_codes.dtype}")
+        code_type, head_dim = Q8_INT4, 2 * width
+    else:
+        code_type, head_dim = q8_code_type(k_codes.dtype), width
+    for t, name, want, dtype in ((k_codes, "k_codes", shape, k_codes.dtype),
+                                 (v_codes, "v_codes", shape, k_codes.dtype),
+                                 (k_scale, "k_scale", shape[:3] + (2,) * four, _f32),
+                                 (v_scale, "v_scale", shape[:3] + (2,) * four, _f32)):
+        if t.shape != want or t.dtype != dtype or not t.is_contiguous() or t.get_device() != device:
+            raise ValueError(f"{name}: expected {tuple(want)}, contiguous, {dtype}, on CUDA device {device}")
+    packed = ctypes.create_string_buffer(_CACHE.pack(
+        k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page_size,
+        kv_heads, head_dim, code_type), _CACHE.size)
+    return ctypes.addressof(packed), kv_heads, head_dim, code_type, device, packed
+
+
+def _heads(t, name, shape, dtype, device):
+    """Address, pitch and head pitch of a matrix of heads [tokens, heads, head_dim]."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+        raise ValueError(f"{name}: expected {tuple(shape)}, {dtype}, on CUDA device {device}, got "
+                         f"{tuple(t.shape)}, {t.dtype}, device {t.get_device()}")
+    pitch, head_pitch, step = t.stride()
+    if step != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: expected contiguous heads")
+    return t.data_ptr(), pitch, head_pitch
+
+
+_NO_HEADS = (0, 0, 0)
+
+
+def _i64(t, name, size, device):
+    """Address of a contiguous int64 vector."""
+    import torch
+    return _q8_vector(t, name, size, device, torch.int64)
+
+
+def heads_q8_run(q=None, q_out=None, k=None, k_out=None, v=None, q_weight=None, k_weight=None,
+                 eps=1e-6, rotary=None, positions=None, cache=None, slots=None, stream=None) -> None:
+    """Query and key heads [tokens, heads, head_dim] normed (with a weight [head_dim]), rotated (with a
+    q8.Rotary and positions [tokens] or [axes, tokens], int64) and written to q_out and k_out; with a
+    cache (q8.CacheQ8, or cache_q8's tuple) k's codes and v's go to the tokens' slots (int64). See
+    heads_q8_run in include/q8_attention.h."""
+    lib = _q8 or _q8_setup()
+    if q is not None and k is not None and q.shape[1] == 0:  # a product that left keys and values only
+        q = q_out = None
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("expected q or k")
+    if len(lead.shape) != 3:
+        raise ValueError("expected heads [tokens, heads, head_dim]")
+    tokens, _, dim = lead.shape
+    dtype, device = lead.dtype, lead.get_device()
+    if device < 0:
+        raise ValueError("expected CUDA tensors")
+    value_type = _q8_value_type(lead, "q" if q is not None else "k")
+    qs = qo = ks = ko = vs = _NO_HEADS
+    q_heads = kv_heads = weight_type = qw = kw = 0
+    if q is not None:
+        shape = q.shape
+        q_heads = shape[1]
+        qs = _heads(q, "q", shape, dtype, device)
+        if q_out is None:
+            raise ValueError("q_out: expected with q")
+        qo = qs if q_out is q else _heads(q_out, "q_out", shape, dtype, device)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q: expected with q_out or q_weight")
+    if k is not None:
+        if len(k.shape) != 3:
+            raise ValueError("k: expected [tokens, heads, head_dim]")
+        shape = (tokens, k.shape[1], dim)
+        kv_heads = k.shape[1]
+        ks = _heads(k, "k", shape, dtype, device)
+        if k_out is not None:
+            ko = ks if k_out is k else _heads(k_out, "k_out", shape, dtype, device)
+        if v is not None:
+            vs = _heads(v, "v", shape, dtype, device)
+    elif k_out is not None or k_weight is not None or v is not None:
+        raise ValueError("k: expected with k_out, k_weight or v")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            t = _q8_value_type(w, name)
+            if weight_type and t != weight_type:
+                raise ValueError("q_weight and k_weight: expected one type")
+            weight_type = t
+    if q_weight is not None:
+        qw = _q8_vector(q_weight, "q_weight", dim, device)
+    if k_weight is not None:
+        kw = _q8_vector(k_weight, "k_weight", dim, device)
+    turns = axis = rot = pos = pos_pitch = adjacent = 0
+    axes = 1
+    if rotary is not None:
+        turns, axis, rot, axes, adjacent, rotary_device = rotary.table
+        if rotary_device != device:
+            raise ValueError(f"rotary: expected one on CUDA device {device}")
+        if positions is None:
+            raise ValueError("positions: expected with a rotary")
+        shape = positions.shape
+        if len(shape) == 1 and axes == 1:
+            pos = _i64(positions, "positions", tokens, device)
+        else:
+            import torch
+            if (shape != (axes, tokens) or positions.dtype != torch.int64 or positions.get_device() != device
+                    or (tokens > 1 and positions.stride(1) != 1)):
+                raise ValueError(f"positions: expected ({axes}, {tokens}), int64, on CUDA device {device}")
+            pos, pos_pitch = positions.data_ptr(), positions.stride(0)
+    elif positions is not None:
+        raise ValueError("rotary: expected with positions")
+    cache_ptr = slot_ptr = 0
+    if cache is not None:
+        cache = getattr(cache, "parts", cache)
+        if slots is None or v is None:
+            raise ValueError("v and slots: expected with a cache")
+        if cache[4] != device:
+            raise ValueError(f"cache: expected one on CUDA device {device}")
+        cache_ptr, slot_ptr = cache[0], _i64(slots, "slots", tokens, device)
+    elif slots is not None or v is not None:
+        raise ValueError("cache: expected with v or slots")
+    if tokens == 0:
+        return
+    status = lib.heads_q8_run(_HEADS_ARGS.pack(
+        qs[0], qo[0], ks[0], ko[0], vs[0], qw, kw, turns, axis, pos, slot_ptr, cache_ptr, qs[1], qs[2], qo[1],
+        qo[2], ks[1], ks[2], ko[1], ko[2], vs[1], vs[2], pos_pitch, tokens, _q8_stream(stream, device), q_heads,
+        kv_heads, dim, rot, axes, adjacent, value_type, weight_type, device, eps))
+    if status:
+        _raise(status, "heads_q8_run")
+
+
+def cache_q8_read_run(cache, slots, k, v, stream=None) -> None:
+    """k and v [tokens, kv_heads, head_dim] = the cache's values at the slots [tokens] (int64); rows of
+    slots outside the cache stay as they were."""
+    lib = _q8 or _q8_setup()
+    cache_ptr, kv_heads, dim, _, device, _ = getattr(cache, "parts", cache)
+    tokens = slots.shape[0]
+    shape = (tokens, kv_heads, dim)
+    ks, vs = _heads(k, "k", shape, k.dtype, device), _heads(v, "v", shape, k.dtype, device)
+    status = lib.cache_q8_read_run(_CACHE_READ_ARGS.pack(
+        cache_ptr, _i64(slots, "slots", tokens, device), ks[0], vs[0], ks[1], ks[2], vs[1], vs[2], tokens,
+        _q8_stream(stream, device), _q8_value_type(k, "k"), device))
+    if status:
+        _raise(status, "cache_q8_read_run")
+
+
+def attn_q8_plan(max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type, device=0) -> int:
+    """Create a plan for attention of up to max_tokens newest tokens of each of up to max_seqs sequences
+    over a cache (code_type: Q8_INT8, Q8_E4M3 or Q8_INT4); returns its handle."""
+    h = ctypes.c_void_p()
+    _raise(load().attn_q8_plan(ctypes.byref(h), max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type,
+                               device), "attn_q8_plan")
+    return h.value
+
+
+def _i32(t, name, device):
+    """Refuses what is not int32 on the device with contiguous rows."""
+    import torch
+    if t.dtype != torch.int32 or t.get_device() != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: expected contiguous int32 on CUDA device {device}")
+
+
+def attn_q8_run(plan, q, cache, table, lengths, o, scale, tokens=1, stream=None) -> None:
+    """o = attention of q [seqs * tokens, q_heads, head_dim] over the cache: sequence b's place s lies in page
+    table[b, s // page_size] (int32 [seqs, width]), lengths [seqs] (int32) count the newest tokens too. See
+    attn_q8_run in include/q8_attention.h."""
+    lib = _q8 or _q8_setup()
+    cache_ptr, _, dim, _, device, _ = getattr(cache, "parts", cache)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != dim or len(table.shape) != 2:
+        raise ValueError(f"expected q [seqs * tokens, q_heads, {dim}] and table [seqs, width]")
+    seqs, width = table.shape
+    if shape[0] != seqs * tokens or lengths.shape != (seqs,):
+        raise ValueError(f"expected {seqs} lengths and {seqs * tokens} rows of q, got "
+                         f"{tuple(lengths.shape)} and {shape[0]}")
+    dtype = q.dtype
+    qs = _heads(q, "q", shape, dtype, device)
+    os_ = qs if o is q else _heads(o, "o", shape, dtype, device)
+    _i32(table, "table", device)
+    _i32(lengths, "lengths", device)
+    status = lib.attn_q8_run(plan, _ATTN_ARGS.pack(
+        cache_ptr, qs[0], os_[0], table.data_ptr(), lengths.data_ptr(), qs[1], qs[2], os_[1], os_[2], seqs, width,
+        table.stride(0), _q8_stream(stream, device), tokens, shape[1], _q8_value_type(q, "q"), scale))
+    if status:
+        _raise(status, "attn_q8_run")
+
+
+def attn_q8_check(plan) -> int:
+    """Synchronise and return (and clear) the plan's device status: CONV3D_OK or CONV3D_EDEVICE."""
+    return load().attn_q8_check(plan)
+
+
+def attn_q8_workspace_size(plan) -> int:
+    return int(load().attn_q8_workspace_size(plan))
+
+
+def attn_q8_destroy(plan) -> None:
+    if plan:
+        load().attn_q8_destroy(plan)
+
+
+def attn_prompt_plan(device=0) -> int:
+    """Create a plan for attention over prompts; returns its handle."""
+    h = ctypes.c_void_p()
+    _raise(load().attn_prompt_plan(ctypes.byref(h), device), "attn_prompt_plan")
+    return h.value
+
+
+def attn_prompt_run(plan, q, k, v, starts, o, scale, causal=True, key_starts=None, stream=None) -> None:
+    """o = attention of packed sequences: q [q_rows, q_heads, head_dim], k and v [k_rows, kv_heads,
+    head_dim], starts (and key_starts) [seqs + 1] int32. See attn_prompt_run in include/q8_attention.h."""
+    lib = _q8 or _q8_setup()
+    device, dtype, shape = q.get_device(), q.dtype, q.shape
+    if len(shape) != 3 or len(k.shape) != 3:
+        raise ValueError("expected heads [rows, heads, head_dim]")
+    if device < 0:
+        raise ValueError("q: expected a CUDA tensor")
+    rows, heads, dim = shape
+    k_rows, kv_heads, _ = k.shape
+    k_shape = (k_rows, kv_heads, dim)
+    qs, os_ = _heads(q, "q", shape, dtype, device), _heads(o, "o", shape, dtype, device)
+    ks, vs = _heads(k, "k", k_shape, dtype, device), _heads(v, "v", k_shape, dtype, device)
+    if len(starts.shape) != 1 or starts.shape[0] < 1:
+        raise ValueError("starts: expected [seqs + 1]")
+    _i32(starts, "starts", device)
+    ks_ptr = 0
+    if key_starts is not None:
+        if key_starts.shape != starts.shape:
+            raise ValueError("key_starts: expected the shape of starts")
+        _i32(key_starts, "key_starts", device)
+        ks_ptr = key_starts.data_ptr()
+    elif k_rows != rows:
+        raise ValueError(f"key_starts: expected with {k_rows} rows of k and {rows} of q")
+    status = lib.attn_prompt_run(plan, _ATTN_PROMPT_ARGS.pack(
+        qs[0], ks[0], vs[0], os_[0], starts.data_ptr(), ks_ptr, qs[1], qs[2], ks[1], ks[2], vs[1], vs[2], os_[1],
+        os_[2], rows, k_rows, starts.shape[0] - 1, _q8_stream(stream, device), heads, kv_heads, dim,
+        _q8_value_type(q, "q"), 1 if causal else 0, scale))
+    if status:
+        _raise(status, "attn_prompt_run")
+
+
+def attn_prompt_check(plan) -> int:
+    """Synchronise and return (and clear) the plan's device status: CONV3D_OK or CONV3D_EDEVICE."""
+    return load().attn_prompt_check(plan)
+
+
+def attn_prompt_destroy(plan) -> None:
+    if plan:
+        load().attn_prompt_destroy(plan)

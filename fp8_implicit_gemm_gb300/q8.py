@@ -1,9 +1,13 @@
-"""The 8-bit transformer operators of ``include/q8.h`` as a program uses them: a linear layer that
-owns its weights' codes and its plan, and a gated MLP block made of the three operators.
+"""The quantised transformer operators of ``include/q8.h`` and ``include/q8_attention.h`` as a program
+uses them: a linear layer that owns its weights' codes and its plan, a gated MLP block made of the
+three operators, and what attention takes: rotations, a paged cache of codes, attention over it and
+over prompts, and a block that makes one layer's attention of them.
 
-    python -m fp8_implicit_gemm_gb300.q8        # one block on random weights, against fp32
+    python -m fp8_implicit_gemm_gb300.q8        # the blocks on random weights, against fp32
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -131,6 +135,133 @@ class MlpQ8:
     def close(self) -> None:
         self.gate_up.close()
         self.down.close()
+
+
+class Rotary:
+    """The rotation of rot_dim elements of each head: pair j turns by frequency j times the token's position on
+    the pair's axis. With sections (pairs for each axis, in order) each axis has its own frequencies
+    theta^(-i / n) over its n pairs; without, there is one axis. `frequencies` (radians a position, rot_dim / 2
+    of them) replaces those. Pairs are neighbours if `adjacent`, else half of rot_dim apart."""
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, sections=None, adjacent: bool = False,
+                 frequencies=None, device="cuda"):
+        pairs = rot_dim // 2
+        sections = [pairs] if sections is None else [int(n) for n in sections]
+        if rot_dim < 2 or rot_dim % 2 or sum(sections) != pairs or min(sections) < 0:
+            raise ValueError(f"expected an even rot_dim and sections of {pairs} pairs, got {rot_dim}, {sections}")
+        if frequencies is None:
+            frequencies = [theta ** -(i / n) for n in sections for i in range(n)]
+        frequencies = [float(f) for f in frequencies]
+        if len(frequencies) != pairs or not all(math.isfinite(f) for f in frequencies):
+            raise ValueError(f"expected {pairs} finite frequencies")
+        # turns a position in units of 2^-64, whole turns left out
+        turns = [round(math.fmod(f / (2.0 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in frequencies]
+        self.rot_dim, self.axes, self.adjacent = rot_dim, len(sections), bool(adjacent)
+        self._turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64,
+                                   device=device)
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        self._axis = torch.tensor(axis, dtype=torch.uint8, device=device)
+        if self._turns.is_cuda:  # in place for calls on every stream
+            torch.cuda.current_stream(self._turns.device).synchronize()
+        self.table = (self._turns.data_ptr(), self._axis.data_ptr(), rot_dim, self.axes, int(self.adjacent),
+                      self._turns.get_device())
+
+
+class CacheQ8:
+    """Keys and values of a layer as codes in pages (the layout of include/q8_attention.h). The tensors may be
+    the caller's: 8-bit codes with scales [pages, kv_heads, page_size], or 4-bit codes, two in a byte, with
+    scales [.., 2]. capi.heads_q8_run writes it, `read` gives rows back, CacheAttention attends over it."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scale: torch.Tensor, v_codes: torch.Tensor,
+                 v_scale: torch.Tensor):
+        self.k_codes, self.k_scale = k_codes.detach(), k_scale.detach()
+        self.v_codes, self.v_scale = v_codes.detach(), v_scale.detach()
+        self.parts = capi.cache_q8(self.k_codes, self.k_scale, self.v_codes, self.v_scale)
+        self.pages, self.kv_heads, self.page_size, _ = k_codes.shape
+        self.head_dim, self.code_type = self.parts[2], self.parts[3]
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, codes=torch.int8,
+              device="cuda") -> "CacheQ8":
+        """A cache of zeros; `codes` is torch.int8, torch.float8_e4m3fn, or 4 for 4-bit codes."""
+        if codes != 4:
+            capi.q8_code_type(codes)
+        shape = (pages, kv_heads, page_size)
+        width, dtype = (head_dim // 2, torch.uint8) if codes == 4 else (head_dim, codes)
+        c = [torch.zeros(shape + (width,), dtype=torch.uint8, device=device).view(dtype) for _ in "kv"]
+        s = [torch.zeros(shape + (2,) * (codes == 4), dtype=torch.float32, device=device) for _ in "kv"]
+        if c[0].is_cuda:  # in place for calls on every stream
+            torch.cuda.current_stream(c[0].device).synchronize()
+        return cls(c[0], s[0], c[1], s[1])
+
+    def read(self, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+        """k and v [tokens, kv_heads, head_dim] = the values at the slots [tokens] (int64)."""
+        capi.cache_q8_read_run(self.parts, slots, k, v, stream)
+
+
+class CacheAttention:
+    """Attention of the newest tokens of up to max_seqs sequences over a cache. Owns a plan: one call at a
+    time."""
+
+    def __init__(self, cache: CacheQ8, q_heads: int, max_seqs: int = 256, max_tokens: int = 1,
+                 scale: float | None = None):
+        self._plan = 0
+        self.cache, self.scale = cache, cache.head_dim ** -0.5 if scale is None else scale
+        self._plan = capi.attn_q8_plan(max_seqs, max_tokens, q_heads, cache.kv_heads, cache.head_dim,
+                                       cache.code_type, cache.parts[4])
+
+    def __call__(self, q: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, o: torch.Tensor,
+                 stream=None) -> torch.Tensor:
+        """q, o: [seqs * tokens, q_heads, head_dim]; table: [seqs, width] pages, int32; lengths: [seqs], int32,
+        the newest tokens, whose rows are in the cache already, included."""
+        seqs = table.shape[0]
+        capi.attn_q8_run(self._plan, q, self.cache.parts, table, lengths, o, self.scale,
+                         q.shape[0] // seqs if seqs else 1, stream)
+        return o
+
+    def check(self) -> int:
+        return capi.attn_q8_check(self._plan)
+
+    def close(self) -> None:
+        plan, self._plan = self._plan, 0
+        capi.attn_q8_destroy(plan)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # the interpreter is ending and the library's module is gone
+            pass
+
+
+class PromptAttention:
+    """Attention over whole prompts, packed one behind the other. Owns a plan, whose runs may be in flight
+    at once."""
+
+    def __init__(self, scale: float | None = None, device: int | None = None):
+        self._plan = 0
+        self.scale = scale
+        self._plan = capi.attn_prompt_plan(torch.cuda.current_device() if device is None else device)
+
+    def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, o: torch.Tensor,
+                 causal: bool = True, key_starts: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """q, o: [rows, q_heads, head_dim]; k, v: [key rows, kv_heads, head_dim]; starts: [seqs + 1] int32, of
+        the keys too unless key_starts is given."""
+        scale = q.shape[2] ** -0.5 if self.scale is None else self.scale
+        capi.attn_prompt_run(self._plan, q, k, v, starts, o, scale, causal, key_starts, stream)
+        return o
+
+    def check(self) -> int:
+        return capi.attn_prompt_check(self._plan)
+
+    def close(self) -> None:
+        plan, self._plan = self._plan, 0
+        capi.attn_prompt_destroy(plan)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # the interpreter is ending and the library's module is gone
+            pass
 
 
 def _demo() -> None:
