@@ -391,7 +391,8 @@ def run(state):
             capi.heads_q8_run(q=s["q"], q_out=s["q_out"], k=s["k"], k_out=s.get("k_out"),
                               v=s["v"] if op == "write" else None, q_weight=s["weights"][0],
                               k_weight=s["weights"][1], eps=EPS, rotary=s["rotary"],
-                              positions=s["positions"], cache=s.get("paged"), slots=s.get("slots"))
+                              positions=s["positions"] if s["rotary"] else None,
+                              cache=s.get("paged"), slots=s.get("slots"))
         if op == "heads":
             return {"q": s["q_out"], "k": s["k_out"]}
         if op == "read" or s["case"].get("back"):
