@@ -108,7 +108,7 @@ Cache cache_of(const q8_cache* c) {
 
 struct attn_q8_plan_s : Plan {
   long long max_seqs = 0;
-  int max_tokens = 0, q_heads = 0, kv_heads = 0, head_dim = 0, code_type = 0;
+  int max_tokens = 0, q_heads = 0, kv_heads = 0, head_dim = 0, code_type = 0, sms = 0;
 };
 struct attn_prompt_plan_s : Plan {};
 
@@ -227,7 +227,14 @@ extern "C" conv3d_status attn_q8_plan(attn_q8_plan_t* plan, long long max_seqs, 
   pl->kv_heads = kv_heads;
   pl->head_dim = head_dim;
   pl->code_type = code_type;
-  st = plan_memory(*pl, device, kStatusBytes);
+  if (cudaDeviceGetAttribute(&pl->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
+      cache_attn_setup(code_type, head_dim) != cudaSuccess) {
+    cudaGetLastError();
+    delete pl;
+    return CONV3D_ECUDA;
+  }
+  st = plan_memory(*pl, device,
+                   kStatusBytes + cache_attn_workspace(pl->sms, max_tokens, q_heads, kv_heads, head_dim));
   if (st != CONV3D_OK) {
     delete pl;
     return st;
@@ -269,7 +276,8 @@ extern "C" conv3d_status attn_q8_run(attn_q8_plan_t plan, const attn_q8_args* a)
   p.table_width = (int)a->table_width;
   p.scale = a->scale;
   p.status = reinterpret_cast<int*>(plan->workspace);
-  return launched(launch_cache_attn(p, a->value_type, static_cast<cudaStream_t>(a->stream)));
+  return launched(launch_cache_attn(p, a->value_type, plan->workspace + kStatusBytes, plan->sms,
+                                    static_cast<cudaStream_t>(a->stream)));
 }
 
 extern "C" conv3d_status attn_q8_check(attn_q8_plan_t plan) {

@@ -1,72 +1,757 @@
 // q8_attn_cache.cu -- attention of each sequence's newest tokens over a paged cache of codes.
 //
-// A warp a row of q: its lanes hold the head's elements, each key's score is a sum over the warp, and the
-// softmax runs along with it (a running maximum and sum).
+// Each cached row is read once, so the memory is the bound (a key of 4-bit codes and 128 channels is 144
+// bytes with its value and scales), as long as turning codes into operands stays short: at 6.8 TB/s an SM
+// meets 47 such codes a cycle.
+//
+// Products. m16n8k16 with the keys as rows and up to 8 rows of q (heads of one group, newest tokens) as columns
+// (16 with two instructions): S^T = K q^T, then O^T = V^T P^T with V's channels as rows, so that a group of 8 heads
+// fills the instruction. What the instruction sums over may come in any order if both operands agree:
+//   - a lane's operands of K are the codes that lie next to each other in its part of a key's row, with q
+//     arranged to match once a sequence; those of V pairs of keys of neighbouring channels;
+//   - the two keys x heads of S^T that a lane holds become its operand of the second product by one transposition
+//     of an 8 x 8 block (movmatrix), the softmax in between running in registers.
+// Codes as f16, all exact. A 4-bit code masked in place under the exponent of 1024 (from the next four bits: of 64) is
+// 1024 + code (64 + code): one LOP3 and one subtraction for two codes. What is subtracted leaves code - 8, and
+// lowest + 8 * scale takes the place of the lowest value: sums of codes of both signs stay small and keep their bits (the
+// instruction cuts its sum a bit or two below fp32's last). Without the subtraction, as subnormal numbers, the products
+// would be cut at 2^-14 of a code: the instruction does not normalise them. An int8 code's byte under the exponent of
+// 1024, minus 1152; e4m3 by its conversion.
+//
+// Softmax. A warp takes 16 keys at a time and keeps one reference M for each row of q, for the weights with their
+// scale of v, p'' = 2^(x + log2 scale_v - M), which are rounded to f16, and for p = 2^(x - M), whose sum stays fp32.
+// M moves only when a weight would pass 2^8 (a vote; the sums over the warp are taken then only), so p'' keeps its
+// bits relative to the largest one whatever v's scales are. The lowest values of 4-bit rows are added with the rounded
+// weight (p'' * (lowest + 8 * scale_v) / scale_v), so that its rounding errs by 2^-11 of a value, not of code and lowest value apart;
+// with p where p'' has lost bits beside rows of larger scales.
+//
+// Copies. Every warp has a ring of its own, filled by bulk copies of 16 rows of codes and their scales (pages
+// are multiples of 16 tokens: a copy never leaves its page), so no barrier but its own holds it up.
+//
+// Split. All groups of 64 keys of all sequences and key heads are cut into equal runs, one a block, on the device, from
+// the lengths there (a captured graph keeps its grid for every length). A block's warps join in shared memory;
+// where a sequence's head is shared by several blocks each leaves sums in the plan's workspace and a second kernel, that is
+// waiting already, joins them in the blocks' order: results do not depend on which is ready first.
+#include <algorithm>
+#include <type_traits>
+
+#include "ptx.cuh"
 #include "q8_attn_internal.h"
 #include "q8_common.cuh"
 
 namespace c3d {
 
-constexpr int kRowThreads = 128;
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kTile = 16;                    // keys of a step
+constexpr int kGroup = kTile * kWarps;       // keys of the smallest share
+constexpr int kLeastGroups = 4;              // of a block, where there are fewer than enough for all
+constexpr float kLowest = -1e30f;            // M before the first key
+constexpr float kLeastLog = -100.0f;         // scales of v below 2^-100 do not move M
+constexpr uint64_t kCacheTimeoutNs = 2000ull * 1000 * 1000;
 
-__device__ __forceinline__ float cache_value(const Cache& c, const uint8_t* codes, const float* scales,
-                                             long long row, int i) {
-  if (c.code_type == Q8_INT4) {
-    const unsigned b = codes[(row * c.head_dim + i) / 2];
-    return fmaf((float)((i & 1) ? b >> 4 : b & 15u), scales[2 * row], scales[2 * row + 1]);
+template <int CODE>
+constexpr int kScaleBytes = CODE == Q8_INT4 ? 8 : 4;
+template <int CODE, int D>
+constexpr int kRowBytes = CODE == Q8_INT4 ? D / 2 : D;
+template <int CODE, int D>
+constexpr int kStageBytes = 2 * kTile * (kRowBytes<CODE, D> + kScaleBytes<CODE>);
+template <int CODE, int D>
+constexpr int kStages = CODE == Q8_INT4 ? 4 : D == 256 ? 2 : 3;  // what kBlocksPerSm blocks have room for
+// Channels of a row of the sums in shared memory: 4 more, so that the lanes of a store meet all banks.
+template <int D>
+constexpr int kSumPitch = D + 4;
+template <int CODE, int D, int NB>
+constexpr int kRingBytes = std::max(kWarps * kStages<CODE, D> * kStageBytes<CODE, D>,
+                                    kWarps * NB * 8 * kSumPitch<D> * 4);
+template <int D, int NB>
+constexpr int kBlocksPerSm = D * NB <= 128 ? 4 : D * NB == 256 ? 3 : 2;
+
+// What a block leaves of a share: for each row the reference, the sum of weights and the channels' sums.
+__host__ __device__ constexpr size_t part_floats(int rows, int dim) { return (size_t)rows * (dim + 2); }
+// The first block of a sequence's head that is shared: its blocks are [this one, last].
+struct SharedHead {
+  int last;        // -1: none begins here and ends elsewhere
+  int seq, head, row0;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+// Of the eight 4-bit codes of a word the ones of bits 0 and 16 (from bits 4 and 20: int4_odd) on, minus 8, as a pair.
+__device__ __forceinline__ uint32_t int4_even(uint32_t w) {
+  const uint32_t u = (w & 0x000F000Fu) | 0x64006400u;
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(1032.0f, 1032.0f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t int4_odd(uint32_t w) {
+  const uint32_t u = (w & 0x00F000F0u) | 0x54005400u;
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(72.0f, 72.0f));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// WORDS consecutive words of shared memory.
+template <int WORDS>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (WORDS == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS / 4; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
   }
-  const uint8_t b = codes[row * c.head_dim + i];
-  if (c.code_type == Q8_INT8) return (float)(int8_t)b * scales[row];
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3))) * scales[row];
+}
+
+// The channel behind code n of word w of lane t4's part of a key's row.
+template <int CODE, int D>
+__device__ __forceinline__ int key_channel(int t4, int w, int n) {
+  if constexpr (CODE == Q8_INT4)
+    return (w / 4) * 128 + t4 * (D < 128 ? D / 4 : 32) + (w % 4) * 8 + n;
+  else
+    return (w / 4) * 64 + t4 * 16 + (w % 4) * 4 + n;
+}
+
+// Lane t4's part of a key's row.
+template <int CODE, int D>
+__device__ __forceinline__ void load_key(const uint8_t* row, int t4, uint32_t* w) {
+  constexpr int kWords = kRowBytes<CODE, D> / 16;
+  if constexpr (kWords < 4) {
+    load_words<kWords>(row + t4 * kWords * 4, w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kWords / 4; ++j) load_words<4>(row + j * 64 + t4 * 16, w + 4 * j);
+  }
+}
+
+struct Found {
+  int seq;
+  long long before;  // groups of the sequences before it
+};
+
+// Groups of a sequence's keys, one at least: a sequence without keys has an output too. A bad length counts as none.
+__device__ __forceinline__ int groups_of(const CacheAttnParams& p, int b) {
+  const int n = p.lengths[b];
+  const bool bad = n < 0 || n > (long long)p.table_width * p.cache.page_size;
+  return bad || n <= 0 ? 1 : (int)(((unsigned)n + kGroup - 1) / kGroup);
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+template <typename T, int CODE, int D, int NB>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
+    cache_attn_kernel(const CacheAttnParams p, float* parts, SharedHead* shared_heads) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t bars[kWarps * kStages<CODE, D>];
+  __shared__ float stat[2][kWarps][NB * 8];
+  __shared__ long long scan[kWarps];
+  __shared__ Found found;
+  __shared__ int abort_flag, bad_input[2];  // the flag of this round and of the next
+
+  constexpr int kRows = NB * 8, kS = kStages<CODE, D>, kBlocks = D / 16;
+  constexpr int kKeyWords = kRowBytes<CODE, D> / 16, kValueWords = kRowBytes<CODE, D> / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
+  const Cache& c = p.cache;
+  const int group = p.q_heads / c.kv_heads, rows_all = p.tokens * group;
+  const int row_blocks = (rows_all + kRows - 1) / kRows;
+  const long long heads = (long long)c.kv_heads * row_blocks;
+
+  uint8_t* my_ring = ring + warp * kS * kStageBytes<CODE, D>;
+  const uint32_t ring_at = smem_u32(my_ring), bar_at = smem_u32(bars) + warp * kS * 8;
+  if (threadIdx.x == 0) abort_flag = 0, bad_input[0] = 0;
+  if (lane < kS) mbar_init(bar_at + 8 * lane, 1);
+  fence_mbar_init();
+
+  // ---- this block's share
+  long long total = 0;
+  for (int b = threadIdx.x; b < p.seqs; b += kThreads) total += groups_of(p, b);
+  total = warp_sum(total);
+  if (lane == 0) scan[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += scan[w];
+  __syncthreads();
+  total *= heads;
+  const int blocks = (int)min((long long)gridDim.x, max(1LL, total / kLeastGroups));
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) shared_heads[blockIdx.x].last = -1;
+  if ((int)blockIdx.x >= blocks) return;
+  long long at = blockIdx.x * total / blocks;
+  const long long until = (blockIdx.x + 1) * total / blocks;
+  {
+    const long long want = at / heads;
+    long long before = 0;
+    for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int mine = b < p.seqs ? groups_of(p, b) : 0;
+      long long sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (lane == 31) scan[warp] = sum;
+      __syncthreads();
+      long long end = before;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) sum += scan[w];
+        end += scan[w];
+      }
+      if (before + sum > want && before + sum - mine <= want) found = Found{b, before + sum - mine};
+      __syncthreads();
+      if (end > want) break;
+      before = end;
+    }
+  }
+  int seq = found.seq;
+  long long before = found.before;
+
+  const AbortState ab{&abort_flag, p.status, kCacheTimeoutNs};
+  const float scale_log2 = p.scale * 1.44269504088896f;
+  uint32_t issued = 0, used = 0;  // this warp's copies so far
+
+  // ---- the heads of sequences that it covers, or parts of them
+  for (int round = 0; at < until; round ^= 1) {
+    const int groups = groups_of(p, seq);
+    const long long head_index = (at - before * heads) / groups;
+    const int first_group = (int)((at - before * heads) - head_index * groups);
+    const int take = (int)min((long long)groups - first_group, until - at);
+    const int head = (int)(head_index / row_blocks), row0 = (int)(head_index % row_blocks) * kRows;
+    const int length = p.lengths[seq];
+    bool bad = length < 0 || length > (long long)p.table_width * c.page_size;
+    const int keys = bad ? 0 : length;
+    const int tiles = (int)(((unsigned)keys + kTile - 1) / kTile);
+    const int first = first_group * kWarps + warp;
+    const int end = min(tiles, (first_group + take) * kWarps);
+    const int count = first < end ? (end - first + kWarps - 1) / kWarps : 0;
+    const int* table = p.table + seq * p.table_pitch;
+
+    // The pages of 32 of this warp's tiles, a lane each.
+    auto pages_from = [&](int i) {
+      int page = 0;
+      if (i + lane < count) {
+        page = table[(first + (i + lane) * kWarps) * kTile / c.page_size];
+        if (page < 0 || page >= (int)(c.slots / (unsigned)c.page_size)) {
+          bad = true;
+          page = 0;  // some page of the cache; what is read there is dropped
+        }
+      }
+      return page;
+    };
+    int pages = pages_from(0);
+    auto issue = [&](int i) {
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, i % 32);
+      const int place = (first + i * kWarps) * kTile % c.page_size;
+      const long long row = ((long long)page * c.kv_heads + head) * c.page_size + place;
+      const uint32_t stage = issued % kS, bar = bar_at + 8 * stage;
+      const uint32_t dst = ring_at + stage * kStageBytes<CODE, D>;
+      constexpr uint32_t kCodes = kTile * kRowBytes<CODE, D>, kScales = kTile * kScaleBytes<CODE>;
+      if (lane == 0) mbar_arrive_expect_tx(bar, kStageBytes<CODE, D>);
+      __syncwarp();
+      if (lane < 4) {
+        const bool is_scale = lane >= 2;
+        const uint8_t* src =
+            is_scale ? reinterpret_cast<const uint8_t*>(lane == 2 ? c.k_scale : c.v_scale) + row * kScaleBytes<CODE>
+                     : (lane == 0 ? c.k_codes : c.v_codes) + row * kRowBytes<CODE, D>;
+        bulk_load(dst + (lane == 0   ? 0
+                         : lane == 1 ? kCodes
+                         : lane == 2 ? 2 * kCodes
+                                     : 2 * kCodes + kScales),
+                  src, is_scale ? kScales : kCodes, bar);
+      }
+      ++issued;
+    };
+    int ahead = min(count, kS);
+    for (int i = 0; i < ahead; ++i) issue(i);
+
+    // ---- q's operands: row g of the columns, in the order of the codes
+    uint32_t q_frag[NB][kBlocks][2];
+    float factor[NB][2], q_sum[NB][2];  // of the columns 2 t4 and the next
+    int limit[NB][2];                   // keys that they see
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = row0 + 8 * nb + g;
+      const bool live = r < rows_all;
+      const int t = live ? r / group : 0, h = live ? r - t * group : 0;
+      const T* q = static_cast<const T*>(p.q.p) + ((long long)seq * p.tokens + t) * p.q.pitch +
+                   (long long)(head * group + h) * p.q.head_pitch;
+      float amax = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kKeyWords; ++w)
+#pragma unroll
+        for (int n = 0; n < (CODE == Q8_INT4 ? 8 : 4); ++n)
+          amax = fmaxf(amax, live ? fabsf(q8_to_float(q[key_channel<CODE, D>(t4, w, n)])) : 0.0f);
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      // the largest between 2^8 and 2^9, by a power of two
+      const int up = amax > 0.0f && amax < 3.4e38f ? 8 - ilogbf(amax) : 0;
+      auto value = [&](int w, int n) {
+        const float v = live ? q8_to_float(q[key_channel<CODE, D>(t4, w, n)]) : 0.0f;
+        return scalbnf(v, up);
+      };
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kKeyWords; ++w) {
+        if constexpr (CODE == Q8_INT4) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // as int4_even and int4_odd leave them: the codes 2i and 2i + 4, then 2i + 1 and 2i + 5
+            const __half2 even = __floats2half2_rn(value(w, 2 * i), value(w, 2 * i + 4));
+            const __half2 odd = __floats2half2_rn(value(w, 2 * i + 1), value(w, 2 * i + 5));
+            sum += (__low2float(even) + __high2float(even)) + (__low2float(odd) + __high2float(odd));
+            q_frag[nb][2 * w + i][0] = *reinterpret_cast<const uint32_t*>(&even);
+            q_frag[nb][2 * w + i][1] = *reinterpret_cast<const uint32_t*>(&odd);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __half2 v = __floats2half2_rn(value(w, 2 * i), value(w, 2 * i + 1));
+            q_frag[nb][w][i] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+        }
+      }
+      const float back = scalbnf(scale_log2, -up);
+      float s = 0.0f;
+      if constexpr (CODE == Q8_INT4) {
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        s = back * sum;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        factor[nb][j] = __shfl_sync(0xFFFFFFFFu, back, (2 * t4 + j) * 4);
+        q_sum[nb][j] = __shfl_sync(0xFFFFFFFFu, s, (2 * t4 + j) * 4);
+        const int rj = row0 + 8 * nb + 2 * t4 + j;
+        limit[nb][j] = rj < rows_all ? keys - p.tokens + 1 + rj / group : 0;
+      }
+    }
+
+    float o[NB][kBlocks][4] = {};
+    float top[NB][2], weight[NB][2], low_sum[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) top[nb][j] = kLowest, weight[nb][j] = 0.0f, low_sum[nb][j] = 0.0f;
+
+    bool waited = true;
+    for (int i = 0; i < count; ++i) {
+      const uint32_t stage = used % kS;
+      if (waited) waited = wait_bounded_warp(bar_at + 8 * stage, (used / kS) & 1, ab, kAttnTimeout);
+      if (!waited) break;
+      const uint8_t* at_stage = my_ring + stage * kStageBytes<CODE, D>;
+      const uint8_t* k_codes = at_stage;
+      const uint8_t* v_codes = at_stage + kTile * kRowBytes<CODE, D>;
+      const float* k_scale = reinterpret_cast<const float*>(at_stage + 2 * kTile * kRowBytes<CODE, D>);
+      const float* v_scale = k_scale + kTile * kScaleBytes<CODE> / 4;
+      const int key0 = (first + i * kWarps) * kTile;
+      const bool masked = keys - p.tokens + 1 - key0 < kTile;  // for some row
+
+      // scores of the keys g and g + 8
+      float s[NB][4] = {};
+      {
+        uint32_t a[kKeyWords], b[kKeyWords];
+        load_key<CODE, D>(k_codes + g * kRowBytes<CODE, D>, t4, a);
+        load_key<CODE, D>(k_codes + (g + 8) * kRowBytes<CODE, D>, t4, b);
+        float s2[NB][4] = {};  // every other product: two chains
+#pragma unroll
+        for (int w = 0; w < kKeyWords; ++w) {
+          if constexpr (CODE == Q8_INT4) {
+            const uint32_t ah = a[w] >> 8, bh = b[w] >> 8;
+            const uint32_t m0[4] = {int4_even(a[w]), int4_even(b[w]), int4_odd(a[w]), int4_odd(b[w])};
+            const uint32_t m1[4] = {int4_even(ah), int4_even(bh), int4_odd(ah), int4_odd(bh)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma_f16(s[nb], m0, q_frag[nb][2 * w][0], q_frag[nb][2 * w][1]);
+              mma_f16(s2[nb], m1, q_frag[nb][2 * w + 1][0], q_frag[nb][2 * w + 1][1]);
+            }
+          } else {
+            uint32_t ha[2], hb[2];
+            if constexpr (CODE == Q8_INT8) {
+              int8_to_f16(a[w], ha);
+              int8_to_f16(b[w], hb);
+            } else {
+              ha[0] = e4m3_pair(a[w] & 0xFFFFu), ha[1] = e4m3_pair(a[w] >> 16);
+              hb[0] = e4m3_pair(b[w] & 0xFFFFu), hb[1] = e4m3_pair(b[w] >> 16);
+            }
+            const uint32_t m[4] = {ha[0], hb[0], ha[1], hb[1]};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              mma_f16(w % 2 ? s2[nb] : s[nb], m, q_frag[nb][w][0], q_frag[nb][w][1]);
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nb][e] += s2[nb][e];
+      }
+      float ks[2], kl[2] = {}, vl[2] = {}, v_low[2] = {}, vlog[2];  // of the keys g and g + 8
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int key = g + 8 * j;
+        float vs;
+        if constexpr (CODE == Q8_INT4) {
+          const float2 a = reinterpret_cast<const float2*>(k_scale)[key], b = reinterpret_cast<const float2*>(v_scale)[key];
+          ks[j] = a.x, kl[j] = fmaf(8.0f, a.x, a.y), vs = b.x, vl[j] = fmaf(8.0f, b.x, b.y);
+        } else {
+          ks[j] = k_scale[key], vs = v_scale[key];
+        }
+        if (masked && key0 + key >= keys) vs = 1.0f, vl[j] = 0.0f;  // whatever lies there
+        vlog[j] = __log2f(vs);
+        if constexpr (CODE == Q8_INT4) v_low[j] = __fdividef(vl[j], vs);
+      }
+      bool grows = false;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = e / 2;
+          float x = s[nb][e] * (ks[j] * factor[nb][e % 2]);
+          if constexpr (CODE == Q8_INT4) x = fmaf(kl[j], q_sum[nb][e % 2], x);
+          if (masked && key0 + g + 8 * j >= limit[nb][e % 2]) x = -INFINITY;
+          s[nb][e] = x;
+          grows |= x + fmaxf(vlog[j], kLeastLog) > top[nb][e % 2] + 8.0f;
+        }
+      if (__any_sync(0xFFFFFFFFu, grows)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float m = fmaxf(s[nb][j] + fmaxf(vlog[0], kLeastLog), s[nb][2 + j] + fmaxf(vlog[1], kLeastLog));
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
+            m = fmaxf(m, top[nb][j]);
+            const float keep = exp2_fast(top[nb][j] - m);
+            top[nb][j] = m;
+            weight[nb][j] *= keep;
+            low_sum[nb][j] *= keep;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) o[nb][b][j] *= keep, o[nb][b][2 + j] *= keep;
+          }
+      }
+      uint32_t p_frag[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x0 = s[nb][2 * j] - top[nb][0], x1 = s[nb][2 * j + 1] - top[nb][1];
+          const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
+          weight[nb][0] += p0;
+          weight[nb][1] += p1;
+          const bool hidden0 = masked && x0 == -INFINITY, hidden1 = masked && x1 == -INFINITY;
+          x0 += hidden0 ? 0.0f : vlog[j];  // which may be NaN
+          x1 += hidden1 ? 0.0f : vlog[j];
+          const __half2 h = __floats2half2_rn(exp2_fast(x0), exp2_fast(x1));
+          p_frag[nb][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h));
+          if constexpr (CODE == Q8_INT4) {
+            const float2 r = __half22float2(h);
+            low_sum[nb][0] += r.x >= 0x1p-14f ? r.x * v_low[j] : hidden0 ? 0.0f : p0 * vl[j];
+            low_sum[nb][1] += r.y >= 0x1p-14f ? r.y * v_low[j] : hidden1 ? 0.0f : p1 * vl[j];
+          }
+        }
+
+      // values of the keys 2 t4, the next, and both 8 further on
+      {
+        uint32_t v[4][kValueWords];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = 2 * t4 + (j & 1) + 8 * (j >> 1);
+          load_words<kValueWords>(v_codes + key * kRowBytes<CODE, D> + g * kValueWords * 4, v[j]);
+          if (CODE == Q8_E4M3 && masked && key0 + key >= keys) {
+#pragma unroll
+            for (int w = 0; w < kValueWords; ++w) v[j][w] = 0;  // it may be a NaN
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kValueWords; ++w) {
+          if constexpr (CODE == Q8_INT4) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // the codes 0 to 3 and 4 to 7
+              const uint32_t pick = half ? 0x7632u : 0x5410u;
+              uint32_t lo = __byte_perm(v[0][w], v[1][w], pick), hi = __byte_perm(v[2][w], v[3][w], pick);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t m[4] = {int4_even(lo), int4_odd(lo), int4_even(hi), int4_odd(hi)};
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                  mma_f16(o[nb][4 * w + 2 * half + i], m, p_frag[nb][0], p_frag[nb][1]);
+                lo >>= 8, hi >>= 8;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // the codes 0 and 1, 2 and 3
+              const uint32_t pick = half ? 0x7362u : 0x5140u;
+              const uint32_t lo = __byte_perm(v[0][w], v[1][w], pick), hi = __byte_perm(v[2][w], v[3][w], pick);
+              uint32_t hl[2], hh[2];
+              if constexpr (CODE == Q8_INT8) {
+                int8_to_f16(lo, hl);
+                int8_to_f16(hi, hh);
+              } else {
+                hl[0] = e4m3_pair(lo & 0xFFFFu), hl[1] = e4m3_pair(lo >> 16);
+                hh[0] = e4m3_pair(hi & 0xFFFFu), hh[1] = e4m3_pair(hi >> 16);
+              }
+              const uint32_t m[4] = {hl[0], hl[1], hh[0], hh[1]};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][2 * w + half], m, p_frag[nb][0], p_frag[nb][1]);
+            }
+          }
+        }
+      }
+      ++used;
+      __syncwarp();  // the stage is free
+      if (ahead < count) {
+        if (ahead % 32 == 0) pages = pages_from(ahead);
+        issue(ahead++);
+      }
+    }
+    if (!waited) {  // the copies under way land before the ring is used again; then all is given up
+      for (; used < issued; ++used) {
+        int own = 0;
+        wait_bounded_warp(bar_at + 8 * (used % kS), (used / kS) & 1,
+                          AbortState{&own, p.status, 1000000ull}, kAttnTimeout);
+      }
+      bad = true;
+    }
+    if (bad) bad_input[round] = 1;
+
+    // ---- the warps' sums, joined
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) {
+          weight[nb][j] += __shfl_xor_sync(0xFFFFFFFFu, weight[nb][j], w);
+          low_sum[nb][j] += __shfl_xor_sync(0xFFFFFFFFu, low_sum[nb][j], w);
+        }
+        if (g == 0) stat[0][warp][8 * nb + 2 * t4 + j] = top[nb][j];
+      }
+    __syncthreads();  // all rings are idle: their memory takes the sums
+    float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * nb + 2 * t4 + j;
+        float m = stat[0][0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, stat[0][w][r]);
+        const float keep = exp2_fast(top[nb][j] - m);
+        if (g == 0) stat[1][warp][r] = weight[nb][j] * keep;
+        const float add = low_sum[nb][j] * keep;
+        float* row = sums + (warp * kRows + r) * kSumPitch<D> + 2 * g;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+          *reinterpret_cast<float2*>(row + 16 * b) =
+              make_float2(fmaf(o[nb][b][j], keep, add), fmaf(o[nb][b][2 + j], keep, add));
+      }
+    __syncthreads();
+    const bool whole = take == groups;
+    const bool tail = first_group + take == groups && !whole;  // the head began in an earlier block
+    float* part = parts + (2 * (long long)blockIdx.x + (tail || first_group > 0 ? 0 : 1)) * part_floats(kRows, D);
+    const float nan = __int_as_float(0x7FFFFFFF);
+    if (threadIdx.x == 0) {
+      bad_input[round ^ 1] = 0;
+      if (bad_input[round] && !abort_flag) atomicOr(p.status, kAttnBadInput);
+      if (!whole && first_group == 0) {
+        // the block that holds this head's last group
+        const long long last = before * heads + (head_index + 1) * groups - 1;
+        shared_heads[blockIdx.x] = SharedHead{(int)(((last + 1) * blocks - 1) / total), seq, head, row0};
+      }
+    }
+    for (int i = threadIdx.x; i < kRows * (D / 2); i += kThreads) {
+      const int r = i / (D / 2), pair = i % (D / 2);
+      const int lane_of = 2 * pair / (D / 8), block_of = pair % (D / 16);
+      float2 sum = make_float2(0.0f, 0.0f);
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(sums + (w * kRows + r) * kSumPitch<D> + 16 * block_of + 2 * lane_of);
+        sum.x += v.x;
+        sum.y += v.y;
+        l += stat[1][w][r];
+      }
+      if (bad_input[round]) l = nan;
+      const int rr = row0 + r;
+      if (!whole) {
+        *reinterpret_cast<float2*>(part + 2 * kRows + r * D + 2 * pair) = sum;
+        if (pair == 0) {
+          float m = stat[0][0][r];
+#pragma unroll
+          for (int w = 1; w < kWarps; ++w) m = fmaxf(m, stat[0][w][r]);
+          part[r] = m;
+          part[kRows + r] = l;
+        }
+      } else if (rr < rows_all) {
+        const int t = rr / group, h = rr - t * group;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.o.p) + ((long long)seq * p.tokens + t) * p.o.pitch +
+                                                    (long long)(head * group + h) * p.o.head_pitch + 2 * pair);
+        *out = q8_pack2<T>(make_float2(sum.x * inv, sum.y * inv));
+      }
+    }
+    fence_proxy_async_smem();  // the ring takes copies again
+    at += take;
+    if (at == (before + groups) * heads) before += groups, ++seq;
+    if (__syncthreads_or(abort_flag)) break;
+  }
+}
+
+// Joins the sums of heads that several blocks share: a block for each first block of such a head and row.
+template <typename T, int D, int NB>
+__global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttnParams p, const float* parts,
+                                                         const SharedHead* shared_heads) {
+  constexpr int kRows = NB * 8, kVec = D / 32;
+  __shared__ float sums[4][D];
+  __shared__ float weights[4];
+  pdl_wait_primary();
+  const SharedHead s = shared_heads[blockIdx.x];
+  if (s.last < 0) return;
+  const int r = blockIdx.y, rr = s.row0 + r;
+  const int group = p.q_heads / p.cache.kv_heads;
+  if (rr >= p.tokens * group) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n = s.last - (int)blockIdx.x + 1;
+  auto part_of = [&](int i) { return parts + (2 * ((long long)blockIdx.x + i) + (i == 0)) * part_floats(kRows, D); };
+  float m = kLowest;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, part_of(i)[r]);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
+  float sum[kVec] = {}, l = 0.0f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += 4) {
+    const float* part = part_of(i);
+    const float keep = exp2_fast(part[r] - m);
+    l = fmaf(part[kRows + r], keep, l);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) sum[e] = fmaf(part[2 * kRows + r * D + 32 * e + lane], keep, sum[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) sums[warp][32 * e + lane] = sum[e];
+  if (lane == 0) weights[warp] = l;
+  __syncthreads();
+  l = (weights[0] + weights[1]) + (weights[2] + weights[3]);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int t = rr / group, h = rr - t * group;
+  T* out = static_cast<T*>(p.o.p) + ((long long)s.seq * p.tokens + t) * p.o.pitch +
+           (long long)(s.head * group + h) * p.o.head_pitch;
+  for (int i = threadIdx.x; i < D; i += 128)
+    out[i] = q8_from_float<T>(((sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i])) * inv);
+}
+
+// Rows of q that the instructions' columns hold, in eights: 16 where 8 do not hold all of a key head's.
+static int cache_attn_eights(int tokens, int q_heads, int kv_heads) {
+  return tokens * (q_heads / kv_heads) <= 8 ? 1 : 2;
+}
+
+static int cache_attn_blocks(int sms, int dim, int nb) {
+  return sms * (dim * nb <= 128 ? 4 : dim * nb == 256 ? 3 : 2);
+}
+
+size_t cache_attn_workspace(int sms, int tokens, int q_heads, int kv_heads, int dim) {
+  // a run of fewer tokens may use the form with fewer rows, and more blocks
+  size_t most = 0;
+  for (int nb = 1; nb <= cache_attn_eights(tokens, q_heads, kv_heads); ++nb)
+    most = std::max(most, cache_attn_blocks(sms, dim, nb) *
+                              (2 * part_floats(8 * nb, dim) * sizeof(float) + sizeof(SharedHead)));
+  return most;
+}
+
+// One form of the kernels: with p null only what it needs of the device is set up.
+template <typename T, int CODE, int D, int NB>
+static cudaError_t cache_attn_form(const CacheAttnParams* p, void* workspace, int sms, cudaStream_t stream) {
+  constexpr int kSmem = kRingBytes<CODE, D, NB>;
+  auto kernel = cache_attn_kernel<T, CODE, D, NB>;
+  if (!p) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const int blocks = cache_attn_blocks(sms, D, NB);
+  float* parts = static_cast<float*>(workspace);
+  SharedHead* shared_heads = reinterpret_cast<SharedHead*>(parts + 2 * blocks * part_floats(8 * NB, D));
+  kernel<<<blocks, kThreads, kSmem, stream>>>(*p, parts, shared_heads);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(blocks, NB * 8);
+  config.blockDim = dim3(128);
+  config.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, cache_join_kernel<T, D, NB>, *p, (const float*)parts,
+                            (const SharedHead*)shared_heads);
+}
+
+template <typename T, int CODE>
+static cudaError_t cache_attn_of(int dim, int eights, const CacheAttnParams* p, void* workspace, int sms,
+                                 cudaStream_t stream) {
+  auto form = dim == 64    ? (eights == 2 ? cache_attn_form<T, CODE, 64, 2> : cache_attn_form<T, CODE, 64, 1>)
+              : dim == 128 ? (eights == 2 ? cache_attn_form<T, CODE, 128, 2> : cache_attn_form<T, CODE, 128, 1>)
+                           : (eights == 2 ? cache_attn_form<T, CODE, 256, 2> : cache_attn_form<T, CODE, 256, 1>);
+  return form(p, workspace, sms, stream);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) cache_attn_kernel(const CacheAttnParams p) {
-  const long long id = (long long)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31, dim = p.cache.head_dim;
-  if (id >= (long long)p.seqs * p.tokens * p.q_heads) return;
-  const int head = (int)(id % p.q_heads);
-  const long long row = id / p.q_heads;
-  const int seq = (int)(row / p.tokens), t = (int)(row % p.tokens);
-  const int kv = head / (p.q_heads / p.cache.kv_heads), size = p.cache.page_size;
-  const T* q = static_cast<const T*>(p.q.p) + row * p.q.pitch + head * p.q.head_pitch;
-  float qf[8], o[8] = {};
-  for (int i = 0; i < dim / 32; ++i) qf[i] = q8_to_float(q[32 * i + lane]) * p.scale * 1.44269504f;
-  const int length = p.lengths[seq];
-  bool bad = length < 0 || length > (long long)p.table_width * size;
-  float top = -1e30f, sum = 0.0f;
-  for (int s = 0; !bad && s < length - p.tokens + 1 + t; ++s) {
-    const int page = p.table[seq * p.table_pitch + s / size];
-    if (page < 0 || page >= (int)(p.cache.slots / size)) {
-      bad = true;
-      break;
-    }
-    const long long at = ((long long)page * p.cache.kv_heads + kv) * size + s % size;
-    float x = 0.0f;
-    for (int i = 0; i < dim / 32; ++i)
-      x = fmaf(qf[i], cache_value(p.cache, p.cache.k_codes, p.cache.k_scale, at, 32 * i + lane), x);
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, w);
-    const float now = fmaxf(top, x), keep = exp2f(top - now), pr = exp2f(x - now);
-    top = now;
-    sum = sum * keep + pr;
-    for (int i = 0; i < dim / 32; ++i)
-      o[i] = fmaf(pr, cache_value(p.cache, p.cache.v_codes, p.cache.v_scale, at, 32 * i + lane), o[i] * keep);
+static cudaError_t cache_attn_in(int code_type, int dim, int eights, const CacheAttnParams* p, void* workspace,
+                                 int sms, cudaStream_t stream) {
+  switch (code_type) {
+    case Q8_INT8: return cache_attn_of<T, Q8_INT8>(dim, eights, p, workspace, sms, stream);
+    case Q8_E4M3: return cache_attn_of<T, Q8_E4M3>(dim, eights, p, workspace, sms, stream);
+    default: return cache_attn_of<T, Q8_INT4>(dim, eights, p, workspace, sms, stream);
   }
-  if (bad && lane == 0) atomicOr(p.status, kAttnBadInput);
-  T* out = static_cast<T*>(p.o.p) + row * p.o.pitch + head * p.o.head_pitch;
-  for (int i = 0; i < dim / 32; ++i)
-    out[32 * i + lane] =
-        q8_from_float<T>(bad ? __int_as_float(0x7FFFFFFF) : sum == 0.0f ? 0.0f : o[i] / sum);
 }
 
-cudaError_t launch_cache_attn(const CacheAttnParams& p, int value_type, cudaStream_t stream) {
-  const long long rows = (long long)p.seqs * p.tokens * p.q_heads;
-  const unsigned blocks = (unsigned)((rows + kRowThreads / 32 - 1) / (kRowThreads / 32));
-  if (value_type == Q8_BF16)
-    cache_attn_kernel<__nv_bfloat16><<<blocks, kRowThreads, 0, stream>>>(p);
-  else
-    cache_attn_kernel<__half><<<blocks, kRowThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t cache_attn_setup(int code_type, int dim) {
+  for (int eights = 1; eights <= 2; ++eights) {
+    cudaError_t e = cache_attn_in<__nv_bfloat16>(code_type, dim, eights, nullptr, nullptr, 0, nullptr);
+    if (e == cudaSuccess) e = cache_attn_in<__half>(code_type, dim, eights, nullptr, nullptr, 0, nullptr);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_cache_attn(const CacheAttnParams& p, int value_type, void* workspace, int sms, cudaStream_t stream) {
+  const int eights = cache_attn_eights(p.tokens, p.q_heads, p.cache.kv_heads);
+  auto in = value_type == Q8_BF16 ? cache_attn_in<__nv_bfloat16> : cache_attn_in<__half>;
+  return in(p.cache.code_type, p.cache.head_dim, eights, &p, workspace, sms, stream);
 }
 
 }  // namespace c3d

@@ -59,7 +59,10 @@ struct CacheAttnParams {
   float scale;
   int* status;
 };
-cudaError_t launch_cache_attn(const CacheAttnParams& p, int value_type, cudaStream_t stream);
+// Bytes that the runs of a plan need for the sums of heads that several blocks share.
+size_t cache_attn_workspace(int sms, int tokens, int q_heads, int kv_heads, int dim);
+cudaError_t cache_attn_setup(int code_type, int dim);  // the kernels' shared-memory grant on this device
+cudaError_t launch_cache_attn(const CacheAttnParams& p, int value_type, void* workspace, int sms, cudaStream_t stream);
 
 struct PromptParams {
   Heads q, k, v, o;
