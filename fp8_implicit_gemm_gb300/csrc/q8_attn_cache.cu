@@ -18,17 +18,19 @@
 // would be cut at 2^-14 of a code: the instruction does not normalise them. An int8 code's byte under the exponent of
 // 1024, minus 1152; e4m3 by its conversion.
 //
-// Softmax. A warp takes 16 keys at a time and keeps one reference M for each row of q, for the weights with their
-// scale of v, p'' = 2^(x + log2 scale_v - M), which are rounded to f16, and for p = 2^(x - M), whose sum stays fp32.
-// M moves only when a weight would pass 2^8 (a vote; the sums over the warp are taken then only), so p'' keeps its
-// bits relative to the largest one whatever v's scales are. The lowest values of 4-bit rows are added with the rounded
-// weight (p'' * (lowest + 8 * scale_v) / scale_v), so that its rounding errs by 2^-11 of a value, not of code and lowest value apart;
-// with p where p'' has lost bits beside rows of larger scales.
+// Softmax. A warp takes 16 or 32 keys at a time and keeps one reference M for each row of q. The weights that meet codes have v's
+// scale in them, w = 2^(x + log2 scale_v - M), cut to f16's bits; the sum of the weights alone, of w / scale_v, and that of
+// the lowest values of 4-bit rows, of w * (lowest + 8 * scale_v) / scale_v, take the same w in fp32. So the cut, by d of
+// w with 0 <= d < 2^-10, weighs a key's code, lowest value and share alike, and what all keys' d have in common cancels:
+// an output errs by at most 2^-11 of sum p |v - o|. (Below 2^-14 f16 has fewer bits: the code's part of such a weight errs
+// by 2^-24 of the largest w, where that of the lowest value, which may be large beside a small scale, does not.)
+// M moves only when a w would pass 2^8 (a vote; maxima over the warp are taken then only), so w keeps its bits
+// relative to the largest one whatever v's scales are.
 //
 // Copies. Every warp has a ring of its own, filled by bulk copies of 16 rows of codes and their scales (pages
 // are multiples of 16 tokens: a copy never leaves its page), so no barrier but its own holds it up.
 //
-// Split. All groups of 64 keys of all sequences and key heads are cut into equal runs, one a block, on the device, from
+// Split. All groups of 64 or 128 keys of all sequences and key heads are cut into equal runs, one a block, on the device, from
 // the lengths there (a captured graph keeps its grid for every length). A block's warps join in shared memory;
 // where a sequence's head is shared by several blocks each leaves sums in the plan's workspace and a second kernel, that is
 // waiting already, joins them in the blocks' order: results do not depend on which is ready first.
@@ -42,35 +44,44 @@
 namespace c3d {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 16;                    // keys of a step
-constexpr int kGroup = kTile * kWarps;       // keys of the smallest share
-constexpr int kLeastGroups = 4;              // of a block, where there are fewer than enough for all
+constexpr int kTile = 16;                    // keys of an instruction
+constexpr int kLeastKeys = 256;              // of a block, where there are fewer than enough for all
 constexpr float kLowest = -1e30f;            // M before the first key
-constexpr float kLeastLog = -100.0f;         // scales of v below 2^-100 do not move M
+constexpr float kLeastScale = 0x1p-100f;     // of v: a smaller one counts as this
 constexpr uint64_t kCacheTimeoutNs = 2000ull * 1000 * 1000;
 
 template <int CODE>
 constexpr int kScaleBytes = CODE == Q8_INT4 ? 8 : 4;
 template <int CODE, int D>
 constexpr int kRowBytes = CODE == Q8_INT4 ? D / 2 : D;
+// Tiles of a step. Two of 4-bit codes take their turns at the waits, votes and copies together, where registers allow.
+template <int CODE, int D, int NB>
+constexpr int kStepTiles = CODE == Q8_INT4 && NB == 1 && D <= 128 ? 2 : 1;
+template <int CODE, int D, int NB>
+constexpr int kStepKeys = kTile * kStepTiles<CODE, D, NB>;
+template <int CODE, int D, int NB>
+constexpr int kGroup = kStepKeys<CODE, D, NB> * kWarps;  // keys of the smallest share
 template <int CODE, int D>
-constexpr int kStageBytes = 2 * kTile * (kRowBytes<CODE, D> + kScaleBytes<CODE>);
-template <int CODE, int D>
-constexpr int kStages = CODE == Q8_INT4 ? 4 : D == 256 ? 2 : 3;  // what kBlocksPerSm blocks have room for
+constexpr int kTileBytes = 2 * kTile * (kRowBytes<CODE, D> + kScaleBytes<CODE>);
+// Stages of a warp's ring: what kBlocksPerSm blocks have room for.
+template <int CODE, int D, int NB>
+constexpr int kStages = CODE == Q8_INT4 ? 4 / kStepTiles<CODE, D, NB> : D == 256 ? 2 : 3;
 // Channels of a row of the sums in shared memory: 4 more, so that the lanes of a store meet all banks.
 template <int D>
 constexpr int kSumPitch = D + 4;
 template <int CODE, int D, int NB>
-constexpr int kRingBytes = std::max(kWarps * kStages<CODE, D> * kStageBytes<CODE, D>,
+constexpr int kRingBytes = std::max(kWarps * kStages<CODE, D, NB> * kStepTiles<CODE, D, NB> * kTileBytes<CODE, D>,
                                     kWarps * NB * 8 * kSumPitch<D> * 4);
 template <int D, int NB>
 constexpr int kBlocksPerSm = D * NB <= 128 ? 4 : D * NB == 256 ? 3 : 2;
 
 // What a block leaves of a share: for each row the reference, the sum of weights and the channels' sums.
 __host__ __device__ constexpr size_t part_floats(int rows, int dim) { return (size_t)rows * (dim + 2); }
-// The first block of a sequence's head that is shared: its blocks are [this one, last].
+// A sequence's head (with some rows of q) that blocks first to last share. There is one of these for each head, left by
+// the block that begins it, or, where there are more heads than blocks, for each block (which leaves one head unfinished
+// at most).
 struct SharedHead {
-  int last;        // -1: none begins here and ends elsewhere
+  int first, last;  // last -1: none
   int seq, head, row0;
 };
 
@@ -87,17 +98,39 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// x without the bits that f16 has no room for.
+__device__ __forceinline__ float f16_bits(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
+__device__ __forceinline__ float reciprocal_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// d += a * b, or d = a * b for a first product.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                        bool first = false) {
+  if (first)
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 
@@ -106,15 +139,17 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
   return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
 
-// Of the eight 4-bit codes of a word the ones of bits 0 and 16 (from bits 4 and 20: int4_odd) on, minus 8, as a pair.
-__device__ __forceinline__ uint32_t int4_even(uint32_t w) {
-  const uint32_t u = (w & 0x000F000Fu) | 0x64006400u;
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(1032.0f, 1032.0f));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t int4_odd(uint32_t w) {
-  const uint32_t u = (w & 0x00F000F0u) | 0x54005400u;
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(72.0f, 72.0f));
+// Of the eight 4-bit codes of a word the ones from bits 0 and 16 (kOdd: 4 and 20) on, minus 8, as a pair of f16. The
+// masking is one LOP3: written as an AND and an OR of constants it became two.
+template <bool kOdd>
+__device__ __forceinline__ uint32_t int4_signed(uint32_t w) {
+  uint32_t u;
+  if constexpr (kOdd)
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w), "n"(0x00F000F0), "r"(0x54005400));
+  else
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w), "n"(0x000F000F), "r"(0x64006400));
+  const float over = kOdd ? 72.0f : 1032.0f;
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(over, over));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -162,10 +197,11 @@ struct Found {
 };
 
 // Groups of a sequence's keys, one at least: a sequence without keys has an output too. A bad length counts as none.
+template <int GROUP>
 __device__ __forceinline__ int groups_of(const CacheAttnParams& p, int b) {
   const int n = p.lengths[b];
   const bool bad = n < 0 || n > (long long)p.table_width * p.cache.page_size;
-  return bad || n <= 0 ? 1 : (int)(((unsigned)n + kGroup - 1) / kGroup);
+  return bad || n <= 0 ? 1 : (int)(((unsigned)n + GROUP - 1) / GROUP);
 }
 
 __device__ __forceinline__ long long warp_sum(long long v) {
@@ -178,21 +214,23 @@ template <typename T, int CODE, int D, int NB>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     cache_attn_kernel(const CacheAttnParams p, float* parts, SharedHead* shared_heads) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ __align__(8) uint64_t bars[kWarps * kStages<CODE, D>];
+  __shared__ __align__(8) uint64_t bars[kWarps * kStages<CODE, D, NB>];
   __shared__ float stat[2][kWarps][NB * 8];
   __shared__ long long scan[kWarps];
   __shared__ Found found;
   __shared__ int abort_flag, bad_input[2];  // the flag of this round and of the next
 
-  constexpr int kRows = NB * 8, kS = kStages<CODE, D>, kBlocks = D / 16;
+  constexpr int kRows = NB * 8, kS = kStages<CODE, D, NB>, kBlocks = D / 16, kTiles = kStepTiles<CODE, D, NB>;
+  constexpr int kStep = kStepKeys<CODE, D, NB>, kOneTile = kTileBytes<CODE, D>, kStageBytes = kTiles * kOneTile;
   constexpr int kKeyWords = kRowBytes<CODE, D> / 16, kValueWords = kRowBytes<CODE, D> / 32;
+  constexpr int kShare = kGroup<CODE, D, NB>;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
   const Cache& c = p.cache;
   const int group = p.q_heads / c.kv_heads, rows_all = p.tokens * group;
   const int row_blocks = (rows_all + kRows - 1) / kRows;
   const long long heads = (long long)c.kv_heads * row_blocks;
 
-  uint8_t* my_ring = ring + warp * kS * kStageBytes<CODE, D>;
+  uint8_t* my_ring = ring + warp * kS * kStageBytes;
   const uint32_t ring_at = smem_u32(my_ring), bar_at = smem_u32(bars) + warp * kS * 8;
   if (threadIdx.x == 0) abort_flag = 0, bad_input[0] = 0;
   if (lane < kS) mbar_init(bar_at + 8 * lane, 1);
@@ -200,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
 
   // ---- this block's share
   long long total = 0;
-  for (int b = threadIdx.x; b < p.seqs; b += kThreads) total += groups_of(p, b);
+  for (int b = threadIdx.x; b < p.seqs; b += kThreads) total += groups_of<kShare>(p, b);
   total = warp_sum(total);
   if (lane == 0) scan[warp] = total;
   __syncthreads();
@@ -209,9 +247,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   for (int w = 0; w < kWarps; ++w) total += scan[w];
   __syncthreads();
   total *= heads;
-  const int blocks = (int)min((long long)gridDim.x, max(1LL, total / kLeastGroups));
+  const int blocks = (int)min((long long)gridDim.x, max(1LL, total / max(1, kLeastKeys / kShare)));
   pdl_launch_dependents();
-  if (threadIdx.x == 0) shared_heads[blockIdx.x].last = -1;
+  const bool by_head = p.seqs * heads <= (long long)gridDim.x;
+  if (threadIdx.x == 0 && !by_head) shared_heads[blockIdx.x].last = -1;
   if ((int)blockIdx.x >= blocks) return;
   long long at = blockIdx.x * total / blocks;
   const long long until = (blockIdx.x + 1) * total / blocks;
@@ -220,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     long long before = 0;
     for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      const int mine = b < p.seqs ? groups_of(p, b) : 0;
+      const int mine = b < p.seqs ? groups_of<kShare>(p, b) : 0;
       long long sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -247,10 +286,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   const AbortState ab{&abort_flag, p.status, kCacheTimeoutNs};
   const float scale_log2 = p.scale * 1.44269504088896f;
   uint32_t issued = 0, used = 0;  // this warp's copies so far
+  // A tile is four copies: the codes of k and of v and their scales, by the lanes 0 to 3 (4 to 7: the second tile's).
+  constexpr uint32_t kCodes = kTile * kRowBytes<CODE, D>, kScales = kTile * kScaleBytes<CODE>;
+  const uint32_t copy_bytes = t4 < 2 ? kCodes : kScales;
+  const uint32_t copy_dst = ring_at + g * kOneTile + (t4 < 2 ? t4 * kCodes : 2 * kCodes + (t4 - 2) * kScales);
+  const uint8_t* copy_src = t4 == 0   ? c.k_codes
+                            : t4 == 1 ? c.v_codes
+                                      : reinterpret_cast<const uint8_t*>(t4 == 2 ? c.k_scale : c.v_scale);
 
   // ---- the heads of sequences that it covers, or parts of them
   for (int round = 0; at < until; round ^= 1) {
-    const int groups = groups_of(p, seq);
+    const int groups = groups_of<kShare>(p, seq);
     const long long head_index = (at - before * heads) / groups;
     const int first_group = (int)((at - before * heads) - head_index * groups);
     const int take = (int)min((long long)groups - first_group, until - at);
@@ -258,45 +304,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     const int length = p.lengths[seq];
     bool bad = length < 0 || length > (long long)p.table_width * c.page_size;
     const int keys = bad ? 0 : length;
-    const int tiles = (int)(((unsigned)keys + kTile - 1) / kTile);
-    const int first = first_group * kWarps + warp;
-    const int end = min(tiles, (first_group + take) * kWarps);
+    const int tiles = (int)(((unsigned)keys + kTile - 1) / kTile), steps = (tiles + kTiles - 1) / kTiles;
+    const int first = first_group * kWarps + warp;  // of this warp's steps, which are kWarps apart
+    const int end = min(steps, (first_group + take) * kWarps);
     const int count = first < end ? (end - first + kWarps - 1) / kWarps : 0;
     const int* table = p.table + seq * p.table_pitch;
 
-    // The pages of 32 of this warp's tiles, a lane each.
-    auto pages_from = [&](int i) {
-      int page = 0;
-      if (i + lane < count) {
-        page = table[(first + (i + lane) * kWarps) * kTile / c.page_size];
-        if (page < 0 || page >= (int)(c.slots / (unsigned)c.page_size)) {
-          bad = true;
-          page = 0;  // some page of the cache; what is read there is dropped
-        }
+    // Where 32 of this warp's tiles lie, a lane each, in tiles of the whole cache; -1 behind the end.
+    const unsigned page_tiles = (unsigned)c.page_size / kTile;
+    auto places_from = [&](int i) {
+      const int tile = (first + (i + lane / kTiles) * kWarps) * kTiles + lane % kTiles;
+      if (i + lane / kTiles >= count || tile >= tiles) return -1LL;
+      const unsigned entry = (unsigned)tile / page_tiles;
+      unsigned page = (unsigned)table[entry];
+      if (page >= c.slots / (unsigned)c.page_size) {
+        bad = true;
+        page = 0;  // some page of the cache; what is read there is dropped
       }
-      return page;
+      return ((long long)page * c.kv_heads + head) * page_tiles + ((unsigned)tile - entry * page_tiles);
     };
-    int pages = pages_from(0);
+    long long places = places_from(0);
     auto issue = [&](int i) {
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, i % 32);
-      const int place = (first + i * kWarps) * kTile % c.page_size;
-      const long long row = ((long long)page * c.kv_heads + head) * c.page_size + place;
+      const long long place = __shfl_sync(0xFFFFFFFFu, places, i * kTiles % 32 + g % kTiles);
       const uint32_t stage = issued % kS, bar = bar_at + 8 * stage;
-      const uint32_t dst = ring_at + stage * kStageBytes<CODE, D>;
-      constexpr uint32_t kCodes = kTile * kRowBytes<CODE, D>, kScales = kTile * kScaleBytes<CODE>;
-      if (lane == 0) mbar_arrive_expect_tx(bar, kStageBytes<CODE, D>);
+      const bool mine = lane < 4 * kTiles && place >= 0;
+      const bool all = kTiles == 1 || (__ballot_sync(0xFFFFFFFFu, mine) >> 4) != 0;
+      if (lane == 0) mbar_arrive_expect_tx(bar, all ? kStageBytes : kOneTile);
       __syncwarp();
-      if (lane < 4) {
-        const bool is_scale = lane >= 2;
-        const uint8_t* src =
-            is_scale ? reinterpret_cast<const uint8_t*>(lane == 2 ? c.k_scale : c.v_scale) + row * kScaleBytes<CODE>
-                     : (lane == 0 ? c.k_codes : c.v_codes) + row * kRowBytes<CODE, D>;
-        bulk_load(dst + (lane == 0   ? 0
-                         : lane == 1 ? kCodes
-                         : lane == 2 ? 2 * kCodes
-                                     : 2 * kCodes + kScales),
-                  src, is_scale ? kScales : kCodes, bar);
-      }
+      if (mine) bulk_load(copy_dst + stage * kStageBytes, copy_src + place * copy_bytes, copy_bytes, bar);
       ++issued;
     };
     int ahead = min(count, kS);
@@ -313,19 +348,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
       const int t = live ? r / group : 0, h = live ? r - t * group : 0;
       const T* q = static_cast<const T*>(p.q.p) + ((long long)seq * p.tokens + t) * p.q.pitch +
                    (long long)(head * group + h) * p.q.head_pitch;
+      // this lane's channels, 16 bytes at a time
+      constexpr int kCodesOf = CODE == Q8_INT4 ? 8 : 4, kPer = 8 / kCodesOf;  // codes of a word, words of 16 bytes
+      uint4 raw[kKeyWords / kPer];
+#pragma unroll
+      for (int w = 0; w < kKeyWords / kPer; ++w)
+        raw[w] = live ? *reinterpret_cast<const uint4*>(q + key_channel<CODE, D>(t4, w * kPer, 0)) : make_uint4(0, 0, 0, 0);
       float amax = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kKeyWords; ++w)
+      for (int w = 0; w < kKeyWords / kPer; ++w)
 #pragma unroll
-        for (int n = 0; n < (CODE == Q8_INT4 ? 8 : 4); ++n)
-          amax = fmaxf(amax, live ? fabsf(q8_to_float(q[key_channel<CODE, D>(t4, w, n)])) : 0.0f);
+        for (int n = 0; n < 8; ++n) amax = fmaxf(amax, fabsf(q8_to_float(reinterpret_cast<const T*>(&raw[w])[n])));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      // the largest between 2^8 and 2^9, by a power of two
-      const int up = amax > 0.0f && amax < 3.4e38f ? 8 - ilogbf(amax) : 0;
+      // the largest between 2^8 and 2^9, by a power of two (in two parts, each of which fp32 holds)
+      const int up = amax > 0.0f && amax < 3.4e38f ? 135 - (int)(__float_as_uint(amax) >> 23) : 0;
+      const float up0 = __uint_as_float((127 + up / 2) << 23), up1 = __uint_as_float((127 + up - up / 2) << 23);
+      const float down0 = __uint_as_float((127 - up / 2) << 23), down1 = __uint_as_float((127 - up + up / 2) << 23);
       auto value = [&](int w, int n) {
-        const float v = live ? q8_to_float(q[key_channel<CODE, D>(t4, w, n)]) : 0.0f;
-        return scalbnf(v, up);
+        return q8_to_float(reinterpret_cast<const T*>(&raw[w / kPer])[w % kPer * kCodesOf + n]) * up0 * up1;
       };
       float sum = 0.0f;
 #pragma unroll
@@ -333,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
         if constexpr (CODE == Q8_INT4) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            // as int4_even and int4_odd leave them: the codes 2i and 2i + 4, then 2i + 1 and 2i + 5
+            // as int4_signed leaves them: the codes 2i and 2i + 4, then 2i + 1 and 2i + 5
             const __half2 even = __floats2half2_rn(value(w, 2 * i), value(w, 2 * i + 4));
             const __half2 odd = __floats2half2_rn(value(w, 2 * i + 1), value(w, 2 * i + 5));
-            sum += (__low2float(even) + __high2float(even)) + (__low2float(odd) + __high2float(odd));
+            sum += __low2float(even) + __high2float(even) + __low2float(odd) + __high2float(odd);
             q_frag[nb][2 * w + i][0] = *reinterpret_cast<const uint32_t*>(&even);
             q_frag[nb][2 * w + i][1] = *reinterpret_cast<const uint32_t*>(&odd);
           }
@@ -348,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
           }
         }
       }
-      const float back = scalbnf(scale_log2, -up);
+      const float back = scale_log2 * down0 * down1;
       float s = 0.0f;
       if constexpr (CODE == Q8_INT4) {
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
@@ -365,42 +406,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     }
 
     float o[NB][kBlocks][4] = {};
-    float top[NB][2], weight[NB][2], low_sum[NB][2];
+    float top[NB][2], most[NB][2], weight[NB][2], low_sum[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) top[nb][j] = kLowest, weight[nb][j] = 0.0f, low_sum[nb][j] = 0.0f;
+      for (int j = 0; j < 2; ++j) top[nb][j] = most[nb][j] = kLowest, weight[nb][j] = low_sum[nb][j] = 0.0f;
 
-    bool waited = true;
-    for (int i = 0; i < count; ++i) {
-      const uint32_t stage = used % kS;
-      if (waited) waited = wait_bounded_warp(bar_at + 8 * stage, (used / kS) & 1, ab, kAttnTimeout);
-      if (!waited) break;
-      const uint8_t* at_stage = my_ring + stage * kStageBytes<CODE, D>;
-      const uint8_t* k_codes = at_stage;
-      const uint8_t* v_codes = at_stage + kTile * kRowBytes<CODE, D>;
-      const float* k_scale = reinterpret_cast<const float*>(at_stage + 2 * kTile * kRowBytes<CODE, D>);
-      const float* v_scale = k_scale + kTile * kScaleBytes<CODE> / 4;
-      const int key0 = (first + i * kWarps) * kTile;
-      const bool masked = keys - p.tokens + 1 - key0 < kTile;  // for some row
-
-      // scores of the keys g and g + 8
-      float s[NB][4] = {};
-      {
+    // One step: the keys from key0 on, in a stage. kMasked: some row does not see all of them.
+    auto step = [&](auto is_masked, const uint8_t* stage, int key0) {
+      constexpr bool kMasked = decltype(is_masked)::value;
+      float s[kTiles][NB][4];  // of the keys g and g + 8 of each tile
+#pragma unroll
+      for (int u = 0; u < kTiles; ++u) {
         uint32_t a[kKeyWords], b[kKeyWords];
-        load_key<CODE, D>(k_codes + g * kRowBytes<CODE, D>, t4, a);
-        load_key<CODE, D>(k_codes + (g + 8) * kRowBytes<CODE, D>, t4, b);
-        float s2[NB][4] = {};  // every other product: two chains
+        load_key<CODE, D>(stage + u * kOneTile + g * kRowBytes<CODE, D>, t4, a);
+        load_key<CODE, D>(stage + u * kOneTile + (g + 8) * kRowBytes<CODE, D>, t4, b);
+        float s2[NB][4];  // every other product: two chains
 #pragma unroll
         for (int w = 0; w < kKeyWords; ++w) {
           if constexpr (CODE == Q8_INT4) {
             const uint32_t ah = a[w] >> 8, bh = b[w] >> 8;
-            const uint32_t m0[4] = {int4_even(a[w]), int4_even(b[w]), int4_odd(a[w]), int4_odd(b[w])};
-            const uint32_t m1[4] = {int4_even(ah), int4_even(bh), int4_odd(ah), int4_odd(bh)};
+            const uint32_t m0[4] = {int4_signed<false>(a[w]), int4_signed<false>(b[w]), int4_signed<true>(a[w]),
+                                    int4_signed<true>(b[w])};
+            const uint32_t m1[4] = {int4_signed<false>(ah), int4_signed<false>(bh), int4_signed<true>(ah),
+                                    int4_signed<true>(bh)};
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              mma_f16(s[nb], m0, q_frag[nb][2 * w][0], q_frag[nb][2 * w][1]);
-              mma_f16(s2[nb], m1, q_frag[nb][2 * w + 1][0], q_frag[nb][2 * w + 1][1]);
+              mma_f16(s[u][nb], m0, q_frag[nb][2 * w][0], q_frag[nb][2 * w][1], w == 0);
+              mma_f16(s2[nb], m1, q_frag[nb][2 * w + 1][0], q_frag[nb][2 * w + 1][1], w == 0);
             }
           } else {
             uint32_t ha[2], hb[2];
@@ -414,87 +447,95 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
             const uint32_t m[4] = {ha[0], hb[0], ha[1], hb[1]};
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
-              mma_f16(w % 2 ? s2[nb] : s[nb], m, q_frag[nb][w][0], q_frag[nb][w][1]);
+              mma_f16(w % 2 ? s2[nb] : s[u][nb], m, q_frag[nb][w][0], q_frag[nb][w][1], w < 2);
           }
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nb][e] += s2[nb][e];
+          for (int e = 0; e < 4; ++e) s[u][nb][e] += s2[nb][e];
       }
-      float ks[2], kl[2] = {}, vl[2] = {}, v_low[2] = {}, vlog[2];  // of the keys g and g + 8
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int key = g + 8 * j;
-        float vs;
-        if constexpr (CODE == Q8_INT4) {
-          const float2 a = reinterpret_cast<const float2*>(k_scale)[key], b = reinterpret_cast<const float2*>(v_scale)[key];
-          ks[j] = a.x, kl[j] = fmaf(8.0f, a.x, a.y), vs = b.x, vl[j] = fmaf(8.0f, b.x, b.y);
-        } else {
-          ks[j] = k_scale[key], vs = v_scale[key];
-        }
-        if (masked && key0 + key >= keys) vs = 1.0f, vl[j] = 0.0f;  // whatever lies there
-        vlog[j] = __log2f(vs);
-        if constexpr (CODE == Q8_INT4) v_low[j] = __fdividef(vl[j], vs);
-      }
+      float v_mid[kTiles][2], v_inv[kTiles][2];  // of the keys g and g + 8
       bool grows = false;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = e / 2;
-          float x = s[nb][e] * (ks[j] * factor[nb][e % 2]);
-          if constexpr (CODE == Q8_INT4) x = fmaf(kl[j], q_sum[nb][e % 2], x);
-          if (masked && key0 + g + 8 * j >= limit[nb][e % 2]) x = -INFINITY;
-          s[nb][e] = x;
-          grows |= x + fmaxf(vlog[j], kLeastLog) > top[nb][e % 2] + 8.0f;
+        for (int j = 0; j < 2; ++j) {
+          const int key = kTile * u + g + 8 * j;
+          const float* k_scale = reinterpret_cast<const float*>(stage + u * kOneTile + 2 * kCodes);
+          const float* v_scale = k_scale + kScales / 4;
+          float ks, vs, vl = 0.0f;
+          [[maybe_unused]] float k_mid = 0.0f;
+          if constexpr (CODE == Q8_INT4) {
+            const float2 a = reinterpret_cast<const float2*>(k_scale)[g + 8 * j];
+            const float2 b = reinterpret_cast<const float2*>(v_scale)[g + 8 * j];
+            ks = a.x, k_mid = fmaf(8.0f, a.x, a.y), vs = b.x, vl = fmaf(8.0f, b.x, b.y);
+          } else {
+            ks = k_scale[g + 8 * j], vs = v_scale[g + 8 * j];
+          }
+          vs = vs < kLeastScale ? kLeastScale : vs;  // a NaN stays
+          if (kMasked && key0 + key >= keys) vs = 1.0f, vl = 0.0f;  // whatever lies there
+          const float v_log = log2_fast(vs);
+          v_inv[u][j] = reciprocal_fast(vs);
+          v_mid[u][j] = vl * v_inv[u][j];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = fmaf(s[u][nb][2 * j + i], ks * factor[nb][i], v_log);
+              if constexpr (CODE == Q8_INT4) x = fmaf(k_mid, q_sum[nb][i], x);
+              if (kMasked && key0 + key >= limit[nb][i]) x = -INFINITY;
+              s[u][nb][2 * j + i] = x;
+              grows |= x > most[nb][i];
+            }
         }
       if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float m = fmaxf(s[nb][j] + fmaxf(vlog[0], kLeastLog), s[nb][2 + j] + fmaxf(vlog[1], kLeastLog));
+            float m = fmaxf(s[0][nb][j], s[0][nb][2 + j]);
+            if constexpr (kTiles == 2) m = fmaxf(m, fmaxf(s[kTiles - 1][nb][j], s[kTiles - 1][nb][2 + j]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
             m = fmaxf(m, top[nb][j]);
             const float keep = exp2_fast(top[nb][j] - m);
             top[nb][j] = m;
+            most[nb][j] = m + 8.0f;
             weight[nb][j] *= keep;
             low_sum[nb][j] *= keep;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b) o[nb][b][j] *= keep, o[nb][b][2 + j] *= keep;
           }
       }
-      uint32_t p_frag[NB][2];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+      for (int u = 0; u < kTiles; ++u) {
+        uint32_t p_frag[NB][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x0 = s[nb][2 * j] - top[nb][0], x1 = s[nb][2 * j + 1] - top[nb][1];
-          const float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
-          weight[nb][0] += p0;
-          weight[nb][1] += p1;
-          const bool hidden0 = masked && x0 == -INFINITY, hidden1 = masked && x1 == -INFINITY;
-          x0 += hidden0 ? 0.0f : vlog[j];  // which may be NaN
-          x1 += hidden1 ? 0.0f : vlog[j];
-          const __half2 h = __floats2half2_rn(exp2_fast(x0), exp2_fast(x1));
-          p_frag[nb][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h));
-          if constexpr (CODE == Q8_INT4) {
-            const float2 r = __half22float2(h);
-            low_sum[nb][0] += r.x >= 0x1p-14f ? r.x * v_low[j] : hidden0 ? 0.0f : p0 * vl[j];
-            low_sum[nb][1] += r.y >= 0x1p-14f ? r.y * v_low[j] : hidden1 ? 0.0f : p1 * vl[j];
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float x0 = s[u][nb][2 * j], x1 = s[u][nb][2 * j + 1];
+            const float w0 = f16_bits(exp2_fast(x0 - top[nb][0])), w1 = f16_bits(exp2_fast(x1 - top[nb][1]));
+            const __half2 h = __floats2half2_rn(w0, w1);
+            p_frag[nb][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h));
+            // a key that a row does not see may be marked NaN
+            const bool see0 = !kMasked || x0 != -INFINITY, see1 = !kMasked || x1 != -INFINITY;
+            if (see0) weight[nb][0] = fmaf(w0, v_inv[u][j], weight[nb][0]);
+            if (see1) weight[nb][1] = fmaf(w1, v_inv[u][j], weight[nb][1]);
+            if constexpr (CODE == Q8_INT4) {
+              if (see0) low_sum[nb][0] = fmaf(w0, v_mid[u][j], low_sum[nb][0]);
+              if (see1) low_sum[nb][1] = fmaf(w1, v_mid[u][j], low_sum[nb][1]);
+            }
           }
-        }
-
-      // values of the keys 2 t4, the next, and both 8 further on
-      {
+        // values of the keys 2 t4, the next, and both 8 further on
+        const uint8_t* v_codes = stage + u * kOneTile + kCodes;
         uint32_t v[4][kValueWords];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int key = 2 * t4 + (j & 1) + 8 * (j >> 1);
           load_words<kValueWords>(v_codes + key * kRowBytes<CODE, D> + g * kValueWords * 4, v[j]);
-          if (CODE == Q8_E4M3 && masked && key0 + key >= keys) {
+          if (CODE == Q8_E4M3 && kMasked && key0 + kTile * u + key >= keys) {
 #pragma unroll
             for (int w = 0; w < kValueWords; ++w) v[j][w] = 0;  // it may be a NaN
           }
@@ -508,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
               uint32_t lo = __byte_perm(v[0][w], v[1][w], pick), hi = __byte_perm(v[2][w], v[3][w], pick);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t m[4] = {int4_even(lo), int4_odd(lo), int4_even(hi), int4_odd(hi)};
+                const uint32_t m[4] = {int4_signed<false>(lo), int4_signed<true>(lo), int4_signed<false>(hi),
+                                       int4_signed<true>(hi)};
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
                   mma_f16(o[nb][4 * w + 2 * half + i], m, p_frag[nb][0], p_frag[nb][1]);
@@ -535,10 +577,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
           }
         }
       }
+    };
+
+    bool waited = true;
+    for (int i = 0; i < count; ++i) {
+      const uint32_t stage = used % kS;
+      waited = wait_bounded_warp(bar_at + 8 * stage, (used / kS) & 1, ab, kAttnTimeout);
+      if (!waited) break;
+      const int key0 = (first + i * kWarps) * kStep;
+      if (keys - p.tokens + 1 - key0 >= kStep)
+        step(std::false_type{}, my_ring + stage * kStageBytes, key0);
+      else
+        step(std::true_type{}, my_ring + stage * kStageBytes, key0);
       ++used;
       __syncwarp();  // the stage is free
       if (ahead < count) {
-        if (ahead % 32 == 0) pages = pages_from(ahead);
+        if (ahead * kTiles % 32 == 0) places = places_from(ahead);
         issue(ahead++);
       }
     }
@@ -591,10 +645,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     if (threadIdx.x == 0) {
       bad_input[round ^ 1] = 0;
       if (bad_input[round] && !abort_flag) atomicOr(p.status, kAttnBadInput);
-      if (!whole && first_group == 0) {
+      if (first_group == 0 && (by_head || !whole)) {
         // the block that holds this head's last group
         const long long last = before * heads + (head_index + 1) * groups - 1;
-        shared_heads[blockIdx.x] = SharedHead{(int)(((last + 1) * blocks - 1) / total), seq, head, row0};
+        shared_heads[by_head ? seq * heads + head_index : blockIdx.x] =
+            SharedHead{(int)blockIdx.x, whole ? -1 : (int)(((last + 1) * blocks - 1) / total), seq, head, row0};
       }
     }
     for (int i = threadIdx.x; i < kRows * (D / 2); i += kThreads) {
@@ -635,46 +690,62 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   }
 }
 
-// Joins the sums of heads that several blocks share: a block for each first block of such a head and row.
+// Joins the sums of heads that several blocks share: gridDim.y blocks for each of them, between whose rows the warps
+// are divided.
+constexpr int kJoinWarps = 8;
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttnParams p, const float* parts,
-                                                         const SharedHead* shared_heads) {
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheAttnParams p, const float* parts,
+                                                                     const SharedHead* shared_heads) {
   constexpr int kRows = NB * 8, kVec = D / 32;
-  __shared__ float sums[4][D];
-  __shared__ float weights[4];
+  __shared__ float sums[kJoinWarps][D];
+  __shared__ float weights[kJoinWarps];
   pdl_wait_primary();
   const SharedHead s = shared_heads[blockIdx.x];
   if (s.last < 0) return;
-  const int r = blockIdx.y, rr = s.row0 + r;
   const int group = p.q_heads / p.cache.kv_heads;
-  if (rr >= p.tokens * group) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int n = s.last - (int)blockIdx.x + 1;
-  auto part_of = [&](int i) { return parts + (2 * ((long long)blockIdx.x + i) + (i == 0)) * part_floats(kRows, D); };
-  float m = kLowest;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, part_of(i)[r]);
+  const int rows = kRows / gridDim.y, at_once = min(rows, kJoinWarps), share = kJoinWarps / at_once;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, mine = warp % share;
+  const int n = s.last - s.first + 1;
+  auto part_of = [&](int i) { return parts + (2 * ((long long)s.first + i) + (i == 0)) * part_floats(kRows, D); };
+  for (int r0 = blockIdx.y * rows; r0 < (blockIdx.y + 1) * rows; r0 += at_once) {
+    const int r = r0 + warp / share;
+    float m = kLowest;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, part_of(i)[r]);
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
-  float sum[kVec] = {}, l = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += 4) {
-    const float* part = part_of(i);
-    const float keep = exp2_fast(part[r] - m);
-    l = fmaf(part[kRows + r], keep, l);
+    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
+    float sum[kVec] = {}, l = 0.0f;
+#pragma unroll 8
+    for (int i = mine; i < n; i += share) {
+      const float* part = part_of(i);
+      const float keep = exp2_fast(part[r] - m);
+      l = fmaf(part[kRows + r], keep, l);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sum[e] = fmaf(part[2 * kRows + r * D + 32 * e + lane], keep, sum[e]);
+      for (int e = 0; e < kVec; ++e) sum[e] = fmaf(part[2 * kRows + r * D + 32 * e + lane], keep, sum[e]);
+    }
+    if (share > 1) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) sums[warp][32 * e + lane] = sum[e];
+      if (lane == 0) weights[warp] = l;
+      __syncthreads();
+      if (mine == 0) {
+        for (int w = 1; w < share; ++w) {
+          l += weights[warp + w];
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) sum[e] += sums[warp + w][32 * e + lane];
+        }
+      }
+      __syncthreads();
+    }
+    const int rr = s.row0 + r;
+    if (mine == 0 && rr < p.tokens * group) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int t = rr / group, h = rr - t * group;
+      T* out = static_cast<T*>(p.o.p) + ((long long)s.seq * p.tokens + t) * p.o.pitch +
+               (long long)(s.head * group + h) * p.o.head_pitch;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) out[32 * e + lane] = q8_from_float<T>(sum[e] * inv);
+    }
   }
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) sums[warp][32 * e + lane] = sum[e];
-  if (lane == 0) weights[warp] = l;
-  __syncthreads();
-  l = (weights[0] + weights[1]) + (weights[2] + weights[3]);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int t = rr / group, h = rr - t * group;
-  T* out = static_cast<T*>(p.o.p) + ((long long)s.seq * p.tokens + t) * p.o.pitch +
-           (long long)(s.head * group + h) * p.o.head_pitch;
-  for (int i = threadIdx.x; i < D; i += 128)
-    out[i] = q8_from_float<T>(((sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i])) * inv);
 }
 
 // Rows of q that the instructions' columns hold, in eights: 16 where 8 do not hold all of a key head's.
@@ -708,8 +779,11 @@ static cudaError_t cache_attn_form(const CacheAttnParams* p, void* workspace, in
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t config{};
-  config.gridDim = dim3(blocks, NB * 8);
-  config.blockDim = dim3(128);
+  const int row_blocks = (p->tokens * (p->q_heads / p->cache.kv_heads) + 8 * NB - 1) / (8 * NB);
+  const long long heads = (long long)p->seqs * p->cache.kv_heads * row_blocks;
+  // few heads have many parts: blocks for each of their rows of their own
+  config.gridDim = heads <= sms ? dim3((unsigned)heads, NB * 8) : dim3((unsigned)std::min<long long>(heads, blocks), 1);
+  config.blockDim = dim3(kJoinWarps * 32);
   config.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -121,8 +121,8 @@ conv3d_status cache_q8_read_run(const cache_q8_read_args *args);
  * sees nothing (a length below tokens - t) gets 0. The place s of sequence b is page table[b][s /
  * page_size]. A cached row whose scale is NaN makes every output that sees it NaN. Codes and q are multiplied in f16, where
  * codes are exact and a row of q, scaled to 1 by a power of two, errs by at most 2^-12 of each element (2^-25 of the
- * row's largest below 2^-14 of it); p is rounded to f16 beside v's scale; sums, maxima and scales are fp32. Values whose
- * scale is below 2^-100 count as 0 or with fewer bits.
+ * row's largest below 2^-14 of it); p is rounded to f16 beside v's scale; sums, maxima and scales are fp32. Scales of v
+ * below 2^-100 count as 2^-100.
  *
  * A plan holds the device's workspace: a status word and the partial results of sequences that several blocks share,
  * fixed by q_heads, kv_heads, max_tokens and head_dim, whatever the lengths. At most one run of a plan may be in
