@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
             if constexpr (kTiles == 2) m = fmaxf(m, fmaxf(s[kTiles - 1][nb][j], s[kTiles - 1][nb][2 + j]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
-            m = fmaxf(m, top[nb][j]);
-            const float keep = exp2_fast(top[nb][j] - m);
+            if (!(m > most[nb][j])) m = top[nb][j];  // a row's results do not depend on its neighbours
+            const float keep = m == top[nb][j] ? 1.0f : exp2_fast(top[nb][j] - m);
             top[nb][j] = m;
             most[nb][j] = m + 8.0f;
             weight[nb][j] *= keep;

@@ -68,9 +68,11 @@ struct PromptParams {
   Heads q, k, v, o;
   const int *starts, *key_starts;
   int q_rows, k_rows, seqs, q_heads, kv_heads, head_dim, causal;
-  float scale;
+  int negate;            // the scale is negative
+  float scale;           // its magnitude times log2(e)
   int* status;
 };
+cudaError_t prompt_attn_setup();       // the kernels' shared-memory grant on this device
 cudaError_t launch_prompt_attn(const PromptParams& p, int value_type, cudaStream_t stream);
 
 }  // namespace c3d

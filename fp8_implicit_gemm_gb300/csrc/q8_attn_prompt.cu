@@ -1,59 +1,479 @@
-// q8_attn_prompt.cu -- attention over whole prompts, packed one behind the other.
+// q8_attn_prompt.cu -- attention over whole prompts on the tensor cores, packed sequences, grouped heads.
 //
-// A warp a row of q: its lanes hold the head's elements, each key's score is a sum over the warp, and the
-// softmax runs along with it (a running maximum and sum).
+// A block takes 256 rows of q of one head, two tiles A and B of 128, and walks over the keys 128 at a time:
+//   S = Q K^T (tcgen05, both operands in shared memory), P = 2^(S scale - m) in registers, O += P V (P from TMEM, V from
+//   shared memory), the running maximum m and sum l of a row held by the one thread that owns the row.
+// TMEM is full: two S of 128 columns, two O of up to 128; P, half as wide as S, takes S's place. While one tile's
+// softmax runs the tensor cores work on the other: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1). A commit after each product
+// hands it on; products of one thread run in the order of their issue, so QK may overwrite the P that PV before it reads.
+//
+// m lags behind: O and l are scaled only when a row's maximum has grown by more than 2^8 over m (P stays below 2^8 and keeps
+// its bits), which is rare after the first keys; the row's thread then waits for the tile's last product and
+// rescales O in TMEM.
+//
+// What a row does not see. A masked score is -inf, its weight 0; but 0 times a value that is not finite is NaN, so the tiles
+// that some row sees only in part (the last ones of a block) pass two more warps, which zero such values in shared
+// memory. Rows that do see them add them when they are done, read from memory again (their weight is positive, so the
+// sum is the value).
+//
+// Roles: warps 0 to 7 softmax and epilogue (a row a thread), 8 the products, 9 the copies, 10 and 11 the check of values.
+// Every wait is bounded; one that runs out records a status bit and the block winds down.
+#include <algorithm>
+
+#include "conv_common.cuh"
 #include "q8_attn_internal.h"
 #include "q8_common.cuh"
+#include "q8_host.h"
 
 namespace c3d {
 
-constexpr int kRowThreads = 128;
+constexpr int kRows = 128;                   // of a tile of q
+constexpr int kKeys = 128;                   // of a tile of k and v
+constexpr int kUnitRows = 2 * kRows;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kCheckWarp = 10;
+constexpr int kPromptThreads = 12 * 32;
+constexpr uint32_t kHalfBytes = 128 * 128;   // 64 channels of a tile: 128 rows of 128 bytes
+constexpr int kPromptSlots = 5;              // tiles of k and v under way
+constexpr float kNone = -1e30f;              // m before the first key
+constexpr float kGrowth = 8.0f;              // of a maximum, as a power of two, before O follows
+constexpr uint64_t kPromptTimeoutNs = 2000ull * 1000 * 1000, kSettleNs = 2ull * 1000 * 1000;
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256, kColTile = 128;
+
+template <int HALVES>
+constexpr uint32_t kTileBytes = HALVES * kHalfBytes;
+template <int HALVES>
+constexpr size_t kPromptSmem = 1024 + (2 + kPromptSlots) * (size_t)kTileBytes<HALVES> + 256;
+
+// Barriers. The copies of tiles of v that are checked have one each, as the warps that check do not follow the slots' phases;
+// they then arrive for the slot in the copy's place. (The rows of a block end within 255 keys of each other: 3 tiles.)
+constexpr int kMostChecked = 3;
+enum { kBarQ, kBarDrain, kBarRaw, kBarS = kBarRaw + kMostChecked, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarFull = kBarO + 2,
+       kBarEmpty = kBarFull + kPromptSlots, kBarCount = kBarEmpty + kPromptSlots };
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// D (+)= A * B with A in TMEM (row i in lane i, two consecutive elements of K in each column), one CTA.
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of V as the B operand: channels (the product's N) contiguous, keys (its K) 128 bytes apart, 128-byte
+// swizzle. Groups of 8 keys follow each other by 1024 bytes (stride offset), blocks of 64 channels by kHalfBytes
+// (leading offset).
+__device__ __forceinline__ uint64_t make_v_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kHalfBytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(kLayoutSw128) << 61;
+  return d;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) prompt_attn_kernel(const PromptParams p) {
-  const long long id = (long long)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31, dim = p.head_dim;
-  if (id >= (long long)p.q_rows * p.q_heads) return;
-  const int head = (int)(id % p.q_heads), kv = head / (p.q_heads / p.kv_heads);
-  const int row = (int)(id / p.q_heads);
-  int seq = -1, begin = 0, end = 0;
-  for (int b = 0; b < p.seqs && seq < 0; ++b) {
-    begin = max(0, p.starts[b]);
-    end = min(p.q_rows, p.starts[b + 1]);
-    if (row >= begin && row < end) seq = b;
+constexpr uint32_t kExponent2 = std::is_same_v<T, __half> ? 0x7C007C00u : 0x7F807F80u;  // of a pair
+template <typename T>
+constexpr uint32_t kCarry2 = std::is_same_v<T, __half> ? 0x04000400u : 0x00800080u;     // to the sign if all set
+
+template <typename T, int HALVES>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const PromptParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[kBarCount];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word, poison_word;
+  __shared__ int scan[kPromptThreads / 32];
+  __shared__ int found[2];
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8u * i; };
+
+  if (threadIdx.x == 0) {
+    abort_word = 0;
+    poison_word = 0;
+    found[0] = -1;
+    for (int i = 0; i < kBarCount; ++i)
+      mbar_init(bar(i), i == kBarP || i == kBarP + 1 ? 4 : 1);
+    fence_mbar_init();
   }
-  if (seq < 0) return;
-  const int* ks = p.key_starts ? p.key_starts : p.starts;
-  const int k0 = min(max(0, ks[seq]), p.k_rows), k1 = min(max(k0, ks[seq + 1]), p.k_rows), keys = k1 - k0;
-  const int limit = p.causal ? min(keys, row - begin + 1 + keys - (end - begin)) : keys;
-  const T* q = static_cast<const T*>(p.q.p) + row * p.q.pitch + head * p.q.head_pitch;
-  float qf[4] = {}, o[4] = {};
-  for (int i = 0; 32 * i + lane < dim; ++i) qf[i] = q8_to_float(q[32 * i + lane]) * p.scale * 1.44269504f;
-  float top = -1e30f, sum = 0.0f;
-  for (int s = 0; s < limit; ++s) {
-    const T* k = static_cast<const T*>(p.k.p) + (k0 + s) * p.k.pitch + kv * p.k.head_pitch;
-    const T* v = static_cast<const T*>(p.v.p) + (k0 + s) * p.v.pitch + kv * p.v.head_pitch;
-    float x = 0.0f;
-    for (int i = 0; 32 * i + lane < dim; ++i) x = fmaf(qf[i], q8_to_float(k[32 * i + lane]), x);
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, w);
-    const float now = fmaxf(top, x), keep = exp2f(top - now), pr = exp2f(x - now);
-    top = now;
-    sum = sum * keep + pr;
-    for (int i = 0; 32 * i + lane < dim; ++i) o[i] = fmaf(pr, q8_to_float(v[32 * i + lane]), o[i] * keep);
+
+  // ---- the rows: unit `want` of all sequences' units, counted from the last one, whose keys are the most
+  const int head = blockIdx.x % p.q_heads, kv_head = head / (p.q_heads / p.kv_heads);
+  auto begin_of = [&](const int* starts, int b, int rows) { return min(max(starts[b], 0), rows); };
+  auto end_of = [&](const int* starts, int b, int rows, int begin) { return min(max(starts[b + 1], begin), rows); };
+  auto units_of = [&](int b) {
+    if (b >= p.seqs) return 0;
+    const int begin = begin_of(p.starts, b, p.q_rows);
+    return (end_of(p.starts, b, p.q_rows, begin) - begin + kUnitRows - 1) / kUnitRows;
+  };
+  const int want = blockIdx.x / p.q_heads;
+  {
+    int after = 0;  // units of the sequences behind
+    for (int b1 = p.seqs; b1 > 0; b1 -= kPromptThreads) {
+      const int b = b1 - 1 - (int)threadIdx.x, mine = b >= 0 ? units_of(b) : 0;
+      int sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (lane == 31) scan[warp] = sum;
+      __syncthreads();
+      int all = after;
+      sum += after;
+      for (int w = 0; w < kPromptThreads / 32; ++w) {
+        if (w < warp) sum += scan[w];
+        all += scan[w];
+      }
+      if (sum > want && sum - mine <= want) {
+        found[0] = b;
+        found[1] = mine - 1 - (want - (sum - mine));
+      }
+      __syncthreads();
+      after = all;
+      if (all > want) break;
+    }
   }
-  T* out = static_cast<T*>(p.o.p) + row * p.o.pitch + head * p.o.head_pitch;
-  for (int i = 0; 32 * i + lane < dim; ++i)
-    out[32 * i + lane] = q8_from_float<T>(sum == 0.0f ? 0.0f : o[i] / sum);
+  __syncthreads();
+  const int seq = found[0];
+  if (seq < 0) return;  // more blocks than units
+  const int* key_starts = p.key_starts ? p.key_starts : p.starts;
+  const int q0 = begin_of(p.starts, seq, p.q_rows), queries = end_of(p.starts, seq, p.q_rows, q0) - q0;
+  const int k0 = begin_of(key_starts, seq, p.k_rows), keys = end_of(key_starts, seq, p.k_rows, k0) - k0;
+  const int row0 = found[1] * kUnitRows;
+  // Keys that row r of the sequence sees.
+  auto limit_of = [&](int r) { return p.causal ? min(keys, max(0, r + 1 + keys - queries)) : keys; };
+  int tiles[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int first = row0 + t * kRows, last = min(first + kRows, queries) - 1;
+    tiles[t] = first < queries ? (limit_of(last) + kKeys - 1) / kKeys : 0;
+  }
+  const int all_tiles = max(tiles[0], tiles[1]);
+  const int checked_from = limit_of(row0) / kKeys;  // tiles from here on are not seen whole by every row
+
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_flag = &abort_word;
+  const AbortState ab{abort_flag, p.status, kPromptTimeoutNs};
+  auto q_at = [&](int t) { return base + t * kTileBytes<HALVES>; };
+  auto slot_at = [&](int i) { return base + (2 + i % kPromptSlots) * kTileBytes<HALVES>; };
+  auto full = [&](int i) { return bar(kBarFull + i % kPromptSlots); };
+  auto empty = [&](int i) { return bar(kBarEmpty + i % kPromptSlots); };
+  auto lap = [&](int i) { return (uint32_t)(i / kPromptSlots) & 1u; };  // K of tile j is copy 2j, V copy 2j + 1
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------------------------ softmax
+    const int t = warp / 4, row = row0 + t * kRows + (warp % 4) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's lanes of TMEM, << 16
+    const uint32_t s_at = tmem + kColS + t * kColTile + lanes, o_at = tmem + kColO + t * kColTile + lanes;
+    const int limit = row < queries ? limit_of(row) : 0;
+    const int whole = limit_of(row0 + t * kRows + (warp % 4) * 32);  // of this warp's first row: the fewest
+    const bool some_row_out = row0 + t * kRows + (warp % 4) * 32 + 31 >= queries;
+    float m = kNone;
+    float2 l = make_float2(0.0f, 0.0f);
+    bool ok = true;
+    for (int j = 0; j < tiles[t]; ++j) {
+      ok = wait_bounded_warp(bar(kBarS + t), j & 1, ab, kAttnTimeout);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_at + 32 * i, s[i]);
+      tmem_ld_wait();
+      auto f = [&](int c) -> float { return __uint_as_float(s[c / 32][c % 32]); };
+      if (whole - j * kKeys < kKeys || some_row_out) {
+        const int seen = limit - j * kKeys;
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+          if (c >= seen) s[c / 32][c % 32] = 0xFF800000u;
+      }
+      float top[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i] = fmaxf(f(32 * i), f(32 * i + 1));
+#pragma unroll
+      for (int c = 2; c < 32; c += 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], f(32 * i + c), f(32 * i + c + 1));
+      const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+      const bool grows = most > m && (m == kNone || (most - m) * p.scale > kGrowth);
+      if (__any_sync(0xFFFFFFFFu, grows)) {
+        // of the rows that grow: the others' results do not depend on their neighbours
+        const float now = grows ? most : m, keep = !grows ? 1.0f : m == kNone ? 0.0f : exp2_fast((m - now) * p.scale);
+        if (j > 0) {
+          ok = wait_bounded_warp(bar(kBarO + t), (j - 1) & 1, ab, kAttnTimeout);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < 2 * HALVES; ++i) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_at + 32 * i, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * keep);
+            tmem_st_32x32b_x32(o_at + 32 * i, o);
+          }
+        }
+        l.x *= keep;
+        l.y *= keep;
+        m = now;
+      }
+      const float neg = m == kNone ? 0.0f : -m * p.scale;
+      const float2 scale2 = make_float2(p.scale, p.scale), neg2 = make_float2(neg, neg);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float2 x = make_float2(f(64 * half + 2 * c), f(64 * half + 2 * c + 1));
+          x = q8_fma2(x, scale2, neg2);
+          x.x = exp2_fast(x.x);
+          x.y = exp2_fast(x.y);
+          l = q8_add2(l, x);
+          w[c] = q8_pack2<T>(x);
+        }
+        tmem_st_32x32b_x32(s_at + 32 * half, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarP + t));
+    }
+    // ---- the row's output
+    if (ok && tiles[t] > 0) {
+      ok = wait_bounded_warp(bar(kBarO + t), (tiles[t] - 1) & 1, ab, kAttnTimeout);
+      tc_fence_after();
+    }
+    if (ok) {
+      const bool poison = *reinterpret_cast<volatile int*>(&poison_word) != 0;
+      const float sum = l.x + l.y, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      T* out = static_cast<T*>(p.o.p) + (long long)(q0 + row) * p.o.pitch + head * p.o.head_pitch;
+      const T* v = static_cast<const T*>(p.v.p) + (long long)k0 * p.v.pitch + kv_head * p.v.head_pitch;
+#pragma unroll
+      for (int i = 0; i < 2 * HALVES; ++i) {
+        uint32_t o[32];
+        if (tiles[t] > 0) {  // the same for the whole warp
+          tmem_ld_32x32b_x32(o_at + 32 * i, o);
+          tmem_ld_wait();
+        }
+        float x[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = sum == 0.0f ? 0.0f : __uint_as_float(o[c]) * inv;
+        if (poison)
+          for (int k = checked_from * kKeys; k < limit; ++k)
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (32 * i + c < p.head_dim) {
+                const float add = q8_to_float(v[k * p.v.pitch + 32 * i + c]);
+                if (!(fabsf(add) <= 3.4028234e38f)) x[c] += add;
+              }
+        if (row < queries) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            if (32 * i + c < p.head_dim) {
+              uint4 w;
+              w.x = q8_pack2<T>(make_float2(x[c], x[c + 1]));
+              w.y = q8_pack2<T>(make_float2(x[c + 2], x[c + 3]));
+              w.z = q8_pack2<T>(make_float2(x[c + 4], x[c + 5]));
+              w.w = q8_pack2<T>(make_float2(x[c + 6], x[c + 7]));
+              *reinterpret_cast<uint4*>(out + 32 * i + c) = w;
+            }
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------------------ products
+    constexpr bool kBf16 = !std::is_same_v<T, __half>;
+    const uint32_t type = kBf16 ? make_idesc_bf16_f32(kRows, kKeys) : make_idesc_f16_f32(kRows, kKeys);
+    const uint32_t qk_idesc = type | (p.negate ? 1u << 13 : 0u);  // -Q for a negative scale
+    const uint32_t pv_idesc = (kBf16 ? make_idesc_bf16_f32(kRows, 64 * HALVES) : make_idesc_f16_f32(kRows, 64 * HALVES)) |
+                              (1u << 16);  // B lies with its N contiguous
+    const int qk_steps = (p.head_dim + 15) / 16;
+    auto qk = [&](int t, int j) {
+      if (elect_one()) {
+        for (int s = 0; s < qk_steps; ++s) {
+          const uint32_t at = (s / 4) * kHalfBytes + (s % 4) * 32;
+          mma_bf16(tmem + kColS + t * kColTile, make_sw128_kmajor_desc(q_at(t) + at),
+                   make_sw128_kmajor_desc(slot_at(2 * j) + at), qk_idesc, s > 0);
+        }
+        mma_commit(bar(kBarS + t));
+        if (t == 1 || tiles[1] <= j) mma_commit(empty(2 * j));
+      }
+      __syncwarp();
+    };
+    bool ok = all_tiles == 0 || wait_bounded_warp(bar(kBarQ), 0, ab, kAttnTimeout);
+    if (ok && all_tiles > 0) ok = wait_bounded_warp(full(0), 0, ab, kAttnTimeout);
+    tc_fence_after();
+    for (int t = 0; t < 2; ++t)
+      if (ok && tiles[t] > 0) qk(t, 0);
+    for (int j = 0; ok && j < all_tiles; ++j) {
+      for (int t = 0; ok && t < 2; ++t) {
+        if (j >= tiles[t]) continue;
+        ok = wait_bounded_warp(bar(kBarP + t), j & 1, ab, kAttnTimeout) &&
+             wait_bounded_warp(full(2 * j + 1), lap(2 * j + 1), ab, kAttnTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < kKeys / 16; ++s)
+            mma_f16_tmem_a(tmem + kColO + t * kColTile, tmem + kColS + t * kColTile + 8 * s,
+                           make_v_desc(slot_at(2 * j + 1) + s * 2048), pv_idesc, j > 0 || s > 0);
+          mma_commit(bar(kBarO + t));
+          if (t == 1 || tiles[1] <= j) mma_commit(empty(2 * j + 1));
+        }
+        __syncwarp();
+        if (j + 1 < tiles[t]) {
+          ok = wait_bounded_warp(full(2 * j + 2), lap(2 * j + 2), ab, kAttnTimeout);
+          if (!ok) break;
+          tc_fence_after();
+          qk(t, j + 1);
+        }
+      }
+    }
+    // every product is complete before TMEM is released
+    if (elect_one()) mma_commit(bar(kBarDrain));
+    __syncwarp();
+    wait_drain(bar(kBarDrain), 0, kPromptTimeoutNs, p.status, kAttnTimeout);
+  } else if (warp == kTmaWarp) {
+    // ------------------------------------------------------------------------------ copies
+    if (all_tiles > 0) {
+      if (elect_one()) {
+        const int q_tiles = tiles[1] > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(bar(kBarQ), q_tiles * kTileBytes<HALVES>);
+        for (int t = 0; t < q_tiles; ++t)
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_3d(q_at(t) + h * kHalfBytes, &qmap, bar(kBarQ), 64 * h, head, q0 + row0 + t * kRows);
+      }
+      __syncwarp();
+    }
+    for (int i = 0; i < 2 * all_tiles; ++i) {
+      if (i >= kPromptSlots && !wait_bounded_warp(empty(i), lap(i) ^ 1u, ab, kAttnTimeout)) break;
+      if (elect_one()) {
+        const uint32_t to = i % 2 && i / 2 >= checked_from ? bar(kBarRaw + i / 2 - checked_from) : full(i);
+        mbar_arrive_expect_tx(to, kTileBytes<HALVES>);
+        for (int h = 0; h < HALVES; ++h)
+          tma_load_3d(slot_at(i) + h * kHalfBytes, i % 2 ? &vmap : &kmap, to, 64 * h, kv_head,
+                      k0 + (i / 2) * kKeys);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------------------------ values that are not finite
+    const int thread = threadIdx.x - kCheckWarp * 32;
+    for (int j = checked_from; j < all_tiles; ++j) {
+      if (!wait_bounded_warp(bar(kBarRaw + j - checked_from), 0, ab, kAttnTimeout)) break;
+      uint8_t* tile = raw + (slot_at(2 * j + 1) - smem_u32(raw));
+      // 16 bytes at a time: whether any is not finite, before which
+      uint32_t any = 0;
+#pragma unroll 8
+      for (uint32_t i = thread; i < kTileBytes<HALVES> / 16; i += 64) {
+        const uint4 w = *reinterpret_cast<const uint4*>(tile + 16 * i);
+        any |= (w.x & kExponent2<T>) + kCarry2<T>;
+        any |= (w.y & kExponent2<T>) + kCarry2<T>;
+        any |= (w.z & kExponent2<T>) + kCarry2<T>;
+        any |= (w.w & kExponent2<T>) + kCarry2<T>;
+      }
+      if (__any_sync(0xFFFFFFFFu, any & 0x80008000u)) {
+        for (uint32_t i = 4 * thread; i < kTileBytes<HALVES> / 4; i += i % 4 == 3 ? 4 * 64 - 3 : 1) {  // the same ones
+          uint32_t* word = reinterpret_cast<uint32_t*>(tile) + i;
+          const uint32_t bad = ((*word & kExponent2<T>) + kCarry2<T>) & 0x80008000u;
+          if (!bad) continue;
+          const int key = j * kKeys + (int)(i * 4 % kHalfBytes) / 128;
+          *word &= (bad & 0x8000u ? 0u : 0xFFFFu) | (bad & 0x80000000u ? 0u : 0xFFFF0000u);
+          if (key < keys) *reinterpret_cast<volatile int*>(&poison_word) = 1;
+        }
+        __threadfence_block();
+        fence_proxy_async_smem();
+      }
+      named_barrier_sync(1, 64);
+      if (thread == 0) mbar_arrive(full(2 * j + 1));
+    }
+  }
+  __syncwarp();
+  if (*abort_flag) sleep_ns_bounded(kSettleNs);  // copies in flight land
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Heads of 16-bit values in boxes of 64 channels by 128 rows of one head; what lies outside reads zero.
+static bool encode_heads(CUtensorMap* map, const Heads& m, bool bf16, int rows, int heads, int dim) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const long long unit = (dim + 7) / 8 * 8;  // a pitch that no second row uses
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)(2 * (heads > 1 ? m.head_pitch : unit)),
+                                 (cuuint64_t)(2 * (rows > 1 ? m.pitch : unit * heads))};
+  const cuuint32_t box[3] = {64, 1, 128}, steps[3] = {1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, m.p, dims, strides,
+             box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int HALVES>
+static cudaError_t prompt_form(const PromptParams* p, cudaStream_t stream) {
+  auto kernel = prompt_attn_kernel<T, HALVES>;
+  if (!p) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPromptSmem<HALVES>);
+  constexpr bool kBf16 = !std::is_same_v<T, __half>;
+  CUtensorMap qmap{}, kmap{}, vmap{};
+  if (!encode_heads(&qmap, p->q, kBf16, p->q_rows, p->q_heads, p->head_dim)) return cudaErrorInvalidValue;
+  if (p->k_rows == 0) {
+    kmap = vmap = qmap;  // not used
+  } else if (!encode_heads(&kmap, p->k, kBf16, p->k_rows, p->kv_heads, p->head_dim) ||
+             !encode_heads(&vmap, p->v, kBf16, p->k_rows, p->kv_heads, p->head_dim)) {
+    return cudaErrorInvalidValue;
+  }
+  const long long units = p->q_rows / kUnitRows + std::min<long long>(p->seqs, p->q_rows);  // at most
+  kernel<<<(unsigned)(units * p->q_heads), kPromptThreads, kPromptSmem<HALVES>, stream>>>(qmap, kmap, vmap, *p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t prompt_of(int dim, const PromptParams* p, cudaStream_t stream) {
+  return dim <= 64 ? prompt_form<T, 1>(p, stream) : prompt_form<T, 2>(p, stream);
+}
+
+cudaError_t prompt_attn_setup() {
+  for (int dim : {64, 128}) {
+    cudaError_t e = prompt_of<__nv_bfloat16>(dim, nullptr, nullptr);
+    if (e == cudaSuccess) e = prompt_of<__half>(dim, nullptr, nullptr);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_prompt_attn(const PromptParams& p, int value_type, cudaStream_t stream) {
-  const long long rows = (long long)p.q_rows * p.q_heads;
-  const unsigned blocks = (unsigned)((rows + kRowThreads / 32 - 1) / (kRowThreads / 32));
-  if (value_type == Q8_BF16)
-    prompt_attn_kernel<__nv_bfloat16><<<blocks, kRowThreads, 0, stream>>>(p);
-  else
-    prompt_attn_kernel<__half><<<blocks, kRowThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return value_type == Q8_BF16 ? prompt_of<__nv_bfloat16>(p.head_dim, &p, stream) : prompt_of<__half>(p.head_dim, &p, stream);
 }
 
 }  // namespace c3d
