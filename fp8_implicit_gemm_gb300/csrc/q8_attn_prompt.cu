@@ -50,6 +50,19 @@ constexpr int kMostChecked = 3;
 enum { kBarQ, kBarDrain, kBarRaw, kBarS = kBarRaw + kMostChecked, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarFull = kBarO + 2,
        kBarEmpty = kBarFull + kPromptSlots, kBarCount = kBarEmpty + kPromptSlots };
 
+// A warpgroup's registers a thread, raised or lowered. The block is launched with 168 for each of its 384 threads; 256 x 208
+// and 128 x 80 are less than that in all, so the raise never waits for more than the others' drop.
+constexpr int kSoftmaxRegisters = 208, kOtherRegisters = 80;
+static_assert(256 * kSoftmaxRegisters + 128 * kOtherRegisters <= 384 * 168);
+template <int N>
+__device__ __forceinline__ void set_max_registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -192,6 +205,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   auto lap = [&](int i) { return (uint32_t)(i / kPromptSlots) & 1u; };  // K of tile j is copy 2j, V copy 2j + 1
 
   if (warp < kSoftmaxWarps) {
+    set_max_registers_up<kSoftmaxRegisters>();
     // ------------------------------------------------------------------------------ softmax
     const int t = warp / 4, row = row0 + t * kRows + (warp % 4) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's lanes of TMEM, << 16
@@ -310,7 +324,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (set_max_registers_down<kOtherRegisters>(); warp == kMmaWarp) {
     // ------------------------------------------------------------------------------ products
     constexpr bool kBf16 = !std::is_same_v<T, __half>;
     const uint32_t type = kBf16 ? make_idesc_bf16_f32(kRows, kKeys) : make_idesc_f16_f32(kRows, kKeys);
