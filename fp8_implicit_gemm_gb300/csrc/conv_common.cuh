@@ -64,6 +64,32 @@ __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, uint64
   }
 }
 
+// wait_bounded_warp with less in the way of the next try: the timer, whose read takes several hundred
+// cycles, and the abort flag are looked at after every 64 misses.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const AbortState& ab,
+                                        int code) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xFFFFFFFFu, ok)) {
+    uint64_t t0 = 0;
+    for (uint32_t misses = 1; !ok; ++misses) {
+      ok = mbar_try_wait(bar, parity);
+      if (ok || (misses & 63u) != 0) continue;
+      if (*ab.flag) break;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > ab.timeout_ns) {
+        *ab.flag = 1;
+        atomicOr(ab.status, code);
+        __threadfence();
+        break;
+      }
+    }
+    ok = __all_sync(0xFFFFFFFFu, ok);
+  }
+  return ok;
+}
+
 // Busy-wait for `ns` nanoseconds (used only on the abort path, to let copies in flight land).
 __device__ __forceinline__ void sleep_ns_bounded(uint64_t ns) {
   const uint64_t t0 = globaltimer_ns();

@@ -37,7 +37,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "conv_common.cuh"
 #include "q8_attn_internal.h"
 #include "q8_common.cuh"
 
@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     bool waited = true;
     for (int i = 0; i < count; ++i) {
       const uint32_t stage = used % kS;
-      waited = wait_bounded_warp(bar_at + 8 * stage, (used / kS) & 1, ab, kAttnTimeout);
+      waited = tc_wait(bar_at + 8 * stage, (used / kS) & 1, ab, kAttnTimeout);
       if (!waited) break;
       const int key0 = (first + i * kWarps) * kStep;
       if (keys - p.tokens + 1 - key0 >= kStep)
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     if (!waited) {  // the copies under way land before the ring is used again; then all is given up
       for (; used < issued; ++used) {
         int own = 0;
-        wait_bounded_warp(bar_at + 8 * (used % kS), (used / kS) & 1,
+        tc_wait(bar_at + 8 * (used % kS), (used / kS) & 1,
                           AbortState{&own, p.status, 1000000ull}, kAttnTimeout);
       }
       bad = true;

@@ -4,12 +4,12 @@
 //   S = Q K^T (tcgen05, both operands in shared memory), P = 2^(S scale - m) in registers, O += P V (P from TMEM, V from
 //   shared memory), the running maximum m and sum l of a row held by the one thread that owns the row.
 // TMEM is full: two S of 128 columns, two O of up to 128; P, half as wide as S, takes S's place. While one tile's
-// softmax runs the tensor cores work on the other: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1). A commit after each product
-// hands it on; products of one thread run in the order of their issue, so QK may overwrite the P that PV before it reads.
+// softmax runs the tensor cores work on the other: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1). The commit after QK_A(j+1)
+// says that PV_A(j) is done too; products of one thread run in the order of their issue, so QK may overwrite the P that
+// PV before it reads.
 //
 // m lags behind: O and l are scaled only when a row's maximum has grown by more than 2^8 over m (P stays below 2^8 and keeps
-// its bits), which is rare after the first keys; the row's thread then waits for the tile's last product and
-// rescales O in TMEM.
+// its bits), which is rare after the first keys; the row's thread then rescales O in TMEM.
 //
 // What a row does not see. A masked score is -inf, its weight 0; but 0 times a value that is not finite is NaN, so the tiles
 // that some row sees only in part (the last ones of a block) pass two more warps, which zero such values in shared
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     float2 l = make_float2(0.0f, 0.0f);
     bool ok = true;
     for (int j = 0; j < tiles[t]; ++j) {
-      ok = wait_bounded_warp(bar(kBarS + t), j & 1, ab, kAttnTimeout);
+      ok = tc_wait(bar(kBarS + t), j & 1, ab, kAttnTimeout);
       if (!ok) break;
       tc_fence_after();
       uint32_t s[4][32];
@@ -243,10 +243,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (__any_sync(0xFFFFFFFFu, grows)) {
         // of the rows that grow: the others' results do not depend on their neighbours
         const float now = grows ? most : m, keep = !grows ? 1.0f : m == kNone ? 0.0f : exp2_fast((m - now) * p.scale);
-        if (j > 0) {
-          ok = wait_bounded_warp(bar(kBarO + t), (j - 1) & 1, ab, kAttnTimeout);
-          if (!ok) break;
-          tc_fence_after();
+        if (j > 0) {  // the tile's product before these scores is complete
 #pragma unroll
           for (int i = 0; i < 2 * HALVES; ++i) {
             uint32_t o[32];
@@ -284,7 +281,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     // ---- the row's output
     if (ok && tiles[t] > 0) {
-      ok = wait_bounded_warp(bar(kBarO + t), (tiles[t] - 1) & 1, ab, kAttnTimeout);
+      ok = tc_wait(bar(kBarO + t), 0, ab, kAttnTimeout);
       tc_fence_after();
     }
     if (ok) {
@@ -332,45 +329,57 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t pv_idesc = (kBf16 ? make_idesc_bf16_f32(kRows, 64 * HALVES) : make_idesc_f16_f32(kRows, 64 * HALVES)) |
                               (1u << 16);  // B lies with its N contiguous
     const int qk_steps = (p.head_dim + 15) / 16;
-    auto qk = [&](int t, int j) {
+    // Descriptors of the first tiles; others lie a multiple of 16 bytes further on. This warp's instructions bound a block
+    // whose softmax keeps up (a wait takes it some 160 cycles, a commit 60, a product of 128 x 128 x 16 is 64 for the
+    // tensor cores), so it waits for a tile of k or v once, and commits what somebody waits for.
+    constexpr uint32_t kTile16 = kTileBytes<HALVES> >> 4;
+    const uint64_t q_desc = make_sw128_kmajor_desc(q_at(0)), k_desc = make_sw128_kmajor_desc(slot_at(0));
+    const uint64_t v_desc = make_v_desc(slot_at(0));
+    auto qk = [&](int t, uint32_t slot, bool last_use) {
       if (elect_one()) {
-        for (int s = 0; s < qk_steps; ++s) {
-          const uint32_t at = (s / 4) * kHalfBytes + (s % 4) * 32;
-          mma_bf16(tmem + kColS + t * kColTile, make_sw128_kmajor_desc(q_at(t) + at),
-                   make_sw128_kmajor_desc(slot_at(2 * j) + at), qk_idesc, s > 0);
-        }
-        mma_commit(bar(kBarS + t));
-        if (t == 1 || tiles[1] <= j) mma_commit(empty(2 * j));
+        const uint64_t a = q_desc + t * kTile16, b = k_desc + slot * kTile16;
+#pragma unroll
+        for (int s = 0; s < 4 * HALVES; ++s)
+          if (s < qk_steps) {
+            const uint32_t at = (s / 4) * (kHalfBytes >> 4) + (s % 4) * 2;
+            mma_bf16(tmem + kColS + t * kColTile, a + at, b + at, qk_idesc, s > 0);
+          }
+        mma_commit(bar(kBarS + t));  // the product of P and V before it is then complete too
+        if (last_use) mma_commit(bar(kBarEmpty + slot));
       }
       __syncwarp();
     };
-    bool ok = all_tiles == 0 || wait_bounded_warp(bar(kBarQ), 0, ab, kAttnTimeout);
-    if (ok && all_tiles > 0) ok = wait_bounded_warp(full(0), 0, ab, kAttnTimeout);
+    bool ok = all_tiles == 0 || (tc_wait(bar(kBarQ), 0, ab, kAttnTimeout) && tc_wait(full(0), 0, ab, kAttnTimeout));
     tc_fence_after();
     for (int t = 0; t < 2; ++t)
-      if (ok && tiles[t] > 0) qk(t, 0);
+      if (ok && tiles[t] > 0) qk(t, 0, t == 1 || tiles[1] == 0);
     for (int j = 0; ok && j < all_tiles; ++j) {
-      for (int t = 0; ok && t < 2; ++t) {
+      const uint32_t v_slot = (2 * j + 1) % kPromptSlots, k_slot = (2 * j + 2) % kPromptSlots;
+      bool v_there = false, k_there = false;
+      for (int t = 0; t < 2; ++t) {
         if (j >= tiles[t]) continue;
-        ok = wait_bounded_warp(bar(kBarP + t), j & 1, ab, kAttnTimeout) &&
-             wait_bounded_warp(full(2 * j + 1), lap(2 * j + 1), ab, kAttnTimeout);
+        ok = tc_wait(bar(kBarP + t), j & 1, ab, kAttnTimeout) &&
+             (v_there || tc_wait(full(2 * j + 1), lap(2 * j + 1), ab, kAttnTimeout));
         if (!ok) break;
+        v_there = true;
         tc_fence_after();
+        const bool more = j + 1 < tiles[t], last_use = t == 1 || tiles[1] <= j;
         if (elect_one()) {
+          const uint64_t b = v_desc + v_slot * kTile16;
 #pragma unroll
           for (int s = 0; s < kKeys / 16; ++s)
-            mma_f16_tmem_a(tmem + kColO + t * kColTile, tmem + kColS + t * kColTile + 8 * s,
-                           make_v_desc(slot_at(2 * j + 1) + s * 2048), pv_idesc, j > 0 || s > 0);
-          mma_commit(bar(kBarO + t));
-          if (t == 1 || tiles[1] <= j) mma_commit(empty(2 * j + 1));
+            mma_f16_tmem_a(tmem + kColO + t * kColTile, tmem + kColS + t * kColTile + 8 * s, b + s * (2048 >> 4),
+                           pv_idesc, j > 0 || s > 0);
+          if (!more) mma_commit(bar(kBarO + t));
+          if (last_use) mma_commit(bar(kBarEmpty + v_slot));
         }
         __syncwarp();
-        if (j + 1 < tiles[t]) {
-          ok = wait_bounded_warp(full(2 * j + 2), lap(2 * j + 2), ab, kAttnTimeout);
-          if (!ok) break;
-          tc_fence_after();
-          qk(t, j + 1);
-        }
+        if (!more) continue;
+        ok = k_there || tc_wait(full(2 * j + 2), lap(2 * j + 2), ab, kAttnTimeout);
+        if (!ok) break;
+        k_there = true;
+        tc_fence_after();
+        qk(t, k_slot, t == 1 || tiles[1] <= j + 1);
       }
     }
     // every product is complete before TMEM is released
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       __syncwarp();
     }
     for (int i = 0; i < 2 * all_tiles; ++i) {
-      if (i >= kPromptSlots && !wait_bounded_warp(empty(i), lap(i) ^ 1u, ab, kAttnTimeout)) break;
+      if (i >= kPromptSlots && !tc_wait(empty(i), lap(i) ^ 1u, ab, kAttnTimeout)) break;
       if (elect_one()) {
         const uint32_t to = i % 2 && i / 2 >= checked_from ? bar(kBarRaw + i / 2 - checked_from) : full(i);
         mbar_arrive_expect_tx(to, kTileBytes<HALVES>);
@@ -404,7 +413,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // ------------------------------------------------------------------------------ values that are not finite
     const int thread = threadIdx.x - kCheckWarp * 32;
     for (int j = checked_from; j < all_tiles; ++j) {
-      if (!wait_bounded_warp(bar(kBarRaw + j - checked_from), 0, ab, kAttnTimeout)) break;
+      if (!tc_wait(bar(kBarRaw + j - checked_from), 0, ab, kAttnTimeout)) break;
       uint8_t* tile = raw + (slot_at(2 * j + 1) - smem_u32(raw));
       // 16 bytes at a time: whether any is not finite, before which
       uint32_t any = 0;

@@ -70,32 +70,6 @@ constexpr int kTcBars = 2 * kTcMaxStages + 2 * kTcDepth + 5;
 constexpr int kTcBarBytes = 512;                    // barriers, the TMEM address, the abort flag
 static_assert(kTcBars * 8 + 8 <= kTcBarBytes);
 
-// wait_bounded_warp with less in the way of the next try: the timer, whose read takes several hundred
-// cycles, and the abort flag are looked at after every 64 misses.
-__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const AbortState& ab,
-                                        int code) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!__all_sync(0xFFFFFFFFu, ok)) {
-    uint64_t t0 = 0;
-    for (uint32_t misses = 1; !ok; ++misses) {
-      ok = mbar_try_wait(bar, parity);
-      if (ok || (misses & 63u) != 0) continue;
-      if (*ab.flag) break;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > ab.timeout_ns) {
-        *ab.flag = 1;
-        atomicOr(ab.status, code);
-        __threadfence();
-        break;
-      }
-    }
-    ok = __all_sync(0xFFFFFFFFu, ok);
-  }
-  return ok;
-}
-
 // A box of x's codes of one CTA (half of the tile's tokens), or of half as many as f16. Either way a
 // stage (e4m3) or a slot (int8) of x is two.
 __host__ __device__ inline uint32_t tc_x_bytes(int block_t) {
