@@ -16,7 +16,8 @@
 // memory. Rows that do see them add them when they are done, read from memory again (their weight is positive, so the
 // sum is the value).
 //
-// Roles: warps 0 to 7 softmax and epilogue (a row a thread), 8 the products, 9 the copies, 10 and 11 the check of values.
+// Roles: warps 0 to 7 softmax and epilogue (a row a thread), 8 the products, 9 the copies, 10 the gate (below), 11 the check of
+// values.
 // Every wait is bounded; one that runs out records a status bit and the block winds down.
 #include <algorithm>
 
@@ -30,7 +31,7 @@ namespace c3d {
 constexpr int kRows = 128;                   // of a tile of q
 constexpr int kKeys = 128;                   // of a tile of k and v
 constexpr int kUnitRows = 2 * kRows;
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kCheckWarp = 10;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kGateWarp = 10;  // and the check
 constexpr int kPromptThreads = 12 * 32;
 constexpr uint32_t kHalfBytes = 128 * 128;   // 64 channels of a tile: 128 rows of 128 bytes
 constexpr int kPromptSlots = 5;              // tiles of k and v under way
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     poison_word = 0;
     found[0] = -1;
     for (int i = 0; i < kBarCount; ++i)
-      mbar_init(bar(i), i == kBarP || i == kBarP + 1 ? 4 : 1);
+      mbar_init(bar(i), i == kBarP || i == kBarP + 1 ? 5 : 1);
     fence_mbar_init();
   }
 
@@ -329,9 +330,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t pv_idesc = (kBf16 ? make_idesc_bf16_f32(kRows, 64 * HALVES) : make_idesc_f16_f32(kRows, 64 * HALVES)) |
                               (1u << 16);  // B lies with its N contiguous
     const int qk_steps = (p.head_dim + 15) / 16;
-    // Descriptors of the first tiles; others lie a multiple of 16 bytes further on. This warp's instructions bound a block
-    // whose softmax keeps up (a wait takes it some 160 cycles, a commit 60, a product of 128 x 128 x 16 is 64 for the
-    // tensor cores), so it waits for a tile of k or v once, and commits what somebody waits for.
+    // The tensor cores take few instructions ahead, so whatever this warp does between two products leaves them idle (a wait
+    // takes it some 150 cycles, eight products 512): it waits once a round, for P, whose barrier the gate warp holds until
+    // V and the next K are there too, and commits what somebody waits for.
+    // Descriptors of the first tiles; others lie a multiple of 16 bytes further on.
     constexpr uint32_t kTile16 = kTileBytes<HALVES> >> 4;
     const uint64_t q_desc = make_sw128_kmajor_desc(q_at(0)), k_desc = make_sw128_kmajor_desc(slot_at(0));
     const uint64_t v_desc = make_v_desc(slot_at(0));
@@ -355,13 +357,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (ok && tiles[t] > 0) qk(t, 0, t == 1 || tiles[1] == 0);
     for (int j = 0; ok && j < all_tiles; ++j) {
       const uint32_t v_slot = (2 * j + 1) % kPromptSlots, k_slot = (2 * j + 2) % kPromptSlots;
-      bool v_there = false, k_there = false;
       for (int t = 0; t < 2; ++t) {
         if (j >= tiles[t]) continue;
-        ok = tc_wait(bar(kBarP + t), j & 1, ab, kAttnTimeout) &&
-             (v_there || tc_wait(full(2 * j + 1), lap(2 * j + 1), ab, kAttnTimeout));
+        ok = tc_wait(bar(kBarP + t), j & 1, ab, kAttnTimeout);
         if (!ok) break;
-        v_there = true;
         tc_fence_after();
         const bool more = j + 1 < tiles[t], last_use = t == 1 || tiles[1] <= j;
         if (elect_one()) {
@@ -374,12 +373,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (last_use) mma_commit(bar(kBarEmpty + v_slot));
         }
         __syncwarp();
-        if (!more) continue;
-        ok = k_there || tc_wait(full(2 * j + 2), lap(2 * j + 2), ab, kAttnTimeout);
-        if (!ok) break;
-        k_there = true;
-        tc_fence_after();
-        qk(t, k_slot, t == 1 || tiles[1] <= j + 1);
+        if (more) qk(t, k_slot, t == 1 || tiles[1] <= j + 1);
       }
     }
     // every product is complete before TMEM is released
@@ -409,16 +403,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       __syncwarp();
     }
+  } else if (warp == kGateWarp) {
+    // ------------------------------------------------------------------------------ the gate
+    // Arrives for round j of P once the copies are there that its products read, and the round before is over.
+    bool ok = true;
+    for (int j = 0; ok && j < all_tiles; ++j) {
+      ok = tc_wait(full(2 * j + 1), lap(2 * j + 1), ab, kAttnTimeout) &&
+           (j + 1 >= all_tiles || tc_wait(full(2 * j + 2), lap(2 * j + 2), ab, kAttnTimeout));
+      for (int t = 0; ok && t < 2; ++t) {
+        if (j >= tiles[t]) continue;
+        ok = j == 0 || tc_wait(bar(kBarP + t), (j - 1) & 1, ab, kAttnTimeout);
+        if (ok && lane == 0) mbar_arrive(bar(kBarP + t));
+      }
+    }
   } else {
     // ------------------------------------------------------------------------------ values that are not finite
-    const int thread = threadIdx.x - kCheckWarp * 32;
     for (int j = checked_from; j < all_tiles; ++j) {
       if (!tc_wait(bar(kBarRaw + j - checked_from), 0, ab, kAttnTimeout)) break;
       uint8_t* tile = raw + (slot_at(2 * j + 1) - smem_u32(raw));
       // 16 bytes at a time: whether any is not finite, before which
       uint32_t any = 0;
 #pragma unroll 8
-      for (uint32_t i = thread; i < kTileBytes<HALVES> / 16; i += 64) {
+      for (uint32_t i = lane; i < kTileBytes<HALVES> / 16; i += 32) {
         const uint4 w = *reinterpret_cast<const uint4*>(tile + 16 * i);
         any |= (w.x & kExponent2<T>) + kCarry2<T>;
         any |= (w.y & kExponent2<T>) + kCarry2<T>;
@@ -426,7 +432,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         any |= (w.w & kExponent2<T>) + kCarry2<T>;
       }
       if (__any_sync(0xFFFFFFFFu, any & 0x80008000u)) {
-        for (uint32_t i = 4 * thread; i < kTileBytes<HALVES> / 4; i += i % 4 == 3 ? 4 * 64 - 3 : 1) {  // the same ones
+        for (uint32_t i = lane; i < kTileBytes<HALVES> / 4; i += 32) {
           uint32_t* word = reinterpret_cast<uint32_t*>(tile) + i;
           const uint32_t bad = ((*word & kExponent2<T>) + kCarry2<T>) & 0x80008000u;
           if (!bad) continue;
@@ -437,8 +443,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __threadfence_block();
         fence_proxy_async_smem();
       }
-      named_barrier_sync(1, 64);
-      if (thread == 0) mbar_arrive(full(2 * j + 1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(2 * j + 1));
     }
   }
   __syncwarp();
