@@ -1,6 +1,7 @@
 // q8_attn_prompt.cu -- attention over whole prompts on the tensor cores, packed sequences, grouped heads.
 //
-// A block takes 256 rows of q of one head, two tiles A and B of 128, and walks over the keys 128 at a time:
+// A block takes one unit after another: 256 rows of q of one head, two tiles A and B of 128. It walks over the keys 128 at
+// a time:
 //   S = Q K^T (tcgen05, both operands in shared memory), P = 2^(S scale - m) in registers, O += P V (P from TMEM, V from
 //   shared memory), the running maximum m and sum l of a row held by the one thread that owns the row.
 // TMEM is full: two S of 128 columns, two O of up to 128; P, half as wide as S, takes S's place. While one tile's
@@ -16,8 +17,9 @@
 // memory. Rows that do see them add them when they are done, read from memory again (their weight is positive, so the
 // sum is the value).
 //
-// Roles: warps 0 to 7 softmax and epilogue (a row a thread), 8 the products, 9 the copies, 10 the gate (below), 11 the check of
-// values.
+// Roles: warps 0 to 7 softmax and epilogue (a row a thread), 8 the products, 9 the units and copies, 10 the gate (below), 11
+// the check of values. They pass from unit to unit on their own: the next unit's copies and first scores run beside this
+// one's last softmax and epilogue (a block for each unit: 4.3 us of 8 were its start and end for 500 keys of 64 channels).
 // Every wait is bounded; one that runs out records a status bit and the block winds down.
 #include <algorithm>
 
@@ -45,11 +47,23 @@ constexpr uint32_t kTileBytes = HALVES * kHalfBytes;
 template <int HALVES>
 constexpr size_t kPromptSmem = 1024 + (2 + kPromptSlots) * (size_t)kTileBytes<HALVES> + 256;
 
-// Barriers. The copies of tiles of v that are checked have one each, as the warps that check do not follow the slots' phases;
-// they then arrive for the slot in the copy's place. (The rows of a block end within 255 keys of each other: 3 tiles.)
+// Barriers. The copies of tiles of v that are checked have their own, as the warp that checks does not follow the slots'
+// phases; it then arrives for the slot in the copy's place. (The rows of a unit end within 255 keys of each other: 3 tiles.)
+// Units alternate between two places, and with them those barriers: a role is at most one unit ahead of another.
 constexpr int kMostChecked = 3;
-enum { kBarQ, kBarDrain, kBarRaw, kBarS = kBarRaw + kMostChecked, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarFull = kBarO + 2,
+enum { kBarUnit, kBarUnitFree = kBarUnit + 2, kBarQ = kBarUnitFree + 2, kBarQFree, kBarDrain, kBarRaw,
+       kBarS = kBarRaw + 2 * kMostChecked, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarFull = kBarO + 2,
        kBarEmpty = kBarFull + kPromptSlots, kBarCount = kBarEmpty + kPromptSlots };
+
+// 256 rows of one head of a sequence.
+struct PromptUnit {
+  int q0, queries;     // the sequence's rows of q
+  int k0, keys;        // and of k
+  int row0, head;      // the unit's first row in the sequence; head < 0: no more units
+  int tiles[2];        // tiles of keys that each tile of rows sees
+  int checked_from;    // tiles from here on are not seen whole by every row
+  int poison;          // a value that is not finite was zeroed in one of those
+};
 
 // A warpgroup's registers a thread, raised or lowered. The block is launched with 168 for each of its 384 threads; 256 x 208
 // and 128 x 80 are less than that in all, so the raise never waits for more than the others' drop.
@@ -115,10 +129,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                        const __grid_constant__ CUtensorMap vmap, const PromptParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[kBarCount];
+  __shared__ PromptUnit units[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_word, poison_word;
-  __shared__ int scan[kPromptThreads / 32];
-  __shared__ int found[2];
+  __shared__ int abort_word;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -127,68 +140,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   if (threadIdx.x == 0) {
     abort_word = 0;
-    poison_word = 0;
-    found[0] = -1;
     for (int i = 0; i < kBarCount; ++i)
-      mbar_init(bar(i), i == kBarP || i == kBarP + 1 ? 5 : 1);
+      mbar_init(bar(i), i == kBarP || i == kBarP + 1                 ? 5                  // four of softmax, the gate
+                        : i == kBarUnitFree || i == kBarUnitFree + 1 ? kSoftmaxWarps + 3  // all roles but the copies
+                                                                     : 1);
     fence_mbar_init();
   }
-
-  // ---- the rows: unit `want` of all sequences' units, counted from the last one, whose keys are the most
-  const int head = blockIdx.x % p.q_heads, kv_head = head / (p.q_heads / p.kv_heads);
-  auto begin_of = [&](const int* starts, int b, int rows) { return min(max(starts[b], 0), rows); };
-  auto end_of = [&](const int* starts, int b, int rows, int begin) { return min(max(starts[b + 1], begin), rows); };
-  auto units_of = [&](int b) {
-    if (b >= p.seqs) return 0;
-    const int begin = begin_of(p.starts, b, p.q_rows);
-    return (end_of(p.starts, b, p.q_rows, begin) - begin + kUnitRows - 1) / kUnitRows;
-  };
-  const int want = blockIdx.x / p.q_heads;
-  {
-    int after = 0;  // units of the sequences behind
-    for (int b1 = p.seqs; b1 > 0; b1 -= kPromptThreads) {
-      const int b = b1 - 1 - (int)threadIdx.x, mine = b >= 0 ? units_of(b) : 0;
-      int sum = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (lane == 31) scan[warp] = sum;
-      __syncthreads();
-      int all = after;
-      sum += after;
-      for (int w = 0; w < kPromptThreads / 32; ++w) {
-        if (w < warp) sum += scan[w];
-        all += scan[w];
-      }
-      if (sum > want && sum - mine <= want) {
-        found[0] = b;
-        found[1] = mine - 1 - (want - (sum - mine));
-      }
-      __syncthreads();
-      after = all;
-      if (all > want) break;
-    }
-  }
-  __syncthreads();
-  const int seq = found[0];
-  if (seq < 0) return;  // more blocks than units
-  const int* key_starts = p.key_starts ? p.key_starts : p.starts;
-  const int q0 = begin_of(p.starts, seq, p.q_rows), queries = end_of(p.starts, seq, p.q_rows, q0) - q0;
-  const int k0 = begin_of(key_starts, seq, p.k_rows), keys = end_of(key_starts, seq, p.k_rows, k0) - k0;
-  const int row0 = found[1] * kUnitRows;
-  // Keys that row r of the sequence sees.
-  auto limit_of = [&](int r) { return p.causal ? min(keys, max(0, r + 1 + keys - queries)) : keys; };
-  int tiles[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = row0 + t * kRows, last = min(first + kRows, queries) - 1;
-    tiles[t] = first < queries ? (limit_of(last) + kKeys - 1) / kKeys : 0;
-  }
-  const int all_tiles = max(tiles[0], tiles[1]);
-  const int checked_from = limit_of(row0) / kKeys;  // tiles from here on are not seen whole by every row
-
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -200,100 +157,127 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   volatile int* abort_flag = &abort_word;
   const AbortState ab{abort_flag, p.status, kPromptTimeoutNs};
   auto q_at = [&](int t) { return base + t * kTileBytes<HALVES>; };
-  auto slot_at = [&](int i) { return base + (2 + i % kPromptSlots) * kTileBytes<HALVES>; };
-  auto full = [&](int i) { return bar(kBarFull + i % kPromptSlots); };
-  auto empty = [&](int i) { return bar(kBarEmpty + i % kPromptSlots); };
-  auto lap = [&](int i) { return (uint32_t)(i / kPromptSlots) & 1u; };  // K of tile j is copy 2j, V copy 2j + 1
+  auto slot_at = [&](uint32_t i) { return base + (2 + i % kPromptSlots) * kTileBytes<HALVES>; };
+  auto full = [&](uint32_t i) { return bar(kBarFull + i % kPromptSlots); };
+  auto empty = [&](uint32_t i) { return bar(kBarEmpty + i % kPromptSlots); };
+  auto lap = [&](uint32_t i) { return (i / kPromptSlots) & 1u; };
+  // Keys that row r of a unit's sequence sees.
+  auto limit_of = [&](const PromptUnit& u, int r) { return p.causal ? min(u.keys, max(0, r + 1 + u.keys - u.queries)) : u.keys; };
+  // The block's n-th unit; false when there is none, or on abort.
+  auto next_unit = [&](int n, PromptUnit& u) {
+    if (!tc_wait(bar(kBarUnit + n % 2), (n / 2) & 1, ab, kAttnTimeout)) return false;
+    u = units[n % 2];
+    return u.head >= 0;
+  };
+  auto free_unit = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarUnitFree + n % 2));
+  };
 
   if (warp < kSoftmaxWarps) {
     set_max_registers_up<kSoftmaxRegisters>();
     // ------------------------------------------------------------------------------ softmax
-    const int t = warp / 4, row = row0 + t * kRows + (warp % 4) * 32 + lane;
+    const int t = warp / 4, row_in = t * kRows + (warp % 4) * 32;
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's lanes of TMEM, << 16
     const uint32_t s_at = tmem + kColS + t * kColTile + lanes, o_at = tmem + kColO + t * kColTile + lanes;
-    const int limit = row < queries ? limit_of(row) : 0;
-    const int whole = limit_of(row0 + t * kRows + (warp % 4) * 32);  // of this warp's first row: the fewest
-    const bool some_row_out = row0 + t * kRows + (warp % 4) * 32 + 31 >= queries;
-    float m = kNone;
-    float2 l = make_float2(0.0f, 0.0f);
+    uint32_t scores = 0, outputs = 0;  // of this tile so far
     bool ok = true;
-    for (int j = 0; j < tiles[t]; ++j) {
-      ok = tc_wait(bar(kBarS + t), j & 1, ab, kAttnTimeout);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_at + 32 * i, s[i]);
-      tmem_ld_wait();
-      auto f = [&](int c) -> float { return __uint_as_float(s[c / 32][c % 32]); };
-      if (whole - j * kKeys < kKeys || some_row_out) {
-        const int seen = limit - j * kKeys;
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-          if (c >= seen) s[c / 32][c % 32] = 0xFF800000u;
+    for (int n = 0; ok; ++n) {
+      int count, limit, whole;  // tiles; keys that this row sees, and that all rows of the warp see
+      {
+        PromptUnit u;
+        if (!next_unit(n, u)) break;
+        const int first = u.row0 + row_in;
+        count = u.tiles[t];
+        limit = first + lane < u.queries ? limit_of(u, first + lane) : 0;
+        whole = first + 31 < u.queries ? limit_of(u, first) : 0;
       }
-      float top[4];
+      float m = kNone;
+      float2 l = make_float2(0.0f, 0.0f);
+      for (int j = 0; j < count; ++j, ++scores) {
+        ok = tc_wait(bar(kBarS + t), scores & 1, ab, kAttnTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+        auto load = [&] {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top[i] = fmaxf(f(32 * i), f(32 * i + 1));
+          for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(s_at + 32 * i, s[i]);
+          tmem_ld_wait();
+          if (whole - j * kKeys < kKeys) {
+            const int seen = limit - j * kKeys;
 #pragma unroll
-      for (int c = 2; c < 32; c += 2)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], f(32 * i + c), f(32 * i + c + 1));
-      const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-      const bool grows = most > m && (m == kNone || (most - m) * p.scale > kGrowth);
-      if (__any_sync(0xFFFFFFFFu, grows)) {
-        // of the rows that grow: the others' results do not depend on their neighbours
-        const float now = grows ? most : m, keep = !grows ? 1.0f : m == kNone ? 0.0f : exp2_fast((m - now) * p.scale);
-        if (j > 0) {  // the tile's product before these scores is complete
-#pragma unroll
-          for (int i = 0; i < 2 * HALVES; ++i) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(o_at + 32 * i, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * keep);
-            tmem_st_32x32b_x32(o_at + 32 * i, o);
+            for (int c = 0; c < kKeys; ++c)
+              if (c >= seen) s[c / 32][c % 32] = 0xFF800000u;
           }
-        }
-        l.x *= keep;
-        l.y *= keep;
-        m = now;
-      }
-      const float neg = m == kNone ? 0.0f : -m * p.scale;
-      const float2 scale2 = make_float2(p.scale, p.scale), neg2 = make_float2(neg, neg);
+        };
+        load();
+        auto f = [&](int c) -> float { return __uint_as_float(s[c / 32][c % 32]); };
+        float top[4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(f(32 * i), f(32 * i + 1));
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float2 x = make_float2(f(64 * half + 2 * c), f(64 * half + 2 * c + 1));
-          x = q8_fma2(x, scale2, neg2);
-          x.x = exp2_fast(x.x);
-          x.y = exp2_fast(x.y);
-          l = q8_add2(l, x);
-          w[c] = q8_pack2<T>(x);
+        for (int c = 2; c < 32; c += 2)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = max3(top[i], f(32 * i + c), f(32 * i + c + 1));
+        const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        const bool grows = most > m && (m == kNone || (most - m) * p.scale > kGrowth);
+        if (__any_sync(0xFFFFFFFFu, grows)) {
+          // of the rows that grow: the others' results do not depend on their neighbours
+          const float now = grows ? most : m, keep = !grows ? 1.0f : m == kNone ? 0.0f : exp2_fast((m - now) * p.scale);
+          if (j > 0) {  // the tile's product before these scores is complete
+#pragma unroll
+            for (int i = 0; i < 2 * HALVES; ++i) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(o_at + 32 * i, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * keep);
+              tmem_st_32x32b_x32(o_at + 32 * i, o);
+            }
+            load();  // there are no registers to hold them meanwhile
+          }
+          l.x *= keep;
+          l.y *= keep;
+          m = now;
         }
-        tmem_st_32x32b_x32(s_at + 32 * half, w);
+        const float neg = m == kNone ? 0.0f : -m * p.scale;
+        const float2 scale2 = make_float2(p.scale, p.scale), neg2 = make_float2(neg, neg);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float2 x = make_float2(f(64 * half + 2 * c), f(64 * half + 2 * c + 1));
+            x = q8_fma2(x, scale2, neg2);
+            x.x = exp2_fast(x.x);
+            x.y = exp2_fast(x.y);
+            l = q8_add2(l, x);
+            w[c] = q8_pack2<T>(x);
+          }
+          tmem_st_32x32b_x32(s_at + 32 * half, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + t));
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarP + t));
-    }
-    // ---- the row's output
-    if (ok && tiles[t] > 0) {
-      ok = tc_wait(bar(kBarO + t), 0, ab, kAttnTimeout);
-      tc_fence_after();
-    }
-    if (ok) {
-      const bool poison = *reinterpret_cast<volatile int*>(&poison_word) != 0;
+      // ---- the row's output
+      if (ok && count > 0) {
+        ok = tc_wait(bar(kBarO + t), outputs++ & 1, ab, kAttnTimeout);
+        tc_fence_after();
+      }
+      if (!ok) break;
+      const PromptUnit u = units[n % 2];  // read again: the loop above has no registers for it
+      const int row = u.row0 + row_in + lane;
+      const bool poison = u.poison != 0;
       const float sum = l.x + l.y, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      T* out = static_cast<T*>(p.o.p) + (long long)(q0 + row) * p.o.pitch + head * p.o.head_pitch;
-      const T* v = static_cast<const T*>(p.v.p) + (long long)k0 * p.v.pitch + kv_head * p.v.head_pitch;
+      T* out = static_cast<T*>(p.o.p) + (long long)(u.q0 + row) * p.o.pitch + u.head * p.o.head_pitch;
+      const T* v = static_cast<const T*>(p.v.p) + (long long)u.k0 * p.v.pitch +
+                   (u.head / (p.q_heads / p.kv_heads)) * p.v.head_pitch;
 #pragma unroll
       for (int i = 0; i < 2 * HALVES; ++i) {
         uint32_t o[32];
-        if (tiles[t] > 0) {  // the same for the whole warp
+        if (count > 0) {  // the same for the whole warp
           tmem_ld_32x32b_x32(o_at + 32 * i, o);
           tmem_ld_wait();
         }
@@ -301,14 +285,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] = sum == 0.0f ? 0.0f : __uint_as_float(o[c]) * inv;
         if (poison)
-          for (int k = checked_from * kKeys; k < limit; ++k)
+          for (int k = u.checked_from * kKeys; k < limit; ++k)
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (32 * i + c < p.head_dim) {
                 const float add = q8_to_float(v[k * p.v.pitch + 32 * i + c]);
                 if (!(fabsf(add) <= 3.4028234e38f)) x[c] += add;
               }
-        if (row < queries) {
+        if (row < u.queries) {
 #pragma unroll
           for (int c = 0; c < 32; c += 8)
             if (32 * i + c < p.head_dim) {
@@ -321,6 +305,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
         }
       }
+      tc_fence_before();  // O is read before the next unit's first P arrives
+      free_unit(n);
     }
   } else if (set_max_registers_down<kOtherRegisters>(); warp == kMmaWarp) {
     // ------------------------------------------------------------------------------ products
@@ -337,7 +323,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     constexpr uint32_t kTile16 = kTileBytes<HALVES> >> 4;
     const uint64_t q_desc = make_sw128_kmajor_desc(q_at(0)), k_desc = make_sw128_kmajor_desc(slot_at(0));
     const uint64_t v_desc = make_v_desc(slot_at(0));
-    auto qk = [&](int t, uint32_t slot, bool last_use) {
+    auto qk = [&](int t, uint32_t slot, bool last_use, bool last_of_unit) {
       if (elect_one()) {
         const uint64_t a = q_desc + t * kTile16, b = k_desc + slot * kTile16;
 #pragma unroll
@@ -348,103 +334,207 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         mma_commit(bar(kBarS + t));  // the product of P and V before it is then complete too
         if (last_use) mma_commit(bar(kBarEmpty + slot));
+        if (last_of_unit) mma_commit(bar(kBarQFree));
       }
       __syncwarp();
     };
-    bool ok = all_tiles == 0 || (tc_wait(bar(kBarQ), 0, ab, kAttnTimeout) && tc_wait(full(0), 0, ab, kAttnTimeout));
-    tc_fence_after();
-    for (int t = 0; t < 2; ++t)
-      if (ok && tiles[t] > 0) qk(t, 0, t == 1 || tiles[1] == 0);
-    for (int j = 0; ok && j < all_tiles; ++j) {
-      const uint32_t v_slot = (2 * j + 1) % kPromptSlots, k_slot = (2 * j + 2) % kPromptSlots;
-      for (int t = 0; t < 2; ++t) {
-        if (j >= tiles[t]) continue;
-        ok = tc_wait(bar(kBarP + t), j & 1, ab, kAttnTimeout);
-        if (!ok) break;
+    uint32_t copies = 0, with_tiles = 0;      // before this unit: copies of k and v, units that had any
+    uint32_t rounds[2] = {0, 0};              // of P so far
+    PromptUnit u;
+    bool ok = true;
+    for (int n = 0; ok && next_unit(n, u); ++n) {
+      const int all = max(u.tiles[0], u.tiles[1]);
+      if (all > 0) {
+        ok = tc_wait(bar(kBarQ), with_tiles++ & 1, ab, kAttnTimeout) && tc_wait(full(copies), lap(copies), ab, kAttnTimeout);
         tc_fence_after();
-        const bool more = j + 1 < tiles[t], last_use = t == 1 || tiles[1] <= j;
-        if (elect_one()) {
-          const uint64_t b = v_desc + v_slot * kTile16;
-#pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            mma_f16_tmem_a(tmem + kColO + t * kColTile, tmem + kColS + t * kColTile + 8 * s, b + s * (2048 >> 4),
-                           pv_idesc, j > 0 || s > 0);
-          if (!more) mma_commit(bar(kBarO + t));
-          if (last_use) mma_commit(bar(kBarEmpty + v_slot));
-        }
-        __syncwarp();
-        if (more) qk(t, k_slot, t == 1 || tiles[1] <= j + 1);
       }
+      // Tile t's last use of the tile j of keys.
+      auto last_use = [&](int t, int j) { return t == 1 || u.tiles[1] <= j; };
+      for (int t = 0; t < 2; ++t)
+        if (ok && u.tiles[t] > 0) qk(t, copies % kPromptSlots, last_use(t, 0), all == 1 && last_use(t, 0));
+      for (int j = 0; ok && j < all; ++j) {
+        const uint32_t v_slot = (copies + 2 * j + 1) % kPromptSlots, k_slot = (copies + 2 * j + 2) % kPromptSlots;
+        for (int t = 0; t < 2; ++t) {
+          if (j >= u.tiles[t]) continue;
+          ok = tc_wait(bar(kBarP + t), rounds[t]++ & 1, ab, kAttnTimeout);
+          if (!ok) break;
+          tc_fence_after();
+          const bool more = j + 1 < u.tiles[t];
+          if (elect_one()) {
+            const uint64_t b = v_desc + v_slot * kTile16;
+#pragma unroll
+            for (int s = 0; s < kKeys / 16; ++s)
+              mma_f16_tmem_a(tmem + kColO + t * kColTile, tmem + kColS + t * kColTile + 8 * s, b + s * (2048 >> 4),
+                             pv_idesc, j > 0 || s > 0);
+            if (!more) mma_commit(bar(kBarO + t));
+            if (last_use(t, j)) mma_commit(bar(kBarEmpty + v_slot));
+          }
+          __syncwarp();
+          if (more) qk(t, k_slot, last_use(t, j + 1), j + 2 == all && last_use(t, j + 1));
+        }
+      }
+      copies += 2 * all;
+      if (ok) free_unit(n);
     }
     // every product is complete before TMEM is released
     if (elect_one()) mma_commit(bar(kBarDrain));
     __syncwarp();
     wait_drain(bar(kBarDrain), 0, kPromptTimeoutNs, p.status, kAttnTimeout);
   } else if (warp == kTmaWarp) {
-    // ------------------------------------------------------------------------------ copies
-    if (all_tiles > 0) {
+    // ------------------------------------------------------------------------------ units and copies
+    // Units of all sequences are counted from the last one, which has the most keys, heads first; a block takes every
+    // gridDim.x-th of them, from the left and from the right in turn, which evens out what they cost.
+    auto begin_of = [&](const int* starts, int b, int rows) { return min(max(starts[b], 0), rows); };
+    auto end_of = [&](const int* starts, int b, int rows, int begin) { return min(max(starts[b + 1], begin), rows); };
+    const int* key_starts = p.key_starts ? p.key_starts : p.starts;
+    long long behind = 0;  // units of the sequences from `from` on
+    int from = p.seqs;
+    auto find = [&](long long want, PromptUnit& u) {
+      while (from > 0) {
+        const int b = from - 1 - lane;
+        int q0 = 0, queries = 0;
+        if (b >= 0) {
+          q0 = begin_of(p.starts, b, p.q_rows);
+          queries = end_of(p.starts, b, p.q_rows, q0) - q0;
+        }
+        const int mine = (queries + kUnitRows - 1) / kUnitRows;
+        long long sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, behind + sum > want);
+        if (hit) {
+          const int at = __ffs(hit) - 1;
+          const long long upto = __shfl_sync(0xFFFFFFFFu, sum, at);
+          const int b_at = from - 1 - at;
+          u.q0 = __shfl_sync(0xFFFFFFFFu, q0, at);
+          u.queries = __shfl_sync(0xFFFFFFFFu, queries, at);
+          u.row0 = (int)(behind + upto - 1 - want) * kUnitRows;
+          u.k0 = begin_of(key_starts, b_at, p.k_rows);
+          u.keys = end_of(key_starts, b_at, p.k_rows, u.k0) - u.k0;
+          return true;
+        }
+        behind += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        from -= 32;
+      }
+      return false;
+    };
+    uint32_t copies = 0, with_tiles = 0;
+    for (int n = 0;; ++n) {
+      const long long w = (long long)n * gridDim.x + (n % 2 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      PromptUnit u;
+      u.poison = 0;
+      u.head = find(w / p.q_heads, u) ? (int)(w % p.q_heads) : -1;
+      if (u.head >= 0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int first = u.row0 + t * kRows, last = min(first + kRows, u.queries) - 1;
+          u.tiles[t] = first < u.queries ? (limit_of(u, last) + kKeys - 1) / kKeys : 0;
+        }
+        u.checked_from = limit_of(u, u.row0) / kKeys;
+      }
+      if (n >= 2 && !tc_wait(bar(kBarUnitFree + n % 2), (n / 2 - 1) & 1, ab, kAttnTimeout)) break;
+      if (lane == 0) {
+        units[n % 2] = u;
+        mbar_arrive(bar(kBarUnit + n % 2));
+      }
+      __syncwarp();
+      if (u.head < 0) break;
+      const int all = max(u.tiles[0], u.tiles[1]), kv_head = u.head / (p.q_heads / p.kv_heads);
+      if (all == 0) continue;
+      if (with_tiles > 0 && !tc_wait(bar(kBarQFree), (with_tiles - 1) & 1, ab, kAttnTimeout)) break;
+      ++with_tiles;
       if (elect_one()) {
-        const int q_tiles = tiles[1] > 0 ? 2 : 1;
+        const int q_tiles = u.tiles[1] > 0 ? 2 : 1;
         mbar_arrive_expect_tx(bar(kBarQ), q_tiles * kTileBytes<HALVES>);
         for (int t = 0; t < q_tiles; ++t)
           for (int h = 0; h < HALVES; ++h)
-            tma_load_3d(q_at(t) + h * kHalfBytes, &qmap, bar(kBarQ), 64 * h, head, q0 + row0 + t * kRows);
+            tma_load_3d(q_at(t) + h * kHalfBytes, &qmap, bar(kBarQ), 64 * h, u.head, u.q0 + u.row0 + t * kRows);
       }
       __syncwarp();
-    }
-    for (int i = 0; i < 2 * all_tiles; ++i) {
-      if (i >= kPromptSlots && !tc_wait(empty(i), lap(i) ^ 1u, ab, kAttnTimeout)) break;
-      if (elect_one()) {
-        const uint32_t to = i % 2 && i / 2 >= checked_from ? bar(kBarRaw + i / 2 - checked_from) : full(i);
-        mbar_arrive_expect_tx(to, kTileBytes<HALVES>);
-        for (int h = 0; h < HALVES; ++h)
-          tma_load_3d(slot_at(i) + h * kHalfBytes, i % 2 ? &vmap : &kmap, to, 64 * h, kv_head,
-                      k0 + (i / 2) * kKeys);
+      bool ok = true;
+      for (int i = 0; ok && i < 2 * all; ++i) {  // k of tile i / 2, then v
+        const uint32_t c = copies + i;
+        if (c >= kPromptSlots) ok = tc_wait(empty(c), lap(c) ^ 1u, ab, kAttnTimeout);
+        if (ok && elect_one()) {
+          const uint32_t to =
+              i % 2 && i / 2 >= u.checked_from ? bar(kBarRaw + kMostChecked * (n % 2) + i / 2 - u.checked_from) : full(c);
+          mbar_arrive_expect_tx(to, kTileBytes<HALVES>);
+          for (int h = 0; h < HALVES; ++h)
+            tma_load_3d(slot_at(c) + h * kHalfBytes, i % 2 ? &vmap : &kmap, to, 64 * h, kv_head, u.k0 + (i / 2) * kKeys);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if (!ok) break;
+      copies += 2 * all;
     }
   } else if (warp == kGateWarp) {
     // ------------------------------------------------------------------------------ the gate
     // Arrives for round j of P once the copies are there that its products read, and the round before is over.
+    uint32_t copies = 0, rounds[2] = {0, 0};
+    PromptUnit u;
     bool ok = true;
-    for (int j = 0; ok && j < all_tiles; ++j) {
-      ok = tc_wait(full(2 * j + 1), lap(2 * j + 1), ab, kAttnTimeout) &&
-           (j + 1 >= all_tiles || tc_wait(full(2 * j + 2), lap(2 * j + 2), ab, kAttnTimeout));
-      for (int t = 0; ok && t < 2; ++t) {
-        if (j >= tiles[t]) continue;
-        ok = j == 0 || tc_wait(bar(kBarP + t), (j - 1) & 1, ab, kAttnTimeout);
-        if (ok && lane == 0) mbar_arrive(bar(kBarP + t));
+    for (int n = 0; ok && next_unit(n, u); ++n) {
+      const int all = max(u.tiles[0], u.tiles[1]);
+      if (all > 0) ok = tc_wait(full(copies), lap(copies), ab, kAttnTimeout);  // no phase of a slot is passed over
+      for (int j = 0; ok && j < all; ++j) {
+        const uint32_t v = copies + 2 * j + 1;
+        ok = tc_wait(full(v), lap(v), ab, kAttnTimeout) &&
+             (j + 1 >= all || tc_wait(full(v + 1), lap(v + 1), ab, kAttnTimeout));
+        for (int t = 0; ok && t < 2; ++t) {
+          if (j >= u.tiles[t]) continue;
+          ok = rounds[t] == 0 || tc_wait(bar(kBarP + t), (rounds[t] - 1) & 1, ab, kAttnTimeout);
+          ++rounds[t];
+          if (ok && lane == 0) mbar_arrive(bar(kBarP + t));
+        }
       }
+      copies += 2 * all;
+      if (ok) free_unit(n);
     }
   } else {
     // ------------------------------------------------------------------------------ values that are not finite
-    for (int j = checked_from; j < all_tiles; ++j) {
-      if (!tc_wait(bar(kBarRaw + j - checked_from), 0, ab, kAttnTimeout)) break;
-      uint8_t* tile = raw + (slot_at(2 * j + 1) - smem_u32(raw));
-      // 16 bytes at a time: whether any is not finite, before which
-      uint32_t any = 0;
+    uint32_t copies = 0, checked[2][kMostChecked] = {};
+    PromptUnit u;
+    bool ok = true;
+    for (int n = 0; ok && next_unit(n, u); ++n) {
+      const int all = max(u.tiles[0], u.tiles[1]);
+#pragma unroll
+      for (int c = 0; c < kMostChecked; ++c) {
+        const int j = u.checked_from + c;
+        if (!ok || j >= all) break;
+        ok = tc_wait(bar(kBarRaw + kMostChecked * (n % 2) + c), (n % 2 ? checked[1][c]++ : checked[0][c]++) & 1, ab, kAttnTimeout);
+        if (!ok) break;
+        const uint32_t copy = copies + 2 * j + 1;
+        uint8_t* tile = raw + (slot_at(copy) - smem_u32(raw));
+        // 16 bytes at a time: whether any is not finite, before which
+        uint32_t any = 0;
 #pragma unroll 8
-      for (uint32_t i = lane; i < kTileBytes<HALVES> / 16; i += 32) {
-        const uint4 w = *reinterpret_cast<const uint4*>(tile + 16 * i);
-        any |= (w.x & kExponent2<T>) + kCarry2<T>;
-        any |= (w.y & kExponent2<T>) + kCarry2<T>;
-        any |= (w.z & kExponent2<T>) + kCarry2<T>;
-        any |= (w.w & kExponent2<T>) + kCarry2<T>;
-      }
-      if (__any_sync(0xFFFFFFFFu, any & 0x80008000u)) {
-        for (uint32_t i = lane; i < kTileBytes<HALVES> / 4; i += 32) {
-          uint32_t* word = reinterpret_cast<uint32_t*>(tile) + i;
-          const uint32_t bad = ((*word & kExponent2<T>) + kCarry2<T>) & 0x80008000u;
-          if (!bad) continue;
-          const int key = j * kKeys + (int)(i * 4 % kHalfBytes) / 128;
-          *word &= (bad & 0x8000u ? 0u : 0xFFFFu) | (bad & 0x80000000u ? 0u : 0xFFFF0000u);
-          if (key < keys) *reinterpret_cast<volatile int*>(&poison_word) = 1;
+        for (uint32_t i = lane; i < kTileBytes<HALVES> / 16; i += 32) {
+          const uint4 w = *reinterpret_cast<const uint4*>(tile + 16 * i);
+          any |= (w.x & kExponent2<T>) + kCarry2<T>;
+          any |= (w.y & kExponent2<T>) + kCarry2<T>;
+          any |= (w.z & kExponent2<T>) + kCarry2<T>;
+          any |= (w.w & kExponent2<T>) + kCarry2<T>;
         }
-        __threadfence_block();
-        fence_proxy_async_smem();
+        if (__any_sync(0xFFFFFFFFu, any & 0x80008000u)) {
+          for (uint32_t i = lane; i < kTileBytes<HALVES> / 4; i += 32) {
+            uint32_t* word = reinterpret_cast<uint32_t*>(tile) + i;
+            const uint32_t bad = ((*word & kExponent2<T>) + kCarry2<T>) & 0x80008000u;
+            if (!bad) continue;
+            const int key = j * kKeys + (int)(i * 4 % kHalfBytes) / 128;
+            *word &= (bad & 0x8000u ? 0u : 0xFFFFu) | (bad & 0x80000000u ? 0u : 0xFFFF0000u);
+            if (key < u.keys) *reinterpret_cast<volatile int*>(&units[n % 2].poison) = 1;
+          }
+          __threadfence_block();
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(copy));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(2 * j + 1));
+      copies += 2 * all;
+      if (ok) free_unit(n);
     }
   }
   __syncwarp();
@@ -483,7 +573,8 @@ static cudaError_t prompt_form(const PromptParams* p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   }
   const long long units = p->q_rows / kUnitRows + std::min<long long>(p->seqs, p->q_rows);  // at most
-  kernel<<<(unsigned)(units * p->q_heads), kPromptThreads, kPromptSmem<HALVES>, stream>>>(qmap, kmap, vmap, *p);
+  const unsigned blocks = (unsigned)std::min<long long>(units * p->q_heads, p->sms);
+  kernel<<<blocks, kPromptThreads, kPromptSmem<HALVES>, stream>>>(qmap, kmap, vmap, *p);
   return cudaGetLastError();
 }
 
