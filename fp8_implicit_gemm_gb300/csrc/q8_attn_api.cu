@@ -110,9 +110,7 @@ struct attn_q8_plan_s : Plan {
   long long max_seqs = 0;
   int max_tokens = 0, q_heads = 0, kv_heads = 0, head_dim = 0, code_type = 0, sms = 0;
 };
-struct attn_prompt_plan_s : Plan {
-  int sms = 0;
-};
+struct attn_prompt_plan_s : Plan {};
 
 extern "C" conv3d_status heads_q8_run(const heads_q8_args* a) {
   if (!a) return CONV3D_EINVAL;
@@ -300,11 +298,6 @@ extern "C" conv3d_status attn_prompt_plan(attn_prompt_plan_t* plan, int device) 
   if (st != CONV3D_OK) return st;
   attn_prompt_plan_s* pl = new (std::nothrow) attn_prompt_plan_s();
   if (!pl) return CONV3D_ENOMEM;
-  if (cudaDeviceGetAttribute(&pl->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
-    cudaGetLastError();
-    delete pl;
-    return CONV3D_ECUDA;
-  }
   st = plan_memory(*pl, device, kStatusBytes);
   if (st != CONV3D_OK) {
     delete pl;
@@ -321,7 +314,8 @@ extern "C" conv3d_status attn_prompt_run(attn_prompt_plan_t plan, const attn_pro
       (a->value_type != Q8_BF16 && a->value_type != Q8_F16) || !std::isfinite(a->scale))
     return CONV3D_EINVAL;
   if (a->head_dim % 8 != 0 || a->head_dim > 128 || a->q_rows >= (1LL << 31) - 256 ||
-      a->k_rows >= (1LL << 31) - 256 || a->seqs > 65536 || a->q_heads >= 65536)
+      a->k_rows >= (1LL << 31) - 256 || a->seqs > 65536 || a->q_heads >= 65536 ||
+      (a->q_rows / 256 + a->seqs) * a->q_heads >= (1LL << 31))
     return CONV3D_EUNSUPPORTED;
   if (a->seqs > 0 && a->q_rows > 0) {
     if (!heads_ok(a->q, a->q_rows, a->q_heads, a->head_dim, a->q_pitch, a->q_head_pitch, 2) ||
@@ -350,7 +344,6 @@ extern "C" conv3d_status attn_prompt_run(attn_prompt_plan_t plan, const attn_pro
   p.head_dim = a->head_dim;
   p.causal = a->causal;
   p.negate = a->scale < 0.0f;
-  p.sms = plan->sms;
   // a scale of 0 as one that leaves every finite score 0 and -inf, a masked one, -inf
   p.scale = std::fmax(std::fabs(a->scale) * 1.44269504088896f, 1e-30f);
   p.status = reinterpret_cast<int*>(plan->workspace);

@@ -69,7 +69,6 @@ struct PromptParams {
   const int *starts, *key_starts;
   int q_rows, k_rows, seqs, q_heads, kv_heads, head_dim, causal;
   int negate;            // the scale is negative
-  int sms;               // of the device
   float scale;           // its magnitude times log2(e)
   int* status;
 };

@@ -51,7 +51,7 @@ constexpr size_t kPromptSmem = 1024 + (2 + kPromptSlots) * (size_t)kTileBytes<HA
 // phases; it then arrives for the slot in the copy's place. (The rows of a unit end within 255 keys of each other: 3 tiles.)
 // Units alternate between two places, and with them those barriers: a role is at most one unit ahead of another.
 constexpr int kMostChecked = 3;
-enum { kBarUnit, kBarUnitFree = kBarUnit + 2, kBarQ = kBarUnitFree + 2, kBarQFree, kBarDrain, kBarRaw,
+enum { kBarUnit, kBarUnitFree = kBarUnit + 2, kBarQ = kBarUnitFree + 2, kBarQFree, kBarBlock, kBarDrain, kBarRaw,
        kBarS = kBarRaw + 2 * kMostChecked, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarFull = kBarO + 2,
        kBarEmpty = kBarFull + kPromptSlots, kBarCount = kBarEmpty + kPromptSlots };
 
@@ -95,6 +95,27 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// Takes over a block of this grid that has not started: asks for one, with the answer (16 bytes) in shared memory and its
+// completion on the barrier, then whether there was one and which. Not to be asked again after there was none.
+__device__ __forceinline__ void ask_for_block(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool answered_block(uint32_t answer, uint32_t& block) {
+  uint32_t some;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(some), "=r"(block)
+      : "r"(answer)
+      : "memory");
+  return some != 0;
+}
 // D (+)= A * B with A in TMEM (row i in lane i, two consecutive elements of K in each column), one CTA.
 __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
@@ -130,6 +151,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[kBarCount];
   __shared__ PromptUnit units[2];
+  __shared__ __align__(16) uint4 answer;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
 
@@ -382,14 +404,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     wait_drain(bar(kBarDrain), 0, kPromptTimeoutNs, p.status, kAttnTimeout);
   } else if (warp == kTmaWarp) {
     // ------------------------------------------------------------------------------ units and copies
-    // Units of all sequences are counted from the last one, which has the most keys, heads first; a block takes every
-    // gridDim.x-th of them, from the left and from the right in turn, which evens out what they cost.
+    // Units of all sequences are counted from the last one, which has the most keys, heads first; there is a block for each
+    // (or more). A block that has issued its unit's copies takes over another that has not started.
     auto begin_of = [&](const int* starts, int b, int rows) { return min(max(starts[b], 0), rows); };
     auto end_of = [&](const int* starts, int b, int rows, int begin) { return min(max(starts[b + 1], begin), rows); };
     const int* key_starts = p.key_starts ? p.key_starts : p.starts;
-    long long behind = 0;  // units of the sequences from `from` on
+    long long behind = 0, wanted = 0;  // units of the sequences from `from` on; the last one asked for
     int from = p.seqs;
     auto find = [&](long long want, PromptUnit& u) {
+      if (want < wanted) behind = 0, from = p.seqs;
+      wanted = want;
       while (from > 0) {
         const int b = from - 1 - lane;
         int q0 = 0, queries = 0;
@@ -422,11 +446,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return false;
     };
     uint32_t copies = 0, with_tiles = 0;
+    uint32_t block = blockIdx.x;
     for (int n = 0;; ++n) {
-      const long long w = (long long)n * gridDim.x + (n % 2 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      bool some = true;
+      if (n > 0) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kBarBlock), 16);
+          ask_for_block(smem_u32(&answer), bar(kBarBlock));
+        }
+        __syncwarp();
+        if (!tc_wait(bar(kBarBlock), (n - 1) & 1, ab, kAttnTimeout)) break;
+        some = answered_block(smem_u32(&answer), block);
+        fence_proxy_async_smem();  // the next answer comes to the same place
+        __syncwarp();
+      }
       PromptUnit u;
       u.poison = 0;
-      u.head = find(w / p.q_heads, u) ? (int)(w % p.q_heads) : -1;
+      u.head = some && find(block / p.q_heads, u) ? (int)(block % p.q_heads) : -1;
       if (u.head >= 0) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -573,8 +609,7 @@ static cudaError_t prompt_form(const PromptParams* p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   }
   const long long units = p->q_rows / kUnitRows + std::min<long long>(p->seqs, p->q_rows);  // at most
-  const unsigned blocks = (unsigned)std::min<long long>(units * p->q_heads, p->sms);
-  kernel<<<blocks, kPromptThreads, kPromptSmem<HALVES>, stream>>>(qmap, kmap, vmap, *p);
+  kernel<<<(unsigned)(units * p->q_heads), kPromptThreads, kPromptSmem<HALVES>, stream>>>(qmap, kmap, vmap, *p);
   return cudaGetLastError();
 }
 
