@@ -65,13 +65,12 @@ template <int CODE, int D>
 constexpr int kTileBytes = 2 * kTile * (kRowBytes<CODE, D> + kScaleBytes<CODE>);
 // Stages of a warp's ring: what kBlocksPerSm blocks have room for.
 template <int CODE, int D, int NB>
-constexpr int kStages = CODE == Q8_INT4 ? 4 / kStepTiles<CODE, D, NB> : D == 256 ? 2 : 3;
+constexpr int kStages = CODE == Q8_INT4 && D < 256 ? 4 / kStepTiles<CODE, D, NB> : D == 256 && CODE != Q8_INT4 ? 2 : 3;
 // Channels of a row of the sums in shared memory: 4 more, so that the lanes of a store meet all banks.
 template <int D>
 constexpr int kSumPitch = D + 4;
 template <int CODE, int D, int NB>
-constexpr int kRingBytes = std::max(kWarps * kStages<CODE, D, NB> * kStepTiles<CODE, D, NB> * kTileBytes<CODE, D>,
-                                    kWarps * NB * 8 * kSumPitch<D> * 4);
+constexpr int kRingBytes = kWarps * kStages<CODE, D, NB> * kStepTiles<CODE, D, NB> * kTileBytes<CODE, D>;
 template <int D, int NB>
 constexpr int kBlocksPerSm = D * NB <= 128 ? 4 : D * NB == 256 ? 3 : 2;
 
@@ -196,6 +195,23 @@ struct Found {
   long long before;  // groups of the sequences before it
 };
 
+// Quotients of sizes that nearly always fit 32 bits (64-bit ones take some hundred cycles).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+// All units in `blocks` runs, the first `extra` of them one longer: where a block's begins, and which block has a unit.
+struct Runs {
+  long long each;
+  int extra;
+  __device__ __forceinline__ Runs(long long total, int blocks)
+      : each(divide(total, blocks)), extra((int)(total - each * blocks)) {}
+  __device__ __forceinline__ long long begin(int block) const { return block * each + min(block, extra); }
+  __device__ __forceinline__ int block_of(long long unit) const {
+    const long long longer = extra * (each + 1);
+    return (int)(unit < longer ? divide(unit, each + 1) : extra + divide(unit - longer, each));
+  }
+};
+
 // Groups of a sequence's keys, one at least: a sequence without keys has an output too. A bad length counts as none.
 template <int GROUP>
 __device__ __forceinline__ int groups_of(const CacheAttnParams& p, int b) {
@@ -216,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t bars[kWarps * kStages<CODE, D, NB>];
   __shared__ float stat[2][kWarps][NB * 8];
+  __shared__ __align__(8) float sums[NB * 8 * kSumPitch<D>];
   __shared__ long long scan[kWarps];
   __shared__ Found found;
   __shared__ int abort_flag, bad_input[2];  // the flag of this round and of the next
@@ -236,52 +253,73 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   if (lane < kS) mbar_init(bar_at + 8 * lane, 1);
   fence_mbar_init();
 
+  pdl_wait_primary();
   // ---- this block's share
-  long long total = 0;
-  for (int b = threadIdx.x; b < p.seqs; b += kThreads) total += groups_of<kShare>(p, b);
-  total = warp_sum(total);
-  if (lane == 0) scan[warp] = total;
-  __syncthreads();
-  total = 0;
+  long long total, at, until, before = 0;
+  int blocks, seq = 0;
+  auto cut_runs = [&] {
+    total *= heads;
+    blocks = (int)min((long long)gridDim.x, max(1LL, total / max(1, kLeastKeys / kShare)));
+    const Runs runs(total, blocks);
+    at = runs.begin(blockIdx.x);
+    until = runs.begin(blockIdx.x + 1);
+  };
+  if (p.seqs <= 32) {  // each warp by itself: without barriers and a second look (2 us of a short call)
+    const int mine = lane < p.seqs ? groups_of<kShare>(p, lane) : 0;
+    long long sum = mine;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += scan[w];
-  __syncthreads();
-  total *= heads;
-  const int blocks = (int)min((long long)gridDim.x, max(1LL, total / max(1, kLeastKeys / kShare)));
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, sum, 31);
+    cut_runs();
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, sum > divide(at, heads));
+    seq = hit ? __ffs(hit) - 1 : 0;
+    before = __shfl_sync(0xFFFFFFFFu, sum - mine, seq);
+  } else {
+    total = 0;
+    for (int b = threadIdx.x; b < p.seqs; b += kThreads) total += groups_of<kShare>(p, b);
+    total = warp_sum(total);
+    if (lane == 0) scan[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += scan[w];
+    __syncthreads();
+    cut_runs();
+    const long long want = divide(at, heads);
+    if ((int)blockIdx.x < blocks) {
+      for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        const int mine = b < p.seqs ? groups_of<kShare>(p, b) : 0;
+        long long sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        if (lane == 31) scan[warp] = sum;
+        __syncthreads();
+        long long end = before;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) sum += scan[w];
+          end += scan[w];
+        }
+        if (before + sum > want && before + sum - mine <= want) found = Found{b, before + sum - mine};
+        __syncthreads();
+        if (end > want) break;
+        before = end;
+      }
+      seq = found.seq;
+      before = found.before;
+    }
+  }
   pdl_launch_dependents();
   const bool by_head = p.seqs * heads <= (long long)gridDim.x;
   if (threadIdx.x == 0 && !by_head) shared_heads[blockIdx.x].last = -1;
   if ((int)blockIdx.x >= blocks) return;
-  long long at = blockIdx.x * total / blocks;
-  const long long until = (blockIdx.x + 1) * total / blocks;
-  {
-    const long long want = at / heads;
-    long long before = 0;
-    for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      const int mine = b < p.seqs ? groups_of<kShare>(p, b) : 0;
-      long long sum = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (lane == 31) scan[warp] = sum;
-      __syncthreads();
-      long long end = before;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) sum += scan[w];
-        end += scan[w];
-      }
-      if (before + sum > want && before + sum - mine <= want) found = Found{b, before + sum - mine};
-      __syncthreads();
-      if (end > want) break;
-      before = end;
-    }
-  }
-  int seq = found.seq;
-  long long before = found.before;
 
   const AbortState ab{&abort_flag, p.status, kCacheTimeoutNs};
   const float scale_log2 = p.scale * 1.44269504088896f;
@@ -294,71 +332,79 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
                             : t4 == 1 ? c.v_codes
                                       : reinterpret_cast<const uint8_t*>(t4 == 2 ? c.k_scale : c.v_scale);
 
-  // ---- the heads of sequences that it covers, or parts of them
-  for (int round = 0; at < until; round ^= 1) {
-    const int groups = groups_of<kShare>(p, seq);
-    const long long head_index = (at - before * heads) / groups;
-    const int first_group = (int)((at - before * heads) - head_index * groups);
-    const int take = (int)min((long long)groups - first_group, until - at);
-    const int head = (int)(head_index / row_blocks), row0 = (int)(head_index % row_blocks) * kRows;
+  // ---- the heads of sequences that it covers, or parts of them: of the one that it is at
+  long long head_index;
+  int groups, first_group, take, head, row0, keys, tiles, first, count;
+  bool bad;
+  long long places;  // where 32 of this warp's tiles lie, a lane each, in tiles of the whole cache; -1 behind the end
+  int ahead;         // steps whose copies are issued
+  // This lane's channels of q's rows, 16 bytes at a time.
+  constexpr int kCodesOf = CODE == Q8_INT4 ? 8 : 4, kPer = 8 / kCodesOf;  // codes of a word, words of 16 bytes
+  const unsigned page_tiles = (unsigned)c.page_size / kTile;
+  auto places_from = [&](int i) {
+    const int tile = (first + (i + lane / kTiles) * kWarps) * kTiles + lane % kTiles;
+    if (i + lane / kTiles >= count || tile >= tiles) return -1LL;
+    const unsigned entry = (unsigned)tile / page_tiles;
+    unsigned page = (unsigned)p.table[seq * p.table_pitch + entry];
+    if (page >= c.slots / (unsigned)c.page_size) {
+      bad = true;
+      page = 0;  // some page of the cache; what is read there is dropped
+    }
+    return ((long long)page * c.kv_heads + head) * page_tiles + ((unsigned)tile - entry * page_tiles);
+  };
+  auto issue = [&](int i) {
+    const long long place = __shfl_sync(0xFFFFFFFFu, places, i * kTiles % 32 + g % kTiles);
+    const uint32_t stage = issued % kS, bar = bar_at + 8 * stage;
+    const bool mine = lane < 4 * kTiles && place >= 0;
+    const bool all = kTiles == 1 || (__ballot_sync(0xFFFFFFFFu, mine) >> 4) != 0;
+    if (lane == 0) mbar_arrive_expect_tx(bar, all ? kStageBytes : kOneTile);
+    __syncwarp();
+    if (mine) bulk_load(copy_dst + stage * kStageBytes, copy_src + place * copy_bytes, copy_bytes, bar);
+    ++issued;
+  };
+  auto start = [&] {
+    groups = groups_of<kShare>(p, seq);
+    head_index = divide(at - before * heads, groups);
+    first_group = (int)((at - before * heads) - head_index * groups);
+    take = (int)min((long long)groups - first_group, until - at);
+    head = row_blocks == 1 ? (int)head_index : (int)head_index / row_blocks;
+    row0 = ((int)head_index - head * row_blocks) * kRows;
     const int length = p.lengths[seq];
-    bool bad = length < 0 || length > (long long)p.table_width * c.page_size;
-    const int keys = bad ? 0 : length;
-    const int tiles = (int)(((unsigned)keys + kTile - 1) / kTile), steps = (tiles + kTiles - 1) / kTiles;
-    const int first = first_group * kWarps + warp;  // of this warp's steps, which are kWarps apart
+    bad = length < 0 || length > (long long)p.table_width * c.page_size;
+    keys = bad ? 0 : length;
+    tiles = (int)(((unsigned)keys + kTile - 1) / kTile);
+    const int steps = (tiles + kTiles - 1) / kTiles;
+    first = first_group * kWarps + warp;  // of this warp's steps, which are kWarps apart
     const int end = min(steps, (first_group + take) * kWarps);
-    const int count = first < end ? (end - first + kWarps - 1) / kWarps : 0;
-    const int* table = p.table + seq * p.table_pitch;
-
-    // Where 32 of this warp's tiles lie, a lane each, in tiles of the whole cache; -1 behind the end.
-    const unsigned page_tiles = (unsigned)c.page_size / kTile;
-    auto places_from = [&](int i) {
-      const int tile = (first + (i + lane / kTiles) * kWarps) * kTiles + lane % kTiles;
-      if (i + lane / kTiles >= count || tile >= tiles) return -1LL;
-      const unsigned entry = (unsigned)tile / page_tiles;
-      unsigned page = (unsigned)table[entry];
-      if (page >= c.slots / (unsigned)c.page_size) {
-        bad = true;
-        page = 0;  // some page of the cache; what is read there is dropped
-      }
-      return ((long long)page * c.kv_heads + head) * page_tiles + ((unsigned)tile - entry * page_tiles);
-    };
-    long long places = places_from(0);
-    auto issue = [&](int i) {
-      const long long place = __shfl_sync(0xFFFFFFFFu, places, i * kTiles % 32 + g % kTiles);
-      const uint32_t stage = issued % kS, bar = bar_at + 8 * stage;
-      const bool mine = lane < 4 * kTiles && place >= 0;
-      const bool all = kTiles == 1 || (__ballot_sync(0xFFFFFFFFu, mine) >> 4) != 0;
-      if (lane == 0) mbar_arrive_expect_tx(bar, all ? kStageBytes : kOneTile);
-      __syncwarp();
-      if (mine) bulk_load(copy_dst + stage * kStageBytes, copy_src + place * copy_bytes, copy_bytes, bar);
-      ++issued;
-    };
-    int ahead = min(count, kS);
+    count = first < end ? (end - first + kWarps - 1) / kWarps : 0;
+    places = places_from(0);
+    ahead = min(count, kS);
     for (int i = 0; i < ahead; ++i) issue(i);
-
+  };
+  start();
+  for (int round = 0;; round ^= 1) {
     // ---- q's operands: row g of the columns, in the order of the codes
+    uint4 q_raw[NB][kKeyWords / kPer];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = row0 + 8 * nb + g, t = r / group;
+      const T* q = static_cast<const T*>(p.q.p) + ((long long)seq * p.tokens + t) * p.q.pitch +
+                   (long long)(head * group + r - t * group) * p.q.head_pitch;
+#pragma unroll
+      for (int w = 0; w < kKeyWords / kPer; ++w)
+        q_raw[nb][w] = r < rows_all ? *reinterpret_cast<const uint4*>(q + key_channel<CODE, D>(t4, w * kPer, 0))
+                                    : make_uint4(0, 0, 0, 0);
+    }
     uint32_t q_frag[NB][kBlocks][2];
     float factor[NB][2], q_sum[NB][2];  // of the columns 2 t4 and the next
     int limit[NB][2];                   // keys that they see
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      const int r = row0 + 8 * nb + g;
-      const bool live = r < rows_all;
-      const int t = live ? r / group : 0, h = live ? r - t * group : 0;
-      const T* q = static_cast<const T*>(p.q.p) + ((long long)seq * p.tokens + t) * p.q.pitch +
-                   (long long)(head * group + h) * p.q.head_pitch;
-      // this lane's channels, 16 bytes at a time
-      constexpr int kCodesOf = CODE == Q8_INT4 ? 8 : 4, kPer = 8 / kCodesOf;  // codes of a word, words of 16 bytes
-      uint4 raw[kKeyWords / kPer];
-#pragma unroll
-      for (int w = 0; w < kKeyWords / kPer; ++w)
-        raw[w] = live ? *reinterpret_cast<const uint4*>(q + key_channel<CODE, D>(t4, w * kPer, 0)) : make_uint4(0, 0, 0, 0);
       float amax = 0.0f;
 #pragma unroll
       for (int w = 0; w < kKeyWords / kPer; ++w)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) amax = fmaxf(amax, fabsf(q8_to_float(reinterpret_cast<const T*>(&raw[w])[n])));
+        for (int n = 0; n < 8; ++n) amax = fmaxf(amax, fabsf(q8_to_float(reinterpret_cast<const T*>(&q_raw[nb][w])[n])));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
       // the largest between 2^8 and 2^9, by a power of two (in two parts, each of which fp32 holds)
@@ -366,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
       const float up0 = __uint_as_float((127 + up / 2) << 23), up1 = __uint_as_float((127 + up - up / 2) << 23);
       const float down0 = __uint_as_float((127 - up / 2) << 23), down1 = __uint_as_float((127 - up + up / 2) << 23);
       auto value = [&](int w, int n) {
-        return q8_to_float(reinterpret_cast<const T*>(&raw[w / kPer])[w % kPer * kCodesOf + n]) * up0 * up1;
+        return q8_to_float(reinterpret_cast<const T*>(&q_raw[nb][w / kPer])[w % kPer * kCodesOf + n]) * up0 * up1;
       };
       float sum = 0.0f;
 #pragma unroll
@@ -596,15 +642,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
         issue(ahead++);
       }
     }
-    if (!waited) {  // the copies under way land before the ring is used again; then all is given up
-      for (; used < issued; ++used) {
-        int own = 0;
-        tc_wait(bar_at + 8 * (used % kS), (used / kS) & 1,
-                          AbortState{&own, p.status, 1000000ull}, kAttnTimeout);
-      }
-      bad = true;
+    if (bad || !waited) bad_input[round] = 1;
+
+    // ---- the next one's copies are under way while this one's sums are joined
+    const bool whole = take == groups;
+    const int part_side = first_group > 0 ? 0 : 1, done_seq = seq, done_head = head, done_row0 = row0;
+    const bool begins = first_group == 0;
+    const long long done_index = head_index, last_unit = before * heads + (head_index + 1) * groups - 1;
+    at += take;
+    const bool more = at < until;
+    if (more && waited) {
+      if (at == (before + groups) * heads) before += groups, ++seq;
+      start();
     }
-    if (bad) bad_input[round] = 1;
 
     // ---- the warps' sums, joined
 #pragma unroll
@@ -618,54 +668,52 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
         }
         if (g == 0) stat[0][warp][8 * nb + 2 * t4 + j] = top[nb][j];
       }
-    __syncthreads();  // all rings are idle: their memory takes the sums
-    float* sums = reinterpret_cast<float*>(ring);
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = 8 * nb + 2 * t4 + j;
-        float m = stat[0][0][r];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, stat[0][w][r]);
-        const float keep = exp2_fast(top[nb][j] - m);
-        if (g == 0) stat[1][warp][r] = weight[nb][j] * keep;
-        const float add = low_sum[nb][j] * keep;
-        float* row = sums + (warp * kRows + r) * kSumPitch<D> + 2 * g;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          *reinterpret_cast<float2*>(row + 16 * b) =
-              make_float2(fmaf(o[nb][b][j], keep, add), fmaf(o[nb][b][2 + j], keep, add));
-      }
     __syncthreads();
-    const bool whole = take == groups;
-    const bool tail = first_group + take == groups && !whole;  // the head began in an earlier block
-    float* part = parts + (2 * (long long)blockIdx.x + (tail || first_group > 0 ? 0 : 1)) * part_floats(kRows, D);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {  // one after another: there is room for one warp's beside the rings
+      if (w == warp) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = 8 * nb + 2 * t4 + j;
+            float m = stat[0][0][r];
+#pragma unroll
+            for (int v = 1; v < kWarps; ++v) m = fmaxf(m, stat[0][v][r]);
+            const float keep = top[nb][j] == m ? 1.0f : exp2_fast(top[nb][j] - m);
+            if (g == 0) stat[1][warp][r] = weight[nb][j] * keep;
+            const float add = low_sum[nb][j] * keep;
+            float* row = sums + r * kSumPitch<D> + 2 * g;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+              float2 v = make_float2(fmaf(o[nb][b][j], keep, add), fmaf(o[nb][b][2 + j], keep, add));
+              float2* to = reinterpret_cast<float2*>(row + 16 * b);
+              if (w > 0) v.x += to->x, v.y += to->y;
+              *to = v;
+            }
+          }
+      }
+      __syncthreads();
+    }
+    float* part = parts + (2 * (long long)blockIdx.x + part_side) * part_floats(kRows, D);
     const float nan = __int_as_float(0x7FFFFFFF);
     if (threadIdx.x == 0) {
       bad_input[round ^ 1] = 0;
       if (bad_input[round] && !abort_flag) atomicOr(p.status, kAttnBadInput);
-      if (first_group == 0 && (by_head || !whole)) {
-        // the block that holds this head's last group
-        const long long last = before * heads + (head_index + 1) * groups - 1;
-        shared_heads[by_head ? seq * heads + head_index : blockIdx.x] =
-            SharedHead{(int)blockIdx.x, whole ? -1 : (int)(((last + 1) * blocks - 1) / total), seq, head, row0};
-      }
+      if (begins && (by_head || !whole))
+        // its last block is the one that holds the head's last group
+        shared_heads[by_head ? done_seq * heads + done_index : blockIdx.x] =
+            SharedHead{(int)blockIdx.x, whole ? -1 : Runs(total, blocks).block_of(last_unit), done_seq, done_head, done_row0};
     }
     for (int i = threadIdx.x; i < kRows * (D / 2); i += kThreads) {
       const int r = i / (D / 2), pair = i % (D / 2);
       const int lane_of = 2 * pair / (D / 8), block_of = pair % (D / 16);
-      float2 sum = make_float2(0.0f, 0.0f);
+      const float2 sum = *reinterpret_cast<const float2*>(sums + r * kSumPitch<D> + 16 * block_of + 2 * lane_of);
       float l = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(sums + (w * kRows + r) * kSumPitch<D> + 16 * block_of + 2 * lane_of);
-        sum.x += v.x;
-        sum.y += v.y;
-        l += stat[1][w][r];
-      }
+      for (int w = 0; w < kWarps; ++w) l += stat[1][w][r];
       if (bad_input[round]) l = nan;
-      const int rr = row0 + r;
+      const int rr = done_row0 + r;
       if (!whole) {
         *reinterpret_cast<float2*>(part + 2 * kRows + r * D + 2 * pair) = sum;
         if (pair == 0) {
@@ -678,27 +726,33 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
       } else if (rr < rows_all) {
         const int t = rr / group, h = rr - t * group;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.o.p) + ((long long)seq * p.tokens + t) * p.o.pitch +
-                                                    (long long)(head * group + h) * p.o.head_pitch + 2 * pair);
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(p.o.p) +
+                                                    ((long long)done_seq * p.tokens + t) * p.o.pitch +
+                                                    (long long)(done_head * group + h) * p.o.head_pitch + 2 * pair);
         *out = q8_pack2<T>(make_float2(sum.x * inv, sum.y * inv));
       }
     }
-    fence_proxy_async_smem();  // the ring takes copies again
-    at += take;
-    if (at == (before + groups) * heads) before += groups, ++seq;
-    if (__syncthreads_or(abort_flag)) break;
+    const bool stop = __syncthreads_or(!waited) || !more;
+    if (stop) {
+      // on abort another warp may have copies of the next one under way
+      for (; used < issued; ++used) {
+        int own = 0;
+        tc_wait(bar_at + 8 * (used % kS), (used / kS) & 1, AbortState{&own, p.status, 1000000ull}, kAttnTimeout);
+      }
+      break;
+    }
   }
 }
 
 // Joins the sums of heads that several blocks share: gridDim.y blocks for each of them, between whose rows the warps
-// are divided.
+// are divided. A warp joins its parts as the main kernel does keys, so that they are looked at once.
 constexpr int kJoinWarps = 8;
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheAttnParams p, const float* parts,
                                                                      const SharedHead* shared_heads) {
-  constexpr int kRows = NB * 8, kVec = D / 32;
+  constexpr int kRows = NB * 8, kVec = D / 32, kAtOnce = 4;
   __shared__ float sums[kJoinWarps][D];
-  __shared__ float weights[kJoinWarps];
+  __shared__ float2 stats[kJoinWarps];  // the reference and the sum of the weights
   pdl_wait_primary();
   const SharedHead s = shared_heads[blockIdx.x];
   if (s.last < 0) return;
@@ -706,32 +760,58 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
   const int rows = kRows / gridDim.y, at_once = min(rows, kJoinWarps), share = kJoinWarps / at_once;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, mine = warp % share;
   const int n = s.last - s.first + 1;
-  auto part_of = [&](int i) { return parts + (2 * ((long long)s.first + i) + (i == 0)) * part_floats(kRows, D); };
-  for (int r0 = blockIdx.y * rows; r0 < (blockIdx.y + 1) * rows; r0 += at_once) {
+  for (int r0 = blockIdx.y * rows; r0 < (int)(blockIdx.y + 1) * rows; r0 += at_once) {
     const int r = r0 + warp / share;
-    float m = kLowest;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, part_of(i)[r]);
+    float m = kLowest, l = 0.0f, sum[kVec] = {};
+    for (int i0 = mine; i0 < n; i0 += share * kAtOnce) {
+      float pm[kAtOnce], pl[kAtOnce], v[kAtOnce][kVec];
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
-    float sum[kVec] = {}, l = 0.0f;
-#pragma unroll 8
-    for (int i = mine; i < n; i += share) {
-      const float* part = part_of(i);
-      const float keep = exp2_fast(part[r] - m);
-      l = fmaf(part[kRows + r], keep, l);
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int i = i0 + a * share;
+        pm[a] = kLowest;
+        if (i < n) {
+          const float* part = parts + (2 * ((long long)s.first + i) + (i == 0)) * part_floats(kRows, D);
+          pm[a] = part[r];
+          pl[a] = part[kRows + r];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) sum[e] = fmaf(part[2 * kRows + r * D + 32 * e + lane], keep, sum[e]);
+          for (int e = 0; e < kVec; ++e) v[a][e] = part[2 * kRows + r * D + 32 * e + lane];
+        }
+      }
+      float now = m;
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) now = fmaxf(now, pm[a]);
+      const float before = now == m ? 1.0f : exp2_fast(m - now);
+      m = now;
+      l *= before;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) sum[e] *= before;
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        if (i0 + a * share >= n) continue;
+        const float keep = pm[a] == m ? 1.0f : exp2_fast(pm[a] - m);
+        l = fmaf(pl[a], keep, l);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum[e] = fmaf(v[a][e], keep, sum[e]);
+      }
     }
     if (share > 1) {
+      if (lane == 0) stats[warp] = make_float2(m, l);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) sums[warp][32 * e + lane] = sum[e];
-      if (lane == 0) weights[warp] = l;
       __syncthreads();
       if (mine == 0) {
-        for (int w = 1; w < share; ++w) {
-          l += weights[warp + w];
+        float now = m;
+        for (int w = 1; w < share; ++w) now = fmaxf(now, stats[warp + w].x);
+        const float before = m == now ? 1.0f : exp2_fast(m - now);
+        l *= before;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) sum[e] += sums[warp + w][32 * e + lane];
+        for (int e = 0; e < kVec; ++e) sum[e] *= before;
+        for (int w = 1; w < share; ++w) {
+          const float2 st = stats[warp + w];
+          const float keep = st.x == now ? 1.0f : exp2_fast(st.x - now);
+          l = fmaf(st.y, keep, l);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) sum[e] = fmaf(sums[warp + w][32 * e + lane], keep, sum[e]);
         }
       }
       __syncthreads();
@@ -775,21 +855,24 @@ static cudaError_t cache_attn_form(const CacheAttnParams* p, void* workspace, in
   const int blocks = cache_attn_blocks(sms, D, NB);
   float* parts = static_cast<float*>(workspace);
   SharedHead* shared_heads = reinterpret_cast<SharedHead*>(parts + 2 * blocks * part_floats(8 * NB, D));
-  kernel<<<blocks, kThreads, kSmem, stream>>>(*p, parts, shared_heads);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t config{};
+  config.stream = stream;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  config.gridDim = dim3(blocks);
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = kSmem;
+  const cudaError_t e = cudaLaunchKernelEx(&config, kernel, *p, parts, shared_heads);
+  if (e != cudaSuccess) return e;
+  config.dynamicSmemBytes = 0;
   const int row_blocks = (p->tokens * (p->q_heads / p->cache.kv_heads) + 8 * NB - 1) / (8 * NB);
   const long long heads = (long long)p->seqs * p->cache.kv_heads * row_blocks;
   // few heads have many parts: blocks for each of their rows of their own
   config.gridDim = heads <= sms ? dim3((unsigned)heads, NB * 8) : dim3((unsigned)std::min<long long>(heads, blocks), 1);
   config.blockDim = dim3(kJoinWarps * 32);
-  config.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &attr;
-  config.numAttrs = 1;
   return cudaLaunchKernelEx(&config, cache_join_kernel<T, D, NB>, *p, (const float*)parts,
                             (const SharedHead*)shared_heads);
 }
