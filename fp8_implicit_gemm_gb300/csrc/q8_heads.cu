@@ -3,8 +3,7 @@
 //
 // A row is one token's head. L = 8, 16 or 32 lanes hold it, eight elements each, so that its sums, its
 // partners in the rotation and its scale are shuffles, and every element is read once and written once:
-// the memory's bandwidth is the bound. A block takes a few tokens and all their heads; the sines of
-// a token's angles are taken once, into shared memory.
+// the memory's bandwidth is the bound. A warp takes a token's heads; the sines of its angles are taken once.
 //
 // Angles. In turns an angle is frequency / 2 pi * position, and only its fraction matters. With the
 // frequency as an integer f of 2^-64 turns the fraction of f * position is the 64-bit product, whose
@@ -14,8 +13,11 @@
 // Codes. The code of v is T * v / amax, to the nearest, ties to even (for 4 bits 15 * (v - lowest) / (highest -
 // lowest)). With 16-bit inputs such quotients lie on ties often, so the quotient has to be right to the
 // last bit: q0 = a * r with r = 1 / w rounded, then q0 + r * (a - q0 * w) with both steps fused, which
-// is the correctly rounded a / w (Markstein, 1990). The product of a reciprocal alone gave 1.2% of the norm of
-// 8192 x 8 x 128 bf16 keys in codes that went the other way.
+// is the correctly rounded a / w (Markstein, 1990). (Division by the rounded scale, in fp32 with torch, sends so many 4-bit
+// codes of 8192 x 8 x 128 bf16 keys the other way that their values differ by 1.3%.)
+#include <algorithm>
+#include <type_traits>
+
 #include "q8_attn_internal.h"
 #include "q8_common.cuh"
 
@@ -24,22 +26,9 @@ namespace c3d {
 constexpr int kHeadsThreads = 256;
 constexpr int kLane = 8;             // elements of a row that a lane holds
 constexpr int kMostPairs = Q8_MAX_HEAD_DIM / 2;
-constexpr int kMostTokens = 16;      // of a block
 constexpr int kNoCodes = 0;
 
 // ------------------------------------------------------------------ eight values of a row
-__device__ __forceinline__ void load8(const float* p, float (&f)[kLane]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[kLane]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const T* h = reinterpret_cast<const T*>(&a);
-#pragma unroll
-  for (int e = 0; e < kLane; ++e) f[e] = q8_to_float(h[e]);
-}
 __device__ __forceinline__ void store8(float* p, const float (&f)[kLane]) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
@@ -61,21 +50,40 @@ __device__ __forceinline__ float row_sum(float v) {
   for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-// The largest magnitude as bits, whose order is that of the magnitudes with every NaN above them.
+// Extremes that keep a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 template <int L>
-__device__ __forceinline__ unsigned row_amax(const float (&f)[kLane]) {
-  unsigned m = 0;
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-  for (int e = 0; e < kLane; ++e) m = max(m, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+  for (int o = L / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+// The largest magnitude, NaN if there is one.
+template <int L>
+__device__ __forceinline__ float row_amax(const float (&f)[kLane]) {
+  float m = 0.0f;
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return m;
+  for (int e = 0; e < kLane; e += 2)
+    asm("max.NaN.abs.f32 %0, %1, %2, %0;" : "+f"(m) : "f"(f[e]), "f"(f[e + 1]));
+  return row_max<L>(m);
 }
 
-// a / w rounded once, given r = 1 / w rounded.
-__device__ __forceinline__ float quotient(float a, float w, float r) {
-  const float q = a * r;
-  return fmaf(fmaf(-q, w, a), r, q);
+constexpr float kLargest = 3.4028234e38f;
+constexpr float kInteger = 12582912.0f;  // 1.5 * 2^23: added to a small number it leaves its nearest integer in the low bits
+
+// a / w rounded once, for two, given r = 1 / w rounded.
+__device__ __forceinline__ float2 quotients(float2 a, float w, float r) {
+  const float2 r2 = make_float2(r, r), q = q8_mul2(a, r2);
+  return q8_fma2(q8_fma2(make_float2(-q.x, -q.y), make_float2(w, w), a), r2, q);
 }
 
 // A power of two that takes w (not 0) to where neither its reciprocal nor 448 times it leaves fp32's normal range.
@@ -89,65 +97,62 @@ __device__ __forceinline__ float lift_of(float w) {
 template <int CODE, int L>
 __device__ __forceinline__ void write_codes(uint8_t* codes, float* scales, long long row, int chunk,
                                             const float (&f)[kLane], bool store) {
-  const unsigned amax_bits = row_amax<L>(f);
+  const float nan = __int_as_float(0x7FFFFFFF);
   if constexpr (CODE == Q8_INT4) {
     float lo = f[0], hi = f[0];
 #pragma unroll
     for (int e = 1; e < kLane; ++e) {
-      lo = fminf(lo, f[e]);
-      hi = fmaxf(hi, f[e]);
+      lo = min_nan(lo, f[e]);
+      hi = max_nan(hi, f[e]);
     }
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-    }
+    hi = row_max<L>(hi);
+    lo = -row_max<L>(-lo);
     const float width = hi - lo;
-    const bool bad = amax_bits >= 0x7F800000u || width > 3.4028234e38f;
-    const bool flat = !(width > 0.0f) || bad;
+    const bool bad = !(width <= kLargest), flat = bad || width == 0.0f;
     const float lift = lift_of(width);
-    const float w = flat ? 1.0f : width * lift, r = __frcp_rn(w);
-    unsigned word = 0;
+    const float w = width * lift, r = __frcp_rn(w);
+    const float2 times = make_float2(15.0f * lift, 15.0f * lift), least = make_float2(-lo, -lo);
+    unsigned bytes[4];
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) {
-      const float a = flat ? 0.0f : (f[e] - lo) * lift * 15.0f;
-      word |= (unsigned)__float2int_rn(quotient(a, w, r)) << (4 * e);
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = q8_mul2(q8_add2(make_float2(f[2 * e], f[2 * e + 1]), least), times);
+      const float2 t = q8_add2(quotients(a, w, r), make_float2(kInteger, kInteger));
+      bytes[e] = __float_as_uint(fmaf(16.0f, t.y - kInteger, t.x));  // in the low byte: both codes
     }
+    const unsigned word = __byte_perm(__byte_perm(bytes[0], bytes[1], 0x0040), __byte_perm(bytes[2], bytes[3], 0x0040), 0x5410);
     if (!store) return;
-    *reinterpret_cast<unsigned*>(codes + (row * L + chunk) * (kLane / 2)) = word;
+    *reinterpret_cast<unsigned*>(codes + (row * L + chunk) * (kLane / 2)) = flat ? 0u : word;
     if (chunk == 0)
       *reinterpret_cast<float2*>(scales + 2 * row) =
-          make_float2(bad ? __int_as_float(0x7FFFFFFF) : flat ? 1.0f : __fdiv_rn(width, 15.0f),
-                      bad ? 0.0f : lo);
+          make_float2(bad ? nan : flat ? 1.0f : __fdiv_rn(width, 15.0f), bad ? 0.0f : lo);
   } else {
     constexpr float kTop = CODE == Q8_INT8 ? 127.0f : 448.0f;
-    const float amax = __uint_as_float(amax_bits);
-    const bool bad = amax_bits >= 0x7F800000u, flat = bad || amax_bits == 0;
+    const float amax = row_amax<L>(f);
+    const bool bad = !(amax <= kLargest), flat = bad || amax == 0.0f;
     const float lift = lift_of(amax);
-    const float w = flat ? 1.0f : amax * lift, r = __frcp_rn(w);
-    float q[kLane];
+    const float w = amax * lift, r = __frcp_rn(w);
+    const float2 times = make_float2(kTop * lift, kTop * lift);
+    float2 q[kLane / 2];
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) q[e] = flat ? 0.0f : quotient(f[e] * lift * kTop, w, r);
-    uint2 word = make_uint2(0, 0);
+    for (int e = 0; e < kLane / 2; ++e) q[e] = quotients(q8_mul2(make_float2(f[2 * e], f[2 * e + 1]), times), w, r);
+    uint2 word;
     if constexpr (CODE == Q8_INT8) {
+      unsigned half[4];  // two codes in the low bytes
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        word.x |= ((unsigned)__float2int_rn(q[e]) & 0xFFu) << (8 * e);
-        word.y |= ((unsigned)__float2int_rn(q[4 + e]) & 0xFFu) << (8 * e);
+        const float2 t = q8_add2(q[e], make_float2(kInteger, kInteger));
+        half[e] = __byte_perm(__float_as_uint(t.x), __float_as_uint(t.y), 0x0040);
       }
+      word = make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
     } else {
+      unsigned half[4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        word.x |= (unsigned)__nv_cvt_float2_to_fp8x2(make_float2(q[2 * e], q[2 * e + 1]), __NV_SATFINITE,
-                                                     __NV_E4M3) << (16 * e);
-        word.y |= (unsigned)__nv_cvt_float2_to_fp8x2(make_float2(q[4 + 2 * e], q[5 + 2 * e]),
-                                                     __NV_SATFINITE, __NV_E4M3) << (16 * e);
-      }
+      for (int e = 0; e < 4; ++e) half[e] = __nv_cvt_float2_to_fp8x2(q[e], __NV_SATFINITE, __NV_E4M3);
+      word = make_uint2(half[0] | half[1] << 16, half[2] | half[3] << 16);
     }
     if (!store) return;
-    *reinterpret_cast<uint2*>(codes + (row * L + chunk) * kLane) = word;
-    if (chunk == 0)
-      scales[row] = bad ? __int_as_float(0x7FFFFFFF) : flat ? 1.0f : __fdiv_rn(amax, kTop);
+    *reinterpret_cast<uint2*>(codes + (row * L + chunk) * kLane) = flat ? make_uint2(0, 0) : word;
+    if (chunk == 0) scales[row] = bad ? nan : flat ? 1.0f : __fdiv_rn(amax, kTop);
   }
 }
 
@@ -156,148 +161,219 @@ __device__ __forceinline__ void write_codes(uint8_t* codes, float* scales, long 
 // lanes (the partner is then read a second time).
 enum { kAdjacent, kHalves, kLooseHalves };
 
-template <typename T, int CODE, int L, int PAIRS>
-__global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const HeadsParams p, int block_tokens) {
-  __shared__ float2 turned[kMostTokens * kMostPairs];  // cosine and sine, [token][pair]
-  const int t0 = blockIdx.x * block_tokens;
-  const int tokens = min(block_tokens, p.tokens - t0);
-  const int half = p.rot_dim / 2, pairs = (half + kLane - 1) / kLane * kLane;
-  if (p.turns) {
-    for (int i = threadIdx.x; i < tokens * pairs; i += kHeadsThreads) {
-      const int t = i / pairs, j = i - t * pairs;
-      float s = 0.0f, c = 1.0f;
-      if (j < half) {
-        int axis = p.axis ? p.axis[j] : 0;
-        if (axis >= p.axes) axis = 0;
-        const long long pos = p.positions[axis * p.positions_pitch + t0 + t];
-        const long long turn = (long long)(p.turns[j] * (unsigned long long)pos);
-        sincospif((float)turn * 0x1p-63f, &s, &c);
+// What a lane holds of a row as it lies in memory: a row ahead is under way while one is worked on.
+template <typename T>
+struct RawLane {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void values(float (&f)[kLane]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < kLane; ++e) f[e] = reinterpret_cast<const float*>(w)[e];
+    } else if constexpr (std::is_same_v<T, __half>) {
+#pragma unroll
+      for (int e = 0; e < kLane; e += 2) {
+        const float2 v = __half22float2(reinterpret_cast<const __half2*>(w)[e / 2]);
+        f[e] = v.x, f[e + 1] = v.y;
       }
-      turned[i] = make_float2(c, s);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kLane; e += 2) {
+        const uint32_t v = reinterpret_cast<const uint32_t*>(w)[e / 2];
+        f[e] = __uint_as_float(v << 16), f[e + 1] = __uint_as_float(v & 0xFFFF0000u);
+      }
     }
   }
-  __syncthreads();
-  constexpr int kRows = kHeadsThreads / L;
-  const int chunk = threadIdx.x % L, e0 = chunk * kLane;
+};
+
+// A warp takes a token, or a share of its heads where there are few tokens: 32 / L rows of one kind (queries, keys, values) at a
+// time, all of the kind's, with the angles' sines and cosines in its lanes' registers.
+template <typename T, int CODE, int L, int PAIRS>
+__global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const HeadsParams p, int shares) {
+  constexpr int kRows = 32 / L;  // of a warp at a time
+  __shared__ float2 turned[kHeadsThreads / 32][kMostPairs];  // cosine and sine
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, chunk = lane % L, e0 = chunk * kLane;
   const bool mine = e0 < p.head_dim;
-  const int k_heads = p.k.p ? p.kv_heads : 0, v_heads = CODE != kNoCodes ? p.kv_heads : 0;
-  const int heads = p.q_heads + k_heads + v_heads;
-  const int rows = tokens * heads;
-  const int share = (rows + gridDim.y - 1) / gridDim.y;
-  const int first = blockIdx.y * share, end = min(rows, first + share);
-  // whole warps go around together
-  for (int base = first; base < end; base += kRows) {
-    const int row = base + threadIdx.x / L;
-    const bool live = row < end;
-    const int t = live ? row / heads : 0, h = live ? row - t * heads : 0;
-    const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + k_heads;
-    const int kv = is_q ? 0 : is_v ? h - p.q_heads - k_heads : h - p.q_heads;
-    const Heads& m = is_q ? p.q : is_v ? p.v : p.k;
-    const T* src = static_cast<const T*>(m.p) + (t0 + t) * m.pitch + (is_q ? h : kv) * m.head_pitch;
-    const void* weight = is_v ? nullptr : is_q ? p.q_weight : p.k_weight;
-    float f[kLane] = {};
-    if (live && mine) load8(src + e0, f);
-    float rms = 1.0f;
-    if (p.q_weight || p.k_weight) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int e = 0; e < kLane; ++e) sum = fmaf(f[e], f[e], sum);
-      sum = row_sum<L>(sum);
-      float lift = 1.0f;
-      const bool lifted = !(sum <= 0x1p100f) || (sum < 0x1p-80f && p.eps < 0x1p-100f);
-      if (__any_sync(0xFFFFFFFFu, lifted)) {
-        if (lifted) lift = sum < 1.0f ? 0x1p100f : 0x1p-100f;
-        float again = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) again = fmaf(f[e] * lift, f[e] * lift, again);
-        again = row_sum<L>(again);
-        if (lifted) sum = again;
+  const bool rotated = p.turns && e0 < p.rot_dim;
+  const int half = p.rot_dim / 2;
+  const float one_over_dim = 1.0f / p.head_dim;
+  // Rows of each kind, in units of what a warp takes at a time.
+  const int q_units = (p.q_heads + kRows - 1) / kRows;
+  const int k_units = p.k.p ? (p.kv_heads + kRows - 1) / kRows : 0;
+  const int units = q_units + k_units + (CODE != kNoCodes ? (p.kv_heads + kRows - 1) / kRows : 0);
+  const int per_share = (units + shares - 1) / shares;
+  __shared__ __align__(16) float weights[2][Q8_MAX_HEAD_DIM];  // of queries and of keys
+  if (p.q_weight || p.k_weight) {
+    for (int i = threadIdx.x; i < p.head_dim; i += kHeadsThreads) {
+      if (p.q_weight) weights[0][i] = q8_load_value(p.q_weight, p.weight_type, i);
+      if (p.k_weight) weights[1][i] = q8_load_value(p.k_weight, p.weight_type, i);
+    }
+    __syncthreads();
+  }
+  const long long items = (long long)p.tokens * shares, step = (long long)gridDim.x * (kHeadsThreads / 32);
+  for (long long item = (long long)blockIdx.x * (kHeadsThreads / 32) + warp; item < items; item += step) {
+    const int t = shares == 1 ? (int)item : (int)(item / shares);
+    const int first = shares == 1 ? 0 : (int)(item - (long long)t * shares) * per_share;
+    const int end = min(units, first + per_share);
+    long long slot = -1;
+    if constexpr (CODE != kNoCodes) slot = p.slots[t];
+    float2 turn[kLane];  // of this lane's elements (kAdjacent: pairs, of which there are half as many)
+    if (p.turns && (first < q_units + k_units)) {
+      __syncwarp();
+      for (int j = lane; j < half; j += 32) {
+        int axis = p.axis ? p.axis[j] : 0;
+        if (axis >= p.axes) axis = 0;
+        const long long pos = p.positions[axis * p.positions_pitch + t];
+        const long long angle = (long long)(p.turns[j] * (unsigned long long)pos);
+        float s, c;
+        sincospif((float)angle * 0x1p-63f, &s, &c);
+        turned[warp][j] = make_float2(c, s);
       }
-      if (weight) {
-        const float mean = sum / p.head_dim + p.eps * lift * lift;
-        rms = mean == 0.0f ? 0.0f : rsqrtf(mean);
+      __syncwarp();
+      if (rotated) {
 #pragma unroll
-        for (int e = 0; e < kLane; ++e)
-          f[e] = f[e] * lift * rms *
-                 (mine ? q8_load_value(weight, p.weight_type, e0 + e) : 0.0f);
-        rms *= lift;
+        for (int e = 0; e < kLane; ++e) {
+          if (PAIRS == kAdjacent && e >= kLane / 2) break;
+          const int i = PAIRS == kAdjacent ? e0 / 2 + e : e0 + e >= half ? e0 + e - half : e0 + e;
+          turn[e] = i < half ? turned[warp][i] : make_float2(1.0f, 0.0f);
+        }
       }
     }
-    if (p.turns) {
-      const float2* cs = turned + t * pairs;
-      const bool rotated = !is_v && e0 < p.rot_dim;
-      if constexpr (PAIRS == kAdjacent) {
-        if (rotated) {
+    long long at = 0;  // the slot's row of its page's first head
+    bool store = false;
+    if constexpr (CODE != kNoCodes) {
+      store = slot >= 0 && slot < (long long)p.cache.slots;
+      const unsigned page = (unsigned)slot / (unsigned)p.cache.page_size;
+      at = (long long)page * p.kv_heads * p.cache.page_size + ((unsigned)slot - page * p.cache.page_size);
+    }
+    // The rows of one kind, of which this share has the units [from, to).
+    auto rows = [&](auto kind_of, int from, int to, const Heads& in, const Heads& out, const void* w, int heads) {
+      constexpr int kind = decltype(kind_of)::value;
+      if (from >= to) return;
+      const int head0 = from * kRows + lane / L;
+      const T* src = static_cast<const T*>(in.p) + t * in.pitch + head0 * in.head_pitch + e0;
+      T* dst = static_cast<T*>(out.p) + t * out.pitch + head0 * out.head_pitch + e0;
+      RawLane<T> ahead{};
+      if (head0 < heads && mine) ahead.load(src);
+      for (int u = from, head = head0; u < to; ++u, head += kRows) {
+        const bool live = head < heads && mine;
+        const RawLane<T> raw = ahead;
+        [[maybe_unused]] const T* here = src;
+        src += kRows * in.head_pitch;
+        if (u + 1 < to && head + kRows < heads && mine) ahead.load(src);
+        float f[kLane];
+        raw.values(f);
+        float rms = 1.0f;
+        if (kind < 2 && w) {
+          float2 two = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int e = 0; e < kLane; e += 2) {
-            const float2 c = cs[(e0 + e) / 2];
-            const float a = f[e], b = f[e + 1];
-            f[e] = a * c.x - b * c.y;
-            f[e + 1] = b * c.x + a * c.y;
+            const float2 v = make_float2(f[e], f[e + 1]);
+            two = q8_fma2(v, v, two);
+          }
+          float sum = row_sum<L>(two.x + two.y);
+          float lift = 1.0f;
+          const bool lifted = !(sum <= 0x1p100f) || (sum < 0x1p-80f && p.eps < 0x1p-100f);
+          if (__any_sync(0xFFFFFFFFu, lifted)) {
+            if (lifted) lift = sum < 1.0f ? 0x1p100f : 0x1p-100f;
+            float again = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) {
+              if (lifted) f[e] *= lift;
+              again = fmaf(f[e], f[e], again);
+            }
+            again = row_sum<L>(again);
+            if (lifted) sum = again;
+          }
+          const float mean = fmaf(sum, one_over_dim, p.eps * lift * lift);
+          rms = mean == 0.0f ? 0.0f : rsqrtf(mean);
+          if (mine) {
+            const float2 rms2 = make_float2(rms, rms);
+#pragma unroll
+            for (int e = 0; e < kLane; e += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(&weights[kind][e0 + e]);
+              const float2 a = q8_mul2(make_float2(f[e], f[e + 1]), q8_mul2(rms2, make_float2(v.x, v.y)));
+              const float2 b = q8_mul2(make_float2(f[e + 2], f[e + 3]), q8_mul2(rms2, make_float2(v.z, v.w)));
+              f[e] = a.x, f[e + 1] = a.y, f[e + 2] = b.x, f[e + 3] = b.y;
+            }
+          }
+          rms *= lift;
+        }
+        if (kind < 2 && p.turns) {
+          if constexpr (PAIRS == kAdjacent) {
+            if (rotated) {
+#pragma unroll
+              for (int e = 0; e < kLane; e += 2) {
+                const float2 c = turn[e / 2];
+                const float a = f[e], b = f[e + 1];
+                f[e] = a * c.x - b * c.y;
+                f[e + 1] = b * c.x + a * c.y;
+              }
+            }
+          } else if constexpr (PAIRS == kHalves) {
+            const bool second = e0 >= half;
+            const int from_lane = lane + (rotated ? (second ? -half : half) / kLane : 0);
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) {
+              const float b = __shfl_sync(0xFFFFFFFFu, f[e], from_lane);
+              if (rotated) f[e] = fmaf(f[e], turn[e].x, b * (second ? turn[e].y : -turn[e].y));
+            }
+          } else {
+            float g[kLane];
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) {
+              g[e] = f[e];
+              const int i = e0 + e;
+              if (live && i < p.rot_dim) {
+                const int other = i < half ? i + half : i - half;
+                float b = q8_to_float(here[other - e0]);
+                if (w) b *= rms * weights[kind][other];
+                g[e] = i < half ? f[e] * turn[e].x - b * turn[e].y : f[e] * turn[e].x + b * turn[e].y;
+              }
+            }
+            __syncwarp();  // the output may be the input
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) f[e] = g[e];
           }
         }
-      } else if constexpr (PAIRS == kHalves) {
-        const bool second = e0 >= half;
-        const int partner = second ? chunk - half / kLane : chunk + half / kLane;
-        const int lane = (threadIdx.x & 31) - chunk + (rotated ? partner : chunk);
-        const int j0 = second ? e0 - half : e0;
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-          const float b = __shfl_sync(0xFFFFFFFFu, f[e], lane);
-          if (rotated) {
-            const float2 c = cs[j0 + e];
-            f[e] = second ? f[e] * c.x + b * c.y : f[e] * c.x - b * c.y;
-          }
+        if (kind < 2) {
+          if (live && out.p) store8(dst, f);
+          dst += kRows * out.head_pitch;
         }
-      } else {
-        float g[kLane];
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-          g[e] = f[e];
-          const int i = e0 + e;
-          if (live && rotated && i < p.rot_dim) {
-            const int j = i < half ? i : i - half, other = i < half ? i + half : j;
-            float b = q8_to_float(src[other]);
-            if (weight) b = b * rms * q8_load_value(weight, p.weight_type, other);
-            const float2 c = cs[j];
-            g[e] = i < half ? f[e] * c.x - b * c.y : f[e] * c.x + b * c.y;
-          }
-        }
-        __syncwarp();  // the output may be the input
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) f[e] = g[e];
+        if constexpr (CODE != kNoCodes && kind > 0)
+          write_codes<CODE, L>(kind == 2 ? p.cache.v_codes : p.cache.k_codes,
+                               kind == 2 ? p.cache.v_scale : p.cache.k_scale, at + (long long)head * p.cache.page_size,
+                               chunk, f, store && live);
       }
-    }
-    const Heads& out = is_q ? p.q_out : p.k_out;
-    if (live && mine && !is_v && out.p)
-      store8(static_cast<T*>(out.p) + (t0 + t) * out.pitch + (is_q ? h : kv) * out.head_pitch + e0, f);
-    if constexpr (CODE != kNoCodes) {
-      const long long slot = live && !is_q ? p.slots[t0 + t] : -1;
-      const bool store = slot >= 0 && slot < (long long)p.cache.slots;
-      const unsigned page = (unsigned)slot / (unsigned)p.cache.page_size;
-      const long long at = ((long long)page * p.kv_heads + kv) * p.cache.page_size +
-                           ((unsigned)slot - page * p.cache.page_size);
-      write_codes<CODE, L>(is_v ? p.cache.v_codes : p.cache.k_codes,
-                           is_v ? p.cache.v_scale : p.cache.k_scale, at, chunk, f, store);
-    }
+    };
+    rows(std::integral_constant<int, 0>{}, first, min(end, q_units), p.q, p.q_out, p.q_weight, p.q_heads);
+    rows(std::integral_constant<int, 1>{}, max(first - q_units, 0), min(end - q_units, k_units), p.k, p.k_out, p.k_weight,
+         p.kv_heads);
+    if constexpr (CODE != kNoCodes)
+      rows(std::integral_constant<int, 2>{}, max(first - q_units - k_units, 0), end - q_units - k_units, p.v, p.v, nullptr,
+           p.kv_heads);
   }
 }
 
 template <typename T, int CODE, int L>
 cudaError_t launch_heads_as(const HeadsParams& p, bool adjacent, cudaStream_t stream) {
-  const int heads = p.q_heads + (p.k.p ? p.kv_heads : 0) + (CODE != kNoCodes ? p.kv_heads : 0);
-  constexpr int kRows = kHeadsThreads / L;
-  const int block_tokens = heads >= kRows ? 1 : min(kMostTokens, (kRows + heads - 1) / heads);
-  const int blocks = (p.tokens + block_tokens - 1) / block_tokens;
-  const int passes = (block_tokens * heads + kRows - 1) / kRows;
-  const int split = blocks >= 2 * 152 ? 1 : min(passes, (2 * 152 + blocks - 1) / blocks);
-  const dim3 grid(blocks, split);
+  constexpr int kRows = 32 / L, kWarps = kHeadsThreads / 32;
+  auto units_of = [](int heads) { return (heads + kRows - 1) / kRows; };
+  const int units = units_of(p.q_heads) + (p.k.p ? units_of(p.kv_heads) : 0) + (CODE != kNoCodes ? units_of(p.kv_heads) : 0);
+  // few tokens: their heads are shared out until there are warps for a good part of the device
+  const int wanted = 152 * 2 * kWarps;
+  const int shares = p.tokens >= wanted ? 1 : std::min(units, (wanted + p.tokens - 1) / p.tokens);
+  const long long blocks = ((long long)p.tokens * shares + kWarps - 1) / kWarps;
+  const unsigned grid = (unsigned)std::min<long long>(blocks, 152 * 8);
   if (adjacent || !p.turns)
-    heads_kernel<T, CODE, L, kAdjacent><<<grid, kHeadsThreads, 0, stream>>>(p, block_tokens);
+    heads_kernel<T, CODE, L, kAdjacent><<<grid, kHeadsThreads, 0, stream>>>(p, shares);
   else if (p.rot_dim % (2 * kLane) == 0)
-    heads_kernel<T, CODE, L, kHalves><<<grid, kHeadsThreads, 0, stream>>>(p, block_tokens);
+    heads_kernel<T, CODE, L, kHalves><<<grid, kHeadsThreads, 0, stream>>>(p, shares);
   else
-    heads_kernel<T, CODE, L, kLooseHalves><<<grid, kHeadsThreads, 0, stream>>>(p, block_tokens);
+    heads_kernel<T, CODE, L, kLooseHalves><<<grid, kHeadsThreads, 0, stream>>>(p, shares);
   return cudaGetLastError();
 }
 
