@@ -27,6 +27,7 @@ constexpr int kHeadsThreads = 256;
 constexpr int kLane = 8;             // elements of a row that a lane holds
 constexpr int kMostPairs = Q8_MAX_HEAD_DIM / 2;
 constexpr int kNoCodes = 0;
+constexpr int kBlocksPerSm = 3;      // the kernel's and the grid's: each warp takes the same number of tokens, but for one
 
 // ------------------------------------------------------------------ eight values of a row
 __device__ __forceinline__ void store8(float* p, const float (&f)[kLane]) {
@@ -192,8 +193,9 @@ struct RawLane {
 // A warp takes a token, or a share of its heads where there are few tokens: 32 / L rows of one kind (queries, keys, values) at a
 // time, all of the kind's, with the angles' sines and cosines in its lanes' registers.
 template <typename T, int CODE, int L, int PAIRS>
-__global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const HeadsParams p, int shares) {
+__global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(const HeadsParams p, int shares) {
   constexpr int kRows = 32 / L;  // of a warp at a time
+  constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;  // times that, on their way beside as many that are worked on
   __shared__ float2 turned[kHeadsThreads / 32][kMostPairs];  // cosine and sine
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, chunk = lane % L, e0 = chunk * kLane;
   const bool mine = e0 < p.head_dim;
@@ -218,6 +220,15 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const HeadsPara
     const int t = shares == 1 ? (int)item : (int)(item / shares);
     const int first = shares == 1 ? 0 : (int)(item - (long long)t * shares) * per_share;
     const int end = min(units, first + per_share);
+    // The first queries are on their way while the angles are taken.
+    RawLane<T> ahead[kAhead] = {};
+    if (first < min(end, q_units)) {
+      const T* src = static_cast<const T*>(p.q.p) + t * p.q.pitch + (long long)(first * kRows + lane / L) * p.q.head_pitch + e0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (first + i < end && (first + i) * kRows + lane / L < p.q_heads && mine)
+          ahead[i].load(src + i * kRows * p.q.head_pitch);
+    }
     long long slot = -1;
     if constexpr (CODE != kNoCodes) slot = p.slots[t];
     float2 turn[kLane];  // of this lane's elements (kAdjacent: pairs, of which there are half as many)
@@ -256,97 +267,113 @@ __global__ void __launch_bounds__(kHeadsThreads, 3) heads_kernel(const HeadsPara
       const int head0 = from * kRows + lane / L;
       const T* src = static_cast<const T*>(in.p) + t * in.pitch + head0 * in.head_pitch + e0;
       T* dst = static_cast<T*>(out.p) + t * out.pitch + head0 * out.head_pitch + e0;
-      RawLane<T> ahead{};
-      if (head0 < heads && mine) ahead.load(src);
-      for (int u = from, head = head0; u < to; ++u, head += kRows) {
-        const bool live = head < heads && mine;
-        const RawLane<T> raw = ahead;
-        [[maybe_unused]] const T* here = src;
-        src += kRows * in.head_pitch;
-        if (u + 1 < to && head + kRows < heads && mine) ahead.load(src);
-        float f[kLane];
-        raw.values(f);
-        float rms = 1.0f;
-        if (kind < 2 && w) {
-          float2 two = make_float2(0.0f, 0.0f);
+      auto load = [&](int u) {
 #pragma unroll
-          for (int e = 0; e < kLane; e += 2) {
-            const float2 v = make_float2(f[e], f[e + 1]);
-            two = q8_fma2(v, v, two);
-          }
-          float sum = row_sum<L>(two.x + two.y);
-          float lift = 1.0f;
-          const bool lifted = !(sum <= 0x1p100f) || (sum < 0x1p-80f && p.eps < 0x1p-100f);
-          if (__any_sync(0xFFFFFFFFu, lifted)) {
-            if (lifted) lift = sum < 1.0f ? 0x1p100f : 0x1p-100f;
-            float again = 0.0f;
+        for (int i = 0; i < kAhead; ++i)
+          if (u + i < to && (u + i) * kRows + lane / L < heads && mine) ahead[i].load(src + i * kRows * in.head_pitch);
+        src += kAhead * kRows * in.head_pitch;
+      };
+      if (kind == 0)
+        src += kAhead * kRows * in.head_pitch;  // loaded before
+      else
+        load(from);
+      for (int u0 = from; u0 < to; u0 += kAhead) {
+        RawLane<T> raws[kAhead];
 #pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-              if (lifted) f[e] *= lift;
-              again = fmaf(f[e], f[e], again);
+        for (int i = 0; i < kAhead; ++i) raws[i] = ahead[i];
+        [[maybe_unused]] const T* here0 = src - kAhead * kRows * in.head_pitch;
+        load(u0 + kAhead);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int u = u0 + i, head = u * kRows + lane / L;
+          if (u >= to) break;
+          const bool live = head < heads && mine;
+          const RawLane<T>& raw = raws[i];
+          [[maybe_unused]] const T* here = here0 + i * kRows * in.head_pitch;
+          float f[kLane];
+          raw.values(f);
+          float rms = 1.0f;
+          if (kind < 2 && w) {
+            float2 two = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < kLane; e += 2) {
+              const float2 v = make_float2(f[e], f[e + 1]);
+              two = q8_fma2(v, v, two);
             }
-            again = row_sum<L>(again);
-            if (lifted) sum = again;
-          }
-          const float mean = fmaf(sum, one_over_dim, p.eps * lift * lift);
-          rms = mean == 0.0f ? 0.0f : rsqrtf(mean);
-          if (mine) {
-            const float2 rms2 = make_float2(rms, rms);
+            float sum = row_sum<L>(two.x + two.y);
+            float lift = 1.0f;
+            const bool lifted = !(sum <= 0x1p100f) || (sum < 0x1p-80f && p.eps < 0x1p-100f);
+            if (__any_sync(0xFFFFFFFFu, lifted)) {
+              if (lifted) lift = sum < 1.0f ? 0x1p100f : 0x1p-100f;
+              float again = 0.0f;
 #pragma unroll
-            for (int e = 0; e < kLane; e += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(&weights[kind][e0 + e]);
-              const float2 a = q8_mul2(make_float2(f[e], f[e + 1]), q8_mul2(rms2, make_float2(v.x, v.y)));
-              const float2 b = q8_mul2(make_float2(f[e + 2], f[e + 3]), q8_mul2(rms2, make_float2(v.z, v.w)));
-              f[e] = a.x, f[e + 1] = a.y, f[e + 2] = b.x, f[e + 3] = b.y;
+              for (int e = 0; e < kLane; ++e) {
+                if (lifted) f[e] *= lift;
+                again = fmaf(f[e], f[e], again);
+              }
+              again = row_sum<L>(again);
+              if (lifted) sum = again;
             }
-          }
-          rms *= lift;
-        }
-        if (kind < 2 && p.turns) {
-          if constexpr (PAIRS == kAdjacent) {
-            if (rotated) {
+            const float mean = fmaf(sum, one_over_dim, p.eps * lift * lift);
+            rms = mean == 0.0f ? 0.0f : rsqrtf(mean);
+            if (mine) {
+              const float2 rms2 = make_float2(rms, rms);
 #pragma unroll
-              for (int e = 0; e < kLane; e += 2) {
-                const float2 c = turn[e / 2];
-                const float a = f[e], b = f[e + 1];
-                f[e] = a * c.x - b * c.y;
-                f[e + 1] = b * c.x + a * c.y;
+              for (int e = 0; e < kLane; e += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(&weights[kind][e0 + e]);
+                const float2 a = q8_mul2(make_float2(f[e], f[e + 1]), q8_mul2(rms2, make_float2(v.x, v.y)));
+                const float2 b = q8_mul2(make_float2(f[e + 2], f[e + 3]), q8_mul2(rms2, make_float2(v.z, v.w)));
+                f[e] = a.x, f[e + 1] = a.y, f[e + 2] = b.x, f[e + 3] = b.y;
               }
             }
-          } else if constexpr (PAIRS == kHalves) {
-            const bool second = e0 >= half;
-            const int from_lane = lane + (rotated ? (second ? -half : half) / kLane : 0);
-#pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-              const float b = __shfl_sync(0xFFFFFFFFu, f[e], from_lane);
-              if (rotated) f[e] = fmaf(f[e], turn[e].x, b * (second ? turn[e].y : -turn[e].y));
-            }
-          } else {
-            float g[kLane];
-#pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-              g[e] = f[e];
-              const int i = e0 + e;
-              if (live && i < p.rot_dim) {
-                const int other = i < half ? i + half : i - half;
-                float b = q8_to_float(here[other - e0]);
-                if (w) b *= rms * weights[kind][other];
-                g[e] = i < half ? f[e] * turn[e].x - b * turn[e].y : f[e] * turn[e].x + b * turn[e].y;
-              }
-            }
-            __syncwarp();  // the output may be the input
-#pragma unroll
-            for (int e = 0; e < kLane; ++e) f[e] = g[e];
+            rms *= lift;
           }
+          if (kind < 2 && p.turns) {
+            if constexpr (PAIRS == kAdjacent) {
+              if (rotated) {
+#pragma unroll
+                for (int e = 0; e < kLane; e += 2) {
+                  const float2 c = turn[e / 2];
+                  const float a = f[e], b = f[e + 1];
+                  f[e] = a * c.x - b * c.y;
+                  f[e + 1] = b * c.x + a * c.y;
+                }
+              }
+            } else if constexpr (PAIRS == kHalves) {
+              const bool second = e0 >= half;
+              const int from_lane = lane + (rotated ? (second ? -half : half) / kLane : 0);
+#pragma unroll
+              for (int e = 0; e < kLane; ++e) {
+                const float b = __shfl_sync(0xFFFFFFFFu, f[e], from_lane);
+                if (rotated) f[e] = fmaf(f[e], turn[e].x, b * (second ? turn[e].y : -turn[e].y));
+              }
+            } else {
+              float g[kLane];
+#pragma unroll
+              for (int e = 0; e < kLane; ++e) {
+                g[e] = f[e];
+                const int i = e0 + e;
+                if (live && i < p.rot_dim) {
+                  const int other = i < half ? i + half : i - half;
+                  float b = q8_to_float(here[other - e0]);
+                  if (w) b *= rms * weights[kind][other];
+                  g[e] = i < half ? f[e] * turn[e].x - b * turn[e].y : f[e] * turn[e].x + b * turn[e].y;
+                }
+              }
+              __syncwarp();  // the output may be the input
+#pragma unroll
+              for (int e = 0; e < kLane; ++e) f[e] = g[e];
+            }
+          }
+          if (kind < 2) {
+            if (live && out.p) store8(dst, f);
+            dst += kRows * out.head_pitch;
+          }
+          if constexpr (CODE != kNoCodes && kind > 0)
+            write_codes<CODE, L>(kind == 2 ? p.cache.v_codes : p.cache.k_codes,
+                                 kind == 2 ? p.cache.v_scale : p.cache.k_scale, at + (long long)head * p.cache.page_size,
+                                 chunk, f, store && live);
         }
-        if (kind < 2) {
-          if (live && out.p) store8(dst, f);
-          dst += kRows * out.head_pitch;
-        }
-        if constexpr (CODE != kNoCodes && kind > 0)
-          write_codes<CODE, L>(kind == 2 ? p.cache.v_codes : p.cache.k_codes,
-                               kind == 2 ? p.cache.v_scale : p.cache.k_scale, at + (long long)head * p.cache.page_size,
-                               chunk, f, store && live);
       }
     };
     rows(std::integral_constant<int, 0>{}, first, min(end, q_units), p.q, p.q_out, p.q_weight, p.q_heads);
@@ -367,7 +394,7 @@ cudaError_t launch_heads_as(const HeadsParams& p, bool adjacent, cudaStream_t st
   const int wanted = 152 * 2 * kWarps;
   const int shares = p.tokens >= wanted ? 1 : std::min(units, (wanted + p.tokens - 1) / p.tokens);
   const long long blocks = ((long long)p.tokens * shares + kWarps - 1) / kWarps;
-  const unsigned grid = (unsigned)std::min<long long>(blocks, 152 * 8);
+  const unsigned grid = (unsigned)std::min<long long>(blocks, 152 * kBlocksPerSm);
   if (adjacent || !p.turns)
     heads_kernel<T, CODE, L, kAdjacent><<<grid, kHeadsThreads, 0, stream>>>(p, shares);
   else if (p.rot_dim % (2 * kLane) == 0)
