@@ -479,16 +479,17 @@ _LINEAR_ARGS = struct.Struct("@6P6qP4i")
 
 _value_types = {}
 _code_types = {}
-# Set by the first call: the library, torch's fp32 and its current stream's handle. These calls cost
+# Set by the first call: the library, some of torch's types and its current stream's handle. These calls cost
 # the host more than the GPU where there are few tokens, so nothing is looked up twice in them.
-_q8 = _f32 = _raw_stream = None
+_q8 = _f32 = _i32 = _i64 = _raw_stream = None
 
 
 def _q8_setup():
-    global _q8, _f32, _raw_stream
+    global _q8, _f32, _i32, _i64, _raw_stream
     import torch
     lib = load()
     _f32, _raw_stream = torch.float32, torch._C._cuda_getCurrentRawStream
+    _i32, _i64 = torch.int32, torch.int64
     _value_types.update({torch.float32: Q8_F32, torch.bfloat16: Q8_BF16, torch.float16: Q8_F16})
     _code_types.update({torch.int8: Q8_INT8, torch.uint8: Q8_E4M3, torch.float8_e4m3fn: Q8_E4M3})
     _q8 = lib
@@ -715,7 +716,7 @@ def cache_q8(k_codes, k_scale, v_codes, v_scale) -> tuple:
 
 def _heads(t, name, shape, dtype, device):
     """Address, pitch and head pitch of a matrix of heads [tokens, heads, head_dim]."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device:
+    if t.dtype != dtype or t.get_device() != device or t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)}, {dtype}, on CUDA device {device}, got "
                          f"{tuple(t.shape)}, {t.dtype}, device {t.get_device()}")
     pitch, head_pitch, step = t.stride()
@@ -725,12 +726,6 @@ def _heads(t, name, shape, dtype, device):
 
 
 _NO_HEADS = (0, 0, 0)
-
-
-def _i64(t, name, size, device):
-    """Address of a contiguous int64 vector."""
-    import torch
-    return _q8_vector(t, name, size, device, torch.int64)
 
 
 def heads_q8_run(q=None, q_out=None, k=None, k_out=None, v=None, q_weight=None, k_weight=None,
@@ -795,10 +790,9 @@ def heads_q8_run(q=None, q_out=None, k=None, k_out=None, v=None, q_weight=None, 
             raise ValueError("positions: expected with a rotary")
         shape = positions.shape
         if len(shape) == 1 and axes == 1:
-            pos = _i64(positions, "positions", tokens, device)
+            pos = _q8_vector(positions, "positions", tokens, device, _i64)
         else:
-            import torch
-            if (shape != (axes, tokens) or positions.dtype != torch.int64 or positions.get_device() != device
+            if (shape != (axes, tokens) or positions.dtype != _i64 or positions.get_device() != device
                     or (tokens > 1 and positions.stride(1) != 1)):
                 raise ValueError(f"positions: expected ({axes}, {tokens}), int64, on CUDA device {device}")
             pos, pos_pitch = positions.data_ptr(), positions.stride(0)
@@ -806,12 +800,12 @@ def heads_q8_run(q=None, q_out=None, k=None, k_out=None, v=None, q_weight=None, 
         raise ValueError("rotary: expected with positions")
     cache_ptr = slot_ptr = 0
     if cache is not None:
-        cache = getattr(cache, "parts", cache)
+        cache = cache if cache.__class__ is tuple else cache.parts
         if slots is None or v is None:
             raise ValueError("v and slots: expected with a cache")
         if cache[4] != device:
             raise ValueError(f"cache: expected one on CUDA device {device}")
-        cache_ptr, slot_ptr = cache[0], _i64(slots, "slots", tokens, device)
+        cache_ptr, slot_ptr = cache[0], _q8_vector(slots, "slots", tokens, device, _i64)
     elif slots is not None or v is not None:
         raise ValueError("cache: expected with v or slots")
     if tokens == 0:
@@ -828,12 +822,12 @@ def cache_q8_read_run(cache, slots, k, v, stream=None) -> None:
     """k and v [tokens, kv_heads, head_dim] = the cache's values at the slots [tokens] (int64); rows of
     slots outside the cache stay as they were."""
     lib = _q8 or _q8_setup()
-    cache_ptr, kv_heads, dim, _, device, _ = getattr(cache, "parts", cache)
+    cache_ptr, kv_heads, dim, _, device, _ = cache if cache.__class__ is tuple else cache.parts
     tokens = slots.shape[0]
     shape = (tokens, kv_heads, dim)
     ks, vs = _heads(k, "k", shape, k.dtype, device), _heads(v, "v", shape, k.dtype, device)
     status = lib.cache_q8_read_run(_CACHE_READ_ARGS.pack(
-        cache_ptr, _i64(slots, "slots", tokens, device), ks[0], vs[0], ks[1], ks[2], vs[1], vs[2], tokens,
+        cache_ptr, _q8_vector(slots, "slots", tokens, device, _i64), ks[0], vs[0], ks[1], ks[2], vs[1], vs[2], tokens,
         _q8_stream(stream, device), _q8_value_type(k, "k"), device))
     if status:
         _raise(status, "cache_q8_read_run")
@@ -848,10 +842,9 @@ def attn_q8_plan(max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type, d
     return h.value
 
 
-def _i32(t, name, device):
+def _q8_index(t, name, device):
     """Refuses what is not int32 on the device with contiguous rows."""
-    import torch
-    if t.dtype != torch.int32 or t.get_device() != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dtype != _i32 or t.get_device() != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name}: expected contiguous int32 on CUDA device {device}")
 
 
@@ -860,7 +853,7 @@ def attn_q8_run(plan, q, cache, table, lengths, o, scale, tokens=1, stream=None)
     table[b, s // page_size] (int32 [seqs, width]), lengths [seqs] (int32) count the newest tokens too. See
     attn_q8_run in include/q8_attention.h."""
     lib = _q8 or _q8_setup()
-    cache_ptr, _, dim, _, device, _ = getattr(cache, "parts", cache)
+    cache_ptr, _, dim, _, device, _ = cache if cache.__class__ is tuple else cache.parts
     shape = q.shape
     if len(shape) != 3 or shape[2] != dim or len(table.shape) != 2:
         raise ValueError(f"expected q [seqs * tokens, q_heads, {dim}] and table [seqs, width]")
@@ -871,8 +864,8 @@ def attn_q8_run(plan, q, cache, table, lengths, o, scale, tokens=1, stream=None)
     dtype = q.dtype
     qs = _heads(q, "q", shape, dtype, device)
     os_ = qs if o is q else _heads(o, "o", shape, dtype, device)
-    _i32(table, "table", device)
-    _i32(lengths, "lengths", device)
+    _q8_index(table, "table", device)
+    _q8_index(lengths, "lengths", device)
     status = lib.attn_q8_run(plan, _ATTN_ARGS.pack(
         cache_ptr, qs[0], os_[0], table.data_ptr(), lengths.data_ptr(), qs[1], qs[2], os_[1], os_[2], seqs, width,
         table.stride(0), _q8_stream(stream, device), tokens, shape[1], _q8_value_type(q, "q"), scale))
@@ -917,12 +910,12 @@ def attn_prompt_run(plan, q, k, v, starts, o, scale, causal=True, key_starts=Non
     ks, vs = _heads(k, "k", k_shape, dtype, device), _heads(v, "v", k_shape, dtype, device)
     if len(starts.shape) != 1 or starts.shape[0] < 1:
         raise ValueError("starts: expected [seqs + 1]")
-    _i32(starts, "starts", device)
+    _q8_index(starts, "starts", device)
     ks_ptr = 0
     if key_starts is not None:
         if key_starts.shape != starts.shape:
             raise ValueError("key_starts: expected the shape of starts")
-        _i32(key_starts, "key_starts", device)
+        _q8_index(key_starts, "key_starts", device)
         ks_ptr = key_starts.data_ptr()
     elif k_rows != rows:
         raise ValueError(f"key_starts: expected with {k_rows} rows of k and {rows} of q")

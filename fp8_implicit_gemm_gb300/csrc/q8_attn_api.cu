@@ -188,7 +188,8 @@ extern "C" conv3d_status cache_q8_read_run(const cache_q8_read_args* a) {
   if (!a || !a->cache || a->tokens < 0 || !value_type_ok(a->value_type)) return CONV3D_EINVAL;
   conv3d_status st = check_cache(a->cache);
   if (st != CONV3D_OK) return st;
-  if (a->tokens >= (1LL << 31)) return CONV3D_EUNSUPPORTED;
+  if (a->tokens >= (1LL << 31) || a->tokens / 32 * 2 * a->cache->kv_heads >= (1LL << 30))
+    return CONV3D_EUNSUPPORTED;
   const int vb = value_bytes(a->value_type), heads = a->cache->kv_heads, dim = a->cache->head_dim;
   if (a->tokens > 0 &&
       (!a->slots || !aligned(a->slots, 8) ||

@@ -437,13 +437,15 @@ template <typename T, int CODE, int L>
 __global__ void __launch_bounds__(kHeadsThreads) cache_read_kernel(const ReadParams p) {
   constexpr int kRows = kHeadsThreads / L;
   const Cache& c = p.cache;
-  const bool is_v = (int)blockIdx.y >= c.kv_heads;
-  const int head = blockIdx.y - (is_v ? c.kv_heads : 0);
+  // k and v of all heads by turns: blocks that run at the same time write neighbouring rows
+  const unsigned side = blockIdx.x % (2u * c.kv_heads), tokens = blockIdx.x / (2u * c.kv_heads);
+  const bool is_v = (int)side >= c.kv_heads;
+  const int head = side - (is_v ? c.kv_heads : 0);
   const uint8_t* codes = is_v ? c.v_codes : c.k_codes;
   const float* scales = is_v ? c.v_scale : c.k_scale;
   const Heads& out = is_v ? p.v : p.k;
   const int chunk = threadIdx.x % L;
-  const long long t0 = (long long)blockIdx.x * (kRows * kReadRows) + threadIdx.x / L;
+  const long long t0 = (long long)tokens * (kRows * kReadRows) + threadIdx.x / L;
   long long row[kReadRows];
   uint2 word[kReadRows];
   float2 scale[kReadRows];
@@ -502,7 +504,8 @@ __global__ void __launch_bounds__(kHeadsThreads) cache_read_kernel(const ReadPar
 template <typename T, int CODE>
 cudaError_t launch_read_of(const ReadParams& p, cudaStream_t stream) {
   const int lanes = p.cache.head_dim / kLane, rows = kHeadsThreads / lanes * kReadRows;
-  const dim3 grid((p.tokens + rows - 1) / rows, 2 * p.cache.kv_heads);
+  const long long blocks = ((long long)p.tokens + rows - 1) / rows * 2 * p.cache.kv_heads;
+  const unsigned grid = (unsigned)blocks;
   if (lanes == 8)
     cache_read_kernel<T, CODE, 8><<<grid, kHeadsThreads, 0, stream>>>(p);
   else if (lanes == 16)
