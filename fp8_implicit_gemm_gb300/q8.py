@@ -264,6 +264,91 @@ class PromptAttention:
             pass
 
 
+class AttentionQ8:
+    """A layer's attention on 8-bit codes and a paged cache, up to its output product:
+
+        residual += x;  a = norm(residual);  q, k, v = a * w_qkv^T, in heads;  q, k = their norms, turned;
+        k and v to the cache;  o = attention
+
+    for prompts (over their own keys in 16 bits) and for the newest tokens of running sequences (over the
+    cache): four calls of the library either way, in the caller's buffers and its own, one call at a time.
+    w_qkv [(q_heads + 2 * kv_heads) * head_dim, dim] holds the heads of q, then k's, then v's; the norms'
+    weights [head_dim] and the rotary may be missing."""
+
+    def __init__(self, norm_weight, w_qkv, q_heads, cache: CacheQ8, rotary: Rotary | None = None, q_norm=None,
+                 k_norm=None, max_rows=8192, max_seqs=256, max_tokens=1, codes=torch.int8, eps=1e-6):
+        kv, head_dim = cache.kv_heads, cache.head_dim
+        rows, dim = w_qkv.shape
+        if rows != (q_heads + 2 * kv) * head_dim or norm_weight.shape != (dim,):
+            raise ValueError(f"expected norm_weight [dim] and w_qkv [{(q_heads + 2 * kv) * head_dim}, dim], got "
+                             f"{tuple(norm_weight.shape)} and {tuple(w_qkv.shape)}")
+        norms = [w for w in (q_norm, k_norm) if w is not None]
+        if any(w.shape != (head_dim,) or w.dtype != norms[0].dtype for w in norms):
+            raise ValueError(f"expected q_norm and k_norm [{head_dim}] of one type")
+        if rotary is not None and rotary.rot_dim > head_dim:
+            raise ValueError(f"expected a rotary of up to {head_dim} elements, got {rotary.rot_dim}")
+        self.norm_weight, self.eps, self.max_rows = norm_weight, eps, max_rows
+        self.cache, self.rotary, self.q_norm, self.k_norm = cache, rotary, q_norm, k_norm
+        self.qkv = LinearQ8(*quantise_rows(w_qkv, codes), max_rows=max_rows)
+        self.newest = CacheAttention(cache, q_heads, max_seqs, max_tokens)
+        dev = w_qkv.device
+        self.prompts = PromptAttention(device=dev.index)
+        torch.cuda.current_stream(dev).synchronize()  # the codes are in place for calls on every stream
+        self._a = empty_codes(max_rows, dim, codes, dev)
+        self._scale = torch.empty(max_rows, dtype=torch.float32, device=dev)
+        self._qkv = torch.empty(max_rows, q_heads + 2 * kv, head_dim, dtype=norm_weight.dtype, device=dev)
+        self._heads, self._dim = (q_heads, kv, head_dim), dim
+
+    def _start(self, x, residual, positions, slots, o, keep_keys, stream):
+        rows, (heads, kv, head_dim) = x.shape[0], self._heads
+        if rows > self.max_rows:
+            raise ValueError(f"{rows} rows, planned for up to {self.max_rows}")
+        # what the later calls take is refused here, before the first one has updated the residual
+        device = x.get_device()
+        capi._heads(o, "o", (rows, heads, head_dim), self._qkv.dtype, device)
+        capi._q8_vector(slots, "slots", rows, device, torch.int64)
+        if self.rotary is not None:
+            want = (rows,) if self.rotary.axes == 1 and positions.dim() == 1 else (self.rotary.axes, rows)
+            if positions.shape != want or positions.dtype != torch.int64 or positions.get_device() != device:
+                raise ValueError(f"positions: expected {want}, int64, on CUDA device {device}")
+        a, scale, qkv = self._a[:rows], self._scale[:rows], self._qkv[:rows]
+        capi.rmsnorm_q8_run(x, self.norm_weight, a, scale, self.eps, residual=residual, residual_out=residual,
+                            stream=stream)
+        self.qkv(a, scale, qkv.view(rows, -1), stream)
+        q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]
+        capi.heads_q8_run(q=q, q_out=q, k=k, k_out=k if keep_keys else None, v=v, q_weight=self.q_norm,
+                          k_weight=self.k_norm, eps=self.eps, rotary=self.rotary,
+                          positions=None if self.rotary is None else positions, cache=self.cache.parts, slots=slots,
+                          stream=stream)
+        return q, k, v
+
+    def prompt(self, x, residual, starts, positions, slots, o, stream=None) -> torch.Tensor:
+        """Whole prompts, packed: x, residual [rows, dim] (residual is updated in place), starts [seqs + 1]
+        int32, positions [rows] or [axes, rows] and slots [rows] int64, o [rows, q_heads, head_dim]."""
+        capi._q8_index(starts, "starts", x.get_device())
+        q, k, v = self._start(x, residual, positions, slots, o, True, stream)
+        return self.prompts(q, k, v, starts, o, stream=stream)
+
+    def decode(self, x, residual, positions, slots, table, lengths, o, stream=None) -> torch.Tensor:
+        """The newest tokens of sequences, as many of each: x, residual [seqs * tokens, dim], table [seqs,
+        width] and lengths [seqs] int32 (the newest tokens included), the rest as for prompts."""
+        rows, seqs, device = x.shape[0], table.shape[0], x.get_device()
+        capi._q8_index(table, "table", device)
+        capi._q8_index(lengths, "lengths", device)
+        if table.dim() != 2 or lengths.shape != (seqs,) or (rows % seqs if seqs else rows):
+            raise ValueError(f"expected a table and lengths of as many sequences as divide {rows} rows")
+        q, _, _ = self._start(x, residual, positions, slots, o, False, stream)
+        return self.newest(q, table, lengths, o, stream)
+
+    def check(self) -> int:
+        statuses = [part.check() for part in (self.qkv, self.newest, self.prompts)]  # each clears what it reports
+        return next((s for s in statuses if s != capi.CONV3D_OK), capi.CONV3D_OK)
+
+    def close(self) -> None:
+        for part in (self.qkv, self.newest, self.prompts):
+            part.close()
+
+
 def _demo() -> None:
     torch.manual_seed(0)
     dim, inner, rows = 4096, 8192, 64
@@ -283,6 +368,43 @@ def _demo() -> None:
         print(f"gated MLP {dim} -> {inner} -> {dim}, {rows} tokens, {codes}: "
               f"relative error against fp32 weights {err:.4f}")
         mlp.close()
+    _demo_attention()
+
+
+def _demo_attention() -> None:
+    dim, heads, kv, head_dim, page, rows = 4096, 32, 8, 128, 64, 500
+    w = torch.randn((heads + 2 * kv) * head_dim, dim, device="cuda") / dim ** 0.5
+    weight = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(rows, dim, device="cuda").bfloat16()
+    a = x.float() * torch.rsqrt(x.float().square().mean(dim=1, keepdim=True) + 1e-6)
+    q, k, v = (a @ w.t()).view(rows, -1, head_dim).split([heads, kv, kv], dim=1)
+    angle = torch.arange(rows, device="cuda").double()[:, None] * 10000.0 ** -(
+        torch.arange(head_dim // 2, device="cuda", dtype=torch.float64) / (head_dim // 2))
+    turn = torch.polar(torch.ones_like(angle), angle)[:, None]
+
+    def turned(t):
+        z = torch.complex(*t.double().chunk(2, dim=-1)) * turn
+        return torch.cat([z.real, z.imag], dim=-1).float()
+    q, k = turned(q), turned(k)
+    score = torch.einsum("ihgd,jhd->hgij", q.view(rows, kv, -1, head_dim), k) * head_dim ** -0.5
+    score = score.masked_fill(torch.ones(rows, rows, dtype=torch.bool, device="cuda").triu(1), -torch.inf)
+    want = torch.einsum("hgij,jhd->ihgd", score.softmax(dim=-1), v).reshape(rows, heads, head_dim)
+    table = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    at = torch.arange(rows, device="cuda")
+    for codes, name in ((4, "4-bit"), (torch.int8, "int8"), (torch.float8_e4m3fn, "e4m3")):
+        cache = CacheQ8.empty(8, page, kv, head_dim, codes)
+        layer = AttentionQ8(weight, w, heads, cache, Rotary(head_dim), max_rows=rows)
+        o = torch.empty(rows, heads, head_dim, dtype=torch.bfloat16, device="cuda")
+        n = rows - 1  # the last token comes by itself, over the cache
+        starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        layer.prompt(x[:n], torch.zeros_like(x[:n]), starts, at[:n], at[:n], o[:n])
+        lengths = torch.tensor([rows], dtype=torch.int32, device="cuda")
+        layer.decode(x[n:], torch.zeros_like(x[n:]), at[n:], at[n:], table, lengths, o[n:])
+        assert layer.check() == capi.CONV3D_OK
+        prompt, newest = [float((o[s].float() - want[s]).norm() / want[s].norm()) for s in (slice(n), slice(n, rows))]
+        print(f"attention {dim} -> {heads} + 2 x {kv} heads of {head_dim}, int8 weights, {name} cache: relative "
+              f"error against fp32 {prompt:.4f} (prompt of {n}), {newest:.4f} (the next token)")
+        layer.close()
 
 
 if __name__ == "__main__":
