@@ -45,6 +45,10 @@ class LinearOptions(ctypes.Structure):
                 ("debug_flags", ctypes.c_int)]
 
 
+class AttnOptions(ctypes.Structure):
+    _fields_ = [("wait_timeout_ms", ctypes.c_int), ("debug_flags", ctypes.c_int)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("Do", ctypes.c_int), ("Ho", ctypes.c_int), ("Wo", ctypes.c_int),
                 ("npq", ctypes.c_longlong), ("k_gemm", ctypes.c_int), ("block_m", ctypes.c_int),
@@ -152,6 +156,10 @@ def load() -> ctypes.CDLL:
             lib.attn_q8_plan.argtypes = [ctypes.POINTER(vp), cq] + [ci] * 6
             lib.attn_prompt_plan.restype = ci
             lib.attn_prompt_plan.argtypes = [ctypes.POINTER(vp), ci]
+            lib.attn_q8_plan_ex.restype = ci
+            lib.attn_q8_plan_ex.argtypes = [ctypes.POINTER(vp), cq] + [ci] * 6 + [ctypes.POINTER(AttnOptions)]
+            lib.attn_prompt_plan_ex.restype = ci
+            lib.attn_prompt_plan_ex.argtypes = [ctypes.POINTER(vp), ci, ctypes.POINTER(AttnOptions)]
             for name in ("attn_q8_run", "attn_prompt_run"):
                 getattr(lib, name).restype = ci
                 getattr(lib, name).argtypes = [vp, ctypes.c_char_p]
@@ -833,12 +841,14 @@ def cache_q8_read_run(cache, slots, k, v, stream=None) -> None:
         _raise(status, "cache_q8_read_run")
 
 
-def attn_q8_plan(max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type, device=0) -> int:
+def attn_q8_plan(max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type, device=0, **options) -> int:
     """Create a plan for attention of up to max_tokens newest tokens of each of up to max_seqs sequences
-    over a cache (code_type: Q8_INT8, Q8_E4M3 or Q8_INT4); returns its handle."""
+    over a cache (code_type: Q8_INT8, Q8_E4M3 or Q8_INT4); returns its handle. Keyword options:
+    wait_timeout_ms, debug_flags; see attn_options in include/q8_attention.h."""
     h = ctypes.c_void_p()
-    _raise(load().attn_q8_plan(ctypes.byref(h), max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type,
-                               device), "attn_q8_plan")
+    o = AttnOptions(**{k: int(v) for k, v in options.items()})
+    _raise(load().attn_q8_plan_ex(ctypes.byref(h), max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type,
+                                  device, ctypes.byref(o)), "attn_q8_plan")
     return h.value
 
 
@@ -887,10 +897,11 @@ def attn_q8_destroy(plan) -> None:
         load().attn_q8_destroy(plan)
 
 
-def attn_prompt_plan(device=0) -> int:
-    """Create a plan for attention over prompts; returns its handle."""
+def attn_prompt_plan(device=0, **options) -> int:
+    """Create a plan for attention over prompts; returns its handle. Options as attn_q8_plan's."""
     h = ctypes.c_void_p()
-    _raise(load().attn_prompt_plan(ctypes.byref(h), device), "attn_prompt_plan")
+    o = AttnOptions(**{k: int(v) for k, v in options.items()})
+    _raise(load().attn_prompt_plan_ex(ctypes.byref(h), device, ctypes.byref(o)), "attn_prompt_plan")
     return h.value
 
 

@@ -16,7 +16,16 @@ struct Plan {
   int device = -1;
   uint8_t* workspace = nullptr;
   size_t bytes = 0;
+  unsigned long long timeout_ns = 0;
+  int debug_flags = 0;
 };
+
+constexpr unsigned long long kTimeoutNs = 2000ull * 1000 * 1000;
+
+void plan_options(Plan& plan, const attn_options* opts) {
+  plan.timeout_ns = opts && opts->wait_timeout_ms > 0 ? opts->wait_timeout_ms * 1000000ull : kTimeoutNs;
+  plan.debug_flags = opts ? opts->debug_flags : 0;
+}
 
 conv3d_status plan_memory(Plan& plan, int device, size_t bytes) {
   plan.device = device;
@@ -210,8 +219,15 @@ extern "C" conv3d_status cache_q8_read_run(const cache_q8_read_args* a) {
 extern "C" conv3d_status attn_q8_plan(attn_q8_plan_t* plan, long long max_seqs, int max_tokens,
                                       int q_heads, int kv_heads, int head_dim, int code_type,
                                       int device) {
+  return attn_q8_plan_ex(plan, max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type, device, nullptr);
+}
+
+extern "C" conv3d_status attn_q8_plan_ex(attn_q8_plan_t* plan, long long max_seqs, int max_tokens,
+                                         int q_heads, int kv_heads, int head_dim, int code_type,
+                                         int device, const attn_options* opts) {
   if (!plan) return CONV3D_EINVAL;
   *plan = nullptr;
+  if (opts && opts->wait_timeout_ms < 0) return CONV3D_EINVAL;
   if (max_seqs < 1 || max_tokens < 1 || q_heads < 1 || kv_heads < 1 || head_dim < 1 ||
       q_heads % kv_heads != 0 || (!code_type_ok(code_type) && code_type != Q8_INT4))
     return CONV3D_EINVAL;
@@ -228,6 +244,7 @@ extern "C" conv3d_status attn_q8_plan(attn_q8_plan_t* plan, long long max_seqs, 
   pl->kv_heads = kv_heads;
   pl->head_dim = head_dim;
   pl->code_type = code_type;
+  plan_options(*pl, opts);
   if (cudaDeviceGetAttribute(&pl->sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess ||
       cache_attn_setup(code_type, head_dim) != cudaSuccess) {
     cudaGetLastError();
@@ -277,6 +294,8 @@ extern "C" conv3d_status attn_q8_run(attn_q8_plan_t plan, const attn_q8_args* a)
   p.table_width = (int)a->table_width;
   p.scale = a->scale;
   p.status = reinterpret_cast<int*>(plan->workspace);
+  p.timeout_ns = plan->timeout_ns;
+  p.debug_flags = plan->debug_flags;
   return launched(launch_cache_attn(p, a->value_type, plan->workspace + kStatusBytes, plan->sms,
                                     static_cast<cudaStream_t>(a->stream)));
 }
@@ -292,13 +311,19 @@ extern "C" void attn_q8_destroy(attn_q8_plan_t plan) {
 }
 
 extern "C" conv3d_status attn_prompt_plan(attn_prompt_plan_t* plan, int device) {
+  return attn_prompt_plan_ex(plan, device, nullptr);
+}
+
+extern "C" conv3d_status attn_prompt_plan_ex(attn_prompt_plan_t* plan, int device, const attn_options* opts) {
   if (!plan) return CONV3D_EINVAL;
   *plan = nullptr;
+  if (opts && opts->wait_timeout_ms < 0) return CONV3D_EINVAL;
   conv3d_status st = check_device(device);
   if (st == CONV3D_OK) st = launched(prompt_attn_setup());
   if (st != CONV3D_OK) return st;
   attn_prompt_plan_s* pl = new (std::nothrow) attn_prompt_plan_s();
   if (!pl) return CONV3D_ENOMEM;
+  plan_options(*pl, opts);
   st = plan_memory(*pl, device, kStatusBytes);
   if (st != CONV3D_OK) {
     delete pl;
@@ -348,6 +373,8 @@ extern "C" conv3d_status attn_prompt_run(attn_prompt_plan_t plan, const attn_pro
   // a scale of 0 as one that leaves every finite score 0 and -inf, a masked one, -inf
   p.scale = std::fmax(std::fabs(a->scale) * 1.44269504088896f, 1e-30f);
   p.status = reinterpret_cast<int*>(plan->workspace);
+  p.timeout_ns = plan->timeout_ns;
+  p.debug_flags = plan->debug_flags;
   return launched(launch_prompt_attn(p, a->value_type, static_cast<cudaStream_t>(a->stream)));
 }
 

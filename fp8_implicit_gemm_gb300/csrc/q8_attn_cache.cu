@@ -23,8 +23,8 @@
 // the lowest values of 4-bit rows, of w * (lowest + 8 * scale_v) / scale_v, take the same w in fp32. So the cut, by d of
 // w with 0 <= d < 2^-10, weighs a key's code, lowest value and share alike, and what all keys' d have in common cancels:
 // an output errs by at most 2^-11 of sum p |v - o|. (Below 2^-14 f16 has fewer bits: the code's part of such a weight errs
-// by 2^-24 of the largest w, where that of the lowest value, which may be large beside a small scale, does not.)
-// M moves only when a w would pass 2^8 (a vote; maxima over the warp are taken then only), so w keeps its bits
+// by 2^-31 of the largest w, where that of the lowest value, which may be large beside a small scale, does not.)
+// M moves only when a w would pass 2^15 (a vote; maxima over the warp are taken then only), so w keeps its bits
 // relative to the largest one whatever v's scales are.
 //
 // Copies. Every warp has a ring of its own, filled by bulk copies of 16 rows of codes and their scales (pages
@@ -48,8 +48,10 @@ constexpr int kTile = 16;                    // keys of an instruction
 constexpr int kHeadKeys = 256;               // what a head costs beside its keys, in keys
 constexpr int kLeastShare = 128;             // of a block, where there is too little for all
 constexpr float kLowest = -1e30f;            // M before the first key
-constexpr float kLeastScale = 0x1p-100f;     // of v: a smaller one counts as this
-constexpr uint64_t kCacheTimeoutNs = 2000ull * 1000 * 1000;
+constexpr float kLeastScale = 0x1p-80f;      // of v: a smaller one counts as this
+// The largest w is 2^kHigh when M is set and 2^(kHigh + kGrowth), which f16 holds, before it is set again: so far up that those
+// next to 0 keep their bits (with the largest at 1 an f16 output of 131072 keys erred by 3.4e-4, with this by less).
+constexpr float kHigh = 7.0f, kGrowth = 8.0f;
 
 template <int CODE>
 constexpr int kScaleBytes = CODE == Q8_INT4 ? 8 : 4;
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   if (threadIdx.x == 0 && !by_head) shared_heads[blockIdx.x].last = -1;
   if ((int)blockIdx.x >= blocks) return;
 
-  const AbortState ab{&abort_flag, p.status, kCacheTimeoutNs};
+  const AbortState ab{&abort_flag, p.status, p.timeout_ns};
   const float scale_log2 = p.scale * 1.44269504088896f;
   uint32_t issued = 0, used = 0;  // this warp's copies so far
   // A tile is four copies: the codes of k and of v and their scales, by the lanes 0 to 3 (4 to 7: the second tile's).
@@ -367,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     const bool all = kTiles == 1 || (__ballot_sync(0xFFFFFFFFu, mine) >> 4) != 0;
     if (lane == 0) mbar_arrive_expect_tx(bar, all ? kStageBytes : kOneTile);
     __syncwarp();
-    if (mine) bulk_load(copy_dst + stage * kStageBytes, copy_src + place * copy_bytes, copy_bytes, bar);
+    const bool skip = (p.debug_flags & 1) && seq == 0 && head == 0 && row0 == 0 && first + i == 0;
+    if (mine && !skip) bulk_load(copy_dst + stage * kStageBytes, copy_src + place * copy_bytes, copy_bytes, bar);
     ++issued;
   };
   auto start = [&] {
@@ -553,10 +556,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
             if constexpr (kTiles == 2) m = fmaxf(m, fmaxf(s[kTiles - 1][nb][j], s[kTiles - 1][nb][2 + j]));
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
-            if (!(m > most[nb][j])) m = top[nb][j];  // a row's results do not depend on its neighbours
-            const float keep = m == top[nb][j] ? 1.0f : exp2_fast(top[nb][j] - m);
-            top[nb][j] = m;
-            most[nb][j] = m + 8.0f;
+            const bool up = m > most[nb][j];  // only then: a row's results do not depend on its neighbours
+            const float keep = up ? exp2_fast(top[nb][j] - (m - kHigh)) : 1.0f;
+            if (up) top[nb][j] = m - kHigh, most[nb][j] = m + kGrowth;
             weight[nb][j] *= keep;
             low_sum[nb][j] *= keep;
 #pragma unroll
@@ -743,7 +745,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
     }
     const bool stop = __syncthreads_or(!waited) || !more;
     if (stop) {
-      // on abort another warp may have copies of the next one under way
+      // On abort: heads that would have begun here are marked whole, so that nothing is joined for them by what an earlier
+      // run left; and another warp may have copies of the next one under way.
+      if (threadIdx.x == 0 && by_head && more) {
+        if (waited && first_group == 0) shared_heads[seq * heads + head_index].last = -1;  // the one started above
+        long long unit = before * heads + (head_index + 1) * groups;
+        if (!waited) unit = last_unit + 1;  // not started: what `seq` and `groups` still stand for is done
+        while (unit < until) {
+          if (unit >= (before + groups) * heads) before += groups, groups = groups_of<kShare>(p, ++seq);
+          shared_heads[seq * heads + divide(unit - before * heads, groups)].last = -1;
+          unit += groups;
+        }
+      }
       for (; used < issued; ++used) {
         int own = 0;
         tc_wait(bar_at + 8 * (used % kS), (used / kS) & 1, AbortState{&own, p.status, 1000000ull}, kAttnTimeout);
@@ -764,7 +777,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const Cache
   __shared__ float2 stats[kJoinWarps];  // the reference and the sum of the weights
   pdl_wait_primary();
   const SharedHead s = shared_heads[blockIdx.x];
-  if (s.last < 0) return;
+  if (s.last < 0) return;  // whole in its block, or given up
   const int group = p.q_heads / p.cache.kv_heads;
   const int rows = kRows / gridDim.y, at_once = min(rows, kJoinWarps), share = kJoinWarps / at_once;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, mine = warp % share;

@@ -58,6 +58,8 @@ struct CacheAttnParams {
   int seqs, tokens, q_heads, table_width;
   float scale;
   int* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
 };
 // Bytes that the runs of a plan need for the sums of heads that several blocks share.
 size_t cache_attn_workspace(int sms, int tokens, int q_heads, int kv_heads, int dim);
@@ -71,6 +73,8 @@ struct PromptParams {
   int negate;            // the scale is negative
   float scale;           // its magnitude times log2(e)
   int* status;
+  unsigned long long timeout_ns;
+  int debug_flags;
 };
 cudaError_t prompt_attn_setup();       // the kernels' shared-memory grant on this device
 cudaError_t launch_prompt_attn(const PromptParams& p, int value_type, cudaStream_t stream);

@@ -9,8 +9,8 @@
 // says that PV_A(j) is done too; products of one thread run in the order of their issue, so QK may overwrite the P that
 // PV before it reads.
 //
-// m lags behind: O and l are scaled only when a row's maximum has grown by more than 2^8 over m (P stays below 2^8 and keeps
-// its bits), which is rare after the first keys; the row's thread then rescales O in TMEM.
+// m lags behind: O and l are scaled only when a row's maximum has grown by more than 2^8 over m (P is 2^7 there and stays below
+// 2^15, so that f16 holds the largest and the small ones keep their bits), which is rare after the first keys; the row's thread then rescales O in TMEM.
 //
 // What a row does not see. A masked score is -inf, its weight 0; but 0 times a value that is not finite is NaN, so the tiles
 // that some row sees only in part (the last ones of a block) pass two more warps, which zero such values in shared
@@ -39,7 +39,8 @@ constexpr uint32_t kHalfBytes = 128 * 128;   // 64 channels of a tile: 128 rows 
 constexpr int kPromptSlots = 5;              // tiles of k and v under way
 constexpr float kNone = -1e30f;              // m before the first key
 constexpr float kGrowth = 8.0f;              // of a maximum, as a power of two, before O follows
-constexpr uint64_t kPromptTimeoutNs = 2000ull * 1000 * 1000, kSettleNs = 2ull * 1000 * 1000;
+constexpr float kHigh = 7.0f;                // P of the maximum, as a power of two: f16 has bits for small ones then
+constexpr uint64_t kSettleNs = 2ull * 1000 * 1000;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256, kColTile = 128;
 
 template <int HALVES>
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   volatile int* abort_flag = &abort_word;
-  const AbortState ab{abort_flag, p.status, kPromptTimeoutNs};
+  const AbortState ab{abort_flag, p.status, p.timeout_ns};
   auto q_at = [&](int t) { return base + t * kTileBytes<HALVES>; };
   auto slot_at = [&](uint32_t i) { return base + (2 + i % kPromptSlots) * kTileBytes<HALVES>; };
   auto full = [&](uint32_t i) { return bar(kBarFull + i % kPromptSlots); };
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           l.y *= keep;
           m = now;
         }
-        const float neg = m == kNone ? 0.0f : -m * p.scale;
+        const float neg = m == kNone ? 0.0f : fmaf(-m, p.scale, kHigh);
         const float2 scale2 = make_float2(p.scale, p.scale), neg2 = make_float2(neg, neg);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // every product is complete before TMEM is released
     if (elect_one()) mma_commit(bar(kBarDrain));
     __syncwarp();
-    wait_drain(bar(kBarDrain), 0, kPromptTimeoutNs, p.status, kAttnTimeout);
+    wait_drain(bar(kBarDrain), 0, p.timeout_ns, p.status, kAttnTimeout);
   } else if (warp == kTmaWarp) {
     // ------------------------------------------------------------------------------ units and copies
     // Units of all sequences are counted from the last one, which has the most keys, heads first; there is a block for each
@@ -446,23 +447,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return false;
     };
     uint32_t copies = 0, with_tiles = 0;
-    uint32_t block = blockIdx.x;
+    uint32_t block = blockIdx.x, asked = 0;
+    bool first = true;  // this block's own
     for (int n = 0;; ++n) {
-      bool some = true;
-      if (n > 0) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(kBarBlock), 16);
-          ask_for_block(smem_u32(&answer), bar(kBarBlock));
-        }
-        __syncwarp();
-        if (!tc_wait(bar(kBarBlock), (n - 1) & 1, ab, kAttnTimeout)) break;
-        some = answered_block(smem_u32(&answer), block);
-        fence_proxy_async_smem();  // the next answer comes to the same place
-        __syncwarp();
-      }
+      // The next block that has a unit (those behind the last unit have none: they are taken over here one after another,
+      // where it is known that there are no more).
       PromptUnit u;
       u.poison = 0;
-      u.head = some && find(block / p.q_heads, u) ? (int)(block % p.q_heads) : -1;
+      u.head = -1;
+      bool answered = true;
+      for (bool some = true; some; first = false) {
+        if (!first) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kBarBlock), 16);
+            ask_for_block(smem_u32(&answer), bar(kBarBlock));
+          }
+          __syncwarp();
+          answered = tc_wait(bar(kBarBlock), asked++ & 1, ab, kAttnTimeout);
+          some = answered && answered_block(smem_u32(&answer), block);
+          fence_proxy_async_smem();  // the next answer comes to the same place
+          __syncwarp();
+        }
+        if (some && find(block / p.q_heads, u)) {
+          u.head = (int)(block % p.q_heads);
+          first = false;
+          break;
+        }
+      }
+      if (!answered) break;
       if (u.head >= 0) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -498,7 +510,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const uint32_t to =
               i % 2 && i / 2 >= u.checked_from ? bar(kBarRaw + kMostChecked * (n % 2) + i / 2 - u.checked_from) : full(c);
           mbar_arrive_expect_tx(to, kTileBytes<HALVES>);
-          for (int h = 0; h < HALVES; ++h)
+          const bool skip = (p.debug_flags & 1) && blockIdx.x == 0 && c == 0;
+          for (int h = skip ? HALVES : 0; h < HALVES; ++h)
             tma_load_3d(slot_at(c) + h * kHalfBytes, i % 2 ? &vmap : &kmap, to, 64 * h, kv_head, u.k0 + (i / 2) * kKeys);
         }
         __syncwarp();

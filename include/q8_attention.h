@@ -119,10 +119,13 @@ conv3d_status cache_q8_read_run(const cache_q8_read_args *args);
  * over s < lengths[b] - tokens + 1 + t for token t (0 <= t < tokens) of sequence b, whose row is b *
  * tokens + t of q and o; head h of q reads head h / (q_heads / kv_heads) of the cache. A token that
  * sees nothing (a length below tokens - t) gets 0. The place s of sequence b is page table[b][s /
- * page_size]. A cached row whose scale is NaN makes every output that sees it NaN. Codes and q are multiplied in f16, where
- * codes are exact and a row of q, scaled to 1 by a power of two, errs by at most 2^-12 of each element (2^-25 of the
- * row's largest below 2^-14 of it); p is rounded to f16 beside v's scale; sums, maxima and scales are fp32. Scales of v
- * below 2^-100 count as 2^-100.
+ * page_size]. A cached row whose scale is NaN makes every output that sees it NaN, and no other.
+ *
+ * Codes and q are multiplied in f16, where codes are exact and a row of q, scaled by a power of two, is too
+ * but for elements below 2^-22 of the row's largest, which err by 2^-33 of that. A weight times v's scale is cut to
+ * f16's 11 bits, the same for all that is made of it (an output errs by at most 2^-11 of sum p |v - o|; codes of
+ * weights below 2^-21 of the largest by 2^-31 of it); sums, maxima and scales are fp32. Scales of v below 2^-80
+ * count as 2^-80. Results are the same from run to run.
  *
  * A plan holds the device's workspace: a status word and the partial results of sequences that several blocks share,
  * fixed by q_heads, kv_heads, max_tokens and head_dim, whatever the lengths. At most one run of a plan may be in
@@ -131,11 +134,22 @@ conv3d_status cache_q8_read_run(const cache_q8_read_args *args);
  */
 typedef struct attn_q8_plan_s *attn_q8_plan_t; /* opaque, owned by the library */
 
+/* Optional planning knobs of both attentions; none changes what is computed. Zero-initialise. */
+typedef struct {
+    int wait_timeout_ms; /* 0: 2000 ms; a bounded wait inside a kernel gives up after this long */
+    int debug_flags;     /* test-only: bit 0 leaves out the copy of the first sequence's first keys (for prompts: the
+                            first block's first copy), so that the waits on it must run out (exercises the error path without faulting anything) */
+} attn_options;
+
 /* Errors: EINVAL (a size below 1, q_heads no multiple of kv_heads, an unknown code type), EUNSUPPORTED (a head_dim
  * other than 64, 128 and 256, max_seqs above 65536, max_tokens above 64, q_heads of 4096 or more, a device that is
  * not sm_103), ENOMEM, ECUDA. On error *plan is set to NULL. */
 conv3d_status attn_q8_plan(attn_q8_plan_t *plan, long long max_seqs, int max_tokens, int q_heads,
                            int kv_heads, int head_dim, int code_type, int device);
+/* With planning knobs (opts may be NULL; EINVAL for a negative timeout). */
+conv3d_status attn_q8_plan_ex(attn_q8_plan_t *plan, long long max_seqs, int max_tokens, int q_heads,
+                              int kv_heads, int head_dim, int code_type, int device,
+                              const attn_options *opts);
 
 /* Errors: EINVAL (a NULL pointer with seqs > 0, seqs < 0 or above max_seqs, tokens outside 1 .. max_tokens, a cache
  * that does not fit the plan, q and o not bf16 or f16 on 16 bytes with pitches of whole 16 bytes, table_pitch below
@@ -180,6 +194,7 @@ typedef struct attn_prompt_plan_s *attn_prompt_plan_t; /* opaque, owned by the l
 
 /* Errors: EINVAL (`device` not the current one), EUNSUPPORTED (not an sm_103), ENOMEM, ECUDA. */
 conv3d_status attn_prompt_plan(attn_prompt_plan_t *plan, int device);
+conv3d_status attn_prompt_plan_ex(attn_prompt_plan_t *plan, int device, const attn_options *opts);
 
 /* Errors: EINVAL (a NULL pointer with seqs, q_rows > 0, sizes below 1 or negative, q_heads no multiple of kv_heads, value_type not bf16 or f16,
  * matrices that are not on 16 bytes, pitches that are no whole 16 bytes or make rows overlap, scale not finite, the wrong

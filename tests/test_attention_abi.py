@@ -24,9 +24,9 @@ def lib():
 def test_library_exports_every_declared_symbol(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = set(re.findall(r"\b((?:heads|cache|attn)_[a-z0-9_]+)\s*\(", text))
-    assert {"heads_q8_run", "cache_q8_read_run", "attn_q8_plan", "attn_q8_run", "attn_q8_check",
-            "attn_q8_workspace_size", "attn_q8_destroy", "attn_prompt_plan", "attn_prompt_run",
-            "attn_prompt_check", "attn_prompt_destroy"} == names
+    assert {"heads_q8_run", "cache_q8_read_run", "attn_q8_plan", "attn_q8_plan_ex", "attn_q8_run", "attn_q8_check",
+            "attn_q8_workspace_size", "attn_q8_destroy", "attn_prompt_plan", "attn_prompt_plan_ex",
+            "attn_prompt_run", "attn_prompt_check", "attn_prompt_destroy"} == names
     for n in names:
         assert hasattr(lib, n), n
 
@@ -138,6 +138,9 @@ def test_plans_refuse(lib):
         assert lib.attn_q8_plan(ctypes.byref(h), *args, 0) == capi.CONV3D_EUNSUPPORTED
     assert lib.attn_q8_plan(None, 1, 1, 4, 2, 64, 1, 0) == capi.CONV3D_EINVAL
     assert lib.attn_prompt_plan(None, 0) == capi.CONV3D_EINVAL
+    o = capi.AttnOptions(wait_timeout_ms=-1)
+    assert lib.attn_prompt_plan_ex(ctypes.byref(h), 0, ctypes.byref(o)) == capi.CONV3D_EINVAL
+    assert lib.attn_q8_plan_ex(ctypes.byref(h), 1, 1, 4, 2, 64, 1, 0, ctypes.byref(o)) == capi.CONV3D_EINVAL
 
 
 def test_null_arguments(lib):
