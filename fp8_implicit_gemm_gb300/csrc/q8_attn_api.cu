@@ -149,7 +149,7 @@ extern "C" conv3d_status heads_q8_run(const heads_q8_args* a) {
     const int vb = value_bytes(a->value_type), dim = a->head_dim;
     const int wb = a->q_weight || a->k_weight ? value_bytes(a->weight_type) : 1;
     if (a->turns && (!a->positions || !aligned(a->positions, 8) ||
-                     (a->axes > 1 && a->positions_pitch < a->tokens)))
+                     (a->axes > 1 && a->positions_pitch != 0 && a->positions_pitch < a->tokens)))
       return CONV3D_EINVAL;
     if (!aligned(a->q_weight, wb) || !aligned(a->k_weight, wb) || !aligned(a->slots, 8))
       return CONV3D_EINVAL;

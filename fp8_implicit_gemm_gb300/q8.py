@@ -287,6 +287,8 @@ class AttentionQ8:
             raise ValueError(f"expected q_norm and k_norm [{head_dim}] of one type")
         if rotary is not None and rotary.rot_dim > head_dim:
             raise ValueError(f"expected a rotary of up to {head_dim} elements, got {rotary.rot_dim}")
+        if norm_weight.dtype not in (torch.bfloat16, torch.float16):  # the heads' type, which attention takes
+            raise ValueError(f"expected a norm_weight of bfloat16 or float16, got {norm_weight.dtype}")
         self.norm_weight, self.eps, self.max_rows = norm_weight, eps, max_rows
         self.cache, self.rotary, self.q_norm, self.k_norm = cache, rotary, q_norm, k_norm
         self.qkv = LinearQ8(*quantise_rows(w_qkv, codes), max_rows=max_rows)
@@ -297,7 +299,7 @@ class AttentionQ8:
         self._a = empty_codes(max_rows, dim, codes, dev)
         self._scale = torch.empty(max_rows, dtype=torch.float32, device=dev)
         self._qkv = torch.empty(max_rows, q_heads + 2 * kv, head_dim, dtype=norm_weight.dtype, device=dev)
-        self._heads, self._dim = (q_heads, kv, head_dim), dim
+        self._heads, self._dim, self._newest = (q_heads, kv, head_dim), dim, (max_seqs, max_tokens)
 
     def _start(self, x, residual, positions, slots, o, keep_keys, stream):
         rows, (heads, kv, head_dim) = x.shape[0], self._heads
@@ -305,11 +307,17 @@ class AttentionQ8:
             raise ValueError(f"{rows} rows, planned for up to {self.max_rows}")
         # what the later calls take is refused here, before the first one has updated the residual
         device = x.get_device()
-        capi._heads(o, "o", (rows, heads, head_dim), self._qkv.dtype, device)
+        address, pitch, head_pitch = capi._heads(o, "o", (rows, heads, head_dim), self._qkv.dtype, device)
+        pitch, head_pitch = pitch if rows > 1 else heads * head_pitch, head_pitch if heads > 1 else head_dim
+        apart = (pitch >= (heads - 1) * head_pitch + head_dim and head_pitch >= head_dim
+                 or head_pitch >= (rows - 1) * pitch + head_dim and pitch >= head_dim)
+        if rows and (address % 16 or pitch % 8 or head_pitch % 8 or not apart):
+            raise ValueError("o: expected heads on 16 bytes that do not overlap")
         capi._q8_vector(slots, "slots", rows, device, torch.int64)
         if self.rotary is not None:
             want = (rows,) if self.rotary.axes == 1 and positions.dim() == 1 else (self.rotary.axes, rows)
-            if positions.shape != want or positions.dtype != torch.int64 or positions.get_device() != device:
+            if (positions.shape != want or positions.dtype != torch.int64 or positions.get_device() != device
+                    or (rows > 1 and positions.stride(-1) != 1) or (positions.dim() == 2 and 0 < positions.stride(0) < rows)):
                 raise ValueError(f"positions: expected {want}, int64, on CUDA device {device}")
         a, scale, qkv = self._a[:rows], self._scale[:rows], self._qkv[:rows]
         capi.rmsnorm_q8_run(x, self.norm_weight, a, scale, self.eps, residual=residual, residual_out=residual,
@@ -326,6 +334,8 @@ class AttentionQ8:
         """Whole prompts, packed: x, residual [rows, dim] (residual is updated in place), starts [seqs + 1]
         int32, positions [rows] or [axes, rows] and slots [rows] int64, o [rows, q_heads, head_dim]."""
         capi._q8_index(starts, "starts", x.get_device())
+        if starts.dim() != 1 or not 1 <= starts.shape[0] <= 65537:
+            raise ValueError(f"starts: expected [seqs + 1] of up to 65536 sequences, got {tuple(starts.shape)}")
         q, k, v = self._start(x, residual, positions, slots, o, True, stream)
         return self.prompts(q, k, v, starts, o, stream=stream)
 
@@ -337,6 +347,11 @@ class AttentionQ8:
         capi._q8_index(lengths, "lengths", device)
         if table.dim() != 2 or lengths.shape != (seqs,) or (rows % seqs if seqs else rows):
             raise ValueError(f"expected a table and lengths of as many sequences as divide {rows} rows")
+        if seqs > self._newest[0] or rows > seqs * self._newest[1] or (seqs and (rows < seqs or table.shape[1] < 1)):
+            raise ValueError(f"expected up to {self._newest[0]} sequences of 1 to {self._newest[1]} rows and a page, got "
+                             f"{rows} rows and a table {tuple(table.shape)}")
+        if seqs > 1 and table.stride(0) < table.shape[1]:
+            raise ValueError("table: expected rows that do not overlap")
         q, _, _ = self._start(x, residual, positions, slots, o, False, stream)
         return self.newest(q, table, lengths, o, stream)
 

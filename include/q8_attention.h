@@ -64,10 +64,10 @@ typedef struct {
  *
  * Errors: EINVAL (nothing to do: neither q nor k; an input without its output or the reverse; v or slots without a
  * cache, or a cache without k, v and slots; sizes below 1, tokens < 0, rot_dim above head_dim or odd, axes outside
- * 1 .. Q8_MAX_AXES, positions missing where turns are there, an axis list missing with more than one axis, a pitch or
- * head pitch that makes rows overlap or is not a multiple of 16 bytes, matrices that are not on 16 bytes,
- * vectors that are not aligned to their element, eps negative or not finite, an unknown type, a cache
- * whose kv_heads or head_dim differ, page_size not a multiple of 16; `device` not the current one),
+ * 1 .. Q8_MAX_AXES, positions missing where turns are there or with rows that overlap (but for a pitch of 0), an axis
+ * list missing with more than one axis, a pitch or head pitch that makes rows overlap or is not a multiple of 16 bytes,
+ * matrices that are not on 16 bytes, vectors that are not aligned to their element, eps negative or not finite, an
+ * unknown type, a cache whose kv_heads or head_dim differ, page_size not a multiple of 16; `device` not the current one),
  * EUNSUPPORTED (head_dim not a multiple of 8 or above Q8_MAX_HEAD_DIM; with a cache other than 64, 128 and 256;
  * tokens of 2^31 or more, heads of 2^16 or more, a cache of 2^31 slots or more, a device that is not sm_103), ECUDA.
  * tokens == 0 does nothing. axis[j] >= axes is taken as axis 0.
@@ -86,7 +86,7 @@ typedef struct {
     const q8_cache *cache;      /* NULL: none. Read by the call, not kept */
     long long q_pitch, q_head_pitch, q_out_pitch, q_out_head_pitch;
     long long k_pitch, k_head_pitch, k_out_pitch, k_out_head_pitch, v_pitch, v_head_pitch;
-    long long positions_pitch;  /* between axes */
+    long long positions_pitch;  /* between axes; 0: all axes have one row of positions */
     long long tokens;
     void *stream;
     int q_heads, kv_heads, head_dim, rot_dim, axes, adjacent;
@@ -138,7 +138,8 @@ typedef struct attn_q8_plan_s *attn_q8_plan_t; /* opaque, owned by the library *
 typedef struct {
     int wait_timeout_ms; /* 0: 2000 ms; a bounded wait inside a kernel gives up after this long */
     int debug_flags;     /* test-only: bit 0 leaves out the copy of the first sequence's first keys (for prompts: the
-                            first block's first copy), so that the waits on it must run out (exercises the error path without faulting anything) */
+                            first block's first copy), so that the waits on it must run out (exercises the error path
+                            without faulting anything) */
 } attn_options;
 
 /* Errors: EINVAL (a size below 1, q_heads no multiple of kv_heads, an unknown code type), EUNSUPPORTED (a head_dim

@@ -141,3 +141,40 @@ def test_refusals_leave_the_residual():
 
 def test_demo_runs():
     q8._demo_attention()
+
+
+def test_what_attention_would_refuse_leaves_the_residual():
+    block = layer("i8", max_rows=16)
+    x, residual = randn(8, DIM, dtype=torch.bfloat16, seed=5), randn(8, DIM, dtype=torch.bfloat16, seed=6)
+    before, at = residual.clone(), torch.arange(8, device="cuda")
+    starts = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    o = torch.empty(8, HEADS, HEAD, dtype=torch.bfloat16, device="cuda")
+    spare = torch.empty(8 * HEADS * HEAD + 8, dtype=torch.bfloat16, device="cuda")
+    outputs = (spare[1:1 + o.numel()].view(o.shape), spare.as_strided(o.shape, (HEADS * HEAD - 1, HEAD, 1)),
+               o[:1].expand(o.shape), o[:, :1].expand(o.shape), spare.as_strided(o.shape, (HEAD, HEAD, 1)))
+    for bad in ((starts[:0], at, at, o), (starts[None], at, at, o), *((starts, at, at, out) for out in outputs),
+                (starts, torch.arange(16, device="cuda")[::2], at, o)):
+        with pytest.raises(ValueError):
+            block.prompt(x, residual, *bad)
+
+    def table(seqs, width=1):
+        return torch.zeros(seqs, width, dtype=torch.int32, device="cuda"), torch.ones(seqs, dtype=torch.int32, device="cuda")
+    for t, n in (table(8), table(2), table(1), table(4, 0)):  # too many sequences, too many tokens, twice, no pages
+        with pytest.raises(ValueError):
+            block.decode(x, residual, at, at, t, n, o)
+    with pytest.raises(ValueError):
+        block.decode(x, residual, at, at, table(1, 2)[0].expand(4, 2), table(4)[1], o)
+    assert torch.equal(residual, before) and block.check() == capi.CONV3D_OK
+    with pytest.raises(ValueError):
+        q8.AttentionQ8(block.norm_weight.float(), randn((HEADS + 2 * KV) * HEAD, DIM), HEADS, block.cache)
+
+
+def test_outputs_with_heads_ahead_of_tokens():
+    """An output in the order [heads, tokens], and positions that all axes share."""
+    x, residual = randn(8, DIM, dtype=torch.bfloat16, seed=5), randn(8, DIM, dtype=torch.bfloat16, seed=6)
+    at, starts = torch.arange(8, device="cuda"), torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    o = torch.empty(8, HEADS, HEAD, dtype=torch.bfloat16, device="cuda")
+    other = torch.empty(HEADS, 8, HEAD, dtype=torch.bfloat16, device="cuda")
+    layer("i8", axes=3).prompt(x, residual.clone(), starts, at.expand(3, 8).contiguous(), at, o)
+    layer("i8", axes=3).prompt(x, residual.clone(), starts, at.expand(3, 8), at, other.transpose(0, 1))
+    assert torch.equal(o, other.transpose(0, 1)) and bool(torch.isfinite(o).all())
