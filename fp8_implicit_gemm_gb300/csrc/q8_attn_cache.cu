@@ -18,12 +18,15 @@
 // would be cut at 2^-14 of a code: the instruction does not normalise them. An int8 code's byte under the exponent of
 // 1024, minus 1152; e4m3 by its conversion.
 //
-// Softmax. A warp takes 16 or 32 keys at a time and keeps one reference M for each row of q. The weights that meet codes have v's
-// scale in them, w = 2^(x + log2 scale_v - M), cut to f16's bits; the sum of the weights alone, of w / scale_v, and that of
-// the lowest values of 4-bit rows, of w * (lowest + 8 * scale_v) / scale_v, take the same w in fp32. So the cut, by d of
-// w with 0 <= d < 2^-10, weighs a key's code, lowest value and share alike, and what all keys' d have in common cancels:
-// an output errs by at most 2^-11 of sum p |v - o|. (Below 2^-14 f16 has fewer bits: the code's part of such a weight errs
-// by 2^-31 of the largest w, where that of the lowest value, which may be large beside a small scale, does not.)
+// Softmax. A warp takes 16 or 32 keys at a time and keeps one reference M for each row of q. The weights that meet codes have
+// v's scale in them, w = 2^(x + log2 scale_v - M); the sum of the weights alone, of w / scale_v, and that of the lowest values
+// of 4-bit rows, of w * (lowest + 8 * scale_v) / scale_v, are fp32. For bf16 outputs w is cut to f16's bits, for all
+// three alike: the cut, by d of w with 0 <= d < 2^-10, weighs a key's code, lowest value and share alike, and what all keys' d
+// have in common cancels, so that an output errs by at most 2^-11 of sum p |v - o|, a fourth of its rounding. (Below 2^-14 f16
+// has fewer bits: the code's part of such a weight errs by 2^-31 of the largest w, where that of the lowest value, which
+// may be large beside a small scale, does not.) An f16 output shows that much (3.3e-4 instead of 2.1e-4 of the norm, 131072
+// keys of int8), so there the rest of w is a second part and product: 64 sequences of up to 8192 keys
+// take 102.8 us instead of 101.4 (int8), 124 instead of 119 (e4m3), 89.6 instead of 83.5 (4 bits).
 // M moves only when a w would pass 2^15 (a vote; maxima over the warp are taken then only), so w keeps its bits
 // relative to the largest one whatever v's scales are.
 //
@@ -50,7 +53,7 @@ constexpr int kLeastShare = 128;             // of a block, where there is too l
 constexpr float kLowest = -1e30f;            // M before the first key
 constexpr float kLeastScale = 0x1p-80f;      // of v: a smaller one counts as this
 // The largest w is 2^kHigh when M is set and 2^(kHigh + kGrowth), which f16 holds, before it is set again: so far up that those
-// next to 0 keep their bits (with the largest at 1 an f16 output of 131072 keys erred by 3.4e-4, with this by less).
+// next to 0 keep their bits.
 constexpr float kHigh = 7.0f, kGrowth = 8.0f;
 
 template <int CODE>
@@ -250,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   constexpr int kStep = kStepKeys<CODE, D, NB>, kOneTile = kTileBytes<CODE, D>, kStageBytes = kTiles * kOneTile;
   constexpr int kKeyWords = kRowBytes<CODE, D> / 16, kValueWords = kRowBytes<CODE, D> / 32;
   constexpr int kShare = kGroup<CODE, D, NB>;
+  constexpr bool kTwoParts = std::is_same_v<T, __half>;  // of a weight: an f16 output shows what one leaves out
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
   const Cache& c = p.cache;
   const int group = p.q_heads / c.kv_heads, rows_all = p.tokens * group;
@@ -568,14 +572,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
 #pragma unroll
       for (int u = 0; u < kTiles; ++u) {
         uint32_t p_frag[NB][2];
+        [[maybe_unused]] uint32_t p_rest[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float x0 = s[u][nb][2 * j], x1 = s[u][nb][2 * j + 1];
-            const float w0 = f16_bits(exp2_fast(x0 - top[nb][0])), w1 = f16_bits(exp2_fast(x1 - top[nb][1]));
-            const __half2 h = __floats2half2_rn(w0, w1);
+            float w0 = exp2_fast(x0 - top[nb][0]), w1 = exp2_fast(x1 - top[nb][1]);
+            const float cut0 = f16_bits(w0), cut1 = f16_bits(w1);
+            const __half2 h = __floats2half2_rn(cut0, cut1);
             p_frag[nb][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h));
+            if constexpr (kTwoParts) {
+              const __half2 rest = __floats2half2_rn(w0 - cut0, w1 - cut1);
+              p_rest[nb][j] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&rest));
+            } else {
+              w0 = cut0, w1 = cut1;
+            }
             // a key that a row does not see may be marked NaN
             const bool see0 = !kMasked || x0 != -INFINITY, see1 = !kMasked || x1 != -INFINITY;
             if (see0) weight[nb][0] = fmaf(w0, v_inv[u][j], weight[nb][0]);
@@ -609,8 +621,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
                 const uint32_t m[4] = {int4_signed<false>(lo), int4_signed<true>(lo), int4_signed<false>(hi),
                                        int4_signed<true>(hi)};
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
+                for (int nb = 0; nb < NB; ++nb) {
                   mma_f16(o[nb][4 * w + 2 * half + i], m, p_frag[nb][0], p_frag[nb][1]);
+                  if constexpr (kTwoParts) mma_f16(o[nb][4 * w + 2 * half + i], m, p_rest[nb][0], p_rest[nb][1]);
+                }
                 lo >>= 8, hi >>= 8;
               }
             }
@@ -629,7 +643,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
               }
               const uint32_t m[4] = {hl[0], hl[1], hh[0], hh[1]};
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][2 * w + half], m, p_frag[nb][0], p_frag[nb][1]);
+              for (int nb = 0; nb < NB; ++nb) {
+                mma_f16(o[nb][2 * w + half], m, p_frag[nb][0], p_frag[nb][1]);
+                if constexpr (kTwoParts) mma_f16(o[nb][2 * w + half], m, p_rest[nb][0], p_rest[nb][1]);
+              }
             }
           }
         }
