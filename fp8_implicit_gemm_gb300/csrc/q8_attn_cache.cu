@@ -53,7 +53,7 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 16;                    // keys of an instruction
 constexpr int kHeadKeys = 256;               // what a head costs beside its keys, in keys
 constexpr int kLeastShare = 128;             // of a block, where there is too little for all
-constexpr float kLowest = -1e30f;            // M before the first key
+constexpr float kLowest = -3.4028235e38f;    // M before the first key
 constexpr float kLeastScale = 0x1p-80f;      // of v: a smaller one counts as this
 // The largest w is 2^kHigh when M is set and 2^(kHigh + kGrowth), which f16 holds, before it is set again: so far up that those
 // next to 0 keep their bits.
@@ -565,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
             for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, w));
             const bool up = m > most[nb][j];  // only then: a row's results do not depend on its neighbours
             const float keep = up ? exp2_fast(top[nb][j] - (m - kHigh)) : 1.0f;
-            if (up) top[nb][j] = m - kHigh, most[nb][j] = m + kGrowth;
+            // (rounded down: beside a score of 2^26 a step is 8, and w would pass f16's range)
+            if (up) top[nb][j] = m - kHigh, most[nb][j] = __fadd_rd(top[nb][j], kHigh + kGrowth);
             weight[nb][j] *= keep;
             low_sum[nb][j] *= keep;
 #pragma unroll

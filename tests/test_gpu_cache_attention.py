@@ -255,3 +255,34 @@ def test_refusals():
         attend(off, table, n, o)
     with pytest.raises(capi.Conv3dFp8Error):
         attend(torch.cat([q, q]), table, n, torch.cat([o, o]))  # two tokens, planned for one
+
+
+@pytest.mark.parametrize("codes", CODES)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("b", [2.0 ** 11, 2.0 ** 13, 2.0 ** 15, 2.0 ** 30, 2.0 ** 95])
+def test_scores_far_apart(codes, dtype, sign, b):
+    """Key j scores sign * b * (j + 1) * 2^13 or more, so the last one has all the weight, or the first: the output is its
+    value, off by its rounding to 16 bits and a few steps of fp32 of what the value is made of."""
+    lengths, kv, dim = [1, 16, 100, 900], 2, 64
+    cache, table, n, q = problem(codes, lengths, 1, 4, kv, dim, 16, dtype)
+    q.zero_()
+    q[..., 0] = sign * 2.0 ** 15
+    one = {"i4": 0x01, "i8": 0x01, "e4m3": 0x38}[codes]
+    cache.k_codes.view(torch.uint8).zero_()
+    cache.k_codes.view(torch.uint8)[..., 0] = one
+    for t, length in zip(table, lengths):
+        at = torch.arange(t.numel() * 16, device="cuda").view(-1, 1, 16).expand(-1, kv, -1)
+        scale = b * (at + 1).float()
+        cache.k_scale[t.long()] = torch.stack([scale, torch.zeros_like(scale)], dim=-1) if codes == "i4" else scale
+    attend = q8.CacheAttention(cache, 4, max_seqs=4)
+    o = attend(q, table, n, torch.full_like(q, 7.0))
+    assert attend.check() == capi.CONV3D_OK
+    v64 = values64(cache, "v", codes)
+    for i, length in enumerate(lengths):
+        at = length - 1 if sign > 0 else 0
+        want = v64[int(table[i, at // 16]), :, at % 16].repeat_interleave(2, dim=0)
+        size = cache.v_scale[int(table[i, at // 16]), :, at % 16].double().abs().reshape(kv, -1)
+        size = (size[:, 0] * (16 if codes == "i4" else 1) + size[:, -1]).repeat_interleave(2)[:, None]
+        bound = want.abs() * torch.finfo(dtype).eps / 2 + (want.abs() + size) * 2.0 ** -20 + torch.finfo(dtype).smallest_normal * 2.0 ** -10
+        assert bool(((o[i].double() - want).abs() <= bound).all()), length

@@ -239,3 +239,36 @@ def test_none_and_refusals():
     wide = randn(10, 2, 136, dtype=torch.bfloat16, seed=1)
     with pytest.raises(capi.Conv3dFp8Error):
         attend(wide, wide, wide, starts, torch.empty_like(wide))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,a,b", [(torch.float16, 6e4, 256.0), (torch.float16, -6e4, 256.0), (torch.float16, 6e4, 1.0),
+                                       (torch.bfloat16, 1e16, 2.0 ** 48), (torch.bfloat16, -1e16, 2.0 ** 48),
+                                       (torch.bfloat16, -1e16, 2.0 ** 58), (torch.bfloat16, 1e4, 2.0 ** 20)])
+def test_scores_far_apart(dtype, a, b, causal):
+    """Key j scores a * b * (j + 1) times a constant: the last visible one has all the weight, or the first where a < 0, the
+    others less than 2^-1000 of it. So the output is that key's value v. Its weight p is rounded to the type beside v, by d of
+    it, and not in the sum (p is a power of two only where its exponent is exact, which fp32 scores of up to 2^16 are not), then
+    the output is rounded: with h = eps / 2, |d| <= h and fp32's steps in between of less than 2^-20, |o - v| <= |v| (h + 2^-20) (1 + h)
+    + |v| h <= |v| eps (1 + 2^-7); and half a step of subnormal numbers."""
+    rows, heads, dim = 200, 2, 64
+    q, k = torch.zeros(2, rows, heads, dim, dtype=dtype, device="cuda")
+    q[..., 0] = a
+    k[..., 0] = (b * torch.arange(1, rows + 1, device="cuda", dtype=torch.float64)).to(dtype)[:, None]
+    v = randn(rows, heads, dim, dtype=dtype, seed=3)
+    attend = q8.PromptAttention()
+    o = attend(q, k, v, starts_of([rows]), torch.empty_like(q), causal=causal)
+    assert attend.check() == capi.CONV3D_OK
+    want = (v[:1].expand_as(v) if a < 0 else v if causal else v[-1:].expand_as(v)).double()
+    info = torch.finfo(dtype)
+    assert bool(((o.double() - want).abs() <= want.abs() * info.eps * (1 + 2.0 ** -7) + info.smallest_normal * info.eps).all())
+
+
+@pytest.mark.parametrize("score", [-1e34, -1e31, -1e9, 1e9, 1e34])
+def test_one_key_has_all_the_weight_whatever_its_score(score):
+    q, k = torch.zeros(2, 300, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[..., 0], k[..., 0] = 8.0 * score / abs(score) * abs(score) ** 0.5, abs(score) ** 0.5
+    v = randn(300, 1, 64, dtype=torch.bfloat16, seed=3)
+    starts = torch.arange(301, dtype=torch.int32, device="cuda")
+    o = q8.PromptAttention()(q, k, v, starts, torch.empty_like(q))
+    assert torch.equal(o, v)
