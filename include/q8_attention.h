@@ -188,8 +188,9 @@ void attn_q8_destroy(attn_q8_plan_t plan);          /* waits for the device; NUL
  * kv_heads) of k and v. Scores and sums are fp32, p is rounded to the value type before it meets v. What a query
  * does not see does not reach it, infinities and NaN included.
  *
- * Starts are device memory; those that decrease or leave 0 .. rows (q_rows, k_rows) are cut to it. A plan holds a
- * status word; its runs may be in flight at once.
+ * Starts are device memory; those that decrease or leave 0 .. rows (q_rows, k_rows) are cut to it; rows of q that
+ * several sequences then have are left with any one's output or as they were. A plan holds a status word; its runs may be
+ * in flight at once.
  */
 typedef struct attn_prompt_plan_s *attn_prompt_plan_t; /* opaque, owned by the library */
 
@@ -197,9 +198,9 @@ typedef struct attn_prompt_plan_s *attn_prompt_plan_t; /* opaque, owned by the l
 conv3d_status attn_prompt_plan(attn_prompt_plan_t *plan, int device);
 conv3d_status attn_prompt_plan_ex(attn_prompt_plan_t *plan, int device, const attn_options *opts);
 
-/* Errors: EINVAL (a NULL pointer with seqs, q_rows > 0, sizes below 1 or negative, q_heads no multiple of kv_heads, value_type not bf16 or f16,
- * matrices that are not on 16 bytes, pitches that are no whole 16 bytes or make rows overlap, scale not finite, the wrong
- * current device), EUNSUPPORTED (head_dim not a multiple of 8 or above 128, rows of 2^31 or more, seqs above 65536,
+/* Errors: EINVAL (a NULL pointer with seqs, q_rows > 0, sizes below 1 or negative, q_heads no multiple of kv_heads,
+ * value_type not bf16 or f16, matrices that are not on 16 bytes, pitches that are no whole 16 bytes or make rows
+ * overlap, scale not finite, the wrong current device), EUNSUPPORTED (head_dim not a multiple of 8 or above 128, rows of 2^31 or more, seqs above 65536,
  * q_heads of 65536 or more), ECUDA. Nothing is done where seqs or q_rows is 0. o may not overlap an input. */
 typedef struct {
     const void *q;              /* [q_rows][q_heads][head_dim] value_type */
