@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, NB>)
   if (threadIdx.x == 0) abort_flag = 0, bad_input[0] = 0;
   if (lane < kS) mbar_init(bar_at + 8 * lane, 1);
   fence_mbar_init();
+  __syncthreads();  // the flags and barriers are set before any warp uses them; beside the wait for the kernel before
 
   pdl_wait_primary();
   // ---- this block's share
