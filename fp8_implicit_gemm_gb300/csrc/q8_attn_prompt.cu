@@ -57,13 +57,13 @@ constexpr size_t kPromptSmem = 1024 + (2 + kPromptSlots) * (size_t)kTileBytes<HA
 // phases; it then arrives for the slot in the copy's place. (The rows of a unit end within 255 keys of each other: 3 tiles.)
 // Units alternate between two places, and with them those barriers: a role is at most one unit ahead of another.
 // A slot is free again once the products that read it are complete, and its other readers must have seen its phase by then:
-// the gate has for all copies whose products wait for it, which are all but a unit's first of k. For those it arrives at
-// kBarSeen, where the copies wait before they fill the slot again. A unit has two copies at least, so the last
-// kPromptSlots hold up to kSeen first ones, and a barrier's phase is waited for before its next one can begin.
-constexpr int kMostChecked = 3, kSeen = (kPromptSlots + 1) / 2;
+// the gate has for all copies whose products wait for it, which are all but a unit's first of k. For that one it arrives at
+// kBarSeen, where the copies wait before they fill the slot again, or begin another unit. (A wait for the very copy, three
+// barriers in turn and a record of the last slots, took 392 instead of 386 us for 8192 tokens and as long for short prompts.)
+constexpr int kMostChecked = 3;
 enum { kBarUnit, kBarUnitFree = kBarUnit + 2, kBarQ = kBarUnitFree + 2, kBarQFree, kBarBlock, kBarDrain, kBarRaw,
        kBarS = kBarRaw + 2 * kMostChecked, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarFull = kBarO + 2,
-       kBarEmpty = kBarFull + kPromptSlots, kBarSeen = kBarEmpty + kPromptSlots, kBarCount = kBarSeen + kSeen };
+       kBarEmpty = kBarFull + kPromptSlots, kBarSeen = kBarEmpty + kPromptSlots, kBarCount };
 
 // 256 rows of one head of a sequence.
 struct PromptUnit {
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return false;
     };
     uint32_t copies = 0, with_tiles = 0;
-    uint32_t firsts = 0, seen = 0;  // whether each of the last copies (bit 0: the last) was a unit's first; waits for the gate
+    uint32_t seen = 0;  // units whose first copy of k the gate is known to have seen
     uint32_t block = blockIdx.x, asked = 0;
     bool first = true;  // this block's own
     for (int n = 0;; ++n) {
@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int all = max(u.tiles[0], u.tiles[1]), kv_head = u.head / (p.q_heads / p.kv_heads);
       if (all == 0) continue;
       if (with_tiles > 0 && !tc_wait(bar(kBarQFree), (with_tiles - 1) & 1, ab, kAttnTimeout)) break;
+      if (seen < with_tiles && !tc_wait(bar(kBarSeen), seen++ & 1, ab, kAttnTimeout)) break;
       ++with_tiles;
       if (elect_one()) {
         const int q_tiles = u.tiles[1] > 0 ? 2 : 1;
@@ -523,11 +524,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int i = 0; ok && i < 2 * all; ++i) {  // k of tile i / 2, then v
         const uint32_t c = copies + i;
         if (c >= kPromptSlots) ok = tc_wait(empty(c), lap(c) ^ 1u, ab, kAttnTimeout);
-        if (ok && (firsts >> (kPromptSlots - 1) & 1u)) {  // what the slot held was one
-          ok = tc_wait(bar(kBarSeen + seen % kSeen), (seen / kSeen) & 1, ab, kAttnTimeout);
-          ++seen;
-        }
-        firsts = firsts << 1 | (i == 0);
+        if (ok && i == kPromptSlots) ok = tc_wait(bar(kBarSeen), seen++ & 1, ab, kAttnTimeout);
         if (ok && elect_one()) {
           const uint32_t to =
               i % 2 && i / 2 >= u.checked_from ? bar(kBarRaw + kMostChecked * (n % 2) + i / 2 - u.checked_from) : full(c);
@@ -544,15 +541,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (warp == kGateWarp) {
     // ------------------------------------------------------------------------------ the gate
     // Arrives for round j of P once the copies are there that its products read, and the round before is over.
-    uint32_t copies = 0, with_tiles = 0, rounds[2] = {0, 0};
+    uint32_t copies = 0, rounds[2] = {0, 0};
     PromptUnit u;
     bool ok = true;
     for (int n = 0; ok && next_unit(n, u); ++n) {
       const int all = max(u.tiles[0], u.tiles[1]);
       if (all > 0) {  // no phase of a slot is passed over
         ok = tc_wait(full(copies), lap(copies), ab, kAttnTimeout);
-        if (ok && lane == 0) mbar_arrive(bar(kBarSeen + with_tiles % kSeen));
-        ++with_tiles;
+        if (ok && lane == 0) mbar_arrive(bar(kBarSeen));
       }
       for (int j = 0; ok && j < all; ++j) {
         const uint32_t v = copies + 2 * j + 1;
