@@ -124,8 +124,10 @@ conv3d_status cache_q8_read_run(const cache_q8_read_args *args);
  * Codes and q are multiplied in f16, where codes are exact and a row of q, scaled by a power of two, is too
  * but for elements below 2^-22 of the row's largest, which err by 2^-33 of that. A weight times v's scale has two parts
  * of f16's 11 bits for f16 outputs; for bf16 outputs it is cut to one, the same for all that is made of it (an output errs by at
- * most 2^-11 of sum p |v - o|; codes of weights below 2^-21 of the largest by 2^-31 of it). Sums, maxima and scales are fp32.
- * Scales of v below 2^-80 count as 2^-80. Results are the same from run to run.
+ * most 2^-11 of sum p |v - o|). Either way codes of such products below 2^-21 of the largest err by 2^-31 of it. Sums, maxima and
+ * scales are fp32. Scales of v below 2^-80 count as 2^-80, and the scale 1 of a row of v whose codes are all 0 (zeros, or
+ * equal values in 4 bits) as 2^-64, or as an eighth of its lowest value's magnitude if that is more: such a row takes no bits
+ * from the others, and keeps its own down to 2^-85. Results are the same from run to run.
  *
  * A plan holds the device's workspace: a status word and the partial results of sequences that several blocks share,
  * fixed by q_heads, kv_heads, max_tokens and head_dim, whatever the lengths. At most one run of a plan may be in
