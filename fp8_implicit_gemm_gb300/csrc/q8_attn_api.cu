@@ -370,8 +370,8 @@ extern "C" conv3d_status attn_prompt_run(attn_prompt_plan_t plan, const attn_pro
   p.head_dim = a->head_dim;
   p.causal = a->causal;
   p.negate = a->scale < 0.0f;
-  // a scale of 0 as one that leaves every finite score 0 and -inf, a masked one, -inf
-  p.scale = std::fmax(std::fabs(a->scale) * 1.44269504088896f, 1e-30f);
+  // a scale of 0 as 2^-149, which leaves every finite score below 2^-21 and -inf, a masked one, -inf; the largest ones finite
+  p.scale = std::fmin(std::fmax(std::fabs(a->scale) * 1.44269504088896f, 0x1p-149f), 3.4028234e38f);
   p.status = reinterpret_cast<int*>(plan->workspace);
   p.timeout_ns = plan->timeout_ns;
   p.debug_flags = plan->debug_flags;
