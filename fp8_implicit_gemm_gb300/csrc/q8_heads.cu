@@ -335,6 +335,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
               if (rotated) {
 #pragma unroll
                 for (int e = 0; e < kLane; e += 2) {
+                  if (e0 + e >= p.rot_dim) break;  // elements behind stay, whatever lies beside them
                   const float2 c = turn[e / 2];
                   const float a = f[e], b = f[e + 1];
                   f[e] = a * c.x - b * c.y;
