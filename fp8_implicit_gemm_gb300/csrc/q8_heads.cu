@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
           [[maybe_unused]] const T* here = here0 + i * kRows * in.head_pitch;
           float f[kLane];
           raw.values(f);
-          float rms = 1.0f;
+          float rms = 1.0f, lift = 1.0f;
           if (kind < 2 && w) {
             float2 two = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -303,7 +303,6 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
               two = q8_fma2(v, v, two);
             }
             float sum = row_sum<L>(two.x + two.y);
-            float lift = 1.0f;
             const bool lifted = !(sum <= 0x1p100f) || (sum < 0x1p-80f && p.eps < 0x1p-100f);
             if (__any_sync(0xFFFFFFFFu, lifted)) {
               if (lifted) lift = sum < 1.0f ? 0x1p100f : 0x1p-100f;
@@ -328,7 +327,6 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
                 f[e] = a.x, f[e + 1] = a.y, f[e + 2] = b.x, f[e + 3] = b.y;
               }
             }
-            rms *= lift;
           }
           if (kind < 2 && p.turns) {
             if constexpr (PAIRS == kAdjacent) {
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
                 if (live && i < p.rot_dim) {
                   const int other = i < half ? i + half : i - half;
                   float b = q8_to_float(here[other - e0]);
-                  if (w) b *= rms * weights[kind][other];
+                  if (w) b = b * lift * (rms * weights[kind][other]);  // their product may be past fp32's range
                   g[e] = i < half ? f[e] * turn[e].x - b * turn[e].y : f[e] * turn[e].x + b * turn[e].y;
                 }
               }
