@@ -270,8 +270,8 @@ class AttentionQ8:
         residual += x;  a = norm(residual);  q, k, v = a * w_qkv^T, in heads;  q, k = their norms, turned;
         k and v to the cache;  o = attention
 
-    for prompts (over their own keys in 16 bits) and for the newest tokens of running sequences (over the
-    cache): four calls of the library either way, in the caller's buffers and its own, one call at a time.
+    for prompts (over their own keys in 16 bits; heads of up to 128) and for the newest tokens of running sequences
+    (over the cache): four calls of the library either way, in the caller's buffers and its own, one call at a time.
     w_qkv [(q_heads + 2 * kv_heads) * head_dim, dim] holds the heads of q, then k's, then v's; the norms'
     weights [head_dim] and the rotary may be missing."""
 
@@ -333,6 +333,8 @@ class AttentionQ8:
     def prompt(self, x, residual, starts, positions, slots, o, stream=None) -> torch.Tensor:
         """Whole prompts, packed: x, residual [rows, dim] (residual is updated in place), starts [seqs + 1]
         int32, positions [rows] or [axes, rows] and slots [rows] int64, o [rows, q_heads, head_dim]."""
+        if self.cache.head_dim > 128:  # refused before the residual and the cache change, as in _start
+            raise ValueError(f"prompts: expected heads of up to 128 elements, got {self.cache.head_dim}")
         capi._q8_index(starts, "starts", x.get_device())
         if starts.dim() != 1 or not 1 <= starts.shape[0] <= 65537:
             raise ValueError(f"starts: expected [seqs + 1] of up to 65536 sequences, got {tuple(starts.shape)}")
