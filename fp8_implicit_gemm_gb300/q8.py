@@ -149,6 +149,8 @@ class Rotary:
         sections = [pairs] if sections is None else [int(n) for n in sections]
         if rot_dim < 2 or rot_dim % 2 or sum(sections) != pairs or min(sections) < 0:
             raise ValueError(f"expected an even rot_dim and sections of {pairs} pairs, got {rot_dim}, {sections}")
+        if len(sections) > 4:
+            raise ValueError(f"expected sections of up to 4 axes, got {sections}")
         if frequencies is None:
             frequencies = [theta ** -(i / n) for n in sections for i in range(n)]
         frequencies = [float(f) for f in frequencies]
@@ -285,8 +287,15 @@ class AttentionQ8:
         norms = [w for w in (q_norm, k_norm) if w is not None]
         if any(w.shape != (head_dim,) or w.dtype != norms[0].dtype for w in norms):
             raise ValueError(f"expected q_norm and k_norm [{head_dim}] of one type")
-        if rotary is not None and rotary.rot_dim > head_dim:
-            raise ValueError(f"expected a rotary of up to {head_dim} elements, got {rotary.rot_dim}")
+        device = w_qkv.get_device()
+        if device < 0 or cache.parts[4] != device or norm_weight.get_device() != device:
+            raise ValueError("expected norm_weight, w_qkv and the cache on one CUDA device")
+        for w in norms:  # as the heads take them, after the residual has changed
+            capi._q8_value_type(w, "q_norm, k_norm")
+            capi._q8_vector(w, "q_norm, k_norm", head_dim, device)
+        if rotary is not None and (rotary.rot_dim > head_dim or rotary.table[5] != device):
+            raise ValueError(f"expected a rotary of up to {head_dim} elements on CUDA device {device}, got "
+                             f"{rotary.rot_dim} on {rotary.table[5]}")
         if norm_weight.dtype not in (torch.bfloat16, torch.float16):  # the heads' type, which attention takes
             raise ValueError(f"expected a norm_weight of bfloat16 or float16, got {norm_weight.dtype}")
         self.norm_weight, self.eps, self.max_rows = norm_weight, eps, max_rows

@@ -180,3 +180,9 @@ def test_python_refuses_what_is_not_on_a_gpu():
                       torch.zeros(1, 1, 16, 64, dtype=torch.int8), torch.zeros(1, 1, 16))
     with pytest.raises(ValueError):
         capi.attn_prompt_run(0, x, x, x, torch.zeros(2, dtype=torch.int32), x, 1.0)
+
+
+def test_rotary_of_more_axes_than_the_heads_take():
+    q8.Rotary(16, sections=[2, 2, 2, 2], device="cpu")
+    with pytest.raises(ValueError):
+        q8.Rotary(16, sections=[2, 2, 2, 1, 1], device="cpu")

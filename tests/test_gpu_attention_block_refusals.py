@@ -38,3 +38,18 @@ def test_prompts_of_256_channels(codes):
     block.decode(x[:1], residual[:1], at[:1], at[:1], table, torch.ones(1, dtype=torch.int32, device="cuda"), o[:1])
     assert block.check() == capi.CONV3D_OK and bool(torch.isfinite(o[:1]).all())
     assert torch.equal(residual[:1], (x[:1].float() + before[:1].float()).bfloat16())
+
+
+def test_parts_that_the_heads_would_refuse():
+    """The block is not made of a rotary of another device, norms of another type or layout, or a cache elsewhere."""
+    weight, w, cache = parts()
+    norm = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(rotary=q8.Rotary(64, device="cpu")), dict(q_norm=norm.double()), dict(k_norm=norm.double()),
+               dict(q_norm=norm.int(), k_norm=norm.int()), dict(q_norm=norm.cpu()), dict(k_norm=norm.cpu()),
+               dict(q_norm=torch.ones(128, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            q8.AttentionQ8(weight, w, HEADS, cache, max_rows=16, **kw)
+    with pytest.raises(ValueError):
+        q8.AttentionQ8(weight.cpu(), w, HEADS, cache, max_rows=16)
+    with pytest.raises(ValueError):
+        q8.AttentionQ8(weight, w.cpu(), HEADS, cache, max_rows=16)
