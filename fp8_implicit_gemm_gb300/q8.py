@@ -324,6 +324,8 @@ class AttentionQ8:
             raise ValueError("o: expected heads on 16 bytes that do not overlap")
         capi._q8_vector(slots, "slots", rows, device, torch.int64)
         if self.rotary is not None:
+            if positions is None:
+                raise ValueError("positions: expected with a rotary")
             want = (rows,) if self.rotary.axes == 1 and positions.dim() == 1 else (self.rotary.axes, rows)
             if (positions.shape != want or positions.dtype != torch.int64 or positions.get_device() != device
                     or (rows > 1 and positions.stride(-1) != 1) or (positions.dim() == 2 and 0 < positions.stride(0) < rows)):

@@ -53,3 +53,18 @@ def test_parts_that_the_heads_would_refuse():
         q8.AttentionQ8(weight.cpu(), w, HEADS, cache, max_rows=16)
     with pytest.raises(ValueError):
         q8.AttentionQ8(weight, w.cpu(), HEADS, cache, max_rows=16)
+
+
+def test_missing_positions():
+    weight, w, cache = parts()
+    block = q8.AttentionQ8(weight, w, HEADS, cache, q8.Rotary(64), max_rows=16)
+    x, residual, at, o = rows(4)
+    before, kept = residual.clone(), whole(cache)
+    starts, table = torch.tensor([0, 4], dtype=torch.int32, device="cuda"), torch.zeros(4, 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        block.prompt(x, residual, starts, None, at, o)
+    with pytest.raises(ValueError):
+        block.decode(x, residual, None, at, table, torch.ones(4, dtype=torch.int32, device="cuda"), o)
+    assert torch.equal(residual, before) and all(torch.equal(a, b) for a, b in zip(whole(cache), kept))
+    q8.AttentionQ8(weight, w, HEADS, cache, max_rows=16).prompt(x, residual, starts, None, at, o)  # without a rotary
+    assert bool(torch.isfinite(o).all())
