@@ -841,6 +841,10 @@ def cache_q8_read_run(cache, slots, k, v, stream=None) -> None:
         _raise(status, "cache_q8_read_run")
 
 
+# The devices of the attention plans: their runs get nothing else that says where the tensors lie.
+_attn_devices = {}
+
+
 def attn_q8_plan(max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type, device=0, **options) -> int:
     """Create a plan for attention of up to max_tokens newest tokens of each of up to max_seqs sequences
     over a cache (code_type: Q8_INT8, Q8_E4M3 or Q8_INT4); returns its handle. Keyword options:
@@ -849,6 +853,7 @@ def attn_q8_plan(max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type, d
     o = AttnOptions(**{k: int(v) for k, v in options.items()})
     _raise(load().attn_q8_plan_ex(ctypes.byref(h), max_seqs, max_tokens, q_heads, kv_heads, head_dim, code_type,
                                   device, ctypes.byref(o)), "attn_q8_plan")
+    _attn_devices[h.value] = device
     return h.value
 
 
@@ -865,6 +870,8 @@ def attn_q8_run(plan, q, cache, table, lengths, o, scale, tokens=1, stream=None)
     lib = _q8 or _q8_setup()
     cache_ptr, _, dim, _, device, _ = cache if cache.__class__ is tuple else cache.parts
     shape = q.shape
+    if _attn_devices.get(plan, device) != device:
+        raise ValueError(f"cache: expected one on the plan's CUDA device {_attn_devices[plan]}, got one on {device}")
     if len(shape) != 3 or shape[2] != dim or len(table.shape) != 2:
         raise ValueError(f"expected q [seqs * tokens, q_heads, {dim}] and table [seqs, width]")
     seqs, width = table.shape
@@ -894,6 +901,7 @@ def attn_q8_workspace_size(plan) -> int:
 
 def attn_q8_destroy(plan) -> None:
     if plan:
+        _attn_devices.pop(plan, None)
         load().attn_q8_destroy(plan)
 
 
@@ -902,6 +910,7 @@ def attn_prompt_plan(device=0, **options) -> int:
     h = ctypes.c_void_p()
     o = AttnOptions(**{k: int(v) for k, v in options.items()})
     _raise(load().attn_prompt_plan_ex(ctypes.byref(h), device, ctypes.byref(o)), "attn_prompt_plan")
+    _attn_devices[h.value] = device
     return h.value
 
 
@@ -914,6 +923,8 @@ def attn_prompt_run(plan, q, k, v, starts, o, scale, causal=True, key_starts=Non
         raise ValueError("expected heads [rows, heads, head_dim]")
     if device < 0:
         raise ValueError("q: expected a CUDA tensor")
+    if _attn_devices.get(plan, device) != device:
+        raise ValueError(f"q: expected a tensor on the plan's CUDA device {_attn_devices[plan]}, got one on {device}")
     rows, heads, dim = shape
     k_rows, kv_heads, _ = k.shape
     k_shape = (k_rows, kv_heads, dim)
@@ -945,4 +956,5 @@ def attn_prompt_check(plan) -> int:
 
 def attn_prompt_destroy(plan) -> None:
     if plan:
+        _attn_devices.pop(plan, None)
         load().attn_prompt_destroy(plan)

@@ -186,3 +186,73 @@ def test_rotary_of_more_axes_than_the_heads_take():
     q8.Rotary(16, sections=[2, 2, 2, 2], device="cpu")
     with pytest.raises(ValueError):
         q8.Rotary(16, sections=[2, 2, 2, 1, 1], device="cpu")
+
+
+class _Heads:
+    """What the binding asks of a tensor, on a device that is not there."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, device
+
+    def get_device(self):
+        return self.device
+
+    def stride(self, dim=None):
+        t = torch.empty(self.shape, device="meta")
+        return t.stride() if dim is None else t.stride(dim)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.mark.parametrize("of_plan,of_tensors", [(0, 0), (0, 1), (1, 0)])
+def test_attention_on_another_device_than_the_plans(lib, monkeypatch, of_plan, of_tensors):
+    """Plans of one device with tensors of another are refused, whichever is the current one."""
+    calls = []
+
+    class Fake:
+        def attn_q8_plan_ex(self, h, *args):
+            h._obj.value = 64
+            return 0
+
+        def attn_prompt_plan_ex(self, h, *args):
+            h._obj.value = 128
+            return 0
+
+        def attn_q8_run(self, *args):
+            calls.append("cache")
+            return 0
+
+        def attn_prompt_run(self, *args):
+            calls.append("prompt")
+            return 0
+
+        def attn_q8_destroy(self, plan):
+            pass
+
+        attn_prompt_destroy = attn_q8_destroy
+    capi._q8_setup()
+    fake = Fake()
+    monkeypatch.setattr(capi, "_q8", fake)
+    monkeypatch.setattr(capi, "load", lambda: fake)
+    x = _Heads((2, 4, 64), torch.bfloat16, of_tensors)
+    ints = [_Heads(shape, torch.int32, of_tensors) for shape in ((2,), (2, 1))]
+    cache = (4096, 2, 64, capi.Q8_INT8, of_tensors, None)
+    plans = capi.attn_q8_plan(4, 1, 4, 2, 64, capi.Q8_INT8, of_plan), capi.attn_prompt_plan(of_plan)
+    runs = (lambda: capi.attn_q8_run(plans[0], x, cache, ints[1], ints[0], x, 1.0, stream=0),
+            lambda: capi.attn_prompt_run(plans[1], x, x, x, ints[0], x, 1.0, stream=0))
+    for run in runs:
+        if of_plan == of_tensors:
+            run()
+        else:
+            with pytest.raises(ValueError):
+                run()
+    assert calls == (["cache", "prompt"] if of_plan == of_tensors else [])
+    capi.attn_q8_destroy(plans[0])
+    capi.attn_prompt_destroy(plans[1])
+    again = capi.attn_prompt_plan(of_tensors)  # the same handle, of another device now
+    capi.attn_prompt_run(again, x, x, x, ints[0], x, 1.0, stream=0)
+    capi.attn_prompt_destroy(again)
