@@ -303,7 +303,9 @@ extern "C" conv3d_status linear_q8_check(linear_q8_plan_t plan) {
   if (cudaMemcpy(&word, plan->workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
     return CONV3D_ECUDA;
   if (word == 0) return CONV3D_OK;
-  if (cudaMemset(plan->workspace, 0, sizeof(int)) != cudaSuccess) return CONV3D_ECUDA;
+  // cleared before a run on any stream can report again
+  if (cudaMemset(plan->workspace, 0, sizeof(int)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
+    return CONV3D_ECUDA;
   return CONV3D_EDEVICE;
 }
 

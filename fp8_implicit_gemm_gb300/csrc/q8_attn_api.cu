@@ -54,7 +54,11 @@ conv3d_status plan_check(const Plan& plan) {
     return CONV3D_ECUDA;
   }
   if (word == 0) return CONV3D_OK;
-  if (cudaMemset(plan.workspace, 0, sizeof(int)) != cudaSuccess) return CONV3D_ECUDA;
+  // cleared before a run on any stream can report again
+  if (cudaMemset(plan.workspace, 0, sizeof(int)) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
+    return CONV3D_ECUDA;
+  }
   return CONV3D_EDEVICE;
 }
 

@@ -41,3 +41,16 @@ def test_a_bad_page_of_any_warp_is_reported(codes, seqs):
             product(codes8, ones, spare)
             assert torch.equal(attend(q, table, lengths, torch.full_like(q, 7.0)), want)
             assert attend.check() == capi.CONV3D_OK
+
+
+def test_a_check_does_not_clear_what_the_next_run_reports():
+    """Runs on a stream that the default one does not order, each with a bad page, each reported."""
+    cache = q8.CacheQ8.empty(4, 16, 1, 64)
+    table = torch.full((1, 1), 9, dtype=torch.int32, device="cuda")
+    length, q = torch.ones(1, dtype=torch.int32, device="cuda"), randn(1, 1, 64, dtype=torch.bfloat16, seed=1)
+    attend, o, s = q8.CacheAttention(cache, 1), torch.empty_like(q), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(300):
+        attend(q, table, length, o, stream=s)
+        assert attend.check() == capi.CONV3D_EDEVICE
+    assert attend.check() == capi.CONV3D_OK
