@@ -716,6 +716,12 @@ def cache_q8(k_codes, k_scale, v_codes, v_scale) -> tuple:
                                  (v_scale, "v_scale", shape[:3] + (2,) * four, _f32)):
         if t.shape != want or t.dtype != dtype or not t.is_contiguous() or t.get_device() != device:
             raise ValueError(f"{name}: expected {tuple(want)}, contiguous, {dtype}, on CUDA device {device}")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name}: expected a tensor on 16 bytes")
+    if (page_size % 16 or head_dim not in (64, 128, 256) or not 0 < pages * page_size < 1 << 31
+            or not 0 < kv_heads < 1 << 15):
+        raise ValueError(f"k_codes: expected pages of a multiple of 16 tokens, fewer than 2^31 in all, and heads of 64, 128 or "
+                         f"256, got {pages} pages of {page_size}, {kv_heads} heads of {head_dim}")
     packed = ctypes.create_string_buffer(_CACHE.pack(
         k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page_size,
         kv_heads, head_dim, code_type), _CACHE.size)

@@ -256,3 +256,28 @@ def test_attention_on_another_device_than_the_plans(lib, monkeypatch, of_plan, o
     again = capi.attn_prompt_plan(of_tensors)  # the same handle, of another device now
     capi.attn_prompt_run(again, x, x, x, ints[0], x, 1.0, stream=0)
     capi.attn_prompt_destroy(again)
+
+
+@pytest.mark.parametrize("shape,codes,offset", [
+    ((2, 2, 24, 64), torch.int8, 0), ((2, 2, 16, 80), torch.int8, 0), ((0, 2, 16, 64), torch.int8, 0),
+    ((2, 0, 16, 64), torch.int8, 0), ((2, 2, 16, 512), torch.int8, 0), ((1 << 27, 1, 16, 64), torch.int8, 0),
+    ((2, 1 << 15, 16, 64), torch.int8, 0), ((2, 2, 16, 64), torch.int8, 8), ((2, 2, 16, 64), torch.uint8, 4),
+    ((2, 2, 16, 24), torch.uint8, 0)])
+def test_caches_that_no_call_takes(lib, shape, codes, offset):
+    """They are refused where a cache is made, so that no block finds out after it has updated a residual."""
+    class Tensor(_Heads):
+        def dim(self):
+            return len(self.shape)
+
+        def data_ptr(self):
+            return 4096 + offset
+    four = codes == torch.uint8
+    c = Tensor(shape, codes, 0)
+    scale = Tensor(shape[:3] + (2,) * four, torch.float32, 0)
+    with pytest.raises(ValueError):
+        capi.cache_q8(c, scale, c, scale)
+    good = Tensor((2, 2, 16, 64), codes, 0)
+    good.data_ptr = lambda: 4096
+    scale = Tensor((2, 2, 16) + (2,) * four, torch.float32, 0)
+    scale.data_ptr = good.data_ptr
+    assert capi.cache_q8(good, scale, good, scale)[1:5] == (2, 128 if four else 64, capi.Q8_INT4 if four else capi.Q8_INT8, 0)
