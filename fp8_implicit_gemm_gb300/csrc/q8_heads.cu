@@ -3,8 +3,8 @@
 //
 // A row is one token's head. L = 8, 16 or 32 lanes hold it, eight elements each, so that its sums, its
 // partners in the rotation and its scale are shuffles, and every element is read once and written once:
-// the memory's bandwidth is the bound. A warp takes a token's heads; the sines of its angles are taken once (16384 x 32
-// queries and 8 keys of 128 with three axes: 109 us with a row at a time, 54 now, 5 TB/s, beside 65% of the issue slots;
+// the memory's bandwidth is the bound. A warp takes a token's heads; the sines of its angles are taken once (16384 tokens of
+// 16 queries and 16 keys of 128 with three axes: 109 us with a row at a time, 55.4 now, 4.9 TB/s, beside 65% of the issue slots;
 // 65536 x 8 rows of 4-bit codes read back: 70.6 us, 4.9 TB/s, 81% of them).
 //
 // Angles. In turns an angle is frequency / 2 pi * position, and only its fraction matters. With the
@@ -160,9 +160,10 @@ __device__ __forceinline__ void write_codes(uint8_t* codes, float* scales, long 
 }
 
 // ------------------------------------------------------------------ the rows of heads
-// How pairs lie: next to each other; half of the rotated part apart, in whole lanes; the same, not in whole
-// lanes (the partner is then read a second time).
-enum { kAdjacent, kHalves, kLooseHalves };
+// How pairs lie: next to each other, in whole lanes; the same, where the last rotated lane has elements behind them, which stay
+// whatever lies beside them (with that test in every form: 56.6 instead of 55.4 us for 16384 x 32 x 128 with three axes); half of the
+// rotated part apart, in whole lanes; the same, not in whole lanes (the partner is then read a second time).
+enum { kAdjacent, kLooseAdjacent, kHalves, kLooseHalves };
 
 // What a lane holds of a row as it lies in memory: a row ahead is under way while one is worked on.
 template <typename T>
@@ -196,6 +197,7 @@ struct RawLane {
 // time, all of the kind's, with the angles' sines and cosines in its lanes' registers.
 template <typename T, int CODE, int L, int PAIRS>
 __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(const HeadsParams p, int shares) {
+  constexpr bool kNextTo = PAIRS == kAdjacent || PAIRS == kLooseAdjacent;
   constexpr int kRows = 32 / L;  // of a warp at a time
   constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;  // times that, on their way beside as many that are worked on
   __shared__ float2 turned[kHeadsThreads / 32][kMostPairs];  // cosine and sine
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
     }
     long long slot = -1;
     if constexpr (CODE != kNoCodes) slot = p.slots[t];
-    float2 turn[kLane];  // of this lane's elements (kAdjacent: pairs, of which there are half as many)
+    float2 turn[kLane];  // of this lane's elements (kNextTo: pairs, of which there are half as many)
     if (p.turns && (first < q_units + k_units)) {
       __syncwarp();
       for (int j = lane; j < half; j += 32) {
@@ -249,8 +251,8 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
       if (rotated) {
 #pragma unroll
         for (int e = 0; e < kLane; ++e) {
-          if (PAIRS == kAdjacent && e >= kLane / 2) break;
-          const int i = PAIRS == kAdjacent ? e0 / 2 + e : e0 + e >= half ? e0 + e - half : e0 + e;
+          if (kNextTo && e >= kLane / 2) break;
+          const int i = kNextTo ? e0 / 2 + e : e0 + e >= half ? e0 + e - half : e0 + e;
           turn[e] = i < half ? turned[warp][i] : make_float2(1.0f, 0.0f);
         }
       }
@@ -329,11 +331,11 @@ __global__ void __launch_bounds__(kHeadsThreads, kBlocksPerSm) heads_kernel(cons
             }
           }
           if (kind < 2 && p.turns) {
-            if constexpr (PAIRS == kAdjacent) {
+            if constexpr (kNextTo) {
               if (rotated) {
 #pragma unroll
                 for (int e = 0; e < kLane; e += 2) {
-                  if (e0 + e >= p.rot_dim) break;  // elements behind stay, whatever lies beside them
+                  if (PAIRS == kLooseAdjacent && e0 + e >= p.rot_dim) break;
                   const float2 c = turn[e / 2];
                   const float a = f[e], b = f[e + 1];
                   f[e] = a * c.x - b * c.y;
@@ -396,8 +398,10 @@ cudaError_t launch_heads_as(const HeadsParams& p, bool adjacent, cudaStream_t st
   const int shares = p.tokens >= wanted ? 1 : std::min(units, (wanted + p.tokens - 1) / p.tokens);
   const long long blocks = ((long long)p.tokens * shares + kWarps - 1) / kWarps;
   const unsigned grid = (unsigned)std::min<long long>(blocks, 152 * kBlocksPerSm);
-  if (adjacent || !p.turns)
+  if (!p.turns || (adjacent && p.rot_dim % kLane == 0))
     heads_kernel<T, CODE, L, kAdjacent><<<grid, kHeadsThreads, 0, stream>>>(p, shares);
+  else if (adjacent)
+    heads_kernel<T, CODE, L, kLooseAdjacent><<<grid, kHeadsThreads, 0, stream>>>(p, shares);
   else if (p.rot_dim % (2 * kLane) == 0)
     heads_kernel<T, CODE, L, kHalves><<<grid, kHeadsThreads, 0, stream>>>(p, shares);
   else
