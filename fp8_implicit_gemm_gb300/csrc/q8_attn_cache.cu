@@ -1,8 +1,8 @@
 // q8_attn_cache.cu -- attention of each sequence's newest tokens over a paged cache of codes.
 //
-// Each cached row is read once, so the memory is the bound (a key of 4-bit codes and 128 channels is 144
-// bytes with its value and scales), as long as turning codes into operands stays short: at 6.8 TB/s an SM
-// meets 47 such codes a cycle.
+// Each cached row is read once for every 8 or 16 rows of q (the heads that share it, newest tokens), and nearly always there are no
+// more, so the memory is the bound (a key of 4-bit codes and 128 channels is 144 bytes with its value and scales), as long as
+// turning codes into operands stays short: at 6.8 TB/s an SM meets 47 such codes a cycle.
 //
 // Products. m16n8k16 with the keys as rows and up to 8 rows of q (heads of one group, newest tokens) as columns
 // (16 with two instructions): S^T = K q^T, then O^T = V^T P^T with V's channels as rows, so that a group of 8 heads
@@ -35,7 +35,8 @@
 // 32768 with scales of 0.006: 10% off), and lowest + 8 would cut the lowest value off. Any scale stands for codes of 0,
 // so where a scale is 1 and the codes are 0 the warp puts another one in its place in the copy: 0 for k, for v 2^-64 or an eighth
 // of the lowest value. A vote a step (of all keys, so that a row's results do not depend on its neighbours), and what it calls,
-// not inlined, take 131072 int8 keys from 54.9 to 56.0 us (inlined: 57.2), batches of 4 bits no time that shows.
+// not inlined, take 131072 int8 keys from 54.9 to 56.0 us (inlined: 57.2), 64 x ..8192 of 4 bits from 81.7 to 82.5, 8 x 131072 of
+// them from 255 to 263.
 //
 // Copies. Every warp has a ring of its own, filled by bulk copies of 16 rows of codes and their scales (pages
 // are multiples of 16 tokens: a copy never leaves its page), so no barrier but its own holds it up.
@@ -45,8 +46,9 @@
 // where a sequence's head is shared by several blocks each leaves sums in the plan's workspace and a second kernel, that is
 // waiting already, joins them in the blocks' order: results do not depend on which is ready first.
 //
-// 64 sequences of up to 8192 keys, 8 heads of 128, 32 of q, 4-bit codes: 82 us, 3.7 TB/s, by instructions (0.6 a cycle at 4
-// warps a scheduler, 128 registers a thread); one of 131072 int8 keys 54.9 us, 5 TB/s.
+// 64 sequences of up to 8192 keys, 8 heads of 128, 32 of q, 4-bit codes: 82 us, 3.8 TB/s, by instructions (0.6 a cycle at 4
+// warps a scheduler, 128 registers a thread); one of 131072 int8 keys 56.0 us, 4.9 TB/s. 5 or 8 newest tokens of those sequences,
+// 20 or 32 rows of q a key head, read and convert the cache twice: 260 and 264 us.
 #include <algorithm>
 #include <type_traits>
 

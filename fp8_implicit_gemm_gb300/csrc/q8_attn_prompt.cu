@@ -23,7 +23,7 @@
 // one's last softmax and epilogue (a block for each unit: 4.3 us of 8 were its start and end for 500 keys of 64 channels).
 // Every wait is bounded; one that runs out records a status bit and the block winds down.
 //
-// 8192 tokens, 32 heads of 128, causal: 383 us, 1.44 PFLOP/s, the tensor pipe active 64% of the time. The softmax bounds it:
+// 8192 tokens, 32 heads of 128, causal: 385 us, 1.43 PFLOP/s, the tensor pipe active 63% of the time. The softmax bounds it:
 // ~1300 cycles a tile in one warpgroup, two of which take turns, where the tile's products take ~550.
 #include <algorithm>
 

@@ -118,21 +118,23 @@ conv3d_status cache_q8_read_run(const cache_q8_read_args *args);
  *   o = sum_s p_s v_s / sum_s p_s,   p_s = exp(scale * q . k_s)
  * over s < lengths[b] - tokens + 1 + t for token t (0 <= t < tokens) of sequence b, whose row is b *
  * tokens + t of q and o; head h of q reads head h / (q_heads / kv_heads) of the cache. A token that
- * sees nothing (a length below tokens - t) gets 0. The place s of sequence b is page table[b][s /
- * page_size]. A cached row whose scale is NaN makes every output that sees it NaN, and no other.
+ * sees nothing (a length below tokens - t, scores of -inf) gets 0. The place s of sequence b is page table[b][s /
+ * page_size]. A cached row whose scale is NaN makes every output that sees it NaN, and no other; e4m3
+ * codes that are NaN, which heads_q8_run does not write, may be in no row below lengths[b].
  *
  * Codes and q are multiplied in f16, where codes are exact and a row of q, scaled by a power of two, is too
  * but for elements below 2^-22 of the row's largest, which err by 2^-33 of that. A weight times v's scale has two parts
  * of f16's 11 bits for f16 outputs; for bf16 outputs it is cut to one, the same for all that is made of it (an output errs by at
- * most 2^-11 of sum p |v - o|). Either way codes of such products below 2^-21 of the largest err by 2^-31 of it. Sums, maxima and
- * scales are fp32. Scales of v below 2^-80 count as 2^-80, and the scale 1 of a row of v whose codes are all 0 (zeros, or
- * equal values in 4 bits) as 2^-64, or as an eighth of its lowest value's magnitude if that is more: such a row takes no bits
- * from the others, and keeps its own down to 2^-85. Results are the same from run to run.
+ * most 2^-11 of sum p |v - o|). Either way codes of such products below 2^-21 of the largest err by 2^-31 of it, and a
+ * key whose product is below 2^-133 of it counts as not seen. Sums, maxima and scales are fp32. Scales of v below 2^-80
+ * count as 2^-80, and the scale 1 of a row of v whose codes are all 0 (zeros, or equal values in 4 bits) as 2^-64, or as an
+ * eighth of its lowest value's magnitude if that is more: such a row takes no bits from the others, and keeps its own down to
+ * 2^-85. Results are the same from run to run.
  *
  * A plan holds the device's workspace: a status word and the partial results of sequences that several blocks share,
- * fixed by q_heads, kv_heads, max_tokens and head_dim, whatever the lengths. At most one run of a plan may be in
- * flight at a time (one plan for each concurrent stream; graphs that were captured with one plan are replayed one
- * after another).
+ * fixed by q_heads, kv_heads, max_tokens and head_dim, whatever the lengths. All that a run is given lies on its plan's
+ * device. At most one run of a plan may be in flight at a time (one plan for each concurrent stream; graphs that were captured
+ * with one plan are replayed one after another).
  */
 typedef struct attn_q8_plan_s *attn_q8_plan_t; /* opaque, owned by the library */
 
@@ -186,8 +188,8 @@ void attn_q8_destroy(attn_q8_plan_t plan);          /* waits for the device; NUL
  *   o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale * q_i . k_j)
  * over all keys of the sequence, if `causal` over j <= i + (keys - queries) (the last query sees all keys).
  * key_starts may be starts, or others: a chunk of queries whose keys begin earlier. A query that sees no key
- * gets 0; rows of o outside all sequences are left as they were. Head h of q reads head h / (q_heads /
- * kv_heads) of k and v. Scores and sums are fp32, p is rounded to the value type before it meets v. What a query
+ * gets 0 (a score of -inf is that of a key it does not see); rows of o outside all sequences are left as they were. Head
+ * h of q reads head h / (q_heads / kv_heads) of k and v. Scores and sums are fp32, p is rounded to the value type before it meets v. What a query
  * does not see does not reach it, infinities and NaN included.
  *
  * Starts are device memory; those that decrease or leave 0 .. rows (q_rows, k_rows) are cut to it; rows of q that
