@@ -189,8 +189,9 @@ void attn_q8_destroy(attn_q8_plan_t plan);          /* waits for the device; NUL
  * over all keys of the sequence, if `causal` over j <= i + (keys - queries) (the last query sees all keys).
  * key_starts may be starts, or others: a chunk of queries whose keys begin earlier. A query that sees no key
  * gets 0 (a score of -inf is that of a key it does not see); rows of o outside all sequences are left as they were. Head
- * h of q reads head h / (q_heads / kv_heads) of k and v. Scores and sums are fp32, p is rounded to the value type before it meets v. What a query
- * does not see does not reach it, infinities and NaN included.
+ * h of q reads head h / (q_heads / kv_heads) of k and v. Scores and sums are fp32, p is rounded to the value type before it
+ * meets v. What a query does not see does not reach it, infinities and NaN included. All that a run is given lies on its plan's
+ * device.
  *
  * Starts are device memory; those that decrease or leave 0 .. rows (q_rows, k_rows) are cut to it; rows of q that
  * several sequences then have are left with any one's output or as they were. A plan holds a status word; its runs may be
